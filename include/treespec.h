@@ -20,6 +20,12 @@
  *   tree_commit_accepted    append the accepted path to the paged cache
  *   tree_attn_workspace_size, tree_attn_plan, tree_attn_plan_order, tree_verify_workspace_size
  *                           host-only queries: workspace bytes, split plan
+ *   tree_rope               rotary positions of the tree's queries and keys,
+ *                           before the attention
+ *   tree_cache_append_q8, tree_commit_accepted_q8, tree_attn_fwd_q8
+ *                           an 8-bit paged cache: prompts and accepted paths
+ *                           quantised as they are written, and the attention
+ *                           that reads it
  *
  * Sources (web pages on the method):
  *   [P1] "Tree Attention", inferensys glossary.
@@ -460,6 +466,136 @@ TS_API ts_status tree_verify_greedy_forest(const int32_t* draft_tokens, const fl
                                            int32_t* accepted, int32_t* accept_len, int32_t* bonus,
                                            int32_t* argmax_out, int32_t* status, void* workspace,
                                            size_t workspace_bytes, ts_stream stream);
+
+/*
+ * tree_rope — rotary positions of the tree's queries and keys.
+ *
+ * tree_attn_fwd and tree_attn_fwd_q8 take q and k_tree as already positioned
+ * ([P2] Tradeoffs names the position bookkeeping; tree_build_ancestry gives
+ * pos).  This call positions them, and the keys of prompts before they are
+ * written to a cache.  With R = rotary_dim, f_i = theta^(-2i/R) for i < R/2 and
+ * a = pos * f'_i, each pair (x, y) of a head becomes
+ *     mscale * (x cos a - y sin a,  y cos a + x sin a);
+ * the pair is channels (i, i + R/2), or (2i, 2i + 1) with interleaved; channels
+ * R .. D-1 are copied.  The angle is exact to 2^-31 of a turn for every int32
+ * position; sums are fp32, rounded once to bf16.  f' by `scaling`:
+ *     TS_ROPE_NONE    f
+ *     TS_ROPE_LINEAR  f / factor
+ *     TS_ROPE_NTK     f of theta * factor^(R/(R-2))   (R = 2: f)
+ *     TS_ROPE_BANDS   g f + (1 - g) f / factor,  g = (orig_len f / (2 pi) -
+ *                     low_rot) / (high_rot - low_rot) held within [0, 1]:
+ *                     frequencies that turn high_rot times or more within
+ *                     orig_len tokens are kept, those below low_rot divided.
+ *
+ *   q, k         [B, N, Hq, D] and [B, N, Hkv, D] bf16; either may be NULL
+ *                (its out is then unused).  q_token_stride and the others are
+ *                in elements, multiples of 8, so that q and k may be views of
+ *                a fused projection: token (b, n) starts (b N + n) strides in.
+ *                0 is the dense stride.
+ *   pos          [B, N] int32.
+ *   q_out, k_out dense, as tree_attn_fwd takes them.  A dense input may be
+ *                rotated in place (the same pointer); any other overlap of an
+ *                output with an input or the other output is TS_ERR_SHAPE.
+ *   rotary_dim   even, 2 .. D; 0 is D.   theta > 0, mscale > 0, both finite.
+ * B and N are any positive sizes here (B * N < 2^31): a prompt is B = 1, N its
+ * tokens.  D is 64 or 128.  No workspace.  Returns TS_ERR_NULL / TS_ERR_SHAPE /
+ * TS_ERR_UNSUPPORTED (D, more than 4096 heads, scaling) / TS_ERR_CUDA.
+ */
+enum { TS_ROPE_NONE = 0, TS_ROPE_LINEAR = 1, TS_ROPE_NTK = 2, TS_ROPE_BANDS = 3 };
+
+typedef struct ts_rope_params {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const int32_t* pos;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int B, N, Hq, Hkv, D;
+  int rotary_dim, interleaved;
+  int scaling;
+  double theta, factor, low_rot, high_rot;
+  int orig_len;
+  float mscale;
+} ts_rope_params;
+
+TS_API ts_status tree_rope(const ts_rope_params* p, ts_stream stream);
+
+/*
+ * The 8-bit paged cache.  A row (one token of one KV head, D values) is D e4m3
+ * codes and one scale byte s; its values are code * 2^(s - 127).  The writers
+ * take the smallest power of two that keeps the row's largest magnitude within
+ * 448 (s in [1, 247]), round to the nearest code (ties to even), store an
+ * infinity as +-448 and a NaN as a NaN code.  A power of two scales without
+ * rounding, so codes and bytes are the same on every run.
+ *
+ *   k_cache, v_cache  [num_blocks, Hkv, block_size, D] e4m3, 16-byte aligned.
+ *   kv_scale          [num_blocks, Hkv, block_size, 2] uint8, the K row's byte
+ *                     and the V row's, 16-byte aligned.
+ * Blocks and block tables are those of the bf16 cache.
+ *
+ * tree_cache_append_q8 — quantise new tokens into the cache: prompts, or one
+ * decoded token a sequence ([P1] Key Mechanisms > Speculative KV Cache Reuse:
+ * the verified prefix the tree is scored against).
+ *
+ *   k, v            [T, Hkv, D] bf16, the new tokens of all sequences one after
+ *                   the other; k_stride, v_stride: elements from one token to
+ *                   the next (a multiple of 8; 0 is Hkv * D), so they may be
+ *                   views of a fused projection.  16-byte aligned.
+ *   cu_len          [B + 1] int32: rows cu_len[b] .. cu_len[b+1]-1 are sequence
+ *                   b's (0 <= cu_len[b] <= cu_len[b+1] <= T; rows of no
+ *                   sequence are left out).  A sequence may get none.
+ *   prefix_len      [B] int32, P_b; the rows become tokens P_b, P_b + 1, ...
+ *   new_prefix_len  [B] int32 out: P_b plus the sequence's rows.  Must not
+ *                   overlap prefix_len, cu_len or status (TS_ERR_SHAPE).
+ *   status          [B] int32 in/out (or NULL): a sequence whose status is not
+ *                   0 gets nothing and keeps P_b.  A destination block outside
+ *                   the pool or past the table sets TS_ERR_BAD_BLOCK, cu_len
+ *                   out of order or P_b + rows past 2^30 TS_ERR_SHAPE; such a
+ *                   sequence keeps P_b (rows of it that have a valid block may
+ *                   have been written past it).
+ * T may be 0 (k and v may then be NULL).  No workspace.  Returns TS_ERR_NULL /
+ * TS_ERR_SHAPE / TS_ERR_UNSUPPORTED (D not 64 or 128, Hkv over 4096) /
+ * TS_ERR_CUDA.
+ */
+TS_API ts_status tree_cache_append_q8(const void* k, const void* v, const int32_t* cu_len, const int32_t* prefix_len,
+                                      void* k_cache, void* v_cache, uint8_t* kv_scale, const int32_t* block_table,
+                                      int B, int T, int Hkv, int D, int64_t k_stride, int64_t v_stride,
+                                      int block_size, int num_blocks, int max_blocks, int32_t* new_prefix_len,
+                                      int32_t* status, ts_stream stream);
+
+/*
+ * tree_commit_accepted_q8 — tree_commit_accepted into the 8-bit cache: the
+ * accepted path's keys and values (bf16 k_tree, v_tree) are quantised as they
+ * are appended.  Arguments and errors as tree_commit_accepted, new_prefix_len
+ * may be the prefix_len array; an accept_len outside [0, min(max_depth, N - 1)]
+ * commits nothing.
+ */
+TS_API ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree, const int32_t* accepted,
+                                         const int32_t* accept_len, const int32_t* prefix_len, void* k_cache,
+                                         void* v_cache, uint8_t* kv_scale, const int32_t* block_table, int B, int N,
+                                         int Hkv, int D, int block_size, int num_blocks, int max_blocks,
+                                         int max_depth, int32_t* new_prefix_len, int32_t* status, ts_stream stream);
+
+/*
+ * tree_attn_fwd_q8 — tree_attn_fwd over the 8-bit cache.  Takes the same
+ * parameter block, with p->k_cache and p->v_cache the e4m3 pools, and the
+ * pools' scale bytes; the tree's own k_tree and v_tree are bf16.  The prefix
+ * keys and values are the rows' values, exactly; logits, softmax and output
+ * sums are fp32.
+ * Values past bf16's largest (255 * 2^120; only rows within 3% of it, or with
+ * an infinity, hold any) read as infinite.
+ * A row that sees no key (no prefix and an empty mask row) gives zeros and an
+ * lse of -inf.  kv_scale bytes 0 and 255 (which the writers never store) read
+ * as 0 and infinity.
+ *
+ * tree_attn_q8_workspace_size: bytes of device workspace it needs (256-byte
+ * aligned, ZERO-FILLED before its first use, then left so that stream-ordered
+ * calls may share it, like tree_attn_fwd's).  0 for arguments it would reject.
+ * Returns and statuses as tree_attn_fwd.
+ */
+TS_API size_t tree_attn_q8_workspace_size(const ts_attn_params* p);
+TS_API ts_status tree_attn_fwd_q8(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace,
+                                  size_t workspace_bytes, ts_stream stream);
 
 /* Size of the library-owned scratch behind tree_verify_greedy_noalloc. */
 #define TS_VERIFY_NOALLOC_SCRATCH_BYTES ((size_t)4 << 20)

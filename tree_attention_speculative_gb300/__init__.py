@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import numpy as np
@@ -24,7 +25,8 @@ __all__ = [
     "tree_verify_workspace_size", "tree_verify_greedy",
     "tree_verify_greedy_noalloc", "tree_commit_accepted", "tree_verify_stochastic", "tree_build_dynamic",
     "tree_build_ancestry_forest", "tree_verify_greedy_forest", "NOALLOC_SCRATCH_BYTES",
-    "STATUS",
+    "RopeConfig", "tree_rope", "tree_cache_append_q8", "tree_commit_accepted_q8",
+    "tree_attn_q8_workspace_size", "tree_attn_fwd_q8", "STATUS",
 ]
 
 STATUS = {
@@ -52,6 +54,43 @@ class AttnParams(ctypes.Structure):
     ]
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("pos", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low_rot", ctypes.c_double),
+        ("high_rot", ctypes.c_double), ("orig_len", ctypes.c_int), ("mscale", ctypes.c_float),
+    ]
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
+
+
+@dataclass(frozen=True)
+class RopeConfig:
+    """Rotary positions of a model (treespec.h: tree_rope).
+
+    ``rotary_dim`` 0 rotates the whole head; ``interleaved`` pairs channels
+    (2i, 2i+1) instead of (i, i + rotary_dim/2).  ``scaling``: "none",
+    "linear" (positions / factor), "ntk" (base scaled by factor) or "bands"
+    (frequencies that turn at least ``high_rot`` times within ``orig_len``
+    tokens kept, those below ``low_rot`` divided by factor, a ramp between).
+    """
+    theta: float = 10000.0
+    rotary_dim: int = 0
+    interleaved: bool = False
+    scaling: str = "none"
+    factor: float = 1.0
+    low_rot: float = 1.0
+    high_rot: float = 4.0
+    orig_len: int = 0
+    mscale: float = 1.0
+
+
 _LIB: Optional[ctypes.CDLL] = None
 
 # every symbol include/treespec.h declares
@@ -59,7 +98,8 @@ EXPORTS = ("ts_status_str", "tree_build_ancestry", "tree_attn_workspace_size", "
            "tree_attn_fwd",
            "tree_verify_workspace_size", "tree_verify_greedy", "tree_verify_greedy_noalloc",
            "tree_commit_accepted", "tree_verify_stochastic", "tree_build_dynamic", "tree_build_ancestry_forest",
-           "tree_verify_greedy_forest", "tree_attn_fwd_stall_test", "tree_attn_fwd_ctas_test")
+           "tree_verify_greedy_forest", "tree_attn_fwd_stall_test", "tree_attn_fwd_ctas_test", "tree_rope",
+           "tree_cache_append_q8", "tree_commit_accepted_q8", "tree_attn_q8_workspace_size", "tree_attn_fwd_q8")
 
 # TS_VERIFY_NOALLOC_SCRATCH_BYTES of treespec.h
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -107,6 +147,19 @@ def lib() -> ctypes.CDLL:
         L.tree_build_ancestry_forest.restype = i32
         L.tree_verify_greedy_forest.argtypes = L.tree_verify_greedy.argtypes
         L.tree_verify_greedy_forest.restype = i32
+        i64 = ctypes.c_int64
+        L.tree_rope.argtypes = [ctypes.POINTER(RopeParams), vp]
+        L.tree_rope.restype = i32
+        L.tree_cache_append_q8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i32, i32, i32,
+                                           vp, vp, vp]
+        L.tree_cache_append_q8.restype = i32
+        L.tree_commit_accepted_q8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                              i32, vp, vp, vp]
+        L.tree_commit_accepted_q8.restype = i32
+        L.tree_attn_q8_workspace_size.argtypes = [ctypes.POINTER(AttnParams)]
+        L.tree_attn_q8_workspace_size.restype = sz
+        L.tree_attn_fwd_q8.argtypes = [ctypes.POINTER(AttnParams), vp, vp, sz, vp]
+        L.tree_attn_fwd_q8.restype = i32
         _LIB = L
     return _LIB
 
@@ -166,6 +219,7 @@ def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k
                    B=B, N=N, Hq=Hq, Hkv=Hkv, D=D, block_size=bs, num_blocks=nblk,
                    max_blocks=block_table.shape[1], scale=scale, rope_theta=rope_theta)
     p._keep = (host,)
+    p.cache_dtypes = (getattr(k_cache, "dtype", None), getattr(v_cache, "dtype", None))
     return p
 
 
@@ -282,3 +336,131 @@ def tree_verify_greedy_noalloc(draft_tokens, target_logits, parent_idx, max_dept
     _check(lib().tree_verify_greedy_noalloc(_p(draft_tokens), _p(target_logits), _p(parent_idx), B, N, V, max_depth,
                                             _p(accepted), _p(accept_len), _p(bonus), _p(argmax_out), _p(status),
                                             _s(stream)), "tree_verify_greedy_noalloc")
+
+
+# ---------------------------------------------------------------- rotary positions, 8-bit cache
+#
+# These calls read tensors whose type and strides the C side cannot see (a bf16
+# pool given as the 8-bit one would be read past its rows), so each tensor's
+# type, shape, density and device are checked here first.
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _need(ok: bool, where: str):
+    if not ok:
+        raise TreeSpecError(-2, where)  # TS_ERR_SHAPE
+
+
+def _dense(where: str, t: torch.Tensor, shape, *dtypes):
+    _need(t.dtype in dtypes and tuple(t.shape) == tuple(shape) and t.is_contiguous(), where)
+
+
+def _same_device(where: str, *tensors):
+    """Every tensor on the current CUDA device, whose stream the call uses."""
+    _need(all(t is None or t.is_cuda for t in tensors), where)
+    here = torch.cuda.current_device()
+    _need(all(t is None or t.get_device() == here for t in tensors), where)
+
+
+def _token_heads(where: str, x: torch.Tensor, out: torch.Tensor, B: int, N: int):
+    """Strides (token, head) of bf16 x [B, N, H, D], whose tokens are evenly
+    spaced, for the dense out of the same shape."""
+    _need(x.dim() == 4 and x.dtype == torch.bfloat16 and x.shape[:2] == (B, N), where)
+    _dense(where, out, x.shape, torch.bfloat16)
+    sb, st, sh, sd = x.stride()
+    _need((sd == 1 or x.shape[3] == 1) and (B == 1 or N == 1 or sb == N * st), where)
+    H, D = x.shape[2], x.shape[3]
+    if N == 1:
+        st = sb if B > 1 else H * sh
+    return max(st, (H - 1) * sh + D) if B * N == 1 else st, D if H == 1 else sh
+
+
+def tree_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor, q_out: Optional[torch.Tensor],
+              k_out: Optional[torch.Tensor], rope: RopeConfig, stream=None) -> None:
+    """Rotate q [B,N,Hq,D] and k [B,N,Hkv,D] bf16 at pos [B,N] i32 into the dense
+    q_out and k_out.  q and k may be views of a fused projection (evenly spaced
+    tokens, adjacent channels) or the outputs themselves; either may be None."""
+    B, N = pos.shape
+    _dense("tree_rope", pos, (B, N), torch.int32)
+    p = RopeParams(pos=pos.data_ptr(), B=B, N=N, rotary_dim=rope.rotary_dim, interleaved=int(rope.interleaved),
+                   scaling=ROPE_SCALING.get(rope.scaling, -1), theta=rope.theta, factor=rope.factor,
+                   low_rot=rope.low_rot, high_rot=rope.high_rot, orig_len=rope.orig_len, mscale=rope.mscale)
+    if q is not None:
+        _need(q_out is not None, "tree_rope")
+        p.q_token_stride, p.q_head_stride = _token_heads("tree_rope", q, q_out, B, N)
+        p.q, p.q_out, p.Hq, p.D = q.data_ptr(), q_out.data_ptr(), q.shape[2], q.shape[3]
+    if k is not None:
+        _need(k_out is not None and (q is None or k.shape[3] == q.shape[3]), "tree_rope")
+        p.k_token_stride, p.k_head_stride = _token_heads("tree_rope", k, k_out, B, N)
+        p.k, p.k_out, p.Hkv, p.D = k.data_ptr(), k_out.data_ptr(), k.shape[2], k.shape[3]
+    _same_device("tree_rope", q, k, pos, q_out, k_out)
+    _check(lib().tree_rope(ctypes.byref(p), _s(stream)), "tree_rope")
+
+
+def _q8_pools(where: str, k_cache, v_cache, kv_scale, block_table, B: int, Hkv: int, D: int):
+    nblk, _, bs, _ = k_cache.shape
+    _dense(where, k_cache, (nblk, Hkv, bs, D), *_CODES)
+    _dense(where, v_cache, (nblk, Hkv, bs, D), *_CODES)
+    _dense(where, kv_scale, (nblk, Hkv, bs, 2), torch.uint8)
+    _dense(where, block_table, (B, block_table.shape[1]), torch.int32)
+    return nblk, bs, block_table.shape[1]
+
+
+def tree_cache_append_q8(k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, block_table, new_prefix_len, status=None,
+                         stream=None) -> None:
+    """Quantise the new tokens k, v [T,Hkv,D] bf16 of all sequences (sequence b's
+    are rows cu_len[b] .. cu_len[b+1]-1; heads dense, tokens evenly spaced) into
+    the 8-bit paged cache from prefix_len on, and write new_prefix_len."""
+    where = "tree_cache_append_q8"
+    T, Hkv, D = k.shape
+    B = prefix_len.shape[0]
+    nblk, bs, maxb = _q8_pools(where, k_cache, v_cache, kv_scale, block_table, B, Hkv, D)
+    for x in (k, v):
+        _need(x.dtype == torch.bfloat16 and x.shape == (T, Hkv, D) and x.stride()[2] == 1
+              and (Hkv == 1 or x.stride()[1] == D), where)
+    _dense(where, cu_len, (B + 1,), torch.int32)
+    for x in (prefix_len, new_prefix_len, status):
+        if x is not None:
+            _dense(where, x, (B,), torch.int32)
+    _same_device(where, k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, block_table, new_prefix_len, status)
+    ks, vs = (x.stride()[0] if T > 1 else 0 for x in (k, v))
+    _check(lib().tree_cache_append_q8(_p(k), _p(v), _p(cu_len), _p(prefix_len), _p(k_cache), _p(v_cache),
+                                      _p(kv_scale), _p(block_table), B, T, Hkv, D, ks, vs, bs, nblk, maxb,
+                                      _p(new_prefix_len), _p(status), _s(stream)), where)
+
+
+def tree_commit_accepted_q8(k_tree, v_tree, accepted, accept_len, prefix_len, k_cache, v_cache, kv_scale, block_table,
+                            new_prefix_len, status=None, stream=None) -> None:
+    """tree_commit_accepted into the 8-bit paged cache: the accepted path (root
+    .. n*) of every sequence is quantised as it is appended."""
+    where = "tree_commit_accepted_q8"
+    B, N, Hkv, D = k_tree.shape
+    nblk, bs, maxb = _q8_pools(where, k_cache, v_cache, kv_scale, block_table, B, Hkv, D)
+    _dense(where, k_tree, (B, N, Hkv, D), torch.bfloat16)
+    _dense(where, v_tree, (B, N, Hkv, D), torch.bfloat16)
+    _dense(where, accepted, (B, accepted.shape[1]), torch.int32)
+    for x in (accept_len, prefix_len, new_prefix_len, status):
+        if x is not None:
+            _dense(where, x, (B,), torch.int32)
+    _same_device(where, k_tree, v_tree, accepted, accept_len, prefix_len, k_cache, v_cache, kv_scale, block_table,
+                 new_prefix_len, status)
+    _check(lib().tree_commit_accepted_q8(_p(k_tree), _p(v_tree), _p(accepted), _p(accept_len), _p(prefix_len),
+                                         _p(k_cache), _p(v_cache), _p(kv_scale), _p(block_table), B, N, Hkv, D, bs,
+                                         nblk, maxb, accepted.shape[1] - 1, _p(new_prefix_len), _p(status),
+                                         _s(stream)), where)
+
+
+def tree_attn_q8_workspace_size(params: AttnParams) -> int:
+    return int(lib().tree_attn_q8_workspace_size(ctypes.byref(params)))
+
+
+def tree_attn_fwd_q8(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """tree_attn_fwd over the 8-bit cache: ``params`` from attn_params with the
+    e4m3 pools as k_cache and v_cache, ``kv_scale`` [num_blocks,Hkv,bs,2] uint8."""
+    where = "tree_attn_fwd_q8"
+    _need(all(t in _CODES for t in params.cache_dtypes), where)
+    _dense(where, kv_scale, (params.num_blocks, params.Hkv, params.block_size, 2), torch.uint8)
+    _same_device(where, kv_scale, workspace)
+    _check(lib().tree_attn_fwd_q8(ctypes.byref(params), _p(kv_scale), _p(workspace),
+                                  workspace.numel() * workspace.element_size(), _s(stream)), where)

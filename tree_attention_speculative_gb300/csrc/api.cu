@@ -489,3 +489,204 @@ ts_status tree_verify_greedy_noalloc(const int32_t* draft_tokens, const float* t
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------- rotary positions and the 8-bit cache
+
+namespace ts {
+namespace {
+
+constexpr int MAX_HEADS = 4096;
+
+// Bytes [at, at + n) of two buffers that share any.
+struct Span {
+  uintptr_t at;
+  unsigned long long n;
+};
+Span span(const void* p, unsigned long long n) { return Span{reinterpret_cast<uintptr_t>(p), n}; }
+bool overlap(const Span& a, const Span& b) { return a.n && b.n && a.at < b.at + b.n && b.at < a.at + a.n; }
+
+// A strided [tokens, H, D] input: false when its strides do not hold its rows.
+bool check_strides(int64_t* token, int64_t* head, int H, int D) {
+  if (*head == 0) *head = D;
+  if (*head < D || *head % 8 || *head > (1ll << 40)) return false;
+  const int64_t row = (int64_t)(H - 1) * *head + D;
+  if (*token == 0) *token = (int64_t)H * *head;
+  return *token >= row && *token % 8 == 0 && *token <= (1ll << 40);
+}
+
+// Radians a position for pair i (treespec.h: tree_rope).
+double rope_frequency(const ts_rope_params& p, int R, int i) {
+  double theta = p.theta;
+  if (p.scaling == TS_ROPE_NTK && R > 2) theta *= std::pow(p.factor, (double)R / (R - 2));
+  const double f = std::pow(theta, -2.0 * i / R);
+  if (p.scaling == TS_ROPE_LINEAR) return f / p.factor;
+  if (p.scaling != TS_ROPE_BANDS) return f;
+  const double turns = p.orig_len * f / (2.0 * 3.14159265358979323846);
+  const double g = std::min(1.0, std::max(0.0, (turns - p.low_rot) / (p.high_rot - p.low_rot)));
+  return g * f + (1.0 - g) * f / p.factor;
+}
+
+bool positive(double x) { return x > 0.0 && std::isfinite(x); }
+
+}  // namespace
+}  // namespace ts
+
+extern "C" {
+
+ts_status tree_rope(const ts_rope_params* p, ts_stream stream) {
+  if (!p || !p->pos || (!p->q && !p->k) || (p->q && !p->q_out) || (p->k && !p->k_out)) return TS_ERR_NULL;
+  const int Hq = p->q ? p->Hq : 0, Hkv = p->k ? p->Hkv : 0;
+  if (p->B < 1 || p->N < 1 || (p->q && Hq < 1) || (p->k && Hkv < 1)) return TS_ERR_SHAPE;
+  if ((long long)p->B * p->N > 0x7fffffffll) return TS_ERR_SHAPE;
+  if ((p->D != 64 && p->D != 128) || Hq > MAX_HEADS || Hkv > MAX_HEADS) return TS_ERR_UNSUPPORTED;
+  if (p->scaling < TS_ROPE_NONE || p->scaling > TS_ROPE_BANDS) return TS_ERR_UNSUPPORTED;
+  const int R = p->rotary_dim == 0 ? p->D : p->rotary_dim;
+  if (R < 2 || R > p->D || R % 2) return TS_ERR_SHAPE;
+  if (!positive(p->theta) || !positive(p->mscale)) return TS_ERR_SHAPE;
+  if (p->scaling != TS_ROPE_NONE && !positive(p->factor)) return TS_ERR_SHAPE;
+  if (p->scaling == TS_ROPE_BANDS &&
+      !(p->orig_len > 0 && p->low_rot < p->high_rot && std::isfinite(p->low_rot) && std::isfinite(p->high_rot)))
+    return TS_ERR_SHAPE;
+  RopeArgs a{};
+  a.tokens = p->B * p->N;
+  a.Hq = Hq; a.Hkv = Hkv; a.D = p->D; a.R = R; a.interleaved = p->interleaved != 0;
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  a.k = static_cast<const __nv_bfloat16*>(p->k);
+  a.q_out = static_cast<__nv_bfloat16*>(p->q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(p->k_out);
+  a.pos = p->pos;
+  a.mscale = p->mscale;
+  int64_t qt = p->q_token_stride, qh = p->q_head_stride, kt = p->k_token_stride, kh = p->k_head_stride;
+  // what each buffer spans, for the overlap checks
+  Span in[2] = {}, out[2] = {};
+  bool in_place[2] = {};
+  for (int w = 0; w < 2; ++w) {
+    const void* x = w ? p->k : p->q;
+    if (!x) continue;
+    const void* y = w ? p->k_out : p->q_out;
+    const int H = w ? Hkv : Hq;
+    int64_t &token = w ? kt : qt, &head = w ? kh : qh;
+    if (!check_strides(&token, &head, H, p->D) || !aligned16(x) || !aligned16(y)) return TS_ERR_SHAPE;
+    in[w] = span(x, 2ull * ((unsigned long long)(a.tokens - 1) * token + (H - 1) * head + p->D));
+    out[w] = span(y, 2ull * a.tokens * H * p->D);
+    in_place[w] = x == y && head == p->D && token == (int64_t)H * p->D;
+  }
+  a.q_token = qt; a.q_head = qh; a.k_token = kt; a.k_head = kh;
+  const Span at_pos = span(p->pos, 4ull * a.tokens);
+  for (int w = 0; w < 2; ++w) {
+    if ((!in_place[w] && overlap(out[w], in[w])) || overlap(out[w], in[1 - w]) || overlap(out[w], at_pos))
+      return TS_ERR_SHAPE;
+  }
+  if (overlap(out[0], out[1])) return TS_ERR_SHAPE;
+  for (int i = 0; i < R / 2; ++i) {
+    // the fraction of a turn a position adds; whole turns change nothing
+    const double turn = rope_frequency(*p, R, i) / (2.0 * 3.14159265358979323846);
+    if (!std::isfinite(turn)) return TS_ERR_SHAPE;
+    const double frac = turn - std::floor(turn);
+    a.turn[i] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0;
+  }
+  return launch_rope(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
+ts_status tree_cache_append_q8(const void* k, const void* v, const int32_t* cu_len, const int32_t* prefix_len,
+                               void* k_cache, void* v_cache, uint8_t* kv_scale, const int32_t* block_table, int B,
+                               int T, int Hkv, int D, int64_t k_stride, int64_t v_stride, int block_size,
+                               int num_blocks, int max_blocks, int32_t* new_prefix_len, int32_t* status,
+                               ts_stream stream) {
+  if ((T > 0 && (!k || !v)) || !cu_len || !prefix_len || !k_cache || !v_cache || !kv_scale || !block_table ||
+      !new_prefix_len)
+    return TS_ERR_NULL;
+  if (B < 1 || T < 0 || Hkv < 1 || block_size < 1 || num_blocks < 1 || max_blocks < 1) return TS_ERR_SHAPE;
+  if ((D != 64 && D != 128) || Hkv > MAX_HEADS || block_size % 16 != 0) return TS_ERR_UNSUPPORTED;
+  int64_t head = D;
+  if (!check_strides(&k_stride, &head, Hkv, D) || !check_strides(&v_stride, &head, Hkv, D)) return TS_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kv_scale))
+    return TS_ERR_SHAPE;
+  const Span fresh = span(new_prefix_len, 4ull * B);
+  if (overlap(fresh, span(prefix_len, 4ull * B)) || overlap(fresh, span(cu_len, 4ull * (B + 1ull))) ||
+      (status && overlap(fresh, span(status, 4ull * B))))
+    return TS_ERR_SHAPE;
+  AppendArgs a{};
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.cu_len = cu_len;
+  a.prefix_len = prefix_len;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.kv_scale = kv_scale;
+  a.block_table = block_table;
+  a.new_prefix_len = new_prefix_len;
+  a.status = status;
+  a.B = B; a.T = T; a.Hkv = Hkv; a.D = D; a.bs = block_size; a.num_blocks = num_blocks; a.max_blocks = max_blocks;
+  a.k_token = k_stride;
+  a.v_token = v_stride;
+  return launch_append_q8(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
+ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree, const int32_t* accepted,
+                                  const int32_t* accept_len, const int32_t* prefix_len, void* k_cache, void* v_cache,
+                                  uint8_t* kv_scale, const int32_t* block_table, int B, int N, int Hkv, int D,
+                                  int block_size, int num_blocks, int max_blocks, int max_depth,
+                                  int32_t* new_prefix_len, int32_t* status, ts_stream stream) {
+  if (!k_tree || !v_tree || !accepted || !accept_len || !prefix_len || !k_cache || !v_cache || !kv_scale ||
+      !block_table || !new_prefix_len)
+    return TS_ERR_NULL;
+  if (B < 1 || N < 1 || N > MAX_NODES || Hkv < 1 || block_size < 1 || num_blocks < 1 || max_blocks < 1 ||
+      max_depth < 0)
+    return TS_ERR_SHAPE;
+  if ((D != 64 && D != 128) || Hkv > MAX_HEADS || block_size % 16 != 0) return TS_ERR_UNSUPPORTED;
+  if (!aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kv_scale))
+    return TS_ERR_SHAPE;
+  CommitQ8Args a{};
+  a.k_tree = static_cast<const __nv_bfloat16*>(k_tree);
+  a.v_tree = static_cast<const __nv_bfloat16*>(v_tree);
+  a.accepted = accepted;
+  a.accept_len = accept_len;
+  a.prefix_len = prefix_len;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.kv_scale = kv_scale;
+  a.block_table = block_table;
+  a.new_prefix_len = new_prefix_len;
+  a.status = status;
+  a.B = B; a.N = N; a.Hkv = Hkv; a.D = D; a.bs = block_size; a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks; a.max_depth = max_depth;
+  return launch_commit_q8(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
+size_t tree_attn_q8_workspace_size(const ts_attn_params* p) {
+  if (check_attn(p) != TS_OK) return 0;
+  return ATTN_SCHED_BYTES;
+}
+
+ts_status tree_attn_fwd_q8(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace, size_t workspace_bytes,
+                           ts_stream stream) {
+  const ts_status st = check_attn(p);
+  if (st != TS_OK) return st;
+  if (!kv_scale) return TS_ERR_NULL;
+  if (!aligned16(kv_scale)) return TS_ERR_SHAPE;
+  if (!workspace || workspace_bytes < ATTN_SCHED_BYTES || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return TS_ERR_WORKSPACE;
+  AttnQ8Args q{};
+  AttnArgs& a = q.a;
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  q.k_codes = static_cast<const uint8_t*>(p->k_cache);
+  q.v_codes = static_cast<const uint8_t*>(p->v_cache);
+  q.kv_scale = kv_scale;
+  a.block_table = p->block_table;
+  a.prefix_len = p->prefix_len;
+  a.k_tree = static_cast<const __nv_bfloat16*>(p->k_tree);
+  a.v_tree = static_cast<const __nv_bfloat16*>(p->v_tree);
+  a.anc_mask = p->anc_mask;
+  a.out = static_cast<__nv_bfloat16*>(p->out);
+  a.lse = p->lse;
+  a.status = p->status;
+  a.B = p->B; a.N = p->N; a.Hq = p->Hq; a.Hkv = p->Hkv; a.G = p->Hq / p->Hkv; a.D = p->D;
+  a.W = ceil_div(p->N, 64);
+  a.bs = p->block_size; a.num_blocks = p->num_blocks; a.max_blocks = p->max_blocks;
+  const float scale = p->scale == 0.f ? 1.f / std::sqrt((float)p->D) : p->scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_attn_q8(q, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -254,4 +254,66 @@ constexpr int DYN_MAX_POOL = 1024;
 cudaError_t launch_build_dynamic(const DynArgs& a, cudaStream_t s);
 cudaError_t launch_verify_stoch(const StochArgs& a, cudaStream_t s);
 
+// Rotary positions (strides in elements).
+struct RopeArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  const int32_t* pos;
+  int tokens, Hq, Hkv, D;  // Hq or Hkv is 0 where q or k is absent
+  int R, interleaved;
+  long long q_token, q_head, k_token, k_head;
+  float mscale;
+  int tok;            // tokens a CTA
+  uint64_t turn[64];  // f_i / (2 pi) modulo 1, times 2^64
+};
+cudaError_t launch_rope(RopeArgs a, cudaStream_t s);
+
+// The 8-bit paged cache: e4m3 codes [num_blocks, Hkv, bs, D] for K and V, and
+// scale bytes [num_blocks, Hkv, bs, 2] (K's, V's).
+struct AppendArgs {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int32_t* cu_len;
+  const int32_t* prefix_len;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  uint8_t* kv_scale;
+  const int32_t* block_table;
+  int32_t* new_prefix_len;
+  int32_t* status;
+  int B, T, Hkv, D, bs, num_blocks, max_blocks;
+  long long k_token, v_token;  // elements from one token to the next
+  int rows;                    // (token, head) rows a CTA
+  int len_ctas;                // CTAs that check the sequences and write their lengths
+};
+cudaError_t launch_append_q8(AppendArgs a, cudaStream_t s);
+
+struct CommitQ8Args {
+  const __nv_bfloat16* k_tree;
+  const __nv_bfloat16* v_tree;
+  const int32_t* accepted;
+  const int32_t* accept_len;
+  const int32_t* prefix_len;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  uint8_t* kv_scale;
+  const int32_t* block_table;
+  int32_t* new_prefix_len;
+  int32_t* status;
+  int B, N, Hkv, D, bs, num_blocks, max_blocks, max_depth;
+};
+cudaError_t launch_commit_q8(const CommitQ8Args& a, cudaStream_t s);
+
+// Tree attention over that cache: AttnArgs whose k_cache and v_cache point at
+// the codes.
+struct AttnQ8Args {
+  AttnArgs a;
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const uint8_t* kv_scale;
+};
+cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t s);
+
 }  // namespace ts

@@ -1,0 +1,213 @@
+// Rotary positions of the tree's queries and keys.
+//
+// For a token at position p and each pair i < R/2 of the R rotated channels,
+//   (x, y) -> m (x cos a - y sin a, y cos a + x sin a),  a = p f_i,
+// the pair being channels (i, i + R/2), or (2i, 2i + 1) when interleaved; the
+// other D - R channels are copied.
+//
+// The angle.  Only its fraction of a turn matters, and p is whole, so the host
+// passes f_i / (2 pi) as a 64-bit fixed-point fraction F_i of a turn and the
+// kernel takes p * F_i modulo 2^64: the turns drop out by themselves and what
+// is left is exact to 2^-33 turns for every 32-bit p (a product in fp32 would
+// be off by whole radians past p = 2^24).  sincospif then takes the fraction.
+//
+// Memory-bound: every value is read and written once, 3 flops each.  A CTA
+// takes whole tokens: its R/2 sines and cosines a token are computed once,
+// into shared memory, and every head of the token reads them.  The first
+// loads of the values are issued before the table, so that the sines hide
+// behind them.  A thread's item is two 16-byte chunks, 8 pairs; rotary widths
+// that are no multiple of 16 (and only those) go pair by pair, two bytes at a
+// time.
+#include "internal.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_MAX_TOK = 16;  // tokens a CTA: the table then holds 16 x 64 pairs, 8 KB
+
+__device__ __forceinline__ float2 rope_sincos(int32_t pos, uint64_t turn, float mscale) {
+  const uint64_t a = (uint64_t)(int64_t)pos * turn;
+  const float half_turns = (float)(int32_t)(a >> 32) * 4.656612873077393e-10f;  // 2^-31: in [-1, 1]
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c * mscale, s * mscale);
+}
+
+__device__ __forceinline__ float2 rope_turn(float x, float y, float2 cs) {
+  return make_float2(x * cs.x - y * cs.y, y * cs.x + x * cs.y);
+}
+
+__device__ __forceinline__ float2 up(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+__device__ __forceinline__ uint32_t down(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// Where head `h` of token `t` lies (heads: Hq of q, then Hkv of k).
+struct RopeRow {
+  const __nv_bfloat16* src;
+  __nv_bfloat16* dst;
+};
+__device__ __forceinline__ RopeRow rope_row(const RopeArgs& a, int t, int h) {
+  RopeRow r;
+  if (h < a.Hq) {
+    r.src = a.q + (size_t)t * a.q_token + (size_t)h * a.q_head;
+    r.dst = a.q_out + ((size_t)t * a.Hq + h) * a.D;
+  } else {
+    h -= a.Hq;
+    r.src = a.k + (size_t)t * a.k_token + (size_t)h * a.k_head;
+    r.dst = a.k_out + ((size_t)t * a.Hkv + h) * a.D;
+  }
+  return r;
+}
+
+// Tables of cos, sin of the CTA's tokens: pair i of token k at [k * half + i].
+__device__ __forceinline__ void rope_table(const RopeArgs& a, float2* table, int t0, int ntok) {
+  const int half = a.R / 2;
+  for (int e = threadIdx.x; e < ntok * half; e += ROPE_THREADS) {
+    const int k = e / half;
+    table[e] = rope_sincos(a.pos[t0 + k], a.turn[e - k * half], a.mscale);
+  }
+}
+
+// R a multiple of 16.  Item e of a CTA: item e % per of head e / per of its
+// tokens' heads; items below R/16 of a head rotate, the rest copy.
+template <bool INTERLEAVED>
+__global__ void __launch_bounds__(ROPE_THREADS)
+k_rope_vec(const __grid_constant__ RopeArgs a, FastDiv heads) {
+  __shared__ __align__(16) float2 table[ROPE_MAX_TOK * 64];
+  const int t0 = blockIdx.x * a.tok;
+  const int ntok = min(a.tok, a.tokens - t0);
+  const int lg = a.D == 128 ? 3 : 2;  // items a head: D / 16
+  const int n = (ntok * heads.d) << lg;
+  const int rot = a.R / 16, half = a.R / 2;
+  pdl_wait();
+  pdl_trigger();
+  constexpr int UN = 2;  // items in flight a thread
+  uint4 x[UN], y[UN];
+  const auto at = [&](int e, RopeRow& r, int& k, int& i, int& cx, int& cy) {
+    const int row = e >> lg;
+    k = heads.div(row);
+    r = rope_row(a, t0 + k, row - k * heads.d);
+    i = e & ((1 << lg) - 1);
+    if (i >= rot) {  // copied: two chunks after the rotated channels
+      cx = 16 * i;
+      cy = cx + 8;
+    } else if (INTERLEAVED) {
+      cx = 16 * i;
+      cy = cx + 8;
+    } else {
+      cx = 8 * i;
+      cy = cx + half;
+    }
+  };
+  const auto load = [&](int e0) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int e = e0 + u * ROPE_THREADS;
+      if (e < n) {
+        RopeRow r;
+        int k, i, cx, cy;
+        at(e, r, k, i, cx, cy);
+        x[u] = *reinterpret_cast<const uint4*>(r.src + cx);
+        y[u] = *reinterpret_cast<const uint4*>(r.src + cy);
+      }
+    }
+  };
+  load(threadIdx.x);
+  rope_table(a, table, t0, ntok);
+  __syncthreads();
+  for (int e0 = threadIdx.x; e0 < n; e0 += UN * ROPE_THREADS) {
+    if (e0 != (int)threadIdx.x) load(e0);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int e = e0 + u * ROPE_THREADS;
+      if (e >= n) break;
+      RopeRow r;
+      int k, i, cx, cy;
+      at(e, r, k, i, cx, cy);
+      if (i < rot) {
+        uint32_t* wx = &x[u].x;
+        uint32_t* wy = &y[u].x;
+        const float4* cs = reinterpret_cast<const float4*>(table + k * half + 8 * i);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (INTERLEAVED) {  // a word is a pair: pairs 8i + w in x, 8i + 4 + w in y
+            const float4 c0 = cs[w / 2], c1 = cs[2 + w / 2];
+            const float2 a0 = up(wx[w]), a1 = up(wy[w]);
+            const float2 r0 = rope_turn(a0.x, a0.y, (w & 1) ? make_float2(c0.z, c0.w) : make_float2(c0.x, c0.y));
+            const float2 r1 = rope_turn(a1.x, a1.y, (w & 1) ? make_float2(c1.z, c1.w) : make_float2(c1.x, c1.y));
+            wx[w] = down(r0.x, r0.y);
+            wy[w] = down(r1.x, r1.y);
+          } else {  // words w of x and y hold pairs 8i + 2w and 8i + 2w + 1
+            const float4 c = cs[w];
+            const float2 p = up(wx[w]), q = up(wy[w]);
+            const float2 r0 = rope_turn(p.x, q.x, make_float2(c.x, c.y));
+            const float2 r1 = rope_turn(p.y, q.y, make_float2(c.z, c.w));
+            wx[w] = down(r0.x, r1.x);
+            wy[w] = down(r0.y, r1.y);
+          }
+        }
+      } else if (r.src == r.dst) {
+        continue;  // in place: the copied channels stay
+      }
+      *reinterpret_cast<uint4*>(r.dst + cx) = x[u];
+      *reinterpret_cast<uint4*>(r.dst + cy) = y[u];
+    }
+  }
+}
+
+// Any even R: an item is one pair (or two copied channels).
+__global__ void __launch_bounds__(ROPE_THREADS)
+k_rope_pairs(const __grid_constant__ RopeArgs a, FastDiv heads) {
+  __shared__ __align__(16) float2 table[ROPE_MAX_TOK * 64];
+  const int t0 = blockIdx.x * a.tok;
+  const int ntok = min(a.tok, a.tokens - t0);
+  const int lg = a.D == 128 ? 6 : 5;  // items a head: D / 2
+  const int n = (ntok * heads.d) << lg;
+  const int half = a.R / 2;
+  pdl_wait();
+  pdl_trigger();
+  rope_table(a, table, t0, ntok);
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += ROPE_THREADS) {
+    const int row = e >> lg;
+    const int k = heads.div(row);
+    const RopeRow r = rope_row(a, t0 + k, row - k * heads.d);
+    const int i = e & ((1 << lg) - 1);
+    const int cx = i >= half || a.interleaved ? 2 * i : i;
+    const int cy = i >= half || a.interleaved ? cx + 1 : i + half;
+    const __nv_bfloat16 x = r.src[cx], y = r.src[cy];
+    if (i < half) {
+      const float2 z = rope_turn(__bfloat162float(x), __bfloat162float(y), table[k * half + i]);
+      r.dst[cx] = __float2bfloat16_rn(z.x);
+      r.dst[cy] = __float2bfloat16_rn(z.y);
+    } else {
+      r.dst[cx] = x;
+      r.dst[cy] = y;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
+  const int heads = a.Hq + a.Hkv;
+  const bool vec = a.R % 16 == 0;
+  // Tokens a CTA: enough for two items a thread, but no fewer CTAs than SMs.
+  const int per = vec ? a.D / 16 : a.D / 2;
+  int tok = ceil_div(2 * ROPE_THREADS, heads * per);
+  const int spread = ceil_div(a.tokens, PLAN_SMS);
+  if (tok > spread) tok = spread;
+  a.tok = tok < ROPE_MAX_TOK ? tok : ROPE_MAX_TOK;
+  const dim3 grid(ceil_div(a.tokens, a.tok));
+  const FastDiv fd = FastDiv::make(heads);
+  if (!vec) return launch_pdl(k_rope_pairs, grid, dim3(ROPE_THREADS), 0, s, a, fd);
+  return a.interleaved ? launch_pdl(k_rope_vec<true>, grid, dim3(ROPE_THREADS), 0, s, a, fd)
+                       : launch_pdl(k_rope_vec<false>, grid, dim3(ROPE_THREADS), 0, s, a, fd);
+}
+
+}  // namespace ts

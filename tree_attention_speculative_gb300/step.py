@@ -3,8 +3,10 @@
 ``TreeVerifyStep`` owns the output and workspace buffers (allocated with torch,
 which is only the allocator here) for fixed sizes and enqueues
 tree_build_ancestry -> tree_attn_fwd -> tree_verify_greedy on one stream (their
-_forest variants with ``forest=True``).  Every computation happens in the
-library's kernels.  ``PackedInputs`` stages a step's inputs from host memory
+_forest variants with ``forest=True``).  With a ``rope`` configuration it
+positions q and k_tree in between (tree_rope), with ``kv_scale`` it reads an
+8-bit cache (tree_attn_fwd_q8), and ``commit`` appends the accepted path to
+either cache.  Every computation happens in the library's kernels.  ``PackedInputs`` stages a step's inputs from host memory
 in one copy.
 """
 from __future__ import annotations
@@ -14,8 +16,9 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (attn_params, tree_attn_fwd, tree_attn_workspace_size, tree_build_ancestry,
-               tree_build_ancestry_forest, tree_verify_greedy, tree_verify_greedy_forest,
+from . import (RopeConfig, attn_params, tree_attn_fwd, tree_attn_fwd_q8, tree_attn_q8_workspace_size,
+               tree_attn_workspace_size, tree_build_ancestry, tree_build_ancestry_forest, tree_commit_accepted,
+               tree_commit_accepted_q8, tree_rope, tree_verify_greedy, tree_verify_greedy_forest,
                tree_verify_workspace_size)
 
 
@@ -65,7 +68,8 @@ class PackedInputs:
 
 class TreeVerifyStep:
     def __init__(self, B: int, N: int, Hq: int, Hkv: int, D: int, prefix_len_host, vocab: int = 0,
-                 max_depth: Optional[int] = None, device="cuda", scale: float = 0.0, forest: bool = False):
+                 max_depth: Optional[int] = None, device="cuda", scale: float = 0.0, forest: bool = False,
+                 rope: Optional[RopeConfig] = None):
         self.B, self.N, self.Hq, self.Hkv, self.D = B, N, Hq, Hkv, D
         self.forest = forest
         self.vocab = vocab
@@ -83,6 +87,10 @@ class TreeVerifyStep:
         self.out = torch.empty(B, N, Hq, D, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev)
         self.ws_attn = None
+        self.rope = rope
+        if rope is not None:
+            self.q_rot = torch.empty(B, N, Hq, D, dtype=torch.bfloat16, device=dev)
+            self.k_rot = torch.empty(B, N, Hkv, D, dtype=torch.bfloat16, device=dev)
         if vocab > 0:
             nb = tree_verify_workspace_size(B, N, vocab)
             # zero-filled once; the verify kernel leaves its counters at zero
@@ -103,15 +111,26 @@ class TreeVerifyStep:
         build = tree_build_ancestry_forest if self.forest else tree_build_ancestry
         build(parent, prefix_len, self.anc, self.depth, self.pos, self.status, stream)
 
-    def attention(self, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, stream=None):
+    def position(self, q, k_tree, stream=None):
+        """q and k_tree rotated at the nodes' positions (their own tensors
+        without a rope configuration); the rotated keys are what commit appends."""
+        if self.rope is None:
+            return q, k_tree
+        tree_rope(q, k_tree, self.pos, self.q_rot, self.k_rot, self.rope, stream)
+        return self.q_rot, self.k_rot
+
+    def attention(self, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, stream=None, kv_scale=None):
         p = self._params(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree)
-        need = tree_attn_workspace_size(p)
+        need = tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
         if need == 0:
             raise ValueError("tree_attn_fwd would reject these arguments")
         if self.ws_attn is None or self.ws_attn.numel() < need:
             # zero-filled once; every call leaves its head (the item counter) zero again
             self.ws_attn = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        tree_attn_fwd(p, self.ws_attn, stream)
+        if kv_scale is None:
+            tree_attn_fwd(p, self.ws_attn, stream)
+        else:
+            tree_attn_fwd_q8(p, kv_scale, self.ws_attn, stream)
 
     def verify(self, draft, logits, parent, stream=None):
         verify = tree_verify_greedy_forest if self.forest else tree_verify_greedy
@@ -119,8 +138,22 @@ class TreeVerifyStep:
                self.status, self.ws_verify, stream)
 
     def run(self, parent, prefix_len, q, k_cache, v_cache, block_table, k_tree, v_tree, draft=None, logits=None,
-            stream=None):
+            stream=None, kv_scale=None):
         self.ancestry(parent, prefix_len, stream)
-        self.attention(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, stream)
+        q, k_tree = self.position(q, k_tree, stream)
+        self.attention(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, stream, kv_scale)
         if logits is not None:
             self.verify(draft, logits, parent, stream)
+
+    def commit(self, k_tree, v_tree, prefix_len, k_cache, v_cache, block_table, new_prefix_len, stream=None,
+               kv_scale=None):
+        """Append the accepted path of the last ``run`` (with a rope configuration
+        its rotated keys, in place of k_tree) to the bf16 cache, or to the 8-bit
+        one with its ``kv_scale``."""
+        k = k_tree if self.rope is None else self.k_rot
+        if kv_scale is None:
+            tree_commit_accepted(k, v_tree, self.accepted, self.accept_len, prefix_len, k_cache, v_cache, block_table,
+                                 new_prefix_len, self.status, stream)
+        else:
+            tree_commit_accepted_q8(k, v_tree, self.accepted, self.accept_len, prefix_len, k_cache, v_cache, kv_scale,
+                                    block_table, new_prefix_len, self.status, stream)
