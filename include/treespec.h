@@ -597,6 +597,20 @@ TS_API size_t tree_attn_q8_workspace_size(const ts_attn_params* p);
 TS_API ts_status tree_attn_fwd_q8(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace,
                                   size_t workspace_bytes, ts_stream stream);
 
+/*
+ * tree_attn_fwd_q8_stall_test — for testing the failure path only:
+ * tree_attn_fwd_q8 with sequence `stall_seq`'s key stream stopped before tile
+ * `stall_tile` of each of its segments (tree tiles first, then 128-token prefix
+ * tiles), and every bounded wait limited to `wait_limit_us`.  A CTA whose wait
+ * runs out sets status[b] = TS_ERR_TIMEOUT for the sequence b of every segment
+ * it had not finished; the outputs of those sequences are unspecified, the
+ * other sequences' are those of tree_attn_fwd_q8, and the device stays usable.
+ * Returns as tree_attn_fwd_stall_test.
+ */
+TS_API ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace,
+                                             size_t workspace_bytes, int stall_seq, int stall_tile,
+                                             uint32_t wait_limit_us, ts_stream stream);
+
 /* Size of the library-owned scratch behind tree_verify_greedy_noalloc. */
 #define TS_VERIFY_NOALLOC_SCRATCH_BYTES ((size_t)4 << 20)
 

@@ -378,3 +378,48 @@ def test_a_serving_loop():
         host = (host + L + 1).astype(np.int32)
         assert new.cpu().tolist() == host.tolist() and step.status.cpu().tolist() == [0] * B
         plen = new
+
+
+@pytest.mark.parametrize("host", [[3000, 100, 0], [900, 5000, 300]], ids=["grown", "mixed"])
+def test_device_lengths_other_than_planned(host):
+    """A captured launch keeps its plan while the device's lengths move, within the block table."""
+    case = _case("moved", 3, 20, 8, 2, 128, [2500, 2600, 700], 16, "levels")
+    pools = quantised_pools(case)
+    true_len = case.prefix_len
+    case.prefix_len = np.array(host, np.int32)
+    width = 400
+    table = np.full((3, width), -1, np.int32)
+    table[:, :case.block_table.shape[1]] = case.block_table
+    mask = oracle.tree.build_ancestry(case.parent, true_len)[0]
+    call, out, lse, status, _ = _raw(case, pools, plen_dev=true_len.tolist(), table=table, mask=mask)
+    call()
+    assert status.cpu().tolist() == [0] * 3
+    case.prefix_len = true_len
+    check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())
+
+
+# (these lengths plan as runs of 6 tiles' weight, so a segment has at most 6 tiles to stall before)
+@pytest.mark.parametrize("stall_tile", [0, 1, 2])
+def test_a_wait_that_runs_out_is_reported(stall_tile):
+    """One sequence's key stream stops: it reports TS_ERR_TIMEOUT, sequences that report nothing
+    are right, and the next call on the same workspace is right everywhere."""
+    import tree_attention_speculative_gb300 as ts
+    case = _case("stall", 4, 26, 8, 2, 128, [3000, 2000, 64, 1500], 16, "widths")
+    pools = quantised_pools(case)
+    call, out, lse, status, ws = _raw(case, pools)
+    t, kc, vc, sc, anc, plen, tab, _ = call.keep
+    p = ts.attn_params(t["q"], kc, vc, tab, plen, case.prefix_len, t["k_tree"], t["v_tree"], anc, None, out, lse, status)
+    ts.tree_attn_fwd_q8_stall_test(p, sc, ws, 1, stall_tile, 20000)
+    torch.cuda.synchronize()
+    st = status.cpu().tolist()
+    assert st[1] == -6 and set(st) <= {0, -6}
+    got = out.double().cpu().numpy()
+    ref, A = oracle.attention.tree_attention_case(case), _abs_v(case)
+    for b in range(4):
+        if st[b] == 0:
+            tol = (2.0 ** -8 + 2.0 ** -10) * A[b] + 2.0 ** -8 * np.abs(ref[0][b])
+            assert (np.abs(got[b] - ref[0][b]) <= tol).all()
+    status.zero_()
+    call()
+    assert status.cpu().tolist() == [0] * 4
+    check(case, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, A)

@@ -124,3 +124,11 @@ def test_binding_checks_types_and_shapes(ts):  # noqa: F811
         p = ts.attn_params(z(3, 6, 4, 64), z(9, 2, 16, 64), z(9, 2, 16, 64), i(3, 5), i(3), np.zeros(3, np.int32),
                            z(3, 6, 2, 64), z(3, 6, 2, 64), torch.zeros(3, 6, 1, dtype=torch.int64), None, z(3, 6, 4, 64))
         ts.tree_attn_fwd_q8(p, u(9, 2, 16, 2), u(1024))
+
+
+def test_stall_test_refuses(ts):  # noqa: F811
+    p = _params(ts)
+    n = ts.tree_attn_q8_workspace_size(p)
+    call = lambda seq, tile, us: ts.lib().tree_attn_fwd_q8_stall_test(ctypes.byref(p), A, A, n, seq, tile, us, None)  # noqa: E731
+    assert call(-1, 0, 1000) == SHAPE and call(2, 0, 1000) == SHAPE and call(0, -1, 1000) == SHAPE
+    assert call(0, 0, 99) == UNSUPPORTED and call(0, 0, 1000001) == UNSUPPORTED

@@ -99,7 +99,8 @@ EXPORTS = ("ts_status_str", "tree_build_ancestry", "tree_attn_workspace_size", "
            "tree_verify_workspace_size", "tree_verify_greedy", "tree_verify_greedy_noalloc",
            "tree_commit_accepted", "tree_verify_stochastic", "tree_build_dynamic", "tree_build_ancestry_forest",
            "tree_verify_greedy_forest", "tree_attn_fwd_stall_test", "tree_attn_fwd_ctas_test", "tree_rope",
-           "tree_cache_append_q8", "tree_commit_accepted_q8", "tree_attn_q8_workspace_size", "tree_attn_fwd_q8")
+           "tree_cache_append_q8", "tree_commit_accepted_q8", "tree_attn_q8_workspace_size", "tree_attn_fwd_q8",
+           "tree_attn_fwd_q8_stall_test")
 
 # TS_VERIFY_NOALLOC_SCRATCH_BYTES of treespec.h
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -160,6 +161,8 @@ def lib() -> ctypes.CDLL:
         L.tree_attn_q8_workspace_size.restype = sz
         L.tree_attn_fwd_q8.argtypes = [ctypes.POINTER(AttnParams), vp, vp, sz, vp]
         L.tree_attn_fwd_q8.restype = i32
+        L.tree_attn_fwd_q8_stall_test.argtypes = [ctypes.POINTER(AttnParams), vp, vp, sz, i32, i32, ctypes.c_uint32, vp]
+        L.tree_attn_fwd_q8_stall_test.restype = i32
         _LIB = L
     return _LIB
 
@@ -455,12 +458,26 @@ def tree_attn_q8_workspace_size(params: AttnParams) -> int:
     return int(lib().tree_attn_q8_workspace_size(ctypes.byref(params)))
 
 
-def tree_attn_fwd_q8(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
-    """tree_attn_fwd over the 8-bit cache: ``params`` from attn_params with the
-    e4m3 pools as k_cache and v_cache, ``kv_scale`` [num_blocks,Hkv,bs,2] uint8."""
-    where = "tree_attn_fwd_q8"
+def _check_attn_q8(where: str, params: AttnParams, kv_scale, workspace):
     _need(all(t in _CODES for t in params.cache_dtypes), where)
     _dense(where, kv_scale, (params.num_blocks, params.Hkv, params.block_size, 2), torch.uint8)
     _same_device(where, kv_scale, workspace)
+
+
+def tree_attn_fwd_q8(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """tree_attn_fwd over the 8-bit cache: ``params`` from attn_params with the
+    e4m3 pools as k_cache and v_cache, ``kv_scale`` [num_blocks,Hkv,bs,2] uint8."""
+    _check_attn_q8("tree_attn_fwd_q8", params, kv_scale, workspace)
     _check(lib().tree_attn_fwd_q8(ctypes.byref(params), _p(kv_scale), _p(workspace),
-                                  workspace.numel() * workspace.element_size(), _s(stream)), where)
+                                  workspace.numel() * workspace.element_size(), _s(stream)), "tree_attn_fwd_q8")
+
+
+def tree_attn_fwd_q8_stall_test(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stall_seq: int,
+                                stall_tile: int, wait_limit_us: int, stream=None) -> None:
+    """Testing only: tree_attn_fwd_q8 with sequence ``stall_seq``'s key stream
+    stopped before tile ``stall_tile`` of its segments, so a bounded wait runs out."""
+    where = "tree_attn_fwd_q8_stall_test"
+    _check_attn_q8(where, params, kv_scale, workspace)
+    _check(lib().tree_attn_fwd_q8_stall_test(ctypes.byref(params), _p(kv_scale), _p(workspace),
+                                             workspace.numel() * workspace.element_size(), stall_seq, stall_tile,
+                                             wait_limit_us, _s(stream)), where)

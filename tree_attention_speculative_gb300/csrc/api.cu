@@ -158,6 +158,8 @@ cudaError_t prepare_device(int* stoch_max_cluster = nullptr) {
   if (!done[dev]) {
     e = attn_tc_prepare();
     if (e != cudaSuccess) return e;
+    e = attn_q8_prepare();
+    if (e != cudaSuccess) return e;
     e = stoch_prepare(&max_cluster[dev]);
     if (e != cudaSuccess) return e;
     done[dev] = true;
@@ -528,6 +530,48 @@ double rope_frequency(const ts_rope_params& p, int R, int i) {
 
 bool positive(double x) { return x > 0.0 && std::isfinite(x); }
 
+ts_status check_attn_q8(const ts_attn_params* p) {
+  const ts_status st = check_attn(p);
+  if (st != TS_OK) return st;
+  // (row tile, sequence, KV head) chains are numbered in an int
+  const long long row_tiles = ceil_div(p->N * (p->Hq / p->Hkv), ROW_TILE);
+  return row_tiles * p->B * p->Hkv < (1ll << 30) ? TS_OK : TS_ERR_UNSUPPORTED;
+}
+
+ts_status attn_q8_impl(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace, size_t workspace_bytes,
+                       ts_stream stream, int stall_seq, int stall_tile, unsigned long long wait_limit_ns) {
+  const ts_status st = check_attn_q8(p);
+  if (st != TS_OK) return st;
+  if (!kv_scale) return TS_ERR_NULL;
+  if (!aligned16(kv_scale)) return TS_ERR_SHAPE;
+  if (!workspace || workspace_bytes < attn_q8_workspace(p) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return TS_ERR_WORKSPACE;
+  AttnQ8Args q{};
+  AttnArgs& a = q.a;
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  q.k_codes = static_cast<const uint8_t*>(p->k_cache);
+  q.v_codes = static_cast<const uint8_t*>(p->v_cache);
+  q.kv_scale = kv_scale;
+  a.block_table = p->block_table;
+  a.prefix_len = p->prefix_len;
+  a.k_tree = static_cast<const __nv_bfloat16*>(p->k_tree);
+  a.v_tree = static_cast<const __nv_bfloat16*>(p->v_tree);
+  a.anc_mask = p->anc_mask;
+  a.out = static_cast<__nv_bfloat16*>(p->out);
+  a.lse = p->lse;
+  a.status = p->status;
+  a.B = p->B; a.N = p->N; a.Hq = p->Hq; a.Hkv = p->Hkv; a.G = p->Hq / p->Hkv; a.D = p->D;
+  a.W = ceil_div(p->N, 64);
+  a.bs = p->block_size; a.num_blocks = p->num_blocks; a.max_blocks = p->max_blocks;
+  const float scale = p->scale == 0.f ? 1.f / std::sqrt((float)p->D) : p->scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_limit_ns = wait_limit_ns;
+  a.stall_seq = stall_seq;
+  a.stall_tile = stall_tile;
+  if (prepare_device() != cudaSuccess) return TS_ERR_CUDA;
+  return launch_attn_q8(q, p, workspace, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace ts
 
@@ -655,38 +699,22 @@ ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree, const 
 }
 
 size_t tree_attn_q8_workspace_size(const ts_attn_params* p) {
-  if (check_attn(p) != TS_OK) return 0;
-  return ATTN_SCHED_BYTES;
+  if (check_attn_q8(p) != TS_OK) return 0;
+  return attn_q8_workspace(p);
 }
 
 ts_status tree_attn_fwd_q8(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace, size_t workspace_bytes,
                            ts_stream stream) {
-  const ts_status st = check_attn(p);
-  if (st != TS_OK) return st;
-  if (!kv_scale) return TS_ERR_NULL;
-  if (!aligned16(kv_scale)) return TS_ERR_SHAPE;
-  if (!workspace || workspace_bytes < ATTN_SCHED_BYTES || (reinterpret_cast<uintptr_t>(workspace) & 255))
-    return TS_ERR_WORKSPACE;
-  AttnQ8Args q{};
-  AttnArgs& a = q.a;
-  a.q = static_cast<const __nv_bfloat16*>(p->q);
-  q.k_codes = static_cast<const uint8_t*>(p->k_cache);
-  q.v_codes = static_cast<const uint8_t*>(p->v_cache);
-  q.kv_scale = kv_scale;
-  a.block_table = p->block_table;
-  a.prefix_len = p->prefix_len;
-  a.k_tree = static_cast<const __nv_bfloat16*>(p->k_tree);
-  a.v_tree = static_cast<const __nv_bfloat16*>(p->v_tree);
-  a.anc_mask = p->anc_mask;
-  a.out = static_cast<__nv_bfloat16*>(p->out);
-  a.lse = p->lse;
-  a.status = p->status;
-  a.B = p->B; a.N = p->N; a.Hq = p->Hq; a.Hkv = p->Hkv; a.G = p->Hq / p->Hkv; a.D = p->D;
-  a.W = ceil_div(p->N, 64);
-  a.bs = p->block_size; a.num_blocks = p->num_blocks; a.max_blocks = p->max_blocks;
-  const float scale = p->scale == 0.f ? 1.f / std::sqrt((float)p->D) : p->scale;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  return launch_attn_q8(q, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+  return ts::attn_q8_impl(p, kv_scale, workspace, workspace_bytes, stream, -1, 0, ATTN_WAIT_LIMIT_NS);
+}
+
+ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace,
+                                      size_t workspace_bytes, int stall_seq, int stall_tile, uint32_t wait_limit_us,
+                                      ts_stream stream) {
+  if (p && (stall_seq < 0 || stall_seq >= p->B || stall_tile < 0)) return TS_ERR_SHAPE;
+  if (wait_limit_us < 100 || wait_limit_us > 1000000) return TS_ERR_UNSUPPORTED;
+  return ts::attn_q8_impl(p, kv_scale, workspace, workspace_bytes, stream, stall_seq, stall_tile,
+                          (unsigned long long)wait_limit_us * 1000ull);
 }
 
 }  // extern "C"

@@ -1,92 +1,1100 @@
-// Tree attention over the 8-bit paged cache: one warp a query row, one key at
-// a time, with a running maximum and sum.
+// Tree attention over the 8-bit paged cache, on tcgen05 with TMEM and TMA.
+//
+// The mathematics is that of attn_tc.cu: the G query heads of a sequence's N
+// nodes are packed as the rows of one (sequence, KV head) unit, 128 rows a
+// tile, and one online softmax runs over the tree's own keys (gated by the
+// ancestry bits) and the prefix in 128-token tiles.  What differs is that a
+// prefix row is D e4m3 codes and a power of two.
+//
+// Keys stay 8-bit.  q . k is taken on e4m3 tensor operands with q split in
+// two: with the row of q scaled by a power of two to within 448, hi = e4m3(q)
+// and lo = e4m3(q - hi) hold all 8 bits of a bf16 significand, exactly for
+// channels down to 2^-10 of the row's largest and to 2^-18 of it below that.
+// S = hi . k + lo . k then costs as many MMA cycles as bf16 (e4m3 runs at twice
+// its rate) and the keys need no conversion; the key's power of two and the
+// row's multiply the logits in fp32.
+// Values are widened to bf16, which holds code * 2^e exactly (a 4-bit
+// significand), so P V is the bf16 product of the bf16 kernel.
+//
+// Bytes: 2 D + 2 a token and KV head, half of bf16.  At 128 rows a tile a tile
+// is 32.5 KB, 0.73 us of one SM's share of HBM, about what its products (1024
+// MMA cycles) and its exponentials take: up to 128 rows a unit the kernel is
+// bound by HBM and softmax alike, beyond that by the products and the softmax.
+//
+// Work split.  A chain is one row tile of one unit: its tree tiles, then its
+// prefix tiles.  The host lays all chains end to end, row tile by row tile, and
+// cuts them into one run of equal weight a CTA (one CTA an SM), so every SM
+// finishes at the same time whatever the lengths.  CTAs of the same units and
+// different row tiles run in step and share the K/V tiles in L2.  A CTA does
+// whole chains and at most two parts of chains; a part leaves a partial
+// (16-bit, with a power of two a row, and its fp32 log-sum-exp), and
+// k_merge_q8 joins the parts of each cut chain.  The lists are static: every
+// role walks its CTA's run by itself.  A chain's lengths are the device's, so a
+// captured launch stays right when prefixes have grown since the plan.
+//
+//   warp 0       TMEM allocation; TMA loads of the K codes (and bf16 tree keys)
+//   warp 1       QK issuer: loads each segment's Q tile; S(j) = Q K(j)^T
+//   warp 2       PV issuer: O += P(j) V(j)
+//   warp 3       TMA loads of the V codes
+//   warps 4-7    softmax: thread r owns row r (TMEM lane r)
+//   warps 8-11   conversion: thread t owns token t of a tile.  Splits the Q tile
+//                into hi and lo (in place, row by row), fetches the tokens'
+//                scale bytes two tiles ahead, hands the keys' powers of two to
+//                the softmax, widens V to bf16 with the values' (rows past the
+//                prefix become zeros).  The tree's V is loaded straight into
+//                the widened buffer.
+//
+// Every wait is bounded; one that runs out aborts the CTA, which lets what it
+// has in flight land and reports TS_ERR_TIMEOUT for the sequences of the
+// segments it did not finish.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "internal.cuh"
+#include "fastexp.cuh"
+#include "quant_row.cuh"
+#include "sm100.cuh"
+#include "tensor_map.cuh"
+
+#include <algorithm>
 
 namespace ts {
 namespace {
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-__device__ __forceinline__ float scale_of(uint8_t s) { return __uint_as_float((uint32_t)s << 23); }
+using namespace sm100;
+
+constexpr int THREADS = 384;
+constexpr int GROUP_THREADS = 128;  // softmax, and conversion
+constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4, CONVERT_WARP0 = 8;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TMEM_O = 0;
+constexpr uint32_t TMEM_S0 = 128;
+constexpr int NSB = 3;  // S buffers
+constexpr int NT = 4;   // tiles' key scales in flight
+constexpr int NVB = 2;  // widened V tiles
+constexpr int SLOT = 16384;  // a ring slot: 128 tokens of 128 codes, or a 64-column half of a bf16 tree tile
+constexpr int REG_LAUNCH = 168, REG_CONTROL = 112, REG_SOFTMAX = 240, REG_CONVERT = 152;
+static_assert(REG_CONTROL + REG_SOFTMAX + REG_CONVERT <= 3 * REG_LAUNCH, "warpgroups share what the launch was given");
+constexpr float RESCALE_THRESHOLD = 20.0f;  // as in attn_tc.cu: O follows the running max only past 2^20
+constexpr float NEG_INF = -INFINITY;
 
 template <int D>
-__global__ void __launch_bounds__(256)
-k_attn_q8_rows(const __grid_constant__ AttnQ8Args q) {
-  constexpr int C = D / 32;
-  const AttnArgs& a = q.a;
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int WIDE_BYTES = KV_TILE * D * 2;  // a bf16 tile, and the Q tile
+  static constexpr int HALF_BYTES = KV_TILE * 128;
+  // As many tiles in flight as shared memory holds; a V tile also has a widened buffer to wait in.
+  static constexpr int NSK = D == 128 ? 4 : 5;
+  static constexpr int NSV = D == 128 ? 3 : 5;
+};
+
+template <int D>
+struct __align__(1024) Smem {
+  using C = Cfg<D>;
+  uint8_t q[C::WIDE_BYTES];  // bf16 [half][row][128 B]; then the row's 128-byte pieces hold hi and lo
+  uint8_t k[C::NSK][SLOT];
+  uint8_t v[C::NSV][SLOT];
+  uint8_t vb[NVB][C::WIDE_BYTES];  // bf16 [half][token][128 B]
+  // Scales of tile j (entry j % NT): the token's power of two for its key, and
+  // the row's factor (the query's power of two times scale * log2 e).
+  float key_scale[NT][KV_TILE];
+  float row_scale[NT][ROW_TILE];
+  // q_free: no product reads the bf16 Q any more, it may be split in place
+  uint64_t q_full, q_free, q8_full, q_empty;
+  uint64_t k_full[C::NSK], k_empty[C::NSK];
+  uint64_t v_full[C::NSV], v_empty[C::NSV];
+  uint64_t vb_full[NVB], vb_empty[NVB], vt_full[NVB];
+  uint64_t t_full[NT], t_empty[NT];
+  uint64_t s_full[NSB], p_full[NSB], s_free[NSB];
+  uint64_t o_ready;
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  int abort_flag;
+  int pv_done;    // PVs completed, published by the PV issuer
+  int segs_done;  // segments stored
+};
+
+// The CTAs' runs: CTA c starts at tile tile[c] of chain chain[c] and ends where
+// c + 1 starts.  Chain (rt * B + b) * Hkv + g.
+constexpr int MAX_CTAS = 256;
+struct Runs {
+  int n;
+  int chain[MAX_CTAS + 1];
+  int tile[MAX_CTAS + 1];
+};
+
+struct Q8Args {
+  AttnArgs a;
+  const uint8_t* kv_scale;
+  __half* part_o;    // [2 n, 128, D]: parts of chains, normalised, times a row's 1 / part_ls.y
+  float2* part_ls;   // [2 n, 128]: base-2 log-sum-exp, factor
+  int box_rows, nodes_per_tile, units, n_tree;
+  int out32;
+  FastDiv fd_units, fd_hkv, fd_bs, fd_g;
+  Runs runs;
+};
+
+// A segment: tiles [t_begin, t_begin + n_prefix) of a chain, and its tree tiles
+// if it begins the chain.
+struct Seg {
+  int rt, b, g;
+  int t_begin, n_prefix, n_tree, n_tiles;
+  int P;
+  bool p_ok;
+  bool whole;  // all of the chain: its rows are the output
+};
+__host__ __device__ __forceinline__ Seg make_seg(int chain, int cta, int p_dev, const Q8Args& t) {
+  Seg s;
+  s.rt = t.fd_units.div(chain);
+  const int u = chain - s.rt * t.units;
+  s.b = t.fd_hkv.div(u);
+  s.g = u - s.b * t.a.Hkv;
+  const long long cap = min((long long)t.a.max_blocks * t.a.bs, 1ll << 30);
+  s.P = (int)min((long long)max(p_dev, 0), cap);
+  s.p_ok = s.P == p_dev;
+  const int tiles = prefix_tiles(s.P);
+  const bool from_start = chain != t.runs.chain[cta] || t.runs.tile[cta] == 0;
+  const bool to_end = chain != t.runs.chain[cta + 1];
+  s.t_begin = from_start ? 0 : min(t.runs.tile[cta], tiles);
+  const int t_end = to_end ? tiles : min(t.runs.tile[cta + 1], tiles);
+  s.n_prefix = max(t_end - s.t_begin, 0);
+  s.n_tree = from_start ? t.n_tree : 0;
+  s.n_tiles = s.n_prefix + s.n_tree;
+  s.whole = from_start && to_end;
+  return s;
+}
+__host__ __device__ __forceinline__ int seq_of(int chain, const Q8Args& t) {
+  const int u = chain - t.fd_units.div(chain) * t.units;
+  return t.fd_hkv.div(u);
+}
+
+struct Ctl {
+  volatile int* flag;
+  uint64_t limit;
+};
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*c.flag) return false;
+    if (globaltimer_ns() - t0 > c.limit) {
+      *c.flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_count(const int* counter, int target, const Ctl& c) {
+  const uint32_t addr = smem_u32(counter);
+  uint64_t t0 = 0;
+  while (true) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    if (v >= target) return true;
+    if (*c.flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > c.limit) {
+      *c.flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void publish(int* counter, int v) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(counter)), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2_of(int biased) { return __uint_as_float((uint32_t)biased << 23); }
+
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 16 codes times a power of two as bf16 (exact), two 16-byte chunks.
+__device__ __forceinline__ void widen16(const uint4& c, float scale, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  const uint64_t s2 = fx::pack2(scale, scale);
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t h;  // two codes as fp16
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    float x, y;
+    fx::unpack2(fx::mul2(fx::pack2(f.x, f.y), s2), x, y);
+    o[k] = pack_bf16x2(x, y);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint64_t>(p)),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorMap tm_q,
+          const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
+          const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = args.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Ctl ctl{&sm.abort_flag, a.wait_limit_ns};
+  const int cta = blockIdx.x;
+  const int chain0 = args.runs.chain[cta];
+  // the run's last chain: where the next CTA starts, unless that is the chain's first tile
+  const int chain1 = args.runs.chain[cta + 1] - (args.runs.tile[cta + 1] == 0 ? 1 : 0);
+
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    sm.pv_done = 0;
+    sm.segs_done = 0;
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_free, 1);
+    mbar_init(&sm.q8_full, GROUP_THREADS);
+    mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < C::NSK; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::NSV; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], GROUP_THREADS);
+    }
+    for (int i = 0; i < NVB; ++i) {
+      mbar_init(&sm.vb_full[i], GROUP_THREADS);
+      mbar_init(&sm.vb_empty[i], 1);
+      mbar_init(&sm.vt_full[i], 1);
+    }
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(&sm.t_full[i], GROUP_THREADS);
+      mbar_init(&sm.t_empty[i], GROUP_THREADS / 32);
+    }
+    for (int i = 0; i < NSB; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], GROUP_THREADS);
+      mbar_init(&sm.s_free[i], 1);
+    }
+    mbar_init(&sm.o_ready, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
+    fence_barrier_init();
+  }
+  if (warp == V_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kc);
+    tma_prefetch_desc(&tm_vc);
+    tma_prefetch_desc(&tm_kt);
+    tma_prefetch_desc(&tm_vt);
+  }
+  if (warp == K_WARP) tmem_alloc(&sm.tmem_base, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  pdl_wait();
+
+  // what a role has started and not seen land, for the teardown of an aborted CTA
+  int issued = 0;                  // K or V ring slots this warp filled
+  int q_issued = 0, q_landed = 0;  // Q tiles
+  int vt_issued[NVB] = {0, 0};     // tree V tiles, by buffer
+
+  // Each warpgroup changes its registers where its own code begins, not before
+  // a join: the softmax holds a row of S, taken from the others' shares.
+  if (warp < SOFTMAX_WARP0) {
+  reg_dec<REG_CONTROL>();
+  if (warp == K_WARP || warp == V_WARP) {
+    // ------------------------------------------------------------ K or V codes
+    const bool is_v = warp == V_WARP;
+    const CUtensorMap* tm_pool = is_v ? &tm_vc : &tm_kc;
+    uint64_t* full = is_v ? sm.v_full : sm.k_full;
+    uint64_t* empty = is_v ? sm.v_empty : sm.k_empty;
+    const int nst = is_v ? C::NSV : C::NSK;
+    const int g_box = args.box_rows, lg_boxes = __ffs(KV_TILE / g_box) - 1, g_boxes = 1 << lg_boxes;
+    const int g_tpg = 32 >> lg_boxes;  // tiles a group of 32 table entries covers
+    const uint32_t box_bytes = g_box * D;
+    const int koff = (lane & (g_boxes - 1)) * g_box;
+    const int row_step = args.fd_bs.mod(KV_TILE);
+    int slot = 0, phase = 0;
+    bool ok = true;
+    // the next slot once it is free; false if the wait gave up
+    auto take = [&]() -> bool {
+      bool r = true;
+      if (issued >= nst) {
+        if (lane == 0) r = wait_bar(&empty[slot], phase ^ 1, ctl);
+        r = __shfl_sync(0xffffffffu, r, 0);
+      }
+      return r;
+    };
+    auto next = [&]() {
+      ++issued;
+      if (++slot == nst) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
+    for (int chain = chain0; ok && chain <= chain1; ++chain) {
+      const Seg I = make_seg(chain, cta, p_next, args);
+      if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];  // on its way while this one runs
+      const int stop = !is_v && I.b == a.stall_seq ? a.stall_tile : I.n_tiles;
+      if (!is_v) {
+        for (int tt = 0; ok && tt < I.n_tree; ++tt) {
+          if (tt == stop) ok = false;
+          for (int h = 0; ok && h < C::HALVES; ++h) {
+            if (!(ok = take())) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&full[slot], C::HALF_BYTES);
+              tma_load_4d(sm.k[slot], &tm_kt, &full[slot], 64 * h, I.g, tt * KV_TILE, I.b);
+            }
+            __syncwarp();
+            next();
+          }
+        }
+      }
+      const int* table_row = a.block_table + (size_t)I.b * a.max_blocks;
+      // lane L holds the table entry of box (L % boxes) of tile (L / boxes) of a
+      // group of tiles; the next group loads while this one is issued
+      auto load_group = [&](int grp) -> int {
+        const int t = grp * g_tpg + (lane >> lg_boxes);
+        const int t0 = (I.t_begin + t) * KV_TILE + koff;
+        return t < I.n_prefix && t0 < I.P ? table_row[args.fd_bs.div(t0)] : 0;
+      };
+      int grp_cur = load_group(0);
+      int grp_nxt = I.n_prefix > g_tpg ? load_group(1) : 0;
+      int key = I.t_begin * KV_TILE + koff;
+      int row = args.fd_bs.mod(key);
+      int jt = 0;
+      for (int j = 0; ok && j < I.n_prefix; ++j) {
+        if (j + I.n_tree == stop || !take()) {
+          ok = false;
+          break;
+        }
+        if (jt == 0 && j > 0) {
+          grp_cur = grp_nxt;
+          const int g2 = (j >> (5 - lg_boxes)) + 1;
+          grp_nxt = g2 * g_tpg < I.n_prefix ? load_group(g2) : 0;
+        }
+        int blk = __shfl_sync(0xffffffffu, grp_cur, (jt << lg_boxes) + lane);
+        const bool issue = lane < g_boxes && key < I.P;
+        if (issue && (blk < 0 || blk >= a.num_blocks)) {
+          if (a.status) a.status[I.b] = TS_ERR_BAD_BLOCK;
+          blk = 0;
+        }
+        const unsigned mask = __ballot_sync(0xffffffffu, issue);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(mask) * box_bytes);
+        __syncwarp();
+        if (issue) tma_load_3d((is_v ? sm.v[slot] : sm.k[slot]) + lane * box_bytes, tm_pool, &full[slot], 0, row, blk * a.Hkv + I.g);
+        __syncwarp();
+        key += KV_TILE;
+        row += row_step;
+        if (row >= a.bs) row -= a.bs;
+        jt = (jt + 1) & (g_tpg - 1);
+        next();
+      }
+    }
+  } else if (warp == QK_WARP) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ QK issuer
+      constexpr uint32_t ID_BF16 = idesc_bf16_f32(ROW_TILE, KV_TILE, 0, 0);
+      constexpr uint32_t ID_E4M3 = idesc_e4m3_f32(ROW_TILE, KV_TILE);
+      const uint32_t q_addr = smem_u32(sm.q);
+      int jg = 0;         // tiles
+      int kq = 0;         // K ring slots
+      int q8 = 0;         // Q tiles split
+      bool ok = true;
+      int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
+      for (int chain = chain0; ok && chain <= chain1; ++chain) {
+        const Seg I = make_seg(chain, cta, p_next, args);
+        if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];
+        if (I.n_tiles == 0) continue;
+        if (q_issued > 0 && !(ok = wait_bar(&sm.q_empty, (q_issued - 1) & 1, ctl))) break;
+        mbar_arrive_expect_tx(&sm.q_full, C::WIDE_BYTES);
+        for (int h = 0; h < C::HALVES; ++h)
+          tma_load_4d(sm.q + h * (ROW_TILE * 128), &tm_q, &sm.q_full, 64 * h, I.g * a.G, I.rt * args.nodes_per_tile, I.b);
+        ++q_issued;
+        if (chain < chain1) {  // the next segment's Q tile, into L2
+          const Seg nx = make_seg(chain + 1, cta, 0, args);
+          for (int h = 0; h < C::HALVES; ++h) tma_prefetch_4d(&tm_q, 64 * h, nx.g * a.G, nx.rt * args.nodes_per_tile, nx.b);
+        }
+        if (!(ok = wait_bar(&sm.q_full, (q_issued - 1) & 1, ctl))) break;
+        ++q_landed;
+        if (I.n_tree == 0) mbar_arrive(&sm.q_free);  // no tree: at once
+        for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+          const bool tree = j < I.n_tree;
+          if (j == I.n_tree) {
+            if (!(ok = wait_bar(&sm.q8_full, q8 & 1, ctl))) break;
+            ++q8;
+          }
+          const int s0 = kq % C::NSK, s1 = (kq + 1) % C::NSK;
+          ok = wait_bar(&sm.k_full[s0], (kq / C::NSK) & 1, ctl);
+          if (ok && tree && C::HALVES == 2) ok = wait_bar(&sm.k_full[s1], ((kq + 1) / C::NSK) & 1, ctl);
+          if (ok && jg >= NSB) ok = wait_bar(&sm.s_free[jg % NSB], ((jg / NSB) - 1) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
+          const uint32_t k0 = smem_u32(sm.k[s0]);
+          if (tree) {
+            const uint32_t k1 = smem_u32(sm.k[s1]);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              mma_ss(d_tmem, smem_desc_sw128(q_addr + (i >> 2) * (ROW_TILE * 128) + (i & 3) * 32, 16, 1024),
+                     smem_desc_sw128((i >> 2 ? k1 : k0) + (i & 3) * 32, 16, 1024), ID_BF16, i > 0);
+            mma_commit(&sm.s_full[jg % NSB]);
+            for (int h = 0; h < C::HALVES; ++h) mma_commit(&sm.k_empty[h ? s1 : s0]);
+            kq += C::HALVES;
+            if (j == I.n_tree - 1 && I.n_prefix > 0) mma_commit(&sm.q_free);
+          } else {
+            // D = 128: hi in the first 128-byte pieces, lo in the second; D = 64: hi and lo share a piece
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const bool low = i >= D / 32;
+              const int ks = low ? i - D / 32 : i;  // 32 channels a step
+              const uint32_t qa = q_addr + (D == 128 ? (low ? ROW_TILE * 128 : 0) + ks * 32 : i * 32);
+              const uint64_t kd = D == 128 ? smem_desc_sw128(k0 + ks * 32, 16, 1024) : smem_desc_sw64(k0 + ks * 32, 16, 512);
+              mma_ss_f8(d_tmem, smem_desc_sw128(qa, 16, 1024), kd, ID_E4M3, i > 0);
+            }
+            mma_commit(&sm.s_full[jg % NSB]);
+            mma_commit(&sm.k_empty[s0]);
+            kq += 1;
+          }
+        }
+        if (ok) mma_commit(&sm.q_empty);
+      }
+    }
+  } else if (warp == PV_WARP) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ PV issuer
+      constexpr uint32_t ID_PV = idesc_bf16_f32(ROW_TILE, D, 0, 1);
+      int jg = 0;
+      int vt[NVB] = {0, 0};
+      bool ok = true;
+      int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
+      for (int chain = chain0; ok && chain <= chain1; ++chain) {
+        const Seg I = make_seg(chain, cta, p_next, args);
+        if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];
+        for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+          const int buf = jg % NVB;
+          ok = wait_bar(&sm.p_full[jg % NSB], (jg / NSB) & 1, ctl) && wait_bar(&sm.vb_full[buf], (jg / NVB) & 1, ctl);
+          if (ok && j < I.n_tree) {
+            ok = wait_bar(&sm.vt_full[buf], (buf ? vt[1] : vt[0]) & 1, ctl);
+            if (buf) ++vt[1];
+            else ++vt[0];
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_addr = smem_u32(sm.vb[buf]);
+          const uint32_t p_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
+#pragma unroll
+          for (int i = 0; i < KV_TILE / 16; ++i)
+            mma_ts(tmem + TMEM_O, p_tmem + i * 8, smem_desc_sw128(v_addr + i * 2048, C::HALF_BYTES, 1024), ID_PV, j > 0 || i > 0);
+          mma_commit(&sm.o_ready);
+          mma_commit(&sm.s_free[jg % NSB]);
+          mma_commit(&sm.vb_empty[buf]);
+          if (!(ok = wait_bar(&sm.o_ready, jg & 1, ctl))) break;
+          tc_fence_after();
+          publish(&sm.pv_done, jg + 1);
+        }
+      }
+    }
+  }
+  } else if (warp >= CONVERT_WARP0) {
+    reg_dec<REG_CONVERT>();
+    // ------------------------------------------------------------ conversion
+    const int ct = threadIdx.x - CONVERT_WARP0 * 32;  // token of a tile, row of Q
+    const int swz = ct & 7;
+    int jg = 0, vq = 0, qn = 0, q8 = 0;
+    bool ok = true;
+    int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
+    for (int chain = chain0; ok && chain <= chain1; ++chain) {
+      const Seg I = make_seg(chain, cta, p_next, args);
+      if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];  // on its way while this one runs
+      if (I.n_tiles == 0) continue;
+      // Scales are fetched in two steps, the block of token ct three tiles ahead
+      // and its scale bytes two ahead (a token past the prefix has none).
+      const int* table_row = a.block_table + (size_t)I.b * a.max_blocks;
+      auto block_of = [&](int p) -> int {
+        const int t = (I.t_begin + p) * KV_TILE + ct;
+        if (p >= I.n_prefix || t >= I.P) return -1;
+        const int blk = table_row[args.fd_bs.div(t)];
+        return blk < 0 || blk >= a.num_blocks ? 0 : blk;  // reported by the producers
+      };
+      auto scale_of = [&](int p, int blk) -> uint32_t {
+        if (blk < 0) return 0;
+        const int t = (I.t_begin + p) * KV_TILE + ct;
+        return reinterpret_cast<const uint16_t*>(args.kv_scale)[((size_t)blk * a.Hkv + I.g) * a.bs + args.fd_bs.mod(t)];
+      };
+      const int b0 = block_of(0), b1 = block_of(1);
+      int b_next = block_of(2);
+      uint32_t s_cur = scale_of(0, b0), s_next = scale_of(1, b1);
+      float row_scale = 0.f;
+      if (I.n_prefix > 0) {
+        // the Q tile, row ct: scaled to within 448, hi and lo in place
+        // (q_free comes once a segment with prefix tiles, in step with q8_full;
+        // q_full also for the others, but none can follow before q8_full)
+        if (!(ok = wait_bar(&sm.q_free, q8 & 1, ctl) && wait_bar(&sm.q_full, qn & 1, ctl))) break;
+        uint4 x[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          x[c] = *reinterpret_cast<const uint4*>(sm.q + (c >> 3) * (ROW_TILE * 128) + ct * 128 + (((c & 7) ^ swz) << 4));
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          m = q8_max2(m, q8_max2(q8_max2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu),
+                                 q8_max2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
+        }
+        m = q8_max2(m, m >> 16) & 0xffffu;
+        const int s = q8_scale_byte(m);
+        const float inv = pow2_of(254 - s);
+        // an infinite query has no finite logits
+        row_scale = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {  // 16 channels: a 16-byte chunk of hi and one of lo
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4& y = x[2 * c + (e >> 1)];
+            const uint32_t w0 = (e & 1) ? y.z : y.x, w1 = (e & 1) ? y.w : y.y;
+            const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w0));
+            const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w1));
+            const float2 g0 = make_float2(f0.x * inv, f0.y * inv), g1 = make_float2(f1.x * inv, f1.y * inv);
+            const uint32_t h0 = __nv_cvt_float2_to_fp8x2(g0, __NV_SATFINITE, __NV_E4M3);
+            const uint32_t h1 = __nv_cvt_float2_to_fp8x2(g1, __NV_SATFINITE, __NV_E4M3);
+            const float2 u0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h0, __NV_E4M3)));
+            const float2 u1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h1, __NV_E4M3)));
+            const uint32_t l0 = __nv_cvt_float2_to_fp8x2(make_float2(g0.x - u0.x, g0.y - u0.y), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t l1 = __nv_cvt_float2_to_fp8x2(make_float2(g1.x - u1.x, g1.y - u1.y), __NV_SATFINITE, __NV_E4M3);
+            hi[e] = h0 | (h1 << 16);
+            lo[e] = l0 | (l1 << 16);
+          }
+          uint8_t* hrow = sm.q + ct * 128;
+          uint8_t* lrow = D == 128 ? hrow + ROW_TILE * 128 : hrow;
+          const int lc = D == 128 ? c : c + D / 16;
+          *reinterpret_cast<uint4*>(hrow + ((c ^ swz) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(lrow + ((lc ^ swz) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async();
+        mbar_arrive(&sm.q8_full);
+        ++q8;
+      }
+      ++qn;
+      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+        const bool tree = j < I.n_tree;
+        const int p = j - I.n_tree;
+        const uint32_t sc = tree ? 0 : s_cur;
+        if (!tree) {
+          s_cur = s_next;
+          s_next = scale_of(p + 2, b_next);
+          b_next = block_of(p + 3);
+        }
+        const bool inside = !tree && (I.t_begin + p) * KV_TILE + ct < I.P;
+        if (jg >= NT && !(ok = wait_bar(&sm.t_empty[jg % NT], ((jg / NT) - 1) & 1, ctl))) break;
+        sm.key_scale[jg % NT][ct] = tree ? 1.f : (inside ? pow2_of(sc & 0xff) : 0.f);
+        sm.row_scale[jg % NT][ct] = tree ? a.scale_log2 : row_scale;
+        mbar_arrive(&sm.t_full[jg % NT]);
+        const int buf = jg % NVB;
+        if (jg >= NVB && !(ok = wait_bar(&sm.vb_empty[buf], ((jg / NVB) - 1) & 1, ctl))) break;
+        uint8_t* wide = sm.vb[buf];
+        if (tree) {
+          if (ct == 0) {
+            mbar_arrive_expect_tx(&sm.vt_full[buf], C::WIDE_BYTES);
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_4d(wide + h * C::HALF_BYTES, &tm_vt, &sm.vt_full[buf], 64 * h, I.g, j * KV_TILE, I.b);
+            if (buf) ++vt_issued[1];
+            else ++vt_issued[0];
+          }
+        } else {
+          const int slot = vq % C::NSV;
+          if (!(ok = wait_bar(&sm.v_full[slot], (vq / C::NSV) & 1, ctl))) break;
+          const uint8_t* src = sm.v[slot] + ct * D;
+          const float scale = pow2_of(sc >> 8);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            // chunk c of this row, where the 128-byte (D = 128) or 64-byte swizzle put it
+            const uint4 x = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4));
+            if (inside) widen16(x, scale, lo, hi);
+            uint8_t* row = wide + (c >> 2) * C::HALF_BYTES + ct * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * (c & 3)) ^ swz) << 4)) = lo;
+            *reinterpret_cast<uint4*>(row + (((2 * (c & 3) + 1) ^ swz) << 4)) = hi;
+          }
+          mbar_arrive(&sm.v_empty[slot]);
+          ++vq;
+          fence_proxy_async();
+        }
+        mbar_arrive(&sm.vb_full[buf]);
+      }
+    }
+  } else {
+    reg_inc<REG_SOFTMAX>();
+    // ------------------------------------------------------------ softmax
+    const int r = threadIdx.x - SOFTMAX_WARP0 * 32;
+    const int R = a.N * a.G;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    int jg = 0;
+    bool ok = true;
+    int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
+    for (int chain = chain0; ok && chain <= chain1; ++chain) {
+      const Seg I = make_seg(chain, cta, p_next, args);
+      if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];  // on its way while this one runs
+      if (!I.p_ok && r == 0 && a.status) a.status[I.b] = TS_ERR_SHAPE;
+      const int grow = I.rt * ROW_TILE + r;
+      const bool active = grow < R;
+      const int node = active ? args.fd_g.div(grow) : 0;
+      const int h = I.g * a.G + (active ? grow - node * a.G : 0);
+      // a warp none of whose rows exist only keeps the barriers going
+      const bool busy = I.rt * ROW_TILE + (r & ~31) < R;
+      const int slot = 2 * cta + (chain != chain0 ? 1 : 0);
+      uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
+      if (active && I.n_tree > 0) {
+        const uint64_t* arow = a.anc_mask + ((size_t)I.b * a.N + node) * a.W;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w < a.W) anc[w] = arow[w];
+      }
+      float m_run = NEG_INF, l_run = 0.f;
+      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+        const int tb = jg % NT;
+        if (!__all_sync(0xffffffffu, wait_bar(&sm.t_full[tb], (jg / NT) & 1, ctl) &&
+                                         wait_bar(&sm.s_full[jg % NSB], (jg / NSB) & 1, ctl))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!busy) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.t_empty[tb]);
+          tc_fence_before();
+          mbar_arrive(&sm.p_full[jg % NSB]);
+          continue;
+        }
+        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * 128;
+        float s[KV_TILE];
+        {
+          uint32_t u[KV_TILE / 32][32];
+#pragma unroll
+          for (int c = 0; c < KV_TILE / 32; ++c) tmem_ld32(s_tmem + c * 32, u[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < KV_TILE / 32; ++c) {
+            reg_fence32(u[c]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(u[c][e]);
+          }
+        }
+        const float row_scale = sm.row_scale[tb][r];
+        if (j >= I.n_tree) {
+          const float4* ks = reinterpret_cast<const float4*>(sm.key_scale[tb]);
+#pragma unroll
+          for (int c = 0; c < KV_TILE / 4; ++c) {
+            const float4 f = ks[c];
+            fx::unpack2(fx::mul2(fx::pack2(s[4 * c], s[4 * c + 1]), fx::pack2(f.x, f.y)), s[4 * c], s[4 * c + 1]);
+            fx::unpack2(fx::mul2(fx::pack2(s[4 * c + 2], s[4 * c + 3]), fx::pack2(f.z, f.w)), s[4 * c + 2], s[4 * c + 3]);
+          }
+          const int valid = I.P - (I.t_begin + j - I.n_tree) * KV_TILE;
+          if (valid < KV_TILE) {
+#pragma unroll
+            for (int c = 0; c < KV_TILE; ++c)
+              if (c >= valid) s[c] = NEG_INF;
+          }
+        } else {
+          const uint64_t lo = j == 0 ? anc[0] : anc[2], hi = j == 0 ? anc[1] : anc[3];
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((lo >> c) & 1ull)) s[c] = NEG_INF;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((hi >> c) & 1ull)) s[64 + c] = NEG_INF;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.t_empty[tb]);
+        float mk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mk[e] = s[e];
+#pragma unroll
+        for (int c = 8; c < KV_TILE; c += 8)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
+        float mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
+        mx *= row_scale;
+        const float m_new = fmaxf(m_run, mx);
+        const bool rescale = j > 0 && m_new > m_run + RESCALE_THRESHOLD;
+        float m_use = m_run;
+        if (j == 0 || rescale) m_use = m_new;
+        const float m_exp = m_use == NEG_INF ? 0.f : m_use;
+        const uint64_t scale2 = fx::pack2(row_scale, row_scale);
+        const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
+        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[KV_TILE / 2];
+#pragma unroll
+        for (int e = 0; e < KV_TILE / 2; ++e) {
+          float x0, x1;
+          fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          sum2[e & 3] = fx::add2(sum2[e & 3], fx::pack2(p0, p1));
+          pk[e] = pack_bf16x2(p0, p1);
+        }
+        float rowsum;
+        {
+          float r0, r1;
+          fx::unpack2(fx::add2(fx::add2(sum2[0], sum2[1]), fx::add2(sum2[2], sum2[3])), r0, r1);
+          rowsum = r0 + r1;
+        }
+        {
+          uint32_t part[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[e] = pk[e];
+          tmem_st32(s_tmem, part);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[e] = pk[32 + e];
+          tmem_st32(s_tmem + 32, part);
+        }
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+          // O must hold every earlier PV before it is rescaled
+          if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float f = !rescale ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - m_new));
+          l_run *= f;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t u[32];
+            tmem_ld32(tmem + lane_base + TMEM_O + c, u);
+            tmem_ld_wait();
+            reg_fence32(u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+            tmem_st32(tmem + lane_base + TMEM_O + c, u);
+          }
+        }
+        m_run = m_use;
+        l_run += rowsum;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[jg % NSB]);
+      }
+      if (!ok) break;
+      // end of the segment: normalise and store
+      if (I.n_tiles > 0 && !__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool none = l_run == 0.f;  // the row saw no key
+      const float inv = none ? 0.f : 1.f / l_run;
+      const float lse2 = none ? NEG_INF : m_run + __log2f(l_run);
+      const size_t orow = ((size_t)I.b * a.N + node) * a.Hq + h;
+      if (I.n_tiles == 0) {
+        if (active) args.part_ls[(size_t)slot * ROW_TILE + r] = make_float2(NEG_INF, 0.f);
+      } else if (busy) {
+        float f = inv;
+        if (!I.whole) {
+          // a part: 16-bit values of at most 2^10 with the row's power of two
+          float top = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t u[32];
+            tmem_ld32(tmem + lane_base + TMEM_O + c, u);
+            tmem_ld_wait();
+            reg_fence32(u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(u[e])));
+          }
+          top *= inv;
+          const int e = min(max((int)(__float_as_uint(top) >> 23), 10), 253);  // top < 2^(e - 126)
+          f = inv * pow2_of(263 - e);                                          // times 2^(136 - e): below 2^10
+          if (active) args.part_ls[(size_t)slot * ROW_TILE + r] = make_float2(lse2, pow2_of(e - 9));
+        } else if (active && a.lse) {
+          a.lse[orow] = lse2 * 0.69314718055994531f;
+        }
+        __half* part = args.part_o + ((size_t)slot * ROW_TILE + r) * D;
+        __nv_bfloat16* out = a.out + orow * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t u[32], w[16];
+          tmem_ld32(tmem + lane_base + TMEM_O + c, u);
+          tmem_ld_wait();
+          reg_fence32(u);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = none ? 0.f : __uint_as_float(u[2 * e]) * f;
+            const float y = none ? 0.f : __uint_as_float(u[2 * e + 1]) * f;
+            if (I.whole) {
+              w[e] = pack_bf16x2(x, y);
+            } else {
+              const __half2 t = __floats2half2_rn(x, y);
+              w[e] = *reinterpret_cast<const uint32_t*>(&t);
+            }
+          }
+          if (active) {
+            void* dst = I.whole ? (void*)(out + c) : (void*)(part + c);
+            if (!I.whole || args.out32) {
+              st_global_v8(dst, w);
+              st_global_v8(static_cast<uint8_t*>(dst) + 32, w + 8);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                static_cast<uint4*>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (r == 0) publish(&sm.segs_done, chain - chain0 + 1);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*ctl.flag) {
+    // A wait gave up.  Nothing may still write this CTA's shared memory or TMEM
+    // once it exits: wait (bounded) for the newest loads of each ring, for a Q
+    // tile, for the tree's V tiles and for every MMA started.
+    if ((warp == K_WARP || warp == V_WARP) && lane == 0) {
+      uint64_t* full = warp == V_WARP ? sm.v_full : sm.k_full;
+      const int nst = warp == V_WARP ? C::NSV : C::NSK;
+      for (int j = max(0, issued - nst); j < issued; ++j) mbar_wait(&full[j % nst], (j / nst) & 1, a.wait_limit_ns);
+    } else if ((warp == QK_WARP || warp == PV_WARP) && lane == 0) {
+      if (q_issued > q_landed) mbar_wait(&sm.q_full, (q_issued - 1) & 1, a.wait_limit_ns);
+      uint64_t* d = &sm.drain[warp - QK_WARP];
+      mma_commit(d);
+      mbar_wait(d, 0, a.wait_limit_ns);
+    } else if (threadIdx.x == CONVERT_WARP0 * 32) {
+      for (int i = 0; i < NVB; ++i)
+        if (vt_issued[i] > 0) mbar_wait(&sm.vt_full[i], (vt_issued[i] - 1) & 1, a.wait_limit_ns);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && a.status) {
+      for (int chain = chain0 + sm.segs_done; chain <= chain1; ++chain) a.status[seq_of(chain, args)] = TS_ERR_TIMEOUT;
+    }
+  }
+  pdl_trigger();
+  if (warp == K_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the parts of each cut chain: block (c, i) the chain that begins in CTA
+// c and ends in a later one, rows 128/gridDim.y of it from i on.  With parts
+// O_s, L_s (base 2): out = sum 2^(L_s - M) O_s / sum 2^(L_s - M).
+constexpr int MERGE_THREADS = 128;
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS)
+k_merge_q8(const __grid_constant__ Q8Args args) {
+  constexpr int LANES = D / 8;
+  constexpr int ROWS = MERGE_THREADS / LANES;
+  const AttnArgs& a = args.a;
+  const Runs& runs = args.runs;
+  const int c = blockIdx.x;
+  const int chain = runs.chain[c + 1];
+  if (runs.tile[c + 1] == 0 || (runs.chain[c] == chain && runs.tile[c] > 0)) return;  // nothing cut, or not begun here
+  const int rt = args.fd_units.div(chain), u = chain - rt * args.units;
+  const int b = args.fd_hkv.div(u), g = u - b * a.Hkv;
+  const int r = blockIdx.y * ROWS + (int)threadIdx.x / LANES, sub = (int)threadIdx.x % LANES;
+  const int grow = rt * ROW_TILE + r;
+  if (grow >= a.N * a.G) return;
+  const int first = 2 * c + (runs.chain[c] != chain ? 1 : 0);
+  int last = c + 1;
+  while (last + 1 < runs.n && runs.chain[last + 1] == chain && runs.tile[last + 1] > 0) ++last;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.N * a.Hq) return;
-  const int h = (int)(row % a.Hq), g = h / a.G;
-  const int node = (int)(row / a.Hq % a.N), b = (int)(row / a.Hq / a.N);
-  const int P_dev = a.prefix_len[b];
-  const long long cap = (long long)a.max_blocks * a.bs;
-  const int P = (int)min((long long)max(P_dev, 0), cap);
-  if (P != P_dev && lane == 0 && a.status) a.status[b] = TS_ERR_SHAPE;
-  float x[C], o[C], m = -INFINITY, l = 0.f;
+  float m = NEG_INF, den = 0.f, acc[8];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    x[c] = __bfloat162float(a.q[(size_t)row * D + lane * C + c]) * a.scale_log2;
-    o[c] = 0.f;
-  }
-  const auto step = [&](const float (&k)[C], const float (&v)[C]) {
-    float s = 0.f;
+  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+  for (int p = c; p <= last; ++p) {
+    const int slot = p == c ? first : 2 * p;
+    const float2 ls = args.part_ls[(size_t)slot * ROW_TILE + r];
+    if (ls.x == NEG_INF) continue;  // a part without keys: its values were not written
+    const uint4 raw = reinterpret_cast<const uint4*>(args.part_o + ((size_t)slot * ROW_TILE + r) * D)[sub];
+    const float m_new = fmaxf(m, ls.x);
+    const float f = m == NEG_INF ? 0.f : exp2f(m - m_new), w = exp2f(ls.x - m_new);
+    den = den * f + w;
+    const float ws = w * ls.y;
+    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int c = 0; c < C; ++c) s = fmaf(x[c], k[c], s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float mn = fmaxf(m, s);
-    const float f = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(p, v[c], o[c] * f);
-    m = mn;
-  };
-  for (int t = 0; t < P; ++t) {
-    int blk = a.block_table[(size_t)b * a.max_blocks + t / a.bs];
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (lane == 0 && a.status) a.status[b] = TS_ERR_BAD_BLOCK;
-      blk = 0;
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[k]));
+      acc[2 * k] = fmaf(ws, v.x, acc[2 * k] * f);
+      acc[2 * k + 1] = fmaf(ws, v.y, acc[2 * k + 1] * f);
     }
-    const size_t r = ((size_t)blk * a.Hkv + g) * a.bs + t % a.bs;
-    const float ks = scale_of(q.kv_scale[2 * r]), vs = scale_of(q.kv_scale[2 * r + 1]);
-    float k[C], v[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      k[c] = e4m3(q.k_codes[r * D + lane * C + c]) * ks;
-      v[c] = e4m3(q.v_codes[r * D + lane * C + c]) * vs;
-    }
-    step(k, v);
+    m = m_new;
   }
-  for (int j = 0; j < a.N; ++j) {
-    if (!((a.anc_mask[((size_t)b * a.N + node) * a.W + j / 64] >> (j % 64)) & 1)) continue;
-    const size_t r = ((size_t)b * a.N + j) * a.Hkv + g;
-    float k[C], v[C];
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int node = args.fd_g.div(grow);
+  const size_t orow = ((size_t)b * a.N + node) * a.Hq + g * a.G + (grow - node * a.G);
+  uint32_t o[4];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      k[c] = __bfloat162float(a.k_tree[r * D + lane * C + c]);
-      v[c] = __bfloat162float(a.v_tree[r * D + lane * C + c]);
-    }
-    step(k, v);
+  for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  reinterpret_cast<uint4*>(a.out + orow * D)[sub] = make_uint4(o[0], o[1], o[2], o[3]);
+  if (a.lse && sub == 0) a.lse[orow] = den == 0.f ? NEG_INF : (m + log2f(den)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ plan
+
+// The runs.  A chain weighs its prefix tiles and `head` more: its tree tiles,
+// Q tile and epilogue.
+constexpr int SEG_COST = 3;  // tiles' worth of a segment's start and end
+constexpr int MIN_RUN = 6;   // no CTA for less weight than this
+constexpr int SLIVER = 2;    // no part of fewer tiles
+
+Runs plan_runs(const ts_attn_params* p) {
+  Runs r{};
+  const int G = p->Hq / p->Hkv;
+  const int row_tiles = ceil_div(p->N * G, ROW_TILE);
+  const int head = ceil_div(p->N, KV_TILE) + SEG_COST;
+  long long per_rt = 0, longest = 0;
+  for (int b = 0; b < p->B; ++b) {
+    const long long w = prefix_tiles(p->prefix_len_host[b]) + head;
+    per_rt += w * p->Hkv;
+    longest = std::max(longest, w);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) a.out[(size_t)row * D + lane * C + c] = __float2bfloat16_rn(o[c] * inv);
-  if (a.lse && lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+  const long long total = per_rt * row_tiles;
+  const long long chains = (long long)p->B * p->Hkv * row_tiles;
+  // One CTA an SM; a multiple of the row tiles where that idles few SMs, so
+  // that the row tiles of a unit run in step.
+  int full = PLAN_SMS;
+  if (row_tiles <= PLAN_SMS) {
+    const int even = PLAN_SMS / row_tiles * row_tiles;
+    if (even * 16 >= PLAN_SMS * 15) full = even;
+  }
+  const bool one_each = chains <= full && longest <= 2 * MIN_RUN;  // short chains: not worth a merge
+  long long n = one_each ? chains : std::max(chains < full ? chains : full, total / MIN_RUN);
+  if (n > full) n = full;
+  r.n = (int)n;
+  int c = 0;
+  long long acc = 0;  // weight before the sequence at hand
+  for (int rt = 0; rt < row_tiles; ++rt) {
+    for (int b = 0; b < p->B; ++b) {
+      const long long tiles = prefix_tiles(p->prefix_len_host[b]), w = tiles + head;
+      const int chain_b = (rt * p->B + b) * p->Hkv;
+      // the runs that start within these Hkv chains
+      while (c < r.n) {
+        const long long at = one_each ? 0 : total * c / r.n - acc;
+        if (!one_each && at >= w * p->Hkv) break;
+        if (one_each && c >= chain_b + p->Hkv) break;
+        int g = one_each ? c - chain_b : (int)(at / w);
+        long long t = one_each ? 0 : at % w - head;
+        if (t < SLIVER) t = 0;
+        if (tiles - t < SLIVER && t > 0) {
+          t = 0;
+          ++g;
+        }
+        r.chain[c] = chain_b + g;
+        r.tile[c] = (int)t;
+        ++c;
+      }
+      acc += w * p->Hkv;
+    }
+  }
+  r.chain[r.n] = (int)chains;
+  r.tile[r.n] = 0;
+  return r;
+}
+
+bool any_cut(const Runs& r) {
+  for (int c = 1; c < r.n; ++c)
+    if (r.tile[c] > 0) return true;
+  return false;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+size_t part_o_bytes(const Runs& r, int D) { return any_cut(r) ? round256((size_t)2 * r.n * ROW_TILE * D * 2) : 0; }
+size_t part_ls_bytes(const Runs& r) { return any_cut(r) ? round256((size_t)2 * r.n * ROW_TILE * sizeof(float2)) : 0; }
+
+bool encode_codes(CUtensorMap* m, const void* base, int D, const AttnArgs& a, int box_rows) {
+  // codes [num_blocks * Hkv, bs, D]: a box is box_rows tokens, every channel,
+  // swizzled over its 128-byte (D = 128) or 64-byte rows
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  std::memset(m, 0, sizeof(*m));
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.bs, (cuuint64_t)a.num_blocks * a.Hkv};
+  const cuuint64_t str[2] = {(cuuint64_t)D, (cuuint64_t)a.bs * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)box_rows, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return sizeof(Smem<D>) + 1024;
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a CTA");
+
+template <int D>
+cudaError_t launch(Q8Args& t, const AttnQ8Args& q, cudaStream_t s) {
+  const AttnArgs& a = q.a;
+  CUtensorMap m_q, m_kc, m_vc, m_kt, m_vt;
+  {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.N, (uint64_t)a.B};
+    const uint64_t str[3] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2, (uint64_t)a.N * a.Hq * D * 2};
+    const uint32_t box[4] = {64, (uint32_t)a.G, (uint32_t)(ROW_TILE / a.G), 1};
+    if (!encode_bf16_sw128(&m_q, a.q, 4, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  if (!encode_codes(&m_kc, q.k_codes, D, a, t.box_rows) || !encode_codes(&m_vc, q.v_codes, D, a, t.box_rows))
+    return cudaErrorInvalidValue;
+  {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.Hkv, (uint64_t)a.N, (uint64_t)a.B};
+    const uint64_t str[3] = {(uint64_t)D * 2, (uint64_t)a.Hkv * D * 2, (uint64_t)a.N * a.Hkv * D * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)KV_TILE, 1};
+    if (!encode_bf16_sw128(&m_kt, a.k_tree, 4, dims, str, box) || !encode_bf16_sw128(&m_vt, a.v_tree, 4, dims, str, box))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = launch_pdl(k_attn_q8<D>, dim3(t.runs.n), dim3(THREADS), smem_bytes<D>(), s, t, m_q, m_kc, m_vc, m_kt, m_vt);
+  if (e != cudaSuccess || !any_cut(t.runs)) return e;
+  const dim3 grid(t.runs.n, ROW_TILE / (MERGE_THREADS / (D / 8)));
+  return launch_pdl(k_merge_q8<D>, grid, dim3(MERGE_THREADS), 0, s, t);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_q8(const AttnQ8Args& q, cudaStream_t s) {
-  const long long rows = (long long)q.a.B * q.a.N * q.a.Hq;
-  const dim3 grid((unsigned)((rows + 7) / 8));
-  return q.a.D == 128 ? launch_pdl(k_attn_q8_rows<128>, grid, dim3(256), 0, s, q)
-                      : launch_pdl(k_attn_q8_rows<64>, grid, dim3(256), 0, s, q);
+cudaError_t attn_q8_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(k_attn_q8<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<128>());
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_attn_q8<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<64>());
+}
+
+size_t attn_q8_workspace(const ts_attn_params* p) {
+  const Runs r = plan_runs(p);
+  return 256 + part_o_bytes(r, p->D) + part_ls_bytes(r);
+}
+
+cudaError_t launch_attn_q8(const AttnQ8Args& q, const ts_attn_params* p, void* workspace, cudaStream_t s) {
+  const AttnArgs& a = q.a;
+  Q8Args t{};
+  t.a = a;
+  t.kv_scale = q.kv_scale;
+  t.runs = plan_runs(p);
+  char* ws = static_cast<char*>(workspace) + 256;
+  t.part_o = reinterpret_cast<__half*>(ws);
+  t.part_ls = reinterpret_cast<float2*>(ws + part_o_bytes(t.runs, a.D));
+  t.box_rows = KV_TILE;
+  while (a.bs % t.box_rows != 0) t.box_rows >>= 1;
+  t.nodes_per_tile = ROW_TILE / a.G;
+  t.units = a.B * a.Hkv;
+  t.n_tree = ceil_div(a.N, KV_TILE);
+  t.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  t.fd_units = FastDiv::make(t.units);
+  t.fd_hkv = FastDiv::make(a.Hkv);
+  t.fd_bs = FastDiv::make(a.bs);
+  t.fd_g = FastDiv::make(a.G);
+  return a.D == 128 ? launch<128>(t, q, s) : launch<64>(t, q, s);
 }
 
 }  // namespace ts

@@ -314,6 +314,8 @@ struct AttnQ8Args {
   const uint8_t* v_codes;
   const uint8_t* kv_scale;
 };
-cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t s);
+cudaError_t attn_q8_prepare();
+size_t attn_q8_workspace(const ts_attn_params* p);
+cudaError_t launch_attn_q8(const AttnQ8Args& a, const ts_attn_params* p, void* workspace, cudaStream_t s);
 
 }  // namespace ts
