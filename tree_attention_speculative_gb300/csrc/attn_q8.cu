@@ -72,8 +72,6 @@ constexpr int NSB = 3;  // S buffers
 constexpr int NT = 4;   // tiles' key scales in flight
 constexpr int NVB = 2;  // widened V tiles
 constexpr int SLOT = 16384;  // a ring slot: 128 tokens of 128 codes, or a 64-column half of a bf16 tree tile
-constexpr int REG_LAUNCH = 168, REG_CONTROL = 112, REG_SOFTMAX = 240, REG_CONVERT = 152;
-static_assert(REG_CONTROL + REG_SOFTMAX + REG_CONVERT <= 3 * REG_LAUNCH, "warpgroups share what the launch was given");
 constexpr float RESCALE_THRESHOLD = 20.0f;  // as in attn_tc.cu: O follows the running max only past 2^20
 constexpr float NEG_INF = -INFINITY;
 
@@ -210,11 +208,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float pow2_of(int biased) { return __uint_as_float((uint32_t)biased << 23); }
 
-template <int N>
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // 16 codes times a power of two as bf16 (exact), two 16-byte chunks.
 __device__ __forceinline__ void widen16(const uint4& c, float scale, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -309,10 +302,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
   int q_issued = 0, q_landed = 0;  // Q tiles
   int vt_issued[NVB] = {0, 0};     // tree V tiles, by buffer
 
-  // Each warpgroup changes its registers where its own code begins, not before
-  // a join: the softmax holds a row of S, taken from the others' shares.
-  if (warp < SOFTMAX_WARP0) {
-  reg_dec<REG_CONTROL>();
   if (warp == K_WARP || warp == V_WARP) {
     // ------------------------------------------------------------ K or V codes
     const bool is_v = warp == V_WARP;
@@ -507,9 +496,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         }
       }
     }
-  }
   } else if (warp >= CONVERT_WARP0) {
-    reg_dec<REG_CONVERT>();
     // ------------------------------------------------------------ conversion
     const int ct = threadIdx.x - CONVERT_WARP0 * 32;  // token of a tile, row of Q
     const int swz = ct & 7;
@@ -618,7 +605,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           if (!(ok = wait_bar(&sm.v_full[slot], (vq / C::NSV) & 1, ctl))) break;
           const uint8_t* src = sm.v[slot] + ct * D;
           const float scale = pow2_of(sc >> 8);
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < D / 16; ++c) {
             uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
             // chunk c of this row, where the 128-byte (D = 128) or 64-byte swizzle put it
@@ -636,7 +623,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       }
     }
   } else {
-    reg_inc<REG_SOFTMAX>();
     // ------------------------------------------------------------ softmax
     const int r = threadIdx.x - SOFTMAX_WARP0 * 32;
     const int R = a.N * a.G;
@@ -662,7 +648,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         for (int w = 0; w < 4; ++w)
           if (w < a.W) anc[w] = arow[w];
       }
-      float m_run = NEG_INF, l_run = 0.f;
+      float m_run = NEG_INF;
+      uint64_t sum2[2] = {0ull, 0ull};  // the running sum, in four independent parts
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         const int tb = jg % NT;
         if (!__all_sync(0xffffffffu, wait_bar(&sm.t_full[tb], (jg / NT) & 1, ctl) &&
@@ -671,121 +658,117 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           break;
         }
         tc_fence_after();
-        if (!busy) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.t_empty[tb]);
-          tc_fence_before();
-          mbar_arrive(&sm.p_full[jg % NSB]);
-          continue;
-        }
         const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * 128;
-        float s[KV_TILE];
-        {
-          uint32_t u[KV_TILE / 32][32];
-#pragma unroll
-          for (int c = 0; c < KV_TILE / 32; ++c) tmem_ld32(s_tmem + c * 32, u[c]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < KV_TILE / 32; ++c) {
-            reg_fence32(u[c]);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(u[c][e]);
-          }
-        }
+        const bool tree = j < I.n_tree;
+        // keys of this tile that exist; a whole prefix tile needs no mask
+        const int valid = tree ? 0 : min(I.P - (I.t_begin + j - I.n_tree) * KV_TILE, KV_TILE);
+        const uint64_t vis_lo = j == 0 ? anc[0] : anc[2], vis_hi = j == 0 ? anc[1] : anc[3];
         const float row_scale = sm.row_scale[tb][r];
-        if (j >= I.n_tree) {
-          const float4* ks = reinterpret_cast<const float4*>(sm.key_scale[tb]);
+        const uint64_t scale2 = fx::pack2(row_scale, row_scale);
+        // 32 columns at a time, in a loop that stays rolled: unrolled over the
+        // tile, softmax and conversion together overflowed the instruction
+        // caches (3 of 8 stall cycles an issue, 2.5 us a tile).
+#pragma unroll 1
+        for (int c = 0; busy && c < KV_TILE / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld32(s_tmem + c * 32, u);
+          tmem_ld_wait();
+          reg_fence32(u);
+          uint64_t y[16];
+          const float4* ks = reinterpret_cast<const float4*>(sm.key_scale[tb] + c * 32);
 #pragma unroll
-          for (int c = 0; c < KV_TILE / 4; ++c) {
-            const float4 f = ks[c];
-            fx::unpack2(fx::mul2(fx::pack2(s[4 * c], s[4 * c + 1]), fx::pack2(f.x, f.y)), s[4 * c], s[4 * c + 1]);
-            fx::unpack2(fx::mul2(fx::pack2(s[4 * c + 2], s[4 * c + 3]), fx::pack2(f.z, f.w)), s[4 * c + 2], s[4 * c + 3]);
+          for (int e = 0; e < 8; ++e) {
+            const float4 f = ks[e];
+            y[2 * e] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1])), fx::pack2(f.x, f.y));
+            y[2 * e + 1] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3])), fx::pack2(f.z, f.w));
           }
-          const int valid = I.P - (I.t_begin + j - I.n_tree) * KV_TILE;
           if (valid < KV_TILE) {
+            uint32_t see;
+            if (tree) see = (uint32_t)((c < 2 ? vis_lo : vis_hi) >> (32 * (c & 1)));
+            else see = valid >= 32 * (c + 1) ? ~0u : valid <= 32 * c ? 0u : (1u << (valid - 32 * c)) - 1u;
 #pragma unroll
-            for (int c = 0; c < KV_TILE; ++c)
-              if (c >= valid) s[c] = NEG_INF;
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              fx::unpack2(y[e], x0, x1);
+              y[e] = fx::pack2((see >> (2 * e)) & 1u ? x0 : NEG_INF, (see >> (2 * e + 1)) & 1u ? x1 : NEG_INF);
+            }
           }
-        } else {
-          const uint64_t lo = j == 0 ? anc[0] : anc[2], hi = j == 0 ? anc[1] : anc[3];
+          float mk[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((lo >> c) & 1ull)) s[c] = NEG_INF;
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            fx::unpack2(y[e], x0, x1);
+            mk[(2 * e) & 3] = fmaxf(mk[(2 * e) & 3], x0);
+            mk[(2 * e + 1) & 3] = fmaxf(mk[(2 * e + 1) & 3], x1);
+          }
+          const float mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * row_scale;
+          const bool rescale = mx > m_run + RESCALE_THRESHOLD;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // Rows whose maximum rose past the threshold: what they have so far
+            // is scaled down (the warp together; the others by 1).
+            const float f = !rescale ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - mx));
+            if (rescale) m_run = mx;
+            const uint64_t f2 = fx::pack2(f, f);
+            sum2[0] = fx::mul2(sum2[0], f2);
+            sum2[1] = fx::mul2(sum2[1], f2);
+            if (c > 0) {  // this tile's P so far (what is left of it is below 2^-20)
+              tmem_st_wait();
+#pragma unroll 1
+              for (int i = 0; i < c; ++i) {
+                uint32_t w[16];
+                tmem_ld16(s_tmem + i * 16, w);
+                tmem_ld_wait();
+                reg_fence16(w);
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((hi >> c) & 1ull)) s[64 + c] = NEG_INF;
+                for (int e = 0; e < 16; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+                tmem_st16(s_tmem + i * 16, w);
+              }
+            }
+            if (j > 0) {  // O, which must hold every earlier PV
+              ok = __all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                uint32_t w[32];
+                tmem_ld32(tmem + lane_base + TMEM_O + d, w);
+                tmem_ld_wait();
+                reg_fence32(w);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                tmem_st32(tmem + lane_base + TMEM_O + d, w);
+              }
+            }
+          }
+          // p = 2^(y * row_scale - m) (nothing visible so far: all 0), over S as bf16
+          const float m_exp = m_run == NEG_INF ? 0.f : m_run;
+          const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            fx::unpack2(fx::fma2(y[e], scale2, negm2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(s_tmem + c * 16, pk);
         }
+        if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.t_empty[tb]);
-        float mk[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mk[e] = s[e];
-#pragma unroll
-        for (int c = 8; c < KV_TILE; c += 8)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
-        float mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
-        mx *= row_scale;
-        const float m_new = fmaxf(m_run, mx);
-        const bool rescale = j > 0 && m_new > m_run + RESCALE_THRESHOLD;
-        float m_use = m_run;
-        if (j == 0 || rescale) m_use = m_new;
-        const float m_exp = m_use == NEG_INF ? 0.f : m_use;
-        const uint64_t scale2 = fx::pack2(row_scale, row_scale);
-        const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
-        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[KV_TILE / 2];
-#pragma unroll
-        for (int e = 0; e < KV_TILE / 2; ++e) {
-          float x0, x1;
-          fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          sum2[e & 3] = fx::add2(sum2[e & 3], fx::pack2(p0, p1));
-          pk[e] = pack_bf16x2(p0, p1);
-        }
-        float rowsum;
-        {
-          float r0, r1;
-          fx::unpack2(fx::add2(fx::add2(sum2[0], sum2[1]), fx::add2(sum2[2], sum2[3])), r0, r1);
-          rowsum = r0 + r1;
-        }
-        {
-          uint32_t part[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) part[e] = pk[e];
-          tmem_st32(s_tmem, part);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) part[e] = pk[32 + e];
-          tmem_st32(s_tmem + 32, part);
-        }
-        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-          // O must hold every earlier PV before it is rescaled
-          if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float f = !rescale ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - m_new));
-          l_run *= f;
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t u[32];
-            tmem_ld32(tmem + lane_base + TMEM_O + c, u);
-            tmem_ld_wait();
-            reg_fence32(u);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-            tmem_st32(tmem + lane_base + TMEM_O + c, u);
-          }
-        }
-        m_run = m_use;
-        l_run += rowsum;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.p_full[jg % NSB]);
       }
       if (!ok) break;
+      float l_run;
+      {
+        float r0, r1;
+        fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
+        l_run = r0 + r1;
+      }
       // end of the segment: normalise and store
       if (I.n_tiles > 0 && !__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
         ok = false;
