@@ -585,8 +585,7 @@ TS_API ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree,
  * Values past bf16's largest (255 * 2^120; only rows within 3% of it, or with
  * an infinity, hold any) read as infinite.
  * A row that sees no key (no prefix and an empty mask row) gives zeros and an
- * lse of -inf.  kv_scale bytes 0 and 255 (which the writers never store) read
- * as 0 and infinity.
+ * lse of -inf.  Scale bytes of the prefix's rows must lie in [1, 254].
  *
  * tree_attn_q8_workspace_size: bytes of device workspace it needs (256-byte
  * aligned, ZERO-FILLED before its first use, then left so that stream-ordered

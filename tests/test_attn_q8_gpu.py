@@ -423,3 +423,18 @@ def test_a_wait_that_runs_out_is_reported(stall_tile):
     call()
     assert status.cpu().tolist() == [0] * 4
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, A)
+
+
+def test_nan_codes_reach_their_channels_alone():
+    case = _case("nan", 2, 5, 4, 1, 128, [300, 40], 16, "worked")
+    pools = quantised_pools(case)
+    blk = case.block_table[0, 70 // 16]
+    pools[1][blk, 0, 70 % 16, [0, 5, 63, 64, 127]] = 0x7F, 0xFF, 0x7F, 0xFF, 0x7F
+    call, out, lse, status, _ = _raw(case, pools)
+    call()
+    got = out.double().cpu().numpy()
+    bad = np.isnan(got)
+    assert bad[0][..., [0, 5, 63, 64, 127]].all() and bad.sum() == bad[0][..., [0, 5, 63, 64, 127]].size
+    ref, A = oracle.attention.tree_attention_case(case), _abs_v(case)
+    got[bad] = ref[0][bad]
+    check(case, got, lse.double().cpu().numpy(), ref, A)

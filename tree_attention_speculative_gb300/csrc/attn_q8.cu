@@ -62,17 +62,26 @@ namespace {
 
 using namespace sm100;
 
-constexpr int THREADS = 384;
-constexpr int GROUP_THREADS = 128;  // softmax, and conversion
-constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4, CONVERT_WARP0 = 8;
+constexpr int THREADS = 512;
+constexpr int CONVERT_THREADS = 128;
+constexpr int SOFTMAX_THREADS = 256;
+constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, CONVERT_WARP0 = 4, SOFTMAX_WARP0 = 8;
+// TMEM: an O for each half of a tile's keys, then the S buffers
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_O = 0;
-constexpr uint32_t TMEM_S0 = 128;
-constexpr int NSB = 3;  // S buffers
+constexpr uint32_t O_STRIDE = 128;
+constexpr uint32_t TMEM_S0 = 256;
+constexpr int NSB = 2;        // S buffers
+constexpr int HALF_KEYS = 64;  // keys of a tile a softmax group takes
 constexpr int NT = 4;   // tiles' key scales in flight
 constexpr int NVB = 2;  // widened V tiles
 constexpr int SLOT = 16384;  // a ring slot: 128 tokens of 128 codes, or a 64-column half of a bf16 tree tile
-constexpr float RESCALE_THRESHOLD = 20.0f;  // as in attn_tc.cu: O follows the running max only past 2^20
+// A row keeps the reference m it took from its first keys until a logit passes
+// it by RESCALE (log2 units).  bf16 P, fp32 sums and O have the same precision
+// at every magnitude, so weights up to 2^40 are as good as weights up to 1, and
+// O is hardly ever rescaled, hot keys or not.  (Sums then stay finite for
+// values up to 2^127 / (2^40 x keys), past 2^69.)
+constexpr float RESCALE = 40.0f;
 constexpr float NEG_INF = -INFINITY;
 
 template <int D>
@@ -96,6 +105,7 @@ struct __align__(1024) Smem {
   // the row's factor (the query's power of two times scale * log2 e).
   float key_scale[NT][KV_TILE];
   float row_scale[NT][ROW_TILE];
+  float2 half_ml[2][ROW_TILE];  // (maximum, sum) of each half, at the end of a segment
   // q_free: no product reads the bf16 Q any more, it may be split in place
   uint64_t q_full, q_free, q8_full, q_empty;
   uint64_t k_full[C::NSK], k_empty[C::NSK];
@@ -124,7 +134,8 @@ struct Q8Args {
   AttnArgs a;
   const uint8_t* kv_scale;
   __half* part_o;    // [2 n, 128, D]: parts of chains, normalised, times a row's 1 / part_ls.y
-  float2* part_ls;   // [2 n, 128]: base-2 log-sum-exp, factor
+  float2* part_ls;   // [2 n, 128]: base-2 log-sum-exp, and the factor of channels below D/2
+  float* part_f1;    // [2 n, 128]: the factor of the others
   int box_rows, nodes_per_tile, units, n_tree;
   int out32;
   FastDiv fd_units, fd_hkv, fd_bs, fd_g;
@@ -169,11 +180,17 @@ struct Ctl {
   volatile int* flag;
   uint64_t limit;
 };
+// A wait polls in a loop of nothing but the poll and looks at the abort flag
+// and the clock now and then: sixteen warps polling with both in the loop took
+// a third of the SM's issue slots.
+constexpr int POLLS = 32;
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < POLLS; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*c.flag) return false;
     if (globaltimer_ns() - t0 > c.limit) {
       *c.flag = 1;
@@ -208,19 +225,46 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float pow2_of(int biased) { return __uint_as_float((uint32_t)biased << 23); }
 
-// 16 codes times a power of two as bf16 (exact), two 16-byte chunks.
-__device__ __forceinline__ void widen16(const uint4& c, float scale, uint4& lo, uint4& hi) {
+// A row's power of two as the multipliers of widen16: 2^(s - 127) * 2^120 in
+// one bf16 pair, or where that is too large (s > 134), in two.
+struct WideScale {
+  uint32_t m1, m2;
+  __device__ __forceinline__ explicit WideScale(uint32_t s) {
+    const uint32_t b1 = min(s + 120u, 254u), b2 = s + 247u - b1;
+    m1 = (b1 << 7) | (b1 << 23);
+    m2 = (b2 << 7) | (b2 << 23);
+  }
+};
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two bytes of w, each sign-extended to 16 bits (prmt's msb selector bit repeats a byte's sign).
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t two_bytes(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(w), "n"(SEL));
+  return r;
+}
+// 16 codes times the row's power of two as bf16, two 16-byte chunks.  A code's
+// sign, exponent and mantissa, put where bf16 has them, are its value times
+// 2^-120 (subnormal codes too), so a bit shuffle and a product do: exact, and
+// half the cost of going through fp16 and fp32.  Only a NaN code would come out
+// as a number; *nan collects bits 0x80808080 for those.
+__device__ __forceinline__ void widen16(const uint4& c, const WideScale& ws, bool twice, uint4& lo, uint4& hi, uint32_t* nan) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  const uint64_t s2 = fx::pack2(scale, scale);
   uint32_t o[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    uint32_t h;  // two codes as fp16
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    float x, y;
-    fx::unpack2(fx::mul2(fx::pack2(f.x, f.y), s2), x, y);
-    o[k] = pack_bf16x2(x, y);
+  for (int k = 0; k < 4; ++k) {
+    *nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
+    // shifted so that a code's 4 + 3 bits end at bit 4
+    o[2 * k] = mul_bf16x2((two_bytes<0x9180>(w[k]) << 4) & 0x87f087f0u, ws.m1);
+    o[2 * k + 1] = mul_bf16x2((two_bytes<0xb3a2>(w[k]) << 4) & 0x87f087f0u, ws.m1);
+  }
+  if (twice) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], ws.m2);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
@@ -239,7 +283,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset from the array, not a rounded address, so that accesses stay shared-memory ones)
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   const AttnArgs& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Ctl ctl{&sm.abort_flag, a.wait_limit_ns};
@@ -254,7 +299,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     sm.segs_done = 0;
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_free, 1);
-    mbar_init(&sm.q8_full, GROUP_THREADS);
+    mbar_init(&sm.q8_full, CONVERT_THREADS);
     mbar_init(&sm.q_empty, 1);
     for (int i = 0; i < C::NSK; ++i) {
       mbar_init(&sm.k_full[i], 1);
@@ -262,20 +307,20 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     }
     for (int i = 0; i < C::NSV; ++i) {
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], GROUP_THREADS);
+      mbar_init(&sm.v_empty[i], CONVERT_THREADS);
     }
     for (int i = 0; i < NVB; ++i) {
-      mbar_init(&sm.vb_full[i], GROUP_THREADS);
+      mbar_init(&sm.vb_full[i], CONVERT_THREADS);
       mbar_init(&sm.vb_empty[i], 1);
       mbar_init(&sm.vt_full[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
-      mbar_init(&sm.t_full[i], GROUP_THREADS);
-      mbar_init(&sm.t_empty[i], GROUP_THREADS / 32);
+      mbar_init(&sm.t_full[i], CONVERT_THREADS);
+      mbar_init(&sm.t_empty[i], SOFTMAX_THREADS / 32);
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], GROUP_THREADS);
+      mbar_init(&sm.p_full[i], SOFTMAX_THREADS);
       mbar_init(&sm.s_free[i], 1);
     }
     mbar_init(&sm.o_ready, 1);
@@ -486,7 +531,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           const uint32_t p_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
 #pragma unroll
           for (int i = 0; i < KV_TILE / 16; ++i)
-            mma_ts(tmem + TMEM_O, p_tmem + i * 8, smem_desc_sw128(v_addr + i * 2048, C::HALF_BYTES, 1024), ID_PV, j > 0 || i > 0);
+            mma_ts(tmem + TMEM_O + (i >> 2) * O_STRIDE, p_tmem + (i >> 2) * HALF_KEYS + (i & 3) * 8,
+                   smem_desc_sw128(v_addr + i * 2048, C::HALF_BYTES, 1024), ID_PV, j > 0 || (i & 3) > 0);
           mma_commit(&sm.o_ready);
           mma_commit(&sm.s_free[jg % NSB]);
           mma_commit(&sm.vb_empty[buf]);
@@ -496,7 +542,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         }
       }
     }
-  } else if (warp >= CONVERT_WARP0) {
+  } else if (warp < SOFTMAX_WARP0) {
     // ------------------------------------------------------------ conversion
     const int ct = threadIdx.x - CONVERT_WARP0 * 32;  // token of a tile, row of Q
     const int swz = ct & 7;
@@ -507,23 +553,30 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       const Seg I = make_seg(chain, cta, p_next, args);
       if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];  // on its way while this one runs
       if (I.n_tiles == 0) continue;
-      // Scales are fetched in two steps, the block of token ct three tiles ahead
-      // and its scale bytes two ahead (a token past the prefix has none).
+      // Scales are fetched for groups of four tiles: while one group is converted,
+      // the next one's scale bytes and the blocks of the one after are on their
+      // way (a register handed on from tile to tile would wait for its load; a
+      // token past the prefix has none).
       const int* table_row = a.block_table + (size_t)I.b * a.max_blocks;
       auto block_of = [&](int p) -> int {
         const int t = (I.t_begin + p) * KV_TILE + ct;
-        if (p >= I.n_prefix || t >= I.P) return -1;
-        const int blk = table_row[args.fd_bs.div(t)];
-        return blk < 0 || blk >= a.num_blocks ? 0 : blk;  // reported by the producers
+        return p < I.n_prefix && t < I.P ? table_row[args.fd_bs.div(t)] : 0;
       };
       auto scale_of = [&](int p, int blk) -> uint32_t {
-        if (blk < 0) return 0;
         const int t = (I.t_begin + p) * KV_TILE + ct;
+        if (p >= I.n_prefix || t >= I.P) return 0;
+        if (blk < 0 || blk >= a.num_blocks) blk = 0;  // reported by the producers
         return reinterpret_cast<const uint16_t*>(args.kv_scale)[((size_t)blk * a.Hkv + I.g) * a.bs + args.fd_bs.mod(t)];
       };
-      const int b0 = block_of(0), b1 = block_of(1);
-      int b_next = block_of(2);
-      uint32_t s_cur = scale_of(0, b0), s_next = scale_of(1, b1);
+      int blk[4];
+      uint32_t ahead[4];
+      uint64_t scales = 0;  // this group's, 16 bits a tile
+#pragma unroll
+      for (int i = 0; i < 4; ++i) blk[i] = block_of(i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ahead[i] = scale_of(i, blk[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) blk[i] = block_of(4 + i);
       float row_scale = 0.f;
       if (I.n_prefix > 0) {
         // the Q tile, row ct: scaled to within 448, hi and lo in place
@@ -578,12 +631,14 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         const bool tree = j < I.n_tree;
         const int p = j - I.n_tree;
-        const uint32_t sc = tree ? 0 : s_cur;
-        if (!tree) {
-          s_cur = s_next;
-          s_next = scale_of(p + 2, b_next);
-          b_next = block_of(p + 3);
+        if (!tree && (p & 3) == 0) {
+          scales = (uint64_t)(ahead[0] | (ahead[1] << 16)) | (uint64_t)(ahead[2] | (ahead[3] << 16)) << 32;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ahead[i] = scale_of(p + 4 + i, blk[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) blk[i] = block_of(p + 8 + i);
         }
+        const uint32_t sc = (uint32_t)(scales >> (16 * (p & 3))) & 0xffffu;
         const bool inside = !tree && (I.t_begin + p) * KV_TILE + ct < I.P;
         if (jg >= NT && !(ok = wait_bar(&sm.t_empty[jg % NT], ((jg / NT) - 1) & 1, ctl))) break;
         sm.key_scale[jg % NT][ct] = tree ? 1.f : (inside ? pow2_of(sc & 0xff) : 0.f);
@@ -604,18 +659,41 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           const int slot = vq % C::NSV;
           if (!(ok = wait_bar(&sm.v_full[slot], (vq / C::NSV) & 1, ctl))) break;
           const uint8_t* src = sm.v[slot] + ct * D;
-          const float scale = pow2_of(sc >> 8);
-#pragma unroll 2
-          for (int c = 0; c < D / 16; ++c) {
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            // chunk c of this row, where the 128-byte (D = 128) or 64-byte swizzle put it
-            const uint4 x = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4));
-            if (inside) widen16(x, scale, lo, hi);
-            uint8_t* row = wide + (c >> 2) * C::HALF_BYTES + ct * 128;
-            *reinterpret_cast<uint4*>(row + (((2 * (c & 3)) ^ swz) << 4)) = lo;
-            *reinterpret_cast<uint4*>(row + (((2 * (c & 3) + 1) ^ swz) << 4)) = hi;
-          }
+          // sc: the K row's byte, then the V row's; rows past the prefix become zeros
+          const WideScale ws(inside ? sc >> 8 : 0u);
+          const bool twice = __any_sync(0xffffffffu, (sc >> 8) > 134u);
+          const uint32_t keep = inside ? ~0u : 0u;
+          uint8_t* row = wide + ct * 128;
+          uint32_t nan = 0;
+          // all of the row's chunks at once (shared memory is busy: one load takes
+          // a few hundred cycles), from where the 128-byte (D = 128) or 64-byte
+          // swizzle put them
+          uint4 raw[D / 16];
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            raw[c] = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4));
           mbar_arrive(&sm.v_empty[slot]);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 x = make_uint4(raw[c].x & keep, raw[c].y & keep, raw[c].z & keep, raw[c].w & keep);
+            uint4 lo, hi;
+            widen16(x, ws, twice, lo, hi, &nan);
+            uint8_t* to = row + (c >> 2) * C::HALF_BYTES;
+            *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ swz) << 4)) = lo;
+            *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ swz) << 4)) = hi;
+          }
+          if (nan & 0x80808080u) {  // the row's NaN codes, one at a time
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll 1
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t word = e < 8 ? (e < 4 ? w[0] : w[1]) : (e < 12 ? w[2] : w[3]);
+                if (((word >> (8 * (e & 3))) & 0x7fu) == 0x7fu)
+                  *reinterpret_cast<uint16_t*>(row + (c >> 2) * C::HALF_BYTES + (((2 * (c & 3) + (e >> 3)) ^ swz) << 4) + (e & 7) * 2) = 0x7fff;
+              }
+            }
+          }
           ++vq;
           fence_proxy_async();
         }
@@ -624,9 +702,11 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int r = threadIdx.x - SOFTMAX_WARP0 * 32;
+    const int half = (warp - SOFTMAX_WARP0) >> 2;  // keys [64 half, 64 half + 64) of every tile
+    const int r = (warp & 3) * 32 + lane;
     const int R = a.N * a.G;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_tmem = tmem + lane_base + TMEM_O + half * O_STRIDE;
     int jg = 0;
     bool ok = true;
     int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
@@ -641,12 +721,12 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       // a warp none of whose rows exist only keeps the barriers going
       const bool busy = I.rt * ROW_TILE + (r & ~31) < R;
       const int slot = 2 * cta + (chain != chain0 ? 1 : 0);
-      uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
+      uint64_t anc[2] = {0ull, 0ull};  // this half's word of each tree tile
       if (active && I.n_tree > 0) {
         const uint64_t* arow = a.anc_mask + ((size_t)I.b * a.N + node) * a.W;
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          if (w < a.W) anc[w] = arow[w];
+        for (int w = 0; w < 2; ++w)
+          if (2 * w + half < a.W) anc[w] = arow[2 * w + half];
       }
       float m_run = NEG_INF;
       uint64_t sum2[2] = {0ull, 0ull};  // the running sum, in four independent parts
@@ -658,39 +738,41 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           break;
         }
         tc_fence_after();
-        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * 128;
+        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * 128 + half * HALF_KEYS;
         const bool tree = j < I.n_tree;
-        // keys of this tile that exist; a whole prefix tile needs no mask
-        const int valid = tree ? 0 : min(I.P - (I.t_begin + j - I.n_tree) * KV_TILE, KV_TILE);
-        const uint64_t vis_lo = j == 0 ? anc[0] : anc[2], vis_hi = j == 0 ? anc[1] : anc[3];
+        // which of this half's keys the row sees; a whole prefix tile needs no mask
+        const int valid = I.P - (I.t_begin + j - I.n_tree) * KV_TILE - half * HALF_KEYS;
+        const bool masked = tree || valid < HALF_KEYS;
+        const uint64_t see = tree ? (j == 0 ? anc[0] : anc[1]) : valid <= 0 ? 0ull : (1ull << (valid & 63)) - 1ull;
         const float row_scale = sm.row_scale[tb][r];
         const uint64_t scale2 = fx::pack2(row_scale, row_scale);
         // 32 columns at a time, in a loop that stays rolled: unrolled over the
         // tile, softmax and conversion together overflowed the instruction
         // caches (3 of 8 stall cycles an issue, 2.5 us a tile).
 #pragma unroll 1
-        for (int c = 0; busy && c < KV_TILE / 32; ++c) {
+        for (int c = 0; busy && c < HALF_KEYS / 32; ++c) {
           uint32_t u[32];
           tmem_ld32(s_tmem + c * 32, u);
+          float4 ks[8];  // on their way with S
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            ks[e] = reinterpret_cast<const float4*>(sm.key_scale[tb] + half * HALF_KEYS + c * 32)[e];
           tmem_ld_wait();
           reg_fence32(u);
           uint64_t y[16];
-          const float4* ks = reinterpret_cast<const float4*>(sm.key_scale[tb] + c * 32);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 f = ks[e];
             y[2 * e] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1])), fx::pack2(f.x, f.y));
             y[2 * e + 1] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3])), fx::pack2(f.z, f.w));
           }
-          if (valid < KV_TILE) {
-            uint32_t see;
-            if (tree) see = (uint32_t)((c < 2 ? vis_lo : vis_hi) >> (32 * (c & 1)));
-            else see = valid >= 32 * (c + 1) ? ~0u : valid <= 32 * c ? 0u : (1u << (valid - 32 * c)) - 1u;
+          if (masked) {
+            const uint32_t bits = (uint32_t)(see >> (32 * c));
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float x0, x1;
               fx::unpack2(y[e], x0, x1);
-              y[e] = fx::pack2((see >> (2 * e)) & 1u ? x0 : NEG_INF, (see >> (2 * e + 1)) & 1u ? x1 : NEG_INF);
+              y[e] = fx::pack2((bits >> (2 * e)) & 1u ? x0 : NEG_INF, (bits >> (2 * e + 1)) & 1u ? x1 : NEG_INF);
             }
           }
           float mk[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
@@ -702,16 +784,16 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             mk[(2 * e + 1) & 3] = fmaxf(mk[(2 * e + 1) & 3], x1);
           }
           const float mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * row_scale;
-          const bool rescale = mx > m_run + RESCALE_THRESHOLD;
+          const bool rescale = mx > m_run + RESCALE;
           if (__any_sync(0xffffffffu, rescale)) {
-            // Rows whose maximum rose past the threshold: what they have so far
+            // Rows that get a new reference: what they have so far
             // is scaled down (the warp together; the others by 1).
             const float f = !rescale ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - mx));
             if (rescale) m_run = mx;
             const uint64_t f2 = fx::pack2(f, f);
             sum2[0] = fx::mul2(sum2[0], f2);
             sum2[1] = fx::mul2(sum2[1], f2);
-            if (c > 0) {  // this tile's P so far (what is left of it is below 2^-20)
+            if (c > 0) {  // this tile's P so far (what is left of it is below 2^-40)
               tmem_st_wait();
 #pragma unroll 1
               for (int i = 0; i < c; ++i) {
@@ -732,12 +814,12 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
 #pragma unroll 1
               for (int d = 0; d < D; d += 32) {
                 uint32_t w[32];
-                tmem_ld32(tmem + lane_base + TMEM_O + d, w);
+                tmem_ld32(o_tmem + d, w);
                 tmem_ld_wait();
                 reg_fence32(w);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-                tmem_st32(tmem + lane_base + TMEM_O + d, w);
+                tmem_st32(o_tmem + d, w);
               }
             }
           }
@@ -762,62 +844,83 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         tc_fence_before();
         mbar_arrive(&sm.p_full[jg % NSB]);
       }
-      if (!ok) break;
       float l_run;
       {
         float r0, r1;
         fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
         l_run = r0 + r1;
       }
-      // end of the segment: normalise and store
-      if (I.n_tiles > 0 && !__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
-        ok = false;
-        break;
-      }
+      // End of the segment: the two halves' O, each with its maximum and sum,
+      // are joined, normalised and stored, D/2 channels by each group.  (A warp
+      // whose wait gave up comes here too: its partner may be waiting.)
+      sm.half_ml[half][r] = make_float2(m_run, l_run);
+      ok = ok && (I.n_tiles == 0 || wait_count(&sm.pv_done, jg, ctl));
+      ok = named_barrier_and(1 + (warp & 3), 64, ok);
+      if (!ok) break;
       tc_fence_after();
-      const bool none = l_run == 0.f;  // the row saw no key
-      const float inv = none ? 0.f : 1.f / l_run;
-      const float lse2 = none ? NEG_INF : m_run + __log2f(l_run);
+      const float2 other = sm.half_ml[half ^ 1][r];
+      const float m = fmaxf(m_run, other.x);
+      const float w_own = m_run == NEG_INF ? 0.f : ex2(m_run - m), w_other = other.x == NEG_INF ? 0.f : ex2(other.x - m);
+      const float l = l_run * w_own + other.y * w_other;
+      const bool none = l == 0.f;  // the row saw no key
+      const float inv = none ? 0.f : 1.f / l;
+      const float lse2 = none ? NEG_INF : m + __log2f(l);
       const size_t orow = ((size_t)I.b * a.N + node) * a.Hq + h;
+      float f0 = half == 0 ? w_own * inv : w_other * inv, f1 = half == 0 ? w_other * inv : w_own * inv;
       if (I.n_tiles == 0) {
-        if (active) args.part_ls[(size_t)slot * ROW_TILE + r] = make_float2(NEG_INF, 0.f);
+        if (active && half == 0) args.part_ls[(size_t)slot * ROW_TILE + r] = make_float2(NEG_INF, 0.f);
       } else if (busy) {
-        float f = inv;
+        const uint32_t o0 = tmem + lane_base + TMEM_O;
+        // columns [c, c + 32) of the normalised row (zeros for a row that saw nothing, whatever its O holds)
+        auto columns = [&](int c, float (&x)[32]) {
+          uint32_t u[32], v[32];
+          tmem_ld32(o0 + c, u);
+          tmem_ld32(o0 + O_STRIDE + c, v);
+          tmem_ld_wait();
+          reg_fence32(u);
+          reg_fence32(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float p = f0 == 0.f ? 0.f : __uint_as_float(u[e]) * f0;
+            x[e] = f1 == 0.f ? p : fmaf(__uint_as_float(v[e]), f1, p);
+          }
+        };
         if (!I.whole) {
-          // a part: 16-bit values of at most 2^10 with the row's power of two
+          // a part: 16-bit values below 2^10 with a power of two for these D/2 channels
           float top = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t u[32];
-            tmem_ld32(tmem + lane_base + TMEM_O + c, u);
-            tmem_ld_wait();
-            reg_fence32(u);
+          for (int c = 0; c < D / 2; c += 32) {
+            float x[32];
+            columns(half * (D / 2) + c, x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(u[e])));
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
           }
-          top *= inv;
           const int e = min(max((int)(__float_as_uint(top) >> 23), 10), 253);  // top < 2^(e - 126)
-          f = inv * pow2_of(263 - e);                                          // times 2^(136 - e): below 2^10
-          if (active) args.part_ls[(size_t)slot * ROW_TILE + r] = make_float2(lse2, pow2_of(e - 9));
-        } else if (active && a.lse) {
+          const float up = pow2_of(263 - e);                                   // 2^(136 - e)
+          f0 *= up;
+          f1 *= up;
+          if (active) {
+            float2* ls = args.part_ls + (size_t)slot * ROW_TILE + r;
+            if (half == 0) *ls = make_float2(lse2, pow2_of(e - 9));
+            else args.part_f1[(size_t)slot * ROW_TILE + r] = pow2_of(e - 9);
+          }
+        } else if (active && half == 0 && a.lse) {
           a.lse[orow] = lse2 * 0.69314718055994531f;
         }
         __half* part = args.part_o + ((size_t)slot * ROW_TILE + r) * D;
         __nv_bfloat16* out = a.out + orow * D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t u[32], w[16];
-          tmem_ld32(tmem + lane_base + TMEM_O + c, u);
-          tmem_ld_wait();
-          reg_fence32(u);
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+          const int c = half * (D / 2) + c0;
+          float x[32];
+          uint32_t w[16];
+          columns(c, x);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x = none ? 0.f : __uint_as_float(u[2 * e]) * f;
-            const float y = none ? 0.f : __uint_as_float(u[2 * e + 1]) * f;
             if (I.whole) {
-              w[e] = pack_bf16x2(x, y);
+              w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
             } else {
-              const __half2 t = __floats2half2_rn(x, y);
+              const __half2 t = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
               w[e] = *reinterpret_cast<const uint32_t*>(&t);
             }
           }
@@ -834,9 +937,10 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           }
         }
       }
+      // both halves have read O, and each other's sums, before the next segment's first P
       tc_fence_before();
-      __syncwarp();
-      if (r == 0) publish(&sm.segs_done, chain - chain0 + 1);
+      named_barrier_and(1 + (warp & 3), 64, true);
+      if (half == 0 && r == 0) publish(&sm.segs_done, chain - chain0 + 1);
     }
   }
 
@@ -855,7 +959,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       uint64_t* d = &sm.drain[warp - QK_WARP];
       mma_commit(d);
       mbar_wait(d, 0, a.wait_limit_ns);
-    } else if (threadIdx.x == CONVERT_WARP0 * 32) {
+    } else if (threadIdx.x == CONVERT_WARP0 * 32) {  // (thread 0 of the conversion loads the tree's V)
       for (int i = 0; i < NVB; ++i)
         if (vt_issued[i] > 0) mbar_wait(&sm.vt_full[i], (vt_issued[i] - 1) & 1, a.wait_limit_ns);
     }
@@ -907,7 +1011,7 @@ k_merge_q8(const __grid_constant__ Q8Args args) {
     const float m_new = fmaxf(m, ls.x);
     const float f = m == NEG_INF ? 0.f : exp2f(m - m_new), w = exp2f(ls.x - m_new);
     den = den * f + w;
-    const float ws = w * ls.y;
+    const float ws = w * (sub < LANES / 2 ? ls.y : args.part_f1[(size_t)slot * ROW_TILE + r]);
     const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -998,6 +1102,7 @@ bool any_cut(const Runs& r) {
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t part_o_bytes(const Runs& r, int D) { return any_cut(r) ? round256((size_t)2 * r.n * ROW_TILE * D * 2) : 0; }
 size_t part_ls_bytes(const Runs& r) { return any_cut(r) ? round256((size_t)2 * r.n * ROW_TILE * sizeof(float2)) : 0; }
+size_t part_f1_bytes(const Runs& r) { return part_ls_bytes(r) / 2; }
 
 bool encode_codes(CUtensorMap* m, const void* base, int D, const AttnArgs& a, int box_rows) {
   // codes [num_blocks * Hkv, bs, D]: a box is box_rows tokens, every channel,
@@ -1055,7 +1160,7 @@ cudaError_t attn_q8_prepare() {
 
 size_t attn_q8_workspace(const ts_attn_params* p) {
   const Runs r = plan_runs(p);
-  return 256 + part_o_bytes(r, p->D) + part_ls_bytes(r);
+  return 256 + part_o_bytes(r, p->D) + part_ls_bytes(r) + round256(part_f1_bytes(r));
 }
 
 cudaError_t launch_attn_q8(const AttnQ8Args& q, const ts_attn_params* p, void* workspace, cudaStream_t s) {
@@ -1067,6 +1172,7 @@ cudaError_t launch_attn_q8(const AttnQ8Args& q, const ts_attn_params* p, void* w
   char* ws = static_cast<char*>(workspace) + 256;
   t.part_o = reinterpret_cast<__half*>(ws);
   t.part_ls = reinterpret_cast<float2*>(ws + part_o_bytes(t.runs, a.D));
+  t.part_f1 = reinterpret_cast<float*>(ws + part_o_bytes(t.runs, a.D) + part_ls_bytes(t.runs));
   t.box_rows = KV_TILE;
   while (a.bs % t.box_rows != 0) t.box_rows >>= 1;
   t.nodes_per_tile = ROW_TILE / a.G;
