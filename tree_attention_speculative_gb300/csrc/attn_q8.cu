@@ -180,17 +180,53 @@ struct Ctl {
   volatile int* flag;
   uint64_t limit;
 };
-// A wait polls in a loop of nothing but the poll and looks at the abort flag
-// and the clock now and then: sixteen warps polling with both in the loop took
-// a third of the SM's issue slots.
-constexpr int POLLS = 32;
+// Polls a barrier some times over, two instructions a poll: with sixteen warps
+// on the SM, waits that looked at the clock and the abort flag on every poll
+// took a third of its issue slots.
+__device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "AGAIN_%=:\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 p, n, 16;\n\t"
+      "@p bra AGAIN_%=;\n\t"
+      "setp.ne.u32 p, n, n;\n"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
+  if (poll_bar(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (poll_bar(bar, parity)) return true;
+    if (*c.flag) return false;
+    if (globaltimer_ns() - t0 > c.limit) {
+      *c.flag = 1;
+      return false;
+    }
+  }
+}
+// The same for the loads, which run several tiles ahead: sleeps between polls.
+__device__ __forceinline__ bool wait_bar_idle(uint64_t* bar, uint32_t parity, const Ctl& c) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-#pragma unroll 1
-    for (int i = 0; i < POLLS; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+    __nanosleep(64);
+    if (mbar_try_wait(bar, parity)) return true;
     if (*c.flag) return false;
     if (globaltimer_ns() - t0 > c.limit) {
       *c.flag = 1;
@@ -228,11 +264,11 @@ __device__ __forceinline__ float pow2_of(int biased) { return __uint_as_float((u
 // A row's power of two as the multipliers of widen16: 2^(s - 127) * 2^120 in
 // one bf16 pair, or where that is too large (s > 134), in two.
 struct WideScale {
-  uint32_t m1, m2;
-  __device__ __forceinline__ explicit WideScale(uint32_t s) {
+  uint32_t m1, m2;  // m1 is 0 for a row to be zeroed
+  __device__ __forceinline__ WideScale(uint32_t s, bool keep) {
     const uint32_t b1 = min(s + 120u, 254u), b2 = s + 247u - b1;
-    m1 = (b1 << 7) | (b1 << 23);
-    m2 = (b2 << 7) | (b2 << 23);
+    m1 = keep ? (b1 << 7) | (b1 << 23) : 0u;
+    m2 = (b2 << 7) | (b2 << 23);  // 1 for all but the largest rows
   }
 };
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -252,19 +288,15 @@ __device__ __forceinline__ uint32_t two_bytes(uint32_t w) {
 // 2^-120 (subnormal codes too), so a bit shuffle and a product do: exact, and
 // half the cost of going through fp16 and fp32.  Only a NaN code would come out
 // as a number; *nan collects bits 0x80808080 for those.
-__device__ __forceinline__ void widen16(const uint4& c, const WideScale& ws, bool twice, uint4& lo, uint4& hi, uint32_t* nan) {
+__device__ __forceinline__ void widen16(const uint4& c, uint32_t m1, uint4& lo, uint4& hi, uint32_t* nan) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t o[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     *nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
     // shifted so that a code's 4 + 3 bits end at bit 4
-    o[2 * k] = mul_bf16x2((two_bytes<0x9180>(w[k]) << 4) & 0x87f087f0u, ws.m1);
-    o[2 * k + 1] = mul_bf16x2((two_bytes<0xb3a2>(w[k]) << 4) & 0x87f087f0u, ws.m1);
-  }
-  if (twice) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], ws.m2);
+    o[2 * k] = mul_bf16x2((two_bytes<0x9180>(w[k]) << 4) & 0x87f087f0u, m1);
+    o[2 * k + 1] = mul_bf16x2((two_bytes<0xb3a2>(w[k]) << 4) & 0x87f087f0u, m1);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
@@ -365,7 +397,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     auto take = [&]() -> bool {
       bool r = true;
       if (issued >= nst) {
-        if (lane == 0) r = wait_bar(&empty[slot], phase ^ 1, ctl);
+        if (lane == 0) r = wait_bar_idle(&empty[slot], phase ^ 1, ctl);
         r = __shfl_sync(0xffffffffu, r, 0);
       }
       return r;
@@ -659,41 +691,43 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           const int slot = vq % C::NSV;
           if (!(ok = wait_bar(&sm.v_full[slot], (vq / C::NSV) & 1, ctl))) break;
           const uint8_t* src = sm.v[slot] + ct * D;
-          // sc: the K row's byte, then the V row's; rows past the prefix become zeros
-          const WideScale ws(inside ? sc >> 8 : 0u);
-          const bool twice = __any_sync(0xffffffffu, (sc >> 8) > 134u);
-          const uint32_t keep = inside ? ~0u : 0u;
+          // sc: the K row's byte, then the V row's; rows past the prefix become zeros.
+          // One 16-code chunk an iteration, the next one on its way; rolled, so that
+          // it stays in the instruction cache beside the softmax.
+          const WideScale ws(inside ? sc >> 8 : 0u, inside);
+          auto chunk = [&](int c) {  // chunk c of this row, where the 128-byte (D = 128) or 64-byte swizzle put it
+            return *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4));
+          };
           uint8_t* row = wide + ct * 128;
           uint32_t nan = 0;
-          // all of the row's chunks at once (shared memory is busy: one load takes
-          // a few hundred cycles), from where the 128-byte (D = 128) or 64-byte
-          // swizzle put them
-          uint4 raw[D / 16];
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            raw[c] = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4));
-          mbar_arrive(&sm.v_empty[slot]);
-#pragma unroll
+          uint4 x = chunk(0);
+#pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
-            const uint4 x = make_uint4(raw[c].x & keep, raw[c].y & keep, raw[c].z & keep, raw[c].w & keep);
+            const uint4 x_next = chunk((c + 1) & (D / 16 - 1));
             uint4 lo, hi;
-            widen16(x, ws, twice, lo, hi, &nan);
+            widen16(x, ws.m1, lo, hi, &nan);
             uint8_t* to = row + (c >> 2) * C::HALF_BYTES;
             *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ swz) << 4)) = lo;
             *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ swz) << 4)) = hi;
+            x = x_next;
           }
-          if (nan & 0x80808080u) {  // the row's NaN codes, one at a time
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+          if (inside && ws.m2 != 0x3f803f80u) {  // (a row beyond 2^15: the rest of its power of two)
 #pragma unroll 1
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t word = e < 8 ? (e < 4 ? w[0] : w[1]) : (e < 12 ? w[2] : w[3]);
-                if (((word >> (8 * (e & 3))) & 0x7fu) == 0x7fu)
-                  *reinterpret_cast<uint16_t*>(row + (c >> 2) * C::HALF_BYTES + (((2 * (c & 3) + (e >> 3)) ^ swz) << 4) + (e & 7) * 2) = 0x7fff;
-              }
+            for (int e = 0; e < D / 2; ++e) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(row + (e >> 5) * C::HALF_BYTES + (((e & 31) >> 2) << 4)) + (e & 3);
+              *w = mul_bf16x2(*w, ws.m2);
             }
           }
+          if (inside && (nan & 0x80808080u)) {  // the row's NaN codes, one at a time
+#pragma unroll 1
+            for (int e = 0; e < D; ++e) {
+              const int c = e >> 4;
+              const uint8_t code = src[((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4) + (e & 15)];
+              if ((code & 0x7f) == 0x7f)
+                *reinterpret_cast<uint16_t*>(row + (e >> 6) * C::HALF_BYTES + ((((e & 63) >> 3) ^ swz) << 4) + (e & 7) * 2) = 0x7fff;
+            }
+          }
+          mbar_arrive(&sm.v_empty[slot]);
           ++vq;
           fence_proxy_async();
         }
