@@ -56,6 +56,7 @@
 #include "tensor_map.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ts {
 namespace {
@@ -76,12 +77,12 @@ constexpr int HALF_KEYS = 64;  // keys of a tile a softmax group takes
 constexpr int NT = 4;   // tiles' key scales in flight
 constexpr int NVB = 2;  // widened V tiles
 constexpr int SLOT = 16384;  // a ring slot: 128 tokens of 128 codes, or a 64-column half of a bf16 tree tile
-// A row keeps the reference m it took from its first keys until a logit passes
-// it by RESCALE (log2 units).  bf16 P, fp32 sums and O have the same precision
+// A row keeps the reference m it took from its first keys until the weights of
+// 32 keys sum past RESCALE_SUM.  bf16 P, fp32 sums and O have the same precision
 // at every magnitude, so weights up to 2^40 are as good as weights up to 1, and
 // O is hardly ever rescaled, hot keys or not.  (Sums then stay finite for
 // values up to 2^127 / (2^40 x keys), past 2^69.)
-constexpr float RESCALE = 40.0f;
+constexpr float RESCALE_SUM = 1099511627776.f;  // 2^40
 constexpr float NEG_INF = -INFINITY;
 
 template <int D>
@@ -100,6 +101,8 @@ struct __align__(1024) Smem {
   uint8_t q[C::WIDE_BYTES];  // bf16 [half][row][128 B]; then the row's 128-byte pieces hold hi and lo
   uint8_t k[C::NSK][SLOT];
   uint8_t v[C::NSV][SLOT];
+  uint16_t v_scale[C::NSV][KV_TILE];  // with each V tile its tokens' scale bytes: K row's, V row's
+  uint8_t pad[1024 - (C::NSV * KV_TILE * 2) % 1024];
   uint8_t vb[NVB][C::WIDE_BYTES];  // bf16 [half][token][128 B]
   // Scales of tile j (entry j % NT): the token's power of two for its key, and
   // the row's factor (the query's power of two times scale * log2 e).
@@ -302,6 +305,15 @@ __device__ __forceinline__ void widen16(const uint4& c, uint32_t m1, uint4& lo, 
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// 8 bytes from global to shared memory, asynchronously; cp_async_arrive arrives
+// on the barrier once this thread's have landed.
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint64_t>(p)),
                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -338,7 +350,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       mbar_init(&sm.k_empty[i], 1);
     }
     for (int i = 0; i < C::NSV; ++i) {
-      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_full[i], 1 + 32);  // the tile, and each lane's scale bytes
       mbar_init(&sm.v_empty[i], CONVERT_THREADS);
     }
     for (int i = 0; i < NVB; ++i) {
@@ -461,6 +473,14 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(mask) * box_bytes);
         __syncwarp();
         if (issue) tma_load_3d((is_v ? sm.v[slot] : sm.k[slot]) + lane * box_bytes, tm_pool, &full[slot], 0, row, blk * a.Hkv + I.g);
+        if (is_v) {
+          // scale bytes of tokens 4 lane .. 4 lane + 3 (of one block: blocks are multiples of 16)
+          const int box = 4 * lane / g_box;
+          const int blk_s = __shfl_sync(0xffffffffu, blk, box), row_s = __shfl_sync(0xffffffffu, row, box) + 4 * lane - box * g_box;
+          if (key - koff + 4 * lane < I.P)
+            cp_async8(&sm.v_scale[slot][4 * lane], args.kv_scale + 2 * (((size_t)blk_s * a.Hkv + I.g) * a.bs + row_s));
+          cp_async_arrive(&full[slot]);
+        }
         __syncwarp();
         key += KV_TILE;
         row += row_step;
@@ -585,30 +605,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       const Seg I = make_seg(chain, cta, p_next, args);
       if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];  // on its way while this one runs
       if (I.n_tiles == 0) continue;
-      // Scales are fetched for groups of four tiles: while one group is converted,
-      // the next one's scale bytes and the blocks of the one after are on their
-      // way (a register handed on from tile to tile would wait for its load; a
-      // token past the prefix has none).
-      const int* table_row = a.block_table + (size_t)I.b * a.max_blocks;
-      auto block_of = [&](int p) -> int {
-        const int t = (I.t_begin + p) * KV_TILE + ct;
-        return p < I.n_prefix && t < I.P ? table_row[args.fd_bs.div(t)] : 0;
-      };
-      auto scale_of = [&](int p, int blk) -> uint32_t {
-        const int t = (I.t_begin + p) * KV_TILE + ct;
-        if (p >= I.n_prefix || t >= I.P) return 0;
-        if (blk < 0 || blk >= a.num_blocks) blk = 0;  // reported by the producers
-        return reinterpret_cast<const uint16_t*>(args.kv_scale)[((size_t)blk * a.Hkv + I.g) * a.bs + args.fd_bs.mod(t)];
-      };
-      int blk[4];
-      uint32_t ahead[4];
-      uint64_t scales = 0;  // this group's, 16 bits a tile
-#pragma unroll
-      for (int i = 0; i < 4; ++i) blk[i] = block_of(i);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ahead[i] = scale_of(i, blk[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) blk[i] = block_of(4 + i);
       float row_scale = 0.f;
       if (I.n_prefix > 0) {
         // the Q tile, row ct: scaled to within 448, hi and lo in place
@@ -660,22 +656,29 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         ++q8;
       }
       ++qn;
+      // Hands tile jt's scales (the tree's: 1) to the softmax; p: its prefix tile, at ring position vq + ahead.
+      auto hand_scales = [&](int jt, bool tree, int p, int ahead) -> bool {
+        float key = 1.f, rs = a.scale_log2;
+        if (!tree) {
+          const int slot = (vq + ahead) % C::NSV;
+          if (!wait_bar(&sm.v_full[slot], ((vq + ahead) / C::NSV) & 1, ctl)) return false;
+          key = (I.t_begin + p) * KV_TILE + ct < I.P ? pow2_of(sm.v_scale[slot][ct] & 0xff) : 0.f;
+          rs = row_scale;
+        }
+        if (jt >= NT && !wait_bar(&sm.t_empty[jt % NT], ((jt / NT) - 1) & 1, ctl)) return false;
+        sm.key_scale[jt % NT][ct] = key;
+        sm.row_scale[jt % NT][ct] = rs;
+        mbar_arrive(&sm.t_full[jt % NT]);
+        return true;
+      };
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         const bool tree = j < I.n_tree;
         const int p = j - I.n_tree;
-        if (!tree && (p & 3) == 0) {
-          scales = (uint64_t)(ahead[0] | (ahead[1] << 16)) | (uint64_t)(ahead[2] | (ahead[3] << 16)) << 32;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ahead[i] = scale_of(p + 4 + i, blk[i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) blk[i] = block_of(p + 8 + i);
-        }
-        const uint32_t sc = (uint32_t)(scales >> (16 * (p & 3))) & 0xffffu;
+        // scales go out a tile ahead of the values
+        if (tree || p == 0) ok = hand_scales(jg, tree, p, 0);
+        if (ok && !tree && p + 1 < I.n_prefix) ok = hand_scales(jg + 1, false, p + 1, 1);
+        if (!ok) break;
         const bool inside = !tree && (I.t_begin + p) * KV_TILE + ct < I.P;
-        if (jg >= NT && !(ok = wait_bar(&sm.t_empty[jg % NT], ((jg / NT) - 1) & 1, ctl))) break;
-        sm.key_scale[jg % NT][ct] = tree ? 1.f : (inside ? pow2_of(sc & 0xff) : 0.f);
-        sm.row_scale[jg % NT][ct] = tree ? a.scale_log2 : row_scale;
-        mbar_arrive(&sm.t_full[jg % NT]);
         const int buf = jg % NVB;
         if (jg >= NVB && !(ok = wait_bar(&sm.vb_empty[buf], ((jg / NVB) - 1) & 1, ctl))) break;
         uint8_t* wide = sm.vb[buf];
@@ -689,8 +692,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           }
         } else {
           const int slot = vq % C::NSV;
-          if (!(ok = wait_bar(&sm.v_full[slot], (vq / C::NSV) & 1, ctl))) break;
           const uint8_t* src = sm.v[slot] + ct * D;
+          const uint32_t sc = sm.v_scale[slot][ct];
           // sc: the K row's byte, then the V row's; rows past the prefix become zeros.
           // One 16-code chunk an iteration, the next one on its way; rolled, so that
           // it stays in the instruction cache beside the softmax.
@@ -762,8 +765,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         for (int w = 0; w < 2; ++w)
           if (2 * w + half < a.W) anc[w] = arow[2 * w + half];
       }
-      float m_run = NEG_INF;
-      uint64_t sum2[2] = {0ull, 0ull};  // the running sum, in four independent parts
+      // reference and sum (rows of the padding, which see nothing, need no reference)
+      float m_run = active ? NEG_INF : 0.f, l_run = 0.f;
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         const int tb = jg % NT;
         if (!__all_sync(0xffffffffu, wait_bar(&sm.t_full[tb], (jg / NT) & 1, ctl) &&
@@ -776,113 +779,116 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         const bool tree = j < I.n_tree;
         // which of this half's keys the row sees; a whole prefix tile needs no mask
         const int valid = I.P - (I.t_begin + j - I.n_tree) * KV_TILE - half * HALF_KEYS;
-        const bool masked = tree || valid < HALF_KEYS;
         const uint64_t see = tree ? (j == 0 ? anc[0] : anc[1]) : valid <= 0 ? 0ull : (1ull << (valid & 63)) - 1ull;
         const float row_scale = sm.row_scale[tb][r];
         const uint64_t scale2 = fx::pack2(row_scale, row_scale);
         // 32 columns at a time, in a loop that stays rolled: unrolled over the
         // tile, softmax and conversion together overflowed the instruction
         // caches (3 of 8 stall cycles an issue, 2.5 us a tile).
+        auto columns = [&](auto masked) -> bool {
 #pragma unroll 1
-        for (int c = 0; busy && c < HALF_KEYS / 32; ++c) {
-          uint32_t u[32];
-          tmem_ld32(s_tmem + c * 32, u);
-          float4 ks[8];  // on their way with S
+          for (int c = 0; c < HALF_KEYS / 32; ++c) {
+            uint32_t u[32];
+            tmem_ld32(s_tmem + c * 32, u);
+            float4 ks[8];  // on their way with S
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            ks[e] = reinterpret_cast<const float4*>(sm.key_scale[tb] + half * HALF_KEYS + c * 32)[e];
-          tmem_ld_wait();
-          reg_fence32(u);
-          uint64_t y[16];
+            for (int e = 0; e < 8; ++e)
+              ks[e] = reinterpret_cast<const float4*>(sm.key_scale[tb] + half * HALF_KEYS + c * 32)[e];
+            tmem_ld_wait();
+            reg_fence32(u);
+            uint64_t y[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 f = ks[e];
-            y[2 * e] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1])), fx::pack2(f.x, f.y));
-            y[2 * e + 1] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3])), fx::pack2(f.z, f.w));
-          }
-          if (masked) {
-            const uint32_t bits = (uint32_t)(see >> (32 * c));
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x0, x1;
-              fx::unpack2(y[e], x0, x1);
-              y[e] = fx::pack2((bits >> (2 * e)) & 1u ? x0 : NEG_INF, (bits >> (2 * e + 1)) & 1u ? x1 : NEG_INF);
+            for (int e = 0; e < 8; ++e) {
+              y[2 * e] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1])), fx::pack2(ks[e].x, ks[e].y));
+              y[2 * e + 1] = fx::mul2(fx::pack2(__uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3])), fx::pack2(ks[e].z, ks[e].w));
             }
-          }
-          float mk[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+            if constexpr (decltype(masked)::value) {
+              const uint32_t bits = (uint32_t)(see >> (32 * c));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            fx::unpack2(y[e], x0, x1);
-            mk[(2 * e) & 3] = fmaxf(mk[(2 * e) & 3], x0);
-            mk[(2 * e + 1) & 3] = fmaxf(mk[(2 * e + 1) & 3], x1);
-          }
-          const float mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * row_scale;
-          const bool rescale = mx > m_run + RESCALE;
-          if (__any_sync(0xffffffffu, rescale)) {
-            // Rows that get a new reference: what they have so far
-            // is scaled down (the warp together; the others by 1).
-            const float f = !rescale ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - mx));
-            if (rescale) m_run = mx;
-            const uint64_t f2 = fx::pack2(f, f);
-            sum2[0] = fx::mul2(sum2[0], f2);
-            sum2[1] = fx::mul2(sum2[1], f2);
-            if (c > 0) {  // this tile's P so far (what is left of it is below 2^-40)
-              tmem_st_wait();
-#pragma unroll 1
-              for (int i = 0; i < c; ++i) {
-                uint32_t w[16];
-                tmem_ld16(s_tmem + i * 16, w);
-                tmem_ld_wait();
-                reg_fence16(w);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-                tmem_st16(s_tmem + i * 16, w);
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                fx::unpack2(y[e], x0, x1);
+                y[e] = fx::pack2((bits >> (2 * e)) & 1u ? x0 : NEG_INF, (bits >> (2 * e + 1)) & 1u ? x1 : NEG_INF);
               }
             }
-            if (j > 0) {  // O, which must hold every earlier PV
-              ok = __all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl));
-              if (!ok) break;
-              tc_fence_after();
+            // p = 2^(y * row_scale - m) as bf16, and their sum.  No maximum is
+            // taken: a sum past 2^RESCALE says that m is too low, and a row
+            // without an m has no key yet; then m is set and the chunk repeated.
+            uint32_t pk[16];
+            float sum;
 #pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
-                uint32_t w[32];
-                tmem_ld32(o_tmem + d, w);
-                tmem_ld_wait();
-                reg_fence32(w);
+            while (true) {
+              const float m_exp = m_run == NEG_INF ? 0.f : m_run;  // (no key so far: every p is 0)
+              const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
+              uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-                tmem_st32(o_tmem + d, w);
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                fx::unpack2(fx::fma2(y[e], scale2, negm2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
+                pk[e] = pack_bf16x2(p0, p1);
+              }
+              float r0, r1;
+              fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
+              sum = r0 + r1;
+              const bool high = sum > RESCALE_SUM || m_run == NEG_INF;
+              if (!__any_sync(0xffffffffu, high)) break;
+              float mx = NEG_INF;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                fx::unpack2(y[e], x0, x1);
+                mx = fmaxf(mx, fmaxf(x0, x1));
+              }
+              mx *= row_scale;
+              const bool move = high && mx > m_run;  // (the sum was high, or these are the row's first keys)
+              if (!__any_sync(0xffffffffu, move)) break;
+              // What the row has so far is scaled down (the warp together; the others by 1).
+              const float f = !move ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - mx));
+              if (move) m_run = mx;
+              l_run *= f;
+              if (c > 0) {  // this tile's P so far
+                tmem_st_wait();
+#pragma unroll 1
+                for (int i = 0; i < c; ++i) {
+                  uint32_t w[16];
+                  tmem_ld16(s_tmem + i * 16, w);
+                  tmem_ld_wait();
+                  reg_fence16(w);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+                  tmem_st16(s_tmem + i * 16, w);
+                }
+              }
+              if (j > 0) {  // O, which must hold every earlier PV
+                if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                  uint32_t w[32];
+                  tmem_ld32(o_tmem + d, w);
+                  tmem_ld_wait();
+                  reg_fence32(w);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                  tmem_st32(o_tmem + d, w);
+                }
               }
             }
+            l_run += sum;
+            tmem_st16(s_tmem + c * 16, pk);
           }
-          // p = 2^(y * row_scale - m) (nothing visible so far: all 0), over S as bf16
-          const float m_exp = m_run == NEG_INF ? 0.f : m_run;
-          const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            fx::unpack2(fx::fma2(y[e], scale2, negm2), x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);
-          }
-          tmem_st16(s_tmem + c * 16, pk);
-        }
+          return true;
+        };
+        if (busy) ok = tree || valid < HALF_KEYS ? columns(std::true_type{}) : columns(std::false_type{});
         if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.t_empty[tb]);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.p_full[jg % NSB]);
-      }
-      float l_run;
-      {
-        float r0, r1;
-        fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
-        l_run = r0 + r1;
       }
       // End of the segment: the two halves' O, each with its maximum and sum,
       // are joined, normalised and stored, D/2 channels by each group.  (A warp
@@ -984,6 +990,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     // A wait gave up.  Nothing may still write this CTA's shared memory or TMEM
     // once it exits: wait (bounded) for the newest loads of each ring, for a Q
     // tile, for the tree's V tiles and for every MMA started.
+    if (warp == V_WARP) asm volatile("cp.async.wait_all;" ::: "memory");
     if ((warp == K_WARP || warp == V_WARP) && lane == 0) {
       uint64_t* full = warp == V_WARP ? sm.v_full : sm.k_full;
       const int nst = warp == V_WARP ? C::NSV : C::NSK;
