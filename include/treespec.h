@@ -524,9 +524,10 @@ TS_API ts_status tree_rope(const ts_rope_params* p, ts_stream stream);
  * The 8-bit paged cache.  A row (one token of one KV head, D values) is D e4m3
  * codes and one scale byte s; its values are code * 2^(s - 127).  The writers
  * take the smallest power of two that keeps the row's largest magnitude within
- * 448 (s in [1, 247]), round to the nearest code (ties to even), store an
- * infinity as +-448 and a NaN as a NaN code.  A power of two scales without
- * rounding, so codes and bytes are the same on every run.
+ * 448 (s in [1, 247]), round to the nearest code (ties to even) and store an
+ * infinity as +-448.  A row with a NaN is stored as NaN throughout (s = 255,
+ * every code 0x7f); NaN codes occur in such rows only.  A power of two scales
+ * without rounding, so codes and bytes are the same on every run.
  *
  *   k_cache, v_cache  [num_blocks, Hkv, block_size, D] e4m3, 16-byte aligned.
  *   kv_scale          [num_blocks, Hkv, block_size, 2] uint8, the K row's byte
@@ -585,7 +586,7 @@ TS_API ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree,
  * Values past bf16's largest (255 * 2^120; only rows within 3% of it, or with
  * an infinity, hold any) read as infinite.
  * A row that sees no key (no prefix and an empty mask row) gives zeros and an
- * lse of -inf.  Scale bytes of the prefix's rows must lie in [1, 254].
+ * lse of -inf.  The prefix's rows must be as the writers store them.
  *
  * tree_attn_q8_workspace_size: bytes of device workspace it needs (256-byte
  * aligned, ZERO-FILLED before its first use, then left so that stream-ordered

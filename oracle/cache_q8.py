@@ -2,9 +2,9 @@
 
 A row of values x is stored as e4m3 codes and a scale byte s, value = code *
 2^(s - 127).  s is the smallest in [1, 247] with max |x| <= 448 * 2^(s - 127)
-over the row's numbers (an infinite row takes 247); a code is the e4m3 value
-nearest x * 2^(127 - s), ties to the even code, held within +-448; a NaN is a NaN
-code (0x7f).
+over the row (247 if it has an infinity); a code is the e4m3 value nearest
+x * 2^(127 - s), ties to the even code, held within +-448.  A row with a NaN is
+all NaN: s = 255 and codes of 0x7f.
 
 The e4m3 codes themselves: sign, 4 exponent bits e (bias 7), 3 mantissa bits m:
 2^(e-7) (1 + m/8), or 2^-6 (m/8) for e = 0; 0x7f and 0xff are NaN.
@@ -43,11 +43,13 @@ def encode(x):
 def quantise(x):
     """Rows x [..., D] fp64 -> codes [..., D], scale bytes [...]."""
     x = np.asarray(x, np.float64)
+    bad = np.isnan(x).any(axis=-1)
     top = np.where(np.isnan(x), 0.0, np.abs(x)).max(axis=-1)
     s = np.ones(top.shape, np.int64)
     for b in range(1, 247):
         s = np.where(top > 448.0 * 2.0 ** (b - 127), b + 1, s)
-    return encode(x * 2.0 ** (127.0 - s[..., None])), s.astype(np.uint8)
+    codes = encode(x * 2.0 ** (127.0 - s[..., None]))
+    return np.where(bad[..., None], 0x7F, codes).astype(np.uint8), np.where(bad, 255, s).astype(np.uint8)
 
 
 def values(codes, scale):

@@ -425,16 +425,20 @@ def test_a_wait_that_runs_out_is_reported(stall_tile):
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, A)
 
 
-def test_nan_codes_reach_their_channels_alone():
-    case = _case("nan", 2, 5, 4, 1, 128, [300, 40], 16, "worked")
+def test_a_nan_row_reaches_its_sequence_and_head_alone():
+    """V rows: every row that sees the token; K rows: the same, through the weights."""
+    case = _case("nan", 3, 5, 4, 2, 128, [300, 40, 70], 16, "worked")
     pools = quantised_pools(case)
-    blk = case.block_table[0, 70 // 16]
-    pools[1][blk, 0, 70 % 16, [0, 5, 63, 64, 127]] = 0x7F, 0xFF, 0x7F, 0xFF, 0x7F
+    for b, g, t, w in ((0, 0, 70, 1), (1, 1, 3, 0)):
+        blk = case.block_table[b, t // 16]
+        pools[w][blk, g, t % 16], pools[2][blk, g, t % 16, w] = 0x7F, 255
     call, out, lse, status, _ = _raw(case, pools)
     call()
-    got = out.double().cpu().numpy()
-    bad = np.isnan(got)
-    assert bad[0][..., [0, 5, 63, 64, 127]].all() and bad.sum() == bad[0][..., [0, 5, 63, 64, 127]].size
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    nan = np.zeros(got.shape, bool)
+    nan[0, :, :2] = nan[1, :, 2:] = True
+    np.testing.assert_array_equal(np.isnan(got), nan)
+    assert np.isnan(gl[1, :, 2:]).all() and not np.isnan(gl[0]).any()
     ref, A = oracle.attention.tree_attention_case(case), _abs_v(case)
-    got[bad] = ref[0][bad]
-    check(case, got, lse.double().cpu().numpy(), ref, A)
+    got[nan], gl[1, :, 2:] = ref[0][nan], ref[1][1, :, 2:]
+    check(case, got, gl, ref, A)

@@ -27,9 +27,9 @@ def test_scale_byte(top, byte):
 
 
 def test_special_values():
-    codes, s = cache_q8.quantise(np.array([[np.nan, np.inf, -np.inf, 1.0], [np.nan, 1.0, -1.0, 0.5]]))
-    assert codes[0].tolist()[:3] == [0x7F, 0x7E, 0xFE] and s.tolist() == [247, 119]
-    assert cache_q8.values(codes[1:], s[1:])[0, 1:].tolist() == [1.0, -1.0, 0.5]
+    codes, s = cache_q8.quantise(np.array([[1.0, np.inf, -np.inf, 0.0], [np.nan, 1.0, -1.0, 0.5], [2.0, 1.0, -1.0, 0.5]]))
+    assert codes[0].tolist() == [0, 0x7E, 0xFE, 0] and codes[1].tolist() == [0x7F] * 4 and s.tolist() == [247, 255, 120]
+    assert cache_q8.values(codes[2:], s[2:]).tolist() == [[2.0, 1.0, -1.0, 0.5]]
 
 
 @pytest.mark.parametrize("interleaved", [False, True])

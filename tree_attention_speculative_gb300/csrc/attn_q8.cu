@@ -270,7 +270,7 @@ struct WideScale {
   uint32_t m1, m2;  // m1 is 0 for a row to be zeroed
   __device__ __forceinline__ WideScale(uint32_t s, bool keep) {
     const uint32_t b1 = min(s + 120u, 254u), b2 = s + 247u - b1;
-    m1 = keep ? (b1 << 7) | (b1 << 23) : 0u;
+    m1 = !keep ? 0u : s == 255u ? 0x7fff7fffu : (b1 << 7) | (b1 << 23);  // (255: a NaN row)
     m2 = (b2 << 7) | (b2 << 23);  // 1 for all but the largest rows
   }
 };
@@ -289,14 +289,13 @@ __device__ __forceinline__ uint32_t two_bytes(uint32_t w) {
 // 16 codes times the row's power of two as bf16, two 16-byte chunks.  A code's
 // sign, exponent and mantissa, put where bf16 has them, are its value times
 // 2^-120 (subnormal codes too), so a bit shuffle and a product do: exact, and
-// half the cost of going through fp16 and fp32.  Only a NaN code would come out
-// as a number; *nan collects bits 0x80808080 for those.
-__device__ __forceinline__ void widen16(const uint4& c, uint32_t m1, uint4& lo, uint4& hi, uint32_t* nan) {
+// half the cost of going through fp16 and fp32.  (A NaN code would come out as a
+// number, but rows that have any are marked by their scale byte.)
+__device__ __forceinline__ void widen16(const uint4& c, uint32_t m1, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t o[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    *nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
     // shifted so that a code's 4 + 3 bits end at bit 4
     o[2 * k] = mul_bf16x2((two_bytes<0x9180>(w[k]) << 4) & 0x87f087f0u, m1);
     o[2 * k + 1] = mul_bf16x2((two_bytes<0xb3a2>(w[k]) << 4) & 0x87f087f0u, m1);
@@ -702,13 +701,12 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             return *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4));
           };
           uint8_t* row = wide + ct * 128;
-          uint32_t nan = 0;
           uint4 x = chunk(0);
-#pragma unroll 1
+#pragma unroll 2
           for (int c = 0; c < D / 16; ++c) {
             const uint4 x_next = chunk((c + 1) & (D / 16 - 1));
             uint4 lo, hi;
-            widen16(x, ws.m1, lo, hi, &nan);
+            widen16(x, ws.m1, lo, hi);
             uint8_t* to = row + (c >> 2) * C::HALF_BYTES;
             *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ swz) << 4)) = lo;
             *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ swz) << 4)) = hi;
@@ -719,15 +717,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             for (int e = 0; e < D / 2; ++e) {
               uint32_t* w = reinterpret_cast<uint32_t*>(row + (e >> 5) * C::HALF_BYTES + (((e & 31) >> 2) << 4)) + (e & 3);
               *w = mul_bf16x2(*w, ws.m2);
-            }
-          }
-          if (inside && (nan & 0x80808080u)) {  // the row's NaN codes, one at a time
-#pragma unroll 1
-            for (int e = 0; e < D; ++e) {
-              const int c = e >> 4;
-              const uint8_t code = src[((D == 128 ? c ^ swz : c ^ ((ct >> 1) & 3)) << 4) + (e & 15)];
-              if ((code & 0x7f) == 0x7f)
-                *reinterpret_cast<uint16_t*>(row + (e >> 6) * C::HALF_BYTES + ((((e & 63) >> 3) ^ swz) << 4) + (e & 7) * 2) = 0x7fff;
             }
           }
           mbar_arrive(&sm.v_empty[slot]);
