@@ -91,14 +91,14 @@ struct Cfg {
   static constexpr int WIDE_BYTES = KV_TILE * D * 2;  // a bf16 tile, and the Q tile
   static constexpr int HALF_BYTES = KV_TILE * 128;
   // As many tiles in flight as shared memory holds; a V tile also has a widened buffer to wait in.
-  static constexpr int NSK = D == 128 ? 4 : 5;
-  static constexpr int NSV = D == 128 ? 3 : 5;
+  static constexpr int NSK = D == 128 ? 3 : 5;
+  static constexpr int NSV = D == 128 ? 4 : 5;
 };
 
 template <int D>
 struct __align__(1024) Smem {
   using C = Cfg<D>;
-  uint8_t q[C::WIDE_BYTES];  // bf16 [half][row][128 B]; then the row's 128-byte pieces hold hi and lo
+  uint8_t q[C::WIDE_BYTES];  // bf16 [half][row][128 B]; then hi and lo of a piece's 64 channels, 64 bytes each, in its place
   uint8_t k[C::NSK][SLOT];
   uint8_t v[C::NSV][SLOT];
   uint16_t v_scale[C::NSV][KV_TILE];  // with each V tile its tokens' scale bytes: K row's, V row's
@@ -183,75 +183,50 @@ struct Ctl {
   volatile int* flag;
   uint64_t limit;
 };
-// Polls a barrier some times over, two instructions a poll: with sixteen warps
-// on the SM, waits that looked at the clock and the abort flag on every poll
-// took a third of its issue slots.
-__device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n"
-      "AGAIN_%=:\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE_%=;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE_%=;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE_%=;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 p, n, 16;\n\t"
-      "@p bra AGAIN_%=;\n\t"
-      "setp.ne.u32 p, n, n;\n"
-      "DONE_%=:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
-  if (poll_bar(bar, parity)) return true;
+// Bounded waits that also give up as soon as another role has aborted.  Out of
+// line, and asleep between polls: inlined and polling at full rate they made up
+// most of the kernel's code and a third of its issue slots, and the warps at
+// work waited for instructions.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* flag, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (poll_bar(bar, parity)) return true;
-    if (*c.flag) return false;
-    if (globaltimer_ns() - t0 > c.limit) {
-      *c.flag = 1;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      __nanosleep(16);
+    }
+    if (*flag) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      *flag = 1;
       return false;
     }
   }
 }
-// The same for the loads, which run several tiles ahead: sleeps between polls.
-__device__ __forceinline__ bool wait_bar_idle(uint64_t* bar, uint32_t parity, const Ctl& c) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    __nanosleep(64);
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*c.flag) return false;
-    if (globaltimer_ns() - t0 > c.limit) {
-      *c.flag = 1;
-      return false;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
+  return mbar_try_wait(bar, parity) || wait_more(bar, parity, c.flag, c.limit);
+}
+__device__ __noinline__ bool wait_count(const int* counter, int target, volatile int* flag, uint64_t limit) {
+  const uint32_t addr = smem_u32(counter);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    if (v >= target) return true;
+    __nanosleep(20);
+    if ((i & 15) == 15) {
+      if (*flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit) {
+        *flag = 1;
+        return false;
+      }
     }
   }
 }
 __device__ __forceinline__ bool wait_count(const int* counter, int target, const Ctl& c) {
-  const uint32_t addr = smem_u32(counter);
-  uint64_t t0 = 0;
-  while (true) {
-    int v;
-    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    if (v >= target) return true;
-    if (*c.flag) return false;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > c.limit) {
-      *c.flag = 1;
-      return false;
-    }
-  }
+  return wait_count(counter, target, c.flag, c.limit);
 }
 __device__ __forceinline__ void publish(int* counter, int v) {
   asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(counter)), "r"(v) : "memory");
@@ -304,6 +279,22 @@ __device__ __forceinline__ void widen16(const uint4& c, uint32_t m1, uint4& lo, 
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// Four bf16 channels of a query times inv as e4m3: hi, and lo = what hi leaves.
+__device__ __forceinline__ void split4(uint32_t w0, uint32_t w1, float inv, uint32_t& hi, uint32_t& lo) {
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t w = k ? w1 : w0;
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+    const float2 g = make_float2(f.x * inv, f.y * inv);
+    h[k] = __nv_cvt_float2_to_fp8x2(g, __NV_SATFINITE, __NV_E4M3);
+    const float2 u = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[k], __NV_E4M3)));
+    l[k] = __nv_cvt_float2_to_fp8x2(make_float2(g.x - u.x, g.y - u.y), __NV_SATFINITE, __NV_E4M3);
+  }
+  hi = h[0] | (h[1] << 16);
+  lo = l[0] | (l[1] << 16);
+}
+
 // 8 bytes from global to shared memory, asynchronously; cp_async_arrive arrives
 // on the barrier once this thread's have landed.
 __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
@@ -317,6 +308,35 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint64_t>(p)),
                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// Scales what a row has so far by f: `chunks` of P (16 columns each), and O,
+// which must then hold every earlier PV.  Out of line: it is hardly ever run.
+template <int D>
+__device__ __noinline__ void rescale_tmem(uint32_t p_tmem, int chunks, uint32_t o_tmem, bool with_o, float f) {
+  tmem_st_wait();
+  tc_fence_after();
+#pragma unroll 1
+  for (int i = 0; i < chunks; ++i) {
+    uint32_t w[16];
+    tmem_ld16(p_tmem + i * 16, w);
+    tmem_ld_wait();
+    reg_fence16(w);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+    tmem_st16(p_tmem + i * 16, w);
+  }
+#pragma unroll 1
+  for (int d = 0; with_o && d < D; d += 32) {
+    uint32_t w[32];
+    tmem_ld32(o_tmem + d, w);
+    tmem_ld_wait();
+    reg_fence32(w);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+    tmem_st32(o_tmem + d, w);
+  }
 }
 
 template <int D>
@@ -408,7 +428,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     auto take = [&]() -> bool {
       bool r = true;
       if (issued >= nst) {
-        if (lane == 0) r = wait_bar_idle(&empty[slot], phase ^ 1, ctl);
+        if (lane == 0) r = wait_bar(&empty[slot], phase ^ 1, ctl);
         r = __shfl_sync(0xffffffffu, r, 0);
       }
       return r;
@@ -540,13 +560,12 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             kq += C::HALVES;
             if (j == I.n_tree - 1 && I.n_prefix > 0) mma_commit(&sm.q_free);
           } else {
-            // D = 128: hi in the first 128-byte pieces, lo in the second; D = 64: hi and lo share a piece
+            // 32 channels a step: those of piece h, hi and then lo
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              const bool low = i >= D / 32;
-              const int ks = low ? i - D / 32 : i;  // 32 channels a step
-              const uint32_t qa = q_addr + (D == 128 ? (low ? ROW_TILE * 128 : 0) + ks * 32 : i * 32);
-              const uint64_t kd = D == 128 ? smem_desc_sw128(k0 + ks * 32, 16, 1024) : smem_desc_sw64(k0 + ks * 32, 16, 512);
+              const int h = i >> 2, low = (i >> 1) & 1, step = i & 1;
+              const uint32_t qa = q_addr + h * (ROW_TILE * 128) + low * 64 + step * 32;
+              const uint64_t kd = D == 128 ? smem_desc_sw128(k0 + h * 64 + step * 32, 16, 1024) : smem_desc_sw64(k0 + step * 32, 16, 512);
               mma_ss_f8(d_tmem, smem_desc_sw128(qa, 16, 1024), kd, ID_E4M3, i > 0);
             }
             mma_commit(&sm.s_full[jg % NSB]);
@@ -610,73 +629,58 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         // (q_free comes once a segment with prefix tiles, in step with q8_full;
         // q_full also for the others, but none can follow before q8_full)
         if (!(ok = wait_bar(&sm.q_free, q8 & 1, ctl) && wait_bar(&sm.q_full, qn & 1, ctl))) break;
-        uint4 x[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          x[c] = *reinterpret_cast<const uint4*>(sm.q + (c >> 3) * (ROW_TILE * 128) + ct * 128 + (((c & 7) ^ swz) << 4));
         uint32_t m = 0;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 8; ++c) {
-          m = q8_max2(m, q8_max2(q8_max2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu),
-                                 q8_max2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
+          const uint4 y = *reinterpret_cast<const uint4*>(sm.q + (c >> 3) * (ROW_TILE * 128) + ct * 128 + ((c & 7) << 4));
+          m = q8_max2(m, q8_max2(q8_max2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), q8_max2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
         }
         m = q8_max2(m, m >> 16) & 0xffffu;
         const int s = q8_scale_byte(m);
         const float inv = pow2_of(254 - s);
         // an infinite query has no finite logits
         row_scale = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
+#pragma unroll 1
+        for (int h = 0; h < C::HALVES; ++h) {
+          uint8_t* piece = sm.q + h * (ROW_TILE * 128) + ct * 128;
+          uint4 x[8];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {  // 16 channels: a 16-byte chunk of hi and one of lo
-          uint32_t hi[4], lo[4];
+          for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const uint4*>(piece + ((c ^ swz) << 4));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4& y = x[2 * c + (e >> 1)];
-            const uint32_t w0 = (e & 1) ? y.z : y.x, w1 = (e & 1) ? y.w : y.y;
-            const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w0));
-            const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w1));
-            const float2 g0 = make_float2(f0.x * inv, f0.y * inv), g1 = make_float2(f1.x * inv, f1.y * inv);
-            const uint32_t h0 = __nv_cvt_float2_to_fp8x2(g0, __NV_SATFINITE, __NV_E4M3);
-            const uint32_t h1 = __nv_cvt_float2_to_fp8x2(g1, __NV_SATFINITE, __NV_E4M3);
-            const float2 u0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h0, __NV_E4M3)));
-            const float2 u1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h1, __NV_E4M3)));
-            const uint32_t l0 = __nv_cvt_float2_to_fp8x2(make_float2(g0.x - u0.x, g0.y - u0.y), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t l1 = __nv_cvt_float2_to_fp8x2(make_float2(g1.x - u1.x, g1.y - u1.y), __NV_SATFINITE, __NV_E4M3);
-            hi[e] = h0 | (h1 << 16);
-            lo[e] = l0 | (l1 << 16);
+          for (int c = 0; c < 4; ++c) {  // 16 channels: a 16-byte chunk of hi and one of lo
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4& y = x[2 * c + (e >> 1)];
+              split4((e & 1) ? y.z : y.x, (e & 1) ? y.w : y.y, inv, hi[e], lo[e]);
+            }
+            *reinterpret_cast<uint4*>(piece + ((c ^ swz) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(piece + (((c + 4) ^ swz) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          uint8_t* hrow = sm.q + ct * 128;
-          uint8_t* lrow = D == 128 ? hrow + ROW_TILE * 128 : hrow;
-          const int lc = D == 128 ? c : c + D / 16;
-          *reinterpret_cast<uint4*>(hrow + ((c ^ swz) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(lrow + ((lc ^ swz) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async();
         mbar_arrive(&sm.q8_full);
         ++q8;
       }
       ++qn;
-      // Hands tile jt's scales (the tree's: 1) to the softmax; p: its prefix tile, at ring position vq + ahead.
-      auto hand_scales = [&](int jt, bool tree, int p, int ahead) -> bool {
-        float key = 1.f, rs = a.scale_log2;
-        if (!tree) {
-          const int slot = (vq + ahead) % C::NSV;
-          if (!wait_bar(&sm.v_full[slot], ((vq + ahead) / C::NSV) & 1, ctl)) return false;
-          key = (I.t_begin + p) * KV_TILE + ct < I.P ? pow2_of(sm.v_scale[slot][ct] & 0xff) : 0.f;
-          rs = row_scale;
+      for (int j = -1; j < I.n_tiles; ++j) {
+        // The scales of tile j + 1 (the tree's: 1) go to the softmax, ahead of the values of tile j.
+        if (j + 1 < I.n_tiles) {
+          const int jt = j < 0 ? jg : jg + 1, p = j + 1 - I.n_tree, vt = vq + (j >= I.n_tree ? 1 : 0);
+          float key = 1.f, rs = a.scale_log2;
+          if (p >= 0) {
+            if (!(ok = wait_bar(&sm.v_full[vt % C::NSV], (vt / C::NSV) & 1, ctl))) break;
+            key = (I.t_begin + p) * KV_TILE + ct < I.P ? pow2_of(sm.v_scale[vt % C::NSV][ct] & 0xff) : 0.f;
+            rs = row_scale;
+          }
+          if (jt >= NT && !(ok = wait_bar(&sm.t_empty[jt % NT], ((jt / NT) - 1) & 1, ctl))) break;
+          sm.key_scale[jt % NT][ct] = key;
+          sm.row_scale[jt % NT][ct] = rs;
+          mbar_arrive(&sm.t_full[jt % NT]);
         }
-        if (jt >= NT && !wait_bar(&sm.t_empty[jt % NT], ((jt / NT) - 1) & 1, ctl)) return false;
-        sm.key_scale[jt % NT][ct] = key;
-        sm.row_scale[jt % NT][ct] = rs;
-        mbar_arrive(&sm.t_full[jt % NT]);
-        return true;
-      };
-      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+        if (j < 0) continue;
         const bool tree = j < I.n_tree;
         const int p = j - I.n_tree;
-        // scales go out a tile ahead of the values
-        if (tree || p == 0) ok = hand_scales(jg, tree, p, 0);
-        if (ok && !tree && p + 1 < I.n_prefix) ok = hand_scales(jg + 1, false, p + 1, 1);
-        if (!ok) break;
         const bool inside = !tree && (I.t_begin + p) * KV_TILE + ct < I.P;
         const int buf = jg % NVB;
         if (jg >= NVB && !(ok = wait_bar(&sm.vb_empty[buf], ((jg / NVB) - 1) & 1, ctl))) break;
@@ -724,6 +728,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           fence_proxy_async();
         }
         mbar_arrive(&sm.vb_full[buf]);
+        ++jg;
       }
     }
   } else {
@@ -837,34 +842,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
               const float f = !move ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - mx));
               if (move) m_run = mx;
               l_run *= f;
-              if (c > 0) {  // this tile's P so far
-                tmem_st_wait();
-#pragma unroll 1
-                for (int i = 0; i < c; ++i) {
-                  uint32_t w[16];
-                  tmem_ld16(s_tmem + i * 16, w);
-                  tmem_ld_wait();
-                  reg_fence16(w);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-                  tmem_st16(s_tmem + i * 16, w);
-                }
-              }
-              if (j > 0) {  // O, which must hold every earlier PV
-                if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) return false;
-                tc_fence_after();
-#pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                  uint32_t w[32];
-                  tmem_ld32(o_tmem + d, w);
-                  tmem_ld_wait();
-                  reg_fence32(w);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-                  tmem_st32(o_tmem + d, w);
-                }
-              }
+              if (j > 0 && !__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) return false;
+              rescale_tmem<D>(s_tmem, c, o_tmem, j > 0, f);
             }
             l_run += sum;
             tmem_st16(s_tmem + c * 16, pk);
