@@ -345,37 +345,58 @@ def tree_verify_greedy_noalloc(draft_tokens, target_logits, parent_idx, max_dept
 #
 # These calls read tensors whose type and strides the C side cannot see (a bf16
 # pool given as the 8-bit one would be read past its rows), so each tensor's
-# type, shape, density and device are checked here first.
+# type, shape, density and device are checked here first.  A small call's time
+# is this marshalling, so pointers go over as plain integers and the current
+# stream is asked for by its handle.
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _need(ok: bool, where: str):
-    if not ok:
-        raise TreeSpecError(-2, where)  # TS_ERR_SHAPE
+_BF16, _I32, _U8, _F8 = torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
-def _dense(where: str, t: torch.Tensor, shape, *dtypes):
-    _need(t.dtype in dtypes and tuple(t.shape) == tuple(shape) and t.is_contiguous(), where)
+def _bad(where: str):
+    raise TreeSpecError(-2, where)  # TS_ERR_SHAPE
 
 
-def _same_device(where: str, *tensors):
-    """Every tensor on the current CUDA device, whose stream the call uses."""
-    _need(all(t is None or t.is_cuda for t in tensors), where)
-    here = torch.cuda.current_device()
-    _need(all(t is None or t.get_device() == here for t in tensors), where)
+def _is(t: torch.Tensor, dtype, shape: tuple) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _is_codes(t: torch.Tensor, shape: tuple) -> bool:
+    return (t.dtype is _F8 or t.dtype is _U8) and t.shape == shape and t.is_contiguous()
+
+
+def _launch_stream(where: str, stream, *tensors) -> int:
+    """The stream's handle, once every tensor is on the current CUDA device."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            _bad(where)
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _bad(where)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _opt(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _token_heads(where: str, x: torch.Tensor, out: torch.Tensor, B: int, N: int):
     """Strides (token, head) of bf16 x [B, N, H, D], whose tokens are evenly
-    spaced, for the dense out of the same shape."""
-    _need(x.dim() == 4 and x.dtype == torch.bfloat16 and x.shape[:2] == (B, N), where)
-    _dense(where, out, x.shape, torch.bfloat16)
+    spaced, for the dense out of the same shape; 0, 0 when x is dense."""
+    shape = x.shape
+    if x.dtype is not _BF16 or len(shape) != 4 or shape[0] != B or shape[1] != N or out is None \
+            or not _is(out, _BF16, shape):
+        _bad(where)
+    if x.is_contiguous():
+        return 0, 0
     sb, st, sh, sd = x.stride()
-    _need((sd == 1 or x.shape[3] == 1) and (B == 1 or N == 1 or sb == N * st), where)
-    H, D = x.shape[2], x.shape[3]
+    if sd != 1 or not (B == 1 or N == 1 or sb == N * st):
+        _bad(where)
+    H, D = shape[2], shape[3]
     if N == 1:
-        st = sb if B > 1 else H * sh
+        st = sb
     return max(st, (H - 1) * sh + D) if B * N == 1 else st, D if H == 1 else sh
 
 
@@ -384,30 +405,25 @@ def tree_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.T
     """Rotate q [B,N,Hq,D] and k [B,N,Hkv,D] bf16 at pos [B,N] i32 into the dense
     q_out and k_out.  q and k may be views of a fused projection (evenly spaced
     tokens, adjacent channels) or the outputs themselves; either may be None."""
+    where = "tree_rope"
     B, N = pos.shape
-    _dense("tree_rope", pos, (B, N), torch.int32)
-    p = RopeParams(pos=pos.data_ptr(), B=B, N=N, rotary_dim=rope.rotary_dim, interleaved=int(rope.interleaved),
-                   scaling=ROPE_SCALING.get(rope.scaling, -1), theta=rope.theta, factor=rope.factor,
-                   low_rot=rope.low_rot, high_rot=rope.high_rot, orig_len=rope.orig_len, mscale=rope.mscale)
+    if pos.dtype is not _I32 or not pos.is_contiguous():
+        _bad(where)
+    qt = qh = kt = kh = Hq = Hkv = D = 0
     if q is not None:
-        _need(q_out is not None, "tree_rope")
-        p.q_token_stride, p.q_head_stride = _token_heads("tree_rope", q, q_out, B, N)
-        p.q, p.q_out, p.Hq, p.D = q.data_ptr(), q_out.data_ptr(), q.shape[2], q.shape[3]
+        qt, qh = _token_heads(where, q, q_out, B, N)
+        Hq, D = q.shape[2], q.shape[3]
     if k is not None:
-        _need(k_out is not None and (q is None or k.shape[3] == q.shape[3]), "tree_rope")
-        p.k_token_stride, p.k_head_stride = _token_heads("tree_rope", k, k_out, B, N)
-        p.k, p.k_out, p.Hkv, p.D = k.data_ptr(), k_out.data_ptr(), k.shape[2], k.shape[3]
-    _same_device("tree_rope", q, k, pos, q_out, k_out)
-    _check(lib().tree_rope(ctypes.byref(p), _s(stream)), "tree_rope")
-
-
-def _q8_pools(where: str, k_cache, v_cache, kv_scale, block_table, B: int, Hkv: int, D: int):
-    nblk, _, bs, _ = k_cache.shape
-    _dense(where, k_cache, (nblk, Hkv, bs, D), *_CODES)
-    _dense(where, v_cache, (nblk, Hkv, bs, D), *_CODES)
-    _dense(where, kv_scale, (nblk, Hkv, bs, 2), torch.uint8)
-    _dense(where, block_table, (B, block_table.shape[1]), torch.int32)
-    return nblk, bs, block_table.shape[1]
+        kt, kh = _token_heads(where, k, k_out, B, N)
+        Hkv = k.shape[2]
+        if q is not None and k.shape[3] != D:
+            _bad(where)
+        D = k.shape[3]
+    handle = _launch_stream(where, stream, q, k, pos, q_out, k_out)
+    p = RopeParams(_opt(q), _opt(k), _opt(q_out), _opt(k_out), pos.data_ptr(), qt, qh, kt, kh, B, N, Hq, Hkv, D,
+                   rope.rotary_dim, rope.interleaved, ROPE_SCALING.get(rope.scaling, -1), rope.theta, rope.factor,
+                   rope.low_rot, rope.high_rot, rope.orig_len, rope.mscale)
+    _check(lib().tree_rope(ctypes.byref(p), handle), where)
 
 
 def tree_cache_append_q8(k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, block_table, new_prefix_len, status=None,
@@ -418,19 +434,22 @@ def tree_cache_append_q8(k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, b
     where = "tree_cache_append_q8"
     T, Hkv, D = k.shape
     B = prefix_len.shape[0]
-    nblk, bs, maxb = _q8_pools(where, k_cache, v_cache, kv_scale, block_table, B, Hkv, D)
-    for x in (k, v):
-        _need(x.dtype == torch.bfloat16 and x.shape == (T, Hkv, D) and x.stride()[2] == 1
-              and (Hkv == 1 or x.stride()[1] == D), where)
-    _dense(where, cu_len, (B + 1,), torch.int32)
-    for x in (prefix_len, new_prefix_len, status):
-        if x is not None:
-            _dense(where, x, (B,), torch.int32)
-    _same_device(where, k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, block_table, new_prefix_len, status)
-    ks, vs = (x.stride()[0] if T > 1 else 0 for x in (k, v))
-    _check(lib().tree_cache_append_q8(_p(k), _p(v), _p(cu_len), _p(prefix_len), _p(k_cache), _p(v_cache),
-                                      _p(kv_scale), _p(block_table), B, T, Hkv, D, ks, vs, bs, nblk, maxb,
-                                      _p(new_prefix_len), _p(status), _s(stream)), where)
+    nblk, bs, maxb = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+    pool = (nblk, Hkv, bs, D)
+    ks, vs = k.stride(), v.stride()
+    if not (k.dtype is _BF16 and v.dtype is _BF16 and v.shape == k.shape and ks[2] == 1 and vs[2] == 1
+            and (Hkv == 1 or (ks[1] == D and vs[1] == D))
+            and _is_codes(k_cache, pool) and _is_codes(v_cache, pool) and _is(kv_scale, _U8, (nblk, Hkv, bs, 2))
+            and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,)) and _is(prefix_len, _I32, (B,))
+            and _is(new_prefix_len, _I32, (B,)) and (status is None or _is(status, _I32, (B,)))):
+        _bad(where)
+    handle = _launch_stream(where, stream, k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, block_table,
+                            new_prefix_len, status)
+    _check(lib().tree_cache_append_q8(k.data_ptr(), v.data_ptr(), cu_len.data_ptr(), prefix_len.data_ptr(),
+                                      k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(),
+                                      block_table.data_ptr(), B, T, Hkv, D, ks[0] if T > 1 else 0,
+                                      vs[0] if T > 1 else 0, bs, nblk, maxb, new_prefix_len.data_ptr(), _opt(status),
+                                      handle), where)
 
 
 def tree_commit_accepted_q8(k_tree, v_tree, accepted, accept_len, prefix_len, k_cache, v_cache, kv_scale, block_table,
@@ -439,37 +458,43 @@ def tree_commit_accepted_q8(k_tree, v_tree, accepted, accept_len, prefix_len, k_
     .. n*) of every sequence is quantised as it is appended."""
     where = "tree_commit_accepted_q8"
     B, N, Hkv, D = k_tree.shape
-    nblk, bs, maxb = _q8_pools(where, k_cache, v_cache, kv_scale, block_table, B, Hkv, D)
-    _dense(where, k_tree, (B, N, Hkv, D), torch.bfloat16)
-    _dense(where, v_tree, (B, N, Hkv, D), torch.bfloat16)
-    _dense(where, accepted, (B, accepted.shape[1]), torch.int32)
-    for x in (accept_len, prefix_len, new_prefix_len, status):
-        if x is not None:
-            _dense(where, x, (B,), torch.int32)
-    _same_device(where, k_tree, v_tree, accepted, accept_len, prefix_len, k_cache, v_cache, kv_scale, block_table,
-                 new_prefix_len, status)
-    _check(lib().tree_commit_accepted_q8(_p(k_tree), _p(v_tree), _p(accepted), _p(accept_len), _p(prefix_len),
-                                         _p(k_cache), _p(v_cache), _p(kv_scale), _p(block_table), B, N, Hkv, D, bs,
-                                         nblk, maxb, accepted.shape[1] - 1, _p(new_prefix_len), _p(status),
-                                         _s(stream)), where)
+    nblk, bs, maxb = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+    pool, steps = (nblk, Hkv, bs, D), accepted.shape[1]
+    if not (_is(k_tree, _BF16, (B, N, Hkv, D)) and _is(v_tree, _BF16, (B, N, Hkv, D)) and _is_codes(k_cache, pool)
+            and _is_codes(v_cache, pool) and _is(kv_scale, _U8, (nblk, Hkv, bs, 2))
+            and _is(block_table, _I32, (B, maxb)) and _is(accepted, _I32, (B, steps)) and _is(accept_len, _I32, (B,))
+            and _is(prefix_len, _I32, (B,)) and _is(new_prefix_len, _I32, (B,))
+            and (status is None or _is(status, _I32, (B,)))):
+        _bad(where)
+    handle = _launch_stream(where, stream, k_tree, v_tree, accepted, accept_len, prefix_len, k_cache, v_cache,
+                            kv_scale, block_table, new_prefix_len, status)
+    _check(lib().tree_commit_accepted_q8(k_tree.data_ptr(), v_tree.data_ptr(), accepted.data_ptr(),
+                                         accept_len.data_ptr(), prefix_len.data_ptr(), k_cache.data_ptr(),
+                                         v_cache.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(), B, N, Hkv,
+                                         D, bs, nblk, maxb, steps - 1, new_prefix_len.data_ptr(), _opt(status),
+                                         handle), where)
 
 
 def tree_attn_q8_workspace_size(params: AttnParams) -> int:
     return int(lib().tree_attn_q8_workspace_size(ctypes.byref(params)))
 
 
-def _check_attn_q8(where: str, params: AttnParams, kv_scale, workspace):
-    _need(all(t in _CODES for t in params.cache_dtypes), where)
-    _dense(where, kv_scale, (params.num_blocks, params.Hkv, params.block_size, 2), torch.uint8)
-    _same_device(where, kv_scale, workspace)
+def _attn_q8_stream(where: str, params: AttnParams, kv_scale, workspace, stream) -> int:
+    for t in params.cache_dtypes:
+        if t is not _F8 and t is not _U8:
+            _bad(where)
+    if not _is(kv_scale, _U8, (params.num_blocks, params.Hkv, params.block_size, 2)):
+        _bad(where)
+    return _launch_stream(where, stream, kv_scale, workspace)
 
 
 def tree_attn_fwd_q8(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """tree_attn_fwd over the 8-bit cache: ``params`` from attn_params with the
     e4m3 pools as k_cache and v_cache, ``kv_scale`` [num_blocks,Hkv,bs,2] uint8."""
-    _check_attn_q8("tree_attn_fwd_q8", params, kv_scale, workspace)
-    _check(lib().tree_attn_fwd_q8(ctypes.byref(params), _p(kv_scale), _p(workspace),
-                                  workspace.numel() * workspace.element_size(), _s(stream)), "tree_attn_fwd_q8")
+    where = "tree_attn_fwd_q8"
+    handle = _attn_q8_stream(where, params, kv_scale, workspace, stream)
+    _check(lib().tree_attn_fwd_q8(ctypes.byref(params), kv_scale.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), handle), where)
 
 
 def tree_attn_fwd_q8_stall_test(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stall_seq: int,
@@ -477,7 +502,7 @@ def tree_attn_fwd_q8_stall_test(params: AttnParams, kv_scale: torch.Tensor, work
     """Testing only: tree_attn_fwd_q8 with sequence ``stall_seq``'s key stream
     stopped before tile ``stall_tile`` of its segments, so a bounded wait runs out."""
     where = "tree_attn_fwd_q8_stall_test"
-    _check_attn_q8(where, params, kv_scale, workspace)
-    _check(lib().tree_attn_fwd_q8_stall_test(ctypes.byref(params), _p(kv_scale), _p(workspace),
+    handle = _attn_q8_stream(where, params, kv_scale, workspace, stream)
+    _check(lib().tree_attn_fwd_q8_stall_test(ctypes.byref(params), kv_scale.data_ptr(), workspace.data_ptr(),
                                              workspace.numel() * workspace.element_size(), stall_seq, stall_tile,
-                                             wait_limit_us, _s(stream)), where)
+                                             wait_limit_us, handle), where)

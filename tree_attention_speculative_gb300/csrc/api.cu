@@ -528,6 +528,31 @@ double rope_frequency(const ts_rope_params& p, int R, int i) {
   return g * f + (1.0 - g) * f / p.factor;
 }
 
+// The fraction of a turn a position adds to each pair, times 2^64 (whole turns
+// change nothing).  A thread's last table is kept with the configuration it is
+// of: it takes as long as the launch, and a model asks for one again and again.
+bool rope_turns(const ts_rope_params& p, int R, uint64_t* turn) {
+  struct Table {
+    double theta, factor, low, high;
+    int R, scaling, orig;
+    bool ok;
+    uint64_t turn[64];
+  };
+  static thread_local Table last{};
+  if (!(last.R == R && last.theta == p.theta && last.scaling == p.scaling && last.factor == p.factor &&
+        last.low == p.low_rot && last.high == p.high_rot && last.orig == p.orig_len)) {
+    last = Table{p.theta, p.factor, p.low_rot, p.high_rot, R, p.scaling, p.orig_len, true, {}};
+    for (int i = 0; i < R / 2; ++i) {
+      const double t = rope_frequency(p, R, i) / (2.0 * 3.14159265358979323846);
+      const double frac = t - std::floor(t);
+      last.ok = last.ok && std::isfinite(t);
+      last.turn[i] = std::isfinite(t) && frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0;
+    }
+  }
+  std::memcpy(turn, last.turn, sizeof(last.turn));
+  return last.ok;
+}
+
 bool positive(double x) { return x > 0.0 && std::isfinite(x); }
 
 ts_status check_attn_q8(const ts_attn_params* p) {
@@ -622,13 +647,7 @@ ts_status tree_rope(const ts_rope_params* p, ts_stream stream) {
       return TS_ERR_SHAPE;
   }
   if (overlap(out[0], out[1])) return TS_ERR_SHAPE;
-  for (int i = 0; i < R / 2; ++i) {
-    // the fraction of a turn a position adds; whole turns change nothing
-    const double turn = rope_frequency(*p, R, i) / (2.0 * 3.14159265358979323846);
-    if (!std::isfinite(turn)) return TS_ERR_SHAPE;
-    const double frac = turn - std::floor(turn);
-    a.turn[i] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0;
-  }
+  if (!rope_turns(*p, R, a.turn)) return TS_ERR_SHAPE;
   return launch_rope(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
 }
 
