@@ -23,7 +23,7 @@
 namespace ts {
 namespace {
 
-constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_THREADS = 256;  // at most: a CTA has as many as leave no part of a round idle
 constexpr int ROPE_MAX_TOK = 16;  // tokens a CTA: the table then holds 16 x 64 pairs, 8 KB
 
 __device__ __forceinline__ float2 rope_sincos(int32_t pos, uint64_t turn, float mscale) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ RopeRow rope_row(const RopeArgs& a, int t, int h) {
 // Tables of cos, sin of the CTA's tokens: pair i of token k at [k * half + i].
 __device__ __forceinline__ void rope_table(const RopeArgs& a, float2* table, int t0, int ntok) {
   const int half = a.R / 2;
-  for (int e = threadIdx.x; e < ntok * half; e += ROPE_THREADS) {
+  for (int e = threadIdx.x; e < ntok * half; e += blockDim.x) {
     const int k = e / half;
     table[e] = rope_sincos(a.pos[t0 + k], a.turn[e - k * half], a.mscale);
   }
@@ -83,7 +83,7 @@ k_rope_vec(const __grid_constant__ RopeArgs a, FastDiv heads) {
   const int ntok = min(a.tok, a.tokens - t0);
   const int lg = a.D == 128 ? 3 : 2;  // items a head: D / 16
   const int n = (ntok * heads.d) << lg;
-  const int rot = a.R / 16, half = a.R / 2;
+  const int rot = a.R / 16, half = a.R / 2, threads = blockDim.x;
   pdl_wait();
   pdl_trigger();
   constexpr int UN = 2;  // items in flight a thread
@@ -107,7 +107,7 @@ k_rope_vec(const __grid_constant__ RopeArgs a, FastDiv heads) {
   const auto load = [&](int e0) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int e = e0 + u * ROPE_THREADS;
+      const int e = e0 + u * threads;
       if (e < n) {
         RopeRow r;
         int k, i, cx, cy;
@@ -120,11 +120,11 @@ k_rope_vec(const __grid_constant__ RopeArgs a, FastDiv heads) {
   load(threadIdx.x);
   rope_table(a, table, t0, ntok);
   __syncthreads();
-  for (int e0 = threadIdx.x; e0 < n; e0 += UN * ROPE_THREADS) {
+  for (int e0 = threadIdx.x; e0 < n; e0 += UN * threads) {
     if (e0 != (int)threadIdx.x) load(e0);
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int e = e0 + u * ROPE_THREADS;
+      const int e = e0 + u * threads;
       if (e >= n) break;
       RopeRow r;
       int k, i, cx, cy;
@@ -173,7 +173,7 @@ k_rope_pairs(const __grid_constant__ RopeArgs a, FastDiv heads) {
   pdl_trigger();
   rope_table(a, table, t0, ntok);
   __syncthreads();
-  for (int e = threadIdx.x; e < n; e += ROPE_THREADS) {
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
     const int row = e >> lg;
     const int k = heads.div(row);
     const RopeRow r = rope_row(a, t0 + k, row - k * heads.d);
@@ -204,10 +204,15 @@ cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   if (tok > spread) tok = spread;
   a.tok = tok < ROPE_MAX_TOK ? tok : ROPE_MAX_TOK;
   const dim3 grid(ceil_div(a.tokens, a.tok));
+  // Threads: the items of a CTA in whole rounds (576 items of 72 heads of 128:
+  // 192 threads, 28.1 us for 4096 tokens, 5.4 TB/s; 256 threads, 31.0 us).
+  const int items = a.tok * heads * per;
+  const int rounds = ceil_div(items, ROPE_THREADS);
+  const dim3 block(32 * ceil_div(ceil_div(items, rounds), 32));
   const FastDiv fd = FastDiv::make(heads);
-  if (!vec) return launch_pdl(k_rope_pairs, grid, dim3(ROPE_THREADS), 0, s, a, fd);
-  return a.interleaved ? launch_pdl(k_rope_vec<true>, grid, dim3(ROPE_THREADS), 0, s, a, fd)
-                       : launch_pdl(k_rope_vec<false>, grid, dim3(ROPE_THREADS), 0, s, a, fd);
+  if (!vec) return launch_pdl(k_rope_pairs, grid, block, 0, s, a, fd);
+  return a.interleaved ? launch_pdl(k_rope_vec<true>, grid, block, 0, s, a, fd)
+                       : launch_pdl(k_rope_vec<false>, grid, block, 0, s, a, fd);
 }
 
 }  // namespace ts
