@@ -624,15 +624,15 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];  // on its way while this one runs
       if (I.n_tiles == 0) continue;
       float row_scale = 0.f;
-      if (I.n_prefix > 0) {
-        // the Q tile, row ct: scaled to within 448, hi and lo in place
-        // (q_free comes once a segment with prefix tiles, in step with q8_full;
-        // q_full also for the others, but none can follow before q8_full)
-        if (!(ok = wait_bar(&sm.q_free, q8 & 1, ctl) && wait_bar(&sm.q_full, qn & 1, ctl))) break;
+      // The Q tile, row ct: scaled to within 448, hi and lo in place.  (q_free
+      // comes once a segment with prefix tiles, in step with q8_full; q_full also
+      // for the others, but none can follow before q8_full.)
+      auto split_q = [&]() -> bool {
+        if (!(wait_bar(&sm.q_free, q8 & 1, ctl) && wait_bar(&sm.q_full, qn & 1, ctl))) return false;
         uint32_t m = 0;
 #pragma unroll 1
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 y = *reinterpret_cast<const uint4*>(sm.q + (c >> 3) * (ROW_TILE * 128) + ct * 128 + ((c & 7) << 4));
+          const uint4 y = *reinterpret_cast<const uint4*>(sm.q + (c >> 3) * (ROW_TILE * 128) + ct * 128 + (((c & 7) ^ swz) << 4));
           m = q8_max2(m, q8_max2(q8_max2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), q8_max2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
         }
         m = q8_max2(m, m >> 16) & 0xffffu;
@@ -661,13 +661,28 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         fence_proxy_async();
         mbar_arrive(&sm.q8_full);
         ++q8;
-      }
-      ++qn;
+        return true;
+      };
       for (int j = -1; j < I.n_tiles; ++j) {
+        const bool tree = j >= 0 && j < I.n_tree;
+        const int buf = jg % NVB;
+        uint8_t* wide = sm.vb[buf];
+        if (j >= 0 && jg >= NVB && !(ok = wait_bar(&sm.vb_empty[buf], ((jg / NVB) - 1) & 1, ctl))) break;
+        if (tree) {
+          if (ct == 0) {
+            mbar_arrive_expect_tx(&sm.vt_full[buf], C::WIDE_BYTES);
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_4d(wide + h * C::HALF_BYTES, &tm_vt, &sm.vt_full[buf], 64 * h, I.g, j * KV_TILE, I.b);
+            if (buf) ++vt_issued[1];
+            else ++vt_issued[0];
+          }
+          mbar_arrive(&sm.vb_full[buf]);
+        }
         // The scales of tile j + 1 (the tree's: 1) go to the softmax, ahead of the values of tile j.
         if (j + 1 < I.n_tiles) {
           const int jt = j < 0 ? jg : jg + 1, p = j + 1 - I.n_tree, vt = vq + (j >= I.n_tree ? 1 : 0);
           float key = 1.f, rs = a.scale_log2;
+          if (p == 0 && !(ok = split_q())) break;
           if (p >= 0) {
             if (!(ok = wait_bar(&sm.v_full[vt % C::NSV], (vt / C::NSV) & 1, ctl))) break;
             key = (I.t_begin + p) * KV_TILE + ct < I.P ? pow2_of(sm.v_scale[vt % C::NSV][ct] & 0xff) : 0.f;
@@ -678,22 +693,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           sm.row_scale[jt % NT][ct] = rs;
           mbar_arrive(&sm.t_full[jt % NT]);
         }
-        if (j < 0) continue;
-        const bool tree = j < I.n_tree;
-        const int p = j - I.n_tree;
-        const bool inside = !tree && (I.t_begin + p) * KV_TILE + ct < I.P;
-        const int buf = jg % NVB;
-        if (jg >= NVB && !(ok = wait_bar(&sm.vb_empty[buf], ((jg / NVB) - 1) & 1, ctl))) break;
-        uint8_t* wide = sm.vb[buf];
-        if (tree) {
-          if (ct == 0) {
-            mbar_arrive_expect_tx(&sm.vt_full[buf], C::WIDE_BYTES);
-            for (int h = 0; h < C::HALVES; ++h)
-              tma_load_4d(wide + h * C::HALF_BYTES, &tm_vt, &sm.vt_full[buf], 64 * h, I.g, j * KV_TILE, I.b);
-            if (buf) ++vt_issued[1];
-            else ++vt_issued[0];
-          }
-        } else {
+        if (j >= 0 && !tree) {
+          const bool inside = (I.t_begin + j - I.n_tree) * KV_TILE + ct < I.P;
           const int slot = vq % C::NSV;
           const uint8_t* src = sm.v[slot] + ct * D;
           const uint32_t sc = sm.v_scale[slot][ct];
@@ -726,10 +727,11 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           mbar_arrive(&sm.v_empty[slot]);
           ++vq;
           fence_proxy_async();
+          mbar_arrive(&sm.vb_full[buf]);
         }
-        mbar_arrive(&sm.vb_full[buf]);
-        ++jg;
+        if (j >= 0) ++jg;
       }
+      ++qn;
     }
   } else {
     // ------------------------------------------------------------ softmax
