@@ -115,3 +115,30 @@ def test_rope_many_tokens_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(qo, want)
+
+
+def test_step_positions_and_commits_on_the_bf16_cache():
+    """TreeVerifyStep with a rope configuration is tree_rope, then the step without one; commit
+    appends the rotated keys."""
+    import tree_attention_speculative_gb300 as ts
+    from tests.gpu_util import to_dev
+    from tree_attention_speculative_gb300.step import TreeVerifyStep
+    cfg = ts.RopeConfig(interleaved=True, rotary_dim=64)
+    parent = np.stack([W.tree_from_widths([4, 3, 2, 1, 1])] * 2)
+    case = W.build_case("roped", 3, parent, [40, 300], Hq=8, Hkv=2, D=128, bs=16, permute=True, vocab=300, plant_len=[2, 4],
+                        spare_tokens=6)
+    t = to_dev(case)
+    pools = t["k_cache"].clone(), t["v_cache"].clone()
+    a = TreeVerifyStep(2, 26, 8, 2, 128, case.prefix_len, vocab=300, max_depth=5, rope=cfg)
+    a.run(t["parent"], t["prefix_len"], t["q"], *pools, t["block_table"], t["k_tree"], t["v_tree"], t["draft"], t["logits"])
+    q, k = torch.empty_like(t["q"]), torch.empty_like(t["k_tree"])
+    ts.tree_rope(t["q"], t["k_tree"], a.pos, q, k, cfg)
+    b = TreeVerifyStep(2, 26, 8, 2, 128, case.prefix_len, vocab=300, max_depth=5)
+    b.run(t["parent"], t["prefix_len"], q, *pools, t["block_table"], k, t["v_tree"], t["draft"], t["logits"])
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse) and torch.equal(a.accepted, b.accepted)
+    other = pools[0].clone(), pools[1].clone()
+    new, want = torch.empty_like(t["prefix_len"]), torch.empty_like(t["prefix_len"])
+    a.commit(t["k_tree"], t["v_tree"], t["prefix_len"], *pools, t["block_table"], new)
+    ts.tree_commit_accepted(k, t["v_tree"], b.accepted, b.accept_len, t["prefix_len"], *other, t["block_table"], want)
+    assert torch.equal(pools[0], other[0]) and torch.equal(pools[1], other[1]) and torch.equal(new, want)
+    assert new.cpu().tolist() == [43, 305]

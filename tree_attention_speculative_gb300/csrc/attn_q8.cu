@@ -14,12 +14,21 @@
 // its rate) and the keys need no conversion; the key's power of two and the
 // row's multiply the logits in fp32.
 // Values are widened to bf16, which holds code * 2^e exactly (a 4-bit
-// significand), so P V is the bf16 product of the bf16 kernel.
+// significand), so P V is the bf16 product of the bf16 kernel.  (e4m3 weights
+// for an 8-bit P V would need two terms as well, and lose every weight below
+// 2^-18 of the row's largest.)
 //
-// Bytes: 2 D + 2 a token and KV head, half of bf16.  At 128 rows a tile a tile
-// is 32.5 KB, 0.73 us of one SM's share of HBM, about what its products (1024
-// MMA cycles) and its exponentials take: up to 128 rows a unit the kernel is
-// bound by HBM and softmax alike, beyond that by the products and the softmax.
+// What bounds it.  Bytes: 2 D + 2 a token and KV head, half of bf16: a 128-token
+// tile is 32.5 KB, 0.73 us of one SM's share of HBM.  Its products take 1024 MMA
+// cycles (0.5 us).  What it takes is 1.18 us, the issue slots of the four SM
+// partitions: softmax and widening alone, without a product or a barrier, take
+// 0.7 us of them (a probe of the two loops), and beside the tensor cores each
+// warp runs at about half its lone rate.  So the loops are kept short (a
+// larger kernel fetches its instructions more slowly than it runs them), no
+// maximum is taken in the common case, and the scale bytes arrive by
+// asynchronous copies.  16 prefixes of 1-16K tokens, 26 nodes: 93 us (3.2 TB/s);
+// 64 x 8K tokens with 512 rows a unit: 1.08 ms (1.02 PFLOP/s); 4 x 128K with
+// 768 rows: 1.6 ms.
 //
 // Work split.  A chain is one row tile of one unit: its tree tiles, then its
 // prefix tiles.  The host lays all chains end to end, row tile by row tile, and
@@ -27,22 +36,28 @@
 // finishes at the same time whatever the lengths.  CTAs of the same units and
 // different row tiles run in step and share the K/V tiles in L2.  A CTA does
 // whole chains and at most two parts of chains; a part leaves a partial
-// (16-bit, with a power of two a row, and its fp32 log-sum-exp), and
+// (16-bit, with a power of two a half row, and its fp32 log-sum-exp), and
 // k_merge_q8 joins the parts of each cut chain.  The lists are static: every
 // role walks its CTA's run by itself.  A chain's lengths are the device's, so a
-// captured launch stays right when prefixes have grown since the plan.
+// captured launch stays right when prefixes have grown since the plan.  A
+// segment (a chain, or a part of one) costs 6 us beyond its tiles: its tree
+// tile, the splitting of its queries, the epilogue.
 //
 //   warp 0       TMEM allocation; TMA loads of the K codes (and bf16 tree keys)
 //   warp 1       QK issuer: loads each segment's Q tile; S(j) = Q K(j)^T
 //   warp 2       PV issuer: O += P(j) V(j)
-//   warp 3       TMA loads of the V codes
-//   warps 4-7    softmax: thread r owns row r (TMEM lane r)
-//   warps 8-11   conversion: thread t owns token t of a tile.  Splits the Q tile
-//                into hi and lo (in place, row by row), fetches the tokens'
-//                scale bytes two tiles ahead, hands the keys' powers of two to
-//                the softmax, widens V to bf16 with the values' (rows past the
-//                prefix become zeros).  The tree's V is loaded straight into
-//                the widened buffer.
+//   warp 3       TMA loads of the V codes; asynchronous copies of the tokens'
+//                scale bytes beside them
+//   warps 4-7    conversion: thread t owns token t of a tile and row t of Q.
+//                Splits the Q tile into hi and lo (in place), hands the keys'
+//                powers of two to the softmax a tile ahead, widens V with the
+//                values' (rows past the prefix become zeros).  The tree's V is
+//                loaded straight into the widened buffer.
+//   warps 8-15   softmax, two groups: thread r of a group owns row r (TMEM lane
+//                r), the groups the lower and upper 64 keys of every tile, each
+//                with its own O, reference and sum, joined at a segment's end.
+//                Two warps a partition hide each other's latency, and need no
+//                exchange within a tile.
 //
 // Every wait is bounded; one that runs out aborts the CTA, which lets what it
 // has in flight land and reports TS_ERR_TIMEOUT for the sequences of the
@@ -183,17 +198,16 @@ struct Ctl {
   volatile int* flag;
   uint64_t limit;
 };
-// Bounded waits that also give up as soon as another role has aborted.  Out of
-// line, and asleep between polls: inlined and polling at full rate they made up
-// most of the kernel's code and a third of its issue slots, and the warps at
-// work waited for instructions.
+// Bounded waits that also give up as soon as another role has aborted.  The
+// polling is out of line: inlined at some twenty places, with the clock and the
+// flag, it made the kernel half as large again, and the warps at work waited for
+// instructions (1.37 against 1.16 ms on 64 sequences of 8K tokens).
 __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* flag, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i) {
       if (mbar_try_wait(bar, parity)) return true;
-      __nanosleep(16);
     }
     if (*flag) return false;
     if (globaltimer_ns() - t0 > limit) {
@@ -213,7 +227,6 @@ __device__ __noinline__ bool wait_count(const int* counter, int target, volatile
     int v;
     asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     if (v >= target) return true;
-    __nanosleep(20);
     if ((i & 15) == 15) {
       if (*flag) return false;
       const uint64_t now = globaltimer_ns();
