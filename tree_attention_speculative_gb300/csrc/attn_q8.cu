@@ -1059,7 +1059,7 @@ k_merge_q8(const __grid_constant__ Q8Args args) {
 
 // The runs.  A chain weighs its prefix tiles and `head` more: its tree tiles,
 // Q tile and epilogue.
-constexpr int SEG_COST = 3;  // tiles' worth of a segment's start and end
+constexpr int SEG_COST = 5;  // tiles' worth of a segment's start and end
 constexpr int MIN_RUN = 6;   // no CTA for less weight than this
 constexpr int SLIVER = 2;    // no part of fewer tiles
 
