@@ -573,13 +573,15 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             kq += C::HALVES;
             if (j == I.n_tree - 1 && I.n_prefix > 0) mma_commit(&sm.q_free);
           } else {
+            const uint64_t q_desc = smem_desc_sw128(q_addr, 16, 1024);
+            const uint64_t k_desc = D == 128 ? smem_desc_sw128(k0, 16, 1024) : smem_desc_sw64(k0, 16, 512);
             // 32 channels a step: those of piece h, hi and then lo
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               const int h = i >> 2, low = (i >> 1) & 1, step = i & 1;
-              const uint32_t qa = q_addr + h * (ROW_TILE * 128) + low * 64 + step * 32;
-              const uint64_t kd = D == 128 ? smem_desc_sw128(k0 + h * 64 + step * 32, 16, 1024) : smem_desc_sw64(k0 + step * 32, 16, 512);
-              mma_ss_f8(d_tmem, smem_desc_sw128(qa, 16, 1024), kd, ID_E4M3, i > 0);
+              const uint64_t qd = q_desc + ((h * (ROW_TILE * 128) + low * 64 + step * 32) >> 4);
+              const uint64_t kd = k_desc + (((D == 128 ? h * 64 : 0) + step * 32) >> 4);
+              mma_ss_f8(d_tmem, qd, kd, ID_E4M3, i > 0);
             }
             mma_commit(&sm.s_full[jg % NSB]);
             mma_commit(&sm.k_empty[s0]);
@@ -610,12 +612,12 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v_addr = smem_u32(sm.vb[buf]);
+          const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.vb[buf]), C::HALF_BYTES, 1024);
           const uint32_t p_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
 #pragma unroll
           for (int i = 0; i < KV_TILE / 16; ++i)
             mma_ts(tmem + TMEM_O + (i >> 2) * O_STRIDE, p_tmem + (i >> 2) * HALF_KEYS + (i & 3) * 8,
-                   smem_desc_sw128(v_addr + i * 2048, C::HALF_BYTES, 1024), ID_PV, j > 0 || (i & 3) > 0);
+                   v_desc + ((i * 2048) >> 4), ID_PV, j > 0 || (i & 3) > 0);
           mma_commit(&sm.o_ready);
           mma_commit(&sm.s_free[jg % NSB]);
           mma_commit(&sm.vb_empty[buf]);
