@@ -410,6 +410,14 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     tma_prefetch_desc(&tm_vc);
     tma_prefetch_desc(&tm_kt);
     tma_prefetch_desc(&tm_vt);
+    if (chain0 <= chain1) {
+      // the first Q tile, prefix length and table entry, into L2 (prefetches read no data; see sm100.cuh)
+      const Seg I = make_seg(chain0, cta, 0, args);
+      for (int h = 0; h < C::HALVES; ++h) tma_prefetch_4d(&tm_q, 64 * h, I.g * a.G, I.rt * args.nodes_per_tile, I.b);
+      prefetch_l2(a.prefix_len + I.b);
+      const int i = args.fd_bs.div(args.runs.tile[cta] * KV_TILE);
+      prefetch_l2(a.block_table + (size_t)I.b * a.max_blocks + (i < a.max_blocks ? i : a.max_blocks - 1));
+    }
   }
   if (warp == K_WARP) tmem_alloc(&sm.tmem_base, TMEM_COLS);
   tc_fence_before();
