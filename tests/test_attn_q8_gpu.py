@@ -82,6 +82,11 @@ MORE = [
     ("decode", 9, 1, 8, 2, 128, [0, 1, 15, 16, 127, 128, 129, 255, 1000], 16, "chain"),
     ("decode_d64_g16", 5, 1, 16, 1, 64, [0, 1, 64, 129, 2000], 64, "chain"),
     ("decode_mha", 3, 1, 5, 5, 64, [77, 400, 1], 16, "chain"),
+    # the rows of one warp of the tile, two fewer, one more, and half a warp with many units
+    ("rows_32", 2, 8, 8, 2, 128, [3000, 1700], 16, "levels"),
+    ("rows_30", 3, 15, 4, 2, 64, [2600, 0, 129], 48, "random"),
+    ("rows_33", 2, 33, 2, 2, 128, [3000, 1700], 16, "levels"),
+    ("rows_16_one_node", 40, 1, 16, 1, 128, [(211 * i) % 4000 for i in range(40)], 64, "chain"),
     # two tree tiles; their second one word, one node, full
     ("n129", 2, 129, 2, 1, 128, [130, 0], 16, "random"),
     ("n256_d128", 1, 256, 2, 2, 128, [700], 48, "levels"),
@@ -399,12 +404,12 @@ def test_device_lengths_other_than_planned(host):
 
 
 # (these lengths plan as runs of 6 tiles' weight, so a segment has at most 6 tiles to stall before)
-@pytest.mark.parametrize("stall_tile", [0, 1, 2])
-def test_a_wait_that_runs_out_is_reported(stall_tile):
+@pytest.mark.parametrize("N,stall_tile", [(26, 0), (26, 1), (26, 2), (3, 0), (3, 1)])
+def test_a_wait_that_runs_out_is_reported(N, stall_tile):
     """One sequence's key stream stops: it reports TS_ERR_TIMEOUT, sequences that report nothing
     are right, and the next call on the same workspace is right everywhere."""
     import tree_attention_speculative_gb300 as ts
-    case = _case("stall", 4, 26, 8, 2, 128, [3000, 2000, 64, 1500], 16, "widths")
+    case = _case("stall", 4, N, 8, 2, 128, [3000, 2000, 64, 1500], 16, "widths" if N == 26 else "chain")
     pools = quantised_pools(case)
     call, out, lse, status, ws = _raw(case, pools)
     t, kc, vc, sc, anc, plen, tab, _ = call.keep
