@@ -550,10 +550,11 @@ TS_API ts_status tree_rope(const ts_rope_params* p, ts_stream stream);
  *                   overlap prefix_len, cu_len or status (TS_ERR_SHAPE).
  *   status          [B] int32 in/out (or NULL): a sequence whose status is not
  *                   0 gets nothing and keeps P_b.  A destination block outside
- *                   the pool or past the table sets TS_ERR_BAD_BLOCK, cu_len
- *                   out of order or P_b + rows past 2^30 TS_ERR_SHAPE; such a
- *                   sequence keeps P_b (rows of it that have a valid block may
- *                   have been written past it).
+ *                   the pool or past the table sets TS_ERR_BAD_BLOCK; P_b + rows
+ *                   past 2^30, or cu_len out of order so that the sequence's
+ *                   rows are not its own, TS_ERR_SHAPE.  Such a sequence keeps
+ *                   P_b (rows that have a valid block may have been written
+ *                   past it).
  * T may be 0 (k and v may then be NULL).  No workspace.  Returns TS_ERR_NULL /
  * TS_ERR_SHAPE / TS_ERR_UNSUPPORTED (D not 64 or 128, Hkv over 4096) /
  * TS_ERR_CUDA.
@@ -586,11 +587,15 @@ TS_API ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree,
  * Values past bf16's largest (255 * 2^120; only rows within 3% of it, or with
  * an infinity, hold any) read as infinite.
  * A row that sees no key (no prefix and an empty mask row) gives zeros and an
- * lse of -inf.  The prefix's rows must be as the writers store them.
+ * lse of -inf.  The prefix's rows must be as the writers store them.  A node that
+ * no row sees (the padding of a smaller tree) may hold anything, and so may the
+ * key of one hidden from a row; the value of a node that some rows see must be
+ * finite, or the rows it is hidden from are NaN too (0 * inf).
  *
  * tree_attn_q8_workspace_size: bytes of device workspace it needs (256-byte
- * aligned, ZERO-FILLED before its first use, then left so that stream-ordered
- * calls may share it, like tree_attn_fwd's).  0 for arguments it would reject.
+ * aligned).  Stream-ordered calls may share it, and share one with
+ * tree_attn_fwd: its first 256 bytes, which that call wants zero-filled, stay
+ * as they are.  0 for arguments it would reject.
  * Returns and statuses as tree_attn_fwd.
  */
 TS_API size_t tree_attn_q8_workspace_size(const ts_attn_params* p);

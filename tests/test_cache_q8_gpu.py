@@ -166,7 +166,40 @@ def test_append_reports_bad_sequences():
     status.zero_()
     ts.tree_cache_append_q8(xd[:, :Hkv], xd[:, Hkv:], _dev(bad), torch.zeros(6, dtype=torch.int32, device="cuda"), kd,
                             vd, sd, _dev(np.zeros((6, 4), np.int32)), new_len, status)
-    assert status.cpu().tolist() == [0, -2, -2, -2, -2, -2] and new_len.cpu().tolist() == [4, 0, 0, 0, 0, 0]
+    # (sequence 2 would take rows of sequence 0, which go to one of the two only, so neither counts)
+    assert status.cpu().tolist() == [-2] * 6 and new_len.cpu().tolist() == [0] * 6
+
+
+@pytest.mark.parametrize("cu,want", [
+    ([0, 4, 2, 8, 9], [-2, -2, -2, 0]),     # rows 2 and 3 lie in sequences 0 and 2
+    ([0, 2, 6, 5, 9], [0, -2, -2, -2]),     # row 5 in 1 and 3
+    ([3, 0, 4, 8, 9], [-2, -2, 0, 0]),      # row 3 in sequence 1 and before sequence 0's end
+    ([-1, 2, 4, 8, 9], [-2, 0, 0, 0]),
+    ([0, 2, 4, 8, 10], [0, 0, 0, -2]),      # past the rows
+    ([2, 2, 5, 5, 7], [0, 0, 0, 0]),        # rows of no sequence, and sequences without rows
+])
+def test_append_lengths_out_of_order(cu, want):
+    """A sequence that reports nothing has every one of its rows; the others keep their length."""
+    import tree_attention_speculative_gb300 as ts
+    B, T, Hkv, D, bs = 4, 9, 2, 64, 16
+    x = _values(6, (T, 2 * Hkv, D))
+    xd = _bf(x)
+    pool = _pool(B, Hkv, bs, D)
+    kd, vd, sd = (_dev(p) for p in pool)
+    table = np.arange(B, dtype=np.int32).reshape(B, 1)
+    new = torch.full((B,), -9, dtype=torch.int32, device="cuda")
+    status = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ts.tree_cache_append_q8(xd[:, :Hkv], xd[:, Hkv:], _dev(np.array(cu, np.int32)),
+                            torch.ones(B, dtype=torch.int32, device="cuda"), kd, vd, sd, _dev(table), new, status)
+    assert status.cpu().tolist() == want
+    assert new.cpu().tolist() == [1 + cu[b + 1] - cu[b] if want[b] == 0 else 1 for b in range(B)]
+    got = [p.cpu().numpy() for p in (kd, vd, sd)]
+    for b in range(B):
+        if want[b] == 0:
+            for t in range(cu[b], cu[b + 1]):
+                _put(pool, table, b, 1 + t - cu[b], x[t, :Hkv], x[t, Hkv:])
+            for p, q in zip(got, pool):
+                np.testing.assert_array_equal(p[b], q[b])
 
 
 @pytest.mark.parametrize("Hkv,D,bs,depth", [(2, 128, 16, 7), (1, 64, 64, 3), (8, 128, 48, 19), (3, 64, 144, 0)])

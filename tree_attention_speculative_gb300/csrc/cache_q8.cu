@@ -22,7 +22,7 @@ namespace ts {
 namespace {
 
 constexpr int APPEND_THREADS = 256;
-constexpr int APPEND_MAX_ROWS = 64;  // (token, head) rows a CTA, K and V each
+constexpr int APPEND_MAX_ROWS = 64;  // (token, head) rows a CTA at most, K and V each
 constexpr int COMMIT_Q8_THREADS = 512;
 constexpr int MAX_LEN = 1 << 30;     // positions stay far inside 32 bits
 
@@ -42,7 +42,15 @@ k_append_q8(const __grid_constant__ AppendArgs a, FastDiv heads) {
     if (b >= a.B) return;
     const int P = a.prefix_len[b], c0 = a.cu_len[b], c1 = a.cu_len[b + 1];
     const int st = a.status ? a.status[b] : TS_OK;
-    const bool sized = P >= 0 && P <= MAX_LEN && c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= MAX_LEN - P;
+    // its rows are its own: no sequence before it ends, and none after it begins, among them
+    bool own = true;
+#pragma unroll 4
+    for (int i = lane; i <= a.B; i += 32) {
+      const int c = a.cu_len[i];
+      own = own && (i <= b ? c <= c0 : c >= c1);
+    }
+    own = __all_sync(0xffffffffu, own);
+    const bool sized = own && P >= 0 && P <= MAX_LEN && c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= MAX_LEN - P;
     bool ok = sized;
     if (sized && c1 > c0) {
       const int last = (P + (c1 - c0) - 1) / a.bs;
@@ -195,12 +203,13 @@ k_commit_q8(const __grid_constant__ CommitQ8Args a, FastDiv heads) {
 }  // namespace
 
 cudaError_t launch_append_q8(AppendArgs a, cudaStream_t s) {
-  // Rows a CTA: one round of the CTA's row groups when there are few rows
-  // (so that they spread over the SMs), two or four when there are many.
+  // Rows a CTA: one round of its row groups (32 rows of 128, 64 of 64), so that
+  // few rows spread over the SMs; past four waves of CTAs 64 rows, which halves
+  // the searches.  8 heads of 128: 160K tokens 134 us (32 rows 143 us), 4K tokens
+  // 6.7 us (64 rows 8.0 us).  Heads of 64 on 32 rows, half a round: 16.2 against
+  // 11.7 us for 16K tokens.
   const long long total = (long long)a.T * a.Hkv;
-  const int round = 2 * APPEND_THREADS / (a.D / 8);
-  a.rows = round < APPEND_MAX_ROWS && total > (long long)APPEND_MAX_ROWS * 4 * PLAN_SMS ? APPEND_MAX_ROWS : round;
-  if (a.rows > APPEND_MAX_ROWS) a.rows = APPEND_MAX_ROWS;
+  a.rows = a.D == 64 || total > (long long)APPEND_MAX_ROWS * 4 * PLAN_SMS ? APPEND_MAX_ROWS : APPEND_MAX_ROWS / 2;
   a.len_ctas = ceil_div(a.B, APPEND_THREADS / 32);
   const long long ctas = (total + a.rows - 1) / a.rows + a.len_ctas;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
