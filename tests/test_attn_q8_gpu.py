@@ -403,7 +403,7 @@ def test_device_lengths_other_than_planned(host):
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())
 
 
-# (these lengths plan as runs of 6 tiles' weight, so a segment has at most 6 tiles to stall before)
+# (these lengths plan as short runs, so a segment has few tiles to stall before)
 @pytest.mark.parametrize("N,stall_tile", [(26, 0), (26, 1), (26, 2), (3, 0), (3, 1)])
 def test_a_wait_that_runs_out_is_reported(N, stall_tile):
     """One sequence's key stream stops: it reports TS_ERR_TIMEOUT, sequences that report nothing
@@ -447,3 +447,33 @@ def test_a_nan_row_reaches_its_sequence_and_head_alone():
     ref, A = oracle.attention.tree_attention_case(case), _abs_v(case)
     got[nan], gl[1, :, 2:] = ref[0][nan], ref[1][1, :, 2:]
     check(case, got, gl, ref, A)
+
+
+@pytest.mark.parametrize("N,D", [(26, 128), (70, 64), (200, 128)])
+def test_padding_and_hidden_keys_may_hold_anything(N, D):
+    """Nodes no row sees hold NaN and infinities, a leaf's key too: only the leaf's own row shows it."""
+    case = _case("padding", 3, N, 4, 2, D, [0, 300, 5000], 16, "random")
+    pools = quantised_pools(case)
+    mask = oracle.tree.build_ancestry(case.parent, case.prefix_len)[0].copy()
+    parent = np.asarray(case.parent)
+    pads, leaves = [], []
+    for b in range(3):
+        leaf = [n for n in range(N) if not (parent[b] == n).any()]
+        pads.append(leaf[1:])
+        leaves.append(leaf[0])
+        mask[b, leaf[1:]] = 0
+    clean = _raw(case, pools, mask=mask)
+    clean[0]()
+    junk = np.array([0x7FC0, 0x7F80, 0xFF80, 0xFFC1], np.uint16)
+    for b in range(3):
+        n = len(pads[b])
+        case.v_tree[b, pads[b], :, 3] = junk[np.arange(n) % 4][:, None]
+        case.k_tree[b, pads[b], :, D - 1] = junk[np.arange(n) % 4][:, None]
+        case.k_tree[b, leaves[b], :, 5] = 0x7FC0
+    dirty = _raw(case, pools, mask=mask)
+    dirty[0]()
+    for b in range(3):
+        keep = [n for n in range(N) if n != leaves[b]]
+        for x, y in ((clean[1], dirty[1]), (clean[2], dirty[2])):
+            assert not torch.isnan(x[b]).any() and torch.equal(x[b, keep], y[b, keep])
+            assert torch.isnan(y[b, leaves[b]]).all()

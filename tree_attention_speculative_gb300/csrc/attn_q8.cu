@@ -292,6 +292,29 @@ __device__ __forceinline__ void widen16(const uint4& c, uint32_t m1, uint4& lo, 
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// A node that no row sees may hold anything (the padding of a smaller tree),
+// and 0 * inf is NaN: a row of tree values that are not all finite becomes
+// zeros where no word of the mask column has its bit.
+template <int D>
+__device__ __noinline__ void clear_unseen(uint8_t* row, const uint64_t* word, int bit, int N, int W) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 y = *reinterpret_cast<const uint4*>(row + (c >> 3) * Cfg<D>::HALF_BYTES + (((c ^ (threadIdx.x & 7)) & 7) << 4));
+    top = q8_max2_nan(top, q8_max2_nan(q8_max2_nan(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                                       q8_max2_nan(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+  }
+  if ((q8_max2_nan(top, top >> 16) & 0x7fffu) < 0x7f80u) return;
+  uint64_t seen = 0;
+#pragma unroll 1
+  for (int n = 0; n < N; ++n) seen |= word[(size_t)n * W];
+  if ((seen >> bit) & 1) return;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c)
+    *reinterpret_cast<uint4*>(row + (c >> 3) * Cfg<D>::HALF_BYTES + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+}
+
 // Four bf16 channels of a query times inv as e4m3: hi, and lo = what hi leaves.
 __device__ __forceinline__ void split4(uint32_t w0, uint32_t w1, float inv, uint32_t& hi, uint32_t& lo) {
   uint32_t h[2], l[2];
@@ -604,7 +627,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       // ------------------------------------------------------------ PV issuer
       constexpr uint32_t ID_PV = idesc_bf16_f32(ROW_TILE, D, 0, 1);
       int jg = 0;
-      int vt[NVB] = {0, 0};
       bool ok = true;
       int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
       for (int chain = chain0; ok && chain <= chain1; ++chain) {
@@ -613,11 +635,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         for (int j = 0; j < I.n_tiles; ++j, ++jg) {
           const int buf = jg % NVB;
           ok = wait_bar(&sm.p_full[jg % NSB], (jg / NSB) & 1, ctl) && wait_bar(&sm.vb_full[buf], (jg / NVB) & 1, ctl);
-          if (ok && j < I.n_tree) {
-            ok = wait_bar(&sm.vt_full[buf], (buf ? vt[1] : vt[0]) & 1, ctl);
-            if (buf) ++vt[1];
-            else ++vt[0];
-          }
           if (!ok) break;
           tc_fence_after();
           const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.vb[buf]), C::HALF_BYTES, 1024);
@@ -640,6 +657,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
     const int ct = threadIdx.x - CONVERT_WARP0 * 32;  // token of a tile, row of Q
     const int swz = ct & 7;
     int jg = 0, vq = 0, qn = 0, q8 = 0;
+    int vt_seen[NVB] = {0, 0};
     bool ok = true;
     int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
     for (int chain = chain0; ok && chain <= chain1; ++chain) {
@@ -699,7 +717,6 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             if (buf) ++vt_issued[1];
             else ++vt_issued[0];
           }
-          mbar_arrive(&sm.vb_full[buf]);
         }
         // The scales of tile j + 1 (the tree's: 1) go to the softmax, ahead of the values of tile j.
         if (j + 1 < I.n_tiles) {
@@ -750,6 +767,14 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
           mbar_arrive(&sm.v_empty[slot]);
           ++vq;
           fence_proxy_async();
+          mbar_arrive(&sm.vb_full[buf]);
+        }
+        if (tree) {
+          if (!(ok = wait_bar(&sm.vt_full[buf], (buf ? vt_seen[1] : vt_seen[0]) & 1, ctl))) break;
+          if (buf) ++vt_seen[1];
+          else ++vt_seen[0];
+          const int node = j * KV_TILE + ct;
+          if (node < a.N) clear_unseen<D>(wide + ct * 128, a.anc_mask + (size_t)I.b * a.N * a.W + (node >> 6), node & 63, a.N, a.W);
           mbar_arrive(&sm.vb_full[buf]);
         }
         if (j >= 0) ++jg;
@@ -1069,9 +1094,17 @@ k_merge_q8(const __grid_constant__ Q8Args args) {
 
 // The runs.  A chain weighs its prefix tiles and `head` more: its tree tiles,
 // Q tile and epilogue.
-constexpr int SEG_COST = 5;  // tiles' worth of a segment's start and end
-constexpr int MIN_RUN = 6;   // no CTA for less weight than this
-constexpr int SLIVER = 2;    // no part of fewer tiles
+// SEG_COST: a segment's start and end in tiles' worth of time (32 sequences of
+// 0-8K tokens, one node each: 85 us; with 3, 92 us).
+constexpr int SEG_COST = 5;
+// No CTA for less weight than this: more of them leave more parts to merge.
+// One sequence of 1K tokens, 8 KV heads: 16.6 us; with 6, 20.2, with 12, 18.2;
+// of 4K tokens: 20.9 us; with 3, 22.3, with 6, 22.0.
+constexpr int MIN_RUN = 4;
+// Where every chain weighs this at most and has an SM, none is cut: the merge
+// costs more than it saves (16 sequences of 512 tokens: 15.1 us, cut 18.5).
+constexpr int WHOLE = 12;
+constexpr int SLIVER = 2;  // no part of fewer tiles: it would cost a segment's start and end
 
 Runs plan_runs(const ts_attn_params* p) {
   Runs r{};
@@ -1086,16 +1119,8 @@ Runs plan_runs(const ts_attn_params* p) {
   }
   const long long total = per_rt * row_tiles;
   const long long chains = (long long)p->B * p->Hkv * row_tiles;
-  // One CTA an SM; a multiple of the row tiles where that idles few SMs, so
-  // that the row tiles of a unit run in step.
-  int full = PLAN_SMS;
-  if (row_tiles <= PLAN_SMS) {
-    const int even = PLAN_SMS / row_tiles * row_tiles;
-    if (even * 16 >= PLAN_SMS * 15) full = even;
-  }
-  const bool one_each = chains <= full && longest <= 2 * MIN_RUN;  // short chains: not worth a merge
-  long long n = one_each ? chains : std::max(chains < full ? chains : full, total / MIN_RUN);
-  if (n > full) n = full;
+  const bool one_each = chains <= PLAN_SMS && longest <= WHOLE;
+  const long long n = one_each ? chains : std::min<long long>(PLAN_SMS, std::max(chains, total / MIN_RUN));
   r.n = (int)n;
   int c = 0;
   long long acc = 0;  // weight before the sequence at hand
