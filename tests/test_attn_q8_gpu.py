@@ -477,3 +477,26 @@ def test_padding_and_hidden_keys_may_hold_anything(N, D):
         for x, y in ((clean[1], dirty[1]), (clean[2], dirty[2])):
             assert not torch.isnan(x[b]).any() and torch.equal(x[b, keep], y[b, keep])
             assert torch.isnan(y[b, leaves[b]]).all()
+
+
+def test_step_keeps_a_captured_bf16_call_apart():
+    """TreeVerifyStep reads either cache; the 8-bit call, which wants more workspace here, leaves
+    the one that a captured bf16 call holds."""
+    from tree_attention_speculative_gb300.step import TreeVerifyStep
+    case = _case("apart", 1, 26, 32, 8, 128, [1024], 16, "widths")
+    t = to_dev(case)
+    step = TreeVerifyStep(1, 26, 32, 8, 128, case.prefix_len)
+    args = (t["parent"], t["prefix_len"], t["q"])
+    step.run(*args, t["k_cache"], t["v_cache"], t["block_table"], t["k_tree"], t["v_tree"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run(*args, t["k_cache"], t["v_cache"], t["block_table"], t["k_tree"], t["v_tree"])
+    held, want = step.ws_attn, step.out.clone()
+    pools = quantised_pools(case)
+    kc, vc, sc = codes_dev(pools[0]), codes_dev(pools[1]), torch.from_numpy(pools[2]).cuda()
+    for _ in range(2):
+        step.run(*args, kc, vc, t["block_table"], t["k_tree"], t["v_tree"], kv_scale=sc)
+        check(case, step.out.double().cpu().numpy(), step.lse.double().cpu().numpy())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert step.ws_attn is held and step.ws_attn_q8 is not held and torch.equal(step.out, want)

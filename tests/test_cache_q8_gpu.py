@@ -202,6 +202,21 @@ def test_append_lengths_out_of_order(cu, want):
                 np.testing.assert_array_equal(p[b], q[b])
 
 
+def test_append_refuses_expanded_tokens():
+    import tree_attention_speculative_gb300 as ts
+    Hkv, D, bs = 2, 64, 16
+    kd, vd, sd = (_dev(p) for p in _pool(2, Hkv, bs, D))
+    x = _bf(_values(1, (5, Hkv, D)))
+    new = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rest = (_dev(np.array([0, 5], np.int32)), torch.zeros(1, dtype=torch.int32, device="cuda"), kd, vd, sd,
+            _dev(np.array([[0, 1]], np.int32)), new)
+    for k, v in ((x[:1].expand(5, Hkv, D), x), (x, x[:1].expand(5, Hkv, D)), (x[:, :1].expand(5, Hkv, D), x)):
+        with pytest.raises(ts.TreeSpecError):
+            ts.tree_cache_append_q8(k, v, *rest)
+    ts.tree_cache_append_q8(x, x, *rest)
+    assert new.item() == 5
+
+
 @pytest.mark.parametrize("Hkv,D,bs,depth", [(2, 128, 16, 7), (1, 64, 64, 3), (8, 128, 48, 19), (3, 64, 144, 0)])
 def test_commit_matches_oracle(Hkv, D, bs, depth):
     import tree_attention_speculative_gb300 as ts

@@ -142,3 +142,23 @@ def test_step_positions_and_commits_on_the_bf16_cache():
     ts.tree_commit_accepted(k, t["v_tree"], b.accepted, b.accept_len, t["prefix_len"], *other, t["block_table"], want)
     assert torch.equal(pools[0], other[0]) and torch.equal(pools[1], other[1]) and torch.equal(new, want)
     assert new.cpu().tolist() == [43, 305]
+
+
+def test_expanded_inputs_are_refused():
+    """A token or a head that an expanded view repeats has no stride to hand over."""
+    import tree_attention_speculative_gb300 as ts
+    q, k, pos = _inputs(2, 6, 4, 2, 64)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    for x in (q[:1, :1].expand(2, 6, 4, 64), q[:, :1].expand(2, 6, 4, 64), q[:, :, :1].expand(2, 6, 4, 64)):
+        with pytest.raises(ts.TreeSpecError):
+            ts.tree_rope(x, k, pos, qo, ko, ts.RopeConfig())
+    one = pos[:, :1].contiguous()
+    with pytest.raises(ts.TreeSpecError):
+        ts.tree_rope(q[:1, :1].expand(2, 1, 4, 64), None, one, qo[:, :1].contiguous(), None, ts.RopeConfig())
+    # a single token or head may have any stride
+    wide = torch.empty(1, 1, 4, 64, dtype=torch.bfloat16, device="cuda").as_strided((1, 1, 4, 64), (0, 0, 64, 1))
+    wide.copy_(q[:1, :1])
+    out = torch.empty(1, 1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    ts.tree_rope(wide, None, one[:1], out, None, ts.RopeConfig())
+    ts.tree_rope(q, None, pos, qo, None, ts.RopeConfig())
+    assert torch.equal(out[0, 0], qo[0, 0])

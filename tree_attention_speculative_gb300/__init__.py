@@ -392,12 +392,14 @@ def _token_heads(where: str, x: torch.Tensor, out: torch.Tensor, B: int, N: int)
     if x.is_contiguous():
         return 0, 0
     sb, st, sh, sd = x.stride()
-    if sd != 1 or not (B == 1 or N == 1 or sb == N * st):
-        _bad(where)
     H, D = shape[2], shape[3]
-    if N == 1:
-        st = sb
-    return max(st, (H - 1) * sh + D) if B * N == 1 else st, D if H == 1 else sh
+    head = D if H == 1 else sh
+    row = (H - 1) * head + D
+    token = row if B * N == 1 else sb if N == 1 else st
+    # (an expanded tensor repeats a token or a head: its stride of 0 would mean dense)
+    if sd != 1 or not (B == 1 or N == 1 or sb == N * st) or head < D or token < row:
+        _bad(where)
+    return token, head
 
 
 def tree_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor, q_out: Optional[torch.Tensor],
@@ -439,6 +441,7 @@ def tree_cache_append_q8(k, v, cu_len, prefix_len, k_cache, v_cache, kv_scale, b
     ks, vs = k.stride(), v.stride()
     if not (k.dtype is _BF16 and v.dtype is _BF16 and v.shape == k.shape and ks[2] == 1 and vs[2] == 1
             and (Hkv == 1 or (ks[1] == D and vs[1] == D))
+            and (T <= 1 or (ks[0] >= Hkv * D and vs[0] >= Hkv * D))
             and _is_codes(k_cache, pool) and _is_codes(v_cache, pool) and _is(kv_scale, _U8, (nblk, Hkv, bs, 2))
             and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,)) and _is(prefix_len, _I32, (B,))
             and _is(new_prefix_len, _I32, (B,)) and (status is None or _is(status, _I32, (B,)))):

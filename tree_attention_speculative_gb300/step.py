@@ -6,8 +6,8 @@ tree_build_ancestry -> tree_attn_fwd -> tree_verify_greedy on one stream (their
 _forest variants with ``forest=True``).  With a ``rope`` configuration it
 positions q and k_tree in between (tree_rope), with ``kv_scale`` it reads an
 8-bit cache (tree_attn_fwd_q8), and ``commit`` appends the accepted path to
-either cache.  Every computation happens in the library's kernels.  ``PackedInputs`` stages a step's inputs from host memory
-in one copy.
+either cache.  Every computation happens in the library's kernels.
+``PackedInputs`` stages a step's inputs from host memory in one copy.
 """
 from __future__ import annotations
 
@@ -87,6 +87,7 @@ class TreeVerifyStep:
         self.out = torch.empty(B, N, Hq, D, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev)
         self.ws_attn = None
+        self.ws_attn_q8 = None  # of its own: a captured bf16 call keeps the other
         self.rope = rope
         if rope is not None:
             self.q_rot = torch.empty(B, N, Hq, D, dtype=torch.bfloat16, device=dev)
@@ -124,13 +125,16 @@ class TreeVerifyStep:
         need = tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
         if need == 0:
             raise ValueError("tree_attn_fwd would reject these arguments")
-        if self.ws_attn is None or self.ws_attn.numel() < need:
+        name = "ws_attn" if kv_scale is None else "ws_attn_q8"
+        ws = getattr(self, name)
+        if ws is None or ws.numel() < need:
             # zero-filled once; every call leaves its head (the item counter) zero again
-            self.ws_attn = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            setattr(self, name, ws)
         if kv_scale is None:
-            tree_attn_fwd(p, self.ws_attn, stream)
+            tree_attn_fwd(p, ws, stream)
         else:
-            tree_attn_fwd_q8(p, kv_scale, self.ws_attn, stream)
+            tree_attn_fwd_q8(p, kv_scale, ws, stream)
 
     def verify(self, draft, logits, parent, stream=None):
         verify = tree_verify_greedy_forest if self.forest else tree_verify_greedy
