@@ -87,6 +87,14 @@ MORE = [
     ("rows_30", 3, 15, 4, 2, 64, [2600, 0, 129], 48, "random"),
     ("rows_33", 2, 33, 2, 2, 128, [3000, 1700], 16, "levels"),
     ("rows_16_one_node", 40, 1, 16, 1, 128, [(211 * i) % 4000 for i in range(40)], 64, "chain"),
+    # units of at most 16 rows of 128: trees of a few nodes, one row, eight, nine and sixteen rows, and 17
+    ("few_n4_g4", 5, 4, 8, 2, 128, [0, 77, 128, 1500, 4001], 16, "random"),
+    ("few_n16_g1", 3, 16, 3, 3, 128, [2000, 5, 640], 48, "random"),
+    ("few_n2_g4", 4, 2, 12, 3, 128, [3, 700, 129, 2222], 80, "chain"),
+    ("few_n9_g1", 2, 9, 1, 1, 128, [9000, 128], 144, "levels"),
+    ("few_n1_g1", 70, 1, 2, 2, 128, [(97 * i) % 700 for i in range(70)], 16, "chain"),
+    ("few_long", 1, 3, 16, 4, 128, [40000], 64, "chain"),
+    ("n17_g1", 2, 17, 2, 2, 128, [1300, 257], 16, "random"),
     # two tree tiles; their second one word, one node, full
     ("n129", 2, 129, 2, 1, 128, [130, 0], 16, "random"),
     ("n256_d128", 1, 256, 2, 2, 128, [700], 48, "levels"),
@@ -115,6 +123,23 @@ def test_hot_keys_and_scales_of_many_sizes():
     case.v_cache = W.bf16_bits((oracle.attention.bf16_to_f64(case.v_cache) * 2.0 ** e).astype(np.float32))
     e = g.integers(-3, 2, shape + (1,))
     case.k_cache = W.bf16_bits((oracle.attention.bf16_to_f64(case.k_cache) * 2.0 ** e).astype(np.float32))
+    run_and_check(case)
+
+
+@pytest.mark.parametrize("N,Hq", [(1, 16), (4, 4), (13, 1)])
+def test_few_rows_of_growing_logits(N, Hq):
+    """Keys that grow along the prefix raise a row's reference again and again; hot keys and scales
+    of many sizes; queries from tiny to large; the step from the tree to the prefix."""
+    case = _case("growing", 3, N, Hq, 1, 128, [2900, 131, 900], 16, "chain", hot=0.02)
+    g = W.rng(8, "growing")
+    pos = np.zeros(case.k_cache.shape[:3])
+    for b in range(3):
+        for t in range(int(case.prefix_len[b])):
+            pos[case.block_table[b, t // 16], :, t % 16] = t / 300.0
+    k = oracle.attention.bf16_to_f64(case.k_cache) * 2.0 ** pos[..., None]
+    case.k_cache = W.bf16_bits(k.astype(np.float32))
+    q = oracle.attention.bf16_to_f64(case.q) * 2.0 ** g.integers(-20, 3, case.q.shape[:3] + (1,))
+    case.q = W.bf16_bits(q.astype(np.float32))
     run_and_check(case)
 
 
@@ -449,7 +474,7 @@ def test_a_nan_row_reaches_its_sequence_and_head_alone():
     check(case, got, gl, ref, A)
 
 
-@pytest.mark.parametrize("N,D", [(26, 128), (70, 64), (200, 128)])
+@pytest.mark.parametrize("N,D", [(26, 128), (70, 64), (200, 128), (7, 128)])
 def test_padding_and_hidden_keys_may_hold_anything(N, D):
     """Nodes no row sees hold NaN and infinities, a leaf's key too: only the leaf's own row shows it."""
     case = _case("padding", 3, N, 4, 2, D, [0, 300, 5000], 16, "random")
