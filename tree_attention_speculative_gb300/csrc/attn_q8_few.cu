@@ -29,10 +29,13 @@ constexpr int SOFTMAX_WARP0 = 12;
 constexpr int NSB = 4;                            // S buffers
 constexpr int COLS = 2 * FEW_ROWS;                // hi and lo of every row
 constexpr uint32_t TMEM_COLS = 256;
-constexpr uint32_t TMEM_O = 0;
+constexpr uint32_t TMEM_O = 0;                    // each group's
+constexpr uint32_t O_STRIDE = 32;
 constexpr uint32_t TMEM_S0 = 128;
 constexpr float HIGH_WEIGHT = 1099511627776.f;    // 2^40 (attn_q8.cu: RESCALE_SUM)
-constexpr int SOFTMAX_BARRIER = 1;
+constexpr int THREADS = 640;
+constexpr int GROUP = 128;                        // softmax threads of a group
+constexpr int VOTE_BARRIER = 1, SEG_BARRIER = 3;  // named barriers: a group's (1, 2), and both groups'
 
 struct __align__(1024) Smem {
   static constexpr int NSK = 3, NSV = 4;
@@ -43,8 +46,10 @@ struct __align__(1024) Smem {
   uint8_t q8[2][COLS * FEW_D];           // e4m3 [column][128 B]
   uint8_t p[NVB][FEW_ROWS * KV_TILE * 2];  // bf16 [64 tokens][row][128 B]
   uint16_t v_scale[NSV][KV_TILE];
-  float row_scale[4][FEW_ROWS];  // of segment s in entry s % 4
-  float warp_max[4][FEW_ROWS], warp_sum[4][FEW_ROWS];
+  float row_scale[4][FEW_ROWS];  // of segment s in entry s % 4; so the rows' ancestry words
+  uint64_t anc[4][FEW_ROWS];
+  float tree_scale[FEW_ROWS];
+  float warp_max[2][4][FEW_ROWS], warp_sum[2][4][FEW_ROWS], ref[2][FEW_ROWS];  // by group
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[NSK], k_empty[NSK];
   uint64_t v_full[NSV], v_empty[NSV];
@@ -59,7 +64,7 @@ struct __align__(1024) Smem {
 };
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of a CTA");
 
-__global__ void __launch_bounds__(Q8_THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
 k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorMap tm_kc,
               const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_kt,
               const __grid_constant__ CUtensorMap tm_vt) {
@@ -90,17 +95,17 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
     }
     for (int i = 0; i < Smem::NSV; ++i) {
       mbar_init(&sm.v_full[i], 1 + 32);                    // the tile, and each lane's scale bytes
-      mbar_init(&sm.v_empty[i], CONVERT_THREADS + KV_TILE);  // widened, and the keys' scales read
+      mbar_init(&sm.v_empty[i], CONVERT_THREADS + GROUP);  // widened, and the keys' scales read
     }
     for (int i = 0; i < NVB; ++i) {
       mbar_init(&sm.vb_full[i], CONVERT_THREADS);
       mbar_init(&sm.vb_empty[i], 1);
       mbar_init(&sm.vt_full[i], 1);
-      mbar_init(&sm.p_full[i], KV_TILE);
+      mbar_init(&sm.p_full[i], GROUP);
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_free[i], KV_TILE / 32);
+      mbar_init(&sm.s_free[i], GROUP / 32);
     }
     fence_barrier_init();
   }
@@ -117,6 +122,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       prefetch_l2(a.block_table + (size_t)I.b * a.max_blocks + (i < a.max_blocks ? i : a.max_blocks - 1));
     }
   }
+  if (threadIdx.x < FEW_ROWS) sm.tree_scale[threadIdx.x] = a.scale_log2;
   if (warp == K_WARP) tmem_alloc(&sm.tmem_base, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
@@ -193,8 +199,8 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           const uint32_t p = smem_u32(sm.p[buf]);
 #pragma unroll
           for (int i = 0; i < KV_TILE / 16; ++i)
-            mma_ss(tmem + TMEM_O, v_desc + ((i * 2048) >> 4),
-                   smem_desc_sw128(p + (i >> 2) * (FEW_ROWS * 128) + (i & 3) * 32, 16, 1024), ID_PV, j > 0 || i > 0);
+            mma_ss(tmem + TMEM_O + buf * O_STRIDE, v_desc + ((i * 2048) >> 4),
+                   smem_desc_sw128(p + (i >> 2) * (FEW_ROWS * 128) + (i & 3) * 32, 16, 1024), ID_PV, j > 1 || i > 0);
           mma_commit(&sm.vb_empty[buf]);
         }
       }
@@ -207,10 +213,12 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
     int jg = 0, vq = 0, sg = 0;
     int vt_seen[NVB] = {0, 0};
     bool ok = true;
+    uint64_t anc_next = 0;  // of thread qc = 0: its row's ancestry word
     const auto load_q = [&](int chain) -> uint4 {
       if (qr >= R) return make_uint4(0, 0, 0, 0);
       const int b = args.fd_hkv.div(chain), g = chain - b * a.Hkv;
       const int node = args.fd_g.div(qr);
+      if (qc == 0) anc_next = a.anc_mask[((size_t)b * a.N + node) * a.W];
       return *reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.N + node) * a.Hq + g * a.G + (qr - node * a.G)) * D + qc * 8);
     };
     int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
@@ -218,9 +226,14 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
     for (int chain = chain0; ok && chain <= chain1; ++chain) {
       const Seg I = make_seg(chain, cta, p_next, args);
       const uint4 x = q_next;
+      const uint64_t anc = anc_next;
       if (chain < chain1) {  // on their way while this one runs
         p_next = a.prefix_len[seq_of(chain + 1, args)];
         q_next = load_q(chain + 1);
+        if (ct == 0) {
+          const Seg nx = make_seg(chain + 1, cta, 0, args);
+          for (int h = 0; h < 2; ++h) tma_prefetch_4d(&tm_vt, 64 * h, nx.g, 0, nx.b);
+        }
       }
       if (I.n_tiles == 0) continue;
       {
@@ -246,8 +259,10 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         *reinterpret_cast<uint4*>(to) = x;
         *reinterpret_cast<uint4*>(to + 8 * 128) = make_uint4(0, 0, 0, 0);
         // an infinite query has no finite logits
-        if (qc == 0)
+        if (qc == 0) {
           sm.row_scale[sg & 3][qr] = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
+          sm.anc[sg & 3][qr] = anc;
+        }
         fence_proxy_async();
         mbar_arrive(&sm.q_full[qb]);
         ++sg;
@@ -302,124 +317,122 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = threadIdx.x - SOFTMAX_WARP0 * 32;  // token of a tile, channel of the output
+    const int grp = (warp - SOFTMAX_WARP0) >> 2;   // takes every other tile
+    const int t = threadIdx.x & (GROUP - 1);       // token of a tile, channel of the output
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_tmem = tmem + lane_base + TMEM_O;
     const bool wide = R > 8;
-    int jg = 0, vq = 0, sg = 0;
+    int jg = 0, vq = 0, sg = 0;  // of the segment's first tile
     bool ok = true;
     int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
     for (int chain = chain0; ok && chain <= chain1; ++chain) {
       const Seg I = make_seg(chain, cta, p_next, args);
       if (chain < chain1) p_next = a.prefix_len[seq_of(chain + 1, args)];
-      if (!I.p_ok && t == 0 && a.status) a.status[I.b] = TS_ERR_SHAPE;
+      if (!I.p_ok && grp == 0 && t == 0 && a.status) a.status[I.b] = TS_ERR_SHAPE;
       const int slot_out = 2 * cta + (chain != chain0 ? 1 : 0);
+      const int j0 = (jg ^ grp) & 1;
       uint32_t see = 0;  // rows that see node t
       float m[FEW_ROWS], l[FEW_ROWS];
 #pragma unroll
       for (int r = 0; r < FEW_ROWS; ++r) {
         m[r] = r < R ? NEG_INF : 0.f;  // (rows of the padding need no reference)
         l[r] = 0.f;
-        if (I.n_tree > 0 && r < R && t < a.N)
-          see |= (uint32_t)((a.anc_mask[((size_t)I.b * a.N + args.fd_g.div(r)) * a.W] >> t) & 1) << r;
       }
-      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
-        const bool tree = j < I.n_tree;
-        const int buf = jg % NVB, sb = jg % NSB;
-        bool got = j > 0 || wait_count(&sm.q_done, sg + 1, ctl);
+      const bool split = I.n_tiles == 0 || wait_count(&sm.q_done, sg + 1, ctl);  // (voted on with the first tile)
+      if (I.n_tree > 0 && j0 == 0 && t < a.N) {
+        for (int r = 0; r < R; ++r) see |= (uint32_t)((sm.anc[sg & 3][r] >> t) & 1) << r;
+      }
+      for (int j = j0; ok && j < I.n_tiles; j += 2) {
+        const int tile = jg + j, sb = tile % NSB, uses = tile / NVB;
         float key = 1.f;
         uint32_t vis = see;
-        if (!tree) {
-          const int slot = vq % Smem::NSV;
-          got = got && wait_bar(&sm.v_full[slot], (vq / Smem::NSV) & 1, ctl);
+        bool got = split;
+        if (j >= I.n_tree) {
+          const int v = vq + j - I.n_tree, slot = v % Smem::NSV;
+          got = got && wait_bar(&sm.v_full[slot], (v / Smem::NSV) & 1, ctl);
           const bool inside = (I.t_begin + j - I.n_tree) * KV_TILE + t < I.P;
           key = inside ? pow2_of(sm.v_scale[slot][t] & 0xff) : 0.f;
           vis = inside ? 0xffffu : 0u;
           mbar_arrive(&sm.v_empty[slot]);
-          ++vq;
         }
-        got = got && wait_bar(&sm.s_full[sb], (jg / NSB) & 1, ctl);
-        if (jg >= NVB) got = got && wait_bar(&sm.vb_empty[buf], ((jg / NVB) - 1) & 1, ctl);  // the P buffer
+        got = got && wait_bar(&sm.s_full[sb], (tile / NSB) & 1, ctl);
+        if (uses > 0) got = got && wait_bar(&sm.vb_empty[grp], (uses - 1) & 1, ctl);  // the group's P buffer and O
         got = __all_sync(0xffffffffu, got);
         tc_fence_after();
-        float x[FEW_ROWS], p[FEW_ROWS];
-        uint32_t u[16];
-        tmem_ld16(tmem + lane_base + TMEM_S0 + sb * COLS, u);
-        tmem_ld_wait();
-        reg_fence16(u);
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          x[r] = (vis >> r) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
-        if (wide) {
-          tmem_ld16(tmem + lane_base + TMEM_S0 + sb * COLS + 16, u);
+        const float* scale = j < I.n_tree ? sm.tree_scale : sm.row_scale[sg & 3];
+        float p[FEW_ROWS];
+        // logits before the row's scale
+        const auto logits = [&]() {
+          uint32_t u[16];
+          tmem_ld16(tmem + lane_base + TMEM_S0 + sb * COLS, u);
           tmem_ld_wait();
           reg_fence16(u);
 #pragma unroll
           for (int r = 0; r < 8; ++r)
-            x[r + 8] = (vis >> (r + 8)) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
-        } else {
+            p[r] = (vis >> r) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
+          if (wide) {
+            tmem_ld16(tmem + lane_base + TMEM_S0 + sb * COLS + 16, u);
+            tmem_ld_wait();
+            reg_fence16(u);
+          }
 #pragma unroll
-          for (int r = 8; r < FEW_ROWS; ++r) x[r] = NEG_INF;
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_free[sb]);
-        float scale[FEW_ROWS];
-        const float* rs = sm.row_scale[sg & 3];
-#pragma unroll
-        for (int r = 0; r < FEW_ROWS; ++r) scale[r] = tree ? a.scale_log2 : rs[r];
+          for (int r = 0; r < 8; ++r)
+            p[r + 8] = wide && (vis >> (r + 8)) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
+        };
         // weights; no maximum is taken while they stay below 2^40
         bool fine = true;
         const auto weights = [&]() {
 #pragma unroll
           for (int r = 0; r < FEW_ROWS; ++r) {
-            if (r >= 8 && !wide) {
-              p[r] = 0.f;
-              continue;
-            }
-            p[r] = ex2(fmaf(x[r], scale[r], m[r] == NEG_INF ? 0.f : -m[r]));
-            fine = fine && !(p[r] > HIGH_WEIGHT || (m[r] == NEG_INF && x[r] > NEG_INF));
+            if (r >= 8 && !wide) break;
+            const float y = fmaf(p[r], scale[r], m[r] == NEG_INF ? 0.f : -m[r]);
+            const bool first = m[r] == NEG_INF && p[r] > NEG_INF;
+            p[r] = ex2(y);
+            fine = fine && !(p[r] > HIGH_WEIGHT || first);
           }
         };
+        logits();
         weights();
-        if (!named_barrier_and(SOFTMAX_BARRIER, KV_TILE, got && fine)) {
-          if (!(ok = named_barrier_and(SOFTMAX_BARRIER, KV_TILE, got))) break;
+        if (!named_barrier_and(VOTE_BARRIER + grp, GROUP, got && fine)) {
+          if (!(ok = named_barrier_and(VOTE_BARRIER + grp, GROUP, got))) break;
           // every row's reference goes up to its largest logit of the tile
-          float f[FEW_ROWS];  // what earlier weights are then worth
+          logits();
 #pragma unroll
           for (int r = 0; r < FEW_ROWS; ++r) {
-            float top = x[r] * scale[r];
+            if (r >= R) break;
+            float top = p[r] * scale[r];
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (lane == 0) sm.warp_max[warp & 3][r] = top;
+            if (lane == 0) sm.warp_max[grp][warp & 3][r] = top;
           }
-          named_barrier_and(SOFTMAX_BARRIER, KV_TILE, true);
-#pragma unroll
-          for (int r = 0; r < FEW_ROWS; ++r) {
-            float top = m[r];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) top = fmaxf(top, sm.warp_max[w][r]);
-            f[r] = m[r] == NEG_INF ? 0.f : ex2(m[r] - top);
-            m[r] = top;
-          }
-          if (j > 0) {
-            // what the rows have so far is scaled down: sums here, O once its last PV is done
-            ok = wait_bar(&sm.vb_empty[(jg - 1) % NVB], ((jg - 1) / NVB) & 1, ctl);
-            if (!(ok = named_barrier_and(SOFTMAX_BARRIER, KV_TILE, ok))) break;
-            tc_fence_after();
-            tmem_ld16(tmem + lane_base + TMEM_O, u);
+          named_barrier_and(VOTE_BARRIER + grp, GROUP, true);
+          uint32_t u[16];
+          if (j > 1) {  // (the group's PVs so far are done)
+            tmem_ld16(o_tmem + grp * O_STRIDE, u);
             tmem_ld_wait();
             reg_fence16(u);
+          }
 #pragma unroll
-            for (int r = 0; r < FEW_ROWS; ++r) {
-              l[r] *= f[r];
-              u[r] = f[r] == 0.f ? 0u : __float_as_uint(__uint_as_float(u[r]) * f[r]);
-            }
-            tmem_st16(tmem + lane_base + TMEM_O, u);
+          for (int r = 0; r < FEW_ROWS; ++r) {
+            if (r >= R) break;
+            float top = m[r];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, sm.warp_max[grp][w][r]);
+            const float f = m[r] == NEG_INF ? 0.f : ex2(m[r] - top);  // what earlier weights are then worth
+            m[r] = top;
+            l[r] *= f;
+            u[r] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(u[r]) * f);
+          }
+          if (j > 1) {
+            tmem_st16(o_tmem + grp * O_STRIDE, u);
             tmem_st_wait();
           }
           weights();
         }
-        uint8_t* to = sm.p[buf] + (t >> 6) * (FEW_ROWS * 128) + (t & 7) * 2;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free[sb]);
+        uint8_t* to = sm.p[grp] + (t >> 6) * (FEW_ROWS * 128) + (t & 7) * 2;
         const int chunk = (t & 63) >> 3;
 #pragma unroll
         for (int r = 0; r < FEW_ROWS; ++r) {
@@ -428,32 +441,53 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((chunk ^ (r & 7)) << 4)) = __float2bfloat16_rn(p[r]);
         }
         fence_proxy_async();
-        tc_fence_before();
-        mbar_arrive(&sm.p_full[buf]);
+        mbar_arrive(&sm.p_full[grp]);
       }
-      // End of the segment: the threads' sums are joined, O normalised and stored.
-      if (ok && I.n_tiles > 0) ok = wait_bar(&sm.vb_empty[(jg - 1) % NVB], ((jg - 1) / NVB) & 1, ctl);
-#pragma unroll
-      for (int r = 0; r < FEW_ROWS; ++r) {
-        float y = l[r];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-        if (lane == 0) sm.warp_sum[warp & 3][r] = y;
+      // End of the segment: both groups' sums and O, each at its references, are
+      // joined, normalised and stored, every other row by a group.
+      if (ok) {
+        for (int k = max(0, I.n_tiles - 2); k < I.n_tiles; ++k)
+          ok = ok && wait_bar(&sm.vb_empty[(jg + k) % NVB], ((jg + k) / NVB) & 1, ctl);
       }
-      if (!(ok = named_barrier_and(SOFTMAX_BARRIER, KV_TILE, ok))) break;
-      tc_fence_after();
-      if (I.n_tiles > 0) ++sg;
-      uint32_t u[16];
-      tmem_ld16(tmem + lane_base + TMEM_O, u);
-      tmem_ld_wait();
-      reg_fence16(u);
 #pragma unroll
       for (int r = 0; r < FEW_ROWS; ++r) {
         if (r >= R) break;
-        const float sum = (sm.warp_sum[0][r] + sm.warp_sum[1][r]) + (sm.warp_sum[2][r] + sm.warp_sum[3][r]);
-        const bool none = sum == 0.f;  // the row saw no key
-        const float y = none ? 0.f : __uint_as_float(u[r]) * (1.f / sum);
-        const float lse2 = none ? NEG_INF : m[r] + __log2f(sum);
+        float y = l[r];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+        if (lane == 0) sm.warp_sum[grp][warp & 3][r] = y;
+        if (t == 0) sm.ref[grp][r] = m[r];
+      }
+      if (!(ok = named_barrier_and(SEG_BARRIER, 2 * GROUP, ok))) break;
+      tc_fence_after();
+      if (I.n_tiles > 0) ++sg;
+      jg += I.n_tiles;
+      vq += I.n_prefix;
+      uint32_t u[2][16];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) tmem_ld16(o_tmem + k * O_STRIDE, u[k]);
+      tmem_ld_wait();
+      reg_fence16(u[0]);
+      reg_fence16(u[1]);
+#pragma unroll
+      for (int r = 0; r < FEW_ROWS; ++r) {
+        if (r >= R) break;
+        if ((r & 1) != grp) continue;
+        float sum[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          sum[k] = (sm.warp_sum[k][0][r] + sm.warp_sum[k][1][r]) + (sm.warp_sum[k][2][r] + sm.warp_sum[k][3][r]);
+        const float top = fmaxf(sm.ref[0][r], sm.ref[1][r]);
+        float acc = 0.f, den = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float w = sm.ref[k][r] == NEG_INF ? 0.f : ex2(sm.ref[k][r] - top);
+          den += sum[k] * w;
+          if (w != 0.f) acc = fmaf(__uint_as_float(u[k][r]), w, acc);  // (a group without a weight: whatever its O holds)
+        }
+        const bool none = den == 0.f;  // the row saw no key
+        const float y = none ? 0.f : acc * (1.f / den);
+        const float lse2 = none ? NEG_INF : top + __log2f(den);
         if (I.whole) {
           const int node = args.fd_g.div(r);
           const size_t orow = ((size_t)I.b * a.N + node) * a.Hq + I.g * a.G + (r - node * a.G);
@@ -464,10 +498,10 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           if (t == 0) args.few_lse[slot_out * FEW_ROWS + r] = lse2;
         }
       }
-      // all have read the sums, and this segment's references, before the next one's
+      // all have read O, the sums and this segment's scales before the next one's
       tc_fence_before();
-      named_barrier_and(SOFTMAX_BARRIER, KV_TILE, true);
-      if (t == 0) publish(&sm.segs_done, chain - chain0 + 1);
+      named_barrier_and(SEG_BARRIER, 2 * GROUP, true);
+      if (grp == 0 && t == 0) publish(&sm.segs_done, chain - chain0 + 1);
     }
   }
 
@@ -517,18 +551,30 @@ k_merge_q8_few(const __grid_constant__ Q8Args args) {
   while (last + 1 < runs.n && runs.chain[last + 1] == chain && runs.tile[last + 1] > 0) ++last;
   pdl_wait();
   pdl_trigger();
+  // the parts' weights, 32 at a time a lane each, then their values, several on their way
   float m = NEG_INF, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = c; p <= last; ++p) {
-    const size_t row = (size_t)(2 * p + (p == c && runs.chain[c] != chain ? 1 : 0)) * FEW_ROWS + r;
-    const float lse = args.few_lse[row];
-    if (lse == NEG_INF) continue;  // a part without keys
-    const float4 o = reinterpret_cast<const float4*>(args.few_o + row * FEW_D)[lane];
-    const float m_new = fmaxf(m, lse);
-    const float f = m == NEG_INF ? 0.f : exp2f(m - m_new), w = exp2f(lse - m_new);
-    den = den * f + w;
-    acc = make_float4(acc.x * f + o.x * w, acc.y * f + o.y * w, acc.z * f + o.z * w, acc.w * f + o.w * w);
-    m = m_new;
+  for (int p0 = c; p0 <= last; p0 += 32) {
+    const int p = p0 + lane, slot = 2 * p + (p == c && runs.chain[c] != chain ? 1 : 0);
+    const float lse = p <= last ? args.few_lse[(size_t)slot * FEW_ROWS + r] : NEG_INF;
+    float top = lse;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = fmaxf(top, m);
+    const float f = m == NEG_INF ? 0.f : exp2f(m - top);
+    const float w = lse == NEG_INF ? 0.f : exp2f(lse - top);
+    m = top;
+    den *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    const int n = min(32, last - p0 + 1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int si = __shfl_sync(0xffffffffu, slot, i);
+      const float4 o = reinterpret_cast<const float4*>(args.few_o + ((size_t)si * FEW_ROWS + r) * FEW_D)[lane];
+      den += wi;
+      if (wi != 0.f) acc = make_float4(fmaf(o.x, wi, acc.x), fmaf(o.y, wi, acc.y), fmaf(o.z, wi, acc.z), fmaf(o.w, wi, acc.w));
+    }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
   const int node = args.fd_g.div(r);
@@ -546,7 +592,7 @@ cudaError_t attn_q8_few_prepare() {
 
 cudaError_t launch_attn_q8_few(const Q8Args& t, bool cut, const CUtensorMap& kc, const CUtensorMap& vc,
                                const CUtensorMap& kt, const CUtensorMap& vt, cudaStream_t s) {
-  cudaError_t e = launch_pdl(k_attn_q8_few, dim3(t.runs.n), dim3(Q8_THREADS), sizeof(Smem) + 1024, s, t, kc, vc, kt, vt);
+  cudaError_t e = launch_pdl(k_attn_q8_few, dim3(t.runs.n), dim3(THREADS), sizeof(Smem) + 1024, s, t, kc, vc, kt, vt);
   if (e != cudaSuccess || !cut) return e;
   const dim3 grid(t.runs.n, ceil_div(t.a.N * t.a.G, MERGE_THREADS / 32));
   return launch_pdl(k_merge_q8_few, grid, dim3(MERGE_THREADS), 0, s, t);
