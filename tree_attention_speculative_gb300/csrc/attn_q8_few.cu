@@ -64,6 +64,7 @@ struct __align__(1024) Smem {
 };
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of a CTA");
 
+template <int ROWS>
 __global__ void __launch_bounds__(THREADS, 1)
 k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorMap tm_kc,
               const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_kt,
@@ -138,8 +139,8 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
   } else if (warp == QK_WARP) {
     if (lane == 0) {
       // ------------------------------------------------------------ QK issuer
-      const int n = R > 8 ? 32 : 16;  // columns
-      const uint32_t id_bf16 = idesc_bf16_f32(KV_TILE, n, 0, 0), id_e4m3 = idesc_e4m3_f32(KV_TILE, n);
+      constexpr int n = 2 * ROWS;  // columns
+      constexpr uint32_t id_bf16 = idesc_bf16_f32(KV_TILE, n, 0, 0), id_e4m3 = idesc_e4m3_f32(KV_TILE, n);
       int jg = 0, kq = 0, sg = 0;  // tiles, K ring slots, segments
       bool ok = true;
       int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
@@ -321,7 +322,6 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
     const int t = threadIdx.x & (GROUP - 1);       // token of a tile, channel of the output
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_tmem = tmem + lane_base + TMEM_O;
-    const bool wide = R > 8;
     int jg = 0, vq = 0, sg = 0;  // of the segment's first tile
     bool ok = true;
     int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
@@ -332,9 +332,9 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       const int slot_out = 2 * cta + (chain != chain0 ? 1 : 0);
       const int j0 = (jg ^ grp) & 1;
       uint32_t see = 0;  // rows that see node t
-      float m[FEW_ROWS], l[FEW_ROWS];
+      float m[FEW_ROWS], l[ROWS];
 #pragma unroll
-      for (int r = 0; r < FEW_ROWS; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         m[r] = r < R ? NEG_INF : 0.f;  // (rows of the padding need no reference)
         l[r] = 0.f;
       }
@@ -360,7 +360,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         got = __all_sync(0xffffffffu, got);
         tc_fence_after();
         const float* scale = j < I.n_tree ? sm.tree_scale : sm.row_scale[sg & 3];
-        float p[FEW_ROWS];
+        float p[ROWS];
         // logits before the row's scale
         const auto logits = [&]() {
           uint32_t u[16];
@@ -370,21 +370,20 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
 #pragma unroll
           for (int r = 0; r < 8; ++r)
             p[r] = (vis >> r) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
-          if (wide) {
+          if constexpr (ROWS > 8) {
             tmem_ld16(tmem + lane_base + TMEM_S0 + sb * COLS + 16, u);
             tmem_ld_wait();
             reg_fence16(u);
-          }
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            p[r + 8] = wide && (vis >> (r + 8)) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
+            for (int r = 0; r < 8; ++r)
+              p[r + 8] = (vis >> (r + 8)) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
+          }
         };
         // weights; no maximum is taken while they stay below 2^40
         bool fine = true;
         const auto weights = [&]() {
 #pragma unroll
-          for (int r = 0; r < FEW_ROWS; ++r) {
-            if (r >= 8 && !wide) break;
+          for (int r = 0; r < ROWS; ++r) {
             const float y = fmaf(p[r], scale[r], m[r] == NEG_INF ? 0.f : -m[r]);
             const bool first = m[r] == NEG_INF && p[r] > NEG_INF;
             p[r] = ex2(y);
@@ -398,7 +397,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           // every row's reference goes up to its largest logit of the tile
           logits();
 #pragma unroll
-          for (int r = 0; r < FEW_ROWS; ++r) {
+          for (int r = 0; r < ROWS; ++r) {
             if (r >= R) break;
             float top = p[r] * scale[r];
 #pragma unroll
@@ -413,7 +412,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
             reg_fence16(u);
           }
 #pragma unroll
-          for (int r = 0; r < FEW_ROWS; ++r) {
+          for (int r = 0; r < ROWS; ++r) {
             if (r >= R) break;
             float top = m[r];
 #pragma unroll
@@ -435,8 +434,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         uint8_t* to = sm.p[grp] + (t >> 6) * (FEW_ROWS * 128) + (t & 7) * 2;
         const int chunk = (t & 63) >> 3;
 #pragma unroll
-        for (int r = 0; r < FEW_ROWS; ++r) {
-          if (r >= 8 && !wide) break;
+        for (int r = 0; r < ROWS; ++r) {
           l[r] += p[r];
           *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((chunk ^ (r & 7)) << 4)) = __float2bfloat16_rn(p[r]);
         }
@@ -450,7 +448,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           ok = ok && wait_bar(&sm.vb_empty[(jg + k) % NVB], ((jg + k) / NVB) & 1, ctl);
       }
 #pragma unroll
-      for (int r = 0; r < FEW_ROWS; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         if (r >= R) break;
         float y = l[r];
 #pragma unroll
@@ -470,7 +468,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       reg_fence16(u[0]);
       reg_fence16(u[1]);
 #pragma unroll
-      for (int r = 0; r < FEW_ROWS; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         if (r >= R) break;
         if ((r & 1) != grp) continue;
         float sum[2];
@@ -587,12 +585,15 @@ k_merge_q8_few(const __grid_constant__ Q8Args args) {
 }  // namespace
 
 cudaError_t attn_q8_few_prepare() {
-  return cudaFuncSetAttribute(k_attn_q8_few, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
+  const cudaError_t e = cudaFuncSetAttribute(k_attn_q8_few<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_attn_q8_few<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
 }
 
 cudaError_t launch_attn_q8_few(const Q8Args& t, bool cut, const CUtensorMap& kc, const CUtensorMap& vc,
                                const CUtensorMap& kt, const CUtensorMap& vt, cudaStream_t s) {
-  cudaError_t e = launch_pdl(k_attn_q8_few, dim3(t.runs.n), dim3(THREADS), sizeof(Smem) + 1024, s, t, kc, vc, kt, vt);
+  const auto kernel = t.a.N * t.a.G <= 8 ? k_attn_q8_few<8> : k_attn_q8_few<16>;
+  cudaError_t e = launch_pdl(kernel, dim3(t.runs.n), dim3(THREADS), sizeof(Smem) + 1024, s, t, kc, vc, kt, vt);
   if (e != cudaSuccess || !cut) return e;
   const dim3 grid(t.runs.n, ceil_div(t.a.N * t.a.G, MERGE_THREADS / 32));
   return launch_pdl(k_merge_q8_few, grid, dim3(MERGE_THREADS), 0, s, t);
