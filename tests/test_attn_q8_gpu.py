@@ -87,13 +87,18 @@ MORE = [
     ("rows_30", 3, 15, 4, 2, 64, [2600, 0, 129], 48, "random"),
     ("rows_33", 2, 33, 2, 2, 128, [3000, 1700], 16, "levels"),
     ("rows_16_one_node", 40, 1, 16, 1, 128, [(211 * i) % 4000 for i in range(40)], 64, "chain"),
-    # units of at most 16 rows of 128: trees of a few nodes, one row, eight, nine and sixteen rows, and 17
+    # units of few rows of 128: trees of a few nodes; one row, two, three, eight, nine, sixteen, 17
     ("few_n4_g4", 5, 4, 8, 2, 128, [0, 77, 128, 1500, 4001], 16, "random"),
     ("few_n16_g1", 3, 16, 3, 3, 128, [2000, 5, 640], 48, "random"),
     ("few_n2_g4", 4, 2, 12, 3, 128, [3, 700, 129, 2222], 80, "chain"),
     ("few_n9_g1", 2, 9, 1, 1, 128, [9000, 128], 144, "levels"),
     ("few_n1_g1", 70, 1, 2, 2, 128, [(97 * i) % 700 for i in range(70)], 16, "chain"),
     ("few_long", 1, 3, 16, 4, 128, [40000], 64, "chain"),
+    ("few_n2", 5, 2, 8, 2, 128, [0, 77, 128, 1500, 4001], 16, "chain"),
+    ("few_n8_g1", 3, 8, 3, 3, 128, [2000, 5, 640], 48, "random"),
+    ("few_n3_g1", 4, 3, 2, 2, 128, [3, 700, 129, 2222], 80, "random"),
+    ("few_n1_g8", 40, 1, 16, 2, 128, [(211 * i) % 4000 for i in range(40)], 64, "chain"),
+    ("few_n1_long", 1, 1, 8, 2, 128, [70001], 64, "chain"),
     ("n17_g1", 2, 17, 2, 2, 128, [1300, 257], 16, "random"),
     # two tree tiles; their second one word, one node, full
     ("n129", 2, 129, 2, 1, 128, [130, 0], 16, "random"),
@@ -126,7 +131,7 @@ def test_hot_keys_and_scales_of_many_sizes():
     run_and_check(case)
 
 
-@pytest.mark.parametrize("N,Hq", [(1, 16), (4, 4), (13, 1)])
+@pytest.mark.parametrize("N,Hq", [(1, 16), (4, 4), (13, 1), (1, 8), (2, 4), (7, 1), (1, 1)])
 def test_few_rows_of_growing_logits(N, Hq):
     """Keys that grow along the prefix raise a row's reference again and again; hot keys and scales
     of many sizes; queries from tiny to large; the step from the tree to the prefix."""
@@ -429,7 +434,7 @@ def test_device_lengths_other_than_planned(host):
 
 
 # (these lengths plan as short runs, so a segment has few tiles to stall before)
-@pytest.mark.parametrize("N,stall_tile", [(26, 0), (26, 1), (26, 2), (3, 0), (3, 1)])
+@pytest.mark.parametrize("N,stall_tile", [(26, 0), (26, 1), (26, 2), (3, 0), (3, 1), (2, 0), (2, 1), (2, 2)])
 def test_a_wait_that_runs_out_is_reported(N, stall_tile):
     """One sequence's key stream stops: it reports TS_ERR_TIMEOUT, sequences that report nothing
     are right, and the next call on the same workspace is right everywhere."""
@@ -474,7 +479,7 @@ def test_a_nan_row_reaches_its_sequence_and_head_alone():
     check(case, got, gl, ref, A)
 
 
-@pytest.mark.parametrize("N,D", [(26, 128), (70, 64), (200, 128), (7, 128)])
+@pytest.mark.parametrize("N,D", [(26, 128), (70, 64), (200, 128), (7, 128), (4, 128)])
 def test_padding_and_hidden_keys_may_hold_anything(N, D):
     """Nodes no row sees hold NaN and infinities, a leaf's key too: only the leaf's own row shows it."""
     case = _case("padding", 3, N, 4, 2, D, [0, 300, 5000], 16, "random")

@@ -26,9 +26,9 @@
 // warp runs at about half its lone rate.  So the loops are kept short (a
 // larger kernel fetches its instructions more slowly than it runs them), no
 // maximum is taken in the common case, and the scale bytes arrive by
-// asynchronous copies.  16 prefixes of 1-16K tokens, 26 nodes: 93 us (3.2 TB/s);
-// 64 x 8K tokens with 512 rows a unit: 1.08 ms (1.02 PFLOP/s); 4 x 128K with
-// 768 rows: 1.6 ms.
+// asynchronous copies.  16 prefixes of 1-16K tokens, 26 nodes: 87 us (3.4 TB/s);
+// 64 x 8K tokens with 512 rows a unit: 1.07 ms (1.03 PFLOP/s); 4 x 128K with
+// 768 rows: 1.54 ms.  Units of up to 8 rows go to attn_q8_few.cu.
 //
 // Work split.  A chain is one row tile of one unit: its tree tiles, then its
 // prefix tiles.  The host lays all chains end to end, row tile by row tile, and

@@ -20,7 +20,7 @@ constexpr int NVB = 2;       // widened V tiles
 constexpr int SLOT = 16384;  // a ring slot: 128 tokens of 128 codes, or a 64-column half of a bf16 tree tile
 constexpr float NEG_INF = -INFINITY;
 // Units of N * G up to FEW_ROWS rows with heads of 128 go to attn_q8_few.cu.
-constexpr int FEW_ROWS = 16;
+constexpr int FEW_ROWS = 8;
 
 // The CTAs' runs: CTA c starts at tile tile[c] of chain chain[c] and ends where
 // c + 1 starts.  Chain (rt * B + b) * Hkv + g.

@@ -1,23 +1,30 @@
 // Tree attention over the 8-bit paged cache for units of few rows: N * G up to
-// 16 query rows of heads of 128 (single nodes and the smallest trees).
+// 8 query rows of heads of 128 (single nodes and the smallest trees).
 //
 // attn_q8.cu gives a tile's 128 MMA rows to the queries, so with four of them
 // nearly all of its products, and of the shared memory they read, are padding.
 // Here the tokens are the rows: S^T = K [q_hi; q_lo]^T reads a tile of codes
-// once, for both terms of the split queries (columns 0-7 hi and 8-15 lo of rows
-// 0-7, then the same of rows 8-15), and O^T = V^T P^T has the channels as rows,
-// with the widened values of the other form as its transposed operand.  A
-// softmax thread owns a token of the tile, with every row's logit of it, and a
-// channel of the output.
+// once for both terms of the split queries (columns 0-7 hi, 8-15 lo), and
+// O^T = V^T P^T has the channels as rows, with the widened values of the other
+// form as its transposed operand.  A softmax thread owns a token of the tile,
+// with every row's logit of it, and a channel of the output.
 //
-// The reference of a row's weights is then one value for all threads: it is set
-// at a segment's first tile, and again if a weight passes 2^40 (the threads
-// vote once a tile); sums stay with the threads until the segment's end.
+// The reference of a row's weights is then one value for a whole group of
+// threads.  It is set at a segment's first tile, and again if a weight passes
+// 2^40: the threads vote once a tile.  Sums stay with the threads until the
+// segment's end.  Two groups take alternate tiles, each with a reference, sums
+// and an O of its own, joined at the segment's end: with one group a tile took
+// 1.1 us, the latency of its softmax; with two, 0.79.
 //
-// What bounds it: the bytes of codes, 32.5 KB a tile and SM, and the widening
-// (48 KB of shared memory a tile read and written).  Warps: 0-3 as in
-// attn_q8.cu, 4-11 widen values (half a token's channels a thread) and split
-// the queries, 12-15 softmax.
+// What bounds it: bytes of codes, 32.5 KB a tile and SM (0.73 us of its share
+// of HBM), and where sequences are short a segment's start and end (about 5 us:
+// the split queries, the tree's tile, the join).  32 sequences of 0-8K tokens,
+// one node of 32 heads on 8: 61 us (4.1 TB/s; the other form 85); 256 of 4K:
+// 424 us (5.2 TB/s; 579).  Not beyond 8 rows: with 16 a thread's registers and
+// instructions double, and 16 prefixes of 1-16K took 105 us against 85.
+//
+// Warps: 0-3 as in attn_q8.cu; 4-11 widen values (half a token's channels a
+// thread) and split the queries; 12-19 softmax.
 #include "attn_q8.cuh"
 
 namespace ts {
@@ -27,7 +34,8 @@ constexpr int FEW_D = 128;
 constexpr int CONVERT_THREADS = 256;
 constexpr int SOFTMAX_WARP0 = 12;
 constexpr int NSB = 4;                            // S buffers
-constexpr int COLS = 2 * FEW_ROWS;                // hi and lo of every row
+constexpr int COLS = 2 * FEW_ROWS;                // of S: hi and lo of every row
+constexpr int P_ROWS = 16;                        // the fewest an MMA takes; those past FEW_ROWS hold anything
 constexpr uint32_t TMEM_COLS = 256;
 constexpr uint32_t TMEM_O = 0;                    // each group's
 constexpr uint32_t O_STRIDE = 32;
@@ -38,13 +46,13 @@ constexpr int GROUP = 128;                        // softmax threads of a group
 constexpr int VOTE_BARRIER = 1, SEG_BARRIER = 3;  // named barriers: a group's (1, 2), and both groups'
 
 struct __align__(1024) Smem {
-  static constexpr int NSK = 3, NSV = 4;
+  static constexpr int NSK = 4, NSV = 4;
   uint8_t k[NSK][SLOT];
   uint8_t v[NSV][SLOT];
   uint8_t vb[NVB][KV_TILE * FEW_D * 2];  // bf16 [half][token][128 B]
   uint8_t q[2][COLS * FEW_D * 2];        // bf16 [half][column][128 B] for the tree (its lo columns are 0)
   uint8_t q8[2][COLS * FEW_D];           // e4m3 [column][128 B]
-  uint8_t p[NVB][FEW_ROWS * KV_TILE * 2];  // bf16 [64 tokens][row][128 B]
+  uint8_t p[NVB][P_ROWS * KV_TILE * 2];  // bf16 [64 tokens][row][128 B]
   uint16_t v_scale[NSV][KV_TILE];
   float row_scale[4][FEW_ROWS];  // of segment s in entry s % 4; so the rows' ancestry words
   uint64_t anc[4][FEW_ROWS];
@@ -64,7 +72,6 @@ struct __align__(1024) Smem {
 };
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of a CTA");
 
-template <int ROWS>
 __global__ void __launch_bounds__(THREADS, 1)
 k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorMap tm_kc,
               const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_kt,
@@ -139,8 +146,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
   } else if (warp == QK_WARP) {
     if (lane == 0) {
       // ------------------------------------------------------------ QK issuer
-      constexpr int n = 2 * ROWS;  // columns
-      constexpr uint32_t id_bf16 = idesc_bf16_f32(KV_TILE, n, 0, 0), id_e4m3 = idesc_e4m3_f32(KV_TILE, n);
+      constexpr uint32_t ID_BF16 = idesc_bf16_f32(KV_TILE, COLS, 0, 0), ID_E4M3 = idesc_e4m3_f32(KV_TILE, COLS);
       int jg = 0, kq = 0, sg = 0;  // tiles, K ring slots, segments
       bool ok = true;
       int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
@@ -167,11 +173,11 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
               mma_ss(d_tmem, smem_desc_sw128((i >> 2 ? k1 : k0) + (i & 3) * 32, 16, 1024),
-                     smem_desc_sw128(q + (i >> 2) * (COLS * 128) + (i & 3) * 32, 16, 1024), id_bf16, i > 0);
+                     smem_desc_sw128(q + (i >> 2) * (COLS * 128) + (i & 3) * 32, 16, 1024), ID_BF16, i > 0);
           } else {
             const uint64_t k_desc = smem_desc_sw128(k0, 16, 1024);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) mma_ss_f8(d_tmem, k_desc + 2 * i, q8_desc + 2 * i, id_e4m3, i > 0);
+            for (int i = 0; i < D / 32; ++i) mma_ss_f8(d_tmem, k_desc + 2 * i, q8_desc + 2 * i, ID_E4M3, i > 0);
           }
           mma_commit(&sm.s_full[jg % NSB]);
           mma_commit(&sm.k_empty[s0]);
@@ -184,7 +190,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
   } else if (warp == PV_WARP) {
     if (lane == 0) {
       // ------------------------------------------------------------ PV issuer
-      constexpr uint32_t ID_PV = idesc_bf16_f32(D, FEW_ROWS, 1, 0);
+      constexpr uint32_t ID_PV = idesc_bf16_f32(D, P_ROWS, 1, 0);
       int jg = 0;
       bool ok = true;
       int p_next = chain0 <= chain1 ? a.prefix_len[seq_of(chain0, args)] : 0;
@@ -201,7 +207,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
 #pragma unroll
           for (int i = 0; i < KV_TILE / 16; ++i)
             mma_ss(tmem + TMEM_O + buf * O_STRIDE, v_desc + ((i * 2048) >> 4),
-                   smem_desc_sw128(p + (i >> 2) * (FEW_ROWS * 128) + (i & 3) * 32, 16, 1024), ID_PV, j > 1 || i > 0);
+                   smem_desc_sw128(p + (i >> 2) * (P_ROWS * 128) + (i & 3) * 32, 16, 1024), ID_PV, j > 1 || i > 0);
           mma_commit(&sm.vb_empty[buf]);
         }
       }
@@ -252,17 +258,18 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         uint32_t hi[2], lo[2];
         split4(x.x, x.y, inv, hi[0], lo[0]);
         split4(x.z, x.w, inv, hi[1], lo[1]);
-        const int col = (qr & 8) * 2 + (qr & 7);  // hi's; lo's is 8 further
-        uint8_t* to8 = sm.q8[qb] + col * 128 + (((qc >> 1) ^ (col & 7)) << 4) + (qc & 1) * 8;
-        *reinterpret_cast<uint2*>(to8) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(to8 + 8 * 128) = make_uint2(lo[0], lo[1]);
-        uint8_t* to = sm.q[qb] + (qc >> 3) * (COLS * 128) + col * 128 + (((qc & 7) ^ (col & 7)) << 4);
-        *reinterpret_cast<uint4*>(to) = x;
-        *reinterpret_cast<uint4*>(to + 8 * 128) = make_uint4(0, 0, 0, 0);
-        // an infinite query has no finite logits
-        if (qc == 0) {
-          sm.row_scale[sg & 3][qr] = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
-          sm.anc[sg & 3][qr] = anc;
+        if (qr < FEW_ROWS) {  // column qr; lo's is FEW_ROWS further
+          uint8_t* to8 = sm.q8[qb] + qr * 128 + (((qc >> 1) ^ qr) << 4) + (qc & 1) * 8;
+          *reinterpret_cast<uint2*>(to8) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to8 + FEW_ROWS * 128) = make_uint2(lo[0], lo[1]);
+          uint8_t* to = sm.q[qb] + (qc >> 3) * (COLS * 128) + qr * 128 + (((qc & 7) ^ qr) << 4);
+          *reinterpret_cast<uint4*>(to) = x;
+          *reinterpret_cast<uint4*>(to + FEW_ROWS * 128) = make_uint4(0, 0, 0, 0);
+          // an infinite query has no finite logits
+          if (qc == 0) {
+            sm.row_scale[sg & 3][qr] = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
+            sm.anc[sg & 3][qr] = anc;
+          }
         }
         fence_proxy_async();
         mbar_arrive(&sm.q_full[qb]);
@@ -332,9 +339,9 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       const int slot_out = 2 * cta + (chain != chain0 ? 1 : 0);
       const int j0 = (jg ^ grp) & 1;
       uint32_t see = 0;  // rows that see node t
-      float m[FEW_ROWS], l[ROWS];
+      float m[FEW_ROWS], l[FEW_ROWS];
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
+      for (int r = 0; r < FEW_ROWS; ++r) {
         m[r] = r < R ? NEG_INF : 0.f;  // (rows of the padding need no reference)
         l[r] = 0.f;
       }
@@ -352,7 +359,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           got = got && wait_bar(&sm.v_full[slot], (v / Smem::NSV) & 1, ctl);
           const bool inside = (I.t_begin + j - I.n_tree) * KV_TILE + t < I.P;
           key = inside ? pow2_of(sm.v_scale[slot][t] & 0xff) : 0.f;
-          vis = inside ? 0xffffu : 0u;
+          vis = inside ? 0xffu : 0u;
           mbar_arrive(&sm.v_empty[slot]);
         }
         got = got && wait_bar(&sm.s_full[sb], (tile / NSB) & 1, ctl);
@@ -360,7 +367,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         got = __all_sync(0xffffffffu, got);
         tc_fence_after();
         const float* scale = j < I.n_tree ? sm.tree_scale : sm.row_scale[sg & 3];
-        float p[ROWS];
+        float p[FEW_ROWS];
         // logits before the row's scale
         const auto logits = [&]() {
           uint32_t u[16];
@@ -370,20 +377,12 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
 #pragma unroll
           for (int r = 0; r < 8; ++r)
             p[r] = (vis >> r) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
-          if constexpr (ROWS > 8) {
-            tmem_ld16(tmem + lane_base + TMEM_S0 + sb * COLS + 16, u);
-            tmem_ld_wait();
-            reg_fence16(u);
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-              p[r + 8] = (vis >> (r + 8)) & 1u ? (__uint_as_float(u[r]) + __uint_as_float(u[r + 8])) * key : NEG_INF;
-          }
         };
         // weights; no maximum is taken while they stay below 2^40
         bool fine = true;
         const auto weights = [&]() {
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
+          for (int r = 0; r < FEW_ROWS; ++r) {
             const float y = fmaf(p[r], scale[r], m[r] == NEG_INF ? 0.f : -m[r]);
             const bool first = m[r] == NEG_INF && p[r] > NEG_INF;
             p[r] = ex2(y);
@@ -397,7 +396,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           // every row's reference goes up to its largest logit of the tile
           logits();
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
+          for (int r = 0; r < FEW_ROWS; ++r) {
             if (r >= R) break;
             float top = p[r] * scale[r];
 #pragma unroll
@@ -412,7 +411,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
             reg_fence16(u);
           }
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
+          for (int r = 0; r < FEW_ROWS; ++r) {
             if (r >= R) break;
             float top = m[r];
 #pragma unroll
@@ -431,12 +430,12 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.s_free[sb]);
-        uint8_t* to = sm.p[grp] + (t >> 6) * (FEW_ROWS * 128) + (t & 7) * 2;
+        uint8_t* to = sm.p[grp] + (t >> 6) * (P_ROWS * 128) + (t & 7) * 2;
         const int chunk = (t & 63) >> 3;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
+        for (int r = 0; r < FEW_ROWS; ++r) {
           l[r] += p[r];
-          *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((chunk ^ (r & 7)) << 4)) = __float2bfloat16_rn(p[r]);
+          *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((chunk ^ r) << 4)) = __float2bfloat16_rn(p[r]);
         }
         fence_proxy_async();
         mbar_arrive(&sm.p_full[grp]);
@@ -448,7 +447,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           ok = ok && wait_bar(&sm.vb_empty[(jg + k) % NVB], ((jg + k) / NVB) & 1, ctl);
       }
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
+      for (int r = 0; r < FEW_ROWS; ++r) {
         if (r >= R) break;
         float y = l[r];
 #pragma unroll
@@ -468,7 +467,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       reg_fence16(u[0]);
       reg_fence16(u[1]);
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
+      for (int r = 0; r < FEW_ROWS; ++r) {
         if (r >= R) break;
         if ((r & 1) != grp) continue;
         float sum[2];
@@ -585,15 +584,12 @@ k_merge_q8_few(const __grid_constant__ Q8Args args) {
 }  // namespace
 
 cudaError_t attn_q8_few_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(k_attn_q8_few<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_attn_q8_few<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
+  return cudaFuncSetAttribute(k_attn_q8_few, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
 }
 
 cudaError_t launch_attn_q8_few(const Q8Args& t, bool cut, const CUtensorMap& kc, const CUtensorMap& vc,
                                const CUtensorMap& kt, const CUtensorMap& vt, cudaStream_t s) {
-  const auto kernel = t.a.N * t.a.G <= 8 ? k_attn_q8_few<8> : k_attn_q8_few<16>;
-  cudaError_t e = launch_pdl(kernel, dim3(t.runs.n), dim3(THREADS), sizeof(Smem) + 1024, s, t, kc, vc, kt, vt);
+  cudaError_t e = launch_pdl(k_attn_q8_few, dim3(t.runs.n), dim3(THREADS), sizeof(Smem) + 1024, s, t, kc, vc, kt, vt);
   if (e != cudaSuccess || !cut) return e;
   const dim3 grid(t.runs.n, ceil_div(t.a.N * t.a.G, MERGE_THREADS / 32));
   return launch_pdl(k_merge_q8_few, grid, dim3(MERGE_THREADS), 0, s, t);
