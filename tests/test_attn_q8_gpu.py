@@ -226,12 +226,12 @@ def test_every_code_through_the_keys():
     assert (out == 0).all()
 
 
-def test_rows_that_see_nothing():
+@pytest.mark.parametrize("N,hidden", [(70, [0, 3, 64, 69]), (4, [1]), (1, [0])])
+def test_rows_that_see_nothing(N, hidden):
     """Empty mask rows: the prefix alone; with no prefix, zeros and -inf; and the other rows as ever."""
-    case = _case("empty", 3, 70, 4, 2, 128, [0, 300, 5000], 16, "random")
+    case = _case("empty", 3, N, 4, 2, 128, [0, 300, 5000], 16, "random")
     pools = quantised_pools(case)
     mask = oracle.tree.build_ancestry(case.parent, case.prefix_len)[0].copy()
-    hidden = [0, 3, 64, 69]
     mask[:, hidden] = 0
     call, out, lse, status, _ = _raw(case, pools, mask=mask)
     call()
@@ -250,9 +250,10 @@ def test_rows_that_see_nothing():
     check(case, got, gl, ref, A)
 
 
-def test_garbage_behind_the_prefix_and_unused_table_entries():
+@pytest.mark.parametrize("N", [12, 2])
+def test_garbage_behind_the_prefix_and_unused_table_entries(N):
     """NaN codes and scale bytes of 255 in every row past the prefix, table entries of -1 past its blocks."""
-    case = _case("garbage", 4, 12, 4, 1, 128, [0, 5, 130, 777], 48, "levels")
+    case = _case("garbage", 4, N, 4, 1, 128, [0, 5, 130, 777], 48, "levels" if N > 2 else "chain")
     kc, vc, sc = quantised_pools(case)
     used = np.zeros(kc.shape[:1] + kc.shape[2:3], bool)
     table = np.full((4, case.block_table.shape[1] + 3), -1, np.int32)
@@ -269,9 +270,10 @@ def test_garbage_behind_the_prefix_and_unused_table_entries():
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())
 
 
-def test_bad_blocks_and_long_device_prefixes_are_reported():
+@pytest.mark.parametrize("N", [10, 3])
+def test_bad_blocks_and_long_device_prefixes_are_reported(N):
     """The other sequences are right; nothing is read outside the pool."""
-    case = _case("report", 4, 10, 4, 2, 128, [200, 300, 400, 100], 16, "levels")
+    case = _case("report", 4, N, 4, 2, 128, [200, 300, 400, 100], 16, "levels" if N > 3 else "chain")
     pools = quantised_pools(case)
     table = case.block_table.copy()
     table[1, 3], table[1, 18] = 10 ** 6, -4
@@ -292,7 +294,8 @@ def test_bad_blocks_and_long_device_prefixes_are_reported():
 def test_repeats_bit_for_bit_and_through_graphs_that_share_a_workspace():
     import tree_attention_speculative_gb300 as ts  # noqa: F401
     cases = [_case("graph", 3, 26, 8, 2, 128, [3000, 640, 17], 16, "widths"),
-             _case("graph2", 2, 5, 4, 1, 64, [2000, 100], 64, "worked")]
+             _case("graph2", 2, 5, 4, 1, 64, [2000, 100], 64, "worked"),
+             _case("graph3", 3, 1, 8, 2, 128, [4000, 9, 2222], 16, "chain")]
     need = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
     calls = [_raw(c, quantised_pools(c), workspace=need) for c in cases]
     side = torch.cuda.Stream()
@@ -415,10 +418,11 @@ def test_a_serving_loop():
         plen = new
 
 
+@pytest.mark.parametrize("N", [20, 2])
 @pytest.mark.parametrize("host", [[3000, 100, 0], [900, 5000, 300]], ids=["grown", "mixed"])
-def test_device_lengths_other_than_planned(host):
+def test_device_lengths_other_than_planned(host, N):
     """A captured launch keeps its plan while the device's lengths move, within the block table."""
-    case = _case("moved", 3, 20, 8, 2, 128, [2500, 2600, 700], 16, "levels")
+    case = _case("moved", 3, N, 8, 2, 128, [2500, 2600, 700], 16, "levels" if N > 2 else "chain")
     pools = quantised_pools(case)
     true_len = case.prefix_len
     case.prefix_len = np.array(host, np.int32)
@@ -460,9 +464,10 @@ def test_a_wait_that_runs_out_is_reported(N, stall_tile):
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, A)
 
 
-def test_a_nan_row_reaches_its_sequence_and_head_alone():
+@pytest.mark.parametrize("N", [5, 3])
+def test_a_nan_row_reaches_its_sequence_and_head_alone(N):
     """V rows: every row that sees the token; K rows: the same, through the weights."""
-    case = _case("nan", 3, 5, 4, 2, 128, [300, 40, 70], 16, "worked")
+    case = _case("nan", 3, N, 4, 2, 128, [300, 40, 70], 16, "worked" if N == 5 else "chain")
     pools = quantised_pools(case)
     for b, g, t, w in ((0, 0, 70, 1), (1, 1, 3, 0)):
         blk = case.block_table[b, t // 16]
