@@ -75,88 +75,74 @@ __device__ __forceinline__ void rope_table(const RopeArgs& a, float2* table, int
 
 // R a multiple of 16.  Item e of a CTA: item e % per of head e / per of its
 // tokens' heads; items below R/16 of a head rotate, the rest copy.
+//
+// One item in flight a thread and eight CTAs an SM (32 registers): 4096 tokens
+// of 72 heads of 128 in 26.1 us, 5.8 TB/s (two items, 40 registers: 28.3 us), 16384
+// tokens in 90 us, 6.7 TB/s (98 us).
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(ROPE_THREADS)
+__global__ void __launch_bounds__(ROPE_THREADS, 8)
 k_rope_vec(const __grid_constant__ RopeArgs a, FastDiv heads) {
   __shared__ __align__(16) float2 table[ROPE_MAX_TOK * 64];
   const int t0 = blockIdx.x * a.tok;
   const int ntok = min(a.tok, a.tokens - t0);
   const int lg = a.D == 128 ? 3 : 2;  // items a head: D / 16
   const int n = (ntok * heads.d) << lg;
-  const int rot = a.R / 16, half = a.R / 2, threads = blockDim.x;
+  const int rot = a.R / 16, half = a.R / 2;
   pdl_wait();
   pdl_trigger();
-  constexpr int UN = 2;  // items in flight a thread
-  uint4 x[UN], y[UN];
+  // item e: token k, place i in its head, channels cx and cy of its chunks (beyond
+  // the rotated channels, copied, two chunks one after the other, as when interleaved)
   const auto at = [&](int e, RopeRow& r, int& k, int& i, int& cx, int& cy) {
     const int row = e >> lg;
     k = heads.div(row);
     r = rope_row(a, t0 + k, row - k * heads.d);
     i = e & ((1 << lg) - 1);
-    if (i >= rot) {  // copied: two chunks after the rotated channels
-      cx = 16 * i;
-      cy = cx + 8;
-    } else if (INTERLEAVED) {
-      cx = 16 * i;
-      cy = cx + 8;
-    } else {
-      cx = 8 * i;
-      cy = cx + half;
-    }
+    cx = i >= rot || INTERLEAVED ? 16 * i : 8 * i;
+    cy = i >= rot || INTERLEAVED ? cx + 8 : cx + half;
   };
-  const auto load = [&](int e0) {
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int e = e0 + u * threads;
-      if (e < n) {
-        RopeRow r;
-        int k, i, cx, cy;
-        at(e, r, k, i, cx, cy);
-        x[u] = *reinterpret_cast<const uint4*>(r.src + cx);
-        y[u] = *reinterpret_cast<const uint4*>(r.src + cy);
-      }
-    }
+  uint4 x, y;
+  const auto load = [&](int e) {
+    RopeRow r;
+    int k, i, cx, cy;
+    at(e, r, k, i, cx, cy);
+    x = *reinterpret_cast<const uint4*>(r.src + cx);
+    y = *reinterpret_cast<const uint4*>(r.src + cy);
   };
-  load(threadIdx.x);
+  if ((int)threadIdx.x < n) load(threadIdx.x);
   rope_table(a, table, t0, ntok);
   __syncthreads();
-  for (int e0 = threadIdx.x; e0 < n; e0 += UN * threads) {
-    if (e0 != (int)threadIdx.x) load(e0);
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+    if (e != (int)threadIdx.x) load(e);
+    RopeRow r;  // (worked out again: kept over the table, it would not fit the registers)
+    int k, i, cx, cy;
+    at(e, r, k, i, cx, cy);
+    if (i < rot) {
+      uint32_t* wx = &x.x;
+      uint32_t* wy = &y.x;
+      const float4* cs = reinterpret_cast<const float4*>(table + k * half + 8 * i);
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int e = e0 + u * threads;
-      if (e >= n) break;
-      RopeRow r;
-      int k, i, cx, cy;
-      at(e, r, k, i, cx, cy);
-      if (i < rot) {
-        uint32_t* wx = &x[u].x;
-        uint32_t* wy = &y[u].x;
-        const float4* cs = reinterpret_cast<const float4*>(table + k * half + 8 * i);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (INTERLEAVED) {  // a word is a pair: pairs 8i + w in x, 8i + 4 + w in y
-            const float4 c0 = cs[w / 2], c1 = cs[2 + w / 2];
-            const float2 a0 = up(wx[w]), a1 = up(wy[w]);
-            const float2 r0 = rope_turn(a0.x, a0.y, (w & 1) ? make_float2(c0.z, c0.w) : make_float2(c0.x, c0.y));
-            const float2 r1 = rope_turn(a1.x, a1.y, (w & 1) ? make_float2(c1.z, c1.w) : make_float2(c1.x, c1.y));
-            wx[w] = down(r0.x, r0.y);
-            wy[w] = down(r1.x, r1.y);
-          } else {  // words w of x and y hold pairs 8i + 2w and 8i + 2w + 1
-            const float4 c = cs[w];
-            const float2 p = up(wx[w]), q = up(wy[w]);
-            const float2 r0 = rope_turn(p.x, q.x, make_float2(c.x, c.y));
-            const float2 r1 = rope_turn(p.y, q.y, make_float2(c.z, c.w));
-            wx[w] = down(r0.x, r1.x);
-            wy[w] = down(r0.y, r1.y);
-          }
+      for (int w = 0; w < 4; ++w) {
+        if (INTERLEAVED) {  // a word is a pair: pairs 8i + w in x, 8i + 4 + w in y
+          const float4 c0 = cs[w / 2], c1 = cs[2 + w / 2];
+          const float2 a0 = up(wx[w]), a1 = up(wy[w]);
+          const float2 r0 = rope_turn(a0.x, a0.y, (w & 1) ? make_float2(c0.z, c0.w) : make_float2(c0.x, c0.y));
+          const float2 r1 = rope_turn(a1.x, a1.y, (w & 1) ? make_float2(c1.z, c1.w) : make_float2(c1.x, c1.y));
+          wx[w] = down(r0.x, r0.y);
+          wy[w] = down(r1.x, r1.y);
+        } else {  // words w of x and y hold pairs 8i + 2w and 8i + 2w + 1
+          const float4 c = cs[w];
+          const float2 p = up(wx[w]), q = up(wy[w]);
+          const float2 r0 = rope_turn(p.x, q.x, make_float2(c.x, c.y));
+          const float2 r1 = rope_turn(p.y, q.y, make_float2(c.z, c.w));
+          wx[w] = down(r0.x, r1.x);
+          wy[w] = down(r0.y, r1.y);
         }
-      } else if (r.src == r.dst) {
-        continue;  // in place: the copied channels stay
       }
-      *reinterpret_cast<uint4*>(r.dst + cx) = x[u];
-      *reinterpret_cast<uint4*>(r.dst + cy) = y[u];
+    } else if (r.src == r.dst) {
+      continue;  // in place: the copied channels stay
     }
+    *reinterpret_cast<uint4*>(r.dst + cx) = x;
+    *reinterpret_cast<uint4*>(r.dst + cy) = y;
   }
 }
 
@@ -198,8 +184,8 @@ cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   const int heads = a.Hq + a.Hkv;
   const bool vec = a.R % 16 == 0;
   // Tokens a CTA: enough for an item a thread, but no fewer CTAs than SMs.
-  // 16384 tokens of 9 heads of 128: 17.8 us (two items a thread 21.0, one token
-  // a CTA 20.1); of 2 heads of 64: 7.7 us (one token a CTA 17.2).
+  // 16384 tokens of 9 heads of 128: 16.8 us (one token a CTA 20.1); of 2 heads of
+  // 64: 6.4 us (one token a CTA 17.2).
   const int per = vec ? a.D / 16 : a.D / 2;
   int tok = ceil_div(ROPE_THREADS, heads * per);
   const int spread = ceil_div(a.tokens, PLAN_SMS);
@@ -207,7 +193,7 @@ cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   a.tok = tok < ROPE_MAX_TOK ? tok : ROPE_MAX_TOK;
   const dim3 grid(ceil_div(a.tokens, a.tok));
   // Threads: the items of a CTA in whole rounds (576 items of 72 heads of 128:
-  // 192 threads, 28.1 us for 4096 tokens, 5.4 TB/s; 256 threads, 31.0 us).
+  // 192 threads, a tenth faster than 256, a quarter of which wait in the last round).
   const int items = a.tok * heads * per;
   const int rounds = ceil_div(items, ROPE_THREADS);
   const dim3 block(32 * ceil_div(ceil_div(items, rounds), 32));
