@@ -26,8 +26,10 @@ constexpr int APPEND_MAX_ROWS = 64;  // (token, head) rows a CTA at most, K and 
 constexpr int COMMIT_Q8_THREADS = 512;
 constexpr int MAX_LEN = 1 << 30;     // positions stay far inside 32 bits
 
+// Eight CTAs an SM (32 registers): 149K tokens of 8 heads of 128 in 127 us, 6.7
+// TB/s, against 134 us with five (45 registers; 16 tokens then take 3.1 us, not 3.4).
 template <int D>
-__global__ void __launch_bounds__(APPEND_THREADS)
+__global__ void __launch_bounds__(APPEND_THREADS, 8)
 k_append_q8(const __grid_constant__ AppendArgs a, FastDiv heads) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = APPEND_THREADS / LANES;
@@ -205,9 +207,9 @@ k_commit_q8(const __grid_constant__ CommitQ8Args a, FastDiv heads) {
 cudaError_t launch_append_q8(AppendArgs a, cudaStream_t s) {
   // Rows a CTA: one round of its row groups (32 rows of 128, 64 of 64), so that
   // few rows spread over the SMs; past four waves of CTAs 64 rows, which halves
-  // the searches.  8 heads of 128: 160K tokens 134 us (32 rows 143 us), 4K tokens
-  // 6.7 us (64 rows 8.0 us).  Heads of 64 on 32 rows, half a round: 16.2 against
-  // 11.7 us for 16K tokens.
+  // the searches.  8 heads of 128: 149K tokens 127 us (32 rows 135 us), 4K tokens
+  // 6.4 us (64 rows 6.8 us), 16 tokens 3.4 us (4.5 us).  Heads of 64 on 32 rows,
+  // half a round: 15.2 against 10.8 us for 16K tokens.
   const long long total = (long long)a.T * a.Hkv;
   a.rows = a.D == 64 || total > (long long)APPEND_MAX_ROWS * 4 * PLAN_SMS ? APPEND_MAX_ROWS : APPEND_MAX_ROWS / 2;
   a.len_ctas = ceil_div(a.B, APPEND_THREADS / 32);

@@ -183,7 +183,8 @@ k_rope_pairs(const __grid_constant__ RopeArgs a, FastDiv heads) {
 cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   const int heads = a.Hq + a.Hkv;
   const bool vec = a.R % 16 == 0;
-  // Tokens a CTA: enough for an item a thread, but no fewer CTAs than SMs.
+  // Tokens a CTA: enough for an item a thread, but no fewer CTAs than SMs (300
+  // tokens of 3 heads of 64: 2.4 us, without that 2.7).
   // 16384 tokens of 9 heads of 128: 16.8 us (one token a CTA 20.1); of 2 heads of
   // 64: 6.4 us (one token a CTA 17.2).
   const int per = vec ? a.D / 16 : a.D / 2;
@@ -193,7 +194,7 @@ cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   a.tok = tok < ROPE_MAX_TOK ? tok : ROPE_MAX_TOK;
   const dim3 grid(ceil_div(a.tokens, a.tok));
   // Threads: the items of a CTA in whole rounds (576 items of 72 heads of 128:
-  // 192 threads, a tenth faster than 256, a quarter of which wait in the last round).
+  // 192 threads, 26.1 us for 4096 tokens; 256 threads, 27.1 us).
   const int items = a.tok * heads * per;
   const int rounds = ceil_div(items, ROPE_THREADS);
   const dim3 block(32 * ceil_div(ceil_div(items, rounds), 32));
