@@ -83,6 +83,11 @@ constexpr uint32_t TMEM_S0 = 256;
 constexpr int NSB = 2;        // S buffers
 constexpr int HALF_KEYS = 64;  // keys of a tile a softmax group takes
 constexpr int NT = 4;   // tiles' key scales in flight
+// The weights are rounded to bf16 for the product (half a step, 2^-8 of each at
+// most; as in attn_tc.cu) and summed before that, in fp32.  The sum of the
+// rounded ones would cancel the error of a weight that outweighs the others, but
+// takes 12% (64 sequences of 8K tokens, 1071 -> 1200 us, with the mixed-precision
+// add; 17% with shifts); attn_q8_few.cu takes both sums.
 // A row keeps the reference m it took from its first keys until the weights of
 // 32 keys sum past RESCALE_SUM.  bf16 P, fp32 sums and O have the same precision
 // at every magnitude, so weights up to 2^40 are as good as weights up to 1, and

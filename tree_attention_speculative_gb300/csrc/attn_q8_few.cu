@@ -14,13 +14,19 @@
 // 2^40: the threads vote once a tile.  Sums stay with the threads until the
 // segment's end.  Two groups take alternate tiles, each with a reference, sums
 // and an O of its own, joined at the segment's end: with one group a tile took
-// 1.1 us, the latency of its softmax; with two, 0.79.
+// 1.1 us, the latency of its softmax; with two, 0.85.
+//
+// Weights are bf16 in the product.  They are summed twice: as they are, for the
+// log-sum-exp, and as rounded, for the output, where the error of a weight that
+// outweighs the others then cancels.  (With what bf16 leaves of them in the eight
+// idle columns of P^T the outputs had their own rounding alone, but 32 single
+// nodes took 74 us; without the second sum 61 us.)
 //
 // What bounds it: bytes of codes, 32.5 KB a tile and SM (0.73 us of its share
 // of HBM), and where sequences are short a segment's start and end (about 5 us:
 // the split queries, the tree's tile, the join).  32 sequences of 0-8K tokens,
-// one node of 32 heads on 8: 61 us (4.1 TB/s; the other form 85); 256 of 4K:
-// 424 us (5.2 TB/s; 579).  Not beyond 8 rows: with 16 a thread's registers and
+// one node of 32 heads on 8: 65 us (3.9 TB/s; the other form 85); 256 of 4K:
+// 450 us (4.8 TB/s; 579).  Not beyond 8 rows: with 16 a thread's registers and
 // instructions double, and 16 prefixes of 1-16K took 105 us against 85.
 //
 // Warps: 0-3 as in attn_q8.cu; 4-11 widen values (half a token's channels a
@@ -57,7 +63,8 @@ struct __align__(1024) Smem {
   float row_scale[4][FEW_ROWS];  // of segment s in entry s % 4; so the rows' ancestry words
   uint64_t anc[4][FEW_ROWS];
   float tree_scale[FEW_ROWS];
-  float warp_max[2][4][FEW_ROWS], warp_sum[2][4][FEW_ROWS], ref[2][FEW_ROWS];  // by group
+  float warp_max[2][4][FEW_ROWS], ref[2][FEW_ROWS];  // by group
+  float2 warp_sum[2][4][FEW_ROWS];                   // of the weights, and of the rounded ones
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[NSK], k_empty[NSK];
   uint64_t v_full[NSV], v_empty[NSV];
@@ -339,11 +346,11 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       const int slot_out = 2 * cta + (chain != chain0 ? 1 : 0);
       const int j0 = (jg ^ grp) & 1;
       uint32_t see = 0;  // rows that see node t
-      float m[FEW_ROWS], l[FEW_ROWS];
+      float m[FEW_ROWS], l[FEW_ROWS], lw[FEW_ROWS];  // reference; sums of the weights and of the rounded ones
 #pragma unroll
       for (int r = 0; r < FEW_ROWS; ++r) {
         m[r] = r < R ? NEG_INF : 0.f;  // (rows of the padding need no reference)
-        l[r] = 0.f;
+        l[r] = lw[r] = 0.f;
       }
       const bool split = I.n_tiles == 0 || wait_count(&sm.q_done, sg + 1, ctl);  // (voted on with the first tile)
       if (I.n_tree > 0 && j0 == 0 && t < a.N) {
@@ -419,6 +426,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
             const float f = m[r] == NEG_INF ? 0.f : ex2(m[r] - top);  // what earlier weights are then worth
             m[r] = top;
             l[r] *= f;
+            lw[r] *= f;
             u[r] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(u[r]) * f);
           }
           if (j > 1) {
@@ -434,8 +442,10 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         const int chunk = (t & 63) >> 3;
 #pragma unroll
         for (int r = 0; r < FEW_ROWS; ++r) {
+          const __nv_bfloat16 w = __float2bfloat16_rn(p[r]);
           l[r] += p[r];
-          *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((chunk ^ r) << 4)) = __float2bfloat16_rn(p[r]);
+          lw[r] += __bfloat162float(w);
+          *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((chunk ^ r) << 4)) = w;
         }
         fence_proxy_async();
         mbar_arrive(&sm.p_full[grp]);
@@ -449,9 +459,12 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
 #pragma unroll
       for (int r = 0; r < FEW_ROWS; ++r) {
         if (r >= R) break;
-        float y = l[r];
+        float2 y = make_float2(l[r], lw[r]);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+        for (int d = 16; d > 0; d >>= 1) {
+          y.x += __shfl_xor_sync(0xffffffffu, y.x, d);
+          y.y += __shfl_xor_sync(0xffffffffu, y.y, d);
+        }
         if (lane == 0) sm.warp_sum[grp][warp & 3][r] = y;
         if (t == 0) sm.ref[grp][r] = m[r];
       }
@@ -470,20 +483,23 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
       for (int r = 0; r < FEW_ROWS; ++r) {
         if (r >= R) break;
         if ((r & 1) != grp) continue;
-        float sum[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          sum[k] = (sm.warp_sum[k][0][r] + sm.warp_sum[k][1][r]) + (sm.warp_sum[k][2][r] + sm.warp_sum[k][3][r]);
         const float top = fmaxf(sm.ref[0][r], sm.ref[1][r]);
-        float acc = 0.f, den = 0.f;
+        float acc = 0.f, den = 0.f, norm = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float w = sm.ref[k][r] == NEG_INF ? 0.f : ex2(sm.ref[k][r] - top);
-          den += sum[k] * w;
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            sum.x += sm.warp_sum[k][q][r].x;
+            sum.y += sm.warp_sum[k][q][r].y;
+          }
+          den = fmaf(sum.x, w, den);
+          norm = fmaf(sum.y, w, norm);
           if (w != 0.f) acc = fmaf(__uint_as_float(u[k][r]), w, acc);  // (a group without a weight: whatever its O holds)
         }
         const bool none = den == 0.f;  // the row saw no key
-        const float y = none ? 0.f : acc * (1.f / den);
+        const float y = none ? 0.f : acc * (1.f / norm);
         const float lse2 = none ? NEG_INF : top + __log2f(den);
         if (I.whole) {
           const int node = args.fd_g.div(r);
