@@ -20,15 +20,15 @@
 //
 // What bounds it.  Bytes: 2 D + 2 a token and KV head, half of bf16: a 128-token
 // tile is 32.5 KB, 0.73 us of one SM's share of HBM.  Its products take 1024 MMA
-// cycles (0.5 us).  What it takes is 1.18 us, the issue slots of the four SM
+// cycles (0.5 us).  What it takes is 1.25 us, the issue slots of the four SM
 // partitions: softmax and widening alone, without a product or a barrier, take
 // 0.7 us of them (a probe of the two loops), and beside the tensor cores each
 // warp runs at about half its lone rate.  So the loops are kept short (a
 // larger kernel fetches its instructions more slowly than it runs them), no
 // maximum is taken in the common case, and the scale bytes arrive by
-// asynchronous copies.  16 prefixes of 1-16K tokens, 26 nodes: 87 us (3.4 TB/s);
-// 64 x 8K tokens with 512 rows a unit: 1.07 ms (1.03 PFLOP/s); 4 x 128K with
-// 768 rows: 1.54 ms.  Units of up to 8 rows go to attn_q8_few.cu.
+// asynchronous copies.  16 prefixes of 1-16K tokens, 26 nodes: 94 us (3.1 TB/s);
+// 64 x 8K tokens with 512 rows a unit: 1.12 ms (0.98 PFLOP/s); 4 x 128K with
+// 768 rows: 1.59 ms.  Units of up to 8 rows go to attn_q8_few.cu.
 //
 // Work split.  A chain is one row tile of one unit: its tree tiles, then its
 // prefix tiles.  The host lays all chains end to end, row tile by row tile, and
@@ -84,10 +84,12 @@ constexpr int NSB = 2;        // S buffers
 constexpr int HALF_KEYS = 64;  // keys of a tile a softmax group takes
 constexpr int NT = 4;   // tiles' key scales in flight
 // The weights are rounded to bf16 for the product (half a step, 2^-8 of each at
-// most; as in attn_tc.cu) and summed before that, in fp32.  The sum of the
-// rounded ones would cancel the error of a weight that outweighs the others, but
-// takes 12% (64 sequences of 8K tokens, 1071 -> 1200 us, with the mixed-precision
-// add; 17% with shifts); attn_q8_few.cu takes both sums.
+// most; as in attn_tc.cu) and summed before that, in fp32, for the log-sum-exp.
+// Outputs are divided by the sum of the rounded ones, so that the error of a
+// weight that outweighs the others cancels: with hot keys the outputs are then as
+// exact as their own rounding lets them be.  What rounding adds to the sum is
+// taken for the chunks of 32 keys that weigh more than all before them (64
+// sequences of 8K tokens: 1120 us; for every chunk 1260, for none 1071).
 // A row keeps the reference m it took from its first keys until the weights of
 // 32 keys sum past RESCALE_SUM.  bf16 P, fp32 sums and O have the same precision
 // at every magnitude, so weights up to 2^40 are as good as weights up to 1, and
@@ -119,6 +121,7 @@ struct __align__(1024) Smem {
   // the row's factor (the query's power of two times scale * log2 e).
   float key_scale[NT][KV_TILE];
   float row_scale[NT][ROW_TILE];
+  float half_norm[2][ROW_TILE];  // the sum of the rounded weights
   float2 half_ml[2][ROW_TILE];  // (maximum, sum) of each half, at the end of a segment
   // q_free: no product reads the bf16 Q any more, it may be split in place
   uint64_t q_full, q_free, q8_full, q_empty;
@@ -168,6 +171,20 @@ __device__ __noinline__ void rescale_tmem(uint32_t p_tmem, int chunks, uint32_t 
     for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
     tmem_st32(o_tmem + d, w);
   }
+}
+
+// The sum of 32 weights as rounded to bf16.  Out of line: seldom run.
+__device__ __noinline__ float rounded_sum(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                          uint32_t h, uint32_t i, uint32_t j, uint32_t k, uint32_t l, uint32_t m, uint32_t n,
+                                          uint32_t o, uint32_t p) {
+  const uint32_t w[16] = {a, b, c, d, e, f, g, h, i, j, k, l, m, n, o, p};
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    s0 += __uint_as_float(w[q] << 16);
+    s1 += __uint_as_float(w[q] & 0xffff0000u);
+  }
+  return s0 + s1;
 }
 
 template <int D>
@@ -508,8 +525,9 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         for (int w = 0; w < 2; ++w)
           if (2 * w + half < a.W) anc[w] = arow[2 * w + half];
       }
-      // reference and sum (rows of the padding, which see nothing, need no reference)
-      float m_run = active ? NEG_INF : 0.f, l_run = 0.f;
+      // reference, sum, and what rounding adds to the sum (rows of the padding,
+      // which see nothing, need no reference)
+      float m_run = active ? NEG_INF : 0.f, l_run = 0.f, excess = 0.f;
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         const int tb = jg % NT;
         if (!__all_sync(0xffffffffu, wait_bar(&sm.t_full[tb], (jg / NT) & 1, ctl) &&
@@ -591,8 +609,13 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
               const float f = !move ? 1.f : (m_run == NEG_INF ? 0.f : ex2(m_run - mx));
               if (move) m_run = mx;
               l_run *= f;
+              excess *= f;
               if (j > 0 && !__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) return false;
               rescale_tmem<D>(s_tmem, c, o_tmem, j > 0, f);
+            }
+            if (__any_sync(0xffffffffu, sum > l_run)) {  // (the warp together)
+              excess += rounded_sum(pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7], pk[8], pk[9], pk[10], pk[11],
+                                    pk[12], pk[13], pk[14], pk[15]) - sum;
             }
             l_run += sum;
             tmem_st16(s_tmem + c * 16, pk);
@@ -611,6 +634,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       // are joined, normalised and stored, D/2 channels by each group.  (A warp
       // whose wait gave up comes here too: its partner may be waiting.)
       sm.half_ml[half][r] = make_float2(m_run, l_run);
+      sm.half_norm[half][r] = l_run + excess;
       ok = ok && (I.n_tiles == 0 || wait_count(&sm.pv_done, jg, ctl));
       ok = named_barrier_and(1 + (warp & 3), 64, ok);
       if (!ok) break;
@@ -620,7 +644,8 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       const float w_own = m_run == NEG_INF ? 0.f : ex2(m_run - m), w_other = other.x == NEG_INF ? 0.f : ex2(other.x - m);
       const float l = l_run * w_own + other.y * w_other;
       const bool none = l == 0.f;  // the row saw no key
-      const float inv = none ? 0.f : 1.f / l;
+      const float norm = (l_run + excess) * w_own + sm.half_norm[half ^ 1][r] * w_other;
+      const float inv = none ? 0.f : 1.f / norm;
       const float lse2 = none ? NEG_INF : m + __log2f(l);
       const size_t orow = ((size_t)I.b * a.N + node) * a.Hq + h;
       float f0 = half == 0 ? w_own * inv : w_other * inv, f1 = half == 0 ? w_other * inv : w_own * inv;
@@ -794,11 +819,12 @@ k_merge_q8(const __grid_constant__ Q8Args args) {
 // The runs.  A chain weighs its prefix tiles and `head` more: its tree tiles,
 // Q tile and epilogue.
 // SEG_COST: a segment's start and end in tiles' worth of time (32 sequences of
-// 0-8K tokens, one node each: 85 us; with 3, 92 us).
+// 0-8K tokens, one node each, before attn_q8_few.cu: 85 us; with 3, 92 us; with
+// it: 63 us; with 3, 69 us).
 constexpr int SEG_COST = 5;
-// No CTA for less weight than this: more of them leave more parts to merge.
-// One sequence of 1K tokens, 8 KV heads: 16.6 us; with 6, 20.2, with 12, 18.2;
-// of 4K tokens: 20.9 us; with 3, 22.3, with 6, 22.0.
+// No CTA for less weight than this: more of them leave more parts to merge (one
+// sequence of 1K tokens, 8 KV heads: 16.6 us; with 6, 20.2, with 12, 18.2; of 4K
+// tokens: 20.9 us; with 3, 22.3, with 6, 22.0).
 constexpr int MIN_RUN = 4;
 // Where every chain weighs this at most and has an SM, none is cut: the merge
 // costs more than it saves (16 sequences of 512 tokens: 15.1 us, cut 18.5).
