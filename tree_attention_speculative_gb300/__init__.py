@@ -52,6 +52,7 @@ class AttnParams(ctypes.Structure):
         ("D", ctypes.c_int), ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int),
         ("max_blocks", ctypes.c_int), ("scale", ctypes.c_float), ("rope_theta", ctypes.c_float),
     ]
+    cache_dtypes = ()  # the pools' types, noted by attn_params
 
 
 class RopeParams(ctypes.Structure):
@@ -226,6 +227,14 @@ def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k
     return p
 
 
+def _bf16_pools(where: str, *dtypes):
+    """The bf16 calls read pools, and commit writes one, at two bytes an element:
+    8-bit pools would be passed by half."""
+    for d in dtypes:
+        if d is not None and d.itemsize != 2:
+            _bad(where)
+
+
 def tree_attn_workspace_size(params: AttnParams) -> int:
     return int(lib().tree_attn_workspace_size(ctypes.byref(params)))
 
@@ -248,6 +257,7 @@ def tree_attn_plan_order(params: AttnParams) -> list:
 
 
 def tree_attn_fwd(params: AttnParams, workspace: torch.Tensor, stream=None) -> None:
+    _bf16_pools("tree_attn_fwd", *params.cache_dtypes)
     _check(lib().tree_attn_fwd(ctypes.byref(params), _p(workspace), workspace.numel() * workspace.element_size(),
                                _s(stream)), "tree_attn_fwd")
 
@@ -256,6 +266,7 @@ def tree_attn_fwd_stall_test(params: AttnParams, workspace: torch.Tensor, stall_
                              wait_limit_us: int, stream=None) -> None:
     """Testing only: tree_attn_fwd with sequence ``stall_seq``'s key stream
     stopped before tile ``stall_tile``, so its bounded wait runs out."""
+    _bf16_pools("tree_attn_fwd_stall_test", *params.cache_dtypes)
     _check(lib().tree_attn_fwd_stall_test(ctypes.byref(params), _p(workspace),
                                           workspace.numel() * workspace.element_size(), stall_seq, stall_tile,
                                           wait_limit_us, _s(stream)), "tree_attn_fwd_stall_test")
@@ -266,6 +277,7 @@ def tree_attn_fwd_ctas_test(params: AttnParams, workspace: torch.Tensor, max_cta
     """Testing only: tree_attn_fwd on at most ``max_ctas`` CTAs (and, with
     ``stall_seq >= 0``, that sequence's key stream stopped as in
     tree_attn_fwd_stall_test)."""
+    _bf16_pools("tree_attn_fwd_ctas_test", *params.cache_dtypes)
     _check(lib().tree_attn_fwd_ctas_test(ctypes.byref(params), _p(workspace),
                                          workspace.numel() * workspace.element_size(), max_ctas, stall_seq,
                                          stall_tile, wait_limit_us, _s(stream)), "tree_attn_fwd_ctas_test")
@@ -297,6 +309,7 @@ def tree_verify_greedy_forest(draft_tokens, target_logits, parent_idx, max_depth
 def tree_commit_accepted(k_tree, v_tree, accepted, accept_len, prefix_len, k_cache, v_cache, block_table,
                          new_prefix_len, status=None, stream=None) -> None:
     """Append the accepted path (root .. n*) of every sequence to the paged cache."""
+    _bf16_pools("tree_commit_accepted", getattr(k_cache, "dtype", None), getattr(v_cache, "dtype", None))
     B, N, Hkv, D = k_tree.shape
     nblk, _, bs, _ = k_cache.shape
     _check(lib().tree_commit_accepted(_p(k_tree), _p(v_tree), _p(accepted), _p(accept_len), _p(prefix_len),
