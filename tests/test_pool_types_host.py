@@ -61,3 +61,41 @@ def test_a_step_refuses_8bit_pools_without_their_scales(ts):  # noqa: F811
     k, v = _z(B, N, HKV, D), _z(B, N, HKV, D)
     _refused(ts, lambda: step.attention(_z(B, N, HQ, D), kc, vc, table, plen, k, v, 0))
     _refused(ts, lambda: step.commit(k, v, plen, kc, vc, table, _i(B), 0))
+
+
+def _q8_args(**kw):
+    return _attn_args(**{**dict(k_cache=_pool(torch.float8_e4m3fn), v_cache=_pool(torch.float8_e4m3fn)), **kw})
+
+
+def _q8_refused(ts, a, sc=None, ws=None):  # noqa: F811
+    sc = _z(NBLK, HKV, BS, 2, dtype=torch.uint8) if sc is None else sc
+    ws = _z(1 << 20, dtype=torch.uint8) if ws is None else ws
+    _refused(ts, lambda: ts.tree_attn_fwd_q8(ts.attn_params(**a), sc, ws, 0))
+    _refused(ts, lambda: ts.tree_attn_fwd_q8_stall_test(ts.attn_params(**a), sc, ws, 0, 0, 1000, 0))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v_cache=_z(NBLK - 1, HKV, BS, D, dtype=torch.uint8)), dict(v_cache=_z(NBLK, HKV, BS, 2 * D, dtype=torch.uint8)),
+    dict(k_cache=_z(NBLK, BS, HKV, D, dtype=torch.uint8).transpose(1, 2)), dict(k_cache=_z(NBLK, HKV, BS, D // 2, dtype=torch.uint8)),
+    dict(v_cache=_pool(torch.bfloat16)), dict(block_table=_i(B, MAXB).long()), dict(block_table=_i(B, 2 * MAXB)[:, ::2]),
+    dict(block_table=_i(B - 1, MAXB)), dict(prefix_len=_i(B).long()), dict(prefix_len=_i(B - 1)),
+    dict(prefix_len_host=np.zeros(B - 1, np.int32)), dict(q=_z(B, N, HQ, D).half()),
+    dict(q=_z(B, N, 2 * HQ, D)[:, :, ::2]), dict(k_tree=_z(B, HKV, N, D).transpose(1, 2)), dict(v_tree=_z(B, N - 1, HKV, D)),
+    dict(k_tree=_z(B, N, HKV, D).float()), dict(anc_mask=_i(B, N, 1)), dict(anc_mask=torch.zeros(B, N, dtype=torch.int64)),
+    dict(out=_z(B, N, HQ, D).half()), dict(out=_z(B, N, HQ, 2 * D)[..., :D]), dict(out=_z(B, N - 1, HQ, D)),
+    dict(lse=_z(B, N, HQ)), dict(lse=_z(B, N, HQ - 1, dtype=torch.float32)), dict(status=_i(B).long()), dict(status=_i(B - 1)),
+], ids=lambda kw: next(iter(kw)))
+def test_the_8bit_attention_checks_every_tensor(ts, kw):  # noqa: F811
+    a = _q8_args(**kw)
+    assert ts.attn_params(**a).q8_device is None
+    _q8_refused(ts, a)
+
+
+def test_the_8bit_attention_checks_scales_workspace_and_device(ts):  # noqa: F811
+    _q8_refused(ts, _q8_args(), sc=_z(NBLK, HKV, BS, dtype=torch.uint8))
+    _q8_refused(ts, _q8_args(), ws=_z(2, 1 << 20, dtype=torch.uint8)[:, ::2])
+    _q8_refused(ts, _q8_args())                                   # on the CPU
+    p = ts.attn_params(**_q8_args())
+    assert p.q8_device == -1                                      # well formed but for that
+    assert ts.attn_params(**_q8_args(lse=None, status=None, pos=None)).q8_device == -1
+    assert ts.attn_params(**_q8_args(anc_mask=torch.zeros(B, N, 1, dtype=torch.uint64))).q8_device == -1

@@ -52,7 +52,9 @@ class AttnParams(ctypes.Structure):
         ("D", ctypes.c_int), ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int),
         ("max_blocks", ctypes.c_int), ("scale", ctypes.c_float), ("rope_theta", ctypes.c_float),
     ]
-    cache_dtypes = ()  # the pools' types, noted by attn_params
+    # what attn_params notes of the tensors, for the calls' checks
+    cache_dtypes = ()
+    q8_device = None
 
 
 class RopeParams(ctypes.Structure):
@@ -208,7 +210,8 @@ def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k
     """Fill the C parameter block from tensors (shapes as in treespec.h).
 
     ``prefix_len_host`` is a host int32 tensor/array; the returned object keeps
-    it alive.
+    it alive.  With 8-bit pools every tensor is checked here, for
+    tree_attn_fwd_q8, which raises if one is not as treespec.h has it.
     """
     B, N, Hq, D = q.shape
     nblk, Hkv, bs, _ = k_cache.shape
@@ -223,8 +226,32 @@ def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k
                    B=B, N=N, Hq=Hq, Hkv=Hkv, D=D, block_size=bs, num_blocks=nblk,
                    max_blocks=block_table.shape[1], scale=scale, rope_theta=rope_theta)
     p._keep = (host,)
-    p.cache_dtypes = (getattr(k_cache, "dtype", None), getattr(v_cache, "dtype", None))
+    p.cache_dtypes = kd, vd = getattr(k_cache, "dtype", None), getattr(v_cache, "dtype", None)
+    if (kd is _F8 or kd is _U8) and (vd is _F8 or vd is _U8):
+        p.q8_device = _attn_q8_device((B, N, Hq, D), (nblk, Hkv, bs, D), host, q, k_cache, v_cache, block_table,
+                                      prefix_len, k_tree, v_tree, anc_mask, out, lse, status)
     return p
+
+
+def _attn_q8_device(rows: tuple, pool: tuple, host, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree,
+                    anc_mask, out, lse, status):
+    """The index of the device (-1: the CPU) that all of tree_attn_fwd_q8's
+    tensors are on, or None if one is elsewhere or has another type, shape or
+    density than the call reads."""
+    B, N, Hq, D = rows
+    tree = (B, N, pool[1], D)
+    if not (host.shape == (B,) and _is(q, _BF16, rows) and _is(out, _BF16, rows) and _is_codes(k_cache, pool)
+            and _is_codes(v_cache, pool) and _is(k_tree, _BF16, tree) and _is(v_tree, _BF16, tree)
+            and _is(block_table, _I32, (B, block_table.shape[1])) and _is(prefix_len, _I32, (B,))
+            and (anc_mask.dtype is torch.int64 or anc_mask.dtype is torch.uint64)
+            and _is(anc_mask, anc_mask.dtype, (B, N, (N + 63) // 64))
+            and (lse is None or _is(lse, torch.float32, (B, N, Hq))) and (status is None or _is(status, _I32, (B,)))):
+        return None
+    dev = q.get_device()
+    for t in (out, k_cache, v_cache, k_tree, v_tree, block_table, prefix_len, anc_mask, lse, status):
+        if t is not None and t.get_device() != dev:
+            return None
+    return dev
 
 
 def _bf16_pools(where: str, *dtypes):
@@ -496,12 +523,13 @@ def tree_attn_q8_workspace_size(params: AttnParams) -> int:
 
 
 def _attn_q8_stream(where: str, params: AttnParams, kv_scale, workspace, stream) -> int:
-    for t in params.cache_dtypes:
-        if t is not _F8 and t is not _U8:
-            _bad(where)
-    if not _is(kv_scale, _U8, (params.num_blocks, params.Hkv, params.block_size, 2)):
+    if params.q8_device is None or not workspace.is_contiguous() \
+            or not _is(kv_scale, _U8, (params.num_blocks, params.Hkv, params.block_size, 2)):
         _bad(where)
-    return _launch_stream(where, stream, kv_scale, workspace)
+    handle = _launch_stream(where, stream, kv_scale, workspace)
+    if params.q8_device != kv_scale.get_device():
+        _bad(where)
+    return handle
 
 
 def tree_attn_fwd_q8(params: AttnParams, kv_scale: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
