@@ -33,3 +33,49 @@ def test_a_tensor_on_the_host_is_refused(name):
     with pytest.raises(ts.TreeSpecError):
         ts.tree_attn_fwd_q8(ts.attn_params(**a), scales, ws)
     torch.cuda.synchronize()
+
+
+def _call(case, pools, mask=None):
+    """out and lse [B, N, Hq, ..] of one call on the case's queries over the given pools."""
+    import oracle
+    import tree_attention_speculative_gb300 as ts
+    t = to_dev(case)
+    if mask is None:
+        mask = oracle.tree.build_ancestry(case.parent, case.prefix_len)[0]
+    anc = torch.from_numpy(mask.view(np.int64)).cuda()
+    out = torch.full(t["q"].shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(t["q"].shape[:3], float("nan"), device="cuda")
+    status = torch.zeros(case.B, dtype=torch.int32, device="cuda")
+    kc, vc, sc = codes_dev(pools[0]), codes_dev(pools[1]), torch.from_numpy(pools[2]).cuda()
+    p = ts.attn_params(t["q"], kc, vc, t["block_table"], t["prefix_len"], case.prefix_len, t["k_tree"], t["v_tree"], anc,
+                       None, out, lse, status)
+    ws = torch.zeros(ts.tree_attn_q8_workspace_size(p), dtype=torch.uint8, device="cuda")
+    ts.tree_attn_fwd_q8(p, sc, ws)
+    assert status.cpu().tolist() == [0] * case.B
+    return out, lse
+
+
+@pytest.mark.parametrize("N,Hq,D", [(8, 4, 128), (30, 2, 64)])
+@pytest.mark.parametrize("change", ["hot key late", "hot key first", "hot own key", "NaN"])
+def test_a_row_does_not_depend_on_its_neighbours(N, Hq, D, change):
+    """One query of the last node meets a key far above the others, or holds a NaN: every other
+    row keeps its bits."""
+    from oracle.attention import bf16_to_f64
+    case = W.build_case("alone", 5, W.tree_chain(N), [1000], Hq=Hq, Hkv=1, D=D, bs=16, permute=False)
+    pools = quantised_pools(case)
+    out, lse = _call(case, pools)
+    at = {"hot key late": 700, "hot key first": 3, "hot own key": None, "NaN": None}[change]
+    if at is not None:   # a logit of 60
+        k = bf16_to_f64(case.k_cache[case.block_table[0, at // 16], 0, at % 16])
+    else:
+        k = bf16_to_f64(case.k_tree[0, N - 1, 0])
+    q = k * 60.0 / (case.scale * (k * k).sum())
+    if change == "NaN":
+        q[0] = np.nan
+    case.q[0, N - 1, Hq - 1] = W.bf16_bits(q.astype(np.float32))
+    out2, lse2 = _call(case, pools)
+    others = np.ones((N, Hq), bool)
+    others[N - 1, Hq - 1] = False
+    assert torch.equal(out[0][others], out2[0][others]) and torch.equal(lse[0][others], lse2[0][others])
+    assert not torch.equal(out[0, N - 1, Hq - 1], out2[0, N - 1, Hq - 1])
+    assert torch.isnan(out2[0, N - 1, Hq - 1]).all() == (change == "NaN")

@@ -613,9 +613,10 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
               if (j > 0 && !__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) return false;
               rescale_tmem<D>(s_tmem, c, o_tmem, j > 0, f);
             }
-            if (__any_sync(0xffffffffu, sum > l_run)) {  // (the warp together)
-              excess += rounded_sum(pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7], pk[8], pk[9], pk[10], pk[11],
-                                    pk[12], pk[13], pk[14], pk[15]) - sum;
+            if (__any_sync(0xffffffffu, sum > l_run)) {  // (the warp goes together; a row adds its own chunks' only)
+              const float more = rounded_sum(pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7], pk[8], pk[9], pk[10],
+                                             pk[11], pk[12], pk[13], pk[14], pk[15]) - sum;
+              if (sum > l_run) excess += more;
             }
             l_run += sum;
             tmem_st16(s_tmem + c * 16, pk);
