@@ -55,7 +55,8 @@ def _call(case, pools, mask=None):
     return out, lse
 
 
-@pytest.mark.parametrize("N,Hq,D", [(8, 4, 128), (30, 2, 64)])
+# (units of at most 8 rows of 128 have a kernel of their own)
+@pytest.mark.parametrize("N,Hq,D", [(8, 4, 128), (30, 2, 64), (2, 4, 128), (8, 1, 128)])
 @pytest.mark.parametrize("change", ["hot key late", "hot key first", "hot own key", "NaN"])
 def test_a_row_does_not_depend_on_its_neighbours(N, Hq, D, change):
     """One query of the last node meets a key far above the others, or holds a NaN: every other

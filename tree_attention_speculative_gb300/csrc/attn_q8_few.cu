@@ -10,8 +10,8 @@
 // with every row's logit of it, and a channel of the output.
 //
 // The reference of a row's weights is then one value for a whole group of
-// threads.  It is set at a segment's first tile, and again if a weight passes
-// 2^40: the threads vote once a tile.  Sums stay with the threads until the
+// threads.  It is set at the row's first tile, and again if one of its weights
+// passes 2^40: the threads vote once a tile.  Sums stay with the threads until the
 // segment's end.  Two groups take alternate tiles, each with a reference, sums
 // and an O of its own, joined at the segment's end: with one group a tile took
 // 1.1 us, the latency of its softmax; with two, 0.85.
@@ -400,12 +400,13 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
         weights();
         if (!named_barrier_and(VOTE_BARRIER + grp, GROUP, got && fine)) {
           if (!(ok = named_barrier_and(VOTE_BARRIER + grp, GROUP, got))) break;
-          // every row's reference goes up to its largest logit of the tile
+          // A row whose weights are too high, or that has no reference yet, moves it up to
+          // its largest logit of the tile; the others keep theirs, whatever their neighbours do.
           logits();
 #pragma unroll
           for (int r = 0; r < FEW_ROWS; ++r) {
             if (r >= R) break;
-            float top = p[r] * scale[r];
+            float top = p[r];
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             if (lane == 0) sm.warp_max[grp][warp & 3][r] = top;
@@ -420,9 +421,11 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
 #pragma unroll
           for (int r = 0; r < FEW_ROWS; ++r) {
             if (r >= R) break;
-            float top = m[r];
+            float top = NEG_INF;
 #pragma unroll
             for (int w = 0; w < 4; ++w) top = fmaxf(top, sm.warp_max[grp][w][r]);
+            const bool high = ex2(fmaf(top, scale[r], -m[r])) > HIGH_WEIGHT;  // (as weights() takes it)
+            top = (m[r] == NEG_INF ? top > NEG_INF : high) ? top * scale[r] : m[r];
             const float f = m[r] == NEG_INF ? 0.f : ex2(m[r] - top);  // what earlier weights are then worth
             m[r] = top;
             l[r] *= f;
