@@ -80,3 +80,22 @@ def test_a_row_does_not_depend_on_its_neighbours(N, Hq, D, change):
     assert torch.equal(out[0][others], out2[0][others]) and torch.equal(lse[0][others], lse2[0][others])
     assert not torch.equal(out[0, N - 1, Hq - 1], out2[0, N - 1, Hq - 1])
     assert torch.isnan(out2[0, N - 1, Hq - 1]).all() == (change == "NaN")
+
+
+@pytest.mark.parametrize("B,N,Hq,D,P", [(1, 8, 4, 128, 9000), (1, 30, 4, 64, 5000), (1, 130, 4, 128, 7000), (1, 2, 4, 128, 9000)])
+def test_channels_far_apart_across_the_parts_of_a_chain(B, N, Hq, D, P):
+    """Even tokens hold channels of about 2^20 only, odd ones the others, of about 2^-20: every
+    channel is as exact as if it were alone."""
+    import oracle
+    from tests.test_attn_q8_gpu import check
+    case = W.build_case("apart", 9, W.tree_chain(N), [P] * B, Hq=Hq, Hkv=1, D=D, bs=16, permute=False)
+    v = oracle.attention.bf16_to_f64(case.v_cache)
+    small = np.arange(D) % 2 == 1
+    v[:, :, 0::2] *= np.where(small, 0.0, 2.0 ** 20)
+    v[:, :, 1::2] *= np.where(small, 2.0 ** -20, 0.0)
+    case.v_cache = W.bf16_bits(v.astype(np.float32))
+    t = oracle.attention.bf16_to_f64(case.v_tree) * np.where(small, 2.0 ** -20, 2.0 ** 20)
+    case.v_tree = W.bf16_bits(t.astype(np.float32))
+    pools = quantised_pools(case)
+    out, lse = _call(case, pools)
+    check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())

@@ -35,13 +35,13 @@
 // cuts them into one run of equal weight a CTA (one CTA an SM), so every SM
 // finishes at the same time whatever the lengths.  CTAs of the same units and
 // different row tiles run in step and share the K/V tiles in L2.  A CTA does
-// whole chains and at most two parts of chains; a part leaves a partial
-// (16-bit, with a power of two a half row, and its fp32 log-sum-exp), and
-// k_merge_q8 joins the parts of each cut chain.  The lists are static: every
-// role walks its CTA's run by itself.  A chain's lengths are the device's, so a
-// captured launch stays right when prefixes have grown since the plan.  A
-// segment (a chain, or a part of one) costs 6 us beyond its tiles: its tree
-// tile, the splitting of its queries, the epilogue.
+// whole chains and at most two parts of chains; a part leaves its normalised
+// rows and their log-sum-exp in fp32, and k_merge_q8 joins the parts of each cut
+// chain.  The lists are static: every role walks its CTA's run by itself.  A
+// chain's lengths are the device's, so a captured launch stays right when
+// prefixes have grown since the plan.  A segment (a chain, or a part of one)
+// costs 6 us beyond its tiles: its tree tile, the splitting of its queries, the
+// epilogue.
 //
 //   warp 0       TMEM allocation; TMA loads of the K codes (and bf16 tree keys)
 //   warp 1       QK issuer: loads each segment's Q tile; S(j) = Q K(j)^T
@@ -185,6 +185,44 @@ __device__ __noinline__ float rounded_sum(uint32_t a, uint32_t b, uint32_t c, ui
     s1 += __uint_as_float(w[q] & 0xffff0000u);
   }
   return s0 + s1;
+}
+
+// D/2 channels of a row, its two O joined (zeros for a row that saw nothing,
+// whatever its O holds): fp32 to `part`, or bf16 to `out`.  Out of line, so that
+// the tiles' code stays small.
+template <int D>
+__device__ __noinline__ void store_row(uint32_t o_tmem, float f0, float f1, float* part, __nv_bfloat16* out, bool active,
+                                       int out32) {
+#pragma unroll 1
+  for (int c = 0; c < D / 2; c += 32) {
+    uint32_t u[32], v[32];
+    tmem_ld32(o_tmem + c, u);
+    tmem_ld32(o_tmem + O_STRIDE + c, v);
+    tmem_ld_wait();
+    reg_fence32(u);
+    reg_fence32(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float p = f0 == 0.f ? 0.f : __uint_as_float(u[e]) * f0;
+      u[e] = __float_as_uint(f1 == 0.f ? p : fmaf(__uint_as_float(v[e]), f1, p));
+    }
+    if (!active) continue;
+    if (part) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) st_global_v8(part + c + 8 * q, u + 8 * q);
+      continue;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+    if (out32) {
+      st_global_v8(out + c, w);
+      st_global_v8(out + c + 16, w + 8);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(out + c)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+  }
 }
 
 template <int D>
@@ -649,76 +687,17 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       const float inv = none ? 0.f : 1.f / norm;
       const float lse2 = none ? NEG_INF : m + __log2f(l);
       const size_t orow = ((size_t)I.b * a.N + node) * a.Hq + h;
-      float f0 = half == 0 ? w_own * inv : w_other * inv, f1 = half == 0 ? w_other * inv : w_own * inv;
+      const float f0 = half == 0 ? w_own * inv : w_other * inv, f1 = half == 0 ? w_other * inv : w_own * inv;
       if (I.n_tiles == 0) {
-        if (active && half == 0) args.part_ls[(size_t)slot * ROW_TILE + r] = make_float2(NEG_INF, 0.f);
+        if (active && half == 0) args.part_lse[(size_t)slot * ROW_TILE + r] = NEG_INF;
       } else if (busy) {
-        const uint32_t o0 = tmem + lane_base + TMEM_O;
-        // columns [c, c + 32) of the normalised row (zeros for a row that saw nothing, whatever its O holds)
-        auto columns = [&](int c, float (&x)[32]) {
-          uint32_t u[32], v[32];
-          tmem_ld32(o0 + c, u);
-          tmem_ld32(o0 + O_STRIDE + c, v);
-          tmem_ld_wait();
-          reg_fence32(u);
-          reg_fence32(v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p = f0 == 0.f ? 0.f : __uint_as_float(u[e]) * f0;
-            x[e] = f1 == 0.f ? p : fmaf(__uint_as_float(v[e]), f1, p);
-          }
-        };
-        if (!I.whole) {
-          // a part: 16-bit values below 2^10 with a power of two for these D/2 channels
-          float top = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) {
-            float x[32];
-            columns(half * (D / 2) + c, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
-          }
-          const int e = min(max((int)(__float_as_uint(top) >> 23), 10), 253);  // top < 2^(e - 126)
-          const float up = pow2_of(263 - e);                                   // 2^(136 - e)
-          f0 *= up;
-          f1 *= up;
-          if (active) {
-            float2* ls = args.part_ls + (size_t)slot * ROW_TILE + r;
-            if (half == 0) *ls = make_float2(lse2, pow2_of(e - 9));
-            else args.part_f1[(size_t)slot * ROW_TILE + r] = pow2_of(e - 9);
-          }
-        } else if (active && half == 0 && a.lse) {
-          a.lse[orow] = lse2 * 0.69314718055994531f;
+        if (active && half == 0) {
+          if (!I.whole) args.part_lse[(size_t)slot * ROW_TILE + r] = lse2;
+          else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
         }
-        __half* part = args.part_o + ((size_t)slot * ROW_TILE + r) * D;
-        __nv_bfloat16* out = a.out + orow * D;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          const int c = half * (D / 2) + c0;
-          float x[32];
-          uint32_t w[16];
-          columns(c, x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (I.whole) {
-              w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-            } else {
-              const __half2 t = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
-              w[e] = *reinterpret_cast<const uint32_t*>(&t);
-            }
-          }
-          if (active) {
-            void* dst = I.whole ? (void*)(out + c) : (void*)(part + c);
-            if (!I.whole || args.out32) {
-              st_global_v8(dst, w);
-              st_global_v8(static_cast<uint8_t*>(dst) + 32, w + 8);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                static_cast<uint4*>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-            }
-          }
-        }
+        float* part = args.part_o + ((size_t)slot * ROW_TILE + r) * D + half * (D / 2);
+        __nv_bfloat16* out = a.out + orow * D + half * (D / 2);
+        store_row<D>(tmem + lane_base + TMEM_O + half * (D / 2), f0, f1, I.whole ? nullptr : part, out, active, args.out32);
       }
       // both halves have read O, and each other's sums, before the next segment's first P
       tc_fence_before();
@@ -789,20 +768,16 @@ k_merge_q8(const __grid_constant__ Q8Args args) {
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
   for (int p = c; p <= last; ++p) {
     const int slot = p == c ? first : 2 * p;
-    const float2 ls = args.part_ls[(size_t)slot * ROW_TILE + r];
-    if (ls.x == NEG_INF) continue;  // a part without keys: its values were not written
-    const uint4 raw = reinterpret_cast<const uint4*>(args.part_o + ((size_t)slot * ROW_TILE + r) * D)[sub];
-    const float m_new = fmaxf(m, ls.x);
-    const float f = m == NEG_INF ? 0.f : exp2f(m - m_new), w = exp2f(ls.x - m_new);
+    const float lse = args.part_lse[(size_t)slot * ROW_TILE + r];
+    if (lse == NEG_INF) continue;  // a part without keys: its values were not written
+    const float4* o = reinterpret_cast<const float4*>(args.part_o + ((size_t)slot * ROW_TILE + r) * D + sub * 8);
+    const float4 lo = o[0], hi = o[1];
+    const float m_new = fmaxf(m, lse);
+    const float f = m == NEG_INF ? 0.f : exp2f(m - m_new), w = exp2f(lse - m_new);
     den = den * f + w;
-    const float ws = w * (sub < LANES / 2 ? ls.y : args.part_f1[(size_t)slot * ROW_TILE + r]);
-    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+    const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[k]));
-      acc[2 * k] = fmaf(ws, v.x, acc[2 * k] * f);
-      acc[2 * k + 1] = fmaf(ws, v.y, acc[2 * k + 1] * f);
-    }
+    for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, x[k], acc[k] * f);
     m = m_new;
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
@@ -885,12 +860,10 @@ bool any_cut(const Runs& r) {
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-size_t part_o_bytes(const Runs& r, int D) { return any_cut(r) ? round256((size_t)2 * r.n * ROW_TILE * D * 2) : 0; }
-size_t few_o_bytes(const Runs& r, int D) { return any_cut(r) ? round256((size_t)2 * r.n * FEW_ROWS * D * 4) : 0; }
-size_t few_lse_bytes(const Runs& r) { return any_cut(r) ? round256((size_t)2 * r.n * FEW_ROWS * 4) : 0; }
 bool few_rows(int N, int G, int D) { return N * G <= FEW_ROWS && D == 128; }
-size_t part_ls_bytes(const Runs& r) { return any_cut(r) ? round256((size_t)2 * r.n * ROW_TILE * sizeof(float2)) : 0; }
-size_t part_f1_bytes(const Runs& r) { return part_ls_bytes(r) / 2; }
+// Two parts a CTA at most, of `rows` rows each.
+size_t part_o_bytes(const Runs& r, int rows, int D) { return any_cut(r) ? round256((size_t)2 * r.n * rows * D * 4) : 0; }
+size_t part_lse_bytes(const Runs& r, int rows) { return any_cut(r) ? round256((size_t)2 * r.n * rows * 4) : 0; }
 
 bool encode_codes(CUtensorMap* m, const void* base, int D, const AttnArgs& a, int box_rows) {
   // codes [num_blocks * Hkv, bs, D]: a box is box_rows tokens, every channel,
@@ -951,8 +924,8 @@ cudaError_t attn_q8_prepare() {
 
 size_t attn_q8_workspace(const ts_attn_params* p) {
   const Runs r = plan_runs(p);
-  if (few_rows(p->N, p->Hq / p->Hkv, p->D)) return 256 + few_o_bytes(r, p->D) + few_lse_bytes(r);
-  return 256 + part_o_bytes(r, p->D) + part_ls_bytes(r) + round256(part_f1_bytes(r));
+  const int rows = few_rows(p->N, p->Hq / p->Hkv, p->D) ? FEW_ROWS : ROW_TILE;
+  return 256 + part_o_bytes(r, rows, p->D) + part_lse_bytes(r, rows);
 }
 
 cudaError_t launch_attn_q8(const AttnQ8Args& q, const ts_attn_params* p, void* workspace, cudaStream_t s) {
@@ -962,11 +935,8 @@ cudaError_t launch_attn_q8(const AttnQ8Args& q, const ts_attn_params* p, void* w
   t.kv_scale = q.kv_scale;
   t.runs = plan_runs(p);
   char* ws = static_cast<char*>(workspace) + 256;
-  t.part_o = reinterpret_cast<__half*>(ws);
-  t.part_ls = reinterpret_cast<float2*>(ws + part_o_bytes(t.runs, a.D));
-  t.part_f1 = reinterpret_cast<float*>(ws + part_o_bytes(t.runs, a.D) + part_ls_bytes(t.runs));
-  t.few_o = reinterpret_cast<float*>(ws);
-  t.few_lse = reinterpret_cast<float*>(ws + few_o_bytes(t.runs, a.D));
+  t.part_o = reinterpret_cast<float*>(ws);
+  t.part_lse = reinterpret_cast<float*>(ws + part_o_bytes(t.runs, few_rows(a.N, a.G, a.D) ? FEW_ROWS : ROW_TILE, a.D));
   t.box_rows = KV_TILE;
   while (a.bs % t.box_rows != 0) t.box_rows >>= 1;
   t.nodes_per_tile = ROW_TILE / a.G;

@@ -34,11 +34,9 @@ struct Runs {
 struct Q8Args {
   AttnArgs a;
   const uint8_t* kv_scale;
-  __half* part_o;    // [2 n, 128, D]: parts of chains, normalised, times a row's 1 / part_ls.y
-  float2* part_ls;   // [2 n, 128]: base-2 log-sum-exp, and the factor of channels below D/2
-  float* part_f1;    // [2 n, 128]: the factor of the others
-  float* few_o;      // [2 n, FEW_ROWS, D]: parts of chains of few rows, normalised
-  float* few_lse;    // [2 n, FEW_ROWS]
+  // Parts of chains, rows being 128 here and FEW_ROWS in attn_q8_few.cu.
+  float* part_o;     // [2 n, rows, D]: normalised
+  float* part_lse;   // [2 n, rows]: base-2 log-sum-exp
   int box_rows, nodes_per_tile, units, n_tree;
   int out32;
   FastDiv fd_units, fd_hkv, fd_bs, fd_g;

@@ -510,8 +510,8 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           a.out[orow * D + t] = __float2bfloat16_rn(y);
           if (t == 0 && a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
         } else {
-          args.few_o[((size_t)slot_out * FEW_ROWS + r) * D + t] = y;
-          if (t == 0) args.few_lse[slot_out * FEW_ROWS + r] = lse2;
+          args.part_o[((size_t)slot_out * FEW_ROWS + r) * D + t] = y;
+          if (t == 0) args.part_lse[slot_out * FEW_ROWS + r] = lse2;
         }
       }
       // all have read O, the sums and this segment's scales before the next one's
@@ -572,7 +572,7 @@ k_merge_q8_few(const __grid_constant__ Q8Args args) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p0 = c; p0 <= last; p0 += 32) {
     const int p = p0 + lane, slot = 2 * p + (p == c && runs.chain[c] != chain ? 1 : 0);
-    const float lse = p <= last ? args.few_lse[(size_t)slot * FEW_ROWS + r] : NEG_INF;
+    const float lse = p <= last ? args.part_lse[(size_t)slot * FEW_ROWS + r] : NEG_INF;
     float top = lse;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -587,7 +587,7 @@ k_merge_q8_few(const __grid_constant__ Q8Args args) {
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const int si = __shfl_sync(0xffffffffu, slot, i);
-      const float4 o = reinterpret_cast<const float4*>(args.few_o + ((size_t)si * FEW_ROWS + r) * FEW_D)[lane];
+      const float4 o = reinterpret_cast<const float4*>(args.part_o + ((size_t)si * FEW_ROWS + r) * FEW_D)[lane];
       den += wi;
       if (wi != 0.f) acc = make_float4(fmaf(o.x, wi, acc.x), fmaf(o.y, wi, acc.y), fmaf(o.z, wi, acc.z), fmaf(o.w, wi, acc.w));
     }
