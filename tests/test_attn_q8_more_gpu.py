@@ -35,7 +35,7 @@ def test_a_tensor_on_the_host_is_refused(name):
     torch.cuda.synchronize()
 
 
-def _call(case, pools, mask=None):
+def _call(case, pools, mask=None, scale=0.0):
     """out and lse [B, N, Hq, ..] of one call on the case's queries over the given pools."""
     import oracle
     import tree_attention_speculative_gb300 as ts
@@ -48,7 +48,7 @@ def _call(case, pools, mask=None):
     status = torch.zeros(case.B, dtype=torch.int32, device="cuda")
     kc, vc, sc = codes_dev(pools[0]), codes_dev(pools[1]), torch.from_numpy(pools[2]).cuda()
     p = ts.attn_params(t["q"], kc, vc, t["block_table"], t["prefix_len"], case.prefix_len, t["k_tree"], t["v_tree"], anc,
-                       None, out, lse, status)
+                       None, out, lse, status, scale=scale)
     ws = torch.zeros(ts.tree_attn_q8_workspace_size(p), dtype=torch.uint8, device="cuda")
     ts.tree_attn_fwd_q8(p, sc, ws)
     assert status.cpu().tolist() == [0] * case.B
@@ -98,4 +98,21 @@ def test_channels_far_apart_across_the_parts_of_a_chain(B, N, Hq, D, P):
     case.v_tree = W.bf16_bits(t.astype(np.float32))
     pools = quantised_pools(case)
     out, lse = _call(case, pools)
+    check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())
+
+
+@pytest.mark.parametrize("N,Hq,D", [(8, 4, 128), (30, 2, 64), (2, 4, 128)])
+@pytest.mark.parametrize("scale", [1e-3, 1e-9, 1e-30, 1e-42])
+def test_queries_and_scales_that_leave_no_logit(N, Hq, D, scale):
+    """Zero and tiny queries, and softmax scales whose product with theirs is below fp32's range:
+    every key weighs the same, and masked ones nothing."""
+    import oracle
+    from tests.test_attn_q8_gpu import check
+    case = W.build_case("flat", 9, W.tree_chain(N), [0, 77, 500], Hq=Hq, Hkv=1, D=D, bs=16, permute=False)
+    case.q[:, 0] = 0
+    q = oracle.attention.bf16_to_f64(case.q[:, 1]) * 2.0 ** -120
+    case.q[:, 1] = W.bf16_bits(q.astype(np.float32))
+    case.scale = float(np.float32(scale))
+    pools = quantised_pools(case)
+    out, lse = _call(case, pools, scale=scale)
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())

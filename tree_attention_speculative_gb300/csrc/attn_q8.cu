@@ -434,7 +434,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
         const int s = q8_scale_byte(m);
         const float inv = pow2_of(254 - s);
         // an infinite query has no finite logits
-        row_scale = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
+        row_scale = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : fmaxf(pow2_of(s) * a.scale_log2, LEAST);
 #pragma unroll 1
         for (int h = 0; h < C::HALVES; ++h) {
           uint8_t* piece = sm.q + h * (ROW_TILE * 128) + ct * 128;

@@ -19,6 +19,9 @@ constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, CONVERT_WARP0 = 
 constexpr int NVB = 2;       // widened V tiles
 constexpr int SLOT = 16384;  // a ring slot: 128 tokens of 128 codes, or a 64-column half of a bf16 tree tile
 constexpr float NEG_INF = -INFINITY;
+// fp32's least magnitude.  No row's factor is less, whatever its query and the scale:
+// the logits of masked keys, -inf, times 0 would be NaN.
+constexpr float LEAST = 1.401298464324817e-45f;
 // Units of N * G up to FEW_ROWS rows with heads of 128 go to attn_q8_few.cu.
 constexpr int FEW_ROWS = 8;
 

@@ -274,7 +274,7 @@ k_attn_q8_few(const __grid_constant__ Q8Args args, const __grid_constant__ CUten
           *reinterpret_cast<uint4*>(to + FEW_ROWS * 128) = make_uint4(0, 0, 0, 0);
           // an infinite query has no finite logits
           if (qc == 0) {
-            sm.row_scale[sg & 3][qr] = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2_of(s) * a.scale_log2;
+            sm.row_scale[sg & 3][qr] = m == 0x7f80u ? __uint_as_float(0x7fffffffu) : fmaxf(pow2_of(s) * a.scale_log2, LEAST);
             sm.anc[sg & 3][qr] = anc;
           }
         }
