@@ -116,3 +116,26 @@ def test_queries_and_scales_that_leave_no_logit(N, Hq, D, scale):
     pools = quantised_pools(case)
     out, lse = _call(case, pools, scale=scale)
     check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())
+
+
+@pytest.mark.parametrize("N,Hq,D", [(8, 4, 128), (30, 2, 64), (2, 4, 128), (7, 1, 128)])
+@pytest.mark.parametrize("P", [1000, 9000])
+def test_outputs_are_divided_by_the_sum_of_the_rounded_weights(N, Hq, D, P):
+    """One key of the prefix weighs 2^20 (1 + 0.97 / 256) times any other, which bf16 rounds down by
+    nearly half a step.  Every value is 1.875, so the output is, whatever the weights; divided by the
+    sum of the unrounded ones it would be a step of bf16 less.  (Chunks whose rounding is not counted
+    hold less than 2^-6 of the weight: 2^-14 of the output, and a half step is 2^-9 of 1.875.)"""
+    at = [300 + 7 + 65 * i if P == 1000 else P - 1 - 331 * i for i in range(10)]  # both halves, odd and even tiles
+    case = W.build_case("rounded", 9, W.tree_chain(N), [P] * len(at), Hq=Hq, Hkv=1, D=D, bs=16, permute=False)
+    for x, v in ((case.q, 0), (case.k_cache, 0), (case.k_tree, 0), (case.v_cache, 0x3FF0), (case.v_tree, 0x3FF0)):
+        x[...] = v
+    case.q[..., 0] = 0x3F80
+    for b, t in enumerate(at):
+        case.k_cache[case.block_table[b, t // 16], 0, t % 16, 0] = 0x4100  # 8.0; the other keys 0
+    weight = 2.0 ** 20 * (1 + 0.97 / 256)
+    bf16 = lambda x: float(torch.tensor(x, dtype=torch.float64).bfloat16())  # noqa: E731
+    assert bf16(bf16(weight) / weight * 1.875) != 1.875
+    out, lse = _call(case, quantised_pools(case), scale=float(np.log(weight) / 8))
+    assert (out == 1.875).all()
+    want = np.log(weight + P - 1 + np.arange(1, N + 1))
+    assert (np.abs(lse.double().cpu().numpy() - want[None, :, None]) <= 2.0 ** -17 * want.max()).all()
