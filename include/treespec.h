@@ -582,10 +582,23 @@ TS_API ts_status tree_commit_accepted_q8(const void* k_tree, const void* v_tree,
  * tree_attn_fwd_q8 — tree_attn_fwd over the 8-bit cache.  Takes the same
  * parameter block, with p->k_cache and p->v_cache the e4m3 pools, and the
  * pools' scale bytes; the tree's own k_tree and v_tree are bf16.  The prefix
- * keys and values are the rows' values, exactly; logits, softmax and output
- * sums are fp32.
- * Values past bf16's largest (255 * 2^120; only rows within 3% of it, or with
- * an infinity, hold any) read as infinite.
+ * keys and values are the rows' values; logits, softmax statistics and output
+ * sums are fp32.  Held in fewer bits on the way:
+ *   - the softmax weights, bf16 in the product with the values (half a step,
+ *     2^-8 of each at most), as in tree_attn_fwd.  Outputs are divided by the
+ *     sum of the rounded weights wherever these outweigh the keys before them;
+ *     lse is that of the unrounded ones;
+ *   - a query scored against the prefix, the sum of two e4m3 terms: exact for
+ *     channels down to 2^-9 of its largest, and to 2^-17 of the largest below.
+ * Ranges: a value past bf16's largest (255 * 2^120; only rows within 3% of it,
+ * or with an infinity, hold any) reads as infinite, and one below 2^-130 is
+ * rounded to a multiple of 2^-133.  Weights may reach 2^40 before the sums are
+ * scaled down, so the output of a channel with a value past
+ * 2^87 / (P_b + N) may be infinite; a key with a magnitude past 2^110 may make
+ * its logits NaN.
+ * Calls repeat bit for bit.  A row's bits follow its own query, the keys and
+ * values it sees, and how the plan cuts the prefixes (which follows every
+ * sequence's prefix_len_host), and no other row's data.
  * A row that sees no key (no prefix and an empty mask row) gives zeros and an
  * lse of -inf.  The prefix's rows must be as the writers store them.  A node that
  * no row sees (the padding of a smaller tree) may hold anything, and so may the

@@ -139,3 +139,49 @@ def test_outputs_are_divided_by_the_sum_of_the_rounded_weights(N, Hq, D, P):
     assert (out == 1.875).all()
     want = np.log(weight + P - 1 + np.arange(1, N + 1))
     assert (np.abs(lse.double().cpu().numpy() - want[None, :, None]) <= 2.0 ** -17 * want.max()).all()
+
+
+@pytest.mark.parametrize("N", [1, 9])
+def test_values_of_the_smallest_scales(N):
+    """One prefix token takes all the weight: its V row as bf16, whose smallest step is 2^-133."""
+    import oracle
+    scales = [1, 2, 3, 4]
+    codes = np.arange(256, dtype=np.uint8).reshape(2, 128)
+    codes = np.where((codes & 0x7F) == 0x7F, 0, codes)
+    case = W.build_case("small", 3, W.tree_chain(N), [1] * 8, Hq=1, Hkv=1, D=128, bs=16, permute=False)
+    case.q[:], case.k_tree[:] = 0x3F80, 0xC1A0          # 1.0 and -20: logits of -226 for the nodes
+    pools = [np.full(case.k_cache.shape, 0x38, np.uint8), np.zeros(case.v_cache.shape, np.uint8),
+             np.full(case.v_cache.shape[:3] + (2,), 127, np.uint8)]
+    want = np.empty((8, 128))
+    for b in range(8):
+        blk = case.block_table[b, 0]
+        pools[1][blk, 0, 0], pools[2][blk, 0, 0, 1] = codes[b % 2], scales[b // 2]
+        want[b] = oracle.cache_q8.values(codes[b % 2][None], np.array([scales[b // 2]], np.uint8))[0]
+    out, _ = _call(case, pools)
+    want = np.round(want * 2.0 ** 133) * 2.0 ** -133    # (np.round: halves to even)
+    np.testing.assert_array_equal(out.double().cpu().numpy()[:, 0, 0], want)
+
+
+@pytest.mark.parametrize("N,Hq,D", [(8, 4, 128), (30, 2, 64), (2, 4, 128)])
+def test_the_largest_values_and_keys(N, Hq, D):
+    """Values up to 2^87 / (P + N) under weights that pass 2^37, and keys up to 2^110."""
+    import oracle
+    from tests.test_attn_q8_gpu import check
+    f64 = oracle.attention.bf16_to_f64
+    P = 1000
+    case = W.build_case("large", 9, W.tree_chain(N), [P], Hq=Hq, Hkv=1, D=D, bs=16, permute=False)
+    top = 2.0 ** (87 - 11)
+    for name in ("v_cache", "v_tree"):
+        x = np.minimum(np.abs(f64(getattr(case, name))) / 4, 1.0) * top
+        setattr(case, name, W.bf16_bits(x.astype(np.float32)))
+    case.q[:], case.k_tree[:], case.k_cache[:] = 0x3F80, 0, 0
+    late = np.arange(200, P)                            # their logits: 26
+    case.k_cache[case.block_table[0, late // 16], 0, late % 16] = W.bf16_bits(np.float32([26.0 / (D * case.scale)]))[0]
+    out, lse = _call(case, quantised_pools(case))
+    check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())
+    case = W.build_case("large", 9, W.tree_chain(N), [P], Hq=Hq, Hkv=1, D=D, bs=16, permute=False)
+    for name, e in (("k_cache", 107), ("k_tree", 107), ("q", -107)):
+        x = np.clip(f64(getattr(case, name)), -8, 8) * 2.0 ** e
+        setattr(case, name, W.bf16_bits(x.astype(np.float32)))
+    out, lse = _call(case, quantised_pools(case))
+    check(case, out.double().cpu().numpy(), lse.double().cpu().numpy())

@@ -8,8 +8,9 @@
 //
 // Keys stay 8-bit.  q . k is taken on e4m3 tensor operands with q split in
 // two: with the row of q scaled by a power of two to within 448, hi = e4m3(q)
-// and lo = e4m3(q - hi) hold all 8 bits of a bf16 significand, exactly for
-// channels down to 2^-10 of the row's largest and to 2^-18 of it below that.
+// and lo = e4m3(q - hi) hold all 8 bits of a bf16 significand: exactly down to
+// 2^-2, 2^-9.8 of the row's largest, which is past 224, and below that to half of
+// lo's last step of 2^-9, 2^-17.8 of it.
 // S = hi . k + lo . k then costs as many MMA cycles as bf16 (e4m3 runs at twice
 // its rate) and the keys need no conversion; the key's power of two and the
 // row's multiply the logits in fp32.
