@@ -88,6 +88,7 @@ class TreeVerifyStep:
         self.lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev)
         self.ws_attn = None
         self.ws_attn_q8 = None  # of its own: a captured bf16 call keeps the other
+        self.outgrown = []  # workspaces that grew too small: captured calls still write to them
         self.rope = rope
         if rope is not None:
             self.q_rot = torch.empty(B, N, Hq, D, dtype=torch.bfloat16, device=dev)
@@ -128,6 +129,9 @@ class TreeVerifyStep:
         name = "ws_attn" if kv_scale is None else "ws_attn_q8"
         ws = getattr(self, name)
         if ws is None or ws.numel() < need:
+            if ws is not None:
+                self.outgrown.append(ws)
+                need = max(need, 2 * ws.numel())  # so that what is kept stays below the one in use
             # zero-filled once; every call leaves its head (the item counter) zero again
             ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
             setattr(self, name, ws)
