@@ -178,21 +178,32 @@ k_rope_pairs(const __grid_constant__ RopeArgs a, FastDiv heads) {
   }
 }
 
+// a / b rounded up, for every a >= 1 (ceil_div's a + b - 1 passes 2^31 for the last few a).
+constexpr int rope_ceil_div(int a, int b) { return (a - 1) / b + 1; }
+
+// Tokens a CTA: enough for an item a thread, but no fewer CTAs than SMs (300
+// tokens of 3 heads of 64: 2.4 us, without that 2.7).
+// 16384 tokens of 9 heads of 128: 16.8 us (one token a CTA 20.1); of 2 heads of
+// 64: 6.4 us (one token a CTA 17.2).
+constexpr int rope_tokens_a_cta(int tokens, int items_a_token) {
+  int tok = rope_ceil_div(ROPE_THREADS, items_a_token);
+  const int spread = rope_ceil_div(tokens, PLAN_SMS);
+  if (tok > spread) tok = spread;
+  return tok < ROPE_MAX_TOK ? tok : ROPE_MAX_TOK;
+}
+// The most tokens a call takes, and the fewest.
+static_assert(rope_tokens_a_cta(0x7fffffff, 4) == ROPE_MAX_TOK && rope_tokens_a_cta(0x7fffffff, 8192 * 64) == 1, "");
+static_assert(rope_ceil_div(0x7fffffff, ROPE_MAX_TOK) == 1 << 27 && rope_ceil_div(0x7fffffff, 1) == 0x7fffffff, "");
+static_assert(rope_tokens_a_cta(1, 4) == 1 && rope_tokens_a_cta(300, 12) == 2, "");
+
 }  // namespace
 
 cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   const int heads = a.Hq + a.Hkv;
   const bool vec = a.R % 16 == 0;
-  // Tokens a CTA: enough for an item a thread, but no fewer CTAs than SMs (300
-  // tokens of 3 heads of 64: 2.4 us, without that 2.7).
-  // 16384 tokens of 9 heads of 128: 16.8 us (one token a CTA 20.1); of 2 heads of
-  // 64: 6.4 us (one token a CTA 17.2).
   const int per = vec ? a.D / 16 : a.D / 2;
-  int tok = ceil_div(ROPE_THREADS, heads * per);
-  const int spread = ceil_div(a.tokens, PLAN_SMS);
-  if (tok > spread) tok = spread;
-  a.tok = tok < ROPE_MAX_TOK ? tok : ROPE_MAX_TOK;
-  const dim3 grid(ceil_div(a.tokens, a.tok));
+  a.tok = rope_tokens_a_cta(a.tokens, heads * per);
+  const dim3 grid(rope_ceil_div(a.tokens, a.tok));
   // Threads: the items of a CTA in whole rounds (576 items of 72 heads of 128:
   // 192 threads, 26.1 us for 4096 tokens; 256 threads, 27.1 us).
   const int items = a.tok * heads * per;
