@@ -477,8 +477,9 @@ TS_API ts_status tree_verify_greedy_forest(const int32_t* draft_tokens, const fl
  * a = pos * f'_i, each pair (x, y) of a head becomes
  *     mscale * (x cos a - y sin a,  y cos a + x sin a);
  * the pair is channels (i, i + R/2), or (2i, 2i + 1) with interleaved; channels
- * R .. D-1 are copied.  The angle is exact to 2^-31 of a turn for every int32
- * position; sums are fp32, rounded once to bf16.  f' by `scaling`:
+ * R .. D-1 are copied.  Sums are fp32, rounded once to bf16.  The angle is
+ * within 2^-25 of a turn at positions up to 2^28 and 2^-23 at any (f' up to one
+ * radian a position).  f' by `scaling`:
  *     TS_ROPE_NONE    f
  *     TS_ROPE_LINEAR  f / factor
  *     TS_ROPE_NTK     f of theta * factor^(R/(R-2))   (R = 2: f)

@@ -306,8 +306,8 @@ struct CommitQ8Args {
 };
 cudaError_t launch_commit_q8(const CommitQ8Args& a, cudaStream_t s);
 
-// Tree attention over that cache: AttnArgs whose k_cache and v_cache point at
-// the codes.
+// Tree attention over that cache.  a.k_cache and a.v_cache are null: the pools
+// are the codes.
 struct AttnQ8Args {
   AttnArgs a;
   const uint8_t* k_codes;

@@ -7,9 +7,11 @@
 //
 // The angle.  Only its fraction of a turn matters, and p is whole, so the host
 // passes f_i / (2 pi) as a 64-bit fixed-point fraction F_i of a turn and the
-// kernel takes p * F_i modulo 2^64: the turns drop out by themselves and what
-// is left is exact to 2^-33 turns for every 32-bit p (a product in fp32 would
-// be off by whole radians past p = 2^24).  sincospif then takes the fraction.
+// kernel takes p * F_i modulo 2^64: the turns drop out by themselves (a product
+// in fp32 would be off by whole radians past p = 2^24).  The fraction that is
+// left goes to sincospif in fp32, within 2^-26 of a turn.  F_i comes from
+// doubles and is off by up to 2^-55.2 (f_i up to 1; theta from 1e4 to 1e7 against
+// 70 digits), p times that in the angle: 2^-24.2 of a turn at p = 2^31.
 //
 // Memory-bound: every value is read and written once, 3 flops each.  A CTA
 // takes whole tokens: its R/2 sines and cosines a token are computed once,
