@@ -188,32 +188,43 @@ __device__ __noinline__ float rounded_sum(uint32_t a, uint32_t b, uint32_t c, ui
   return s0 + s1;
 }
 
-// D/2 channels of a row, its two O joined (zeros for a row that saw nothing,
-// whatever its O holds): fp32 to `part`, or bf16 to `out`.  Out of line, so that
-// the tiles' code stays small.
+// Columns [c, c + 32) of a row, the two halves' O joined (zeros for a row that
+// saw nothing, whatever its O holds).
+__device__ __forceinline__ void join_o(uint32_t o_tmem, int c, float f0, float f1, uint32_t (&u)[32]) {
+  uint32_t v[32];
+  tmem_ld32(o_tmem + c, u);
+  tmem_ld32(o_tmem + O_STRIDE + c, v);
+  tmem_ld_wait();
+  reg_fence32(u);
+  reg_fence32(v);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const float p = f0 == 0.f ? 0.f : __uint_as_float(u[e]) * f0;
+    u[e] = __float_as_uint(f1 == 0.f ? p : fmaf(__uint_as_float(v[e]), f1, p));
+  }
+}
+// D/2 channels of a row, fp32 to a part or bf16 to the output.  A loop each: one
+// for both made the loop over the tiles slower (heads of 64, 64 sequences of 8K
+// tokens: 972 us, out of line 1173; 16 prefixes of 1-16K, heads of 128: 91, in
+// line 100).
 template <int D>
-__device__ __noinline__ void store_row(uint32_t o_tmem, float f0, float f1, float* part, __nv_bfloat16* out, bool active,
-                                       int out32) {
+__device__ __forceinline__ void store_part(uint32_t o_tmem, float f0, float f1, float* part, bool active) {
 #pragma unroll 1
   for (int c = 0; c < D / 2; c += 32) {
-    uint32_t u[32], v[32];
-    tmem_ld32(o_tmem + c, u);
-    tmem_ld32(o_tmem + O_STRIDE + c, v);
-    tmem_ld_wait();
-    reg_fence32(u);
-    reg_fence32(v);
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float p = f0 == 0.f ? 0.f : __uint_as_float(u[e]) * f0;
-      u[e] = __float_as_uint(f1 == 0.f ? p : fmaf(__uint_as_float(v[e]), f1, p));
-    }
+    uint32_t u[32];
+    join_o(o_tmem, c, f0, f1, u);
     if (!active) continue;
-    if (part) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) st_global_v8(part + c + 8 * q, u + 8 * q);
-      continue;
-    }
-    uint32_t w[16];
+    for (int q = 0; q < 4; ++q) st_global_v8(part + c + 8 * q, u + 8 * q);
+  }
+}
+template <int D>
+__device__ __forceinline__ void store_out(uint32_t o_tmem, float f0, float f1, __nv_bfloat16* out, int out32, bool active) {
+#pragma unroll 1
+  for (int c = 0; c < D / 2; c += 32) {
+    uint32_t u[32], w[16];
+    join_o(o_tmem, c, f0, f1, u);
+    if (!active) continue;
 #pragma unroll
     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
     if (out32) {
@@ -655,7 +666,7 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
             if (__any_sync(0xffffffffu, sum > l_run)) {  // (the warp goes together; a row adds its own chunks' only)
               const float more = rounded_sum(pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7], pk[8], pk[9], pk[10],
                                              pk[11], pk[12], pk[13], pk[14], pk[15]) - sum;
-              if (sum > l_run) excess += more;
+              excess += sum > l_run ? more : 0.f;
             }
             l_run += sum;
             tmem_st16(s_tmem + c * 16, pk);
@@ -692,13 +703,14 @@ k_attn_q8(const __grid_constant__ Q8Args args, const __grid_constant__ CUtensorM
       if (I.n_tiles == 0) {
         if (active && half == 0) args.part_lse[(size_t)slot * ROW_TILE + r] = NEG_INF;
       } else if (busy) {
-        if (active && half == 0) {
-          if (!I.whole) args.part_lse[(size_t)slot * ROW_TILE + r] = lse2;
-          else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
+        const uint32_t o_row = tmem + lane_base + TMEM_O + half * (D / 2);
+        if (I.whole) {
+          if (active && half == 0 && a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
+          store_out<D>(o_row, f0, f1, a.out + orow * D + half * (D / 2), args.out32, active);
+        } else {
+          if (active && half == 0) args.part_lse[(size_t)slot * ROW_TILE + r] = lse2;
+          store_part<D>(o_row, f0, f1, args.part_o + ((size_t)slot * ROW_TILE + r) * D + half * (D / 2), active);
         }
-        float* part = args.part_o + ((size_t)slot * ROW_TILE + r) * D + half * (D / 2);
-        __nv_bfloat16* out = a.out + orow * D + half * (D / 2);
-        store_row<D>(tmem + lane_base + TMEM_O + half * (D / 2), f0, f1, I.whole ? nullptr : part, out, active, args.out32);
       }
       // both halves have read O, and each other's sums, before the next segment's first P
       tc_fence_before();
