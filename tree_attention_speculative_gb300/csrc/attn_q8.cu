@@ -21,15 +21,17 @@
 //
 // What bounds it.  Bytes: 2 D + 2 a token and KV head, half of bf16: a 128-token
 // tile is 32.5 KB, 0.73 us of one SM's share of HBM.  Its products take 1024 MMA
-// cycles (0.5 us).  What it takes is 1.25 us, the issue slots of the four SM
-// partitions: softmax and widening alone, without a product or a barrier, take
-// 0.7 us of them (a probe of the two loops), and beside the tensor cores each
-// warp runs at about half its lone rate.  So the loops are kept short (a
-// larger kernel fetches its instructions more slowly than it runs them), no
-// maximum is taken in the common case, and the scale bytes arrive by
-// asynchronous copies.  16 prefixes of 1-16K tokens, 26 nodes: 94 us (3.1 TB/s);
-// 64 x 8K tokens with 512 rows a unit: 1.12 ms (0.98 PFLOP/s); 4 x 128K with
-// 768 rows: 1.59 ms.  Units of up to 8 rows go to attn_q8_few.cu.
+// cycles (0.5 us).  It takes 1.25 us, and no unit is full: 59-64 % of the issue
+// slots, the tensor pipe 37-43 %, shared memory 37-43 %, DRAM 42 % (15 % where the
+// products are the most).  What a tile waits for is its chain of stages, S,
+// softmax, widening, P V, each of one or two warps a partition that mostly wait
+// for their own last instruction or load.  So the loops are kept short (a larger
+// kernel fetches its instructions more slowly than it runs them), no maximum is
+// taken in the common case, and the scale bytes arrive by asynchronous copies.
+// 16 prefixes of 1-16K tokens, 26 nodes: 91 us (3.2 TB/s); 64 x 8K tokens with 512
+// rows a unit: 1.09 ms (1.01 PFLOP/s); 4 x 128K with 768 rows: 1.57 ms; heads of
+// 64: 84 us, 0.97 ms and (one node of 32 heads, 32 prefixes of 0-8K) 81 us.  Units
+// of up to 8 rows of heads of 128 go to attn_q8_few.cu.
 //
 // Work split.  A chain is one row tile of one unit: its tree tiles, then its
 // prefix tiles.  The host lays all chains end to end, row tile by row tile, and
@@ -90,7 +92,7 @@ constexpr int NT = 4;   // tiles' key scales in flight
 // weight that outweighs the others cancels: with hot keys the outputs are then as
 // exact as their own rounding lets them be.  What rounding adds to the sum is
 // taken for the chunks of 32 keys that weigh more than all before them (64
-// sequences of 8K tokens: 1120 us; for every chunk 1260, for none 1071).
+// sequences of 8K tokens: 1086 us; for every chunk 1218).
 // A row keeps the reference m it took from its first keys until the weights of
 // 32 keys sum past RESCALE_SUM.  bf16 P, fp32 sums and O have the same precision
 // at every magnitude, so weights up to 2^40 are as good as weights up to 1, and
@@ -808,15 +810,15 @@ k_merge_q8(const __grid_constant__ Q8Args args) {
 // The runs.  A chain weighs its prefix tiles and `head` more: its tree tiles,
 // Q tile and epilogue.
 // SEG_COST: a segment's start and end in tiles' worth of time (32 sequences of
-// 0-8K tokens, one node each, before attn_q8_few.cu: 85 us; with 3, 92 us; with
-// it: 63 us; with 3, 69 us).
+// 0-8K tokens, one node each: 64 us; with 3, 70 us; 16 of 1-16K, 26 nodes: 91 us;
+// with 3, 93 us).
 constexpr int SEG_COST = 5;
 // No CTA for less weight than this: more of them leave more parts to merge (one
-// sequence of 1K tokens, 8 KV heads: 16.6 us; with 6, 20.2, with 12, 18.2; of 4K
-// tokens: 20.9 us; with 3, 22.3, with 6, 22.0).
+// sequence of 1K tokens, 8 KV heads: 16.7 us; with 3 the same, with 6, 20.3, with
+// 12, 23.9; of 4K tokens: 20.8 us; with 3, 22.3, with 6, 22.2, with 12, 27.3).
 constexpr int MIN_RUN = 4;
 // Where every chain weighs this at most and has an SM, none is cut: the merge
-// costs more than it saves (16 sequences of 512 tokens: 15.1 us, cut 18.5).
+// costs more than it saves (16 sequences of 512 tokens: 15.1 us, cut 18.2).
 constexpr int WHOLE = 12;
 constexpr int SLIVER = 2;  // no part of fewer tiles: it would cost a segment's start and end
 

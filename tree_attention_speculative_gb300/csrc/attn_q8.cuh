@@ -22,7 +22,9 @@ constexpr float NEG_INF = -INFINITY;
 // fp32's least magnitude.  No row's factor is less, whatever its query and the scale:
 // the logits of masked keys, -inf, times 0 would be NaN.
 constexpr float LEAST = 1.401298464324817e-45f;
-// Units of N * G up to FEW_ROWS rows with heads of 128 go to attn_q8_few.cu.
+// Units of N * G up to FEW_ROWS rows with heads of 128 go to attn_q8_few.cu, which
+// says how the two forms compare.  Its channels are the 128 MMA rows of O, so heads
+// of 64 stay with attn_q8.cu.
 constexpr int FEW_ROWS = 8;
 
 // The CTAs' runs: CTA c starts at tile tile[c] of chain chain[c] and ends where
@@ -86,8 +88,8 @@ struct Ctl {
 };
 // Bounded waits that also give up as soon as another role has aborted.  The
 // polling is out of line: inlined at some twenty places, with the clock and the
-// flag, it made the kernel half as large again, and the warps at work waited for
-// instructions (1.37 against 1.16 ms on 64 sequences of 8K tokens).
+// flag, it makes the kernel half as large again, and the warps at work wait for
+// instructions (1.40 against 1.09 ms on 64 sequences of 8K tokens).
 static __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* flag, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {

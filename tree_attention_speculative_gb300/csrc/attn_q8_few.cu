@@ -20,14 +20,15 @@
 // log-sum-exp, and as rounded, for the output, where the error of a weight that
 // outweighs the others then cancels.  (With what bf16 leaves of them in the eight
 // idle columns of P^T the outputs had their own rounding alone, but 32 single
-// nodes took 74 us; without the second sum 61 us.)
+// nodes took 74 us, against 61 without either.)
 //
 // What bounds it: bytes of codes, 32.5 KB a tile and SM (0.73 us of its share
 // of HBM), and where sequences are short a segment's start and end (about 5 us:
 // the split queries, the tree's tile, the join).  32 sequences of 0-8K tokens,
-// one node of 32 heads on 8: 65 us (3.9 TB/s; the other form 85); 256 of 4K:
-// 450 us (4.8 TB/s; 579).  Not beyond 8 rows: with 16 a thread's registers and
-// instructions double, and 16 prefixes of 1-16K took 105 us against 85.
+// one node of 32 heads on 8: 64 us (3.9 TB/s; the other form 88), in blocks of 16
+// tokens 72 (88); of 64 heads on 8, 74 us (89); 256 of 4K: 439 us (4.9 TB/s; 582).
+// Not beyond 8 rows: with 16 a thread's registers and instructions double, and 16
+// prefixes of 1-16K took 105 us against the other form's 85 of that time.
 //
 // Warps: 0-3 as in attn_q8.cu; 4-11 widen values (half a token's channels a
 // thread) and split the queries; 12-19 softmax.
