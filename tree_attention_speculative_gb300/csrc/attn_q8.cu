@@ -30,7 +30,7 @@
 // taken in the common case, and the scale bytes arrive by asynchronous copies.
 // 16 prefixes of 1-16K tokens, 26 nodes: 91 us (3.2 TB/s); 64 x 8K tokens with 512
 // rows a unit: 1.09 ms (1.01 PFLOP/s); 4 x 128K with 768 rows: 1.57 ms; heads of
-// 64: 84 us, 0.97 ms and (one node of 32 heads, 32 prefixes of 0-8K) 81 us.  Units
+// 64: 81 us, 0.96 ms and (one node of 32 heads, 32 prefixes of 0-8K) 77 us.  Units
 // of up to 8 rows of heads of 128 go to attn_q8_few.cu.
 //
 // Work split.  A chain is one row tile of one unit: its tree tiles, then its
@@ -207,13 +207,14 @@ __device__ __forceinline__ void join_o(uint32_t o_tmem, int c, float f0, float f
 }
 // D/2 channels of a row, fp32 to a part or bf16 to the output.  A loop each: one
 // for both made the loop over the tiles slower (heads of 64, 64 sequences of 8K
-// tokens: 972 us, out of line 1173; 16 prefixes of 1-16K, heads of 128: 91, in
+// tokens: 962 us, out of line 1173; 16 prefixes of 1-16K, heads of 128: 91, in
 // line 100).
 template <int D>
 __device__ __forceinline__ void store_part(uint32_t o_tmem, float f0, float f1, float* part, bool active) {
 #pragma unroll 1
   for (int c = 0; c < D / 2; c += 32) {
     uint32_t u[32];
+    __syncwarp();  // (TMEM loads want the warp together)
     join_o(o_tmem, c, f0, f1, u);
     if (!active) continue;
 #pragma unroll
@@ -225,6 +226,7 @@ __device__ __forceinline__ void store_out(uint32_t o_tmem, float f0, float f1, _
 #pragma unroll 1
   for (int c = 0; c < D / 2; c += 32) {
     uint32_t u[32], w[16];
+    __syncwarp();  // (TMEM loads want the warp together)
     join_o(o_tmem, c, f0, f1, u);
     if (!active) continue;
 #pragma unroll
