@@ -29,8 +29,8 @@
 // kernel fetches its instructions more slowly than it runs them), no maximum is
 // taken in the common case, and the scale bytes arrive by asynchronous copies.
 // 16 prefixes of 1-16K tokens, 26 nodes: 91 us (3.2 TB/s); 64 x 8K tokens with 512
-// rows a unit: 1.09 ms (1.01 PFLOP/s); 4 x 128K with 768 rows: 1.57 ms; heads of
-// 64: 81 us, 0.96 ms and (one node of 32 heads, 32 prefixes of 0-8K) 77 us.  Units
+// rows a unit: 1.09 ms (1.01 PFLOP/s); 4 x 128K with 768 rows: 1.58 ms; heads of
+// 64: 81 us, 0.96 ms and (one node of 32 heads, 32 prefixes of 0-8K) 78 us.  Units
 // of up to 8 rows of heads of 128 go to attn_q8_few.cu.
 //
 // Work split.  A chain is one row tile of one unit: its tree tiles, then its
