@@ -26,6 +26,11 @@
  *                           an 8-bit paged cache: prompts and accepted paths
  *                           quantised as they are written, and the attention
  *                           that reads it
+ *   tree_cache_append_rope, tree_chunk_attn_fwd
+ *                           prompts and decoded tokens: appended to either cache with
+ *                           their rotary positions, and their attention over it
+ *   tree_attn_fwd_window    the tree's attention in a layer with a sliding window
+ *   tree_token_logprobs     log probabilities of tokens, entropies, alternatives
  *
  * Sources (web pages on the method):
  *   [P1] "Tree Attention", inferensys glossary.
@@ -629,6 +634,193 @@ TS_API ts_status tree_attn_fwd_q8(const ts_attn_params* p, const uint8_t* kv_sca
 TS_API ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint8_t* kv_scale, void* workspace,
                                              size_t workspace_bytes, int stall_seq, int stall_tile,
                                              uint32_t wait_limit_us, ts_stream stream);
+
+/*
+ * tree_cache_append_rope — new tokens into a paged cache, with their rotary
+ * positions applied on the way: in place of tree_rope and then
+ * tree_cache_append_q8, or of tree_rope and an append to the bf16 cache
+ * ([P1] Key Mechanisms > Speculative KV Cache Reuse: the prefix that a tree is
+ * scored against, filled by prompts and by decoded tokens).
+ *
+ * Row cu_len[b] + i of sequence b is at position p = P_b + i.  Its queries and
+ * keys turn at p as tree_rope turns them (the same angles, fp32 sums rounded once
+ * to bf16); the queries go to q_out, keys and values to token p of the sequence's
+ * cache.  With a kv_scale that is the 8-bit cache, and the rounded rows are
+ * quantised as tree_cache_append_q8 quantises them.
+ *
+ *   q              [T, Hq, D] bf16, or NULL: keys and values alone.
+ *   k, v           [T, Hkv, D] bf16.  Strides in elements, multiples of 8, token
+ *                  and head; 0 is dense.  Views of a fused projection are fine.
+ *                  k and v may be NULL when T is 0.
+ *   q_out          [T, Hq, D] bf16 out, dense.  May overlap none of the inputs.
+ *   k_cache,
+ *   v_cache        [num_blocks, Hkv, block_size, D], bf16 or with kv_scale e4m3;
+ *                  nothing of them but the tokens' rows is written.
+ *   kv_scale       [num_blocks, Hkv, block_size, 2] uint8 (the 8-bit cache) or NULL.
+ *   cu_len, prefix_len, new_prefix_len, status, block_table: as
+ *                  tree_cache_append_q8 takes them, with its errors.  Rows of q_out
+ *                  of no sequence, and of one whose status is not 0 or whose sizes
+ *                  are wrong, are left as they were.
+ *   rope           the configuration: rotary_dim, interleaved, scaling, theta,
+ *                  factor, low_rot, high_rot, orig_len and mscale of it are read
+ *                  (host memory).  NULL: nothing turns (q must be NULL).
+ * T may be 0.  No workspace.  Returns TS_ERR_NULL / TS_ERR_SHAPE /
+ * TS_ERR_UNSUPPORTED (D not 64 or 128, more than 4096 heads, a block size that is
+ * no multiple of 16, scaling) / TS_ERR_CUDA.
+ */
+typedef struct ts_append_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  uint8_t* kv_scale;
+  const int32_t* cu_len;
+  const int32_t* prefix_len;
+  const int32_t* block_table;
+  int32_t* new_prefix_len;
+  int32_t* status;
+  const ts_rope_params* rope;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  int B, T, Hq, Hkv, D;
+  int block_size, num_blocks, max_blocks;
+} ts_append_params;
+
+TS_API ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream stream);
+
+/*
+ * tree_chunk_attn_fwd — attention of each sequence's newest tokens over its paged
+ * bf16 cache, which holds them already: a prompt, a chunk of one, or a decoded
+ * token ([P2] How It Works: a token attends to what is before it and to itself;
+ * a tree's nodes are the case that tree_attn_fwd covers).
+ *
+ * With n_b = cu_len[b+1] - cu_len[b] rows and kv_b cached tokens, row cu_len[b] + i
+ * is at position p = kv_b - n_b + i and sees the tokens t <= p that are near,
+ *   window == 0,  or  t > p - window,  or  t < sinks
+ * (a window counts the token itself; sinks are the first tokens, which stay
+ * visible).  out = softmax(scale * q . k) . v over those, lse its natural-log
+ * normaliser.  Logits, statistics and output sums are fp32; the softmax weights
+ * are rounded to bf16 in the product with the values (half a step, 2^-8 of each at
+ * most), and the parts of a chain of keys that is cut between SMs are joined in
+ * fp32.  Calls repeat bit for bit.
+ *
+ *   q            [T, Hq, D] bf16; out the same, lse [T, Hq] fp32 or NULL.  Rows of
+ *                no sequence are left as they were.
+ *   k_cache, v_cache, block_table: as ts_attn_params.  Entries of blocks that no
+ *                row sees into (past kv_b, or wholly between the sinks and the
+ *                window) are not followed, and the tokens there may be anything.
+ *                A token that some rows of its sequence see must have finite values
+ *                (0 * inf is NaN in rows that it is hidden from).
+ *   cu_len       [B + 1] int32 and kv_len [B] int32 on the device, cu_len_host and
+ *                kv_len_host the same values on the host, from which the work is
+ *                cut.  0 <= n_b <= kv_b <= 2^30; n_b may be 0.  In a captured call
+ *                kv_b may have changed by the time it is replayed, and n_b become
+ *                smaller; a sequence with more rows than it was planned for, fewer
+ *                tokens than rows, rows past T or tokens past its table's row gets
+ *                TS_ERR_SHAPE and nothing written.
+ *   status       [B] int32 or NULL: errors as tree_attn_fwd (TS_ERR_BAD_BLOCK: block
+ *                0 was read in its place; TS_ERR_TIMEOUT).
+ *   scale        0 selects 1/sqrt(D).
+ *
+ * workspace: tree_chunk_attn_workspace_size(p) bytes, 256-byte aligned, its first
+ * 256 bytes zero before the first use and left zero by every call; stream-ordered
+ * calls, also of tree_attn_fwd, may share it.
+ * Returns as tree_attn_fwd, and TS_ERR_UNSUPPORTED for more than 4096 heads.
+ */
+typedef struct ts_chunk_params {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* cu_len;
+  const int32_t* kv_len;
+  const int32_t* cu_len_host;
+  const int32_t* kv_len_host;
+  void* out;
+  float* lse;
+  int32_t* status;
+  int B, T, Hq, Hkv, D;
+  int block_size, num_blocks, max_blocks;
+  float scale;
+  int window, sinks;
+} ts_chunk_params;
+
+TS_API size_t tree_chunk_attn_workspace_size(const ts_chunk_params* p);
+TS_API ts_status tree_chunk_attn_fwd(const ts_chunk_params* p, void* workspace, size_t workspace_bytes,
+                                     ts_stream stream);
+
+/*
+ * tree_chunk_attn_fwd_test — for testing only: tree_chunk_attn_fwd on at most
+ * max_ctas CTAs and, with stall_seq >= 0, that sequence's key stream stopped before
+ * tile stall_tile of each of its items, every bounded wait limited to wait_limit_us
+ * (as tree_attn_fwd_ctas_test).
+ */
+TS_API ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* workspace, size_t workspace_bytes,
+                                          int max_ctas, int stall_seq, int stall_tile, uint32_t wait_limit_us,
+                                          ts_stream stream);
+
+/*
+ * tree_attn_fwd_window — tree_attn_fwd for a layer with a sliding window: node i at
+ * position p = P_b + depth (depth: the ancestors in its mask) sees the prefix tokens
+ * t with t > p - window or t < sinks, and of the nodes in its mask the ancestors a
+ * with depth - depth_a < window or P_b + depth_a < sinks.  window >= 1.
+ * Arguments, outputs and errors are tree_attn_fwd's, over the bf16 cache; a row that
+ * sees no key gives zeros and an lse of -inf.  Blocks that no node sees into are not
+ * followed.  Nodes that no row sees may hold anything; the value of one that some
+ * rows see must be finite.  In a captured call prefix_len may have changed when it is
+ * replayed; one outside the table's row gets TS_ERR_SHAPE and nothing written.
+ * workspace: tree_attn_window_workspace_size bytes, as tree_chunk_attn_fwd's, and may
+ * be shared with it.
+ */
+TS_API size_t tree_attn_window_workspace_size(const ts_attn_params* p, int window, int sinks);
+TS_API ts_status tree_attn_fwd_window(const ts_attn_params* p, int window, int sinks, void* workspace,
+                                      size_t workspace_bytes, ts_stream stream);
+
+/*
+ * tree_token_logprobs — log probabilities of given tokens under rows of logits,
+ * the rows' entropies, and their most likely tokens: what a server returns beside
+ * the tokens that tree_verify_greedy or tree_verify_stochastic accepted, and what a
+ * prompt is scored with.
+ *
+ * For output r, with x the logits of row rows[r] (row r without rows) divided by
+ * temperature:  logprob = x[tokens[r]] - ln sum exp x,  entropy = -sum p ln p, and
+ * the `top` largest of the row, best first (equal ones by the lower index), as token
+ * ids and log probabilities.
+ *
+ *   logits        [M, V] fp32, or with `half` bf16, row_stride elements apart (0: V),
+ *                 at any alignment of their type.  Finite or -inf; a NaN or +inf makes
+ *                 its row's outputs unspecified.
+ *   tokens        [R] int32 and logprob [R] fp32 out, both or neither.  A token of -1
+ *                 gets 0; another outside [0, V) gets NaN.
+ *   rows          [R] int32 or NULL.  An output whose row is outside [0, M) is left as
+ *                 it was (all of its outputs).
+ *   entropy       [R] fp32 out or NULL.
+ *   top_ids       [R, top] int32 and top_logprobs [R, top] fp32 out, either may be
+ *                 NULL; both are with top = 0.  Tokens of probability 0 (-inf) are no
+ *                 alternatives: id -1, log probability -inf.
+ * A row of nothing but -inf gives logprob -inf, entropy 0 and no alternatives.
+ * fp32 arithmetic; outputs are within 2^-20 of max(1, |value|) or so.  Calls repeat
+ * bit for bit.
+ * R may be 0.  No workspace.  Returns TS_ERR_NULL / TS_ERR_SHAPE (temperature not
+ * positive and finite, R over M without rows) / TS_ERR_UNSUPPORTED (V over 524224,
+ * top over 32, R over 2^28) / TS_ERR_CUDA.
+ */
+typedef struct ts_logprob_params {
+  const void* logits;
+  const int32_t* tokens;
+  const int32_t* rows;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int64_t row_stride;
+  int R, M, V, top;
+  int half;
+  float temperature;
+} ts_logprob_params;
+
+TS_API ts_status tree_token_logprobs(const ts_logprob_params* p, ts_stream stream);
 
 /* Size of the library-owned scratch behind tree_verify_greedy_noalloc. */
 #define TS_VERIFY_NOALLOC_SCRATCH_BYTES ((size_t)4 << 20)

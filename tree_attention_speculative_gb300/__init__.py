@@ -10,6 +10,7 @@ the library has not been built (``__graft_entry__.build()``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -26,7 +27,9 @@ __all__ = [
     "tree_verify_greedy_noalloc", "tree_commit_accepted", "tree_verify_stochastic", "tree_build_dynamic",
     "tree_build_ancestry_forest", "tree_verify_greedy_forest", "NOALLOC_SCRATCH_BYTES",
     "RopeConfig", "tree_rope", "tree_cache_append_q8", "tree_commit_accepted_q8",
-    "tree_attn_q8_workspace_size", "tree_attn_fwd_q8", "STATUS",
+    "tree_attn_q8_workspace_size", "tree_attn_fwd_q8",
+    "tree_cache_append_rope", "ChunkParams", "chunk_params", "tree_chunk_attn_workspace_size", "tree_chunk_attn_fwd",
+    "tree_attn_window_workspace_size", "tree_attn_fwd_window", "tree_token_logprobs", "STATUS",
 ]
 
 STATUS = {
@@ -55,6 +58,7 @@ class AttnParams(ctypes.Structure):
     # what attn_params notes of the tensors, for the calls' checks
     cache_dtypes = ()
     q8_device = None
+    tensors = ()
 
 
 class RopeParams(ctypes.Structure):
@@ -67,6 +71,43 @@ class RopeParams(ctypes.Structure):
         ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
         ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low_rot", ctypes.c_double),
         ("high_rot", ctypes.c_double), ("orig_len", ctypes.c_int), ("mscale", ctypes.c_float),
+    ]
+
+
+class AppendParams(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("cu_len", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("new_prefix_len", ctypes.c_void_p), ("status", ctypes.c_void_p), ("rope", ctypes.POINTER(RopeParams)),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int), ("max_blocks", ctypes.c_int),
+    ]
+
+
+class ChunkParams(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("cu_len", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("cu_len_host", ctypes.c_void_p), ("kv_len_host", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int), ("max_blocks", ctypes.c_int),
+        ("scale", ctypes.c_float), ("window", ctypes.c_int), ("sinks", ctypes.c_int),
+    ]
+    device = None  # that of every tensor, as chunk_params found it
+
+
+class LogprobParams(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+        ("logprob", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+        ("top_logprobs", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+        ("R", ctypes.c_int), ("M", ctypes.c_int), ("V", ctypes.c_int), ("top", ctypes.c_int),
+        ("half", ctypes.c_int), ("temperature", ctypes.c_float),
     ]
 
 
@@ -103,7 +144,9 @@ EXPORTS = ("ts_status_str", "tree_build_ancestry", "tree_attn_workspace_size", "
            "tree_commit_accepted", "tree_verify_stochastic", "tree_build_dynamic", "tree_build_ancestry_forest",
            "tree_verify_greedy_forest", "tree_attn_fwd_stall_test", "tree_attn_fwd_ctas_test", "tree_rope",
            "tree_cache_append_q8", "tree_commit_accepted_q8", "tree_attn_q8_workspace_size", "tree_attn_fwd_q8",
-           "tree_attn_fwd_q8_stall_test")
+           "tree_attn_fwd_q8_stall_test", "tree_cache_append_rope", "tree_chunk_attn_workspace_size",
+           "tree_chunk_attn_fwd", "tree_chunk_attn_fwd_test", "tree_attn_window_workspace_size",
+           "tree_attn_fwd_window", "tree_token_logprobs")
 
 # TS_VERIFY_NOALLOC_SCRATCH_BYTES of treespec.h
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -166,6 +209,20 @@ def lib() -> ctypes.CDLL:
         L.tree_attn_fwd_q8.restype = i32
         L.tree_attn_fwd_q8_stall_test.argtypes = [ctypes.POINTER(AttnParams), vp, vp, sz, i32, i32, ctypes.c_uint32, vp]
         L.tree_attn_fwd_q8_stall_test.restype = i32
+        L.tree_cache_append_rope.argtypes = [ctypes.POINTER(AppendParams), vp]
+        L.tree_cache_append_rope.restype = i32
+        L.tree_chunk_attn_workspace_size.argtypes = [ctypes.POINTER(ChunkParams)]
+        L.tree_chunk_attn_workspace_size.restype = sz
+        L.tree_chunk_attn_fwd.argtypes = [ctypes.POINTER(ChunkParams), vp, sz, vp]
+        L.tree_chunk_attn_fwd.restype = i32
+        L.tree_chunk_attn_fwd_test.argtypes = [ctypes.POINTER(ChunkParams), vp, sz, i32, i32, i32, ctypes.c_uint32, vp]
+        L.tree_chunk_attn_fwd_test.restype = i32
+        L.tree_attn_window_workspace_size.argtypes = [ctypes.POINTER(AttnParams), i32, i32]
+        L.tree_attn_window_workspace_size.restype = sz
+        L.tree_attn_fwd_window.argtypes = [ctypes.POINTER(AttnParams), i32, i32, vp, sz, vp]
+        L.tree_attn_fwd_window.restype = i32
+        L.tree_token_logprobs.argtypes = [ctypes.POINTER(LogprobParams), vp]
+        L.tree_token_logprobs.restype = i32
         _LIB = L
     return _LIB
 
@@ -226,6 +283,7 @@ def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k
                    B=B, N=N, Hq=Hq, Hkv=Hkv, D=D, block_size=bs, num_blocks=nblk,
                    max_blocks=block_table.shape[1], scale=scale, rope_theta=rope_theta)
     p._keep = (host,)
+    p.tensors = (q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, anc_mask, out, lse, status)
     p.cache_dtypes = kd, vd = getattr(k_cache, "dtype", None), getattr(v_cache, "dtype", None)
     if (kd is _F8 or kd is _U8) and (vd is _F8 or vd is _U8):
         p.q8_device = _attn_q8_device((B, N, Hq, D), (nblk, Hkv, bs, D), host, q, k_cache, v_cache, block_table,
@@ -550,3 +608,194 @@ def tree_attn_fwd_q8_stall_test(params: AttnParams, kv_scale: torch.Tensor, work
     _check(lib().tree_attn_fwd_q8_stall_test(ctypes.byref(params), kv_scale.data_ptr(), workspace.data_ptr(),
                                              workspace.numel() * workspace.element_size(), stall_seq, stall_tile,
                                              wait_limit_us, handle), where)
+
+
+# ---------------------------------------------------------------- prompts, windowed layers, log probabilities
+
+def _token_strides(where: str, x: torch.Tensor, T: int, H: int, D: int):
+    """Strides (token, head) of bf16 x [T, H, D] with adjacent channels; 0, 0 when dense."""
+    if x.dtype is not _BF16 or x.shape != (T, H, D):
+        _bad(where)
+    if x.is_contiguous():
+        return 0, 0
+    st, sh, sd = x.stride()
+    head = D if H == 1 else sh
+    row = (H - 1) * head + D
+    token = row if T == 1 else st
+    if sd != 1 or head < D or token < row:  # (an expanded tensor repeats a token or a head)
+        _bad(where)
+    return token, head
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_params(rope: RopeConfig) -> RopeParams:
+    """The C block of a configuration (the call only reads it)."""
+    return RopeParams(rotary_dim=rope.rotary_dim, interleaved=rope.interleaved,
+                      scaling=ROPE_SCALING.get(rope.scaling, -1), theta=rope.theta, factor=rope.factor,
+                      low_rot=rope.low_rot, high_rot=rope.high_rot, orig_len=rope.orig_len, mscale=rope.mscale)
+
+
+def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cu_len: torch.Tensor,
+                           prefix_len: torch.Tensor, q_out: Optional[torch.Tensor], k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, block_table: torch.Tensor, new_prefix_len: torch.Tensor,
+                           rope: Optional[RopeConfig], status: Optional[torch.Tensor] = None,
+                           kv_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Append the new tokens k, v [T,Hkv,D] bf16 of all sequences (sequence b's are
+    rows cu_len[b] .. cu_len[b+1]-1) to the paged cache from prefix_len on, q
+    [T,Hq,D] and k rotated at their positions (q into the dense q_out), and write
+    new_prefix_len.  With ``kv_scale`` the cache is the 8-bit one.  q, k and v may
+    be views of a fused projection; without ``rope`` (and q) k is stored as it is."""
+    where = "tree_cache_append_rope"
+    T, Hkv, D = k.shape
+    B = prefix_len.shape[0]
+    nblk, bs, maxb = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+    pool = (nblk, Hkv, bs, D)
+    Hq = qt = qh = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qt, qh = _token_strides(where, q, T, Hq, D)
+        if q_out is None or not _is(q_out, _BF16, (T, Hq, D)):
+            _bad(where)
+    kt, kh = _token_strides(where, k, T, Hkv, D)
+    vt, vh = _token_strides(where, v, T, Hkv, D)
+    if kv_scale is None:
+        cache = _is(k_cache, _BF16, pool) and _is(v_cache, _BF16, pool)
+    else:
+        cache = _is_codes(k_cache, pool) and _is_codes(v_cache, pool) and _is(kv_scale, _U8, (nblk, Hkv, bs, 2))
+    if not (cache and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
+            and _is(prefix_len, _I32, (B,)) and _is(new_prefix_len, _I32, (B,))
+            and (status is None or _is(status, _I32, (B,)))):
+        _bad(where)
+    handle = _launch_stream(where, stream, q, k, v, cu_len, prefix_len, q_out if q is not None else None, k_cache,
+                            v_cache, kv_scale, block_table, new_prefix_len, status)
+    p = AppendParams(_opt(q), k.data_ptr(), v.data_ptr(), _opt(q_out) if q is not None else None, k_cache.data_ptr(),
+                     v_cache.data_ptr(), _opt(kv_scale), cu_len.data_ptr(), prefix_len.data_ptr(),
+                     block_table.data_ptr(), new_prefix_len.data_ptr(), _opt(status),
+                     None if rope is None else ctypes.pointer(_rope_params(rope)), qt, qh, kt, kh, vt, vh, B, T, Hq,
+                     Hkv, D, bs, nblk, maxb)
+    _check(lib().tree_cache_append_rope(ctypes.byref(p), handle), where)
+
+
+def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                 cu_len: torch.Tensor, kv_len: torch.Tensor, cu_len_host, kv_len_host, out: torch.Tensor,
+                 lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, scale: float = 0.0,
+                 window: int = 0, sinks: int = 0) -> ChunkParams:
+    """Fill tree_chunk_attn_fwd's parameter block from tensors (shapes as in
+    treespec.h), each of which is checked.  ``cu_len_host`` and ``kv_len_host`` are
+    the host's copies of ``cu_len`` and ``kv_len``; the returned object keeps them."""
+    where = "chunk_params"
+    T, Hq, D = q.shape
+    nblk, Hkv, bs, _ = k_cache.shape
+    B, maxb = block_table.shape
+    cu = np.ascontiguousarray(cu_len_host, np.int32)
+    kv = np.ascontiguousarray(kv_len_host, np.int32)
+    pool = (nblk, Hkv, bs, D)
+    if not (_is(q, _BF16, (T, Hq, D)) and _is(out, _BF16, (T, Hq, D)) and _is(k_cache, _BF16, pool)
+            and _is(v_cache, _BF16, pool) and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
+            and _is(kv_len, _I32, (B,)) and cu.shape == (B + 1,) and kv.shape == (B,)
+            and (lse is None or _is(lse, torch.float32, (T, Hq))) and (status is None or _is(status, _I32, (B,)))):
+        _bad(where)
+    dev = q.get_device()
+    for t in (out, k_cache, v_cache, block_table, cu_len, kv_len, lse, status):
+        if t is not None and t.get_device() != dev:
+            _bad(where)
+    p = ChunkParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_len.data_ptr(),
+                    kv_len.data_ptr(), cu.ctypes.data, kv.ctypes.data, out.data_ptr(), _opt(lse), _opt(status), B, T, Hq,
+                    Hkv, D, bs, nblk, maxb, scale, window, sinks)
+    p._keep = (cu, kv)
+    p.device = dev
+    return p
+
+
+def tree_chunk_attn_workspace_size(params: ChunkParams) -> int:
+    return int(lib().tree_chunk_attn_workspace_size(ctypes.byref(params)))
+
+
+def _chunk_stream(where: str, params: ChunkParams, workspace, stream) -> int:
+    if not workspace.is_contiguous() or params.device != workspace.get_device():
+        _bad(where)
+    return _launch_stream(where, stream, workspace)
+
+
+def tree_chunk_attn_fwd(params: ChunkParams, workspace: torch.Tensor, stream=None) -> None:
+    """Attention of the sequences' newest tokens (``params`` from chunk_params) over
+    their paged cache, causal, with an optional window and sinks."""
+    where = "tree_chunk_attn_fwd"
+    handle = _chunk_stream(where, params, workspace, stream)
+    _check(lib().tree_chunk_attn_fwd(ctypes.byref(params), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), handle), where)
+
+
+def tree_chunk_attn_fwd_test(params: ChunkParams, workspace: torch.Tensor, max_ctas: int, stall_seq: int = -1,
+                             stall_tile: int = 0, wait_limit_us: int = 1000000, stream=None) -> None:
+    """Testing only: tree_chunk_attn_fwd on at most ``max_ctas`` CTAs and, with
+    ``stall_seq >= 0``, that sequence's key stream stopped before tile ``stall_tile``."""
+    where = "tree_chunk_attn_fwd_test"
+    handle = _chunk_stream(where, params, workspace, stream)
+    _check(lib().tree_chunk_attn_fwd_test(ctypes.byref(params), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), max_ctas, stall_seq,
+                                          stall_tile, wait_limit_us, handle), where)
+
+
+def tree_attn_window_workspace_size(params: AttnParams, window: int, sinks: int) -> int:
+    return int(lib().tree_attn_window_workspace_size(ctypes.byref(params), window, sinks))
+
+
+def tree_attn_fwd_window(params: AttnParams, window: int, sinks: int, workspace: torch.Tensor, stream=None) -> None:
+    """tree_attn_fwd (``params`` from attn_params) for a layer with a sliding window
+    of ``window`` positions and ``sinks`` first tokens that stay visible."""
+    where = "tree_attn_fwd_window"
+    q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, anc_mask, out, lse, status = params.tensors
+    B, N, Hq, D = q.shape
+    nblk, Hkv, bs, _ = k_cache.shape
+    tree, pool = (B, N, Hkv, D), (nblk, Hkv, bs, D)
+    if not (_is(q, _BF16, (B, N, Hq, D)) and _is(out, _BF16, (B, N, Hq, D)) and _is(k_cache, _BF16, pool)
+            and _is(v_cache, _BF16, pool) and _is(k_tree, _BF16, tree) and _is(v_tree, _BF16, tree)
+            and _is(block_table, _I32, (B, block_table.shape[1])) and _is(prefix_len, _I32, (B,))
+            and (anc_mask.dtype is torch.int64 or anc_mask.dtype is torch.uint64)
+            and _is(anc_mask, anc_mask.dtype, (B, N, (N + 63) // 64)) and params._keep[0].shape == (B,)
+            and (lse is None or _is(lse, torch.float32, (B, N, Hq))) and (status is None or _is(status, _I32, (B,)))
+            and workspace.is_contiguous()):
+        _bad(where)
+    handle = _launch_stream(where, stream, workspace, *params.tensors)
+    _check(lib().tree_attn_fwd_window(ctypes.byref(params), window, sinks, workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), handle), where)
+
+
+def tree_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], logprob: Optional[torch.Tensor],
+                        entropy: Optional[torch.Tensor] = None, top_ids: Optional[torch.Tensor] = None,
+                        top_logprobs: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                        temperature: float = 1.0, stream=None) -> None:
+    """Log probabilities of tokens [R] i32 under rows of logits [M,V] (or [B,N,V]: M
+    = B N; fp32 or bf16, rows evenly spaced), the rows' entropies [R], and their
+    most likely tokens top_ids, top_logprobs [R,top].  ``rows`` [R] i32 picks the
+    rows; an output whose row is out of range is left as it was."""
+    where = "tree_token_logprobs"
+    V = logits.shape[-1]
+    if logits.dim() == 3:
+        (M0, M1, _), (s0, s1, s2) = logits.shape, logits.stride()
+        M, stride = M0 * M1, s1 if M1 > 1 else s0
+        even = M0 == 1 or M1 == 1 or s0 == M1 * s1
+    else:
+        M, stride, s2, even = logits.shape[0], logits.stride(0), logits.stride(1), logits.dim() == 2
+    if M <= 1:
+        stride = 0
+    some = next((t for t in (logprob, entropy, top_ids, top_logprobs) if t is not None), None)
+    if some is None:
+        _bad(where)
+    R = some.shape[0]
+    best = top_ids if top_ids is not None else top_logprobs
+    top = 0 if best is None else best.shape[1]
+    if not (even and (logits.dtype is torch.float32 or logits.dtype is _BF16) and (s2 == 1 or V == 1)
+            and (M <= 1 or stride >= V)  # (an expanded row would read as dense)
+            and (tokens is None or _is(tokens, _I32, (R,))) and (rows is None or _is(rows, _I32, (R,)))
+            and (logprob is None or _is(logprob, torch.float32, (R,)))
+            and (entropy is None or _is(entropy, torch.float32, (R,)))
+            and (top_ids is None or _is(top_ids, _I32, (R, top)))
+            and (top_logprobs is None or _is(top_logprobs, torch.float32, (R, top)))):
+        _bad(where)
+    handle = _launch_stream(where, stream, logits, tokens, logprob, entropy, top_ids, top_logprobs, rows)
+    p = LogprobParams(logits.data_ptr(), _opt(tokens), _opt(rows), _opt(logprob), _opt(entropy),
+                      _opt(top_ids) if top else None, _opt(top_logprobs) if top else None, stride, R, M, V, top,
+                      logits.dtype is _BF16, temperature)
+    _check(lib().tree_token_logprobs(ctypes.byref(p), handle), where)

@@ -4,6 +4,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attn_paged.cuh"
 #include "internal.cuh"
 
 namespace ts {
@@ -159,6 +160,8 @@ cudaError_t prepare_device(int* stoch_max_cluster = nullptr) {
     e = attn_tc_prepare();
     if (e != cudaSuccess) return e;
     e = attn_q8_prepare();
+    if (e != cudaSuccess) return e;
+    e = attn_paged_prepare();
     if (e != cudaSuccess) return e;
     e = stoch_prepare(&max_cluster[dev]);
     if (e != cudaSuccess) return e;
@@ -498,6 +501,7 @@ namespace ts {
 namespace {
 
 constexpr int MAX_HEADS = 4096;
+constexpr int MAX_POSITION = 1 << 30;
 
 // Bytes [at, at + n) of two buffers that share any.
 struct Span {
@@ -555,6 +559,19 @@ bool rope_turns(const ts_rope_params& p, int R, uint64_t* turn) {
 
 bool positive(double x) { return x > 0.0 && std::isfinite(x); }
 
+// A rotary configuration (of a p whose D is checked).
+ts_status check_rope(const ts_rope_params& p) {
+  if (p.scaling < TS_ROPE_NONE || p.scaling > TS_ROPE_BANDS) return TS_ERR_UNSUPPORTED;
+  const int R = p.rotary_dim == 0 ? p.D : p.rotary_dim;
+  if (R < 2 || R > p.D || R % 2) return TS_ERR_SHAPE;
+  if (!positive(p.theta) || !positive(p.mscale)) return TS_ERR_SHAPE;
+  if (p.scaling != TS_ROPE_NONE && !positive(p.factor)) return TS_ERR_SHAPE;
+  if (p.scaling == TS_ROPE_BANDS &&
+      !(p.orig_len > 0 && p.low_rot < p.high_rot && std::isfinite(p.low_rot) && std::isfinite(p.high_rot)))
+    return TS_ERR_SHAPE;
+  return TS_OK;
+}
+
 ts_status check_attn_q8(const ts_attn_params* p) {
   const ts_status st = check_attn(p);
   if (st != TS_OK) return st;
@@ -608,14 +625,9 @@ ts_status tree_rope(const ts_rope_params* p, ts_stream stream) {
   if (p->B < 1 || p->N < 1 || (p->q && Hq < 1) || (p->k && Hkv < 1)) return TS_ERR_SHAPE;
   if ((long long)p->B * p->N > 0x7fffffffll) return TS_ERR_SHAPE;
   if ((p->D != 64 && p->D != 128) || Hq > MAX_HEADS || Hkv > MAX_HEADS) return TS_ERR_UNSUPPORTED;
-  if (p->scaling < TS_ROPE_NONE || p->scaling > TS_ROPE_BANDS) return TS_ERR_UNSUPPORTED;
+  const ts_status rope_st = check_rope(*p);
+  if (rope_st != TS_OK) return rope_st;
   const int R = p->rotary_dim == 0 ? p->D : p->rotary_dim;
-  if (R < 2 || R > p->D || R % 2) return TS_ERR_SHAPE;
-  if (!positive(p->theta) || !positive(p->mscale)) return TS_ERR_SHAPE;
-  if (p->scaling != TS_ROPE_NONE && !positive(p->factor)) return TS_ERR_SHAPE;
-  if (p->scaling == TS_ROPE_BANDS &&
-      !(p->orig_len > 0 && p->low_rot < p->high_rot && std::isfinite(p->low_rot) && std::isfinite(p->high_rot)))
-    return TS_ERR_SHAPE;
   RopeArgs a{};
   a.tokens = p->B * p->N;
   a.Hq = Hq; a.Hkv = Hkv; a.D = p->D; a.R = R; a.interleaved = p->interleaved != 0;
@@ -734,6 +746,233 @@ ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint8_t* kv
   if (wait_limit_us < 100 || wait_limit_us > 1000000) return TS_ERR_UNSUPPORTED;
   return ts::attn_q8_impl(p, kv_scale, workspace, workspace_bytes, stream, stall_seq, stall_tile,
                           (unsigned long long)wait_limit_us * 1000ull);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- prompts, windowed layers, log probabilities
+
+namespace ts {
+namespace {
+
+// Host validation of tree_chunk_attn_fwd; touches no device memory.
+ts_status check_chunk(const ts_chunk_params* p) {
+  if (!p) return TS_ERR_NULL;
+  if (!p->k_cache || !p->v_cache || !p->block_table || !p->cu_len || !p->kv_len || !p->cu_len_host ||
+      !p->kv_len_host || (p->T > 0 && (!p->q || !p->out)))
+    return TS_ERR_NULL;
+  if (p->B < 1 || p->T < 0 || p->Hq < 1 || p->Hkv < 1 || p->num_blocks < 1 || p->max_blocks < 1 || p->block_size < 1)
+    return TS_ERR_SHAPE;
+  if (p->D != 64 && p->D != 128) return TS_ERR_UNSUPPORTED;
+  if (p->Hq % p->Hkv != 0) return TS_ERR_SHAPE;
+  if (!supported_group(p->Hq / p->Hkv) || p->Hq > MAX_HEADS) return TS_ERR_UNSUPPORTED;
+  if (p->block_size % 16 != 0) return TS_ERR_UNSUPPORTED;
+  if (!(p->scale >= 0.f) || std::isinf(p->scale)) return TS_ERR_SHAPE;
+  if (p->window < 0 || p->sinks < 0) return TS_ERR_SHAPE;
+  if (p->window > MAX_POSITION || p->sinks > MAX_POSITION) return TS_ERR_UNSUPPORTED;
+  if (p->cu_len_host[0] < 0 || p->cu_len_host[p->B] > p->T) return TS_ERR_SHAPE;
+  for (int b = 0; b < p->B; ++b) {
+    const int len = p->cu_len_host[b + 1] - p->cu_len_host[b], kv = p->kv_len_host[b];
+    if (p->cu_len_host[b + 1] < p->cu_len_host[b] || kv < len) return TS_ERR_SHAPE;
+    if (kv > MAX_POSITION) return TS_ERR_UNSUPPORTED;
+    if ((long long)p->max_blocks * p->block_size < kv) return TS_ERR_SHAPE;
+  }
+  if (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->out)) return TS_ERR_SHAPE;
+  return TS_OK;
+}
+
+void fill_paged(PagedArgs* a, const void* q, const void* k, const void* v, const int32_t* table, void* out, float* lse,
+                int32_t* status, int B, int T, int Hq, int Hkv, int D, int bs, int num_blocks, int max_blocks,
+                float scale, int window, int sinks) {
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k_cache = static_cast<const __nv_bfloat16*>(k);
+  a->v_cache = static_cast<const __nv_bfloat16*>(v);
+  a->block_table = table;
+  a->out = static_cast<__nv_bfloat16*>(out);
+  a->lse = lse;
+  a->status = status;
+  a->B = B; a->T = T; a->Hq = Hq; a->Hkv = Hkv; a->G = Hq / Hkv; a->D = D;
+  a->bs = bs; a->num_blocks = num_blocks; a->max_blocks = max_blocks;
+  a->scale_log2 = (scale == 0.f ? 1.f / std::sqrt((float)D) : scale) * 1.4426950408889634f;
+  a->window = window;
+  // (sinks past every position change nothing and would overflow a sum)
+  a->sinks = std::min(sinks, MAX_POSITION);
+  a->tok = ROW_TILE / a->G;
+  a->wait_limit_ns = ATTN_WAIT_LIMIT_NS;
+  a->stall_seq = -1;
+}
+
+PagedArgs chunk_args(const ts_chunk_params* p) {
+  PagedArgs a{};
+  fill_paged(&a, p->q, p->k_cache, p->v_cache, p->block_table, p->out, p->lse, p->status, p->B, p->T, p->Hq, p->Hkv,
+             p->D, p->block_size, p->num_blocks, p->max_blocks, p->scale, p->window, p->sinks);
+  a.cu_len = p->cu_len;
+  a.kv_len = p->kv_len;
+  return a;
+}
+
+PagedArgs window_args(const ts_attn_params* p, int window, int sinks) {
+  PagedArgs a{};
+  fill_paged(&a, p->q, p->k_cache, p->v_cache, p->block_table, p->out, p->lse, p->status, p->B, p->B * p->N, p->Hq,
+             p->Hkv, p->D, p->block_size, p->num_blocks, p->max_blocks, p->scale, window, sinks);
+  a.kv_len = p->prefix_len;
+  a.k_tree = static_cast<const __nv_bfloat16*>(p->k_tree);
+  a.v_tree = static_cast<const __nv_bfloat16*>(p->v_tree);
+  a.anc_mask = p->anc_mask;
+  a.N = p->N;
+  a.W = ceil_div(p->N, 64);
+  return a;
+}
+
+ts_status check_window(const ts_attn_params* p, int window, int sinks) {
+  const ts_status st = check_attn(p);
+  if (st != TS_OK) return st;
+  if (window < 1 || sinks < 0) return TS_ERR_SHAPE;
+  if (window > MAX_POSITION || sinks > MAX_POSITION || p->Hq > MAX_HEADS) return TS_ERR_UNSUPPORTED;
+  if ((long long)p->B * p->N > 0x7fffffffll) return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+
+ts_status paged_impl(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace,
+                     size_t workspace_bytes, ts_stream stream) {
+  const size_t need = attn_paged_workspace(a, cu_len_host, kv_host);
+  if (need == 0) return TS_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return TS_ERR_WORKSPACE;
+  if (a.T == 0) return TS_OK;
+  if (prepare_device() != cudaSuccess) return TS_ERR_CUDA;
+  return launch_attn_paged(a, cu_len_host, kv_host, workspace, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" {
+
+ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream stream) {
+  if (!p || !p->cu_len || !p->prefix_len || !p->k_cache || !p->v_cache || !p->block_table || !p->new_prefix_len ||
+      (p->T > 0 && (!p->k || !p->v)) || (p->q && !p->q_out))
+    return TS_ERR_NULL;
+  const int Hq = p->q ? p->Hq : 0;
+  if (p->B < 1 || p->T < 0 || (p->q && Hq < 1) || p->Hkv < 1 || p->block_size < 1 || p->num_blocks < 1 ||
+      p->max_blocks < 1)
+    return TS_ERR_SHAPE;
+  if ((p->D != 64 && p->D != 128) || Hq > MAX_HEADS || p->Hkv > MAX_HEADS || p->block_size % 16 != 0)
+    return TS_ERR_UNSUPPORTED;
+  AppendRopeArgs a{};
+  if (p->rope) {
+    ts_rope_params r = *p->rope;
+    r.D = p->D;
+    const ts_status st = check_rope(r);
+    if (st != TS_OK) return st;
+    a.R = r.rotary_dim == 0 ? r.D : r.rotary_dim;
+    a.interleaved = r.interleaved != 0;
+    a.mscale = r.mscale;
+    if (!rope_turns(r, a.R, a.turn)) return TS_ERR_SHAPE;
+  } else if (p->q) {
+    return TS_ERR_NULL;  // queries that do not turn need no call
+  }
+  int64_t qt = p->q_token_stride, qh = p->q_head_stride, kt = p->k_token_stride, kh = p->k_head_stride,
+          vt = p->v_token_stride, vh = p->v_head_stride;
+  if ((p->q && !check_strides(&qt, &qh, Hq, p->D)) || !check_strides(&kt, &kh, p->Hkv, p->D) ||
+      !check_strides(&vt, &vh, p->Hkv, p->D))
+    return TS_ERR_SHAPE;
+  if (!aligned16(p->q) || !aligned16(p->q_out) || !aligned16(p->k) || !aligned16(p->v) || !aligned16(p->k_cache) ||
+      !aligned16(p->v_cache) || !aligned16(p->kv_scale))
+    return TS_ERR_SHAPE;
+  const auto rows = [&](const void* x, int64_t token, int64_t head, int H) {
+    return span(p->T > 0 ? x : nullptr, x && p->T > 0 ? 2ull * ((unsigned long long)(p->T - 1) * token + (H - 1) * head + p->D) : 0);
+  };
+  const Span q_out = span(p->q ? p->q_out : nullptr, p->q ? 2ull * p->T * Hq * p->D : 0);
+  const Span fresh = span(p->new_prefix_len, 4ull * p->B);
+  const Span ints[3] = {span(p->prefix_len, 4ull * p->B), span(p->cu_len, 4ull * (p->B + 1ull)),
+                        span(p->status, p->status ? 4ull * p->B : 0)};
+  for (const Span& s : ints)
+    if (overlap(fresh, s) || overlap(q_out, s)) return TS_ERR_SHAPE;
+  if (overlap(q_out, rows(p->q, qt, qh, Hq)) || overlap(q_out, rows(p->k, kt, kh, p->Hkv)) ||
+      overlap(q_out, rows(p->v, vt, vh, p->Hkv)) || overlap(q_out, fresh))
+    return TS_ERR_SHAPE;
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  a.k = static_cast<const __nv_bfloat16*>(p->k);
+  a.v = static_cast<const __nv_bfloat16*>(p->v);
+  a.q_out = static_cast<__nv_bfloat16*>(p->q_out);
+  a.k_cache = p->k_cache;
+  a.v_cache = p->v_cache;
+  a.kv_scale = p->kv_scale;
+  a.cu_len = p->cu_len;
+  a.prefix_len = p->prefix_len;
+  a.block_table = p->block_table;
+  a.new_prefix_len = p->new_prefix_len;
+  a.status = p->status;
+  a.B = p->B; a.T = p->T; a.Hq = Hq; a.Hkv = p->Hkv; a.D = p->D; a.bs = p->block_size;
+  a.num_blocks = p->num_blocks; a.max_blocks = p->max_blocks;
+  a.q_token = qt; a.q_head = qh; a.k_token = kt; a.k_head = kh; a.v_token = vt; a.v_head = vh;
+  return launch_append_rope(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+}
+
+size_t tree_chunk_attn_workspace_size(const ts_chunk_params* p) {
+  if (check_chunk(p) != TS_OK) return 0;
+  return attn_paged_workspace(chunk_args(p), p->cu_len_host, p->kv_len_host);
+}
+
+ts_status tree_chunk_attn_fwd(const ts_chunk_params* p, void* workspace, size_t workspace_bytes, ts_stream stream) {
+  const ts_status st = check_chunk(p);
+  if (st != TS_OK) return st;
+  return paged_impl(chunk_args(p), p->cu_len_host, p->kv_len_host, workspace, workspace_bytes, stream);
+}
+
+ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* workspace, size_t workspace_bytes, int max_ctas,
+                                   int stall_seq, int stall_tile, uint32_t wait_limit_us, ts_stream stream) {
+  if (max_ctas < 1) return TS_ERR_UNSUPPORTED;
+  if (p && (stall_seq < -1 || stall_seq >= p->B || (stall_seq >= 0 && stall_tile < 0))) return TS_ERR_SHAPE;
+  if (wait_limit_us < 100 || wait_limit_us > 1000000) return TS_ERR_UNSUPPORTED;
+  const ts_status st = check_chunk(p);
+  if (st != TS_OK) return st;
+  PagedArgs a = chunk_args(p);
+  a.max_ctas = max_ctas;
+  a.stall_seq = stall_seq;
+  a.stall_tile = stall_seq >= 0 ? stall_tile : 0;
+  a.wait_limit_ns = (unsigned long long)wait_limit_us * 1000ull;
+  return paged_impl(a, p->cu_len_host, p->kv_len_host, workspace, workspace_bytes, stream);
+}
+
+size_t tree_attn_window_workspace_size(const ts_attn_params* p, int window, int sinks) {
+  if (check_window(p, window, sinks) != TS_OK) return 0;
+  return attn_paged_workspace(window_args(p, window, sinks), nullptr, p->prefix_len_host);
+}
+
+ts_status tree_attn_fwd_window(const ts_attn_params* p, int window, int sinks, void* workspace, size_t workspace_bytes,
+                               ts_stream stream) {
+  const ts_status st = check_window(p, window, sinks);
+  if (st != TS_OK) return st;
+  return paged_impl(window_args(p, window, sinks), nullptr, p->prefix_len_host, workspace, workspace_bytes, stream);
+}
+
+ts_status tree_token_logprobs(const ts_logprob_params* p, ts_stream stream) {
+  if (!p || (p->R > 0 && !p->logits)) return TS_ERR_NULL;
+  if ((p->tokens == nullptr) != (p->logprob == nullptr)) return TS_ERR_NULL;
+  if (!p->logprob && !p->entropy && !p->top_ids && !p->top_logprobs) return TS_ERR_NULL;
+  if (p->top > 0 ? !p->top_ids && !p->top_logprobs : p->top_ids || p->top_logprobs) return TS_ERR_NULL;
+  if (p->R < 0 || p->M < 0 || p->V < 1 || p->top < 0 || (!p->rows && p->R > p->M)) return TS_ERR_SHAPE;
+  if (p->V > LOGPROB_MAX_V || p->top > LOGPROB_MAX_TOP || p->R > (1 << 28)) return TS_ERR_UNSUPPORTED;
+  if (p->row_stride != 0 && p->row_stride < p->V) return TS_ERR_SHAPE;
+  if (!positive(p->temperature)) return TS_ERR_SHAPE;
+  const uintptr_t size = p->half ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(p->logits) % size) return TS_ERR_SHAPE;
+  const float k = 1.4426950408889634f / p->temperature;
+  if (!positive(k)) return TS_ERR_SHAPE;
+  if (p->R == 0) return TS_OK;
+  LogprobArgs a{};
+  a.logits = p->logits;
+  a.tokens = p->tokens;
+  a.rows = p->rows;
+  a.logprob = p->logprob;
+  a.entropy = p->entropy;
+  a.top_ids = p->top_ids;
+  a.top_logprobs = p->top_logprobs;
+  a.row_stride = p->row_stride ? p->row_stride : p->V;
+  a.R = p->R; a.M = p->M; a.V = p->V; a.top = p->top; a.half = p->half;
+  a.inv_temp_log2e = k;
+  return launch_logprobs(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
 }
 
 }  // extern "C"

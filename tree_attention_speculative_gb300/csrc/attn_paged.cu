@@ -1,0 +1,1131 @@
+// Attention over the bf16 paged cache for ragged chunks of new tokens, and for
+// trees of windowed layers, on the 5th-generation tensor cores.
+//
+// What it computes.  A row (token i of sequence b, query head h) at position p
+// sees the cached keys t with  t < limit  and, with a window,  t > p - window or
+// t < sinks;  its output is softmax(scale q.k) v over them.
+//   chunk: the rows are the last tokens of the cache itself, p = kv - len + i and
+//          limit = p + 1 (causal);
+//   tree:  the rows are tree nodes past a verified prefix, p = P + depth and
+//          limit = P; the tree's own keys follow, gated by the ancestry mask (and
+//          by the window, counted in depths).
+//
+// How.  The G query heads of a KV head share every key, so ROW_TILE / G tokens
+// of G heads are the 128 rows of one MMA tile.  A work item is such a tile of one
+// KV head and a split of its chain of 128-key tiles; only tiles that some row
+// sees are in the chain: the sinks' tiles, then the window's.  One online softmax
+// runs over the chain, and k_join_paged joins the splits of a cut chain.
+//
+// The kernel is persistent, one CTA an SM taking items from a counter, the
+// longest first, with one role a warp, as tree attention's:
+//   warp 0     takes the items (and hands them to the others through a queue in
+//              shared memory); TMA loads of the K tiles
+//   warp 3     TMA loads of the V tiles
+//   warp 1     S(j) = Q K(j)^T into S buffer j % 3, once PV(j-3) has freed it
+//   warp 2     O += P(j) V(j), P from TMEM
+//   warps 4-7  softmax, a row a thread: masks, running maximum and sum, P in bf16
+//              over S, O rescaled only when a row's maximum rises by more than 2^20
+//              (exact: the final division uses the same reference)
+// Masks cost nothing where a tile is wholly visible; elsewhere each row makes
+// a 128-bit word of its visible keys.  Keys that no row of the item sees may be
+// anything, so their V rows are zeroed in shared memory before PV reads them
+// (0 * NaN), and blocks that hold only such keys are not read at all: a
+// windowed layer may have given them away.
+//
+// Every wait is bounded; a wait that runs out sets a flag, all roles wind down,
+// let their loads and MMAs in flight finish, free the tensor memory and report
+// TS_ERR_TIMEOUT for the sequences of the items they had not finished.
+#include <algorithm>
+#include <climits>
+
+#include "attn_paged.cuh"
+#include "fastexp.cuh"
+#include "tensor_map.cuh"
+#include "waits.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int NUM_THREADS = 256;
+constexpr int SOFTMAX_THREADS = 128;
+constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4;
+constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S0 = 128;
+constexpr int NSB = 3;       // S buffers in TMEM
+constexpr int ITEM_Q = 16;   // entries of the item queue
+// O is rescaled when a row's maximum rises by more than this (in powers of two):
+// weights then stay below 2^20, far inside the range of bf16 and fp32.
+constexpr float RESCALE_THRESHOLD = 20.0f;
+constexpr float NEG_INF = -INFINITY;
+
+template <int D>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE_BYTES = KV_TILE * D * 2;
+  static constexpr int HALF_BYTES = KV_TILE * 128;
+  static constexpr int Q_BYTES = ROW_TILE * D * 2;
+  static constexpr int NST = D == 128 ? 3 : 6;  // tiles in each ring, K and V
+};
+
+// An item and its sequence's lengths.
+struct Work {
+  int b;          // -1: no more items
+  int place;      // KV head, split, row tile, entry: see pack
+  int q0;         // first row's token
+  int len, kv;    // tokens of the sequence here, and in the cache
+};
+
+template <int D>
+struct __align__(1024) Smem {
+  using C = Cfg<D>;
+  uint8_t q[C::Q_BYTES];
+  uint8_t k[C::NST][C::TILE_BYTES];
+  uint8_t v[C::NST][C::TILE_BYTES];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[C::NST], v_full[C::NST];
+  uint64_t k_empty[C::NST], v_empty[C::NST];
+  uint64_t s_full[NSB], p_full[NSB], s_free[NSB];
+  uint64_t o_ready;
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  int abort_flag;
+  int pv_done;  // PVs completed so far
+  // the CTA's items in the order taken; pub published, done stored
+  int item_q[ITEM_Q][8];
+  int items_pub, items_done;
+};
+
+struct KArgs {
+  PagedArgs a;
+  int box_rows, n_items, n_seqs, out32;
+  FastDiv fd_hkv, fd_bs, fd_g;
+  PagedSeq seq[PAGED_MAX_SEQS];
+};
+
+// Entry of an item: the last with item0 <= it.
+__device__ __forceinline__ int entry_of(int it, const KArgs& t) {
+  int lo = 0, hi = t.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.seq[mid].item0 <= it) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct Place {
+  int e, rt, split, g;
+};
+__device__ __forceinline__ Place place_of(int it, const KArgs& t) {
+  Place p;
+  p.e = entry_of(it, t);
+  const int k = it - t.seq[p.e].item0;
+  const int u = t.fd_hkv.div(k);
+  p.g = k - u * t.a.Hkv;
+  const int back = u / t.seq[p.e].splits;
+  p.split = u - back * t.seq[p.e].splits;
+  p.rt = t.seq[p.e].row_tiles - 1 - back;
+  return p;
+}
+
+struct Item {
+  int b, g, split, e;
+  int q0, i0, len;  // the tile's first row is token q0 + i0, the i0-th of len
+  int pos0;         // position of the tile's first row (tree: of the root)
+  PagedSpan sp;
+  int t_begin, n_prefix, n_tiles, ps;
+  bool work;
+};
+template <bool TREE>
+__device__ __forceinline__ Item make_item(const Place& p, int b, int q0, int len, int kv, const KArgs& t) {
+  const PagedArgs& a = t.a;
+  Item I;
+  I.b = b;
+  I.g = p.g;
+  I.split = p.split;
+  I.e = p.e;
+  I.q0 = q0;
+  I.len = len;
+  I.i0 = p.rt * a.tok;
+  I.work = I.i0 < len;
+  if (TREE) {
+    I.pos0 = kv;
+    I.sp = paged_span(kv, kv, a.window, a.sinks);
+  } else {
+    I.pos0 = kv - len + I.i0;
+    I.sp = chunk_span(kv, len, I.i0, a.tok, a.window, a.sinks);
+  }
+  I.ps = paged_splits(I.sp.n, a.chunk_tiles, t.seq[p.e].splits);
+  I.work = I.work && p.split < I.ps;
+  I.t_begin = paged_split_start(I.sp.n, I.ps, p.split);
+  I.n_prefix = paged_split_start(I.sp.n, I.ps, p.split + 1) - I.t_begin;
+  I.n_tiles = I.n_prefix + (TREE && p.split == I.ps - 1 ? ceil_div(a.N, KV_TILE) : 0);
+  return I;
+}
+// First key of the item's prefix tile j.
+__device__ __forceinline__ int tile_key(const Item& I, int j) {
+  const int jj = I.t_begin + j;
+  return (jj < I.sp.n_sink ? jj : jj - I.sp.n_sink + I.sp.win0) * KV_TILE;
+}
+
+// The lengths of sequence b as the device has them.
+struct Lens {
+  int q0, len, kv;
+  bool ok;  // they are what the launch was planned for
+};
+__device__ __forceinline__ int ld_early(const int* p) {  // issued where it is written
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(reinterpret_cast<uint64_t>(p)) : "memory");
+  return v;
+}
+template <bool TREE>
+__device__ __forceinline__ Lens load_lens(int b, int planned, const PagedArgs& a) {
+  Lens l;
+  l.kv = ld_early(a.kv_len + b);
+  const long long cap = min((long long)a.max_blocks * a.bs, 1ll << 30);
+  if (TREE) {
+    l.q0 = b * a.N;
+    l.len = a.N;
+    l.ok = l.kv >= 0 && l.kv <= cap;
+  } else {
+    l.q0 = ld_early(a.cu_len + b);
+    const int q1 = ld_early(a.cu_len + b + 1);
+    l.ok = l.q0 >= 0 && q1 >= l.q0 && q1 <= a.T && q1 - l.q0 <= planned;
+    l.len = l.ok ? q1 - l.q0 : 0;
+    l.ok = l.ok && l.kv >= l.len && l.kv <= cap;
+  }
+  if (!l.ok) l.len = 0;  // nothing of it is read or written
+  return l;
+}
+
+// The first n bits of a 64-bit word.
+__device__ __forceinline__ uint64_t first_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// One 32-byte store (a whole DRAM sector), to a 32-byte aligned address.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint64_t>(p)),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+template <int D, bool TREE>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtensorMap tm_q,
+             const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
+             const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const PagedArgs& a = args.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Ctl ctl{&sm.abort_flag, a.wait_limit_ns};
+  const int n_items = args.n_items;
+
+  const Place pl0 = place_of(blockIdx.x, args);
+  const int b0 = args.seq[pl0.e].b;
+  if (warp == V_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kc);
+    tma_prefetch_desc(&tm_vc);
+    if (TREE) {
+      tma_prefetch_desc(&tm_kt);
+      tma_prefetch_desc(&tm_vt);
+    }
+  }
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    sm.pv_done = 0;
+    sm.items_pub = 0;
+    sm.items_done = 0;
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < NSB; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], SOFTMAX_THREADS);
+      mbar_init(&sm.s_free[i], 1);
+    }
+    mbar_init(&sm.o_ready, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
+    fence_barrier_init();
+  }
+  if (warp == K_WARP) tmem_alloc(&sm.tmem_base, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  // nothing above read an input
+  pdl_wait();
+  // With a CTA an item nothing is taken from the counter and nothing goes through
+  // the queue: every role reads the lengths itself.
+  const bool single = (int)gridDim.x == n_items;
+  const bool grabber = warp == K_WARP && !single;
+  Lens l0{0, 0, 0, false};
+  if (single || grabber) l0 = load_lens<TREE>(b0, args.seq[pl0.e].rows, a);
+  if (single && !l0.ok && threadIdx.x == 0 && a.status) a.status[b0] = TS_ERR_SHAPE;
+  const Item item0 = make_item<TREE>(pl0, b0, l0.q0, l0.len, l0.kv, args);
+
+  // Entry k of the queue as an item (every role but the K producer; with a CTA
+  // an item every role).  false: the wait gave up; work false: no more items.
+  auto queue_item = [&](int k, Item& I) -> bool {
+    if (single) {
+      I = item0;
+      I.work = I.work && k == 0;
+      return true;
+    }
+    if (!wait_count(&sm.items_pub, k + 1, ctl)) return false;
+    const volatile int* q = sm.item_q[k % ITEM_Q];
+    const int b = q[0];
+    if (b < 0) {
+      I.work = false;
+      return true;
+    }
+    const Place p{q[1], q[2], q[3], q[4]};
+    I = make_item<TREE>(p, b, q[5], q[6], q[7], args);
+    return true;
+  };
+  // The K producer's lane 0: the next item, or -1.  The last of all requests puts
+  // the counter back to zero.
+  auto take_item = [&]() -> int {
+    const unsigned v = atomicAdd(a.sched, 1u);
+    if (v == (unsigned)(n_items - 1)) atomicExch(a.sched, 0u);
+    const int it = (int)gridDim.x + (int)v;
+    return it < n_items ? it : -1;
+  };
+  int held = -1;             // an item taken and not published yet
+  bool exhausted = single;   // the counter said that none is left
+
+  auto kv_producer = [&](bool is_v) -> int {
+    const CUtensorMap* tm_pool = is_v ? &tm_vc : &tm_kc;
+    const CUtensorMap* tm_node = is_v ? &tm_vt : &tm_kt;
+    uint64_t* full = is_v ? sm.v_full : sm.k_full;
+    uint64_t* empty = is_v ? sm.v_empty : sm.k_empty;
+    const int g_box = args.box_rows;
+    const int lg_boxes = __ffs(KV_TILE / g_box) - 1;  // 1 .. 8 boxes a tile
+    const int n_boxes = 1 << lg_boxes, tpg = 32 >> lg_boxes;
+    const uint32_t box_bytes = g_box * D * 2;
+    const int koff = (lane & (n_boxes - 1)) * g_box;  // this lane's box of a tile
+    int slot = 0, phase = 0;
+    int jg = 0;  // tiles issued, over every item
+    int cand = blockIdx.x;
+    Place cpl = pl0;
+    Lens cl = l0;
+    if (grabber) held = cand;
+    for (int k = 0;; ++k) {
+      Item I;
+      if (grabber) {
+        for (;;) {
+          if (cand < 0) break;
+          if (!cl.ok && lane == 0 && a.status) a.status[args.seq[cpl.e].b] = TS_ERR_SHAPE;
+          I = make_item<TREE>(cpl, args.seq[cpl.e].b, cl.q0, cl.len, cl.kv, args);
+          if (I.work) break;
+          int nx = -1;
+          if (lane == 0) nx = take_item();
+          cand = __shfl_sync(0xffffffffu, nx, 0);
+          held = cand;
+          exhausted = cand < 0;
+          if (cand >= 0) {
+            cpl = place_of(cand, args);
+            cl = load_lens<TREE>(args.seq[cpl.e].b, args.seq[cpl.e].rows, a);
+          }
+        }
+        bool ok = k < ITEM_Q;  // the entry's last user must be done
+        if (!ok && lane == 0) ok = wait_count(&sm.items_done, k - ITEM_Q + 1, ctl);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
+        if (lane == 0) {
+          volatile int* q = sm.item_q[k % ITEM_Q];
+          q[0] = cand < 0 ? -1 : I.b;
+          q[1] = cpl.e;
+          q[2] = cpl.rt;
+          q[3] = cpl.split;
+          q[4] = cpl.g;
+          q[5] = cl.q0;
+          q[6] = cl.len;
+          q[7] = cl.kv;
+          publish(&sm.items_pub, k + 1);
+        }
+        __syncwarp();
+        held = -1;
+        if (cand < 0) return jg;
+        // take the next one now: its lengths load while this one streams
+        int nx = -1;
+        if (lane == 0) nx = take_item();
+        cand = __shfl_sync(0xffffffffu, nx, 0);
+        held = cand;
+        exhausted = cand < 0;
+        if (cand >= 0) {
+          cpl = place_of(cand, args);
+          cl = load_lens<TREE>(args.seq[cpl.e].b, args.seq[cpl.e].rows, a);
+        }
+      } else {
+        bool ok = true;
+        if (lane == 0 && !single) ok = wait_count(&sm.items_pub, k + 1, ctl);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
+        if (!queue_item(k, I)) return jg;
+        if (!I.work) return jg;
+      }
+      const int b = I.b, g = I.g, n_prefix = I.n_prefix;
+      const int* table_row = a.block_table + (size_t)b * a.max_blocks;
+      // Block-table entries, a group of tiles ahead: lane L holds that of box
+      // L % boxes of tile L / boxes of a group of 32 / boxes tiles.  -1 for a box
+      // that no row of the item sees into: it is not read.
+      auto load_group = [&](int grp) -> int {
+        const int j = grp * tpg + (lane >> lg_boxes);
+        if (j >= n_prefix) return INT_MIN;
+        const int t0 = tile_key(I, j) + koff;
+        if (t0 >= I.sp.hi || (t0 + g_box <= I.sp.lo && t0 >= a.sinks)) return INT_MIN;
+        const int blk = table_row[args.fd_bs.div(t0)];
+        return blk == INT_MIN ? -1 : blk;
+      };
+      int grp_cur = load_group(0);
+      int grp_nxt = n_prefix > tpg ? load_group(1) : INT_MIN;
+      const int stop = !is_v && b == a.stall_seq ? a.stall_tile : I.n_tiles;
+      int jt = 0;
+      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+        uint8_t* dst = is_v ? sm.v[slot] : sm.k[slot];
+        if (jg >= C::NST) {
+          bool ok = true;
+          if (lane == 0) ok = wait_bar(&empty[slot], phase ^ 1, ctl);
+          if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
+        }
+        if (j == stop) return jg;
+        if (j < n_prefix) {
+          if (jt == 0 && j > 0) {
+            grp_cur = grp_nxt;
+            const int g2 = (j >> (5 - lg_boxes)) + 1;
+            grp_nxt = g2 * tpg < n_prefix ? load_group(g2) : INT_MIN;
+          }
+          int blk = __shfl_sync(0xffffffffu, grp_cur, (jt << lg_boxes) + (lane & (n_boxes - 1)));
+          const bool issue = lane < n_boxes && blk != INT_MIN;
+          if (issue && (blk < 0 || blk >= a.num_blocks)) {
+            if (a.status) a.status[b] = TS_ERR_BAD_BLOCK;
+            blk = 0;  // a valid block is read in its place
+          }
+          const unsigned mask = __ballot_sync(0xffffffffu, issue);
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(mask) * box_bytes);
+          __syncwarp();
+          if (issue) {
+            const int row = args.fd_bs.mod(tile_key(I, j) + koff);
+            tma_load_5d(dst + lane * box_bytes, tm_pool, &full[slot], 0, 0, 0, row >> 3, blk * a.Hkv + g);
+          }
+          jt = (jt + 1) & (tpg - 1);
+        } else if (lane == 0) {
+          const int n0 = (j - n_prefix) * KV_TILE;  // nodes >= N read as zeros
+          mbar_arrive_expect_tx(&full[slot], C::TILE_BYTES);
+          for (int h = 0; h < C::HALVES; ++h) tma_load_4d(dst + h * C::HALF_BYTES, tm_node, &full[slot], 64 * h, g, n0, b);
+        }
+        __syncwarp();
+        if (++slot == C::NST) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  };
+  int issued = 0;
+  int q_issued = 0, q_landed = 0;
+
+  if (warp == K_WARP || warp == V_WARP) {
+    issued = kv_producer(warp == V_WARP);
+  } else if (warp == QK_WARP) {
+    if (lane == 0) {
+      constexpr uint32_t ID_QK = idesc_bf16_f32(ROW_TILE, KV_TILE, 0, 0);
+      const uint32_t q_addr = smem_u32(sm.q);
+      int jg = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        Item I;
+        if (!(ok = queue_item(k, I))) break;
+        if (!I.work) break;
+        // this item's Q tile, once every QK of the last one has completed
+        if (k > 0 && !(ok = wait_bar(&sm.q_empty, (k - 1) & 1, ctl))) break;
+        mbar_arrive_expect_tx(&sm.q_full, C::Q_BYTES);
+        for (int h = 0; h < C::HALVES; ++h)
+          tma_load_3d(sm.q + h * (ROW_TILE * 128), &tm_q, &sm.q_full, 64 * h, I.g * a.G, I.q0 + I.i0);
+        ++q_issued;
+        if (!(ok = wait_bar(&sm.q_full, k & 1, ctl))) break;
+        ++q_landed;
+        for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+          const int slot = jg % C::NST;
+          ok = wait_bar(&sm.k_full[slot], (jg / C::NST) & 1, ctl) &&
+               (jg < NSB || wait_bar(&sm.s_free[jg % NSB], ((jg / NSB) - 1) & 1, ctl));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_addr = smem_u32(sm.k[slot]);
+          const uint32_t d_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
+          // cached tiles: [8-row group][64-column half]; tree tiles: [half][rows]
+          const bool tree = TREE && j >= I.n_prefix;
+          const uint32_t k_half = tree ? C::HALF_BYTES : 1024;
+          const uint32_t k_sbo = tree ? 1024 : C::HALVES * 1024;
+#pragma unroll
+          for (int k2 = 0; k2 < D / 16; ++k2) {
+            const uint32_t off = (k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32;
+            const uint32_t koff = (k2 >> 2) * k_half + (k2 & 3) * 32;
+            mma_ss(d_tmem, smem_desc_sw128(q_addr + off, 16, 1024), smem_desc_sw128(k_addr + koff, 16, k_sbo), ID_QK,
+                   k2 > 0);
+          }
+          mma_commit(&sm.s_full[jg % NSB]);
+          mma_commit(&sm.k_empty[slot]);
+        }
+        if (ok) mma_commit(&sm.q_empty);
+      }
+    }
+  } else if (warp == PV_WARP) {
+    if (lane == 0) {
+      constexpr uint32_t ID_PV = idesc_bf16_f32(ROW_TILE, D, 0, 1);
+      int jg = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        Item I;
+        if (!(ok = queue_item(k, I))) break;
+        if (!I.work) break;
+        for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+          const int slot = jg % C::NST;
+          if (!(ok = wait_bar(&sm.p_full[jg % NSB], (jg / NSB) & 1, ctl))) break;
+          if (!(ok = wait_bar(&sm.v_full[slot], (jg / C::NST) & 1, ctl))) break;
+          tc_fence_after();
+          const uint32_t v_addr = smem_u32(sm.v[slot]);
+          const uint32_t p_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
+          const bool tree = TREE && j >= I.n_prefix;
+          const uint32_t v_lbo = tree ? C::HALF_BYTES : 1024;
+          const uint32_t v_sbo = tree ? 1024 : C::HALVES * 1024;
+#pragma unroll
+          for (int k2 = 0; k2 < KV_TILE / 16; ++k2)
+            mma_ts(tmem + TMEM_O, p_tmem + k2 * 8, smem_desc_sw128(v_addr + k2 * 2 * v_sbo, v_lbo, v_sbo), ID_PV,
+                   j > 0 || k2 > 0);
+          mma_commit(&sm.o_ready);
+          mma_commit(&sm.s_free[jg % NSB]);
+          mma_commit(&sm.v_empty[slot]);
+          // published so that the softmax looks at O only when it has to
+          if (!(ok = wait_bar(&sm.o_ready, jg & 1, ctl))) break;
+          tc_fence_after();
+          publish(&sm.pv_done, jg + 1);
+        }
+      }
+    }
+  } else {
+    const int r = threadIdx.x - SOFTMAX_WARP0 * 32;  // TMEM lane, and row of the tile
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int i_in = args.fd_g.div(r);  // token of the tile, and head of the group
+    const int h_in = r - i_in * a.G;
+    int jg = 0;
+    Item I;
+    bool ok = __all_sync(0xffffffffu, queue_item(0, I));
+    for (int k = 0; ok && I.work; ++k) {
+      const bool active = I.i0 + i_in < I.len;
+      const int i = active ? I.i0 + i_in : I.len - 1;
+      // the row's position, and the cached keys it sees: t < hi, and t >= lo or t < sinks
+      int pos, hi, hi_least, lo_most;
+      uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
+      if (TREE) {
+        const int P = I.pos0;
+        int depth = 0;
+        if (active) {
+          const uint64_t* arow = a.anc_mask + ((size_t)I.b * a.N + i) * a.W;
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (w < a.W) anc[w] = arow[w];
+          depth = __popcll(anc[0]) + __popcll(anc[1]) + __popcll(anc[2]) + __popcll(anc[3]) - 1;
+        }
+        pos = P + depth;
+        hi = hi_least = P;
+        lo_most = P + a.N - a.window;
+        // Ancestors out of the window.  Node indices rise along a chain, so the
+        // k-th set bit is the ancestor at depth k: hidden if depth - k >= window
+        // and P + k >= sinks.
+        const int hide_end = depth + 1 - a.window, hide0 = max(a.sinks - P, 0);
+        if (a.window > 0 && hide_end > hide0) {
+          int at = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint64_t left = anc[w];
+            while (left && at < hide_end) {
+              const uint64_t bit = left & (0ull - left);
+              left ^= bit;
+              if (at >= hide0) anc[w] ^= bit;
+              ++at;
+            }
+          }
+        }
+      } else {
+        pos = I.pos0 + (i - I.i0);
+        hi = pos + 1;
+        hi_least = I.pos0 + 1;
+        lo_most = I.sp.hi - a.window;
+      }
+      if (a.window == 0) lo_most = 0;
+      const int lo = a.window == 0 ? 0 : pos - a.window + 1;
+      float m_run = NEG_INF, l_run = 0.f;
+      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
+        if (!__all_sync(0xffffffffu, wait_bar(&sm.s_full[jg % NSB], (jg / NSB) & 1, ctl))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * 128;
+        float s[KV_TILE];
+        {
+          uint32_t u[KV_TILE / 32][32];
+#pragma unroll
+          for (int c = 0; c < KV_TILE / 32; ++c) tmem_ld32(s_tmem + c * 32, u[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < KV_TILE / 32; ++c) {
+            reg_fence32(u[c]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(u[c][e]);
+          }
+        }
+        // which keys this row sees, where it may not see all
+        const bool cached = !TREE || j < I.n_prefix;
+        const int key0 = cached ? tile_key(I, j) : 0;
+        bool masked, dead = false;
+        if (cached) {
+          masked = key0 + KV_TILE > hi_least || (key0 < lo_most && key0 + KV_TILE > a.sinks);
+          dead = key0 + KV_TILE > I.sp.hi || (key0 < I.sp.lo && key0 + KV_TILE > a.sinks);
+        } else {
+          masked = true;
+        }
+        if (masked) {
+          uint64_t w0, w1;
+          if (cached) {
+            const int nh = hi - key0, nl = lo - key0, ns = a.sinks - key0;
+            w0 = first_bits(nh) & (~first_bits(nl) | first_bits(ns));
+            w1 = first_bits(nh - 64) & (~first_bits(nl - 64) | first_bits(ns - 64));
+          } else {
+            const bool second = j > I.n_prefix;  // nodes 128 ..
+            w0 = second ? anc[2] : anc[0];
+            w1 = second ? anc[3] : anc[1];
+          }
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((w0 >> c) & 1ull)) s[c] = NEG_INF;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((w1 >> c) & 1ull)) s[64 + c] = NEG_INF;
+        }
+        float mk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mk[e] = s[e];
+#pragma unroll
+        for (int c = 8; c < KV_TILE; c += 8)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
+        float mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
+        mx *= a.scale_log2;
+        const float m_new = fmaxf(m_run, mx);
+        const bool rescale = j > 0 && active && m_new > m_run + RESCALE_THRESHOLD;
+        float m_use = m_run;
+        if (j == 0 || rescale) m_use = m_new;
+        const float m_exp = m_use == NEG_INF ? 0.f : m_use;  // nothing visible so far: every weight is 0
+        const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
+        const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
+        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[KV_TILE / 2];
+#pragma unroll
+        for (int e = 0; e < KV_TILE / 2; ++e) {
+          float x0, x1;
+          fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          sum2[e & 3] = fx::add2(sum2[e & 3], fx::pack2(p0, p1));
+          pk[e] = pack_bf16x2(p0, p1);
+        }
+        float rowsum;
+        {
+          float r0, r1;
+          fx::unpack2(fx::add2(fx::add2(sum2[0], sum2[1]), fx::add2(sum2[2], sum2[3])), r0, r1);
+          rowsum = r0 + r1;
+        }
+        {
+          uint32_t part[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[e] = pk[e];
+          tmem_st32(s_tmem, part);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[e] = pk[32 + e];
+          tmem_st32(s_tmem + 32, part);
+        }
+        if (dead) {
+          // V rows that no row of the item sees hold whatever the pool, or the
+          // ring, had there: zeroed, so that 0 * V is 0
+          const int slot = jg % C::NST;
+          if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (jg / C::NST) & 1, ctl))) {
+            ok = false;
+            break;
+          }
+          const int t = key0 + r;
+          if (t >= I.sp.hi || (t < I.sp.lo && t >= a.sinks)) {
+            for (int hh = 0; hh < C::HALVES; ++hh) {
+              uint4* row = reinterpret_cast<uint4*>(sm.v[slot] + ((r >> 3) * C::HALVES + hh) * 1024 + (r & 7) * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async();
+        }
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+          // every earlier PV complete; the whole warp takes part, by 1 where a
+          // row's maximum did not move enough
+          if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float f = !rescale ? 1.f : m_run == NEG_INF ? 0.f : ex2(m_run - m_new);
+          l_run *= f;
+#pragma unroll
+          for (int c = 0; c < D; c += 64) {
+            uint32_t u0[32], u1[32];
+            tmem_ld32(tmem + lane_base + TMEM_O + c, u0);
+            tmem_ld32(tmem + lane_base + TMEM_O + c + 32, u1);
+            tmem_ld_wait();
+            reg_fence32(u0);
+            reg_fence32(u1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u0[e] = __float_as_uint(__uint_as_float(u0[e]) * f);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u1[e] = __float_as_uint(__uint_as_float(u1[e]) * f);
+            tmem_st32(tmem + lane_base + TMEM_O + c, u0);
+            tmem_st32(tmem + lane_base + TMEM_O + c + 32, u1);
+          }
+        }
+        m_run = m_use;
+        l_run += rowsum;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[jg % NSB]);
+      }
+      if (!ok) break;
+      // the item's end: its last PV, then the rows divided and stored
+      if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;  // a row that sees no key: zeros
+      const float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : NEG_INF;
+      const bool direct = I.ps == 1;
+      const PagedSeq& sq = args.seq[I.e];
+      const size_t orow = direct ? (size_t)(I.q0 + i) * a.Hq + I.g * a.G + h_in
+                                 : ((size_t)sq.part_row + (size_t)I.split * sq.rows + i) * a.Hq + I.g * a.G + h_in;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t u[32];
+        tmem_ld32(tmem + lane_base + TMEM_O + c, u);
+        tmem_ld_wait();
+        reg_fence32(u);
+        if (!active) continue;
+        if (direct) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
+          __nv_bfloat16* dst = a.out + orow * D + c;
+          if (args.out32) {
+            st_v8(dst, w);
+            st_v8(dst + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          }
+        } else {
+          float* dst = a.part_o + orow * D + c;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * inv);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) st_v8(dst + 8 * q, u + 8 * q);
+        }
+      }
+      if (active) {
+        if (!direct) a.part_lse[orow] = lse2;
+        else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
+      }
+      // O has been read: the next item's first PV waits for that item's first P
+      tc_fence_before();
+      __syncwarp();
+      if (r == 0) publish(&sm.items_done, k + 1);
+      ok = __all_sync(0xffffffffu, queue_item(k + 1, I));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*ctl.flag) {
+    // A wait gave up: nothing may still write this CTA's shared memory or TMEM
+    // once it exits.
+    if ((warp == K_WARP || warp == V_WARP) && lane == 0) {
+      uint64_t* full = warp == K_WARP ? sm.k_full : sm.v_full;
+      for (int j = max(0, issued - C::NST); j < issued; ++j) mbar_wait(&full[j % C::NST], (j / C::NST) & 1, a.wait_limit_ns);
+    } else if ((warp == QK_WARP || warp == PV_WARP) && lane == 0) {
+      if (q_issued > q_landed) mbar_wait(&sm.q_full, (q_issued - 1) & 1, a.wait_limit_ns);
+      uint64_t* d = &sm.drain[warp - QK_WARP];
+      mma_commit(d);
+      mbar_wait(d, 0, a.wait_limit_ns);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      auto report = [&](int it) {
+        if (it < 0 || !a.status) return;
+        const Place p = place_of(it, args);
+        const int b = args.seq[p.e].b;
+        const Lens l = load_lens<TREE>(b, args.seq[p.e].rows, a);
+        if (make_item<TREE>(p, b, l.q0, l.len, l.kv, args).work) a.status[b] = TS_ERR_TIMEOUT;
+      };
+      const int done = sm.items_done;
+      if (single) {
+        if (done == 0) report(blockIdx.x);
+      } else {
+        for (int k = done; k < sm.items_pub && k < done + ITEM_Q; ++k) {
+          const int b = sm.item_q[k % ITEM_Q][0];
+          if (b >= 0 && a.status) a.status[b] = TS_ERR_TIMEOUT;
+        }
+      }
+      report(held);
+      while (!exhausted) {
+        const int it = take_item();
+        exhausted = it < 0;
+        report(it);
+      }
+    }
+  }
+  pdl_trigger();
+  if (warp == K_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the splits of cut chains: out = sum_s 2^(L_s - M) O_s / sum_s 2^(L_s - M),
+// M = max L_s.  D/8 lanes a row (token, head), 8 channels each; a group of GRP
+// splits' loads is in flight at once.
+constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_GRP = 8;
+
+struct JoinArgs {
+  PagedArgs a;
+  int n_seqs;
+  FastDiv fd_hq;
+  PagedSeq seq[PAGED_MAX_SEQS];  // cut ones only; item0: first (token, head) row of the grid
+};
+
+template <int D, bool TREE>
+__global__ void __launch_bounds__(JOIN_THREADS)
+k_join_paged(const __grid_constant__ JoinArgs t) {
+  constexpr int LPR = D / 8, ROWS = JOIN_THREADS / LPR;
+  const PagedArgs& a = t.a;
+  const int row = blockIdx.x * ROWS + (int)threadIdx.x / LPR;
+  const int sub = (int)threadIdx.x % LPR;
+  int e = 0, hi = t.n_seqs - 1;
+  while (e < hi) {
+    const int mid = (e + hi + 1) >> 1;
+    if (t.seq[mid].item0 <= row) e = mid;
+    else hi = mid - 1;
+  }
+  const PagedSeq& sq = t.seq[e];
+  const int x = row - sq.item0;
+  const int i = t.fd_hq.div(x), h = x - i * a.Hq;
+  pdl_wait();
+  pdl_trigger();
+  if (i >= sq.rows) return;
+  const Lens l = load_lens<TREE>(sq.b, sq.rows, a);
+  if (i >= l.len) return;
+  const PagedSpan sp = TREE ? paged_span(l.kv, l.kv, a.window, a.sinks)
+                            : chunk_span(l.kv, l.len, i / a.tok * a.tok, a.tok, a.window, a.sinks);
+  const int ps = paged_splits(sp.n, a.chunk_tiles, sq.splits);
+  if (ps == 1) return;  // written by the attention kernel
+  const size_t stride = (size_t)sq.rows * a.Hq;  // (token, head) rows of a split
+  const size_t at = ((size_t)sq.part_row + i) * a.Hq + h;
+  float m = NEG_INF, den = 0.f, acc[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+  for (int s0 = 0; s0 < ps; s0 += JOIN_GRP) {
+    float w[JOIN_GRP];
+    float4 x0[JOIN_GRP], x1[JOIN_GRP];
+    float gm = NEG_INF;
+#pragma unroll
+    for (int s = 0; s < JOIN_GRP; ++s) {
+      w[s] = NEG_INF;
+      x0[s] = x1[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + s < ps) {
+        const size_t k = at + (s0 + s) * stride;
+        w[s] = a.part_lse[k];
+        const float4* p = reinterpret_cast<const float4*>(a.part_o + k * D + sub * 8);
+        x0[s] = p[0];
+        x1[s] = p[1];
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < JOIN_GRP; ++s) gm = fmaxf(gm, w[s]);
+    const float m_new = fmaxf(m, gm);
+    if (m_new == NEG_INF) continue;  // nothing visible in these splits
+    const float f = m == NEG_INF ? 0.f : exp2f(m - m_new);
+    den *= f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= f;
+    m = m_new;
+#pragma unroll
+    for (int s = 0; s < JOIN_GRP; ++s) {
+      const float p = exp2f(w[s] - m);
+      den += p;
+      acc[0] = fmaf(p, x0[s].x, acc[0]);
+      acc[1] = fmaf(p, x0[s].y, acc[1]);
+      acc[2] = fmaf(p, x0[s].z, acc[2]);
+      acc[3] = fmaf(p, x0[s].w, acc[3]);
+      acc[4] = fmaf(p, x1[s].x, acc[4]);
+      acc[5] = fmaf(p, x1[s].y, acc[5]);
+      acc[6] = fmaf(p, x1[s].z, acc[6]);
+      acc[7] = fmaf(p, x1[s].w, acc[7]);
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const size_t orow = (size_t)(l.q0 + i) * a.Hq + h;
+  uint32_t o[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) o[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  reinterpret_cast<uint4*>(a.out + orow * D)[sub] = make_uint4(o[0], o[1], o[2], o[3]);
+  if (a.lse && sub == 0) a.lse[orow] = den > 0.f ? (m + log2f(den)) * 0.69314718055994531f : NEG_INF;
+}
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return sizeof(Smem<D>) + 1024;
+}
+
+template <int D, bool TREE>
+cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_items, bool cut, cudaStream_t s) {
+  KArgs t{};
+  t.a = a;
+  t.box_rows = KV_TILE;
+  while (a.bs % t.box_rows != 0) t.box_rows >>= 1;
+  t.n_items = n_items;
+  t.n_seqs = n_seqs;
+  t.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  t.fd_hkv = FastDiv::make(a.Hkv);
+  t.fd_bs = FastDiv::make(a.bs);
+  t.fd_g = FastDiv::make(a.G);
+  std::copy(seq, seq + n_seqs, t.seq);
+  CUtensorMap m_q, m_kc, m_vc, m_kt, m_vt;
+  {  // q [T, Hq, D]: a box of 64 channels, G heads, ROW_TILE / G tokens is 64 channels of 128 rows
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.T};
+    const uint64_t str[2] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2};
+    const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tok};
+    if (!encode_bf16_sw128(&m_q, a.q, 3, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  {  // pool [num_blocks, Hkv, bs, D] as 64 channels, 8 rows, halves, row groups, slabs
+    const uint64_t dims[5] = {64, 8, (uint64_t)(D / 64), (uint64_t)(a.bs / 8), (uint64_t)a.num_blocks * a.Hkv};
+    const uint64_t str[4] = {(uint64_t)D * 2, 128, (uint64_t)8 * D * 2, (uint64_t)a.bs * D * 2};
+    const uint32_t box[5] = {64, 8, (uint32_t)(D / 64), (uint32_t)(t.box_rows / 8), 1};
+    if (!encode_bf16_sw128(&m_kc, a.k_cache, 5, dims, str, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16_sw128(&m_vc, a.v_cache, 5, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  m_kt = m_kc;
+  m_vt = m_vc;
+  if (TREE) {  // tree K/V [B, N, Hkv, D]: 128 nodes of one head; nodes >= N read as zeros
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.Hkv, (uint64_t)a.N, (uint64_t)a.B};
+    const uint64_t str[3] = {(uint64_t)D * 2, (uint64_t)a.Hkv * D * 2, (uint64_t)a.N * a.Hkv * D * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)KV_TILE, 1};
+    if (!encode_bf16_sw128(&m_kt, a.k_tree, 4, dims, str, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16_sw128(&m_vt, a.v_tree, 4, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  int ctas = sm_count();
+  if (ctas <= 0) return cudaErrorInvalidDevice;
+  if (a.max_ctas > 0 && a.max_ctas < ctas) ctas = a.max_ctas;
+  const dim3 grid(n_items < ctas ? n_items : ctas);
+  cudaError_t e = launch_pdl(k_attn_paged<D, TREE>, grid, dim3(NUM_THREADS), smem_bytes<D>(), s, t, m_q, m_kc, m_vc,
+                             m_kt, m_vt);
+  if (e != cudaSuccess || !cut) return e;
+  JoinArgs j{};
+  j.a = a;
+  j.fd_hq = FastDiv::make(a.Hq);
+  int rows = 0;
+  for (int k = 0; k < n_seqs; ++k) {
+    if (seq[k].splits == 1) continue;
+    j.seq[j.n_seqs] = seq[k];
+    j.seq[j.n_seqs++].item0 = rows;
+    rows += seq[k].rows * a.Hq;
+  }
+  const int per = JOIN_THREADS / (D / 8);
+  return launch_pdl(k_join_paged<D, TREE>, dim3(ceil_div(rows, per)), dim3(JOIN_THREADS), 0, s, j);
+}
+
+// The plan of a launch's sequences: how long a split may be.  Every chain of key
+// tiles (a row tile of a KV head) is an item or, cut, several; a CTA an SM takes
+// them longest first.  In units of a tile's time on an SM, an item costs its
+// tiles and 1.5 more, the launch ends when the SMs have shared all of that out
+// and the last items have run, and cut chains cost a second kernel and their
+// partial results' round trip (3.6 MB of traffic in a tile's time; the same
+// prices as tree attention's plan).
+struct Chains {
+  int count;     // row tiles
+  int most;      // tiles of the longest chain
+  double total;  // tiles of all
+};
+
+int plan_chunk_tiles(const Chains* c, const int* rows, int n, int Hkv, int Hq, int D, int tree_tiles) {
+  int longest = 1;
+  for (int k = 0; k < n; ++k) longest = std::max(longest, c[k].most);
+  double best = 1e300;
+  int best_chunk = longest, last = 0;
+  for (int s = 1; s <= 256; s += 1 + s / 8) {
+    const int chunk = ceil_div(longest, s);
+    if (chunk == last) continue;
+    last = chunk;
+    double items = 0, tiles = 0, part_rows = 0, worst = 0;
+    for (int k = 0; k < n; ++k) {
+      const int ps = paged_splits(c[k].most, chunk, INT_MAX);
+      items += (double)c[k].count * ps;
+      tiles += c[k].total + (double)c[k].count * tree_tiles;
+      worst = std::max(worst, (double)ceil_div(c[k].most, ps) + tree_tiles);
+      if (ps > 1) part_rows += (double)ps * rows[k];
+    }
+    items *= Hkv;
+    tiles *= Hkv;
+    const double item = (tiles + 1.5 * items) / items;  // an average item
+    const double waves = items / PLAN_SMS;
+    double cost = std::max(worst + 1.5, item * (waves > 1 ? waves + 0.5 : 1.0));
+    if (part_rows > 0) cost += 4.0 + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / 3.6e6;
+    if (cost < best) {
+      best = cost;
+      best_chunk = chunk;
+    }
+    if (chunk == 1) break;
+  }
+  return best_chunk;
+}
+
+// Sequences [b0, b1) of a call: their entries (in the order the items are taken),
+// and what the launch needs.  rows_of(b), kv_of(b): tokens here, and in the cache.
+struct LaunchPlan {
+  PagedSeq seq[PAGED_MAX_SEQS];
+  int n_seqs, n_items, chunk_tiles, b_end;
+  long long part_rows;  // tokens' rows of partial results
+  bool ok;
+};
+
+template <bool TREE>
+void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, int b0, LaunchPlan* pl) {
+  Chains c[PAGED_MAX_SEQS];
+  int rows[PAGED_MAX_SEQS], bs[PAGED_MAX_SEQS], order[PAGED_MAX_SEQS];
+  int n = 0, b = b0;
+  for (; b < a.B && n < PAGED_MAX_SEQS; ++b) {
+    const int len = TREE ? a.N : cu_len_host[b + 1] - cu_len_host[b];
+    if (len == 0) continue;
+    const int kv = kv_host[b];
+    rows[n] = len;
+    bs[n] = b;
+    c[n].count = ceil_div(len, a.tok);
+    if (TREE) {
+      c[n].most = paged_span(kv, kv, a.window, a.sinks).n;
+      c[n].total = (double)c[n].most * c[n].count;
+    } else {
+      const int first = chunk_span(kv, len, 0, a.tok, a.window, a.sinks).n;
+      const int last = chunk_span(kv, len, (c[n].count - 1) * a.tok, a.tok, a.window, a.sinks).n;
+      c[n].most = std::max(std::max(first, last), 1);
+      // a window's chains may be a tile longer or shorter in between
+      if (a.window > 0 && c[n].count > 2)
+        c[n].most = std::max(c[n].most, std::min(ceil_div(kv, KV_TILE), ceil_div(a.window + a.tok, KV_TILE) + 1 + ceil_div(a.sinks, KV_TILE)));
+      c[n].total = 0.5 * (first + last) * c[n].count;
+    }
+    order[n] = n;
+    ++n;
+  }
+  pl->b_end = b;
+  pl->n_seqs = n;
+  pl->n_items = 0;
+  pl->part_rows = 0;
+  pl->chunk_tiles = 1;
+  pl->ok = true;
+  if (n == 0) return;
+  const int tree_tiles = TREE ? ceil_div(a.N, KV_TILE) : 0;
+  pl->chunk_tiles = plan_chunk_tiles(c, rows, n, a.Hkv, a.Hq, a.D, tree_tiles);
+  int each[PAGED_MAX_SEQS];
+  for (int k = 0; k < n; ++k) {
+    const int ps = paged_splits(c[k].most, pl->chunk_tiles, INT_MAX);
+    each[k] = ceil_div(c[k].most, ps);
+  }
+  std::stable_sort(order, order + n, [&](int x, int y) { return each[x] > each[y]; });
+  long long items = 0, part = 0;
+  for (int k = 0; k < n; ++k) {
+    const int x = order[k];
+    PagedSeq& q = pl->seq[k];
+    q.item0 = (int)items;
+    q.b = bs[x];
+    q.row_tiles = c[x].count;
+    q.splits = paged_splits(c[x].most, pl->chunk_tiles, INT_MAX);
+    q.rows = rows[x];
+    q.part_row = (int)part;
+    items += (long long)q.row_tiles * q.splits * a.Hkv;
+    if (q.splits > 1) part += (long long)q.splits * q.rows;
+    if (items > (1ll << 30) || part * a.Hq >= (1ll << 31)) pl->ok = false;
+  }
+  pl->n_items = (int)items;
+  pl->part_rows = part;
+}
+
+template <bool TREE>
+size_t workspace_of(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host) {
+  long long most = 0;
+  for (int b = 0; b < a.B;) {
+    LaunchPlan pl;
+    plan_launch<TREE>(a, cu_len_host, kv_host, b, &pl);
+    if (!pl.ok) return 0;
+    most = std::max(most, pl.part_rows);
+    b = pl.b_end;
+  }
+  return ATTN_SCHED_BYTES + (size_t)most * a.Hq * (4 * a.D + 4);
+}
+
+template <bool TREE>
+cudaError_t run(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace, cudaStream_t s) {
+  a.sched = static_cast<unsigned*>(workspace);
+  for (int b = 0; b < a.B;) {
+    LaunchPlan pl;
+    plan_launch<TREE>(a, cu_len_host, kv_host, b, &pl);
+    if (!pl.ok) return cudaErrorInvalidValue;
+    b = pl.b_end;
+    if (pl.n_items == 0) continue;
+    a.chunk_tiles = pl.chunk_tiles;
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ATTN_SCHED_BYTES);
+    a.part_lse = a.part_o + (size_t)pl.part_rows * a.Hq * a.D;
+    const cudaError_t e = a.D == 128 ? launch<128, TREE>(a, pl.seq, pl.n_seqs, pl.n_items, pl.part_rows > 0, s)
+                                     : launch<64, TREE>(a, pl.seq, pl.n_seqs, pl.n_items, pl.part_rows > 0, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int D, bool TREE>
+cudaError_t opt_in() {
+  return cudaFuncSetAttribute(k_attn_paged<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+}
+
+}  // namespace
+
+cudaError_t attn_paged_prepare() {
+  cudaError_t e = opt_in<128, false>();
+  if (e == cudaSuccess) e = opt_in<128, true>();
+  if (e == cudaSuccess) e = opt_in<64, false>();
+  if (e == cudaSuccess) e = opt_in<64, true>();
+  return e;
+}
+
+size_t attn_paged_workspace(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host) {
+  return cu_len_host ? workspace_of<false>(a, cu_len_host, kv_host) : workspace_of<true>(a, cu_len_host, kv_host);
+}
+
+cudaError_t launch_attn_paged(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace,
+                              cudaStream_t s) {
+  return cu_len_host ? run<false>(a, cu_len_host, kv_host, workspace, s) : run<true>(a, cu_len_host, kv_host, workspace, s);
+}
+
+}  // namespace ts

@@ -9,6 +9,7 @@
 #include "quant_row.cuh"
 #include "sm100.cuh"
 #include "tensor_map.cuh"
+#include "waits.cuh"
 
 namespace ts {
 
@@ -82,62 +83,6 @@ __host__ __device__ __forceinline__ int seq_of(int chain, const Q8Args& t) {
   return t.fd_hkv.div(u);
 }
 
-struct Ctl {
-  volatile int* flag;
-  uint64_t limit;
-};
-// Bounded waits that also give up as soon as another role has aborted.  The
-// polling is out of line: inlined at some twenty places, with the clock and the
-// flag, it makes the kernel half as large again, and the warps at work wait for
-// instructions (1.40 against 1.09 ms on 64 sequences of 8K tokens).
-static __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* flag, uint64_t limit) {
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-    }
-    if (*flag) return false;
-    if (globaltimer_ns() - t0 > limit) {
-      *flag = 1;
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Ctl& c) {
-  return mbar_try_wait(bar, parity) || wait_more(bar, parity, c.flag, c.limit);
-}
-static __device__ __noinline__ bool wait_count(const int* counter, int target, volatile int* flag, uint64_t limit) {
-  const uint32_t addr = smem_u32(counter);
-  uint64_t t0 = 0;
-#pragma unroll 1
-  for (int i = 0;; ++i) {
-    int v;
-    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    if (v >= target) return true;
-    if ((i & 15) == 15) {
-      if (*flag) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > limit) {
-        *flag = 1;
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool wait_count(const int* counter, int target, const Ctl& c) {
-  return wait_count(counter, target, c.flag, c.limit);
-}
-__device__ __forceinline__ void publish(int* counter, int v) {
-  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(counter)), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float pow2_of(int biased) { return __uint_as_float((uint32_t)biased << 23); }
 
 // A row's power of two as the multipliers of widen16: 2^(s - 127) * 2^120 in

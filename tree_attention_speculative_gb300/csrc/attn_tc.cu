@@ -1001,20 +1001,6 @@ constexpr size_t smem_bytes() {
   return sizeof(Smem<D>) + 1024;  // + alignment slack for the 1024-byte swizzle atoms
 }
 
-// Streaming multiprocessors of the current device (queried once per device).
-int sm_count() {
-  static int cache[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  if (dev < 0 || dev >= 64) return -1;
-  if (cache[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 template <int D>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
   TcArgs t{};

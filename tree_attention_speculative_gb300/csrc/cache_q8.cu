@@ -16,6 +16,7 @@
 // k_commit_q8: one CTA a sequence, which checks every destination before it
 // writes any, so a sequence is never left half-committed; the new length is
 // written after a barrier, so it may alias the old one.
+#include "append.cuh"
 #include "quant_row.cuh"
 
 namespace ts {
@@ -24,7 +25,6 @@ namespace {
 constexpr int APPEND_THREADS = 256;
 constexpr int APPEND_MAX_ROWS = 64;  // (token, head) rows a CTA at most, K and V each
 constexpr int COMMIT_Q8_THREADS = 512;
-constexpr int MAX_LEN = 1 << 30;     // positions stay far inside 32 bits
 
 // Eight CTAs an SM (32 registers): 149K tokens of 8 heads of 128 in 127 us, 6.7
 // TB/s, against 134 us with five (45 registers; 16 tokens then take 3.1 us, not 3.4).
@@ -42,33 +42,7 @@ k_append_q8(const __grid_constant__ AppendArgs a, FastDiv heads) {
   if ((int)blockIdx.x < a.len_ctas) {  // a warp a sequence: its blocks and its new length
     const int b = blockIdx.x * (APPEND_THREADS / 32) + warp;
     if (b >= a.B) return;
-    const int P = a.prefix_len[b], c0 = a.cu_len[b], c1 = a.cu_len[b + 1];
-    const int st = a.status ? a.status[b] : TS_OK;
-    // its rows are its own: no sequence before it ends, and none after it begins, among them
-    bool own = true;
-#pragma unroll 4
-    for (int i = lane; i <= a.B; i += 32) {
-      const int c = a.cu_len[i];
-      own = own && (i <= b ? c <= c0 : c >= c1);
-    }
-    own = __all_sync(0xffffffffu, own);
-    const bool sized = own && P >= 0 && P <= MAX_LEN && c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= MAX_LEN - P;
-    bool ok = sized;
-    if (sized && c1 > c0) {
-      const int last = (P + (c1 - c0) - 1) / a.bs;
-      for (int i = P / a.bs + lane; i <= last; i += 32) {
-        const int blk = i < a.max_blocks ? a.block_table[(size_t)b * a.max_blocks + i] : -1;
-        if (blk < 0 || blk >= a.num_blocks) {
-          ok = false;
-          break;
-        }
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (lane == 0) {
-      a.new_prefix_len[b] = ok && st == TS_OK ? P + (c1 - c0) : P;
-      if (!ok && st == TS_OK && a.status) a.status[b] = sized ? TS_ERR_BAD_BLOCK : TS_ERR_SHAPE;
-    }
+    append_sequence(a, b, lane);
     return;
   }
 
@@ -95,28 +69,7 @@ k_append_q8(const __grid_constant__ AppendArgs a, FastDiv heads) {
     }
   };
   load(grp);
-  if ((int)threadIdx.x < ntok) {
-    const int t = t0 + threadIdx.x;
-    // the sequence b with cu_len[b] <= t < cu_len[b + 1]
-    int lo = 0, hi = a.B;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu_len[mid + 1] <= t) lo = mid + 1;
-      else hi = mid;
-    }
-    long long row = -1;
-    if (lo < a.B) {
-      const int c0 = a.cu_len[lo], c1 = a.cu_len[lo + 1], P = a.prefix_len[lo];
-      const int st = a.status ? a.status[lo] : TS_OK;
-      if (st == TS_OK && c0 >= 0 && t >= c0 && t < c1 && P >= 0 && P <= MAX_LEN && c1 - c0 <= MAX_LEN - P) {
-        const int p = P + (t - c0);
-        const int i = p / a.bs;
-        const int blk = i < a.max_blocks ? a.block_table[(size_t)lo * a.max_blocks + i] : -1;
-        if (blk >= 0 && blk < a.num_blocks) row = (long long)blk * a.Hkv * a.bs + (p - i * a.bs);
-      }
-    }
-    dest[threadIdx.x] = row;
-  }
+  if ((int)threadIdx.x < ntok) dest[threadIdx.x] = append_place(a, t0 + threadIdx.x).row;
   __syncthreads();
   const int rounds = (n + GROUPS * UN - 1) / (GROUPS * UN);  // the same on every lane: the shuffles need them all
   for (int it = 0; it < rounds; ++it) {
@@ -156,7 +109,7 @@ k_commit_q8(const __grid_constant__ CommitQ8Args a, FastDiv heads) {
   const int L = a.accept_len[b];
   const int st = a.status ? a.status[b] : TS_OK;
   // a path has at most N steps
-  const bool commit = st == TS_OK && L >= 0 && L <= a.max_depth && L < a.N && P >= 0 && P <= MAX_LEN;
+  const bool commit = st == TS_OK && L >= 0 && L <= a.max_depth && L < a.N && P >= 0 && P <= APPEND_MAX_LEN;
   const int steps = commit ? L + 1 : 0;
   bool ok = true;
   if ((int)threadIdx.x < steps) {

@@ -42,6 +42,20 @@ constexpr int ROW_TILE = 128;
 constexpr int MAX_NODES = 256;
 constexpr int PLAN_SMS = 152;  // GB300: the planner sizes grids for 152 SMs
 
+// Streaming multiprocessors of the current device (queried once per device).
+inline int sm_count() {
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev < 0 || dev >= 64) return -1;
+  if (cache[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Division by a divisor fixed for a whole launch, for numerators in [0, 2^31),
@@ -289,6 +303,49 @@ struct AppendArgs {
   int len_ctas;                // CTAs that check the sequences and write their lengths
 };
 cudaError_t launch_append_q8(AppendArgs a, cudaStream_t s);
+
+// Appending with rotary positions: q and k turned at their positions, k and v
+// written to the cache (strides in elements).
+struct AppendRopeArgs {
+  const __nv_bfloat16* q;  // null: no queries, Hq is 0
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;
+  void* k_cache;
+  void* v_cache;
+  uint8_t* kv_scale;  // null: a bf16 cache
+  const int32_t* cu_len;
+  const int32_t* prefix_len;
+  const int32_t* block_table;
+  int32_t* new_prefix_len;
+  int32_t* status;
+  int B, T, Hq, Hkv, D, bs, num_blocks, max_blocks;
+  int R, interleaved;  // R = 0: nothing turns
+  long long q_token, q_head, k_token, k_head, v_token, v_head;
+  float mscale;
+  int tok;       // tokens a CTA
+  int len_ctas;  // CTAs that check the sequences and write their lengths
+  uint64_t turn[64];  // RopeArgs
+};
+cudaError_t launch_append_rope(AppendRopeArgs a, cudaStream_t s);
+
+// Log probabilities of given tokens (treespec.h: tree_token_logprobs).
+struct LogprobArgs {
+  const void* logits;
+  const int32_t* tokens;
+  const int32_t* rows;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  long long row_stride;  // elements
+  int R, M, V, top, half;
+  float inv_temp_log2e;  // log2(e) / temperature
+  int slice;             // vectors a CTA of the row's cluster
+};
+constexpr int LOGPROB_MAX_TOP = 32;
+constexpr int LOGPROB_MAX_V = 8 * (65536 - 8);  // a cluster of 8 CTAs, 16384 vectors of 4 each, wherever the row starts
+cudaError_t launch_logprobs(LogprobArgs a, cudaStream_t s);
 
 struct CommitQ8Args {
   const __nv_bfloat16* k_tree;

@@ -35,21 +35,23 @@ __device__ __forceinline__ uint32_t q8_max2_nan(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// LANES consecutive lanes hold a row, 8 values each: this lane's 8 codes, and
-// the row's scale byte on each of them.  All 32 lanes take part.
+// Magnitudes of this lane's 8 values, folded to one pair.
+__device__ __forceinline__ uint32_t q8_fold(const uint4& x) {
+  return q8_max2_nan(q8_max2_nan(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), q8_max2_nan(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+}
+
+// The bf16 bits of the largest magnitude of a row that LANES consecutive lanes
+// hold, from their folded pairs.  All 32 lanes take part.
 template <int LANES>
-__device__ __forceinline__ uint2 q8_row(const uint4& x, int* scale_byte) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = q8_max2_nan(q8_max2_nan(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                           q8_max2_nan(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+__device__ __forceinline__ uint32_t q8_row_max(uint32_t m) {
 #pragma unroll
   for (int d = LANES / 2; d > 0; d >>= 1) m = q8_max2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-  m = q8_max2_nan(m, m >> 16) & 0x7fffu;
-  if (m > 0x7f80u) {
-    *scale_byte = Q8_NAN_SCALE;
-    return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-  }
-  const int s = q8_scale_byte(m);
+  return q8_max2_nan(m, m >> 16) & 0x7fffu;
+}
+
+// The codes of 8 values in a row with scale byte s.
+__device__ __forceinline__ uint2 q8_codes(const uint4& x, int s) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   const float inv = __uint_as_float((uint32_t)(254 - s) << 23);  // 2^(127 - s)
   uint32_t c[4];
 #pragma unroll
@@ -57,8 +59,20 @@ __device__ __forceinline__ uint2 q8_row(const uint4& x, int* scale_byte) {
     const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
     c[k] = __nv_cvt_float2_to_fp8x2(make_float2(f.x * inv, f.y * inv), __NV_SATFINITE, __NV_E4M3);
   }
-  *scale_byte = s;
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// LANES consecutive lanes hold a row, 8 values each: this lane's 8 codes, and
+// the row's scale byte on each of them.  All 32 lanes take part.
+template <int LANES>
+__device__ __forceinline__ uint2 q8_row(const uint4& x, int* scale_byte) {
+  const uint32_t m = q8_row_max<LANES>(q8_fold(x));
+  if (m > 0x7f80u) {
+    *scale_byte = Q8_NAN_SCALE;
+    return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  *scale_byte = q8_scale_byte(m);
+  return q8_codes(x, *scale_byte);
 }
 
 }  // namespace ts
