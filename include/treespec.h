@@ -767,8 +767,8 @@ TS_API ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* worksp
  * with depth - depth_a < window or P_b + depth_a < sinks.  window >= 1.
  * Arguments, outputs and errors are tree_attn_fwd's, over the bf16 cache; a row that
  * sees no key gives zeros and an lse of -inf.  Blocks that no node sees into are not
- * followed.  Nodes that no row sees may hold anything; the value of one that some
- * rows see must be finite.  In a captured call prefix_len may have changed when it is
+ * followed.  The key of a node may hold anything for the rows it is hidden from; its
+ * value must be finite.  In a captured call prefix_len may have changed when it is
  * replayed; one outside the table's row gets TS_ERR_SHAPE and nothing written.
  * workspace: tree_attn_window_workspace_size bytes, as tree_chunk_attn_fwd's, and may
  * be shared with it.
@@ -800,9 +800,9 @@ TS_API ts_status tree_attn_fwd_window(const ts_attn_params* p, int window, int s
  *                 NULL; both are with top = 0.  Tokens of probability 0 (-inf) are no
  *                 alternatives: id -1, log probability -inf.
  * A row of nothing but -inf gives logprob -inf, entropy 0 and no alternatives.
- * fp32 arithmetic; outputs are within 2^-20 of max(1, |value|) or so.  Calls repeat
- * bit for bit.
- * R may be 0.  No workspace.  Returns TS_ERR_NULL / TS_ERR_SHAPE (temperature not
+ * fp32 arithmetic: a log probability or entropy is within 2^-15 plus 2^-22 of its
+ * magnitude (2^-21 is usual).  Calls repeat bit for bit.
+ * R may be 0 (the pointers may then be NULL).  No workspace.  Returns TS_ERR_NULL / TS_ERR_SHAPE (temperature not
  * positive and finite, R over M without rows) / TS_ERR_UNSUPPORTED (V over 524224,
  * top over 32, R over 2^28) / TS_ERR_CUDA.
  */

@@ -28,13 +28,15 @@ Modules:
   dynamic    — reranking a draft's candidate pool into the tree to verify.
   forest     — several roots in one flattened sequence: masks and acceptance.
   rope       — rotary positions of queries and keys, fp64.
+  window     — attention of a chunk of cached tokens, and of a tree in a windowed layer.
+  logprobs   — log probabilities of tokens, entropies, most likely alternatives.
   cache_q8   — rows of the 8-bit cache: codes, scale bytes and their values.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test against
 the pages' worked example, closed forms, library routines on special cases, or
 brute force (see tests/test_oracle_*.py).  No function is "parity unpinned".
 """
-from . import tree, attention, verify, commit, stochastic, dynamic, forest, rope, cache_q8  # noqa: F401
+from . import tree, attention, verify, commit, stochastic, dynamic, forest, rope, cache_q8, window, logprobs  # noqa: F401
 
 # Status codes, restated here (the oracle shares no header with the library).
 OK = 0

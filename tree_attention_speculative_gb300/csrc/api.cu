@@ -948,10 +948,12 @@ ts_status tree_attn_fwd_window(const ts_attn_params* p, int window, int sinks, v
 }
 
 ts_status tree_token_logprobs(const ts_logprob_params* p, ts_stream stream) {
-  if (!p || (p->R > 0 && !p->logits)) return TS_ERR_NULL;
-  if ((p->tokens == nullptr) != (p->logprob == nullptr)) return TS_ERR_NULL;
-  if (!p->logprob && !p->entropy && !p->top_ids && !p->top_logprobs) return TS_ERR_NULL;
-  if (p->top > 0 ? !p->top_ids && !p->top_logprobs : p->top_ids || p->top_logprobs) return TS_ERR_NULL;
+  if (!p) return TS_ERR_NULL;
+  if (p->R > 0) {
+    if (!p->logits || (p->tokens == nullptr) != (p->logprob == nullptr)) return TS_ERR_NULL;
+    if (!p->logprob && !p->entropy && !p->top_ids && !p->top_logprobs) return TS_ERR_NULL;
+    if (p->top > 0 ? !p->top_ids && !p->top_logprobs : p->top_ids || p->top_logprobs) return TS_ERR_NULL;
+  }
   if (p->R < 0 || p->M < 0 || p->V < 1 || p->top < 0 || (!p->rows && p->R > p->M)) return TS_ERR_SHAPE;
   if (p->V > LOGPROB_MAX_V || p->top > LOGPROB_MAX_TOP || p->R > (1 << 28)) return TS_ERR_UNSUPPORTED;
   if (p->row_stride != 0 && p->row_stride < p->V) return TS_ERR_SHAPE;
@@ -959,7 +961,7 @@ ts_status tree_token_logprobs(const ts_logprob_params* p, ts_stream stream) {
   const uintptr_t size = p->half ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(p->logits) % size) return TS_ERR_SHAPE;
   const float k = 1.4426950408889634f / p->temperature;
-  if (!positive(k)) return TS_ERR_SHAPE;
+  if (!positive(k)) return TS_ERR_SHAPE;  // (a temperature next to 0, or past 2^126)
   if (p->R == 0) return TS_OK;
   LogprobArgs a{};
   a.logits = p->logits;
@@ -971,6 +973,7 @@ ts_status tree_token_logprobs(const ts_logprob_params* p, ts_stream stream) {
   a.top_logprobs = p->top_logprobs;
   a.row_stride = p->row_stride ? p->row_stride : p->V;
   a.R = p->R; a.M = p->M; a.V = p->V; a.top = p->top; a.half = p->half;
+  a.inv_temp = 1.f / p->temperature;
   a.inv_temp_log2e = k;
   return launch_logprobs(a, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
 }

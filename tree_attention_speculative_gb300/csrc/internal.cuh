@@ -340,8 +340,8 @@ struct LogprobArgs {
   float* top_logprobs;
   long long row_stride;  // elements
   int R, M, V, top, half;
-  float inv_temp_log2e;  // log2(e) / temperature
-  int slice;             // vectors a CTA of the row's cluster
+  float inv_temp, inv_temp_log2e;  // 1 / temperature, log2(e) / temperature
+  int slice;  // vectors a CTA of the row's cluster
 };
 constexpr int LOGPROB_MAX_TOP = 32;
 constexpr int LOGPROB_MAX_V = 8 * (65536 - 8);  // a cluster of 8 CTAs, 16384 vectors of 4 each, wherever the row starts

@@ -2,7 +2,7 @@
 // rows of logits, in one pass over the rows.
 //
 // With y = (x - m) log2(e) / temperature over a row, m its maximum,
-//   S = sum 2^y,  U = sum 2^y y:   log p(x) = ln 2 (y - log2 S),
+//   S = sum 2^y,  U = sum 2^y y:   log p(x) = (x - m) / temperature - ln 2 log2 S,
 //                                  entropy  = ln 2 (log2 S - U / S).
 // Each thread keeps m, S and U of its values (rescaled when its m grows), which are
 // joined over the CTA and over the row's cluster.  All terms of U have one sign.
@@ -364,7 +364,7 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
       if (a.logprob) {
         const int t = a.tokens[r];
         float lp = t == -1 ? 0.f : NAN;
-        if (t >= 0 && t < a.V) lp = empty ? -INFINITY : ((widen(row.x[t]) - b.m) * k - ls) * LN2;
+        if (t >= 0 && t < a.V) lp = empty ? -INFINITY : (widen(row.x[t]) - b.m) * a.inv_temp - ls * LN2;
         a.logprob[r] = lp;
       }
       if (a.entropy) a.entropy[r] = empty ? 0.f : (ls - b.u / b.s) * LN2;
@@ -373,7 +373,7 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
       const unsigned long long key = sh.best[tid];
       const size_t at = (size_t)r * top + tid;
       if (a.top_ids) a.top_ids[at] = key ? (int)(0xffffffffu - (uint32_t)key) : -1;
-      if (a.top_logprobs) a.top_logprobs[at] = key ? ((unordered((uint32_t)(key >> 32)) - b.m) * k - ls) * LN2 : -INFINITY;
+      if (a.top_logprobs) a.top_logprobs[at] = key ? (unordered((uint32_t)(key >> 32)) - b.m) * a.inv_temp - ls * LN2 : -INFINITY;
     }
   }
   if (ranks > 1) cluster.sync();  // the CTAs' shared memory stays until it has been read

@@ -1,4 +1,4 @@
-"""One verification step on the GPU: device buffers plus the three library calls.
+"""Steps on the GPU: device buffers plus the library's calls.
 
 ``TreeVerifyStep`` owns the output and workspace buffers (allocated with torch,
 which is only the allocator here) for fixed sizes and enqueues
@@ -6,7 +6,15 @@ tree_build_ancestry -> tree_attn_fwd -> tree_verify_greedy on one stream (their
 _forest variants with ``forest=True``).  With a ``rope`` configuration it
 positions q and k_tree in between (tree_rope), with ``kv_scale`` it reads an
 8-bit cache (tree_attn_fwd_q8), and ``commit`` appends the accepted path to
-either cache.  Every computation happens in the library's kernels.
+either cache.  With a ``window`` it is the step of a windowed layer
+(tree_attn_fwd_window), and ``logprobs`` scores the accepted path
+(tree_token_logprobs).  Every computation happens in the library's kernels (the
+accepted path's rows are picked with a few of torch's index operations).
+
+``PromptStep`` is the step that fills the cache: a ragged batch of prompts, chunks of
+them or decoded tokens goes through tree_cache_append_rope, tree_chunk_attn_fwd
+and, for its logits, tree_token_logprobs.
+
 ``PackedInputs`` stages a step's inputs from host memory in one copy.
 """
 from __future__ import annotations
@@ -16,10 +24,11 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (RopeConfig, attn_params, tree_attn_fwd, tree_attn_fwd_q8, tree_attn_q8_workspace_size,
-               tree_attn_workspace_size, tree_build_ancestry, tree_build_ancestry_forest, tree_commit_accepted,
-               tree_commit_accepted_q8, tree_rope, tree_verify_greedy, tree_verify_greedy_forest,
-               tree_verify_workspace_size)
+from . import (RopeConfig, attn_params, chunk_params, tree_attn_fwd, tree_attn_fwd_q8, tree_attn_fwd_window,
+               tree_attn_q8_workspace_size, tree_attn_window_workspace_size, tree_attn_workspace_size,
+               tree_build_ancestry, tree_build_ancestry_forest, tree_cache_append_rope, tree_chunk_attn_fwd,
+               tree_chunk_attn_workspace_size, tree_commit_accepted, tree_commit_accepted_q8, tree_rope,
+               tree_token_logprobs, tree_verify_greedy, tree_verify_greedy_forest, tree_verify_workspace_size)
 
 
 class PackedInputs:
@@ -66,15 +75,40 @@ class PackedInputs:
             self.dev.copy_(self.host, non_blocking=True)
 
 
+def _grown(step, name: str, need: int) -> torch.Tensor:
+    """The step's workspace of that name, of ``need`` bytes at least.  One that grew too
+    small stays allocated: captured calls still write to it."""
+    ws = getattr(step, name)
+    if ws is None or ws.numel() < need:
+        if ws is not None:
+            step.outgrown.append(ws)
+            need = max(need, 2 * ws.numel())  # so that what is kept stays below the one in use
+        # zero-filled once; every call leaves its head (the item counter) zero again
+        ws = torch.zeros(need, dtype=torch.uint8, device=step.device)
+        setattr(step, name, ws)
+    return ws
+
+
+class _Scores:
+    """Outputs of tree_token_logprobs for ``rows`` rows."""
+
+    def __init__(self, rows: int, top: int, device):
+        f32 = dict(dtype=torch.float32, device=device)
+        self.logprob, self.entropy = torch.zeros(rows, **f32), torch.zeros(rows, **f32)
+        self.top_ids = torch.full((rows, top), -1, dtype=torch.int32, device=device) if top else None
+        self.top_logprobs = torch.zeros(rows, top, **f32) if top else None
+
+
 class TreeVerifyStep:
     def __init__(self, B: int, N: int, Hq: int, Hkv: int, D: int, prefix_len_host, vocab: int = 0,
                  max_depth: Optional[int] = None, device="cuda", scale: float = 0.0, forest: bool = False,
-                 rope: Optional[RopeConfig] = None):
+                 rope: Optional[RopeConfig] = None, window: int = 0, sinks: int = 0):
         self.B, self.N, self.Hq, self.Hkv, self.D = B, N, Hq, Hkv, D
         self.forest = forest
         self.vocab = vocab
         self.max_depth = N - 1 if max_depth is None else max_depth
         self.scale = scale
+        self.window, self.sinks = window, sinks  # a window of 0: every prefix token is visible
         self.device = torch.device(device)
         self.prefix_len_host = np.ascontiguousarray(np.asarray(prefix_len_host, np.int32))
         W = (N + 63) // 64
@@ -123,19 +157,18 @@ class TreeVerifyStep:
 
     def attention(self, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, stream=None, kv_scale=None):
         p = self._params(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree)
-        need = tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
+        if self.window and kv_scale is not None:
+            raise ValueError("a windowed layer's cache is bf16")
+        if self.window:
+            need = tree_attn_window_workspace_size(p, self.window, self.sinks)
+        else:
+            need = tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
         if need == 0:
             raise ValueError("tree_attn_fwd would reject these arguments")
-        name = "ws_attn" if kv_scale is None else "ws_attn_q8"
-        ws = getattr(self, name)
-        if ws is None or ws.numel() < need:
-            if ws is not None:
-                self.outgrown.append(ws)
-                need = max(need, 2 * ws.numel())  # so that what is kept stays below the one in use
-            # zero-filled once; every call leaves its head (the item counter) zero again
-            ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
-            setattr(self, name, ws)
-        if kv_scale is None:
+        ws = _grown(self, "ws_attn" if kv_scale is None else "ws_attn_q8", need)
+        if self.window:
+            tree_attn_fwd_window(p, self.window, self.sinks, ws, stream)
+        elif kv_scale is None:
             tree_attn_fwd(p, ws, stream)
         else:
             tree_attn_fwd_q8(p, kv_scale, ws, stream)
@@ -165,3 +198,72 @@ class TreeVerifyStep:
         else:
             tree_commit_accepted_q8(k, v_tree, self.accepted, self.accept_len, prefix_len, k_cache, v_cache, kv_scale,
                                     block_table, new_prefix_len, self.status, stream)
+
+    def logprobs(self, draft, logits, temperature: float = 1.0, top: int = 0, stream=None) -> _Scores:
+        """Log probabilities of the tokens the last ``run`` emitted: row b (max_depth + 1)
+        + d scores the token after path step d, the next accepted draft or at the end
+        the bonus, under that step's logits.  Rows past a path stay 0 (ids -1)."""
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+            path, after = self.accepted, torch.cat((self.accepted[:, 1:], self.accepted.new_full((self.B, 1), -1)), 1)
+            base = torch.arange(self.B, dtype=torch.int32, device=self.device)[:, None] * self.N
+            rows = torch.where(path >= 0, base + path, -1).view(-1)
+            tokens = torch.where(after >= 0, draft.gather(1, after.clamp(min=0).long()), self.bonus[:, None])
+            out = _Scores(rows.numel(), top, self.device)
+            tree_token_logprobs(logits, tokens.int().view(-1).contiguous(), out.logprob, out.entropy, out.top_ids,
+                                out.top_logprobs, rows=rows.contiguous(), temperature=temperature)
+        return out
+
+
+class PromptStep:
+    """One layer's pass over a ragged batch of new tokens (sequence b's are rows
+    cu_len[b] .. cu_len[b+1]-1, at most ``max_tokens`` in all): ``run`` appends them to
+    the paged cache with their rotary positions and attends; ``score`` gives the
+    log probabilities of the tokens that followed.  ``window`` and ``sinks`` are those
+    of a windowed layer (0: none)."""
+
+    def __init__(self, B: int, max_tokens: int, Hq: int, Hkv: int, D: int, rope: RopeConfig, device="cuda",
+                 scale: float = 0.0, window: int = 0, sinks: int = 0):
+        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        self.rope, self.scale, self.window, self.sinks = rope, scale, window, sinks
+        self.device = dev = torch.device(device)
+        self.q_rot = torch.zeros(max_tokens, Hq, D, dtype=torch.bfloat16, device=dev)
+        self.out = torch.zeros(max_tokens, Hq, D, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros(max_tokens, Hq, dtype=torch.float32, device=dev)
+        self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.ws_attn = None
+        self.outgrown = []
+
+    def append(self, q, k, v, cu_len, prefix_len, k_cache, v_cache, block_table, kv_scale=None, stream=None):
+        """The tokens into the cache (with ``kv_scale`` the 8-bit one); the rotated queries
+        and, in ``kv_len``, the sequences' new lengths."""
+        q_rot = None if q is None else self.q_rot[:q.shape[0]]
+        tree_cache_append_rope(q, k, v, cu_len, prefix_len, q_rot, k_cache, v_cache, block_table, self.kv_len,
+                               self.rope, self.status, kv_scale, stream)
+        return q_rot
+
+    def attention(self, q, k_cache, v_cache, block_table, cu_len, cu_len_host, kv_len_host, stream=None):
+        T = q.shape[0]
+        p = chunk_params(q, k_cache, v_cache, block_table, cu_len, self.kv_len, cu_len_host, kv_len_host, self.out[:T],
+                         self.lse[:T], self.status, self.scale, self.window, self.sinks)
+        need = tree_chunk_attn_workspace_size(p)
+        if need == 0:
+            raise ValueError("tree_chunk_attn_fwd would reject these arguments")
+        tree_chunk_attn_fwd(p, _grown(self, "ws_attn", need), stream)
+        return self.out[:T]
+
+    def run(self, q, k, v, cu_len, cu_len_host, prefix_len, prefix_len_host, k_cache, v_cache, block_table, stream=None):
+        """append, then attention: the tokens' outputs [T, Hq, D].  ``*_host`` are the
+        host's copies of cu_len and prefix_len."""
+        cu = np.asarray(cu_len_host, np.int32)
+        kv_host = np.asarray(prefix_len_host, np.int32) + (cu[1:] - cu[:-1])
+        q = self.append(q, k, v, cu_len, prefix_len, k_cache, v_cache, block_table, stream=stream)
+        return self.attention(q, k_cache, v_cache, block_table, cu_len, cu, kv_host, stream)
+
+    def score(self, logits, tokens, rows=None, temperature: float = 1.0, top: int = 0, stream=None) -> _Scores:
+        """Log probabilities of ``tokens`` [R] under ``logits`` rows (those of ``rows``, or the
+        first R)."""
+        out = _Scores(tokens.shape[0], top, self.device)
+        tree_token_logprobs(logits, tokens, out.logprob, out.entropy, out.top_ids, out.top_logprobs, rows=rows,
+                            temperature=temperature, stream=stream)
+        return out
