@@ -682,7 +682,7 @@ def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
                  window: int = 0, sinks: int = 0) -> ChunkParams:
     """Fill tree_chunk_attn_fwd's parameter block from tensors (shapes as in
     treespec.h), each of which is checked.  ``cu_len_host`` and ``kv_len_host`` are
-    the host's copies of ``cu_len`` and ``kv_len``; the returned object keeps them."""
+    the host's copies of ``cu_len`` and ``kv_len``.  The returned object keeps them all."""
     where = "chunk_params"
     T, Hq, D = q.shape
     nblk, Hkv, bs, _ = k_cache.shape
@@ -702,7 +702,7 @@ def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     p = ChunkParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_len.data_ptr(),
                     kv_len.data_ptr(), cu.ctypes.data, kv.ctypes.data, out.data_ptr(), _opt(lse), _opt(status), B, T, Hq,
                     Hkv, D, bs, nblk, maxb, scale, window, sinks)
-    p._keep = (cu, kv)
+    p._keep = (cu, kv, q, k_cache, v_cache, block_table, cu_len, kv_len, out, lse, status)
     p.device = dev
     return p
 

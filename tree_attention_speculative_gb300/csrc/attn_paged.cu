@@ -46,15 +46,15 @@
 namespace ts {
 namespace {
 
-constexpr int NUM_THREADS = 256;
-constexpr int SOFTMAX_THREADS = 128;
+constexpr int NUM_THREADS = 384;
+constexpr int GROUP_THREADS = 128;  // a softmax group: a row a thread
 constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4;
-constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S0 = 128;
-constexpr int NSB = 3;       // S buffers in TMEM
-constexpr int ITEM_Q = 16;   // entries of the item queue
-// O is rescaled when a row's maximum rises by more than this (in powers of two):
-// weights then stay below 2^20, far inside the range of bf16 and fp32.
-constexpr float RESCALE_THRESHOLD = 20.0f;
+constexpr int HALF = KV_TILE / 2;  // keys of a tile that one softmax group takes
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int ITEM_Q = 8;    // entries of the item queue
+// O is rescaled when a row's maximum rises by more than this (in powers of two).
+// Weights then stay below 2^40; their precision does not depend on it.
+constexpr float RESCALE_THRESHOLD = 40.0f;
 constexpr float NEG_INF = -INFINITY;
 
 template <int D>
@@ -64,14 +64,9 @@ struct Cfg {
   static constexpr int HALF_BYTES = KV_TILE * 128;
   static constexpr int Q_BYTES = ROW_TILE * D * 2;
   static constexpr int NST = D == 128 ? 3 : 6;  // tiles in each ring, K and V
-};
-
-// An item and its sequence's lengths.
-struct Work {
-  int b;          // -1: no more items
-  int place;      // KV head, split, row tile, entry: see pack
-  int q0;         // first row's token
-  int len, kv;    // tokens of the sequence here, and in the cache
+  // TMEM: the groups' accumulators at 0 and D, then the S buffers
+  static constexpr uint32_t TMEM_S0 = 2 * D;
+  static constexpr int NSB = (TMEM_COLS - TMEM_S0) / KV_TILE;  // 2 for heads of 128, 3 for 64
 };
 
 template <int D>
@@ -83,15 +78,19 @@ struct __align__(1024) Smem {
   uint64_t q_full, q_empty;
   uint64_t k_full[C::NST], v_full[C::NST];
   uint64_t k_empty[C::NST], v_empty[C::NST];
-  uint64_t s_full[NSB], p_full[NSB], s_free[NSB];
+  uint64_t s_full[C::NSB], p_full[C::NSB][2], s_free[C::NSB];
   uint64_t o_ready;
+  uint64_t ml_full, f_full, o_free;  // an item's end: see ml; both groups have read the accumulators
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int pv_done;  // PVs completed so far
   // the CTA's items in the order taken; pub published, done stored
-  int item_q[ITEM_Q][8];
+  int4 item_q[ITEM_Q][4];
   int items_pub, items_done;
+  // an item's end: group 1's (m, l) of each row, then from group 0 the factors of
+  // both accumulators (1 KB each way would not fit beside heads of 128)
+  float2 ml[ROW_TILE];
 };
 
 struct KArgs {
@@ -127,13 +126,12 @@ __device__ __forceinline__ Place place_of(int it, const KArgs& t) {
   return p;
 }
 
+// An item as the roles take it; four int4 of the queue.
 struct Item {
   int b, g, split, e;
-  int q0, i0, len;  // the tile's first row is token q0 + i0, the i0-th of len
-  int pos0;         // position of the tile's first row (tree: of the root)
-  PagedSpan sp;
-  int t_begin, n_prefix, n_tiles, ps;
-  bool work;
+  int q0, i0, len, pos0;  // the tile's first row is token q0 + i0, the i0-th of len, at position pos0 (tree: the root's)
+  int lo, hi, n_sink, win0;  // PagedSpan
+  int t_begin, n_prefix, n_tiles, ps;  // n_tiles 0: nothing to do, or no more items
 };
 template <bool TREE>
 __device__ __forceinline__ Item make_item(const Place& p, int b, int q0, int len, int kv, const KArgs& t) {
@@ -146,25 +144,23 @@ __device__ __forceinline__ Item make_item(const Place& p, int b, int q0, int len
   I.q0 = q0;
   I.len = len;
   I.i0 = p.rt * a.tok;
-  I.work = I.i0 < len;
-  if (TREE) {
-    I.pos0 = kv;
-    I.sp = paged_span(kv, kv, a.window, a.sinks);
-  } else {
-    I.pos0 = kv - len + I.i0;
-    I.sp = chunk_span(kv, len, I.i0, a.tok, a.window, a.sinks);
-  }
-  I.ps = paged_splits(I.sp.n, a.chunk_tiles, t.seq[p.e].splits);
-  I.work = I.work && p.split < I.ps;
-  I.t_begin = paged_split_start(I.sp.n, I.ps, p.split);
-  I.n_prefix = paged_split_start(I.sp.n, I.ps, p.split + 1) - I.t_begin;
+  I.pos0 = TREE ? kv : kv - len + I.i0;
+  const PagedSpan sp = TREE ? paged_span(kv, kv, a.window, a.sinks) : chunk_span(kv, len, I.i0, a.tok, a.window, a.sinks);
+  I.lo = sp.lo;
+  I.hi = sp.hi;
+  I.n_sink = sp.n_sink;
+  I.win0 = sp.win0;
+  I.ps = paged_splits(sp.n, a.chunk_tiles, t.seq[p.e].splits);
+  I.t_begin = paged_split_start(sp.n, I.ps, p.split);
+  I.n_prefix = paged_split_start(sp.n, I.ps, p.split + 1) - I.t_begin;
   I.n_tiles = I.n_prefix + (TREE && p.split == I.ps - 1 ? ceil_div(a.N, KV_TILE) : 0);
+  if (I.i0 >= len || p.split >= I.ps) I.n_tiles = 0;
   return I;
 }
 // First key of the item's prefix tile j.
 __device__ __forceinline__ int tile_key(const Item& I, int j) {
   const int jj = I.t_begin + j;
-  return (jj < I.sp.n_sink ? jj : jj - I.sp.n_sink + I.sp.win0) * KV_TILE;
+  return (jj < I.n_sink ? jj : jj - I.n_sink + I.win0) * KV_TILE;
 }
 
 // The lengths of sequence b as the device has them.
@@ -215,10 +211,13 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
              const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
              const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt) {
   using C = Cfg<D>;
+  constexpr int NSB = C::NSB;
+  constexpr uint32_t TMEM_S0 = C::TMEM_S0;
   extern __shared__ uint8_t smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const PagedArgs& a = args.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const bool leader = elect_one();  // one lane of the warp
   const Ctl ctl{&sm.abort_flag, a.wait_limit_ns};
   const int n_items = args.n_items;
 
@@ -248,10 +247,14 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], SOFTMAX_THREADS);
+      mbar_init(&sm.p_full[i][0], GROUP_THREADS);
+      mbar_init(&sm.p_full[i][1], GROUP_THREADS);
       mbar_init(&sm.s_free[i], 1);
     }
     mbar_init(&sm.o_ready, 1);
+    mbar_init(&sm.ml_full, GROUP_THREADS);
+    mbar_init(&sm.f_full, GROUP_THREADS);
+    mbar_init(&sm.o_free, 2 * GROUP_THREADS);
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
     fence_barrier_init();
@@ -273,23 +276,18 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
   if (single && !l0.ok && threadIdx.x == 0 && a.status) a.status[b0] = TS_ERR_SHAPE;
   const Item item0 = make_item<TREE>(pl0, b0, l0.q0, l0.len, l0.kv, args);
 
-  // Entry k of the queue as an item (every role but the K producer; with a CTA
-  // an item every role).  false: the wait gave up; work false: no more items.
+  // Entry k of the queue (every role but the K producer; with a CTA an item every
+  // role).  false: the wait gave up.
   auto queue_item = [&](int k, Item& I) -> bool {
     if (single) {
       I = item0;
-      I.work = I.work && k == 0;
+      if (k > 0) I.n_tiles = 0;
       return true;
     }
     if (!wait_count(&sm.items_pub, k + 1, ctl)) return false;
-    const volatile int* q = sm.item_q[k % ITEM_Q];
-    const int b = q[0];
-    if (b < 0) {
-      I.work = false;
-      return true;
-    }
-    const Place p{q[1], q[2], q[3], q[4]};
-    I = make_item<TREE>(p, b, q[5], q[6], q[7], args);
+    const int4* q = sm.item_q[k % ITEM_Q];
+    const int4 x = q[0], y = q[1], z = q[2], w = q[3];
+    I = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w, w.x, w.y, w.z, w.w};
     return true;
   };
   // The K producer's lane 0: the next item, or -1.  The last of all requests puts
@@ -322,11 +320,12 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
     for (int k = 0;; ++k) {
       Item I;
       if (grabber) {
+        I.n_tiles = 0;
         for (;;) {
           if (cand < 0) break;
           if (!cl.ok && lane == 0 && a.status) a.status[args.seq[cpl.e].b] = TS_ERR_SHAPE;
           I = make_item<TREE>(cpl, args.seq[cpl.e].b, cl.q0, cl.len, cl.kv, args);
-          if (I.work) break;
+          if (I.n_tiles) break;
           int nx = -1;
           if (lane == 0) nx = take_item();
           cand = __shfl_sync(0xffffffffu, nx, 0);
@@ -341,16 +340,14 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         if (!ok && lane == 0) ok = wait_count(&sm.items_done, k - ITEM_Q + 1, ctl);
         if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
         if (lane == 0) {
-          volatile int* q = sm.item_q[k % ITEM_Q];
-          q[0] = cand < 0 ? -1 : I.b;
-          q[1] = cpl.e;
-          q[2] = cpl.rt;
-          q[3] = cpl.split;
-          q[4] = cpl.g;
-          q[5] = cl.q0;
-          q[6] = cl.len;
-          q[7] = cl.kv;
+          int4* q = sm.item_q[k % ITEM_Q];
+          q[0] = make_int4(I.b, I.g, I.split, I.e);
+          q[1] = make_int4(I.q0, I.i0, I.len, I.pos0);
+          q[2] = make_int4(I.lo, I.hi, I.n_sink, I.win0);
+          q[3] = make_int4(I.t_begin, I.n_prefix, I.n_tiles, I.ps);
           publish(&sm.items_pub, k + 1);
+          if (I.n_tiles)  // its queries, into L2, while the last item's keys are still at work
+            for (int h = 0; h < C::HALVES; ++h) tma_prefetch_3d(&tm_q, 64 * h, I.g * a.G, I.q0 + I.i0);
         }
         __syncwarp();
         held = -1;
@@ -366,61 +363,57 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           cl = load_lens<TREE>(args.seq[cpl.e].b, args.seq[cpl.e].rows, a);
         }
       } else {
-        bool ok = true;
-        if (lane == 0 && !single) ok = wait_count(&sm.items_pub, k + 1, ctl);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
-        if (!queue_item(k, I)) return jg;
-        if (!I.work) return jg;
+        const bool ok = queue_item(k, I);
+        if (!__all_sync(0xffffffffu, ok)) return jg;
+        if (I.n_tiles == 0) return jg;
       }
-      const int b = I.b, g = I.g, n_prefix = I.n_prefix;
+      const int b = I.b, n_prefix = I.n_prefix;
       const int* table_row = a.block_table + (size_t)b * a.max_blocks;
       // Block-table entries, a group of tiles ahead: lane L holds that of box
-      // L % boxes of tile L / boxes of a group of 32 / boxes tiles.  -1 for a box
-      // that no row of the item sees into: it is not read.
+      // L % boxes of tile L / boxes of a group of 32 / boxes tiles, and makes the
+      // box's coordinates of it when the group's turn comes.  A box that no row of
+      // the item sees into is not read (slab -1).
       auto load_group = [&](int grp) -> int {
         const int j = grp * tpg + (lane >> lg_boxes);
         if (j >= n_prefix) return INT_MIN;
         const int t0 = tile_key(I, j) + koff;
-        if (t0 >= I.sp.hi || (t0 + g_box <= I.sp.lo && t0 >= a.sinks)) return INT_MIN;
+        if (t0 >= I.hi || (t0 + g_box <= I.lo && t0 >= a.sinks)) return INT_MIN;
         const int blk = table_row[args.fd_bs.div(t0)];
         return blk == INT_MIN ? -1 : blk;
       };
-      int grp_cur = load_group(0);
-      int grp_nxt = n_prefix > tpg ? load_group(1) : INT_MIN;
+      int raw = load_group(0);
+      int slab = -1, row8 = 0;
+      unsigned boxes = 0;  // which lanes' are read
       const int stop = !is_v && b == a.stall_seq ? a.stall_tile : I.n_tiles;
-      int jt = 0;
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         uint8_t* dst = is_v ? sm.v[slot] : sm.k[slot];
-        if (jg >= C::NST) {
-          bool ok = true;
-          if (lane == 0) ok = wait_bar(&empty[slot], phase ^ 1, ctl);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
+        const int jt = j & (tpg - 1);
+        if (jt == 0 && j < n_prefix) {
+          const int grp = j >> (5 - lg_boxes);
+          slab = -1;
+          if (raw != INT_MIN) {
+            if (raw < 0 || raw >= a.num_blocks) {
+              if (a.status) a.status[b] = TS_ERR_BAD_BLOCK;
+              raw = 0;  // a valid block is read in its place
+            }
+            slab = raw * a.Hkv + I.g;
+            row8 = args.fd_bs.mod(tile_key(I, grp * tpg + (lane >> lg_boxes)) + koff) >> 3;
+          }
+          boxes = __ballot_sync(0xffffffffu, slab >= 0);
+          raw = (grp + 1) * tpg < n_prefix ? load_group(grp + 1) : INT_MIN;
         }
+        if (jg >= C::NST && !__all_sync(0xffffffffu, wait_bar(&empty[slot], phase ^ 1, ctl))) return jg;
         if (j == stop) return jg;
         if (j < n_prefix) {
-          if (jt == 0 && j > 0) {
-            grp_cur = grp_nxt;
-            const int g2 = (j >> (5 - lg_boxes)) + 1;
-            grp_nxt = g2 * tpg < n_prefix ? load_group(g2) : INT_MIN;
-          }
-          int blk = __shfl_sync(0xffffffffu, grp_cur, (jt << lg_boxes) + (lane & (n_boxes - 1)));
-          const bool issue = lane < n_boxes && blk != INT_MIN;
-          if (issue && (blk < 0 || blk >= a.num_blocks)) {
-            if (a.status) a.status[b] = TS_ERR_BAD_BLOCK;
-            blk = 0;  // a valid block is read in its place
-          }
-          const unsigned mask = __ballot_sync(0xffffffffu, issue);
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(mask) * box_bytes);
+          // the lanes that hold this tile's boxes issue them
+          if (leader) mbar_arrive_expect_tx(&full[slot], __popc((boxes >> (jt << lg_boxes)) & ((1u << n_boxes) - 1)) * box_bytes);
           __syncwarp();
-          if (issue) {
-            const int row = args.fd_bs.mod(tile_key(I, j) + koff);
-            tma_load_5d(dst + lane * box_bytes, tm_pool, &full[slot], 0, 0, 0, row >> 3, blk * a.Hkv + g);
-          }
-          jt = (jt + 1) & (tpg - 1);
-        } else if (lane == 0) {
+          if ((lane >> lg_boxes) == jt && slab >= 0)
+            tma_load_5d(dst + (lane & (n_boxes - 1)) * box_bytes, tm_pool, &full[slot], 0, 0, 0, row8, slab);
+        } else if (leader) {
           const int n0 = (j - n_prefix) * KV_TILE;  // nodes >= N read as zeros
           mbar_arrive_expect_tx(&full[slot], C::TILE_BYTES);
-          for (int h = 0; h < C::HALVES; ++h) tma_load_4d(dst + h * C::HALF_BYTES, tm_node, &full[slot], 64 * h, g, n0, b);
+          for (int h = 0; h < C::HALVES; ++h) tma_load_4d(dst + h * C::HALF_BYTES, tm_node, &full[slot], 64 * h, I.g, n0, b);
         }
         __syncwarp();
         if (++slot == C::NST) {
@@ -436,133 +429,189 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
   if (warp == K_WARP || warp == V_WARP) {
     issued = kv_producer(warp == V_WARP);
   } else if (warp == QK_WARP) {
-    if (lane == 0) {
-      constexpr uint32_t ID_QK = idesc_bf16_f32(ROW_TILE, KV_TILE, 0, 0);
-      const uint32_t q_addr = smem_u32(sm.q);
-      int jg = 0;
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        Item I;
-        if (!(ok = queue_item(k, I))) break;
-        if (!I.work) break;
-        // this item's Q tile, once every QK of the last one has completed
-        if (k > 0 && !(ok = wait_bar(&sm.q_empty, (k - 1) & 1, ctl))) break;
+    // The whole warp runs the issuers' loops, on values that are the same on every
+    // lane, and one lane issues: descriptors then stay in uniform registers.
+    constexpr uint32_t ID_QK = idesc_bf16_f32(ROW_TILE, KV_TILE, 0, 0);
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
+    // cached tiles: [8-row group][64-column half]; tree tiles: [half][rows]
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, C::HALVES * 1024);
+    const uint64_t kt_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+    int jg = 0, slot = 0, k_phase = 0, buf = 0, s_phase = 1;  // (the first NSB waits for s_free pass)
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Item I;
+      if (!__all_sync(0xffffffffu, queue_item(k, I))) break;
+      const int n_tiles = __shfl_sync(0xffffffffu, I.n_tiles, 0), n_prefix = __shfl_sync(0xffffffffu, I.n_prefix, 0);
+      if (n_tiles == 0) break;
+      // this item's Q tile, once every QK of the last one has completed
+      if (k > 0 && !__all_sync(0xffffffffu, wait_bar(&sm.q_empty, (k - 1) & 1, ctl))) break;
+      if (leader) {
         mbar_arrive_expect_tx(&sm.q_full, C::Q_BYTES);
         for (int h = 0; h < C::HALVES; ++h)
           tma_load_3d(sm.q + h * (ROW_TILE * 128), &tm_q, &sm.q_full, 64 * h, I.g * a.G, I.q0 + I.i0);
-        ++q_issued;
-        if (!(ok = wait_bar(&sm.q_full, k & 1, ctl))) break;
-        ++q_landed;
-        for (int j = 0; j < I.n_tiles; ++j, ++jg) {
-          const int slot = jg % C::NST;
-          ok = wait_bar(&sm.k_full[slot], (jg / C::NST) & 1, ctl) &&
-               (jg < NSB || wait_bar(&sm.s_free[jg % NSB], ((jg / NSB) - 1) & 1, ctl));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t k_addr = smem_u32(sm.k[slot]);
-          const uint32_t d_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
-          // cached tiles: [8-row group][64-column half]; tree tiles: [half][rows]
-          const bool tree = TREE && j >= I.n_prefix;
-          const uint32_t k_half = tree ? C::HALF_BYTES : 1024;
-          const uint32_t k_sbo = tree ? 1024 : C::HALVES * 1024;
+      }
+      __syncwarp();
+      ++q_issued;
+      if (!__all_sync(0xffffffffu, wait_bar(&sm.q_full, k & 1, ctl))) break;
+      ++q_landed;
+      for (int j = 0; j < n_tiles; ++j, ++jg) {
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.k_full[slot], k_phase, ctl) && wait_bar(&sm.s_free[buf], s_phase, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + TMEM_S0 + buf * KV_TILE;
+        if (leader) {
+          if (!TREE || j < n_prefix) {
+            const uint64_t kd = k_desc + slot * (C::TILE_BYTES >> 4);
 #pragma unroll
-          for (int k2 = 0; k2 < D / 16; ++k2) {
-            const uint32_t off = (k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32;
-            const uint32_t koff = (k2 >> 2) * k_half + (k2 & 3) * 32;
-            mma_ss(d_tmem, smem_desc_sw128(q_addr + off, 16, 1024), smem_desc_sw128(k_addr + koff, 16, k_sbo), ID_QK,
-                   k2 > 0);
+            for (int k2 = 0; k2 < D / 16; ++k2)
+              mma_ss(d_tmem, q_desc + (((k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32) >> 4),
+                     kd + (((k2 >> 2) * 1024 + (k2 & 3) * 32) >> 4), ID_QK, k2 > 0);
+          } else {
+            const uint64_t kd = kt_desc + slot * (C::TILE_BYTES >> 4);
+#pragma unroll
+            for (int k2 = 0; k2 < D / 16; ++k2)
+              mma_ss(d_tmem, q_desc + (((k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32) >> 4),
+                     kd + (((k2 >> 2) * C::HALF_BYTES + (k2 & 3) * 32) >> 4), ID_QK, k2 > 0);
           }
-          mma_commit(&sm.s_full[jg % NSB]);
+          mma_commit(&sm.s_full[buf]);
           mma_commit(&sm.k_empty[slot]);
         }
-        if (ok) mma_commit(&sm.q_empty);
+        __syncwarp();
+        if (++slot == C::NST) {
+          slot = 0;
+          k_phase ^= 1;
+        }
+        if (++buf == NSB) {
+          buf = 0;
+          s_phase ^= 1;
+        }
       }
+      if (ok && leader) mma_commit(&sm.q_empty);
+      __syncwarp();
     }
   } else if (warp == PV_WARP) {
-    if (lane == 0) {
-      constexpr uint32_t ID_PV = idesc_bf16_f32(ROW_TILE, D, 0, 1);
-      int jg = 0;
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        Item I;
-        if (!(ok = queue_item(k, I))) break;
-        if (!I.work) break;
-        for (int j = 0; j < I.n_tiles; ++j, ++jg) {
-          const int slot = jg % C::NST;
-          if (!(ok = wait_bar(&sm.p_full[jg % NSB], (jg / NSB) & 1, ctl))) break;
-          if (!(ok = wait_bar(&sm.v_full[slot], (jg / C::NST) & 1, ctl))) break;
-          tc_fence_after();
-          const uint32_t v_addr = smem_u32(sm.v[slot]);
-          const uint32_t p_tmem = tmem + TMEM_S0 + (jg % NSB) * 128;
-          const bool tree = TREE && j >= I.n_prefix;
-          const uint32_t v_lbo = tree ? C::HALF_BYTES : 1024;
-          const uint32_t v_sbo = tree ? 1024 : C::HALVES * 1024;
+    constexpr uint32_t ID_PV = idesc_bf16_f32(ROW_TILE, D, 0, 1);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), 1024, C::HALVES * 1024);
+    const uint64_t vt_desc = smem_desc_sw128(smem_u32(sm.v[0]), C::HALF_BYTES, 1024);
+    int jg = 0, slot = 0, v_phase = 0, buf = 0, p_phase = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Item I;
+      if (!__all_sync(0xffffffffu, queue_item(k, I))) break;
+      const int n_tiles = __shfl_sync(0xffffffffu, I.n_tiles, 0), n_prefix = __shfl_sync(0xffffffffu, I.n_prefix, 0);
+      if (n_tiles == 0) break;
+      if (k > 0 && !__all_sync(0xffffffffu, wait_bar(&sm.o_free, (k - 1) & 1, ctl))) break;
+      for (int j = 0; j < n_tiles; ++j, ++jg) {
+        const uint32_t p_tmem = tmem + TMEM_S0 + buf * KV_TILE;
+        const bool tree = TREE && j >= n_prefix;
+        const uint64_t vd = (tree ? vt_desc : v_desc) + slot * (C::TILE_BYTES >> 4);
 #pragma unroll
-          for (int k2 = 0; k2 < KV_TILE / 16; ++k2)
-            mma_ts(tmem + TMEM_O, p_tmem + k2 * 8, smem_desc_sw128(v_addr + k2 * 2 * v_sbo, v_lbo, v_sbo), ID_PV,
-                   j > 0 || k2 > 0);
-          mma_commit(&sm.o_ready);
-          mma_commit(&sm.s_free[jg % NSB]);
-          mma_commit(&sm.v_empty[slot]);
-          // published so that the softmax looks at O only when it has to
-          if (!(ok = wait_bar(&sm.o_ready, jg & 1, ctl))) break;
+        for (int half = 0; half < 2; ++half) {
+          ok = __all_sync(0xffffffffu, wait_bar(&sm.p_full[buf][half], p_phase, ctl) &&
+                                           (half || wait_bar(&sm.v_full[slot], v_phase, ctl)));
+          if (!ok) break;
           tc_fence_after();
-          publish(&sm.pv_done, jg + 1);
+          if (leader) {
+            if (!tree) {
+#pragma unroll
+              for (int k2 = 0; k2 < HALF / 16; ++k2)
+                mma_ts(tmem + half * D, p_tmem + half * HALF + k2 * 8,
+                       vd + (((half * (HALF / 16) + k2) * 2 * C::HALVES * 1024) >> 4), ID_PV, j > 0 || k2 > 0);
+            } else {
+#pragma unroll
+              for (int k2 = 0; k2 < HALF / 16; ++k2)
+                mma_ts(tmem + half * D, p_tmem + half * HALF + k2 * 8,
+                       vd + (((half * (HALF / 16) + k2) * 2 * 1024) >> 4), ID_PV, j > 0 || k2 > 0);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) {
+          mma_commit(&sm.s_free[buf]);
+          mma_commit(&sm.o_ready);
+          mma_commit(&sm.v_empty[slot]);
+        }
+        __syncwarp();
+        // published so that the softmax looks at O only when it has to
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.o_ready, jg & 1, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) publish(&sm.pv_done, jg + 1);
+        __syncwarp();
+        if (++slot == C::NST) {
+          slot = 0;
+          v_phase ^= 1;
+        }
+        if (++buf == NSB) {
+          buf = 0;
+          p_phase ^= 1;
         }
       }
     }
   } else {
-    const int r = threadIdx.x - SOFTMAX_WARP0 * 32;  // TMEM lane, and row of the tile
+    const int half = (warp - SOFTMAX_WARP0) >> 2;  // the group: keys 64 half .. of each tile, accumulator half
+    const int r = (threadIdx.x - SOFTMAX_WARP0 * 32) & (GROUP_THREADS - 1);  // TMEM lane, and row of the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_tmem = tmem + lane_base + half * D;
     const int i_in = args.fd_g.div(r);  // token of the tile, and head of the group
     const int h_in = r - i_in * a.G;
     int jg = 0;
     Item I;
     bool ok = __all_sync(0xffffffffu, queue_item(0, I));
-    for (int k = 0; ok && I.work; ++k) {
+    for (int k = 0; ok && I.n_tiles; ++k) {
       const bool active = I.i0 + i_in < I.len;
       const int i = active ? I.i0 + i_in : I.len - 1;
-      // the row's position, and the cached keys it sees: t < hi, and t >= lo or t < sinks
-      int pos, hi, hi_least, lo_most;
-      uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
+      // the cached keys the row sees: t < hi, and t >= lo or t < sinks
+      int lo, hi, hi_least, lo_most;
+      uint64_t anc[2] = {0ull, 0ull};  // this group's keys of the two tree tiles
       if (TREE) {
         const int P = I.pos0;
+        uint64_t w4[4] = {0ull, 0ull, 0ull, 0ull};
         int depth = 0;
         if (active) {
           const uint64_t* arow = a.anc_mask + ((size_t)I.b * a.N + i) * a.W;
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            if (w < a.W) anc[w] = arow[w];
-          depth = __popcll(anc[0]) + __popcll(anc[1]) + __popcll(anc[2]) + __popcll(anc[3]) - 1;
+            if (w < a.W) w4[w] = arow[w];
+          depth = __popcll(w4[0]) + __popcll(w4[1]) + __popcll(w4[2]) + __popcll(w4[3]) - 1;
         }
-        pos = P + depth;
+        lo = P + depth - a.window + 1;
         hi = hi_least = P;
         lo_most = P + a.N - a.window;
         // Ancestors out of the window.  Node indices rise along a chain, so the
         // k-th set bit is the ancestor at depth k: hidden if depth - k >= window
         // and P + k >= sinks.
         const int hide_end = depth + 1 - a.window, hide0 = max(a.sinks - P, 0);
-        if (a.window > 0 && hide_end > hide0) {
+        if (hide_end > hide0) {
           int at = 0;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint64_t left = anc[w];
+            uint64_t left = w4[w];
             while (left && at < hide_end) {
               const uint64_t bit = left & (0ull - left);
               left ^= bit;
-              if (at >= hide0) anc[w] ^= bit;
+              if (at >= hide0) w4[w] ^= bit;
               ++at;
             }
           }
         }
+        anc[0] = half ? w4[1] : w4[0];
+        anc[1] = half ? w4[3] : w4[2];
       } else {
-        pos = I.pos0 + (i - I.i0);
+        const int pos = I.pos0 + (i - I.i0);
+        lo = pos - a.window + 1;
         hi = pos + 1;
         hi_least = I.pos0 + 1;
-        lo_most = I.sp.hi - a.window;
+        lo_most = I.hi - a.window;
       }
-      if (a.window == 0) lo_most = 0;
-      const int lo = a.window == 0 ? 0 : pos - a.window + 1;
+      if (a.window == 0) lo = lo_most = 0;
+      // Tiles j in [clear0, clear1) are wholly visible to every row: those before
+      // hold sinks, or keys that a later row's window is past; those after, keys
+      // past an earlier row.
+      int clear0 = 0;
+      if (lo_most > 0) clear0 = I.n_sink + max(ceil_div(lo_most, KV_TILE) - I.win0, 0) - I.t_begin;
+      const int clear1 = I.n_sink + hi_least / KV_TILE - I.win0 - I.t_begin;
       float m_run = NEG_INF, l_run = 0.f;
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
         if (!__all_sync(0xffffffffu, wait_bar(&sm.s_full[jg % NSB], (jg / NSB) & 1, ctl))) {
@@ -570,104 +619,78 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           break;
         }
         tc_fence_after();
-        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * 128;
-        float s[KV_TILE];
+        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * KV_TILE + half * HALF;
+        float s[HALF];
         {
-          uint32_t u[KV_TILE / 32][32];
-#pragma unroll
-          for (int c = 0; c < KV_TILE / 32; ++c) tmem_ld32(s_tmem + c * 32, u[c]);
+          uint32_t u[2][32];
+          tmem_ld32(s_tmem, u[0]);
+          tmem_ld32(s_tmem + 32, u[1]);
           tmem_ld_wait();
+          reg_fence32(u[0]);
+          reg_fence32(u[1]);
 #pragma unroll
-          for (int c = 0; c < KV_TILE / 32; ++c) {
-            reg_fence32(u[c]);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(u[c][e]);
-          }
+          for (int e = 0; e < HALF; ++e) s[e] = __uint_as_float(u[e / 32][e % 32]);
         }
-        // which keys this row sees, where it may not see all
-        const bool cached = !TREE || j < I.n_prefix;
-        const int key0 = cached ? tile_key(I, j) : 0;
-        bool masked, dead = false;
-        if (cached) {
-          masked = key0 + KV_TILE > hi_least || (key0 < lo_most && key0 + KV_TILE > a.sinks);
-          dead = key0 + KV_TILE > I.sp.hi || (key0 < I.sp.lo && key0 + KV_TILE > a.sinks);
-        } else {
-          masked = true;
-        }
-        if (masked) {
-          uint64_t w0, w1;
-          if (cached) {
-            const int nh = hi - key0, nl = lo - key0, ns = a.sinks - key0;
-            w0 = first_bits(nh) & (~first_bits(nl) | first_bits(ns));
-            w1 = first_bits(nh - 64) & (~first_bits(nl - 64) | first_bits(ns - 64));
+        bool dead = false;
+        int key0 = 0;
+        if (j < clear0 || j >= clear1) {
+          uint64_t w;  // the keys this row sees
+          if (TREE && j >= I.n_prefix) {
+            w = j > I.n_prefix ? anc[1] : anc[0];
           } else {
-            const bool second = j > I.n_prefix;  // nodes 128 ..
-            w0 = second ? anc[2] : anc[0];
-            w1 = second ? anc[3] : anc[1];
+            key0 = tile_key(I, j) + half * HALF;
+            w = first_bits(hi - key0) & (~first_bits(lo - key0) | first_bits(a.sinks - key0));
+            dead = key0 + HALF > I.hi || (key0 < I.lo && key0 + HALF > a.sinks);
           }
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((w0 >> c) & 1ull)) s[c] = NEG_INF;
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((w1 >> c) & 1ull)) s[64 + c] = NEG_INF;
+          for (int e = 0; e < HALF; ++e)
+            if (!((w >> e) & 1ull)) s[e] = NEG_INF;
         }
-        float mk[8];
+        float mk[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mk[e] = s[e];
+        for (int e = 0; e < 4; ++e) mk[e] = s[e];
 #pragma unroll
-        for (int c = 8; c < KV_TILE; c += 8)
+        for (int c = 4; c < HALF; c += 4)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
-        float mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
-        mx *= a.scale_log2;
-        const float m_new = fmaxf(m_run, mx);
+          for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
+        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
         const bool rescale = j > 0 && active && m_new > m_run + RESCALE_THRESHOLD;
         float m_use = m_run;
         if (j == 0 || rescale) m_use = m_new;
         const float m_exp = m_use == NEG_INF ? 0.f : m_use;  // nothing visible so far: every weight is 0
         const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
         const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
-        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[KV_TILE / 2];
+        uint64_t sum2[2] = {0ull, 0ull};
+        uint32_t pk[HALF / 2];
 #pragma unroll
-        for (int e = 0; e < KV_TILE / 2; ++e) {
+        for (int e = 0; e < HALF / 2; ++e) {
           float x0, x1;
           fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
           const float p0 = ex2(x0), p1 = ex2(x1);
-          sum2[e & 3] = fx::add2(sum2[e & 3], fx::pack2(p0, p1));
+          sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
           pk[e] = pack_bf16x2(p0, p1);
         }
+        tmem_st32(s_tmem, pk);
         float rowsum;
         {
           float r0, r1;
-          fx::unpack2(fx::add2(fx::add2(sum2[0], sum2[1]), fx::add2(sum2[2], sum2[3])), r0, r1);
+          fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
           rowsum = r0 + r1;
-        }
-        {
-          uint32_t part[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) part[e] = pk[e];
-          tmem_st32(s_tmem, part);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) part[e] = pk[32 + e];
-          tmem_st32(s_tmem + 32, part);
         }
         if (dead) {
           // V rows that no row of the item sees hold whatever the pool, or the
-          // ring, had there: zeroed, so that 0 * V is 0
+          // ring, had there: zeroed, so that 0 * V is 0.  Two threads a row.
           const int slot = jg % C::NST;
           if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (jg / C::NST) & 1, ctl))) {
             ok = false;
             break;
           }
-          const int t = key0 + r;
-          if (t >= I.sp.hi || (t < I.sp.lo && t >= a.sinks)) {
-            for (int hh = 0; hh < C::HALVES; ++hh) {
-              uint4* row = reinterpret_cast<uint4*>(sm.v[slot] + ((r >> 3) * C::HALVES + hh) * 1024 + (r & 7) * 128);
+          const int t = key0 + (r & (HALF - 1)), hh = r / HALF;
+          if (hh < C::HALVES && (t >= I.hi || (t < I.lo && t >= a.sinks))) {
+            const int vr = half * HALF + (r & (HALF - 1));
+            uint4* row = reinterpret_cast<uint4*>(sm.v[slot] + ((vr >> 3) * C::HALVES + hh) * 1024 + (vr & 7) * 128);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
-            }
+            for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
         }
@@ -681,53 +704,72 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           tc_fence_after();
           const float f = !rescale ? 1.f : m_run == NEG_INF ? 0.f : ex2(m_run - m_new);
           l_run *= f;
-#pragma unroll
-          for (int c = 0; c < D; c += 64) {
-            uint32_t u0[32], u1[32];
-            tmem_ld32(tmem + lane_base + TMEM_O + c, u0);
-            tmem_ld32(tmem + lane_base + TMEM_O + c + 32, u1);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t u0[32];
+            tmem_ld32(o_tmem + c, u0);
             tmem_ld_wait();
             reg_fence32(u0);
-            reg_fence32(u1);
 #pragma unroll
             for (int e = 0; e < 32; ++e) u0[e] = __float_as_uint(__uint_as_float(u0[e]) * f);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) u1[e] = __float_as_uint(__uint_as_float(u1[e]) * f);
-            tmem_st32(tmem + lane_base + TMEM_O + c, u0);
-            tmem_st32(tmem + lane_base + TMEM_O + c + 32, u1);
+            tmem_st32(o_tmem + c, u0);
           }
         }
         m_run = m_use;
         l_run += rowsum;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sm.p_full[jg % NSB]);
+        mbar_arrive(&sm.p_full[jg % NSB][half]);
       }
       if (!ok) break;
-      // the item's end: its last PV, then the rows divided and stored
-      if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
-        ok = false;
-        break;
+      // the item's end: its last PV, then the groups' halves joined.  Each group
+      // stores half of the channels, of both accumulators.
+      float f0 = 0.f, f1 = 0.f, lse2 = NEG_INF;
+      if (half == 0) {
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.ml_full, k & 1, ctl) && wait_count(&sm.pv_done, jg, ctl));
+        if (ok) {
+          const float2 other = sm.ml[r];
+          const float m_all = fmaxf(m_run, other.x);
+          f0 = m_run == NEG_INF ? 0.f : ex2(m_run - m_all);
+          f1 = other.x == NEG_INF ? 0.f : ex2(other.x - m_all);
+          const float l_all = l_run * f0 + other.y * f1;
+          const float inv = l_all > 0.f ? 1.f / l_all : 0.f;  // a row that sees no key: zeros
+          if (l_all > 0.f) lse2 = m_all + __log2f(l_all);
+          f0 *= inv;
+          f1 *= inv;
+          sm.ml[r] = make_float2(f0, f1);
+          mbar_arrive(&sm.f_full);
+        }
+      } else {
+        sm.ml[r] = make_float2(m_run, l_run);
+        mbar_arrive(&sm.ml_full);
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.f_full, k & 1, ctl) && wait_count(&sm.pv_done, jg, ctl));
+        if (ok) {
+          f0 = sm.ml[r].x;
+          f1 = sm.ml[r].y;
+        }
       }
+      if (!ok) break;
       tc_fence_after();
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;  // a row that sees no key: zeros
-      const float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : NEG_INF;
       const bool direct = I.ps == 1;
       const PagedSeq& sq = args.seq[I.e];
       const size_t orow = direct ? (size_t)(I.q0 + i) * a.Hq + I.g * a.G + h_in
                                  : ((size_t)sq.part_row + (size_t)I.split * sq.rows + i) * a.Hq + I.g * a.G + h_in;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t u[32];
-        tmem_ld32(tmem + lane_base + TMEM_O + c, u);
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        uint32_t u[32], v[32];
+        tmem_ld32(tmem + lane_base + c, u);
+        tmem_ld32(tmem + lane_base + D + c, v);
         tmem_ld_wait();
         reg_fence32(u);
+        reg_fence32(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f0 + __uint_as_float(v[e]) * f1);
         if (!active) continue;
         if (direct) {
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
           __nv_bfloat16* dst = a.out + orow * D + c;
           if (args.out32) {
             st_v8(dst, w);
@@ -740,19 +782,18 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         } else {
           float* dst = a.part_o + orow * D + c;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * inv);
-#pragma unroll
           for (int q = 0; q < 4; ++q) st_v8(dst + 8 * q, u + 8 * q);
         }
       }
-      if (active) {
+      if (active && half == 0) {
         if (!direct) a.part_lse[orow] = lse2;
         else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
       }
-      // O has been read: the next item's first PV waits for that item's first P
+      // the accumulators and statistics have been read: the next item may have them
       tc_fence_before();
+      mbar_arrive(&sm.o_free);
       __syncwarp();
-      if (r == 0) publish(&sm.items_done, k + 1);
+      if (half == 0 && r == 0) publish(&sm.items_done, k + 1);
       ok = __all_sync(0xffffffffu, queue_item(k + 1, I));
     }
   }
@@ -765,7 +806,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
     if ((warp == K_WARP || warp == V_WARP) && lane == 0) {
       uint64_t* full = warp == K_WARP ? sm.k_full : sm.v_full;
       for (int j = max(0, issued - C::NST); j < issued; ++j) mbar_wait(&full[j % C::NST], (j / C::NST) & 1, a.wait_limit_ns);
-    } else if ((warp == QK_WARP || warp == PV_WARP) && lane == 0) {
+    } else if ((warp == QK_WARP || warp == PV_WARP) && leader) {
       if (q_issued > q_landed) mbar_wait(&sm.q_full, (q_issued - 1) & 1, a.wait_limit_ns);
       uint64_t* d = &sm.drain[warp - QK_WARP];
       mma_commit(d);
@@ -779,15 +820,15 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         const Place p = place_of(it, args);
         const int b = args.seq[p.e].b;
         const Lens l = load_lens<TREE>(b, args.seq[p.e].rows, a);
-        if (make_item<TREE>(p, b, l.q0, l.len, l.kv, args).work) a.status[b] = TS_ERR_TIMEOUT;
+        if (make_item<TREE>(p, b, l.q0, l.len, l.kv, args).n_tiles) a.status[b] = TS_ERR_TIMEOUT;
       };
       const int done = sm.items_done;
       if (single) {
         if (done == 0) report(blockIdx.x);
       } else {
         for (int k = done; k < sm.items_pub && k < done + ITEM_Q; ++k) {
-          const int b = sm.item_q[k % ITEM_Q][0];
-          if (b >= 0 && a.status) a.status[b] = TS_ERR_TIMEOUT;
+          const int4* q = sm.item_q[k % ITEM_Q];
+          if (q[3].z && a.status) a.status[q[0].x] = TS_ERR_TIMEOUT;
         }
       }
       report(held);
@@ -898,8 +939,9 @@ k_join_paged(const __grid_constant__ JoinArgs t) {
 
 template <int D>
 constexpr size_t smem_bytes() {
-  return sizeof(Smem<D>) + 1024;
+  return sizeof(Smem<D>) + 1024;  // for the 1024-byte alignment of the swizzle atoms
 }
+static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "");
 
 template <int D, bool TREE>
 cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_items, bool cut, cudaStream_t s) {

@@ -75,9 +75,9 @@ __host__ __device__ inline int paged_splits(int n, int chunk_tiles, int most) {
   const int s = ceil_div(n, chunk_tiles);
   return s < 1 ? 1 : s > most ? most : s;
 }
-// Tiles [n s / ps, n (s + 1) / ps) are split s of ps.
+// Tiles [n s / ps, n (s + 1) / ps) are split s of ps (n <= 2^23 + 2^23, s <= ps <= 256).
 __host__ __device__ inline int paged_split_start(int n, int ps, int s) {
-  return (int)((long long)n * s / ps);
+  return ps == 1 ? (s ? n : 0) : (int)((unsigned)n * (unsigned)s / (unsigned)ps);
 }
 
 cudaError_t attn_paged_prepare();
