@@ -173,7 +173,7 @@ def _append_block(ts, **change):  # noqa: F811
         else:
             setattr(p, k, v)
     p._keep = rope
-    return ts.lib().tree_cache_append_rope(ctypes.byref(p), None)
+    return ts.lib().tree_cache_append_rope(bytes(p), None)
 
 
 @pytest.mark.parametrize("change,code", [

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -209,7 +210,7 @@ def lib() -> ctypes.CDLL:
         L.tree_attn_fwd_q8.restype = i32
         L.tree_attn_fwd_q8_stall_test.argtypes = [ctypes.POINTER(AttnParams), vp, vp, sz, i32, i32, ctypes.c_uint32, vp]
         L.tree_attn_fwd_q8_stall_test.restype = i32
-        L.tree_cache_append_rope.argtypes = [ctypes.POINTER(AppendParams), vp]
+        L.tree_cache_append_rope.argtypes = [ctypes.c_char_p, vp]  # the block's bytes
         L.tree_cache_append_rope.restype = i32
         L.tree_chunk_attn_workspace_size.argtypes = [ctypes.POINTER(ChunkParams)]
         L.tree_chunk_attn_workspace_size.restype = sz
@@ -262,6 +263,23 @@ def tree_build_ancestry_forest(parent_idx: torch.Tensor, prefix_len: torch.Tenso
                                             _p(status), _s(stream)), "tree_build_ancestry_forest")
 
 
+# The parameter blocks, packed at once: a small call's time is its marshalling, and a
+# ctypes.Structure's fields cost four times as much one by one.
+_ATTN = struct.Struct("13P8i2f")
+_APPEND = struct.Struct("13P6q8i")
+_CHUNK = struct.Struct("11P8if2i4x")
+assert _ATTN.size == ctypes.sizeof(AttnParams) and _CHUNK.size == ctypes.sizeof(ChunkParams)
+assert _APPEND.size == ctypes.sizeof(AppendParams)
+
+
+def _address(host: np.ndarray) -> int:
+    """Where a contiguous host array is (its ctypes attribute would take twice as long)."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(host))
+    except (TypeError, ValueError):  # read-only, or empty
+        return host.ctypes.data
+
+
 def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k_tree, v_tree, anc_mask, pos,
                 out, lse=None, status=None, scale: float = 0.0, rope_theta: float = 0.0) -> AttnParams:
     """Fill the C parameter block from tensors (shapes as in treespec.h).
@@ -274,14 +292,11 @@ def attn_params(q, k_cache, v_cache, block_table, prefix_len, prefix_len_host, k
     nblk, Hkv, bs, _ = k_cache.shape
     host = np.ascontiguousarray(np.asarray(prefix_len_host.cpu() if torch.is_tensor(prefix_len_host)
                                            else prefix_len_host, dtype=np.int32))
-    p = AttnParams(q=q.data_ptr(), k_cache=k_cache.data_ptr(), v_cache=v_cache.data_ptr(),
-                   block_table=block_table.data_ptr(), prefix_len=prefix_len.data_ptr(),
-                   prefix_len_host=host.ctypes.data, k_tree=k_tree.data_ptr(), v_tree=v_tree.data_ptr(),
-                   anc_mask=anc_mask.data_ptr(), pos=pos.data_ptr() if pos is not None else None,
-                   out=out.data_ptr(), lse=lse.data_ptr() if lse is not None else None,
-                   status=status.data_ptr() if status is not None else None,
-                   B=B, N=N, Hq=Hq, Hkv=Hkv, D=D, block_size=bs, num_blocks=nblk,
-                   max_blocks=block_table.shape[1], scale=scale, rope_theta=rope_theta)
+    p = AttnParams.from_buffer_copy(_ATTN.pack(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(),
+        _address(host), k_tree.data_ptr(), v_tree.data_ptr(), anc_mask.data_ptr(), 0 if pos is None else pos.data_ptr(),
+        out.data_ptr(), 0 if lse is None else lse.data_ptr(), 0 if status is None else status.data_ptr(), B, N, Hq, Hkv,
+        D, bs, nblk, block_table.shape[1], scale, rope_theta))
     p._keep = (host,)
     p.tensors = (q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, anc_mask, out, lse, status)
     p.cache_dtypes = kd, vd = getattr(k_cache, "dtype", None), getattr(v_cache, "dtype", None)
@@ -464,13 +479,16 @@ def _is_codes(t: torch.Tensor, shape: tuple) -> bool:
 
 def _launch_stream(where: str, stream, *tensors) -> int:
     """The stream's handle, once every tensor is on the current CUDA device."""
+    dev = None
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            _bad(where)
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _bad(where)
+        if t is not None:
+            d = t.get_device()  # -1: the CPU
+            if d != dev:
+                if dev is not None or d < 0:
+                    _bad(where)
+                dev = d
+    if dev != torch._C._cuda_getDevice():
+        _bad(where)
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -628,11 +646,12 @@ def _token_strides(where: str, x: torch.Tensor, T: int, H: int, D: int):
 
 
 @functools.lru_cache(maxsize=64)
-def _rope_params(rope: RopeConfig) -> RopeParams:
-    """The C block of a configuration (the call only reads it)."""
-    return RopeParams(rotary_dim=rope.rotary_dim, interleaved=rope.interleaved,
-                      scaling=ROPE_SCALING.get(rope.scaling, -1), theta=rope.theta, factor=rope.factor,
-                      low_rot=rope.low_rot, high_rot=rope.high_rot, orig_len=rope.orig_len, mscale=rope.mscale)
+def _rope_params(rope: RopeConfig):
+    """The C block of a configuration (the call only reads it), and its address."""
+    p = RopeParams(rotary_dim=rope.rotary_dim, interleaved=rope.interleaved,
+                   scaling=ROPE_SCALING.get(rope.scaling, -1), theta=rope.theta, factor=rope.factor,
+                   low_rot=rope.low_rot, high_rot=rope.high_rot, orig_len=rope.orig_len, mscale=rope.mscale)
+    return p, ctypes.addressof(p)
 
 
 def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cu_len: torch.Tensor,
@@ -648,32 +667,36 @@ def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
     where = "tree_cache_append_rope"
     T, Hkv, D = k.shape
     B = prefix_len.shape[0]
-    nblk, bs, maxb = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
-    pool = (nblk, Hkv, bs, D)
+    pool = k_cache.shape
+    nblk, _, bs, _ = pool
+    maxb = block_table.shape[1]
     Hq = qt = qh = 0
     if q is not None:
         Hq = q.shape[1]
         qt, qh = _token_strides(where, q, T, Hq, D)
-        if q_out is None or not _is(q_out, _BF16, (T, Hq, D)):
+        if q_out is None or not (q_out.dtype is _BF16 and q_out.shape == (T, Hq, D) and q_out.is_contiguous()):
             _bad(where)
     kt, kh = _token_strides(where, k, T, Hkv, D)
     vt, vh = _token_strides(where, v, T, Hkv, D)
     if kv_scale is None:
-        cache = _is(k_cache, _BF16, pool) and _is(v_cache, _BF16, pool)
+        cache = (k_cache.dtype is _BF16 and k_cache.is_contiguous() and v_cache.dtype is _BF16
+                 and v_cache.shape == pool and v_cache.is_contiguous())
     else:
-        cache = _is_codes(k_cache, pool) and _is_codes(v_cache, pool) and _is(kv_scale, _U8, (nblk, Hkv, bs, 2))
-    if not (cache and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
+        cache = (_is_codes(k_cache, pool) and _is_codes(v_cache, pool)
+                 and _is(kv_scale, _U8, (nblk, Hkv, bs, 2)))
+    if not (cache and pool == (nblk, Hkv, bs, D) and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
             and _is(prefix_len, _I32, (B,)) and _is(new_prefix_len, _I32, (B,))
             and (status is None or _is(status, _I32, (B,)))):
         _bad(where)
     handle = _launch_stream(where, stream, q, k, v, cu_len, prefix_len, q_out if q is not None else None, k_cache,
                             v_cache, kv_scale, block_table, new_prefix_len, status)
-    p = AppendParams(_opt(q), k.data_ptr(), v.data_ptr(), _opt(q_out) if q is not None else None, k_cache.data_ptr(),
-                     v_cache.data_ptr(), _opt(kv_scale), cu_len.data_ptr(), prefix_len.data_ptr(),
-                     block_table.data_ptr(), new_prefix_len.data_ptr(), _opt(status),
-                     None if rope is None else ctypes.pointer(_rope_params(rope)), qt, qh, kt, kh, vt, vh, B, T, Hq,
-                     Hkv, D, bs, nblk, maxb)
-    _check(lib().tree_cache_append_rope(ctypes.byref(p), handle), where)
+    block = _APPEND.pack(
+        0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if q is None else q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), 0 if kv_scale is None else kv_scale.data_ptr(), cu_len.data_ptr(),
+        prefix_len.data_ptr(), block_table.data_ptr(), new_prefix_len.data_ptr(),
+        0 if status is None else status.data_ptr(), 0 if rope is None else _rope_params(rope)[1], qt, qh, kt, kh, vt, vh,
+        B, T, Hq, Hkv, D, bs, nblk, maxb)
+    _check(lib().tree_cache_append_rope(block, handle), where)
 
 
 def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -699,9 +722,10 @@ def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     for t in (out, k_cache, v_cache, block_table, cu_len, kv_len, lse, status):
         if t is not None and t.get_device() != dev:
             _bad(where)
-    p = ChunkParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_len.data_ptr(),
-                    kv_len.data_ptr(), cu.ctypes.data, kv.ctypes.data, out.data_ptr(), _opt(lse), _opt(status), B, T, Hq,
-                    Hkv, D, bs, nblk, maxb, scale, window, sinks)
+    p = ChunkParams.from_buffer_copy(_CHUNK.pack(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_len.data_ptr(),
+        kv_len.data_ptr(), _address(cu), _address(kv), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        0 if status is None else status.data_ptr(), B, T, Hq, Hkv, D, bs, nblk, maxb, scale, window, sinks))
     p._keep = (cu, kv, q, k_cache, v_cache, block_table, cu_len, kv_len, out, lse, status)
     p.device = dev
     return p
@@ -746,16 +770,15 @@ def tree_attn_fwd_window(params: AttnParams, window: int, sinks: int, workspace:
     of ``window`` positions and ``sinks`` first tokens that stay visible."""
     where = "tree_attn_fwd_window"
     q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, anc_mask, out, lse, status = params.tensors
-    B, N, Hq, D = q.shape
-    nblk, Hkv, bs, _ = k_cache.shape
-    tree, pool = (B, N, Hkv, D), (nblk, Hkv, bs, D)
-    if not (_is(q, _BF16, (B, N, Hq, D)) and _is(out, _BF16, (B, N, Hq, D)) and _is(k_cache, _BF16, pool)
-            and _is(v_cache, _BF16, pool) and _is(k_tree, _BF16, tree) and _is(v_tree, _BF16, tree)
-            and _is(block_table, _I32, (B, block_table.shape[1])) and _is(prefix_len, _I32, (B,))
-            and (anc_mask.dtype is torch.int64 or anc_mask.dtype is torch.uint64)
-            and _is(anc_mask, anc_mask.dtype, (B, N, (N + 63) // 64)) and params._keep[0].shape == (B,)
-            and (lse is None or _is(lse, torch.float32, (B, N, Hq))) and (status is None or _is(status, _I32, (B,)))
-            and workspace.is_contiguous()):
+    rows, pool = q.shape, k_cache.shape
+    B, N, Hq, D = rows
+    tree, masks = (B, N, pool[1], D), anc_mask.dtype
+    if not (q.dtype is _BF16 and q.is_contiguous() and _is(out, _BF16, rows) and k_cache.dtype is _BF16
+            and k_cache.is_contiguous() and pool[3] == D and _is(v_cache, _BF16, pool) and _is(k_tree, _BF16, tree)
+            and _is(v_tree, _BF16, tree) and _is(block_table, _I32, (B, params.max_blocks)) and _is(prefix_len, _I32, (B,))
+            and (masks is torch.int64 or masks is torch.uint64) and _is(anc_mask, masks, (B, N, (N + 63) // 64))
+            and params._keep[0].shape == (B,) and (lse is None or _is(lse, torch.float32, (B, N, Hq)))
+            and (status is None or _is(status, _I32, (B,))) and workspace.is_contiguous()):
         _bad(where)
     handle = _launch_stream(where, stream, workspace, *params.tensors)
     _check(lib().tree_attn_fwd_window(ctypes.byref(params), window, sinks, workspace.data_ptr(),
