@@ -21,6 +21,9 @@
 // memory, so there is no workspace.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
+#include "fastexp.cuh"
 #include "internal.cuh"
 
 namespace ts {
@@ -30,7 +33,8 @@ namespace cg = cooperative_groups;
 
 constexpr int LP_THREADS = 512;
 constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_COLUMN = 32;     // vectors a thread at most: one a lane when a warp reads a column again
+constexpr int LP_COLUMN = 64;     // vectors a thread at most: two a lane when a warp reads a column again
+constexpr int LP_SLOTS = 2 * PLAN_SMS;  // CTAs that run at once
 constexpr float LP_LOW = -200.f;  // 2^LOW is 0 in fp32
 
 // Larger float, larger unsigned; -0 as +0.
@@ -130,7 +134,9 @@ struct Shared {
   unsigned long long best[LOGPROB_MAX_TOP];    // its alternatives, best first; 0: none
   int column[LOGPROB_MAX_TOP];
   int n_columns, n_found;
-  unsigned long long found[LOGPROB_MAX_TOP * LOGPROB_MAX_TOP];
+  uint32_t low[LP_WARPS], high[LP_WARPS];      // of the threads' largest
+  float token;                                 // the given token's logit
+  unsigned long long found[LP_COLUMN / 32 * LOGPROB_MAX_TOP * LOGPROB_MAX_TOP];
 };
 
 // Every thread of the CTA: how many have pred set.
@@ -147,7 +153,7 @@ __device__ __forceinline__ void rank_found(Shared& sh, int n, int top) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(LP_THREADS, 3)
+__global__ void __launch_bounds__(LP_THREADS, 2)
 k_logprobs(const __grid_constant__ LogprobArgs a) {
   constexpr int N = Vec<T>::N, LP_UN = Vec<T>::UN;
   __shared__ Shared sh;
@@ -167,15 +173,26 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
   Stats st{-INFINITY, 0.f, 0.f};
   float best_v = -INFINITY;
   int best_j = -1;
+  // the next batch's loads are in flight while one is at work
+  const auto whole = [&](int j) {
+    const int last = j + (LP_UN - 1) * LP_THREADS;
+    return last < j1 && row.whole(j) && row.whole(last);
+  };
+  uint4 next[LP_UN];
+  bool loaded = whole(j0 + tid);
+  if (loaded) {
+#pragma unroll
+    for (int u = 0; u < LP_UN; ++u) next[u] = row.raw(j0 + tid + u * LP_THREADS);
+  }
+  if (rank == 0 && tid == LP_THREADS - 1 && a.tokens) {
+    const int t = a.tokens[r];
+    sh.token = t >= 0 && t < a.V ? widen(row.x[t]) : 0.f;
+  }
   for (int j = j0 + tid; j < j1; j += LP_UN * LP_THREADS) {
     float v[LP_UN][N];
-    const int last = j + (LP_UN - 1) * LP_THREADS;
-    if (last < j1 && row.whole(j) && row.whole(last)) {
-      uint4 raw[LP_UN];
+    if (loaded) {
 #pragma unroll
-      for (int u = 0; u < LP_UN; ++u) raw[u] = row.raw(j + u * LP_THREADS);
-#pragma unroll
-      for (int u = 0; u < LP_UN; ++u) Vec<T>::unpack(raw[u], v[u]);
+      for (int u = 0; u < LP_UN; ++u) Vec<T>::unpack(next[u], v[u]);
     } else {
 #pragma unroll
       for (int u = 0; u < LP_UN; ++u) {
@@ -186,6 +203,12 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
           for (int e = 0; e < N; ++e) v[u][e] = -INFINITY;
         }
       }
+    }
+    const int jn = j + LP_UN * LP_THREADS;
+    loaded = whole(jn);
+    if (loaded) {
+#pragma unroll
+      for (int u = 0; u < LP_UN; ++u) next[u] = row.raw(jn + u * LP_THREADS);
     }
     float top = st.m;
 #pragma unroll
@@ -207,16 +230,26 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
       st.m = top;
     }
     const float base = st.m == -INFINITY ? 0.f : st.m;
+    uint64_t s2 = 0ull, u2 = 0ull;
+    const uint64_t nb2 = fx::pack2(-base, -base), k2 = fx::pack2(k, k);
 #pragma unroll
     for (int u = 0; u < LP_UN; ++u) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float y = fmaxf((v[u][e] - base) * k, LP_LOW);
-        const float p = lp_ex2(y);
-        st.s += p;
-        st.u = fmaf(p, y, st.u);
+      for (int e = 0; e < N; e += 2) {
+        float y0, y1;
+        fx::unpack2(fx::mul2(fx::add2(fx::pack2(v[u][e], v[u][e + 1]), nb2), k2), y0, y1);
+        y0 = fmaxf(y0, LP_LOW);
+        y1 = fmaxf(y1, LP_LOW);
+        const uint64_t p2 = fx::pack2(lp_ex2(y0), lp_ex2(y1));
+        s2 = fx::add2(s2, p2);
+        u2 = fx::fma2(p2, fx::pack2(y0, y1), u2);
       }
     }
+    float x0, x1;
+    fx::unpack2(s2, x0, x1);
+    st.s += x0 + x1;
+    fx::unpack2(u2, x0, x1);
+    st.u += x0 + x1;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -252,10 +285,20 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
     uint32_t least = ORDERED_NEG_INF + 1;
     int reach = count(any);
     if (reach > top) {
-      uint32_t bits = 0;
-      for (int bit = 31; bit >= 0 && reach != top; --bit) {
+      // (the bits that all of them share need no search)
+      const uint32_t wl = __reduce_min_sync(0xffffffffu, any ? mine : 0xffffffffu), wh = __reduce_max_sync(0xffffffffu, mine);
+      if (lane == 0) {
+        sh.low[warp] = wl;
+        sh.high[warp] = wh;
+      }
+      __syncthreads();
+      const uint32_t lo = __reduce_min_sync(0xffffffffu, sh.low[lane % LP_WARPS]);
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, sh.high[lane % LP_WARPS]);
+      const int first = 31 - __clz(lo ^ hi);  // -1: all alike
+      uint32_t bits = first < 0 ? lo : first == 31 ? 0u : lo >> (first + 1) << (first + 1);
+      for (int bit = first; bit >= 0 && reach != top; --bit) {
         const uint32_t trial = bits | (1u << bit);
-        const int n = count(mine >= trial);
+        const int n = count(any && mine >= trial);
         if (n >= top) {
           bits = trial;
           reach = n;
@@ -277,11 +320,28 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
     if (in) sh.column[atomicAdd(&sh.n_columns, 1)] = tid;
     __syncthreads();
     const int columns = min(sh.n_columns, top);
-    for (int c = warp; c < columns; c += LP_WARPS) {
-      const int j = j0 + sh.column[c] + lane * LP_THREADS;
+    constexpr int PARTS = LP_COLUMN / 32, MINE = LOGPROB_MAX_TOP / LP_WARPS;
+    uint4 w[MINE][PARTS];  // all of the warp's vectors on their way at once
+    const auto place = [&](int c, int h) { return j0 + sh.column[c] + (lane + 32 * h) * LP_THREADS; };
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int c = warp + i * LP_WARPS;
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        w[i][h] = make_uint4(0, 0, 0, 0);
+        if (c < columns && place(c, h) < j1 && row.whole(place(c, h))) w[i][h] = row.raw(place(c, h));
+      }
+    }
+#pragma unroll
+    for (int ih = 0; ih < MINE * PARTS; ++ih) {
+      const int i = ih / PARTS, h = ih % PARTS, c = warp + i * LP_WARPS;
+      if (c >= columns) continue;
+      const int j = place(c, h);
       float v[N];
-      if (j < j1) {
-        row.get(j, v);
+      if (j < j1 && row.whole(j)) {
+        Vec<T>::unpack(w[i][h], v);
+      } else if (j < j1) {
+        row.part(j, v);
       } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = -INFINITY;
@@ -302,7 +362,7 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
           if (key[e]) sh.found[at++] = key[e];
-      } else {  // the best `top` of the column, one after the other
+      } else {  // the best `top` of these, one after the other
         int at = 0;
         if (lane == 0) at = atomicAdd(&sh.n_found, top);
         at = __shfl_sync(0xffffffffu, at, 0);
@@ -364,7 +424,7 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
       if (a.logprob) {
         const int t = a.tokens[r];
         float lp = t == -1 ? 0.f : NAN;
-        if (t >= 0 && t < a.V) lp = empty ? -INFINITY : (widen(row.x[t]) - b.m) * a.inv_temp - ls * LN2;
+        if (t >= 0 && t < a.V) lp = empty ? -INFINITY : (sh.token - b.m) * a.inv_temp - ls * LN2;
         a.logprob[r] = lp;
       }
       if (a.entropy) a.entropy[r] = empty ? 0.f : (ls - b.u / b.s) * LN2;
@@ -382,12 +442,13 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
 template <typename T>
 cudaError_t launch(LogprobArgs a, cudaStream_t s) {
   constexpr int N = Vec<T>::N;
-  // CTAs a row: as few as a thread's column allows, doubled while the SMs are
-  // not all busy and a CTA keeps a batch for each thread.
+  // CTAs a row: one, or as many as the SMs hold at once where there are few rows
+  // (and a CTA keeps a vector for each thread), or a thread's column allows.
   const int vecs = a.V / N + 2;
-  int c = 1;
-  while (ceil_div(vecs, c) > LP_COLUMN * LP_THREADS) c *= 2;
-  while (c < 8 && (long long)a.R * c < 3 * PLAN_SMS && vecs / c > Vec<T>::UN * LP_THREADS) c *= 2;
+  int c = LP_SLOTS / a.R;
+  c = std::min(std::min(c, 8), vecs / LP_THREADS);
+  c = std::max(c, ceil_div(vecs, LP_COLUMN * LP_THREADS));
+  if (c < 1) c = 1;
   a.slice = ceil_div(vecs, c);
   cudaLaunchConfig_t cfg{};
   if ((long long)a.R * c > 0x7fffffffll) return cudaErrorInvalidValue;
