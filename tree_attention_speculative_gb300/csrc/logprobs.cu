@@ -31,10 +31,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int LP_THREADS = 512;
-constexpr int LP_WARPS = LP_THREADS / 32;
+// Threads a CTA: 256, four CTAs an SM (a row's end is shorter, and more of the others
+// run beside it), where a CTA then still holds a whole row; else 512.  4096 rows of
+// 32000 105 us (127 with 512), 500 of 1000 7.8 (12.2), 2048 bf16 rows of 128256 141
+// (147); 2048 fp32 rows of 128256, two CTAs of 256 a row, 221 (194).
+constexpr int LP_FEW = 256, LP_MANY = 512;
 constexpr int LP_COLUMN = 64;     // vectors a thread at most: two a lane when a warp reads a column again
-constexpr int LP_SLOTS = 2 * PLAN_SMS;  // CTAs that run at once
+constexpr int LP_SM_THREADS = 1024;  // threads that run on an SM at once
 constexpr float LP_LOW = -200.f;  // 2^LOW is 0 in fp32
 
 // Larger float, larger unsigned; -0 as +0.
@@ -128,7 +131,9 @@ __device__ __forceinline__ Stats join(const Stats& a, const Stats& b, float k) {
   return r;
 }
 
+template <int LP_THREADS>
 struct Shared {
+  static constexpr int LP_WARPS = LP_THREADS / 32;
   Stats warp[LP_WARPS];
   Stats all;                                   // the CTA's
   unsigned long long best[LOGPROB_MAX_TOP];    // its alternatives, best first; 0: none
@@ -143,7 +148,8 @@ struct Shared {
 __device__ __forceinline__ int count(bool pred) { return __syncthreads_count(pred); }
 
 // found[0 .. n) ranked: the best `top` to best[], in order.  Keys are distinct.
-__device__ __forceinline__ void rank_found(Shared& sh, int n, int top) {
+template <int LP_THREADS>
+__device__ __forceinline__ void rank_found(Shared<LP_THREADS>& sh, int n, int top) {
   for (int c = threadIdx.x; c < n; c += LP_THREADS) {
     const unsigned long long key = sh.found[c];
     int rank = 0;
@@ -152,11 +158,12 @@ __device__ __forceinline__ void rank_found(Shared& sh, int n, int top) {
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(LP_THREADS, 2)
+template <typename T, int LP_THREADS>
+__global__ void __launch_bounds__(LP_THREADS, LP_SM_THREADS / LP_THREADS)
 k_logprobs(const __grid_constant__ LogprobArgs a) {
+  constexpr int LP_WARPS = LP_THREADS / 32;
   constexpr int N = Vec<T>::N, LP_UN = Vec<T>::UN;
-  __shared__ Shared sh;
+  __shared__ Shared<LP_THREADS> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
   const int r = blockIdx.x / ranks;
@@ -439,13 +446,11 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
   if (ranks > 1) cluster.sync();  // the CTAs' shared memory stays until it has been read
 }
 
-template <typename T>
-cudaError_t launch(LogprobArgs a, cudaStream_t s) {
-  constexpr int N = Vec<T>::N;
+template <typename T, int LP_THREADS>
+cudaError_t launch(LogprobArgs a, int vecs, cudaStream_t s) {
   // CTAs a row: one, or as many as the SMs hold at once where there are few rows
   // (and a CTA keeps a vector for each thread), or a thread's column allows.
-  const int vecs = a.V / N + 2;
-  int c = LP_SLOTS / a.R;
+  int c = PLAN_SMS * (LP_SM_THREADS / LP_THREADS) / a.R;
   c = std::min(std::min(c, 8), vecs / LP_THREADS);
   c = std::max(c, ceil_div(vecs, LP_COLUMN * LP_THREADS));
   if (c < 1) c = 1;
@@ -463,7 +468,13 @@ cudaError_t launch(LogprobArgs a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_logprobs<T>, a);
+  return cudaLaunchKernelEx(&cfg, k_logprobs<T, LP_THREADS>, a);
+}
+
+template <typename T>
+cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
+  const int vecs = a.V / Vec<T>::N + 2;
+  return vecs <= LP_COLUMN * LP_FEW ? launch<T, LP_FEW>(a, vecs, s) : launch<T, LP_MANY>(a, vecs, s);
 }
 
 }  // namespace
