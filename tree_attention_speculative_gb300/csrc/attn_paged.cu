@@ -79,7 +79,7 @@ struct __align__(1024) Smem {
   uint64_t k_full[C::NST], v_full[C::NST];
   uint64_t k_empty[C::NST], v_empty[C::NST];
   uint64_t s_full[C::NSB], p_full[C::NSB][2], s_free[C::NSB];
-  uint64_t o_ready;
+  uint64_t o_ready, o_last;  // a tile's PV has completed; an item's last one has
   uint64_t ml_full, f_full, o_free;  // an item's end: see ml; both groups have read the accumulators
   uint64_t drain[2];
   uint32_t tmem_base;
@@ -252,6 +252,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       mbar_init(&sm.s_free[i], 1);
     }
     mbar_init(&sm.o_ready, 1);
+    mbar_init(&sm.o_last, 1);
     mbar_init(&sm.ml_full, GROUP_THREADS);
     mbar_init(&sm.f_full, GROUP_THREADS);
     mbar_init(&sm.o_free, 2 * GROUP_THREADS);
@@ -530,6 +531,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         if (leader) {
           mma_commit(&sm.s_free[buf]);
           mma_commit(&sm.o_ready);
+          if (j == n_tiles - 1) mma_commit(&sm.o_last);
           mma_commit(&sm.v_empty[slot]);
         }
         __syncwarp();
@@ -724,65 +726,72 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       if (!ok) break;
       // the item's end: its last PV, then the groups' halves joined.  Each group
       // stores half of the channels, of both accumulators.
-      float f0 = 0.f, f1 = 0.f, lse2 = NEG_INF;
-      if (half == 0) {
-        ok = __all_sync(0xffffffffu, wait_bar(&sm.ml_full, k & 1, ctl) && wait_count(&sm.pv_done, jg, ctl));
-        if (ok) {
-          const float2 other = sm.ml[r];
-          const float m_all = fmaxf(m_run, other.x);
-          f0 = m_run == NEG_INF ? 0.f : ex2(m_run - m_all);
-          f1 = other.x == NEG_INF ? 0.f : ex2(other.x - m_all);
-          const float l_all = l_run * f0 + other.y * f1;
-          const float inv = l_all > 0.f ? 1.f / l_all : 0.f;  // a row that sees no key: zeros
-          if (l_all > 0.f) lse2 = m_all + __log2f(l_all);
-          f0 *= inv;
-          f1 *= inv;
-          sm.ml[r] = make_float2(f0, f1);
-          mbar_arrive(&sm.f_full);
-        }
-      } else {
+      if (half == 1) {
         sm.ml[r] = make_float2(m_run, l_run);
         mbar_arrive(&sm.ml_full);
-        ok = __all_sync(0xffffffffu, wait_bar(&sm.f_full, k & 1, ctl) && wait_count(&sm.pv_done, jg, ctl));
-        if (ok) {
-          f0 = sm.ml[r].x;
-          f1 = sm.ml[r].y;
-        }
       }
+      Item next;  // asked for while the last PV runs
+      ok = __all_sync(0xffffffffu, queue_item(k + 1, next));
       if (!ok) break;
-      tc_fence_after();
+      float f0 = 0.f, f1 = 0.f, lse2 = NEG_INF;
+      if (half == 0) {
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.ml_full, k & 1, ctl));
+        if (!ok) break;
+        const float2 other = sm.ml[r];
+        const float m_all = fmaxf(m_run, other.x);
+        f0 = m_run == NEG_INF ? 0.f : ex2(m_run - m_all);
+        f1 = other.x == NEG_INF ? 0.f : ex2(other.x - m_all);
+        const float l_all = l_run * f0 + other.y * f1;
+        const float inv = l_all > 0.f ? 1.f / l_all : 0.f;  // a row that sees no key: zeros
+        if (l_all > 0.f) lse2 = m_all + __log2f(l_all);
+        f0 *= inv;
+        f1 *= inv;
+        sm.ml[r] = make_float2(f0, f1);
+        mbar_arrive(&sm.f_full);
+      } else {
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.f_full, k & 1, ctl));
+        if (!ok) break;
+        f0 = sm.ml[r].x;
+        f1 = sm.ml[r].y;
+      }
       const bool direct = I.ps == 1;
       const PagedSeq& sq = args.seq[I.e];
       const size_t orow = direct ? (size_t)(I.q0 + i) * a.Hq + I.g * a.G + h_in
                                  : ((size_t)sq.part_row + (size_t)I.split * sq.rows + i) * a.Hq + I.g * a.G + h_in;
+      ok = __all_sync(0xffffffffu, wait_bar(&sm.o_last, k & 1, ctl));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t f02 = fx::pack2(f0, f0), f12 = fx::pack2(f1, f1);
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-        uint32_t u[32], v[32];
-        tmem_ld32(tmem + lane_base + c, u);
-        tmem_ld32(tmem + lane_base + D + c, v);
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+        uint32_t u[16], v[16];
+        tmem_ld16(tmem + lane_base + c, u);
+        tmem_ld16(tmem + lane_base + D + c, v);
         tmem_ld_wait();
-        reg_fence32(u);
-        reg_fence32(v);
+        reg_fence16(u);
+        reg_fence16(v);
+        float x[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f0 + __uint_as_float(v[e]) * f1);
+        for (int e = 0; e < 16; e += 2)
+          fx::unpack2(fx::fma2(fx::pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f12,
+                               fx::mul2(fx::pack2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), f02)),
+                      x[e], x[e + 1]);
         if (!active) continue;
         if (direct) {
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+          for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
           __nv_bfloat16* dst = a.out + orow * D + c;
           if (args.out32) {
             st_v8(dst, w);
-            st_v8(dst + 16, w + 8);
           } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
         } else {
           float* dst = a.part_o + orow * D + c;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) st_v8(dst + 8 * q, u + 8 * q);
+          st_v8(dst, reinterpret_cast<const uint32_t*>(x));
+          st_v8(dst + 8, reinterpret_cast<const uint32_t*>(x) + 8);
         }
       }
       if (active && half == 0) {
@@ -794,7 +803,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       mbar_arrive(&sm.o_free);
       __syncwarp();
       if (half == 0 && r == 0) publish(&sm.items_done, k + 1);
-      ok = __all_sync(0xffffffffu, queue_item(k + 1, I));
+      I = next;
     }
   }
 
