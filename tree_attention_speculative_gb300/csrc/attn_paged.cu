@@ -64,6 +64,9 @@ struct Cfg {
   static constexpr int HALF_BYTES = KV_TILE * 128;
   static constexpr int Q_BYTES = ROW_TILE * D * 2;
   static constexpr int NST = D == 128 ? 3 : 6;  // tiles in each ring, K and V
+  // The two softmax groups: on heads of 64 they take the tiles in turn, on heads of
+  // 128 half the keys of every tile each.
+  static constexpr bool TURNS = D == 64;
   // TMEM: the groups' accumulators at 0 and D, then the S buffers
   static constexpr uint32_t TMEM_S0 = 2 * D;
   static constexpr int NSB = (TMEM_COLS - TMEM_S0) / KV_TILE;  // 2 for heads of 128, 3 for 64
@@ -79,12 +82,11 @@ struct __align__(1024) Smem {
   uint64_t k_full[C::NST], v_full[C::NST];
   uint64_t k_empty[C::NST], v_empty[C::NST];
   uint64_t s_full[C::NSB], p_full[C::NSB][2], s_free[C::NSB];
-  uint64_t o_ready, o_last;  // a tile's PV has completed; an item's last one has
+  uint64_t o_last;  // an item's last PV has completed
   uint64_t ml_full, f_full, o_free;  // an item's end: see ml; both groups have read the accumulators
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  int pv_done;  // PVs completed so far
   // the CTA's items in the order taken; pub published, done stored
   int4 item_q[ITEM_Q][4];
   int items_pub, items_done;
@@ -234,7 +236,6 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
   }
   if (threadIdx.x == 0) {
     sm.abort_flag = 0;
-    sm.pv_done = 0;
     sm.items_pub = 0;
     sm.items_done = 0;
     mbar_init(&sm.q_full, 1);
@@ -251,7 +252,6 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       mbar_init(&sm.p_full[i][1], GROUP_THREADS);
       mbar_init(&sm.s_free[i], 1);
     }
-    mbar_init(&sm.o_ready, 1);
     mbar_init(&sm.o_last, 1);
     mbar_init(&sm.ml_full, GROUP_THREADS);
     mbar_init(&sm.f_full, GROUP_THREADS);
@@ -406,9 +406,9 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         if (jg >= C::NST && !__all_sync(0xffffffffu, wait_bar(&empty[slot], phase ^ 1, ctl))) return jg;
         if (j == stop) return jg;
         if (j < n_prefix) {
-          // the lanes that hold this tile's boxes issue them
+          // the lanes that hold this tile's boxes issue them (bytes that land before
+          // they are announced count all the same)
           if (leader) mbar_arrive_expect_tx(&full[slot], __popc((boxes >> (jt << lg_boxes)) & ((1u << n_boxes) - 1)) * box_bytes);
-          __syncwarp();
           if ((lane >> lg_boxes) == jt && slab >= 0)
             tma_load_5d(dst + (lane & (n_boxes - 1)) * box_bytes, tm_pool, &full[slot], 0, 0, 0, row8, slab);
         } else if (leader) {
@@ -506,23 +506,30 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         const uint32_t p_tmem = tmem + TMEM_S0 + buf * KV_TILE;
         const bool tree = TREE && j >= n_prefix;
         const uint64_t vd = (tree ? vt_desc : v_desc) + slot * (C::TILE_BYTES >> 4);
+        const int acc = C::TURNS ? (j & 1) * D : 0;  // (halves: the second half's is D)
+        const bool fresh = j < (C::TURNS ? 2 : 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          ok = __all_sync(0xffffffffu, wait_bar(&sm.p_full[buf][half], p_phase, ctl) &&
-                                           (half || wait_bar(&sm.v_full[slot], v_phase, ctl)));
-          if (!ok) break;
-          tc_fence_after();
+          if (!C::TURNS || half == 0) {
+            ok = __all_sync(0xffffffffu, wait_bar(&sm.p_full[buf][half], p_phase, ctl) &&
+                                             (half || wait_bar(&sm.v_full[slot], v_phase, ctl)));
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (leader) {
+            const uint32_t o = tmem + (C::TURNS ? acc : half * D);
             if (!tree) {
 #pragma unroll
               for (int k2 = 0; k2 < HALF / 16; ++k2)
-                mma_ts(tmem + half * D, p_tmem + half * HALF + k2 * 8,
-                       vd + (((half * (HALF / 16) + k2) * 2 * C::HALVES * 1024) >> 4), ID_PV, j > 0 || k2 > 0);
+                mma_ts(o, p_tmem + half * HALF + k2 * 8,
+                       vd + (((half * (HALF / 16) + k2) * 2 * C::HALVES * 1024) >> 4), ID_PV,
+                       !fresh || k2 > 0 || (C::TURNS && half));
             } else {
 #pragma unroll
               for (int k2 = 0; k2 < HALF / 16; ++k2)
-                mma_ts(tmem + half * D, p_tmem + half * HALF + k2 * 8,
-                       vd + (((half * (HALF / 16) + k2) * 2 * 1024) >> 4), ID_PV, j > 0 || k2 > 0);
+                mma_ts(o, p_tmem + half * HALF + k2 * 8,
+                       vd + (((half * (HALF / 16) + k2) * 2 * 1024) >> 4), ID_PV,
+                       !fresh || k2 > 0 || (C::TURNS && half));
             }
           }
           __syncwarp();
@@ -530,16 +537,9 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         if (!ok) break;
         if (leader) {
           mma_commit(&sm.s_free[buf]);
-          mma_commit(&sm.o_ready);
           if (j == n_tiles - 1) mma_commit(&sm.o_last);
           mma_commit(&sm.v_empty[slot]);
         }
-        __syncwarp();
-        // published so that the softmax looks at O only when it has to
-        ok = __all_sync(0xffffffffu, wait_bar(&sm.o_ready, jg & 1, ctl));
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) publish(&sm.pv_done, jg + 1);
         __syncwarp();
         if (++slot == C::NST) {
           slot = 0;
@@ -552,7 +552,12 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       }
     }
   } else {
-    const int half = (warp - SOFTMAX_WARP0) >> 2;  // the group: keys 64 half .. of each tile, accumulator half
+    // Keys of a tile that a group takes, in parts of 64 (that many scores fit the
+    // registers): a tile's are read from TMEM for their maximum, and again for the
+    // weights (the read costs 35 cycles).
+    constexpr int KEYS = C::TURNS ? KV_TILE : HALF, PARTS = KEYS / HALF, STEP = C::TURNS ? 2 : 1;
+    const int half = (warp - SOFTMAX_WARP0) >> 2;  // the group, and its accumulator
+    const int key_in = C::TURNS ? 0 : half * HALF;  // its first key of a tile
     const int r = (threadIdx.x - SOFTMAX_WARP0 * 32) & (GROUP_THREADS - 1);  // TMEM lane, and row of the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_tmem = tmem + lane_base + half * D;
@@ -566,7 +571,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       const int i = active ? I.i0 + i_in : I.len - 1;
       // the cached keys the row sees: t < hi, and t >= lo or t < sinks
       int lo, hi, hi_least, lo_most;
-      uint64_t anc[2] = {0ull, 0ull};  // this group's keys of the two tree tiles
+      uint64_t anc[2][PARTS] = {};  // the group's keys of the two tree tiles
       if (TREE) {
         const int P = I.pos0;
         uint64_t w4[4] = {0ull, 0ull, 0ull, 0ull};
@@ -598,8 +603,11 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             }
           }
         }
-        anc[0] = half ? w4[1] : w4[0];
-        anc[1] = half ? w4[3] : w4[2];
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+          anc[0][h] = (C::TURNS ? h : half) ? w4[1] : w4[0];
+          anc[1][h] = (C::TURNS ? h : half) ? w4[3] : w4[2];
+        }
       } else {
         const int pos = I.pos0 + (i - I.i0);
         lo = pos - a.window + 1;
@@ -615,64 +623,83 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       if (lo_most > 0) clear0 = I.n_sink + max(ceil_div(lo_most, KV_TILE) - I.win0, 0) - I.t_begin;
       const int clear1 = I.n_sink + hi_least / KV_TILE - I.win0 - I.t_begin;
       float m_run = NEG_INF, l_run = 0.f;
-      for (int j = 0; j < I.n_tiles; ++j, ++jg) {
-        if (!__all_sync(0xffffffffu, wait_bar(&sm.s_full[jg % NSB], (jg / NSB) & 1, ctl))) {
+      const int first = C::TURNS ? half : 0;
+      for (int j = first; j < I.n_tiles; j += STEP) {
+        const int jt = jg + j, buf = jt % NSB;
+        if (!__all_sync(0xffffffffu, wait_bar(&sm.s_full[buf], (jt / NSB) & 1, ctl))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + (jg % NSB) * KV_TILE + half * HALF;
+        const uint32_t s_tmem = tmem + lane_base + TMEM_S0 + buf * KV_TILE + key_in;
+        uint64_t see[PARTS];  // the keys this row sees, where it may not see all
+        bool dead = false;
+        int key0 = 0;
+        const bool masked = j < clear0 || j >= clear1;
+        if (masked) {
+          const bool tree = TREE && j >= I.n_prefix;
+          if (!tree) {
+            key0 = tile_key(I, j) + key_in;
+            dead = key0 + KEYS > I.hi || (key0 < I.lo && key0 + KEYS > a.sinks);
+          }
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) {
+            const int at = key0 + h * HALF;
+            see[h] = tree ? anc[j > I.n_prefix][h]
+                          : first_bits(hi - at) & (~first_bits(lo - at) | first_bits(a.sinks - at));
+          }
+        }
         float s[HALF];
-        {
+        const auto load = [&](int h) {
           uint32_t u[2][32];
-          tmem_ld32(s_tmem, u[0]);
-          tmem_ld32(s_tmem + 32, u[1]);
+          tmem_ld32(s_tmem + h * HALF, u[0]);
+          tmem_ld32(s_tmem + h * HALF + 32, u[1]);
           tmem_ld_wait();
           reg_fence32(u[0]);
           reg_fence32(u[1]);
 #pragma unroll
           for (int e = 0; e < HALF; ++e) s[e] = __uint_as_float(u[e / 32][e % 32]);
-        }
-        bool dead = false;
-        int key0 = 0;
-        if (j < clear0 || j >= clear1) {
-          uint64_t w;  // the keys this row sees
-          if (TREE && j >= I.n_prefix) {
-            w = j > I.n_prefix ? anc[1] : anc[0];
-          } else {
-            key0 = tile_key(I, j) + half * HALF;
-            w = first_bits(hi - key0) & (~first_bits(lo - key0) | first_bits(a.sinks - key0));
-            dead = key0 + HALF > I.hi || (key0 < I.lo && key0 + HALF > a.sinks);
+          if (masked) {
+            const uint64_t w = PARTS > 1 && h ? see[PARTS - 1] : see[0];
+#pragma unroll
+            for (int e = 0; e < HALF; ++e)
+              if (!((w >> e) & 1ull)) s[e] = NEG_INF;
           }
+        };
+        float m_new = m_run;
+#pragma unroll 1
+        for (int h = 0; h < PARTS; ++h) {
+          load(h);
+          float mk[4];
 #pragma unroll
-          for (int e = 0; e < HALF; ++e)
-            if (!((w >> e) & 1ull)) s[e] = NEG_INF;
+          for (int e = 0; e < 4; ++e) mk[e] = s[e];
+#pragma unroll
+          for (int c = 4; c < HALF; c += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
+          m_new = fmaxf(m_new, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
         }
-        float mk[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mk[e] = s[e];
-#pragma unroll
-        for (int c = 4; c < HALF; c += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
-        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
-        const bool rescale = j > 0 && active && m_new > m_run + RESCALE_THRESHOLD;
+        const bool rescale = j > first && active && m_new > m_run + RESCALE_THRESHOLD;
         float m_use = m_run;
-        if (j == 0 || rescale) m_use = m_new;
+        if (j == first || rescale) m_use = m_new;
         const float m_exp = m_use == NEG_INF ? 0.f : m_use;  // nothing visible so far: every weight is 0
         const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
         const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
         uint64_t sum2[2] = {0ull, 0ull};
-        uint32_t pk[HALF / 2];
+#pragma unroll 1
+        for (int h = PARTS - 1; h >= 0; --h) {  // (the last part is still there)
+          if (h < PARTS - 1) load(h);
+          uint32_t pk[HALF / 2];
 #pragma unroll
-        for (int e = 0; e < HALF / 2; ++e) {
-          float x0, x1;
-          fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
-          pk[e] = pack_bf16x2(p0, p1);
+          for (int e = 0; e < HALF / 2; ++e) {
+            float x0, x1;
+            fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(s_tmem + h * HALF, pk);
         }
-        tmem_st32(s_tmem, pk);
         float rowsum;
         {
           float r0, r1;
@@ -681,25 +708,28 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         }
         if (dead) {
           // V rows that no row of the item sees hold whatever the pool, or the
-          // ring, had there: zeroed, so that 0 * V is 0.  Two threads a row.
-          const int slot = jg % C::NST;
-          if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (jg / C::NST) & 1, ctl))) {
+          // ring, had there: zeroed, so that 0 * V is 0
+          const int slot = jt % C::NST;
+          if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (jt / C::NST) & 1, ctl))) {
             ok = false;
             break;
           }
-          const int t = key0 + (r & (HALF - 1)), hh = r / HALF;
-          if (hh < C::HALVES && (t >= I.hi || (t < I.lo && t >= a.sinks))) {
-            const int vr = half * HALF + (r & (HALF - 1));
+          // 64-channel pieces of the group's rows, one a thread
+          const int vr = key_in + r % KEYS, hh = r / KEYS, t = key0 + r % KEYS;
+          if (t >= I.hi || (t < I.lo && t >= a.sinks)) {
             uint4* row = reinterpret_cast<uint4*>(sm.v[slot] + ((vr >> 3) * C::HALVES + hh) * 1024 + (vr & 7) * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
         }
-        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-          // every earlier PV complete; the whole warp takes part, by 1 where a
-          // row's maximum did not move enough
-          if (!__all_sync(0xffffffffu, wait_count(&sm.pv_done, jg, ctl))) {
+        if (j > first && __any_sync(0xffffffffu, rescale)) {
+          // The accumulator's last PV complete (its S buffer is free again; the one
+          // before that was when the buffer was filled, and the one after waits for
+          // these weights, so the phase is no other's).  The whole warp takes part, by
+          // 1 where a row's maximum did not move enough.
+          const int last = jt - STEP;
+          if (!__all_sync(0xffffffffu, wait_bar(&sm.s_free[last % NSB], (last / NSB) & 1, ctl))) {
             ok = false;
             break;
           }
@@ -721,8 +751,9 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         l_run += rowsum;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sm.p_full[jg % NSB][half]);
+        mbar_arrive(&sm.p_full[buf][C::TURNS ? 0 : half]);
       }
+      jg += I.n_tiles;
       if (!ok) break;
       // the item's end: its last PV, then the groups' halves joined.  Each group
       // stores half of the channels, of both accumulators.
@@ -766,7 +797,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
         uint32_t u[16], v[16];
         tmem_ld16(tmem + lane_base + c, u);
-        tmem_ld16(tmem + lane_base + D + c, v);
+        // (the second group may have had no tile: its accumulator then holds anything)
+        tmem_ld16(tmem + lane_base + (C::TURNS && I.n_tiles == 1 ? 0 : D) + c, v);
         tmem_ld_wait();
         reg_fence16(u);
         reg_fence16(v);
