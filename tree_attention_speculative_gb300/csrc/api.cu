@@ -755,6 +755,9 @@ ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint8_t* kv
 namespace ts {
 namespace {
 
+// The paged kernels number a pool's rows in groups of 8, in an int.
+bool pool_rows(int num_blocks, int Hkv, int bs) { return (long long)num_blocks * Hkv * (bs / 8) <= 0x7fffffffll; }
+
 // Host validation of tree_chunk_attn_fwd; touches no device memory.
 ts_status check_chunk(const ts_chunk_params* p) {
   if (!p) return TS_ERR_NULL;
@@ -778,7 +781,7 @@ ts_status check_chunk(const ts_chunk_params* p) {
     if ((long long)p->max_blocks * p->block_size < kv) return TS_ERR_SHAPE;
   }
   if (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->out)) return TS_ERR_SHAPE;
-  return TS_OK;
+  return pool_rows(p->num_blocks, p->Hkv, p->block_size) ? TS_OK : TS_ERR_UNSUPPORTED;
 }
 
 void fill_paged(PagedArgs* a, const void* q, const void* k, const void* v, const int32_t* table, void* out, float* lse,
@@ -829,18 +832,20 @@ ts_status check_window(const ts_attn_params* p, int window, int sinks) {
   if (st != TS_OK) return st;
   if (window < 1 || sinks < 0) return TS_ERR_SHAPE;
   if (window > MAX_POSITION || sinks > MAX_POSITION || p->Hq > MAX_HEADS) return TS_ERR_UNSUPPORTED;
-  if ((long long)p->B * p->N > 0x7fffffffll) return TS_ERR_UNSUPPORTED;
+  if ((long long)p->B * p->N > 0x7fffffffll || !pool_rows(p->num_blocks, p->Hkv, p->block_size)) return TS_ERR_UNSUPPORTED;
   return TS_OK;
 }
 
 ts_status paged_impl(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace,
                      size_t workspace_bytes, ts_stream stream) {
-  const size_t need = attn_paged_workspace(a, cu_len_host, kv_host);
+  PagedPlan first;
+  const size_t need = attn_paged_workspace(a, cu_len_host, kv_host, &first);
   if (need == 0) return TS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return TS_ERR_WORKSPACE;
   if (a.T == 0) return TS_OK;
   if (prepare_device() != cudaSuccess) return TS_ERR_CUDA;
-  return launch_attn_paged(a, cu_len_host, kv_host, workspace, (cudaStream_t)stream) == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+  return launch_attn_paged(a, cu_len_host, kv_host, first, workspace, (cudaStream_t)stream) == cudaSuccess ? TS_OK
+                                                                                                        : TS_ERR_CUDA;
 }
 
 }  // namespace
@@ -911,7 +916,8 @@ ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream stream) {
 
 size_t tree_chunk_attn_workspace_size(const ts_chunk_params* p) {
   if (check_chunk(p) != TS_OK) return 0;
-  return attn_paged_workspace(chunk_args(p), p->cu_len_host, p->kv_len_host);
+  PagedPlan first;
+  return attn_paged_workspace(chunk_args(p), p->cu_len_host, p->kv_len_host, &first);
 }
 
 ts_status tree_chunk_attn_fwd(const ts_chunk_params* p, void* workspace, size_t workspace_bytes, ts_stream stream) {
@@ -937,7 +943,8 @@ ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* workspace, si
 
 size_t tree_attn_window_workspace_size(const ts_attn_params* p, int window, int sinks) {
   if (check_window(p, window, sinks) != TS_OK) return 0;
-  return attn_paged_workspace(window_args(p, window, sinks), nullptr, p->prefix_len_host);
+  PagedPlan first;
+  return attn_paged_workspace(window_args(p, window, sinks), nullptr, p->prefix_len_host, &first);
 }
 
 ts_status tree_attn_fwd_window(const ts_attn_params* p, int window, int sinks, void* workspace, size_t workspace_bytes,

@@ -52,9 +52,11 @@ constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 
 constexpr int HALF = KV_TILE / 2;  // keys of a tile that one softmax group takes
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int ITEM_Q = 8;    // entries of the item queue
-// O is rescaled when a row's maximum rises by more than this (in powers of two).
-// Weights then stay below 2^40; their precision does not depend on it.
+// A row's weights are taken against a reference, the maximum of the first keys it
+// sees, and may reach 2^40 of it (their precision does not depend on that).  Then the
+// reference is raised and the sums are scaled down.
 constexpr float RESCALE_THRESHOLD = 40.0f;
+constexpr float SUM_LIMIT = 1099511627776.f;  // 2^40
 constexpr float NEG_INF = -INFINITY;
 
 template <int D>
@@ -372,8 +374,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       const int* table_row = a.block_table + (size_t)b * a.max_blocks;
       // Block-table entries, a group of tiles ahead: lane L holds that of box
       // L % boxes of tile L / boxes of a group of 32 / boxes tiles, and makes the
-      // box's coordinates of it when the group's turn comes.  A box that no row of
-      // the item sees into is not read (slab -1).
+      // box's place in the pool of it when the group's turn comes.  A box that no row
+      // of the item sees into is not read.
       auto load_group = [&](int grp) -> int {
         const int j = grp * tpg + (lane >> lg_boxes);
         if (j >= n_prefix) return INT_MIN;
@@ -383,7 +385,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         return blk == INT_MIN ? -1 : blk;
       };
       int raw = load_group(0);
-      int slab = -1, row8 = 0;
+      int at8 = -1;  // its rows in the pool, in groups of 8
       unsigned boxes = 0;  // which lanes' are read
       const int stop = !is_v && b == a.stall_seq ? a.stall_tile : I.n_tiles;
       for (int j = 0; j < I.n_tiles; ++j, ++jg) {
@@ -391,16 +393,16 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         const int jt = j & (tpg - 1);
         if (jt == 0 && j < n_prefix) {
           const int grp = j >> (5 - lg_boxes);
-          slab = -1;
+          at8 = -1;
           if (raw != INT_MIN) {
             if (raw < 0 || raw >= a.num_blocks) {
               if (a.status) a.status[b] = TS_ERR_BAD_BLOCK;
               raw = 0;  // a valid block is read in its place
             }
-            slab = raw * a.Hkv + I.g;
-            row8 = args.fd_bs.mod(tile_key(I, grp * tpg + (lane >> lg_boxes)) + koff) >> 3;
+            const int row = args.fd_bs.mod(tile_key(I, grp * tpg + (lane >> lg_boxes)) + koff);
+            at8 = (raw * a.Hkv + I.g) * (a.bs >> 3) + (row >> 3);
           }
-          boxes = __ballot_sync(0xffffffffu, slab >= 0);
+          boxes = __ballot_sync(0xffffffffu, at8 >= 0);
           raw = (grp + 1) * tpg < n_prefix ? load_group(grp + 1) : INT_MIN;
         }
         if (jg >= C::NST && !__all_sync(0xffffffffu, wait_bar(&empty[slot], phase ^ 1, ctl))) return jg;
@@ -409,8 +411,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           // the lanes that hold this tile's boxes issue them (bytes that land before
           // they are announced count all the same)
           if (leader) mbar_arrive_expect_tx(&full[slot], __popc((boxes >> (jt << lg_boxes)) & ((1u << n_boxes) - 1)) * box_bytes);
-          if ((lane >> lg_boxes) == jt && slab >= 0)
-            tma_load_5d(dst + (lane & (n_boxes - 1)) * box_bytes, tm_pool, &full[slot], 0, 0, 0, row8, slab);
+          if ((lane >> lg_boxes) == jt && at8 >= 0)
+            tma_load_4d(dst + (lane & (n_boxes - 1)) * box_bytes, tm_pool, &full[slot], 0, 0, 0, at8);
         } else if (leader) {
           const int n0 = (j - n_prefix) * KV_TILE;  // nodes >= N read as zeros
           mbar_arrive_expect_tx(&full[slot], C::TILE_BYTES);
@@ -624,6 +626,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       const int clear1 = I.n_sink + hi_least / KV_TILE - I.win0 - I.t_begin;
       float m_run = NEG_INF, l_run = 0.f;
       const int first = C::TURNS ? half : 0;
+      bool fresh = true;
       for (int j = first; j < I.n_tiles; j += STEP) {
         const int jt = jg + j, buf = jt % NSB;
         if (!__all_sync(0xffffffffu, wait_bar(&sm.s_full[buf], (jt / NSB) & 1, ctl))) {
@@ -666,7 +669,54 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
               if (!((w >> e) & 1ull)) s[e] = NEG_INF;
           }
         };
-        float m_new = m_run;
+        float m_new = m_run, m_use = m_run, rowsum;
+        bool rescale = false;
+        if constexpr (C::TURNS) {
+          uint32_t pk[PARTS][HALF / 2];
+          bool look = fresh;
+          for (;;) {
+            if (look) {
+#pragma unroll 1
+              for (int h = 0; h < PARTS; ++h) {
+                load(h);
+                float mk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mk[e] = s[e];
+#pragma unroll
+                for (int c = 4; c < HALF; c += 4)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
+                m_new = fmaxf(m_new, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
+              }
+              rescale = j > first && active && m_new > m_run + 10.f;
+              if (m_run == NEG_INF || rescale) m_use = m_new;
+            }
+            const float m_exp = m_use == NEG_INF ? 0.f : m_use;
+            const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
+            const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
+            uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) {
+              load(h);
+#pragma unroll
+              for (int e = 0; e < HALF / 2; ++e) {
+                float x0, x1;
+                fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
+                pk[h][e] = pack_bf16x2(p0, p1);
+              }
+            }
+            float r0, r1;
+            fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
+            rowsum = r0 + r1;
+            if (look || !__any_sync(0xffffffffu, active && !(rowsum <= SUM_LIMIT))) break;
+            look = true;
+          }
+          if (fresh) fresh = __any_sync(0xffffffffu, m_use == NEG_INF);
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) tmem_st32(s_tmem + h * HALF, pk[h]);
+        } else {
 #pragma unroll 1
         for (int h = 0; h < PARTS; ++h) {
           load(h);
@@ -679,8 +729,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
           m_new = fmaxf(m_new, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
         }
-        const bool rescale = j > first && active && m_new > m_run + RESCALE_THRESHOLD;
-        float m_use = m_run;
+        rescale = j > first && active && m_new > m_run + RESCALE_THRESHOLD;
         if (j == first || rescale) m_use = m_new;
         const float m_exp = m_use == NEG_INF ? 0.f : m_use;  // nothing visible so far: every weight is 0
         const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
@@ -700,11 +749,11 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           }
           tmem_st32(s_tmem + h * HALF, pk);
         }
-        float rowsum;
         {
           float r0, r1;
           fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
           rowsum = r0 + r1;
+        }
         }
         if (dead) {
           // V rows that no row of the item sees hold whatever the pool, or the
@@ -1004,12 +1053,12 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
     const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tok};
     if (!encode_bf16_sw128(&m_q, a.q, 3, dims, str, box)) return cudaErrorInvalidValue;
   }
-  {  // pool [num_blocks, Hkv, bs, D] as 64 channels, 8 rows, halves, row groups, slabs
-    const uint64_t dims[5] = {64, 8, (uint64_t)(D / 64), (uint64_t)(a.bs / 8), (uint64_t)a.num_blocks * a.Hkv};
-    const uint64_t str[4] = {(uint64_t)D * 2, 128, (uint64_t)8 * D * 2, (uint64_t)a.bs * D * 2};
-    const uint32_t box[5] = {64, 8, (uint32_t)(D / 64), (uint32_t)(t.box_rows / 8), 1};
-    if (!encode_bf16_sw128(&m_kc, a.k_cache, 5, dims, str, box)) return cudaErrorInvalidValue;
-    if (!encode_bf16_sw128(&m_vc, a.v_cache, 5, dims, str, box)) return cudaErrorInvalidValue;
+  {  // pool [num_blocks, Hkv, bs, D] as 64 channels, 8 rows, halves, groups of 8 rows
+    const uint64_t dims[4] = {64, 8, (uint64_t)(D / 64), (uint64_t)a.num_blocks * a.Hkv * (a.bs / 8)};
+    const uint64_t str[3] = {(uint64_t)D * 2, 128, (uint64_t)8 * D * 2};
+    const uint32_t box[4] = {64, 8, (uint32_t)(D / 64), (uint32_t)(t.box_rows / 8)};
+    if (!encode_bf16_sw128(&m_kc, a.k_cache, 4, dims, str, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16_sw128(&m_vc, a.v_cache, 4, dims, str, box)) return cudaErrorInvalidValue;
   }
   m_kt = m_kc;
   m_vt = m_vc;
@@ -1043,11 +1092,11 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
 
 // The plan of a launch's sequences: how long a split may be.  Every chain of key
 // tiles (a row tile of a KV head) is an item or, cut, several; a CTA an SM takes
-// them longest first.  In units of a tile's time on an SM, an item costs its
-// tiles and 1.5 more, the launch ends when the SMs have shared all of that out
-// and the last items have run, and cut chains cost a second kernel and their
-// partial results' round trip (3.6 MB of traffic in a tile's time; the same
-// prices as tree attention's plan).
+// them longest first.  In units of a tile's time on an SM (0.8 us), an item costs its
+// tiles and 3 more (its start and its end), the launch ends when the SMs have shared all of that out
+// and the last items have run, and not before the keys and values have come from
+// memory.  Cut chains cost a second kernel and their partial results' round trip.
+// On the measured shapes the plans are within 5 % of the best of a sweep.
 struct Chains {
   int count;     // row tiles
   int most;      // tiles of the longest chain
@@ -1055,48 +1104,48 @@ struct Chains {
 };
 
 int plan_chunk_tiles(const Chains* c, const int* rows, int n, int Hkv, int Hq, int D, int tree_tiles) {
+  constexpr double item_cost = 3.0, join_launch = 4.0, tile_bytes = 5.4e6;  // traffic in a tile's time
   int longest = 1;
-  for (int k = 0; k < n; ++k) longest = std::max(longest, c[k].most);
+  double tiles = 0, streamed = 0;
+  for (int k = 0; k < n; ++k) {
+    longest = std::max(longest, c[k].most);
+    tiles += c[k].total + (double)c[k].count * tree_tiles;
+    streamed += c[k].most + tree_tiles;  // a sequence's row tiles read the same keys
+  }
+  const double memory = streamed * Hkv * (double)(4 * KV_TILE * D) / tile_bytes;
   double best = 1e300;
   int best_chunk = longest, last = 0;
   for (int s = 1; s <= 256; s += 1 + s / 8) {
     const int chunk = ceil_div(longest, s);
     if (chunk == last) continue;
     last = chunk;
-    double items = 0, tiles = 0, part_rows = 0, worst = 0;
+    double items = 0, part_rows = 0;
+    int worst = 0;
     for (int k = 0; k < n; ++k) {
       const int ps = paged_splits(c[k].most, chunk, INT_MAX);
       items += (double)c[k].count * ps;
-      tiles += c[k].total + (double)c[k].count * tree_tiles;
-      worst = std::max(worst, (double)ceil_div(c[k].most, ps) + tree_tiles);
+      worst = std::max(worst, ceil_div(c[k].most, ps));
       if (ps > 1) part_rows += (double)ps * rows[k];
     }
     items *= Hkv;
-    tiles *= Hkv;
-    const double item = (tiles + 1.5 * items) / items;  // an average item
+    const double item = tiles * Hkv / items + item_cost;  // an average one
     const double waves = items / PLAN_SMS;
-    double cost = std::max(worst + 1.5, item * (waves > 1 ? waves + 0.5 : 1.0));
-    if (part_rows > 0) cost += 4.0 + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / 3.6e6;
+    double cost = std::max(std::max(worst + tree_tiles + item_cost, item * (waves > 1 ? waves + 0.5 : 1.0)), memory);
+    if (part_rows > 0) cost += join_launch + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / tile_bytes;
     if (cost < best) {
       best = cost;
       best_chunk = chunk;
+    } else if (cost > 1.5 * best) {
+      break;
     }
     if (chunk == 1) break;
   }
   return best_chunk;
 }
 
-// Sequences [b0, b1) of a call: their entries (in the order the items are taken),
-// and what the launch needs.  rows_of(b), kv_of(b): tokens here, and in the cache.
-struct LaunchPlan {
-  PagedSeq seq[PAGED_MAX_SEQS];
-  int n_seqs, n_items, chunk_tiles, b_end;
-  long long part_rows;  // tokens' rows of partial results
-  bool ok;
-};
-
+// Sequences [b0, pl->b_end) of a call: their entries, in the order the items are taken.
 template <bool TREE>
-void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, int b0, LaunchPlan* pl) {
+void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, int b0, PagedPlan* pl) {
   Chains c[PAGED_MAX_SEQS];
   int rows[PAGED_MAX_SEQS], bs[PAGED_MAX_SEQS], order[PAGED_MAX_SEQS];
   int n = 0, b = b0;
@@ -1155,26 +1204,33 @@ void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* 
   pl->part_rows = part;
 }
 
+size_t plan_bytes(const PagedArgs& a, long long part_rows) {
+  return ATTN_SCHED_BYTES + (size_t)part_rows * a.Hq * (4 * a.D + 4);
+}
+
 template <bool TREE>
-size_t workspace_of(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host) {
-  long long most = 0;
-  for (int b = 0; b < a.B;) {
-    LaunchPlan pl;
+size_t workspace_of(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, PagedPlan* first) {
+  plan_launch<TREE>(a, cu_len_host, kv_host, 0, first);
+  if (!first->ok) return 0;
+  long long most = first->part_rows;
+  for (int b = first->b_end; b < a.B;) {
+    PagedPlan pl;
     plan_launch<TREE>(a, cu_len_host, kv_host, b, &pl);
     if (!pl.ok) return 0;
     most = std::max(most, pl.part_rows);
     b = pl.b_end;
   }
-  return ATTN_SCHED_BYTES + (size_t)most * a.Hq * (4 * a.D + 4);
+  return plan_bytes(a, most);
 }
 
 template <bool TREE>
-cudaError_t run(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace, cudaStream_t s) {
+cudaError_t run(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host, const PagedPlan& first, void* workspace,
+                cudaStream_t s) {
   a.sched = static_cast<unsigned*>(workspace);
+  PagedPlan later;
   for (int b = 0; b < a.B;) {
-    LaunchPlan pl;
-    plan_launch<TREE>(a, cu_len_host, kv_host, b, &pl);
-    if (!pl.ok) return cudaErrorInvalidValue;
+    if (b > 0) plan_launch<TREE>(a, cu_len_host, kv_host, b, &later);
+    const PagedPlan& pl = b > 0 ? later : first;
     b = pl.b_end;
     if (pl.n_items == 0) continue;
     a.chunk_tiles = pl.chunk_tiles;
@@ -1202,13 +1258,14 @@ cudaError_t attn_paged_prepare() {
   return e;
 }
 
-size_t attn_paged_workspace(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host) {
-  return cu_len_host ? workspace_of<false>(a, cu_len_host, kv_host) : workspace_of<true>(a, cu_len_host, kv_host);
+size_t attn_paged_workspace(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, PagedPlan* first) {
+  return cu_len_host ? workspace_of<false>(a, cu_len_host, kv_host, first) : workspace_of<true>(a, cu_len_host, kv_host, first);
 }
 
-cudaError_t launch_attn_paged(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace,
-                              cudaStream_t s) {
-  return cu_len_host ? run<false>(a, cu_len_host, kv_host, workspace, s) : run<true>(a, cu_len_host, kv_host, workspace, s);
+cudaError_t launch_attn_paged(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host,
+                              const PagedPlan& first, void* workspace, cudaStream_t s) {
+  return cu_len_host ? run<false>(a, cu_len_host, kv_host, first, workspace, s)
+                     : run<true>(a, cu_len_host, kv_host, first, workspace, s);
 }
 
 }  // namespace ts

@@ -80,10 +80,19 @@ __host__ __device__ inline int paged_split_start(int n, int ps, int s) {
   return ps == 1 ? (s ? n : 0) : (int)((unsigned)n * (unsigned)s / (unsigned)ps);
 }
 
+// A launch: sequences [.., b_end) of the call, at most PAGED_MAX_SEQS with rows.
+struct PagedPlan {
+  PagedSeq seq[PAGED_MAX_SEQS];
+  int n_seqs, n_items, chunk_tiles, b_end;
+  long long part_rows;  // tokens' rows of partial results
+  bool ok;              // its items and rows can be numbered
+};
+
 cudaError_t attn_paged_prepare();
-// cu_len_host NULL: a tree.  0 bytes: more than a launch can number.
-size_t attn_paged_workspace(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host);
-cudaError_t launch_attn_paged(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, void* workspace,
-                              cudaStream_t s);
+// Bytes a call needs (0: more than a launch can number), and its first launch's plan.
+// cu_len_host NULL: a tree.
+size_t attn_paged_workspace(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, PagedPlan* first);
+cudaError_t launch_attn_paged(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host,
+                              const PagedPlan& first, void* workspace, cudaStream_t s);
 
 }  // namespace ts
