@@ -703,7 +703,8 @@ TS_API ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream str
  * normaliser.  Logits, statistics and output sums are fp32; the softmax weights
  * are rounded to bf16 in the product with the values (half a step, 2^-8 of each at
  * most), and the parts of a chain of keys that is cut between SMs are joined in
- * fp32.  Calls repeat bit for bit.
+ * fp32.  Weights may reach 2^40 before the sums are scaled down, so the output of a
+ * channel with a value past 2^87 / kv_b may be infinite.  Calls repeat bit for bit.
  *
  *   q            [T, Hq, D] bf16; out the same, lse [T, Hq] fp32 or NULL.  Rows of
  *                no sequence are left as they were.
@@ -765,8 +766,9 @@ TS_API ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* worksp
  * position p = P_b + depth (depth: the ancestors in its mask) sees the prefix tokens
  * t with t > p - window or t < sinks, and of the nodes in its mask the ancestors a
  * with depth - depth_a < window or P_b + depth_a < sinks.  window >= 1.
- * Arguments, outputs and errors are tree_attn_fwd's, over the bf16 cache; a row that
- * sees no key gives zeros and an lse of -inf.  Blocks that no node sees into are not
+ * Arguments, outputs and errors are tree_attn_fwd's, over the bf16 cache, what is held
+ * in fewer bits tree_chunk_attn_fwd's; a row that sees no key gives zeros and an lse of
+ * -inf.  Blocks that no node sees into are not
  * followed.  The key of a node may hold anything for the rows it is hidden from; its
  * value must be finite.  In a captured call prefix_len may have changed when it is
  * replayed; one outside the table's row gets TS_ERR_SHAPE and nothing written.

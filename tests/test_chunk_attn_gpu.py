@@ -70,6 +70,28 @@ def test_hot_keys_and_a_scale():
     c.check(t, scale=0.05)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("levels", [
+    [0, 40, 80, 120, 160, 200, 240], [240, 200, 160, 120, 80, 40, 0], [0, 0, 30, 30, 60, 0, 250], [-250, 250, -250, 0, -100, 9, 12],
+    [5, 5, 5, 5, 5, 5, 5]])
+def test_references_that_rise(D, levels):
+    """Keys whose logits jump by tens to hundreds from tile to tile, whole numbers, so that logits are exact: the
+    references are raised, some rows' more than once, and what came before is scaled down."""
+    c = Chunk([70, 1], [7 * 128 - 70, 800], 4, 2, D, 16, seed=D)
+    g = np.random.default_rng(1)
+    one = np.uint16(0x3F80)
+    c.q[:] = one
+    for b in range(2):
+        for t in range(int(c.kv[b])):
+            for h in range(2):
+                v = np.float32(levels[t // 128] + int(g.integers(0, 4)) - (h * 3 if t % 5 else 0))
+                c.k[c.table[b, t // 16], h, t % 16] = np.uint16(v.view(np.uint32) >> 16)
+    t = c.tensors()
+    run(c, t, c.params(t, scale=1.0 / D))
+    assert t["status"].cpu().tolist() == [0, 0]
+    c.check(t, scale=1.0 / D)
+
+
 def test_repeats_bit_for_bit_and_without_lse_or_status():
     import tree_attention_speculative_gb300 as ts
     c = Chunk([200, 1, 31], [900, 5000, 0], 8, 2, 128, 16, seed=6)

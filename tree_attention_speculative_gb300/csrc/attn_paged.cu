@@ -18,16 +18,41 @@
 //
 // The kernel is persistent, one CTA an SM taking items from a counter, the
 // longest first, with one role a warp, as tree attention's:
-//   warp 0     takes the items (and hands them to the others through a queue in
-//              shared memory); TMA loads of the K tiles
-//   warp 3     TMA loads of the V tiles
-//   warp 1     S(j) = Q K(j)^T into S buffer j % 3, once PV(j-3) has freed it
-//   warp 2     O += P(j) V(j), P from TMEM
-//   warps 4-7  softmax, a row a thread: masks, running maximum and sum, P in bf16
-//              over S, O rescaled only when a row's maximum rises by more than 2^20
-//              (exact: the final division uses the same reference)
+//   warp 0      takes the items (and hands them to the others through a queue in
+//               shared memory); TMA loads of the K tiles
+//   warp 3      TMA loads of the V tiles
+//   warp 1      S(j) = Q K(j)^T, once PV has freed the S buffer
+//   warp 2      O += P(j) V(j), P from TMEM
+//   warps 4-11  softmax, two groups of 128 threads, each with an accumulator O, a
+//               reference and a sum of its own, so that neither waits for the other;
+//               at an item's end they are joined, and each group stores half of the
+//               channels.  Heads of 64: a group takes every other tile.  Heads of 128:
+//               half the keys of every tile, since two O leave room for two S
+//               buffers only and a tile's way through softmax, PV and the next QK has
+//               to be short.
+//
+// What bounds it.  Long chains of heads of 128: the tensor cores under the power cap
+// (4096 tokens over 16K, 32 heads: 607 us in bursts, 1.58 PFLOP/s, 0.84 of the
+// measured GEMM rate; 652 us back to back).  Heads of 64 have half the products for the
+// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 474 us with
+// blocks of 64, 1.09 PFLOP/s), with blocks of 16 the issue of 16 TMA boxes a tile (555-590).
+// Single tokens: memory (32 sequences of 0-8K: 81 us, 6.2 TB/s, 0.92 of the
+// measured copy).  An item costs about 3 us beyond its tiles: the start of its
+// pipeline, the last PV, the stores.  What carried it (64 heads of 128 and of 64 on
+// 64 trees of 64 nodes over 8K, us):
+//   one softmax group, 128 columns a thread                       848  823
+//   two groups                                                    958  700
+//   the issuers' loops run by whole warps on uniform values,
+//     descriptors by offset, one elected lane issuing             778  684
+//   each box issued by the lane that holds its place              788  620
+//   heads of 64: tiles in turn, no look at a tile's maximum                592
+// Tried and not kept: a barrier asked for a tile ahead (a poll that is not needed
+// delays the warp: 671 -> 698); one lane issuing all boxes (656 -> 724); the groups held
+// apart by half a period (580 -> 602); one P arrival a warp (no change); three-input
+// maxima (no change: the compiler's own).
+//
 // Masks cost nothing where a tile is wholly visible; elsewhere each row makes
-// a 128-bit word of its visible keys.  Keys that no row of the item sees may be
+// a word of its visible keys.  Keys that no row of the item sees may be
 // anything, so their V rows are zeroed in shared memory before PV reads them
 // (0 * NaN), and blocks that hold only such keys are not read at all: a
 // windowed layer may have given them away.
@@ -37,6 +62,7 @@
 // TS_ERR_TIMEOUT for the sequences of the items they had not finished.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "attn_paged.cuh"
 #include "fastexp.cuh"
@@ -554,9 +580,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       }
     }
   } else {
-    // Keys of a tile that a group takes, in parts of 64 (that many scores fit the
-    // registers): a tile's are read from TMEM for their maximum, and again for the
-    // weights (the read costs 35 cycles).
+    // Keys of a tile that a group takes, in parts of 64: that many scores fit the
+    // registers (and are read from TMEM again, 35 cycles, where they are wanted twice).
     constexpr int KEYS = C::TURNS ? KV_TILE : HALF, PARTS = KEYS / HALF, STEP = C::TURNS ? 2 : 1;
     const int half = (warp - SOFTMAX_WARP0) >> 2;  // the group, and its accumulator
     const int key_in = C::TURNS ? 0 : half * HALF;  // its first key of a tile
@@ -669,57 +694,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
               if (!((w >> e) & 1ull)) s[e] = NEG_INF;
           }
         };
-        float m_new = m_run, m_use = m_run, rowsum;
-        bool rescale = false;
-        if constexpr (C::TURNS) {
-          uint32_t pk[PARTS][HALF / 2];
-          bool look = fresh;
-          for (;;) {
-            if (look) {
-#pragma unroll 1
-              for (int h = 0; h < PARTS; ++h) {
-                load(h);
-                float mk[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mk[e] = s[e];
-#pragma unroll
-                for (int c = 4; c < HALF; c += 4)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
-                m_new = fmaxf(m_new, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
-              }
-              rescale = j > first && active && m_new > m_run + 10.f;
-              if (m_run == NEG_INF || rescale) m_use = m_new;
-            }
-            const float m_exp = m_use == NEG_INF ? 0.f : m_use;
-            const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
-            const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
-            uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-            for (int h = 0; h < PARTS; ++h) {
-              load(h);
-#pragma unroll
-              for (int e = 0; e < HALF / 2; ++e) {
-                float x0, x1;
-                fx::unpack2(fx::fma2(fx::pack2(s[2 * e], s[2 * e + 1]), scale2, negm2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
-                pk[h][e] = pack_bf16x2(p0, p1);
-              }
-            }
-            float r0, r1;
-            fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
-            rowsum = r0 + r1;
-            if (look || !__any_sync(0xffffffffu, active && !(rowsum <= SUM_LIMIT))) break;
-            look = true;
-          }
-          if (fresh) fresh = __any_sync(0xffffffffu, m_use == NEG_INF);
-#pragma unroll
-          for (int h = 0; h < PARTS; ++h) tmem_st32(s_tmem + h * HALF, pk[h]);
-        } else {
-#pragma unroll 1
-        for (int h = 0; h < PARTS; ++h) {
-          load(h);
+        const auto largest = [&]() {  // of s, in the exponent's units
           float mk[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) mk[e] = s[e];
@@ -727,18 +702,15 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           for (int c = 4; c < HALF; c += 4)
 #pragma unroll
             for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
-          m_new = fmaxf(m_new, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2);
-        }
-        rescale = j > first && active && m_new > m_run + RESCALE_THRESHOLD;
-        if (j == first || rescale) m_use = m_new;
-        const float m_exp = m_use == NEG_INF ? 0.f : m_use;  // nothing visible so far: every weight is 0
+          return fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2;
+        };
         const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
-        const uint64_t negm2 = fx::pack2(-m_exp, -m_exp);
-        uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll 1
-        for (int h = PARTS - 1; h >= 0; --h) {  // (the last part is still there)
-          if (h < PARTS - 1) load(h);
-          uint32_t pk[HALF / 2];
+        uint64_t negm2, sum2[2];
+        const auto against = [&](float m) {  // (-inf: nothing visible so far, every weight is 0)
+          negm2 = m == NEG_INF ? 0ull : fx::pack2(-m, -m);
+          sum2[0] = sum2[1] = 0ull;
+        };
+        const auto weigh = [&](uint32_t (&pk)[HALF / 2]) {  // s to bf16 weights, and their sums
 #pragma unroll
           for (int e = 0; e < HALF / 2; ++e) {
             float x0, x1;
@@ -747,14 +719,56 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
           }
-          tmem_st32(s_tmem + h * HALF, pk);
-        }
-        {
+        };
+        const auto total = [&]() {
           float r0, r1;
           fx::unpack2(fx::add2(sum2[0], sum2[1]), r0, r1);
-          rowsum = r0 + r1;
+          return r0 + r1;
+        };
+        float m_use = m_run, rowsum;
+        if constexpr (C::TURNS) {
+          // A row takes a new reference only by its own weights: where it has none
+          // yet, or its sum has passed the limit.  The warp then looks for maxima and
+          // takes the tile's weights once more.
+          uint32_t pk[PARTS][HALF / 2];
+          bool need = m_run == NEG_INF;
+          bool look = fresh;  // (some row of the warp may have none)
+          for (;;) {
+            if (look) {
+              float m_tile = NEG_INF;
+#pragma unroll 1
+              for (int h = 0; h < PARTS; ++h) {
+                load(h);
+                m_tile = fmaxf(m_tile, largest());
+              }
+              if (need) m_use = fmaxf(m_run, m_tile);
+            }
+            against(m_use);
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) {
+              load(h);
+              weigh(pk[h]);
+            }
+            rowsum = total();
+            const bool over = active && !need && !(rowsum <= SUM_LIMIT);
+            if (!__any_sync(0xffffffffu, over)) break;
+            need = need || over;
+            look = true;
+          }
+          if (fresh) fresh = __any_sync(0xffffffffu, m_use == NEG_INF);
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) tmem_st32(s_tmem + h * HALF, pk[h]);
+        } else {
+          load(0);
+          const float m_new = fmaxf(m_run, largest());
+          if (j == first || (active && m_new > m_run + RESCALE_THRESHOLD)) m_use = m_new;
+          against(m_use);
+          uint32_t pk[HALF / 2];
+          weigh(pk);
+          tmem_st32(s_tmem, pk);
+          rowsum = total();
         }
-        }
+        const bool rescale = j > first && active && m_use != m_run;
         if (dead) {
           // V rows that no row of the item sees hold whatever the pool, or the
           // ring, had there: zeroed, so that 0 * V is 0
@@ -783,7 +797,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             break;
           }
           tc_fence_after();
-          const float f = !rescale ? 1.f : m_run == NEG_INF ? 0.f : ex2(m_run - m_new);
+          const float f = !rescale ? 1.f : m_run == NEG_INF ? 0.f : ex2(m_run - m_use);
           l_run *= f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -1095,8 +1109,8 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
 // them longest first.  In units of a tile's time on an SM (0.8 us), an item costs its
 // tiles and 3 more (its start and its end), the launch ends when the SMs have shared all of that out
 // and the last items have run, and not before the keys and values have come from
-// memory.  Cut chains cost a second kernel and their partial results' round trip.
-// On the measured shapes the plans are within 5 % of the best of a sweep.
+// memory (which the last items, and the items' starts, do not keep busy).  Cut chains cost a second kernel and their partial results' round trip.
+// On the measured shapes the plans are within 8 % of the best of a sweep.
 struct Chains {
   int count;     // row tiles
   int most;      // tiles of the longest chain
@@ -1130,7 +1144,8 @@ int plan_chunk_tiles(const Chains* c, const int* rows, int n, int Hkv, int Hq, i
     items *= Hkv;
     const double item = tiles * Hkv / items + item_cost;  // an average one
     const double waves = items / PLAN_SMS;
-    double cost = std::max(std::max(worst + tree_tiles + item_cost, item * (waves > 1 ? waves + 0.5 : 1.0)), memory);
+    double cost = std::max(std::max(worst + tree_tiles + item_cost, item * (waves > 1 ? waves + 0.5 : 1.0)),
+                           memory + 0.25 * worst + 2.0 * std::ceil(waves));
     if (part_rows > 0) cost += join_launch + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / tile_bytes;
     if (cost < best) {
       best = cost;
