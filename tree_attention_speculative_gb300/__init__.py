@@ -477,6 +477,15 @@ def _is_codes(t: torch.Tensor, shape: tuple) -> bool:
     return (t.dtype is _F8 or t.dtype is _U8) and t.shape == shape and t.is_contiguous()
 
 
+def _stream_on(where: str, dev: int, stream) -> int:
+    """The stream's handle, for tensors that are all on device `dev` (-1: the CPU)."""
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _bad(where)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _launch_stream(where: str, stream, *tensors) -> int:
     """The stream's handle, once every tensor is on the current CUDA device."""
     dev = None
@@ -487,11 +496,7 @@ def _launch_stream(where: str, stream, *tensors) -> int:
                 if dev is not None or d < 0:
                     _bad(where)
                 dev = d
-    if dev != torch._C._cuda_getDevice():
-        _bad(where)
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return _stream_on(where, -1 if dev is None else dev, stream)
 
 
 def _opt(t: Optional[torch.Tensor]):
@@ -630,17 +635,18 @@ def tree_attn_fwd_q8_stall_test(params: AttnParams, kv_scale: torch.Tensor, work
 
 # ---------------------------------------------------------------- prompts, windowed layers, log probabilities
 
-def _token_strides(where: str, x: torch.Tensor, T: int, H: int, D: int):
-    """Strides (token, head) of bf16 x [T, H, D] with adjacent channels; 0, 0 when dense."""
-    if x.dtype is not _BF16 or x.shape != (T, H, D):
+def _token_strides(where: str, x: torch.Tensor, shape: tuple):
+    """Strides (token, head) of bf16 x [T, H, D] with adjacent channels."""
+    if x.dtype is not _BF16 or x.shape != shape:
         _bad(where)
-    if x.is_contiguous():
-        return 0, 0
-    st, sh, sd = x.stride()
-    head = D if H == 1 else sh
+    T, H, D = shape
+    token, head, channel = x.stride()
+    if H == 1:
+        head = D
     row = (H - 1) * head + D
-    token = row if T == 1 else st
-    if sd != 1 or head < D or token < row:  # (an expanded tensor repeats a token or a head)
+    if T <= 1:
+        token = row
+    if channel != 1 or head < D or token < row:  # (an expanded tensor repeats a token or a head)
         _bad(where)
     return token, head
 
@@ -665,31 +671,34 @@ def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
     new_prefix_len.  With ``kv_scale`` the cache is the 8-bit one.  q, k and v may
     be views of a fused projection; without ``rope`` (and q) k is stored as it is."""
     where = "tree_cache_append_rope"
-    T, Hkv, D = k.shape
+    shape = T, Hkv, D = k.shape
     B = prefix_len.shape[0]
     pool = k_cache.shape
     nblk, _, bs, _ = pool
     maxb = block_table.shape[1]
+    dev = k.get_device()
     Hq = qt = qh = 0
     if q is not None:
         Hq = q.shape[1]
-        qt, qh = _token_strides(where, q, T, Hq, D)
-        if q_out is None or not (q_out.dtype is _BF16 and q_out.shape == (T, Hq, D) and q_out.is_contiguous()):
+        qt, qh = _token_strides(where, q, (T, Hq, D))
+        if q_out is None or not (q_out.dtype is _BF16 and q_out.shape == (T, Hq, D) and q_out.is_contiguous()
+                                 and q.get_device() == dev == q_out.get_device()):
             _bad(where)
-    kt, kh = _token_strides(where, k, T, Hkv, D)
-    vt, vh = _token_strides(where, v, T, Hkv, D)
+    kt, kh = _token_strides(where, k, shape)
+    vt, vh = _token_strides(where, v, shape)
     if kv_scale is None:
         cache = (k_cache.dtype is _BF16 and k_cache.is_contiguous() and v_cache.dtype is _BF16
                  and v_cache.shape == pool and v_cache.is_contiguous())
     else:
         cache = (_is_codes(k_cache, pool) and _is_codes(v_cache, pool)
-                 and _is(kv_scale, _U8, (nblk, Hkv, bs, 2)))
+                 and _is(kv_scale, _U8, (nblk, Hkv, bs, 2)) and kv_scale.get_device() == dev)
     if not (cache and pool == (nblk, Hkv, bs, D) and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
             and _is(prefix_len, _I32, (B,)) and _is(new_prefix_len, _I32, (B,))
-            and (status is None or _is(status, _I32, (B,)))):
+            and (status is None or (_is(status, _I32, (B,)) and status.get_device() == dev))
+            and v.get_device() == dev == k_cache.get_device() and v_cache.get_device() == dev == cu_len.get_device()
+            and prefix_len.get_device() == dev == block_table.get_device() and new_prefix_len.get_device() == dev):
         _bad(where)
-    handle = _launch_stream(where, stream, q, k, v, cu_len, prefix_len, q_out if q is not None else None, k_cache,
-                            v_cache, kv_scale, block_table, new_prefix_len, status)
+    handle = _stream_on(where, dev, stream)
     block = _APPEND.pack(
         0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if q is None else q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), 0 if kv_scale is None else kv_scale.data_ptr(), cu_len.data_ptr(),
@@ -738,7 +747,7 @@ def tree_chunk_attn_workspace_size(params: ChunkParams) -> int:
 def _chunk_stream(where: str, params: ChunkParams, workspace, stream) -> int:
     if not workspace.is_contiguous() or params.device != workspace.get_device():
         _bad(where)
-    return _launch_stream(where, stream, workspace)
+    return _stream_on(where, params.device, stream)
 
 
 def tree_chunk_attn_fwd(params: ChunkParams, workspace: torch.Tensor, stream=None) -> None:
@@ -772,15 +781,19 @@ def tree_attn_fwd_window(params: AttnParams, window: int, sinks: int, workspace:
     q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, anc_mask, out, lse, status = params.tensors
     rows, pool = q.shape, k_cache.shape
     B, N, Hq, D = rows
-    tree, masks = (B, N, pool[1], D), anc_mask.dtype
+    tree, masks, dev = (B, N, pool[1], D), anc_mask.dtype, q.get_device()
     if not (q.dtype is _BF16 and q.is_contiguous() and _is(out, _BF16, rows) and k_cache.dtype is _BF16
             and k_cache.is_contiguous() and pool[3] == D and _is(v_cache, _BF16, pool) and _is(k_tree, _BF16, tree)
             and _is(v_tree, _BF16, tree) and _is(block_table, _I32, (B, params.max_blocks)) and _is(prefix_len, _I32, (B,))
             and (masks is torch.int64 or masks is torch.uint64) and _is(anc_mask, masks, (B, N, (N + 63) // 64))
-            and params._keep[0].shape == (B,) and (lse is None or _is(lse, torch.float32, (B, N, Hq)))
-            and (status is None or _is(status, _I32, (B,))) and workspace.is_contiguous()):
+            and params._keep[0].shape == (B,) and workspace.is_contiguous()
+            and (lse is None or (_is(lse, torch.float32, (B, N, Hq)) and lse.get_device() == dev))
+            and (status is None or (_is(status, _I32, (B,)) and status.get_device() == dev))
+            and out.get_device() == dev == k_cache.get_device() and v_cache.get_device() == dev == k_tree.get_device()
+            and v_tree.get_device() == dev == block_table.get_device() and prefix_len.get_device() == dev
+            and anc_mask.get_device() == dev == workspace.get_device()):
         _bad(where)
-    handle = _launch_stream(where, stream, workspace, *params.tensors)
+    handle = _stream_on(where, dev, stream)
     _check(lib().tree_attn_fwd_window(ctypes.byref(params), window, sinks, workspace.data_ptr(),
                                       workspace.numel() * workspace.element_size(), handle), where)
 
