@@ -8,13 +8,14 @@
 // joined over the CTA and over the row's cluster.  All terms of U have one sign.
 // A value of -inf, or so low that 2^y is 0 in fp32, adds nothing to either.
 //
-// The alternatives.  A thread also remembers the largest of its values and which
-// 16-byte vector holds it.  At the row's end the CTA finds the `top` threads whose
-// largest are best (by value, then by the lower index): the row's best `top` values
-// are all in those threads' columns, since every value elsewhere is behind `top`
-// better ones.  Only those columns (4 to 6 % of the row) are read again, from L2
-// mostly, and what reaches the last of those largest is ranked.  So the pass over
-// the row has no exchange between threads and no list to keep.
+// The alternatives.  A thread also remembers the largest of its values, which
+// 16-byte vector holds it, and the largest of its other vectors.  At the row's end the
+// CTA finds the `top` threads whose largest are best (by value, then by the lower
+// index): the row's best `top` values are all in those threads' columns, since every
+// value elsewhere is behind `top` better ones.  Such a thread reads its vector again;
+// where another of its vectors reaches the last of those largest too, which is rare,
+// a warp reads its whole column.  What reaches it is ranked.  So the pass over the row
+// has no exchange between threads and no list to keep.
 //
 // Memory-bound: a row is read once.  A cluster of 1 to 8 CTAs takes a row, more
 // where there are few; CTA 0 joins the CTAs' results over distributed shared
@@ -137,7 +138,7 @@ struct Shared {
   Stats warp[LP_WARPS];
   Stats all;                                   // the CTA's
   unsigned long long best[LOGPROB_MAX_TOP];    // its alternatives, best first; 0: none
-  int column[LOGPROB_MAX_TOP];
+  int column[LOGPROB_MAX_TOP];                 // the columns read again
   int n_columns, n_found;
   uint32_t low[LP_WARPS], high[LP_WARPS];      // of the threads' largest
   float token;                                 // the given token's logit
@@ -178,7 +179,7 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
 
   // One pass: batches of LP_UN vectors.
   Stats st{-INFINITY, 0.f, 0.f};
-  float best_v = -INFINITY;
+  float best_v = -INFINITY, next_v = -INFINITY;  // the largest, and that of the other vectors
   int best_j = -1;
   // the next batch's loads are in flight while one is at work
   const auto whole = [&](int j) {
@@ -224,8 +225,11 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
 #pragma unroll
       for (int e = 1; e < N; ++e) vm = fmaxf(vm, v[u][e]);
       if (vm > best_v) {
+        next_v = best_v;
         best_v = vm;
         best_j = j + u * LP_THREADS;
+      } else {
+        next_v = fmaxf(next_v, vm);
       }
       top = fmaxf(top, vm);
     }
@@ -324,31 +328,28 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
       }
       in = in && (mine > least || (uint32_t)best_j <= limit);
     }
-    if (in) sh.column[atomicAdd(&sh.n_columns, 1)] = tid;
+    const auto key_of = [&](float v, int i) {  // i: its index in the row
+      const uint32_t o = ordered(v);
+      return o >= least ? ((unsigned long long)o << 32) | (0xffffffffu - (uint32_t)i) : 0ull;
+    };
+    if (in && ordered(next_v) < least) {
+      float v[N];
+      row.get(best_j, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const unsigned long long key = key_of(v[e], best_j * N - row.lead + e);
+        if (key) sh.found[atomicAdd(&sh.n_found, 1)] = key;
+      }
+    } else if (in) {
+      sh.column[atomicAdd(&sh.n_columns, 1)] = tid;
+    }
     __syncthreads();
     const int columns = min(sh.n_columns, top);
-    constexpr int PARTS = LP_COLUMN / 32, MINE = LOGPROB_MAX_TOP / LP_WARPS;
-    uint4 w[MINE][PARTS];  // all of the warp's vectors on their way at once
-    const auto place = [&](int c, int h) { return j0 + sh.column[c] + (lane + 32 * h) * LP_THREADS; };
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-      const int c = warp + i * LP_WARPS;
-#pragma unroll
-      for (int h = 0; h < PARTS; ++h) {
-        w[i][h] = make_uint4(0, 0, 0, 0);
-        if (c < columns && place(c, h) < j1 && row.whole(place(c, h))) w[i][h] = row.raw(place(c, h));
-      }
-    }
-#pragma unroll
-    for (int ih = 0; ih < MINE * PARTS; ++ih) {
-      const int i = ih / PARTS, h = ih % PARTS, c = warp + i * LP_WARPS;
-      if (c >= columns) continue;
-      const int j = place(c, h);
+    for (int ch = warp; ch < columns * (LP_COLUMN / 32); ch += LP_WARPS) {
+      const int j = j0 + sh.column[ch / (LP_COLUMN / 32)] + (lane + ch % (LP_COLUMN / 32) * 32) * LP_THREADS;
       float v[N];
-      if (j < j1 && row.whole(j)) {
-        Vec<T>::unpack(w[i][h], v);
-      } else if (j < j1) {
-        row.part(j, v);
+      if (j < j1) {
+        row.get(j, v);
       } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = -INFINITY;
@@ -357,10 +358,8 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
       int n = 0;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const uint32_t o = ordered(v[e]);
-        const bool keep = o >= least;
-        key[e] = keep ? ((unsigned long long)o << 32) | (0xffffffffu - (uint32_t)(j * N - row.lead + e)) : 0ull;
-        n += keep;
+        key[e] = key_of(v[e], j * N - row.lead + e);
+        n += key[e] != 0ull;
       }
       const int all = __reduce_add_sync(0xffffffffu, n);
       if (all <= top) {
