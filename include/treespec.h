@@ -763,13 +763,12 @@ TS_API ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* worksp
 
 /*
  * tree_attn_fwd_window — tree_attn_fwd for a layer with a sliding window: node i at
- * position p = P_b + depth (depth: the ancestors in its mask) sees the prefix tokens
+ * position p = P_b + depth (depth: the ancestors in its mask; 0 if that is empty) sees the prefix tokens
  * t with t > p - window or t < sinks, and of the nodes in its mask the ancestors a
  * with depth - depth_a < window or P_b + depth_a < sinks.  window >= 1.
  * Arguments, outputs and errors are tree_attn_fwd's, over the bf16 cache, what is held
  * in fewer bits tree_chunk_attn_fwd's; a row that sees no key gives zeros and an lse of
- * -inf.  Blocks that no node sees into are not
- * followed.  The key of a node may hold anything for the rows it is hidden from; its
+ * -inf.  Blocks that no node sees into are not followed.  The key of a node may hold anything for the rows it is hidden from; its
  * value must be finite.  In a captured call prefix_len may have changed when it is
  * replayed; one outside the table's row gets TS_ERR_SHAPE and nothing written.
  * workspace: tree_attn_window_workspace_size bytes, as tree_chunk_attn_fwd's, and may
@@ -804,9 +803,9 @@ TS_API ts_status tree_attn_fwd_window(const ts_attn_params* p, int window, int s
  * A row of nothing but -inf gives logprob -inf, entropy 0 and no alternatives.
  * fp32 arithmetic: a log probability or entropy is within 2^-15 plus 2^-22 of its
  * magnitude (2^-21 is usual).  Calls repeat bit for bit.
- * R may be 0 (the pointers may then be NULL).  No workspace.  Returns TS_ERR_NULL / TS_ERR_SHAPE (temperature not
- * positive and finite, R over M without rows) / TS_ERR_UNSUPPORTED (V over 524224,
- * top over 32, R over 2^28) / TS_ERR_CUDA.
+ * R may be 0 (the pointers may then be NULL).  No workspace.  Returns TS_ERR_NULL /
+ * TS_ERR_SHAPE (temperature not positive and finite, R over M without rows) /
+ * TS_ERR_UNSUPPORTED (V over 524224, top over 32, R over 2^28) / TS_ERR_CUDA.
  */
 typedef struct ts_logprob_params {
   const void* logits;

@@ -121,3 +121,64 @@ def test_forests_and_a_bad_prefix():
     torch.cuda.synchronize()
     assert step.status.cpu().tolist() == [0, -2]
     assert (f64(step.out)[1] == 7).all()
+
+
+def test_an_empty_mask_row_is_a_node_at_depth_0():
+    """It sees what the root sees of the prefix, and no node; the pool is NaN at what the root does not see."""
+    window, sinks, P = 20, 3, 300
+    c, _ = build(6, "chain", [P, 7], 4, 2, 128, 16, window, sinks, seed=9)
+    t = to_dev(c)
+    from tree_attention_speculative_gb300.step import TreeVerifyStep
+    step = TreeVerifyStep(c.B, c.N, c.Hq, c.Hkv, c.D, c.prefix_len, window=window, sinks=sinks)
+    step.ancestry(t["parent"], t["prefix_len"])
+    step.anc[:, 2] = 0
+    step.attention(t["q"], t["k_cache"], t["v_cache"], t["block_table"], t["prefix_len"], t["k_tree"], t["v_tree"])
+    torch.cuda.synchronize()
+    at = live_keys(P, 1, window, sinks)
+    at = at[at < P]
+    bits = oracle.attention.bf16_to_f64
+    for h in range(c.Hq):
+        keys, vals = (bits(x[c.block_table[0, at // 16], h // 2, at % 16]) for x in (c.k_cache, c.v_cache))
+        seen = np.ones((1, len(at)), bool)
+        out, lse = oracle.window.attend(bits(c.q[0, 2, h])[None], keys, vals, seen, 128 ** -0.5)
+        mag, _ = oracle.window.attend(bits(c.q[0, 2, h])[None], keys, np.abs(vals), seen, 128 ** -0.5)
+        assert_rows(f64(step.out)[0, 2, h][None], f64(step.lse)[0, 2, h][None], out, lse, mag)
+    assert np.isfinite(f64(step.out)).all()
+
+
+def test_a_captured_call_follows_the_prefix():
+    import tree_attention_speculative_gb300 as ts
+    window, sinks = 40, 5
+    start, end = [200, 0, 30], [391, 64, 1000]
+    c, _ = build(9, "random", end, 4, 1, 128, 16, 1 << 20, 0, seed=11)  # (all of the pool is there)
+    t = to_dev(c)
+    out = torch.zeros((c.B, c.N, c.Hq, c.D), dtype=torch.bfloat16, device="cuda")
+    lse, status = torch.zeros((c.B, c.N, c.Hq), device="cuda"), torch.zeros(c.B, dtype=torch.int32, device="cuda")
+    from tree_attention_speculative_gb300.step import TreeVerifyStep
+    step = TreeVerifyStep(c.B, c.N, c.Hq, c.Hkv, c.D, end, window=window, sinks=sinks)
+    step.ancestry(t["parent"], t["prefix_len"])
+    p = ts.attn_params(t["q"], t["k_cache"], t["v_cache"], t["block_table"], t["prefix_len"], np.array(start, np.int32),
+                       t["k_tree"], t["v_tree"], step.anc, None, out, lse, status)
+    ws = torch.zeros(ts.tree_attn_window_workspace_size(p, window, sinks), dtype=torch.uint8, device="cuda")
+    ts.tree_attn_fwd_window(p, window, sinks, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ts.tree_attn_fwd_window(p, window, sinks, ws)
+    for P in (start, end):
+        t["prefix_len"].copy_(torch.tensor(P, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        a = (c.q, c.k_cache, c.v_cache, c.block_table, np.array(P, np.int32), c.k_tree)
+        ref = oracle.window.tree_attention(*a, c.v_tree, c.parent, window, sinks)
+        mag, _ = oracle.window.tree_attention(a[0], a[1], a[2] & 0x7FFF, *a[3:], c.v_tree & 0x7FFF, c.parent, window, sinks)
+        assert status.cpu().tolist() == [0] * 3
+        assert_rows(f64(out), f64(lse), *ref, mag)
+
+
+def test_more_sequences_than_a_launch_takes():
+    prefix = [(b * 53) % 150 for b in range(260)]
+    c, ref = build(3, "random", prefix, 2, 1, 64, 16, 12, 2, seed=13)
+    step = run(c, 12, 2)
+    assert step.status.cpu().tolist() == [0] * c.B
+    assert_rows(f64(step.out), f64(step.lse), *ref)

@@ -775,8 +775,8 @@ ts_status check_chunk(const ts_chunk_params* p) {
   if (p->window > MAX_POSITION || p->sinks > MAX_POSITION) return TS_ERR_UNSUPPORTED;
   if (p->cu_len_host[0] < 0 || p->cu_len_host[p->B] > p->T) return TS_ERR_SHAPE;
   for (int b = 0; b < p->B; ++b) {
-    const int len = p->cu_len_host[b + 1] - p->cu_len_host[b], kv = p->kv_len_host[b];
-    if (p->cu_len_host[b + 1] < p->cu_len_host[b] || kv < len) return TS_ERR_SHAPE;
+    const int lo = p->cu_len_host[b], hi = p->cu_len_host[b + 1], kv = p->kv_len_host[b];
+    if (lo < 0 || hi < lo || kv < hi - lo) return TS_ERR_SHAPE;
     if (kv > MAX_POSITION) return TS_ERR_UNSUPPORTED;
     if ((long long)p->max_blocks * p->block_size < kv) return TS_ERR_SHAPE;
   }

@@ -608,7 +608,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
 #pragma unroll
           for (int w = 0; w < 4; ++w)
             if (w < a.W) w4[w] = arow[w];
-          depth = __popcll(w4[0]) + __popcll(w4[1]) + __popcll(w4[2]) + __popcll(w4[3]) - 1;
+          depth = max(__popcll(w4[0]) + __popcll(w4[1]) + __popcll(w4[2]) + __popcll(w4[3]) - 1, 0);  // (an empty mask: 0)
         }
         lo = P + depth - a.window + 1;
         hi = hi_least = P;
