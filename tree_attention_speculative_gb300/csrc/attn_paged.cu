@@ -74,7 +74,7 @@ namespace {
 
 constexpr int NUM_THREADS = 384;
 constexpr int GROUP_THREADS = 128;  // a softmax group: a row a thread
-constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4;
+constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4, SOFTMAX_WARPS = 8;
 constexpr int HALF = KV_TILE / 2;  // keys of a tile that one softmax group takes
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int ITEM_Q = 8;    // entries of the item queue
@@ -115,7 +115,8 @@ struct __align__(1024) Smem {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  // the CTA's items in the order taken; pub published, done stored
+  // the CTA's items in the order taken; pub published, done by how many softmax warps
+  // they were stored (no warp is more than one item ahead of another)
   int4 item_q[ITEM_Q][4];
   int items_pub, items_done;
   // an item's end: group 1's (m, l) of each row, then from group 0 the factors of
@@ -366,7 +367,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           }
         }
         bool ok = k < ITEM_Q;  // the entry's last user must be done
-        if (!ok && lane == 0) ok = wait_count(&sm.items_done, k - ITEM_Q + 1, ctl);
+        if (!ok && lane == 0) ok = wait_count(&sm.items_done, SOFTMAX_WARPS * (k - ITEM_Q + 1), ctl);
         if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
         if (lane == 0) {
           int4* q = sm.item_q[k % ITEM_Q];
@@ -897,7 +898,10 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       tc_fence_before();
       mbar_arrive(&sm.o_free);
       __syncwarp();
-      if (half == 0 && r == 0) publish(&sm.items_done, k + 1);
+      if (lane == 0) {
+        __threadfence_block();
+        atomicAdd(&sm.items_done, 1);
+      }
       I = next;
     }
   }
@@ -926,7 +930,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         const Lens l = load_lens<TREE>(b, args.seq[p.e].rows, a);
         if (make_item<TREE>(p, b, l.q0, l.len, l.kv, args).n_tiles) a.status[b] = TS_ERR_TIMEOUT;
       };
-      const int done = sm.items_done;
+      const int done = sm.items_done / SOFTMAX_WARPS;  // wholly
       if (single) {
         if (done == 0) report(blockIdx.x);
       } else {
