@@ -800,7 +800,7 @@ void fill_paged(PagedArgs* a, const void* q, const void* k, const void* v, const
   a->window = window;
   // (sinks past every position change nothing and would overflow a sum)
   a->sinks = std::min(sinks, MAX_POSITION);
-  a->tok = ROW_TILE / a->G;
+  a->tok = a->tok_tile = ROW_TILE / a->G;
   a->wait_limit_ns = ATTN_WAIT_LIMIT_NS;
   a->stall_seq = -1;
 }

@@ -85,25 +85,27 @@ constexpr float RESCALE_THRESHOLD = 40.0f;
 constexpr float SUM_LIMIT = 1099511627776.f;  // 2^40
 constexpr float NEG_INF = -INFINITY;
 
-template <int D>
+template <int D, bool PAIR>
 struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE_BYTES = KV_TILE * D * 2;
   static constexpr int HALF_BYTES = KV_TILE * 128;
-  static constexpr int Q_BYTES = ROW_TILE * D * 2;
-  static constexpr int NST = D == 128 ? 3 : 6;  // tiles in each ring, K and V
-  // The two softmax groups: on heads of 64 they take the tiles in turn, on heads of
-  // 128 half the keys of every tile each.
-  static constexpr bool TURNS = D == 64;
+  static constexpr int Q_BYTES = ROW_TILE * D * 2;  // of a row tile
+  static constexpr int SETS = PAIR ? 2 : 1;         // row tiles an item
+  static constexpr int NST = D == 128 ? 3 : PAIR ? 5 : 6;  // tiles in each ring, K and V
+  static_assert(D == 64 || !PAIR, "");
+  // The two softmax groups: a row tile each of a pair; else on heads of 64 the key
+  // tiles in turn, on heads of 128 half the keys of every tile each.
+  static constexpr bool TURNS = PAIR || D == 64;
   // TMEM: the groups' accumulators at 0 and D, then the S buffers
   static constexpr uint32_t TMEM_S0 = 2 * D;
   static constexpr int NSB = (TMEM_COLS - TMEM_S0) / KV_TILE;  // 2 for heads of 128, 3 for 64
 };
 
-template <int D>
+template <int D, bool PAIR>
 struct __align__(1024) Smem {
-  using C = Cfg<D>;
-  uint8_t q[C::Q_BYTES];
+  using C = Cfg<D, PAIR>;
+  uint8_t q[C::SETS * C::Q_BYTES];
   uint8_t k[C::NST][C::TILE_BYTES];
   uint8_t v[C::NST][C::TILE_BYTES];
   uint64_t q_full, q_empty;
@@ -236,16 +238,16 @@ __device__ __forceinline__ void st_v8(void* p, const uint32_t* w) {
                : "memory");
 }
 
-template <int D, bool TREE>
+template <int D, bool TREE, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtensorMap tm_q,
              const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
              const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt) {
-  using C = Cfg<D>;
+  using C = Cfg<D, PAIR>;
   constexpr int NSB = C::NSB;
   constexpr uint32_t TMEM_S0 = C::TMEM_S0;
   extern __shared__ uint8_t smem_raw[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem<D, PAIR>& sm = *reinterpret_cast<Smem<D, PAIR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const PagedArgs& a = args.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool leader = elect_one();  // one lane of the warp
@@ -466,7 +468,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
     // cached tiles: [8-row group][64-column half]; tree tiles: [half][rows]
     const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, C::HALVES * 1024);
     const uint64_t kt_desc = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
-    int jg = 0, slot = 0, k_phase = 0, buf = 0, s_phase = 1;  // (the first NSB waits for s_free pass)
+    int slot = 0, k_phase = 0, buf = 0, s_phase = 1;  // (the first NSB waits for s_free pass)
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item I;
@@ -476,38 +478,42 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       // this item's Q tile, once every QK of the last one has completed
       if (k > 0 && !__all_sync(0xffffffffu, wait_bar(&sm.q_empty, (k - 1) & 1, ctl))) break;
       if (leader) {
-        mbar_arrive_expect_tx(&sm.q_full, C::Q_BYTES);
-        for (int h = 0; h < C::HALVES; ++h)
-          tma_load_3d(sm.q + h * (ROW_TILE * 128), &tm_q, &sm.q_full, 64 * h, I.g * a.G, I.q0 + I.i0);
+        mbar_arrive_expect_tx(&sm.q_full, C::SETS * C::Q_BYTES);
+        for (int x = 0; x < C::SETS; ++x)
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(sm.q + x * C::Q_BYTES + h * (ROW_TILE * 128), &tm_q, &sm.q_full, 64 * h, I.g * a.G,
+                        I.q0 + I.i0 + x * a.tok_tile);
       }
       __syncwarp();
       ++q_issued;
       if (!__all_sync(0xffffffffu, wait_bar(&sm.q_full, k & 1, ctl))) break;
       ++q_landed;
-      for (int j = 0; j < n_tiles; ++j, ++jg) {
-        ok = __all_sync(0xffffffffu, wait_bar(&sm.k_full[slot], k_phase, ctl) && wait_bar(&sm.s_free[buf], s_phase, ctl));
+      for (int v = 0; v < C::SETS * n_tiles; ++v) {
+        const int j = v / C::SETS, x = v % C::SETS;
+        ok = __all_sync(0xffffffffu, (x > 0 || wait_bar(&sm.k_full[slot], k_phase, ctl)) && wait_bar(&sm.s_free[buf], s_phase, ctl));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + TMEM_S0 + buf * KV_TILE;
+        const uint64_t qd = q_desc + x * (C::Q_BYTES >> 4);
         if (leader) {
           if (!TREE || j < n_prefix) {
             const uint64_t kd = k_desc + slot * (C::TILE_BYTES >> 4);
 #pragma unroll
             for (int k2 = 0; k2 < D / 16; ++k2)
-              mma_ss(d_tmem, q_desc + (((k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32) >> 4),
+              mma_ss(d_tmem, qd + (((k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32) >> 4),
                      kd + (((k2 >> 2) * 1024 + (k2 & 3) * 32) >> 4), ID_QK, k2 > 0);
           } else {
             const uint64_t kd = kt_desc + slot * (C::TILE_BYTES >> 4);
 #pragma unroll
             for (int k2 = 0; k2 < D / 16; ++k2)
-              mma_ss(d_tmem, q_desc + (((k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32) >> 4),
+              mma_ss(d_tmem, qd + (((k2 >> 2) * (ROW_TILE * 128) + (k2 & 3) * 32) >> 4),
                      kd + (((k2 >> 2) * C::HALF_BYTES + (k2 & 3) * 32) >> 4), ID_QK, k2 > 0);
           }
           mma_commit(&sm.s_full[buf]);
-          mma_commit(&sm.k_empty[slot]);
+          if (x == C::SETS - 1) mma_commit(&sm.k_empty[slot]);
         }
         __syncwarp();
-        if (++slot == C::NST) {
+        if (x == C::SETS - 1 && ++slot == C::NST) {
           slot = 0;
           k_phase ^= 1;
         }
@@ -523,7 +529,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
     constexpr uint32_t ID_PV = idesc_bf16_f32(ROW_TILE, D, 0, 1);
     const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), 1024, C::HALVES * 1024);
     const uint64_t vt_desc = smem_desc_sw128(smem_u32(sm.v[0]), C::HALF_BYTES, 1024);
-    int jg = 0, slot = 0, v_phase = 0, buf = 0, p_phase = 0;
+    int slot = 0, v_phase = 0, buf = 0, p_phase = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item I;
@@ -531,12 +537,14 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       const int n_tiles = __shfl_sync(0xffffffffu, I.n_tiles, 0), n_prefix = __shfl_sync(0xffffffffu, I.n_prefix, 0);
       if (n_tiles == 0) break;
       if (k > 0 && !__all_sync(0xffffffffu, wait_bar(&sm.o_free, (k - 1) & 1, ctl))) break;
-      for (int j = 0; j < n_tiles; ++j, ++jg) {
+      for (int v = 0; v < C::SETS * n_tiles; ++v) {
+        const int j = v / C::SETS;
+        const bool last = v % C::SETS == C::SETS - 1;  // of the tile's uses
         const uint32_t p_tmem = tmem + TMEM_S0 + buf * KV_TILE;
         const bool tree = TREE && j >= n_prefix;
         const uint64_t vd = (tree ? vt_desc : v_desc) + slot * (C::TILE_BYTES >> 4);
-        const int acc = C::TURNS ? (j & 1) * D : 0;  // (halves: the second half's is D)
-        const bool fresh = j < (C::TURNS ? 2 : 1);
+        const int acc = C::TURNS ? (v & 1) * D : 0;  // (halves: the second half's is D)
+        const bool fresh = v < (C::TURNS ? 2 : 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!C::TURNS || half == 0) {
@@ -566,11 +574,11 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         if (!ok) break;
         if (leader) {
           mma_commit(&sm.s_free[buf]);
-          if (j == n_tiles - 1) mma_commit(&sm.o_last);
-          mma_commit(&sm.v_empty[slot]);
+          if (v == C::SETS * n_tiles - 1) mma_commit(&sm.o_last);
+          if (last) mma_commit(&sm.v_empty[slot]);
         }
         __syncwarp();
-        if (++slot == C::NST) {
+        if (last && ++slot == C::NST) {
           slot = 0;
           v_phase ^= 1;
         }
@@ -591,12 +599,13 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
     const uint32_t o_tmem = tmem + lane_base + half * D;
     const int i_in = args.fd_g.div(r);  // token of the tile, and head of the group
     const int h_in = r - i_in * a.G;
-    int jg = 0;
+    const int set_in = PAIR ? half * a.tok_tile : 0;  // its first token of the item
+    int jg = 0;  // S buffers filled, over every item
     Item I;
     bool ok = __all_sync(0xffffffffu, queue_item(0, I));
     for (int k = 0; ok && I.n_tiles; ++k) {
-      const bool active = I.i0 + i_in < I.len;
-      const int i = active ? I.i0 + i_in : I.len - 1;
+      const bool active = I.i0 + set_in + i_in < I.len;
+      const int i = active ? I.i0 + set_in + i_in : I.len - 1;
       // the cached keys the row sees: t < hi, and t >= lo or t < sinks
       int lo, hi, hi_least, lo_most;
       uint64_t anc[2][PARTS] = {};  // the group's keys of the two tree tiles
@@ -640,11 +649,11 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         const int pos = I.pos0 + (i - I.i0);
         lo = pos - a.window + 1;
         hi = pos + 1;
-        hi_least = I.pos0 + 1;
-        lo_most = I.hi - a.window;
+        hi_least = I.pos0 + set_in + 1;
+        lo_most = min(I.pos0 + set_in + a.tok_tile, I.hi) - a.window;
       }
       if (a.window == 0) lo = lo_most = 0;
-      // Tiles j in [clear0, clear1) are wholly visible to every row: those before
+      // Tiles j in [clear0, clear1) are wholly visible to the group's rows: those before
       // hold sinks, or keys that a later row's window is past; those after, keys
       // past an earlier row.
       int clear0 = 0;
@@ -653,8 +662,9 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       float m_run = NEG_INF, l_run = 0.f;
       const int first = C::TURNS ? half : 0;
       bool fresh = true;
-      for (int j = first; j < I.n_tiles; j += STEP) {
-        const int jt = jg + j, buf = jt % NSB;
+      const int n_uses = C::SETS * I.n_tiles;
+      for (int use = first; use < n_uses; use += STEP) {
+        const int j = use / C::SETS, jt = jg + use, buf = jt % NSB;
         if (!__all_sync(0xffffffffu, wait_bar(&sm.s_full[buf], (jt / NSB) & 1, ctl))) {
           ok = false;
           break;
@@ -762,19 +772,19 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         } else {
           load(0);
           const float m_new = fmaxf(m_run, largest());
-          if (j == first || (active && m_new > m_run + RESCALE_THRESHOLD)) m_use = m_new;
+          if (use == first || (active && m_new > m_run + RESCALE_THRESHOLD)) m_use = m_new;
           against(m_use);
           uint32_t pk[HALF / 2];
           weigh(pk);
           tmem_st32(s_tmem, pk);
           rowsum = total();
         }
-        const bool rescale = j > first && active && m_use != m_run;
-        if (dead) {
-          // V rows that no row of the item sees hold whatever the pool, or the
+        const bool rescale = use > first && active && m_use != m_run;
+        if (dead && !(PAIR && half)) {
+          // (of a pair the first group, whose PV is the first to read the tile)  V rows that no row of the item sees hold whatever the pool, or the
           // ring, had there: zeroed, so that 0 * V is 0
-          const int slot = jt % C::NST;
-          if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (jt / C::NST) & 1, ctl))) {
+          const int vt = jt / C::SETS, slot = vt % C::NST;
+          if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (vt / C::NST) & 1, ctl))) {
             ok = false;
             break;
           }
@@ -787,7 +797,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           }
           fence_proxy_async();
         }
-        if (j > first && __any_sync(0xffffffffu, rescale)) {
+        if (use > first && __any_sync(0xffffffffu, rescale)) {
           // The accumulator's last PV complete (its S buffer is free again; the one
           // before that was when the buffer was filled, and the one after waits for
           // these weights, so the phase is no other's).  The whole warp takes part, by
@@ -817,11 +827,11 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         tc_fence_before();
         mbar_arrive(&sm.p_full[buf][C::TURNS ? 0 : half]);
       }
-      jg += I.n_tiles;
+      jg += n_uses;
       if (!ok) break;
-      // the item's end: its last PV, then the groups' halves joined.  Each group
-      // stores half of the channels, of both accumulators.
-      if (half == 1) {
+      // the item's end: its last PV, then the groups' halves joined, and each stores half
+      // of the channels, of both accumulators; of a pair each stores its own row tile.
+      if (!PAIR && half == 1) {
         sm.ml[r] = make_float2(m_run, l_run);
         mbar_arrive(&sm.ml_full);
       }
@@ -829,7 +839,10 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       ok = __all_sync(0xffffffffu, queue_item(k + 1, next));
       if (!ok) break;
       float f0 = 0.f, f1 = 0.f, lse2 = NEG_INF;
-      if (half == 0) {
+      if (PAIR) {
+        if (l_run > 0.f) lse2 = m_run + __log2f(l_run);
+        f0 = l_run > 0.f ? 1.f / l_run : 0.f;  // a row that sees no key: zeros
+      } else if (half == 0) {
         ok = __all_sync(0xffffffffu, wait_bar(&sm.ml_full, k & 1, ctl));
         if (!ok) break;
         const float2 other = sm.ml[r];
@@ -857,21 +870,31 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       if (!ok) break;
       tc_fence_after();
       const uint64_t f02 = fx::pack2(f0, f0), f12 = fx::pack2(f1, f1);
+      const int c0 = PAIR ? 0 : half * (D / 2), c1 = PAIR ? D : c0 + D / 2;
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-        uint32_t u[16], v[16];
-        tmem_ld16(tmem + lane_base + c, u);
-        // (the second group may have had no tile: its accumulator then holds anything)
-        tmem_ld16(tmem + lane_base + (C::TURNS && I.n_tiles == 1 ? 0 : D) + c, v);
-        tmem_ld_wait();
-        reg_fence16(u);
-        reg_fence16(v);
+      for (int c = c0; c < c1; c += 16) {
         float x[16];
+        if constexpr (PAIR) {
+          uint32_t u[16];
+          tmem_ld16(o_tmem + c, u);
+          tmem_ld_wait();
+          reg_fence16(u);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          fx::unpack2(fx::fma2(fx::pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f12,
-                               fx::mul2(fx::pack2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), f02)),
-                      x[e], x[e + 1]);
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(u[e]) * f0;
+        } else {
+          uint32_t u[16], v[16];
+          tmem_ld16(tmem + lane_base + c, u);
+          // (the second group may have had no tile: its accumulator then holds anything)
+          tmem_ld16(tmem + lane_base + (C::TURNS && I.n_tiles == 1 ? 0 : D) + c, v);
+          tmem_ld_wait();
+          reg_fence16(u);
+          reg_fence16(v);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            fx::unpack2(fx::fma2(fx::pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f12,
+                                 fx::mul2(fx::pack2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), f02)),
+                        x[e], x[e + 1]);
+        }
         if (!active) continue;
         if (direct) {
           uint32_t w[8];
@@ -890,7 +913,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           st_v8(dst + 8, reinterpret_cast<const uint32_t*>(x) + 8);
         }
       }
-      if (active && half == 0) {
+      if (active && (PAIR || half == 0)) {
         if (!direct) a.part_lse[orow] = lse2;
         else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
       }
@@ -1045,13 +1068,15 @@ k_join_paged(const __grid_constant__ JoinArgs t) {
   if (a.lse && sub == 0) a.lse[orow] = den > 0.f ? (m + log2f(den)) * 0.69314718055994531f : NEG_INF;
 }
 
-template <int D>
+template <int D, bool PAIR>
 constexpr size_t smem_bytes() {
-  return sizeof(Smem<D>) + 1024;  // for the 1024-byte alignment of the swizzle atoms
+  return sizeof(Smem<D, PAIR>) + 1024;  // for the 1024-byte alignment of the swizzle atoms
 }
-static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "");
+static_assert(smem_bytes<128, false>() <= 227 * 1024 && smem_bytes<64, false>() <= 227 * 1024 &&
+                  smem_bytes<64, true>() <= 227 * 1024,
+              "");
 
-template <int D, bool TREE>
+template <int D, bool TREE, bool PAIR>
 cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_items, bool cut, cudaStream_t s) {
   KArgs t{};
   t.a = a;
@@ -1068,7 +1093,7 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
   {  // q [T, Hq, D]: a box of 64 channels, G heads, ROW_TILE / G tokens is 64 channels of 128 rows
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.T};
     const uint64_t str[2] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2};
-    const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tok};
+    const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tok_tile};
     if (!encode_bf16_sw128(&m_q, a.q, 3, dims, str, box)) return cudaErrorInvalidValue;
   }
   {  // pool [num_blocks, Hkv, bs, D] as 64 channels, 8 rows, halves, groups of 8 rows
@@ -1091,7 +1116,7 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
   if (ctas <= 0) return cudaErrorInvalidDevice;
   if (a.max_ctas > 0 && a.max_ctas < ctas) ctas = a.max_ctas;
   const dim3 grid(n_items < ctas ? n_items : ctas);
-  cudaError_t e = launch_pdl(k_attn_paged<D, TREE>, grid, dim3(NUM_THREADS), smem_bytes<D>(), s, t, m_q, m_kc, m_vc,
+  cudaError_t e = launch_pdl(k_attn_paged<D, TREE, PAIR>, grid, dim3(NUM_THREADS), smem_bytes<D, PAIR>(), s, t, m_q, m_kc, m_vc,
                              m_kt, m_vt);
   if (e != cudaSuccess || !cut) return e;
   JoinArgs j{};
@@ -1108,21 +1133,30 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
   return launch_pdl(k_join_paged<D, TREE>, dim3(ceil_div(rows, per)), dim3(JOIN_THREADS), 0, s, j);
 }
 
-// The plan of a launch's sequences: how long a split may be.  Every chain of key
-// tiles (a row tile of a KV head) is an item or, cut, several; a CTA an SM takes
-// them longest first.  In units of a tile's time on an SM (0.8 us), an item costs its
-// tiles and 3 more (its start and its end), the launch ends when the SMs have shared all of that out
-// and the last items have run, and not before the keys and values have come from
-// memory (which the last items, and the items' starts, do not keep busy).  Cut chains cost a second kernel and their partial results' round trip.
+// The plan of a launch's sequences: how long a split may be, and whether an item
+// takes a pair of row tiles.  Every chain of key tiles (an item's rows of a KV head) is
+// an item or, cut, several; a CTA an SM takes them longest first.  In units of 0.8 us,
+// a tile costs TILE_TIME on an SM, an item its tiles and 3 more (its start and its
+// end), the launch ends when the SMs have shared all of that out and the last items have
+// run, and not before the keys and values have come from memory (which the last items,
+// and the items' starts, do not keep busy).  Cut chains cost a second kernel and their
+// partial results' round trip.
 // On the measured shapes the plans are within 8 % of the best of a sweep.
 struct Chains {
-  int count;     // row tiles
+  int count;     // items' rows
   int most;      // tiles of the longest chain
   double total;  // tiles of all
 };
+struct Cut {
+  int chunk_tiles;
+  double cost;
+};
+// A tile's time.  Heads of 64 with blocks of 16 wait for the boxes' issue, which a pair
+// shares between two row tiles.
+double tile_time(int D, int bs, bool pair) { return D == 128 ? 1.0 : pair ? 1.4 : bs % 32 ? 0.86 : 0.74; }
 
-int plan_chunk_tiles(const Chains* c, const int* rows, int n, int Hkv, int Hq, int D, int tree_tiles) {
-  constexpr double item_cost = 3.0, join_launch = 4.0, tile_bytes = 5.4e6;  // traffic in a tile's time
+Cut plan_cut(const Chains* c, const int* rows, int n, int Hkv, int Hq, int D, int tree_tiles, double tile) {
+  constexpr double item_cost = 3.0, join_launch = 4.0, unit_bytes = 5.4e6;  // traffic in a unit
   int longest = 1;
   double tiles = 0, streamed = 0;
   for (int k = 0; k < n; ++k) {
@@ -1130,9 +1164,9 @@ int plan_chunk_tiles(const Chains* c, const int* rows, int n, int Hkv, int Hq, i
     tiles += c[k].total + (double)c[k].count * tree_tiles;
     streamed += c[k].most + tree_tiles;  // a sequence's row tiles read the same keys
   }
-  const double memory = streamed * Hkv * (double)(4 * KV_TILE * D) / tile_bytes;
-  double best = 1e300;
-  int best_chunk = longest, last = 0;
+  const double memory = streamed * Hkv * (double)(4 * KV_TILE * D) / unit_bytes;
+  Cut best{longest, 1e300};
+  int last = 0;
   for (int s = 1; s <= 256; s += 1 + s / 8) {
     const int chunk = ceil_div(longest, s);
     if (chunk == last) continue;
@@ -1146,47 +1180,55 @@ int plan_chunk_tiles(const Chains* c, const int* rows, int n, int Hkv, int Hq, i
       if (ps > 1) part_rows += (double)ps * rows[k];
     }
     items *= Hkv;
-    const double item = tiles * Hkv / items + item_cost;  // an average one
+    const double item = tile * tiles * Hkv / items + item_cost;  // an average one
     const double waves = items / PLAN_SMS;
-    double cost = std::max(std::max(worst + tree_tiles + item_cost, item * (waves > 1 ? waves + 0.5 : 1.0)),
-                           memory + 0.25 * worst + 2.0 * std::ceil(waves));
-    if (part_rows > 0) cost += join_launch + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / tile_bytes;
-    if (cost < best) {
-      best = cost;
-      best_chunk = chunk;
-    } else if (cost > 1.5 * best) {
+    double cost = std::max(std::max(tile * (worst + tree_tiles) + item_cost, item * (waves > 1 ? waves + 0.5 : 1.0)),
+                           memory + 0.25 * tile * worst + 2.0 * std::ceil(waves));
+    if (part_rows > 0) cost += join_launch + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / unit_bytes;
+    if (cost < best.cost) {
+      best = Cut{chunk, cost};
+    } else if (cost > 1.5 * best.cost) {
       break;
     }
     if (chunk == 1) break;
   }
-  return best_chunk;
+  return best;
+}
+
+// The chains of sequence b's items of `tok` tokens.
+template <bool TREE>
+Chains chains_of(const PagedArgs& a, int tok, int len, int kv) {
+  Chains c;
+  c.count = ceil_div(len, tok);
+  if (TREE) {
+    c.most = paged_span(kv, kv, a.window, a.sinks).n;
+    c.total = (double)c.most * c.count;
+    return c;
+  }
+  const int first = chunk_span(kv, len, 0, tok, a.window, a.sinks).n;
+  const int last = chunk_span(kv, len, (c.count - 1) * tok, tok, a.window, a.sinks).n;
+  c.most = std::max(std::max(first, last), 1);
+  // a window's chains may be a tile longer or shorter in between
+  if (a.window > 0 && c.count > 2)
+    c.most = std::max(c.most, std::min(ceil_div(kv, KV_TILE), ceil_div(a.window + tok, KV_TILE) + 1 + ceil_div(a.sinks, KV_TILE)));
+  c.total = 0.5 * (first + last) * c.count;
+  return c;
 }
 
 // Sequences [b0, pl->b_end) of a call: their entries, in the order the items are taken.
 template <bool TREE>
 void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, int b0, PagedPlan* pl) {
-  Chains c[PAGED_MAX_SEQS];
+  Chains both[2][PAGED_MAX_SEQS];
   int rows[PAGED_MAX_SEQS], bs[PAGED_MAX_SEQS], order[PAGED_MAX_SEQS];
   int n = 0, b = b0;
+  bool pairs = false;  // some sequence has a second row tile
   for (; b < a.B && n < PAGED_MAX_SEQS; ++b) {
     const int len = TREE ? a.N : cu_len_host[b + 1] - cu_len_host[b];
     if (len == 0) continue;
-    const int kv = kv_host[b];
     rows[n] = len;
     bs[n] = b;
-    c[n].count = ceil_div(len, a.tok);
-    if (TREE) {
-      c[n].most = paged_span(kv, kv, a.window, a.sinks).n;
-      c[n].total = (double)c[n].most * c[n].count;
-    } else {
-      const int first = chunk_span(kv, len, 0, a.tok, a.window, a.sinks).n;
-      const int last = chunk_span(kv, len, (c[n].count - 1) * a.tok, a.tok, a.window, a.sinks).n;
-      c[n].most = std::max(std::max(first, last), 1);
-      // a window's chains may be a tile longer or shorter in between
-      if (a.window > 0 && c[n].count > 2)
-        c[n].most = std::max(c[n].most, std::min(ceil_div(kv, KV_TILE), ceil_div(a.window + a.tok, KV_TILE) + 1 + ceil_div(a.sinks, KV_TILE)));
-      c[n].total = 0.5 * (first + last) * c[n].count;
-    }
+    both[0][n] = chains_of<TREE>(a, a.tok_tile, len, kv_host[b]);
+    pairs = pairs || len > a.tok_tile;
     order[n] = n;
     ++n;
   }
@@ -1195,10 +1237,19 @@ void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* 
   pl->n_items = 0;
   pl->part_rows = 0;
   pl->chunk_tiles = 1;
+  pl->pair = false;
   pl->ok = true;
   if (n == 0) return;
   const int tree_tiles = TREE ? ceil_div(a.N, KV_TILE) : 0;
-  pl->chunk_tiles = plan_chunk_tiles(c, rows, n, a.Hkv, a.Hq, a.D, tree_tiles);
+  Cut cut = plan_cut(both[0], rows, n, a.Hkv, a.Hq, a.D, tree_tiles, tile_time(a.D, a.bs, false));
+  if (a.D == 64 && pairs) {
+    for (int k = 0; k < n; ++k) both[1][k] = chains_of<TREE>(a, 2 * a.tok_tile, rows[k], kv_host[bs[k]]);
+    const Cut p = plan_cut(both[1], rows, n, a.Hkv, a.Hq, a.D, tree_tiles, tile_time(a.D, a.bs, true));
+    pl->pair = p.cost < cut.cost;
+    if (pl->pair) cut = p;
+  }
+  const Chains* c = both[pl->pair];
+  pl->chunk_tiles = cut.chunk_tiles;
   int each[PAGED_MAX_SEQS];
   for (int k = 0; k < n; ++k) {
     const int ps = paged_splits(c[k].most, pl->chunk_tiles, INT_MAX);
@@ -1255,25 +1306,29 @@ cudaError_t run(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host,
     a.chunk_tiles = pl.chunk_tiles;
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ATTN_SCHED_BYTES);
     a.part_lse = a.part_o + (size_t)pl.part_rows * a.Hq * a.D;
-    const cudaError_t e = a.D == 128 ? launch<128, TREE>(a, pl.seq, pl.n_seqs, pl.n_items, pl.part_rows > 0, s)
-                                     : launch<64, TREE>(a, pl.seq, pl.n_seqs, pl.n_items, pl.part_rows > 0, s);
+    a.tok = pl.pair ? 2 * a.tok_tile : a.tok_tile;
+    const auto f = a.D == 128 ? launch<128, TREE, false> : pl.pair ? launch<64, TREE, true> : launch<64, TREE, false>;
+    const cudaError_t e = f(a, pl.seq, pl.n_seqs, pl.n_items, pl.part_rows > 0, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-template <int D, bool TREE>
+template <int D, bool TREE, bool PAIR>
 cudaError_t opt_in() {
-  return cudaFuncSetAttribute(k_attn_paged<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+  return cudaFuncSetAttribute(k_attn_paged<D, TREE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)smem_bytes<D, PAIR>());
 }
 
 }  // namespace
 
 cudaError_t attn_paged_prepare() {
-  cudaError_t e = opt_in<128, false>();
-  if (e == cudaSuccess) e = opt_in<128, true>();
-  if (e == cudaSuccess) e = opt_in<64, false>();
-  if (e == cudaSuccess) e = opt_in<64, true>();
+  cudaError_t e = opt_in<128, false, false>();
+  if (e == cudaSuccess) e = opt_in<128, true, false>();
+  if (e == cudaSuccess) e = opt_in<64, false, false>();
+  if (e == cudaSuccess) e = opt_in<64, true, false>();
+  if (e == cudaSuccess) e = opt_in<64, false, true>();
+  if (e == cudaSuccess) e = opt_in<64, true, true>();
   return e;
 }
 

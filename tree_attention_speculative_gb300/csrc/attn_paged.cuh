@@ -8,12 +8,12 @@ namespace ts {
 
 constexpr int PAGED_MAX_SEQS = 256;  // sequences a launch; more go in several
 
-// One sequence of a launch.  Its items are numbered item0 .. : row tiles (the
-// last, which sees the most keys, first), splits, KV heads.
+// One sequence of a launch.  Its items are numbered item0 .. : row tiles or pairs of
+// them (the last, which see the most keys, first), splits, KV heads.
 struct PagedSeq {
   int item0;
   int b;
-  int row_tiles;
+  int row_tiles; // or pairs
   int splits;    // its chains of key tiles are cut in so many at most
   int rows;      // tokens it was planned for
   int part_row;  // splits > 1: its first row (a token's) among the partial results
@@ -40,7 +40,8 @@ struct PagedArgs {
   float scale_log2;
   int window, sinks;  // window 0: every earlier key
   int chunk_tiles;    // key tiles a split at most, by the host's lengths
-  int tok;            // tokens a row tile: ROW_TILE / G
+  int tok_tile;       // tokens a row tile: ROW_TILE / G
+  int tok;            // tokens an item: of a row tile, or of a pair
   unsigned long long wait_limit_ns;
   int stall_seq, stall_tile, max_ctas;  // testing (internal.cuh: AttnArgs)
 };
@@ -85,6 +86,7 @@ struct PagedPlan {
   PagedSeq seq[PAGED_MAX_SEQS];
   int n_seqs, n_items, chunk_tiles, b_end;
   long long part_rows;  // tokens' rows of partial results
+  bool pair;            // an item takes two row tiles
   bool ok;              // its items and rows can be numbered
 };
 
