@@ -12,10 +12,10 @@
 // channels copied.  Rotary widths that are no multiple of 16 take 16 channels in
 // a row as well and fetch the other half of each pair two bytes at a time.
 //
-// Measured: 16 prompts of 1-16K, 32 + 2 x 8 heads of 128, bf16: 512 us, 6.65 TB/s, 0.98 of
-// the copy rate.  One token of each of 32 sequences 3.9 us, 529 tokens of 64 + 2 x 8
-// heads into the 8-bit cache 6.7 us (2.6 us of bytes): there it is a launch and a chain of three
-// loads (lengths, the table's entry, then the stores), beside which the values load.
+// Measured: 16 prompts of 1-16K, 32 + 2 x 8 heads of 128, bf16: 497 us, 6.85 TB/s, the copy
+// rate.  One token of each of 32 sequences 3.9 us, 450 tokens of 64 + 2 x 8 heads into the
+// 8-bit cache 6.4 us (2.6 us of bytes): a launch and a chain of three loads (lengths, the
+// table's entry, then the stores), beside which the values load.
 #include "append.cuh"
 #include "quant_row.cuh"
 #include "rope.cuh"
@@ -167,10 +167,10 @@ cudaError_t launch(const AppendRopeArgs& a, unsigned ctas, unsigned threads, Fas
 
 cudaError_t launch_append_rope(AppendRopeArgs a, cudaStream_t s) {
   const int heads = a.Hq + 2 * a.Hkv, per = a.D / 16;
-  // Tokens a CTA: an item a thread at least, but no fewer CTAs than SMs.  (More items
-  // would share one search for the sequence and one table, but loads of one round are
-  // in flight at a time, and only other CTAs fill the gaps.)
-  a.tok = ceil_div(AR_THREADS, heads * per);
+  // Tokens a CTA: two items a thread, but no fewer CTAs than SMs.  Prompts of 1-16K 497 us
+  // (one item a thread 514, four 498), 450 tokens of 80 heads 6.4 (6.7, 8.5); 32 tokens,
+  // one a CTA 3.9, two 4.6.
+  a.tok = 2 * ceil_div(AR_THREADS, heads * per);
   const int spread = a.T ? (a.T - 1) / PLAN_SMS + 1 : 1;
   a.tok = a.tok > spread ? spread : a.tok;
   a.tok = a.tok > AR_MAX_TOK ? AR_MAX_TOK : a.tok;

@@ -982,8 +982,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
 
 // Joins the splits of cut chains: out = sum_s 2^(L_s - M) O_s / sum_s 2^(L_s - M),
 // M = max L_s.  D/8 lanes a row (token, head), 8 channels each; a group of GRP
-// splits' loads is in flight at once.  Latency-bound: a few MB, 3 to 4 us behind the
-// attention, of which 1 to 2 are its launch (it starts early and waits).
+// splits' loads is in flight at once.  Latency-bound: a few MB behind the attention (the
+// plans count 3 us and its bytes).
 constexpr int JOIN_THREADS = 128;
 constexpr int JOIN_GRP = 8;
 

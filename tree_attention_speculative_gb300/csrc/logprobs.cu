@@ -36,10 +36,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 // Threads a CTA: 256, four CTAs an SM (a row's end is shorter, and more of the others
-// run beside it), where a CTA then still holds a whole row; else 512.  Measured when
-// whole columns were read again: 4096 rows of 32000 105 us (127 with 512), 500 of 1000
-// 7.8 (12.2), 2048 bf16 rows of 128256 141 (147); 2048 fp32 rows of 128256, two CTAs of
-// 256 a row, 221 (194).
+// run beside it), where a CTA then still holds a whole row; else 512.  4096 rows of
+// 32000 100 us (122 with 512), 500 of 1000 7.1 (11.4), 2048 bf16 rows of 128256 124
+// (138); 2048 fp32 rows of 128256, two CTAs of 256 a row, 194 (179).
 constexpr int LP_FEW = 256, LP_MANY = 512;
 constexpr int LP_COLUMN = 64;     // vectors a thread at most: two a lane when a warp reads a column again
 constexpr int LP_SM_THREADS = 1024;  // threads that run on an SM at once
@@ -452,7 +451,8 @@ k_logprobs(const __grid_constant__ LogprobArgs a) {
 template <typename T, int LP_THREADS>
 cudaError_t launch(LogprobArgs a, int vecs, cudaStream_t s) {
   // CTAs a row: one, or as many as the SMs hold at once where there are few rows
-  // (and a CTA keeps a vector for each thread), or a thread's column allows.
+  // (and a CTA keeps a vector for each thread), or a thread's column allows.  96 rows of
+  // 128256: 3 a row 16.3 us, 1 20.4, 6 29; 8 rows, 8 a row 9.1, 4 8.9, 2 10.4.
   int c = PLAN_SMS * (LP_SM_THREADS / LP_THREADS) / a.R;
   c = std::min(std::min(c, 8), vecs / LP_THREADS);
   c = std::max(c, ceil_div(vecs, LP_COLUMN * LP_THREADS));
