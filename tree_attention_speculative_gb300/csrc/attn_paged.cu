@@ -873,19 +873,19 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       if (!ok) break;
       tc_fence_after();
       const uint64_t f02 = fx::pack2(f0, f0), f12 = fx::pack2(f1, f1);
-      const int c0 = PAIR ? 0 : half * (D / 2), c1 = PAIR ? D : c0 + D / 2;
-#pragma unroll 1
-      for (int c = c0; c < c1; c += 16) {
-        float x[16];
+      constexpr int MINE = PAIR ? D : D / 2, PIECES = MINE / 16;  // channels a group stores; in 16s
+      const int c0 = PAIR ? 0 : half * MINE;
+      float x[16];
+      const auto piece = [&](int c) {  // 16 channels of the row
+        uint32_t u[16];
         if constexpr (PAIR) {
-          uint32_t u[16];
           tmem_ld16(o_tmem + c, u);
           tmem_ld_wait();
           reg_fence16(u);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(u[e]) * f0;
         } else {
-          uint32_t u[16], v[16];
+          uint32_t v[16];
           tmem_ld16(tmem + lane_base + c, u);
           // (the second group may have had no tile: its accumulator then holds anything)
           tmem_ld16(tmem + lane_base + (C::TURNS && I.n_tiles == 1 ? 0 : D) + c, v);
@@ -898,19 +898,50 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
                                  fx::mul2(fx::pack2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), f02)),
                         x[e], x[e + 1]);
         }
-        if (!active) continue;
-        if (direct) {
-          uint32_t w[8];
+      };
+      if (direct) {
+        // PIECES lanes exchange theirs, so that each store of the warp has whole lines:
+        // a lane then has one piece of PIECES rows.
+        uint32_t w[PIECES][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-          __nv_bfloat16* dst = a.out + orow * D + c;
-          if (args.out32) {
-            st_v8(dst, w);
-          } else {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int n = 0; n < PIECES; ++n) {
+          piece(c0 + 16 * n);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[n][e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        }
+#pragma unroll
+        for (int bit = 1; bit < PIECES; bit <<= 1) {
+          const bool upper = lane & bit;
+#pragma unroll
+          for (int n = 0; n < PIECES; ++n) {
+            if (n & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[n][e] : w[n | bit][e], bit);
+              if (upper) w[n][e] = got;
+              else w[n | bit][e] = got;
+            }
           }
-        } else {
+        }
+        const long long own = active ? (long long)orow : -1;
+#pragma unroll
+        for (int n = 0; n < PIECES; ++n) {
+          const long long row = __shfl_sync(0xffffffffu, own, (lane & ~(PIECES - 1)) | n);
+          if (row < 0) continue;
+          __nv_bfloat16* dst = a.out + row * D + c0 + 16 * (lane & (PIECES - 1));
+          if (args.out32) {
+            st_v8(dst, w[n]);
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[n][4], w[n][5], w[n][6], w[n][7]);
+          }
+        }
+        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int c = c0; c < c0 + MINE; c += 16) {
+          piece(c);
+          if (!active) continue;
           float* dst = a.part_o + orow * D + c;
           st_v8(dst, reinterpret_cast<const uint32_t*>(x));
           st_v8(dst + 8, reinterpret_cast<const uint32_t*>(x) + 8);
