@@ -152,3 +152,34 @@ def test_a_chunk_may_not_mix_devices():
             ts.chunk_params(**{**a, name: a[name].cpu()})
     with pytest.raises(ts.TreeSpecError):
         ts.tree_chunk_attn_fwd(ts.chunk_params(**a), torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_step_on_another_stream_while_the_current_one_is_busy(as_handle):
+    """What a step makes for a call (its workspace, the scores) is filled on the call's stream."""
+    import tree_attention_speculative_gb300 as ts
+    from tree_attention_speculative_gb300.step import PromptStep
+    lens, V = np.array([3, 40], np.int32), 1000
+    cu = np.concatenate(([0], np.cumsum(lens))).astype(np.int32)
+    T, past = int(cu[-1]), np.array([700, 90], np.int32)
+    table = dev(np.arange(2 * 60, dtype=np.int32).reshape(2, 60))
+    x = bf(W.normal_bf16(50, "x", (T, HQ + 2 * HKV, D)))
+    logits, tokens = torch.randn(T, V, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+    pools = [bf(W.normal_bf16(51, n, (120, HKV, BS, D))) for n in "kv"]
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (side.cuda_stream if as_handle else side, None):
+        step = PromptStep(2, T, HQ, HKV, D, ts.RopeConfig())
+        k_cache, v_cache = (p.clone() for p in pools)
+        cud, pastd = dev(cu), dev(past)
+        torch.cuda.synchronize()
+        if stream is not None:
+            torch.cuda._sleep(50_000_000)
+        out = step.run(x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], cud, cu, pastd, past, k_cache, v_cache, table, stream=stream)
+        s = step.score(logits, tokens, top=3, stream=stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        got.append((out, step.lse, s.logprob, s.entropy, s.top_ids, s.top_logprobs))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[0][2] < 0).all()

@@ -699,11 +699,12 @@ def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
             and prefix_len.get_device() == dev == block_table.get_device() and new_prefix_len.get_device() == dev):
         _bad(where)
     handle = _stream_on(where, dev, stream)
+    turn = (None, 0) if rope is None else _rope_params(rope)  # (held until the call is over)
     block = _APPEND.pack(
         0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if q is None else q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), 0 if kv_scale is None else kv_scale.data_ptr(), cu_len.data_ptr(),
         prefix_len.data_ptr(), block_table.data_ptr(), new_prefix_len.data_ptr(),
-        0 if status is None else status.data_ptr(), 0 if rope is None else _rope_params(rope)[1], qt, qh, kt, kh, vt, vh,
+        0 if status is None else status.data_ptr(), turn[1], qt, qh, kt, kh, vt, vh,
         B, T, Hq, Hkv, D, bs, nblk, maxb)
     _check(lib().tree_cache_append_rope(block, handle), where)
 
@@ -778,6 +779,8 @@ def tree_attn_fwd_window(params: AttnParams, window: int, sinks: int, workspace:
     """tree_attn_fwd (``params`` from attn_params) for a layer with a sliding window
     of ``window`` positions and ``sinks`` first tokens that stay visible."""
     where = "tree_attn_fwd_window"
+    if not params.tensors:
+        _bad(where)
     q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, anc_mask, out, lse, status = params.tensors
     rows, pool = q.shape, k_cache.shape
     B, N, Hq, D = rows
@@ -807,13 +810,15 @@ def tree_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], lo
     most likely tokens top_ids, top_logprobs [R,top].  ``rows`` [R] i32 picks the
     rows; an output whose row is out of range is left as it was."""
     where = "tree_token_logprobs"
+    if not 2 <= logits.dim() <= 3:
+        _bad(where)
     V = logits.shape[-1]
     if logits.dim() == 3:
         (M0, M1, _), (s0, s1, s2) = logits.shape, logits.stride()
         M, stride = M0 * M1, s1 if M1 > 1 else s0
         even = M0 == 1 or M1 == 1 or s0 == M1 * s1
     else:
-        M, stride, s2, even = logits.shape[0], logits.stride(0), logits.stride(1), logits.dim() == 2
+        M, stride, s2, even = logits.shape[0], logits.stride(0), logits.stride(1), True
     if M <= 1:
         stride = 0
     some = next((t for t in (logprob, entropy, top_ids, top_logprobs) if t is not None), None)

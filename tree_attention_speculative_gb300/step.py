@@ -75,7 +75,15 @@ class PackedInputs:
             self.dev.copy_(self.host, non_blocking=True)
 
 
-def _grown(step, name: str, need: int) -> torch.Tensor:
+def _on(stream, device):
+    """Makes ``stream`` (a torch stream, a handle, or None: the current one) current, so that
+    what is made for a call is filled before it."""
+    if stream is None or device.type != "cuda":
+        return torch.cuda.stream(None)
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device))
+
+
+def _grown(step, name: str, need: int, stream=None) -> torch.Tensor:
     """The step's workspace of that name, of ``need`` bytes at least.  One that grew too
     small stays allocated: captured calls still write to it."""
     ws = getattr(step, name)
@@ -84,7 +92,8 @@ def _grown(step, name: str, need: int) -> torch.Tensor:
             step.outgrown.append(ws)
             need = max(need, 2 * ws.numel())  # so that what is kept stays below the one in use
         # zero-filled once; every call leaves its head (the item counter) zero again
-        ws = torch.zeros(need, dtype=torch.uint8, device=step.device)
+        with _on(stream, step.device):
+            ws = torch.zeros(need, dtype=torch.uint8, device=step.device)
         setattr(step, name, ws)
     return ws
 
@@ -165,7 +174,7 @@ class TreeVerifyStep:
             need = tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
         if need == 0:
             raise ValueError("tree_attn_fwd would reject these arguments")
-        ws = _grown(self, "ws_attn" if kv_scale is None else "ws_attn_q8", need)
+        ws = _grown(self, "ws_attn" if kv_scale is None else "ws_attn_q8", need, stream)
         if self.window:
             tree_attn_fwd_window(p, self.window, self.sinks, ws, stream)
         elif kv_scale is None:
@@ -203,7 +212,7 @@ class TreeVerifyStep:
         """Log probabilities of the tokens the last ``run`` emitted: row b (max_depth + 1)
         + d scores the token after path step d, the next accepted draft or at the end
         the bonus, under that step's logits.  Rows past a path stay 0 (ids -1)."""
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+        with _on(stream, self.device):
             path, after = self.accepted, torch.cat((self.accepted[:, 1:], self.accepted.new_full((self.B, 1), -1)), 1)
             base = torch.arange(self.B, dtype=torch.int32, device=self.device)[:, None] * self.N
             rows = torch.where(path >= 0, base + path, -1).view(-1)
@@ -219,7 +228,8 @@ class PromptStep:
     cu_len[b] .. cu_len[b+1]-1, at most ``max_tokens`` in all): ``run`` appends them to
     the paged cache with their rotary positions and attends; ``score`` gives the
     log probabilities of the tokens that followed.  ``window`` and ``sinks`` are those
-    of a windowed layer (0: none)."""
+    of a windowed layer (0: none).  ``status`` keeps a sequence's error: nothing more is
+    appended to it until the caller has set it back to 0."""
 
     def __init__(self, B: int, max_tokens: int, Hq: int, Hkv: int, D: int, rope: RopeConfig, device="cuda",
                  scale: float = 0.0, window: int = 0, sinks: int = 0):
@@ -249,7 +259,7 @@ class PromptStep:
         need = tree_chunk_attn_workspace_size(p)
         if need == 0:
             raise ValueError("tree_chunk_attn_fwd would reject these arguments")
-        tree_chunk_attn_fwd(p, _grown(self, "ws_attn", need), stream)
+        tree_chunk_attn_fwd(p, _grown(self, "ws_attn", need, stream), stream)
         return self.out[:T]
 
     def run(self, q, k, v, cu_len, cu_len_host, prefix_len, prefix_len_host, k_cache, v_cache, block_table, stream=None):
@@ -263,7 +273,8 @@ class PromptStep:
     def score(self, logits, tokens, rows=None, temperature: float = 1.0, top: int = 0, stream=None) -> _Scores:
         """Log probabilities of ``tokens`` [R] under ``logits`` rows (those of ``rows``, or the
         first R)."""
-        out = _Scores(tokens.shape[0], top, self.device)
+        with _on(stream, self.device):
+            out = _Scores(tokens.shape[0], top, self.device)
         tree_token_logprobs(logits, tokens, out.logprob, out.entropy, out.top_ids, out.top_logprobs, rows=rows,
                             temperature=temperature, stream=stream)
         return out
