@@ -791,12 +791,15 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             ok = false;
             break;
           }
-          // 64-channel pieces of the group's rows, one a thread
-          const int vr = key_in + r % KEYS, hh = r / KEYS, t = key0 + r % KEYS;
-          if (t >= I.hi || (t < I.lo && t >= a.sinks)) {
-            uint4* row = reinterpret_cast<uint4*>(sm.v[slot] + ((vr >> 3) * C::HALVES + hh) * 1024 + (vr & 7) * 128);
+          // (16 bytes a store, a row's by adjacent threads: a row a thread would take its
+          // stores through the same banks, 32 passes each)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+          for (int n = 0; n < KEYS * C::HALVES * 8 / GROUP_THREADS; ++n) {
+            const int c = n * GROUP_THREADS + r, piece = c >> 3, hh = piece / KEYS, vr = key_in + piece % KEYS;
+            const int t = key0 + piece % KEYS;
+            if (t >= I.hi || (t < I.lo && t >= a.sinks))
+              *reinterpret_cast<uint4*>(sm.v[slot] + ((vr >> 3) * C::HALVES + hh) * 1024 + (vr & 7) * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
         }
