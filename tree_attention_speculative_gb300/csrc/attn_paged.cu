@@ -34,12 +34,12 @@
 // But for pairs, the groups are joined at an item's end, and each stores half of the channels.
 //
 // What bounds it.  Long chains of heads of 128: the tensor cores under the power cap
-// (4096 tokens over 16K, 32 heads: 611 us in bursts, 1.57 PFLOP/s, 0.84 of the
-// measured GEMM rate; 652 us back to back).  Heads of 64 have half the products for the
-// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 455 us,
-// 1.13 PFLOP/s; without pairs 472 with blocks of 64, and 559 with blocks of 16, where
+// (4096 tokens over 16K, 32 heads: 607 us in bursts, 1.58 PFLOP/s, 0.84 of the
+// measured GEMM rate; 645 us back to back).  Heads of 64 have half the products for the
+// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 449 us,
+// 1.15 PFLOP/s; without pairs 472 with blocks of 64, and 559 with blocks of 16, where
 // it is the issue of 16 TMA boxes a tile).  Single tokens: memory (32 sequences of 0-8K:
-// 81 us, 6.2 TB/s, 0.92 of the measured copy).  An item costs about 3 us beyond its
+// 80 us, 6.3 TB/s, 0.92 of the measured copy).  An item costs 2 to 3 us beyond its
 // tiles: the start of its pipeline, the last PV, the stores.  What carried it (64 heads of
 // 128 and of 64 on 64 trees of 64 nodes over 8K, us):
 //   one softmax group, 128 columns a thread                       848  823
@@ -53,6 +53,8 @@
 // apart by half a period (580 -> 602); one P arrival a warp (no change); three-input
 // maxima (no change: the compiler's own).  Pairs of heads of 128: 675 -> 825.  On pairs of
 // heads of 64 (455): loads of 32 columns a step ahead 520, of 128 at once 564 (spills).
+// Heads of 128 with one accumulator, shared references and three S buffers: 4K of 16K 611
+// -> 597, 8 prompts of 512 35 -> 50.
 //
 // Masks cost nothing where a tile is wholly visible; elsewhere each row makes
 // a word of its visible keys.  Keys that no row of the item sees may be
