@@ -384,7 +384,9 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           q[3] = make_int4(I.t_begin, I.n_prefix, I.n_tiles, I.ps);
           publish(&sm.items_pub, k + 1);
           if (I.n_tiles)  // its queries, into L2, while the last item's keys are still at work
-            for (int h = 0; h < C::HALVES; ++h) tma_prefetch_3d(&tm_q, 64 * h, I.g * a.G, I.q0 + I.i0);
+            for (int x = 0; x < C::SETS && I.i0 + x * a.tok_tile < I.len; ++x)
+              for (int h = 0; h < C::HALVES; ++h)
+                tma_prefetch_3d(&tm_q, 64 * h, I.g * a.G, I.q0 + I.i0 + x * a.tok_tile);
         }
         __syncwarp();
         held = -1;
