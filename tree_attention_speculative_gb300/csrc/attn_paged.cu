@@ -1178,12 +1178,15 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
 // The plan of a launch's sequences: how long a split may be, and whether an item
 // takes a pair of row tiles.  Every chain of key tiles (an item's rows of a KV head) is
 // an item or, cut, several; a CTA an SM takes them longest first.  In units of 0.8 us,
-// a tile costs TILE_TIME on an SM, an item its tiles and 3 more (its start and its
-// end), the launch ends when the SMs have shared all of that out and the last items have
-// run, and not before the keys and values have come from memory (which the last items,
-// and the items' starts, do not keep busy).  Cut chains cost a second kernel and their
-// partial results' round trip.
-// On the measured shapes the plans are within 8 % of the best of a sweep.
+// a tile costs tile_time on an SM (STREAMED times as much where no other row tile brings
+// its keys to L2), an item its tiles and 3 more (its start and its end).  The launch ends
+// when the SMs have shared all of that out: a batch of few sequences, whose items may
+// differ much, is dealt out as the kernel will; of many, the average item says it.  And it
+// does not end before the keys and values have come from memory (which the last items, and
+// the items' starts, do not keep busy).  Cut chains cost a second kernel and their partial
+// results' round trip.  On the measured shapes the plans are within 5 % of the best of a
+// sweep (by averages alone, a prompt's 1024 tokens beside 64-tile chains of single tokens
+// were left uncut: 71 us, now 66).
 struct Chains {
   int count;     // items' rows
   int most;      // tiles of the longest chain
@@ -1197,43 +1200,95 @@ struct Cut {
 // shares between two row tiles.
 double tile_time(int D, int bs, bool pair) { return D == 128 ? 1.0 : pair ? 1.4 : bs % 32 ? 0.86 : 0.74; }
 
+constexpr double STREAMED = 1.2;
+constexpr int FEW_SEQS = 16;
+
+// When the last of n groups of items is done, on PLAN_SMS SMs that take them longest first:
+// at[] and sms[], ascending, so many SMs are free at that time.
+double dealt_out(double* time, double* count, int n) {
+  double at[2 * FEW_SEQS + 2], sms[2 * FEW_SEQS + 2];
+  int m = 1;
+  at[0] = 0;
+  sms[0] = PLAN_SMS;
+  for (int k = 1; k < n; ++k)  // longest first
+    for (int j = k; j > 0 && time[j] > time[j - 1]; --j) {
+      std::swap(time[j], time[j - 1]);
+      std::swap(count[j], count[j - 1]);
+    }
+  for (int k = 0; k < n; ++k) {
+    for (double left = count[k]; left > 0;) {
+      const double take = std::min(left, sms[0]), end = at[0] + time[k];
+      left -= take;
+      sms[0] -= take;
+      int to = sms[0] > 0 ? m : m - 1;  // entries once the first, used up, is gone
+      if (sms[0] <= 0) {
+        std::copy(at + 1, at + m, at);
+        std::copy(sms + 1, sms + m, sms);
+      }
+      m = to;
+      while (to > 0 && at[to - 1] > end) {
+        at[to] = at[to - 1];
+        sms[to] = sms[to - 1];
+        --to;
+      }
+      if (to > 0 && at[to - 1] == end) {
+        sms[to - 1] += take;
+        for (; to < m; ++to) at[to] = at[to + 1], sms[to] = sms[to + 1];
+      } else {
+        at[to] = end;
+        sms[to] = take;
+        ++m;
+      }
+    }
+  }
+  return at[m - 1];
+}
+
 Cut plan_cut(const Chains* c, const int* rows, int n, int Hkv, int Hq, int D, int tree_tiles, double tile) {
   constexpr double item_cost = 3.0, join_launch = 4.0, unit_bytes = 5.4e6;  // traffic in a unit
   int longest = 1;
-  double tiles = 0, streamed = 0;
+  double streamed = 0;
   for (int k = 0; k < n; ++k) {
     longest = std::max(longest, c[k].most);
-    tiles += c[k].total + (double)c[k].count * tree_tiles;
     streamed += c[k].most + tree_tiles;  // a sequence's row tiles read the same keys
   }
   const double memory = streamed * Hkv * (double)(4 * KV_TILE * D) / unit_bytes;
   Cut best{longest, 1e300};
-  int last = 0;
-  for (int s = 1; s <= 256; s += 1 + s / 8) {
-    const int chunk = ceil_div(longest, s);
-    if (chunk == last) continue;
-    last = chunk;
-    double items = 0, part_rows = 0;
+  const auto look = [&](int chunk) {  // what cutting to so many tiles costs
+    double items = 0, part_rows = 0, longest_item = 0, work = 0, time[FEW_SEQS], count[FEW_SEQS];
     int worst = 0;
     for (int k = 0; k < n; ++k) {
       const int ps = paged_splits(c[k].most, chunk, INT_MAX);
-      items += (double)c[k].count * ps;
+      const double own = tile * (c[k].count == 1 ? STREAMED : 1.0), group = (double)c[k].count * ps * Hkv;
+      const double mean = own * (c[k].total / c[k].count + tree_tiles) / ps + item_cost;
+      items += group;
+      work += group * mean;
       worst = std::max(worst, ceil_div(c[k].most, ps));
+      longest_item = std::max(longest_item, own * (ceil_div(c[k].most, ps) + tree_tiles) + item_cost);
       if (ps > 1) part_rows += (double)ps * rows[k];
+      if (n <= FEW_SEQS) {
+        time[k] = mean;
+        count[k] = group;
+      }
     }
-    items *= Hkv;
-    const double item = tile * tiles * Hkv / items + item_cost;  // an average one
     const double waves = items / PLAN_SMS;
-    double cost = std::max(std::max(tile * (worst + tree_tiles) + item_cost, item * (waves > 1 ? waves + 0.5 : 1.0)),
-                           memory + 0.25 * tile * worst + 2.0 * std::ceil(waves));
-    if (part_rows > 0) cost += join_launch + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / unit_bytes;
-    if (cost < best.cost) {
-      best = Cut{chunk, cost};
-    } else if (cost > 1.5 * best.cost) {
-      break;
-    }
-    if (chunk == 1) break;
+    double cost = std::max(std::max(longest_item, work / PLAN_SMS), memory + 0.25 * tile * worst + 2.0 * std::ceil(waves));
+    const double join = part_rows > 0 ? join_launch + 2.0 * part_rows * Hq * (4.0 * D + 4.0) / unit_bytes : 0.0;
+    if (n > FEW_SEQS || waves > 4) cost = std::max(cost, work / items * (waves > 1 ? waves + 0.5 : 1.0));
+    else if (waves > 1 && cost + join < best.cost) cost = std::max(cost, dealt_out(time, count, n));
+    cost += join;
+    if (cost < best.cost) best = Cut{chunk, cost};
+    return cost;
+  };
+  for (int s = 1, last = 0; s <= 256; s += 1 + s / 8) {
+    const int chunk = ceil_div(longest, s);
+    if (chunk == last) continue;
+    last = chunk;
+    if (look(chunk) > 1.5 * best.cost || chunk == 1) break;
   }
+  if (n <= FEW_SEQS)  // or those cut that are longer than one of them
+    for (int k = 0; k < n; ++k)
+      if (c[k].most < longest && 2 * c[k].most > longest) look(c[k].most);
   return best;
 }
 
