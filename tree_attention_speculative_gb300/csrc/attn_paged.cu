@@ -1184,9 +1184,9 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
 // differ much, is dealt out as the kernel will; of many, the average item says it.  And it
 // does not end before the keys and values have come from memory (which the last items, and
 // the items' starts, do not keep busy).  Cut chains cost a second kernel and their partial
-// results' round trip.  On the measured shapes the plans are within 5 % of the best of a
-// sweep (by averages alone, a prompt's 1024 tokens beside 64-tile chains of single tokens
-// were left uncut: 71 us, now 66).
+// results' round trip.  On fourteen ragged batches the plans were within 0 to 12 % of the
+// best of a sweep (by averages alone, a prompt's 1024 tokens beside 64-tile chains of
+// single tokens were left uncut: 72 us, now 64).
 struct Chains {
   int count;     // items' rows
   int most;      // tiles of the longest chain
