@@ -107,6 +107,19 @@ def test_chunk_workspace_holds_the_parts_of_cut_chains(ts):  # noqa: F811
     assert ts.tree_chunk_attn_workspace_size(p) == 256
 
 
+def test_a_few_long_chains_are_cut_beside_a_prompt(ts):  # noqa: F811
+    """A prompt's 1024 tokens (32 row tiles of 24 key tiles, 8 heads) keep the SMs busy for about 50 tiles' time; the
+    64-tile chains of two single tokens would outlast them, so they are cut, and nothing else is."""
+    lens, past = [1024, 1, 1, 37, 1, 200, 1, 1], [2048, 8191, 4000, 0, 777, 6001, 7800, 5]
+    cu = np.concatenate(([0], np.cumsum(lens))).astype(np.int32)
+    T = int(cu[-1])
+    p = _chunk(ts, q=_z(T, 32, 128), out=_z(T, 32, 128), lse=None, status=None, k_cache=_z(40, 8, 16, 128), v_cache=_z(40, 8, 16, 128),
+               block_table=_i(8, 600), cu_len=_i(9), kv_len=_i(8), cu_len_host=cu,
+               kv_len_host=np.add(lens, past).astype(np.int32))
+    parts = (ts.tree_chunk_attn_workspace_size(p) - 256) / (32 * (4 * 128 + 4))
+    assert parts in (4, 5, 6)  # two chains (one row each) in two or three
+
+
 # ------------------------------------------------------------------------------------------------- windowed trees
 
 @pytest.mark.parametrize("window,sinks,code", [(0, 0, SHAPE), (-3, 0, SHAPE), (4, -1, SHAPE), ((1 << 30) + 1, 0, UNSUPPORTED),

@@ -497,7 +497,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       ++q_landed;
       for (int v = 0; v < C::SETS * n_tiles; ++v) {
         const int j = v / C::SETS, x = v % C::SETS;
-        ok = __all_sync(0xffffffffu, (x > 0 || wait_bar(&sm.k_full[slot], k_phase, ctl)) && wait_bar(&sm.s_free[buf], s_phase, ctl));
+        ok = __all_sync(0xffffffffu, (x > 0 || wait_bar(&sm.k_full[slot], k_phase, ctl)) &&
+                                         wait_bar(&sm.s_free[buf], s_phase, ctl));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + TMEM_S0 + buf * KV_TILE;
@@ -788,8 +789,9 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         }
         const bool rescale = use > first && active && m_use != m_run;
         if (dead && !(PAIR && half)) {
-          // (of a pair the first group, whose PV is the first to read the tile)  V rows that no row of the item sees hold whatever the pool, or the
-          // ring, had there: zeroed, so that 0 * V is 0
+          // V rows that no row of the item sees hold whatever the pool, or the ring, had
+          // there: zeroed, so that 0 * V is 0 (of a pair by the first group, whose PV is
+          // the first to read the tile)
           const int vt = jt / C::SETS, slot = vt % C::NST;
           if (!__all_sync(0xffffffffu, wait_bar(&sm.v_full[slot], (vt / C::NST) & 1, ctl))) {
             ok = false;
@@ -1307,7 +1309,8 @@ Chains chains_of(const PagedArgs& a, int tok, int len, int kv) {
   c.most = std::max(std::max(first, last), 1);
   // a window's chains may be a tile longer or shorter in between
   if (a.window > 0 && c.count > 2)
-    c.most = std::max(c.most, std::min(ceil_div(kv, KV_TILE), ceil_div(a.window + tok, KV_TILE) + 1 + ceil_div(a.sinks, KV_TILE)));
+    c.most = std::max(c.most, std::min(ceil_div(kv, KV_TILE),
+                                       ceil_div(a.window + tok, KV_TILE) + 1 + ceil_div(a.sinks, KV_TILE)));
   c.total = 0.5 * (first + last) * c.count;
   return c;
 }
