@@ -703,7 +703,9 @@ TS_API ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream str
  * normaliser.  Logits, statistics and output sums are fp32; the softmax weights
  * are rounded to bf16 in the product with the values (half a step, 2^-8 of each at
  * most), and the parts of a chain of keys that is cut between SMs are joined in
- * fp32.  Weights may reach 2^40 before the sums are scaled down, so the output of a
+ * fp32.  Outputs are divided by a sum of weights in which the largest of each 64 or 128
+ * keys counts as rounded, so that the error of a weight that outweighs the others
+ * cancels; lse is of the unrounded ones.  Weights may reach 2^40 before the sums are scaled down, so the output of a
  * channel with a value past 2^87 / kv_b may be infinite.  Calls repeat bit for bit.
  *
  *   q            [T, Hq, D] bf16; out the same, lse [T, Hq] fp32 or NULL.  Rows of

@@ -82,12 +82,21 @@ constexpr int GROUP_THREADS = 128;  // a softmax group: a row a thread
 constexpr int K_WARP = 0, QK_WARP = 1, PV_WARP = 2, V_WARP = 3, SOFTMAX_WARP0 = 4, SOFTMAX_WARPS = 8;
 constexpr int HALF = KV_TILE / 2;  // keys of a tile that one softmax group takes
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int ITEM_Q = 8;    // entries of the item queue
 // A row's weights are taken against a reference, the maximum of the first keys it
 // sees, and may reach 2^40 of it (their precision does not depend on that).  Then the
 // reference is raised and the sums are scaled down.
 constexpr float RESCALE_THRESHOLD = 40.0f;
 constexpr float SUM_LIMIT = 1099511627776.f;  // 2^40
+// The weights are rounded to bf16 for the product with the values (half a step, 2^-8 of
+// each at most) and summed before that, in fp32, for the log-sum-exp.  A weight that
+// outweighs the others is seldom 1, so its rounding would be the output's; outputs are
+// divided by a sum that takes the largest weight of each tile (of its half of one, where the
+// groups share it) as rounded, and that error cancels.  With a hundredth of the keys eight
+// times the others, outputs are off by 1.6e-3 to 1.7e-3 of themselves, 1.5e-3 to 1.6e-3 being
+// their own rounding; 2.1e-3 to 2.3e-3 with the plain sum.  Summing all the rounded weights
+// gives no less.  Heads of 128 know the largest score already; heads of 64 look for it, one
+// instruction in six of the softmax: 2K prompts with a window 294 -> 311 us (361 with the sum
+// of all, which takes heads of 128 from 614 to 648 on 4K of 16K).
 constexpr float NEG_INF = -INFINITY;
 
 template <int D, bool PAIR>
@@ -98,6 +107,7 @@ struct Cfg {
   static constexpr int Q_BYTES = ROW_TILE * D * 2;  // of a row tile
   static constexpr int SETS = PAIR ? 2 : 1;         // row tiles an item
   static constexpr int NST = D == 128 ? 3 : PAIR ? 5 : 6;  // tiles in each ring, K and V
+  static constexpr int ITEM_Q = D == 128 ? 4 : 8;          // entries of the item queue: what shared memory leaves
   static_assert(D == 64 || !PAIR, "");
   // The two softmax groups: a row tile each of a pair; else on heads of 64 the key
   // tiles in turn, on heads of 128 half the keys of every tile each.
@@ -124,11 +134,13 @@ struct __align__(1024) Smem {
   int abort_flag;
   // the CTA's items in the order taken; pub published, done by how many softmax warps
   // they were stored (no warp is more than one item ahead of another)
-  int4 item_q[ITEM_Q][4];
+  int4 item_q[C::ITEM_Q][4];
   int items_pub, items_done;
   // an item's end: group 1's (m, l) of each row, then from group 0 the factors of
-  // both accumulators (1 KB each way would not fit beside heads of 128)
+  // both accumulators (1 KB each way would not fit beside heads of 128); and what group
+  // 1's accumulator is to be divided by
   float2 ml[ROW_TILE];
+  float norm[ROW_TILE];
 };
 
 struct KArgs {
@@ -322,7 +334,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       return true;
     }
     if (!wait_count(&sm.items_pub, k + 1, ctl)) return false;
-    const int4* q = sm.item_q[k % ITEM_Q];
+    const int4* q = sm.item_q[k % C::ITEM_Q];
     const int4 x = q[0], y = q[1], z = q[2], w = q[3];
     I = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w, w.x, w.y, w.z, w.w};
     return true;
@@ -373,11 +385,11 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             cl = load_lens<TREE>(args.seq[cpl.e].b, args.seq[cpl.e].rows, a);
           }
         }
-        bool ok = k < ITEM_Q;  // the entry's last user must be done
-        if (!ok && lane == 0) ok = wait_count(&sm.items_done, SOFTMAX_WARPS * (k - ITEM_Q + 1), ctl);
+        bool ok = k < C::ITEM_Q;  // the entry's last user must be done
+        if (!ok && lane == 0) ok = wait_count(&sm.items_done, SOFTMAX_WARPS * (k - C::ITEM_Q + 1), ctl);
         if (!__shfl_sync(0xffffffffu, ok, 0)) return jg;
         if (lane == 0) {
-          int4* q = sm.item_q[k % ITEM_Q];
+          int4* q = sm.item_q[k % C::ITEM_Q];
           q[0] = make_int4(I.b, I.g, I.split, I.e);
           q[1] = make_int4(I.q0, I.i0, I.len, I.pos0);
           q[2] = make_int4(I.lo, I.hi, I.n_sink, I.win0);
@@ -667,7 +679,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       int clear0 = 0;
       if (lo_most > 0) clear0 = I.n_sink + max(ceil_div(lo_most, KV_TILE) - I.win0, 0) - I.t_begin;
       const int clear1 = I.n_sink + hi_least / KV_TILE - I.win0 - I.t_begin;
-      float m_run = NEG_INF, l_run = 0.f;
+      float m_run = NEG_INF, l_run = 0.f, norm_run = 0.f;  // norm: what the output is divided by
       const int first = C::TURNS ? half : 0;
       bool fresh = true;
       const int n_uses = C::SETS * I.n_tiles;
@@ -713,7 +725,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
               if (!((w >> e) & 1ull)) s[e] = NEG_INF;
           }
         };
-        const auto largest = [&]() {  // of s, in the exponent's units
+        const auto largest = [&]() {  // of s
           float mk[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) mk[e] = s[e];
@@ -721,13 +733,16 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           for (int c = 4; c < HALF; c += 4)
 #pragma unroll
             for (int e = 0; e < 4; ++e) mk[e] = fmaxf(mk[e], s[c + e]);
-          return fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * a.scale_log2;
+          return fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
         };
         const uint64_t scale2 = fx::pack2(a.scale_log2, a.scale_log2);
         uint64_t negm2, sum2[2];
+        float neg_m, top;  // top: the largest weight
         const auto against = [&](float m) {  // (-inf: nothing visible so far, every weight is 0)
-          negm2 = m == NEG_INF ? 0ull : fx::pack2(-m, -m);
+          neg_m = m == NEG_INF ? 0.f : -m;
+          negm2 = fx::pack2(neg_m, neg_m);
           sum2[0] = sum2[1] = 0ull;
+          top = 0.f;
         };
         const auto weigh = [&](uint32_t (&pk)[HALF / 2]) {  // s to bf16 weights, and their sums
 #pragma unroll
@@ -737,6 +752,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
             const float p0 = ex2(x0), p1 = ex2(x1);
             sum2[e & 1] = fx::add2(sum2[e & 1], fx::pack2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
+            if (C::TURNS) top = fx::max3(top, p0, p1);
           }
         };
         const auto total = [&]() {
@@ -758,7 +774,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
 #pragma unroll 1
               for (int h = 0; h < PARTS; ++h) {
                 load(h);
-                m_tile = fmaxf(m_tile, largest());
+                m_tile = fmaxf(m_tile, largest() * a.scale_log2);
               }
               if (need) m_use = fmaxf(m_run, m_tile);
             }
@@ -779,13 +795,14 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           for (int h = 0; h < PARTS; ++h) tmem_st32(s_tmem + h * HALF, pk[h]);
         } else {
           load(0);
-          const float m_new = fmaxf(m_run, largest());
+          const float s_top = largest(), m_new = fmaxf(m_run, s_top * a.scale_log2);
           if (use == first || (active && m_new > m_run + RESCALE_THRESHOLD)) m_use = m_new;
           against(m_use);
           uint32_t pk[HALF / 2];
           weigh(pk);
           tmem_st32(s_tmem, pk);
           rowsum = total();
+          top = ex2(fmaf(s_top, a.scale_log2, neg_m));  // as weigh made it
         }
         const bool rescale = use > first && active && m_use != m_run;
         if (dead && !(PAIR && half)) {
@@ -822,6 +839,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
           tc_fence_after();
           const float f = !rescale ? 1.f : m_run == NEG_INF ? 0.f : ex2(m_run - m_use);
           l_run *= f;
+          norm_run *= f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t u0[32];
@@ -835,6 +853,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         }
         m_run = m_use;
         l_run += rowsum;
+        norm_run += rowsum + (__bfloat162float(__float2bfloat16_rn(top)) - top);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.p_full[buf][C::TURNS ? 0 : half]);
@@ -845,6 +864,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       // of the channels, of both accumulators; of a pair each stores its own row tile.
       if (!PAIR && half == 1) {
         sm.ml[r] = make_float2(m_run, l_run);
+        sm.norm[r] = norm_run;
         mbar_arrive(&sm.ml_full);
       }
       Item next;  // asked for while the last PV runs
@@ -853,7 +873,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       float f0 = 0.f, f1 = 0.f, lse2 = NEG_INF;
       if (PAIR) {
         if (l_run > 0.f) lse2 = m_run + __log2f(l_run);
-        f0 = l_run > 0.f ? 1.f / l_run : 0.f;  // a row that sees no key: zeros
+        f0 = norm_run > 0.f ? 1.f / norm_run : 0.f;  // a row that sees no key: zeros
       } else if (half == 0) {
         ok = __all_sync(0xffffffffu, wait_bar(&sm.ml_full, k & 1, ctl));
         if (!ok) break;
@@ -862,7 +882,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         f0 = m_run == NEG_INF ? 0.f : ex2(m_run - m_all);
         f1 = other.x == NEG_INF ? 0.f : ex2(other.x - m_all);
         const float l_all = l_run * f0 + other.y * f1;
-        const float inv = l_all > 0.f ? 1.f / l_all : 0.f;  // a row that sees no key: zeros
+        const float norm = norm_run * f0 + sm.norm[r] * f1;
+        const float inv = norm > 0.f ? 1.f / norm : 0.f;  // a row that sees no key: zeros
         if (l_all > 0.f) lse2 = m_all + __log2f(l_all);
         f0 *= inv;
         f1 *= inv;
@@ -1000,8 +1021,8 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
       if (single) {
         if (done == 0) report(blockIdx.x);
       } else {
-        for (int k = done; k < sm.items_pub && k < done + ITEM_Q; ++k) {
-          const int4* q = sm.item_q[k % ITEM_Q];
+        for (int k = done; k < sm.items_pub && k < done + C::ITEM_Q; ++k) {
+          const int4* q = sm.item_q[k % C::ITEM_Q];
           if (q[3].z && a.status) a.status[q[0].x] = TS_ERR_TIMEOUT;
         }
       }
