@@ -658,9 +658,12 @@ TS_API ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint
  *                  nothing of them but the tokens' rows is written.
  *   kv_scale       [num_blocks, Hkv, block_size, 2] uint8 (the 8-bit cache) or NULL.
  *   cu_len, prefix_len, new_prefix_len, status, block_table: as
- *                  tree_cache_append_q8 takes them, with its errors.  Rows of q_out
- *                  of no sequence, and of one whose status is not 0 or whose sizes
- *                  are wrong, are left as they were.
+ *                  tree_cache_append_q8 takes them, with its errors.  Of a sequence
+ *                  whose status is not 0 or whose sizes are wrong (TS_ERR_SHAPE)
+ *                  nothing is written; rows of q_out of no sequence are left as they
+ *                  were.  Of one with a bad block (TS_ERR_BAD_BLOCK, found in this
+ *                  call) any of its rows of q_out and of its blocks may have been
+ *                  written or not.
  *   rope           the configuration: rotary_dim, interleaved, scaling, theta,
  *                  factor, low_rot, high_rot, orig_len and mscale of it are read
  *                  (host memory).  NULL: nothing turns (q must be NULL).

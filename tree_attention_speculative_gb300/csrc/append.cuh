@@ -44,6 +44,32 @@ __device__ __forceinline__ void append_sequence(const A& a, int b, int lane) {
   }
 }
 
+// Whether cu_len rises throughout, which makes every sequence's rows its own: this
+// thread's part of the answer (all `threads` of them are to hold).
+template <class A>
+__device__ __forceinline__ bool append_ordered(const A& a, int thread, int threads) {
+  bool ok = true;
+  for (int i = thread; i < a.B; i += threads) ok = ok && a.cu_len[i] <= a.cu_len[i + 1];
+  return ok;
+}
+
+// Where it does not: whether the rows of the sequence that append_place found for
+// token t are its own (append_sequence's test).
+template <class A>
+__device__ __forceinline__ bool append_owns(const A& a, int t) {
+  int lo = 0, hi = a.B;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu_len[mid + 1] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  if (lo == a.B) return false;
+  const int c0 = a.cu_len[lo], c1 = a.cu_len[lo + 1];
+  bool own = true;
+  for (int i = 0; i <= a.B; ++i) own = own && (i <= lo ? a.cu_len[i] <= c0 : a.cu_len[i] >= c1);
+  return own;
+}
+
 // Token t's position (-1: it is no sequence's, or its sequence gets nothing) and
 // the pool row of its KV head 0 (-1: no valid block).
 struct AppendPlace {
@@ -63,7 +89,8 @@ __device__ __forceinline__ AppendPlace append_place(const A& a, int t) {
   if (lo < a.B) {
     const int c0 = a.cu_len[lo], c1 = a.cu_len[lo + 1], P = a.prefix_len[lo];
     const int st = a.status ? a.status[lo] : TS_OK;
-    if (st == TS_OK && c0 >= 0 && t >= c0 && t < c1 && P >= 0 && P <= APPEND_MAX_LEN && c1 - c0 <= APPEND_MAX_LEN - P) {
+    if (st == TS_OK && c0 >= 0 && t >= c0 && t < c1 && c1 <= a.T && P >= 0 && P <= APPEND_MAX_LEN &&
+        c1 - c0 <= APPEND_MAX_LEN - P) {
       p.pos = P + (t - c0);
       const int i = p.pos / a.bs;
       const int blk = i < a.max_blocks ? a.block_table[(size_t)lo * a.max_blocks + i] : -1;

@@ -12,9 +12,9 @@
 // channels copied.  Rotary widths that are no multiple of 16 take 16 channels in
 // a row as well and fetch the other half of each pair two bytes at a time.
 //
-// Measured: 16 prompts of 1-16K, 32 + 2 x 8 heads of 128, bf16: 497 us, 6.85 TB/s, the copy
-// rate.  One token of each of 32 sequences 3.9 us, 450 tokens of 64 + 2 x 8 heads into the
-// 8-bit cache 6.4 us (2.6 us of bytes): a launch and a chain of three loads (lengths, the
+// Measured: 16 prompts of 1-16K, 32 + 2 x 8 heads of 128, bf16: 500 us, 6.8 TB/s, the copy
+// rate.  One token of each of 32 sequences 3.8 us, 450 tokens of 64 + 2 x 8 heads into the
+// 8-bit cache 6.5 us (2.6 us of bytes): a launch and a chain of three loads (lengths, the
 // table's entry, then the stores), beside which the values load.
 #include "append.cuh"
 #include "quant_row.cuh"
@@ -72,12 +72,18 @@ k_append_rope(const __grid_constant__ AppendRopeArgs a, FastDiv heads) {
     at(threadIdx.x);
     load();
   }
+  // (the last threads' loads run beside those of the first, which find the places)
+  const bool ordered = append_ordered(a, blockDim.x - 1 - threadIdx.x, blockDim.x);
   if ((int)threadIdx.x < ntok) {
     const AppendPlace p = append_place(a, t0 + threadIdx.x);
     dest[threadIdx.x] = p.row;
     pos[threadIdx.x] = p.pos;
   }
-  __syncthreads();
+  if (!__syncthreads_and(ordered)) {
+    // some sequence's rows are not its own: such a one gets nothing
+    if ((int)threadIdx.x < ntok && !append_owns(a, t0 + threadIdx.x)) dest[threadIdx.x] = pos[threadIdx.x] = -1;
+    __syncthreads();
+  }
   for (int e = threadIdx.x; e < ntok * half; e += blockDim.x) {
     const int kk = e / half;
     table[e] = rope_sincos(pos[kk], a.turn[e - kk * half], a.mscale);
