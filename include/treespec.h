@@ -664,6 +664,8 @@ TS_API ts_status tree_attn_fwd_q8_stall_test(const ts_attn_params* p, const uint
  *                  were.  Of one with a bad block (TS_ERR_BAD_BLOCK, found in this
  *                  call) any of its rows of q_out and of its blocks may have been
  *                  written or not.
+ *   appended       [B] int32 out or NULL: how many of a sequence's tokens were appended,
+ *                  all of them or, where it keeps its length, 0.
  *   rope           the configuration: rotary_dim, interleaved, scaling, theta,
  *                  factor, low_rot, high_rot, orig_len and mscale of it are read
  *                  (host memory).  NULL: nothing turns (q must be NULL).
@@ -688,6 +690,7 @@ typedef struct ts_append_params {
   int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
   int B, T, Hq, Hkv, D;
   int block_size, num_blocks, max_blocks;
+  int32_t* appended;
 } ts_append_params;
 
 TS_API ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream stream);
@@ -725,8 +728,12 @@ TS_API ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream str
  *                smaller; a sequence with more rows than it was planned for, fewer
  *                tokens than rows, rows past T or tokens past its table's row gets
  *                TS_ERR_SHAPE and nothing written.
+ *   appended     [B] int32 or NULL: how many rows a sequence has in its cache (as
+ *                tree_cache_append_rope gives it).  One with more rows than that, for
+ *                which the append failed, gets TS_ERR_SHAPE and nothing written.
  *   status       [B] int32 or NULL: errors as tree_attn_fwd (TS_ERR_BAD_BLOCK: block
- *                0 was read in its place; TS_ERR_TIMEOUT).
+ *                0 was read in its place; TS_ERR_TIMEOUT).  TS_ERR_SHAPE is not written
+ *                over an error that is there already.
  *   scale        0 selects 1/sqrt(D).
  *
  * workspace: tree_chunk_attn_workspace_size(p) bytes, 256-byte aligned, its first
@@ -750,6 +757,7 @@ typedef struct ts_chunk_params {
   int block_size, num_blocks, max_blocks;
   float scale;
   int window, sinks;
+  const int32_t* appended;
 } ts_chunk_params;
 
 TS_API size_t tree_chunk_attn_workspace_size(const ts_chunk_params* p);
@@ -775,7 +783,8 @@ TS_API ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* worksp
  * in fewer bits tree_chunk_attn_fwd's; a row that sees no key gives zeros and an lse of
  * -inf.  Blocks that no node sees into are not followed.  The key of a node may hold anything for the rows it is hidden from; its
  * value must be finite.  In a captured call prefix_len may have changed when it is
- * replayed; one outside the table's row gets TS_ERR_SHAPE and nothing written.
+ * replayed; one outside the table's row gets TS_ERR_SHAPE (or keeps the error that its
+ * status holds) and nothing written.
  * workspace: tree_attn_window_workspace_size bytes, as tree_chunk_attn_fwd's, and may
  * be shared with it.
  */

@@ -86,6 +86,7 @@ class AppendParams(ctypes.Structure):
         ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
         ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
         ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int), ("max_blocks", ctypes.c_int),
+        ("appended", ctypes.c_void_p),
     ]
 
 
@@ -98,6 +99,7 @@ class ChunkParams(ctypes.Structure):
         ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
         ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int), ("max_blocks", ctypes.c_int),
         ("scale", ctypes.c_float), ("window", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("appended", ctypes.c_void_p),
     ]
     device = None  # that of every tensor, as chunk_params found it
 
@@ -266,8 +268,8 @@ def tree_build_ancestry_forest(parent_idx: torch.Tensor, prefix_len: torch.Tenso
 # The parameter blocks, packed at once: a small call's time is its marshalling, and a
 # ctypes.Structure's fields cost four times as much one by one.
 _ATTN = struct.Struct("13P8i2f")
-_APPEND = struct.Struct("13P6q8i")
-_CHUNK = struct.Struct("11P8if2i4x")
+_APPEND = struct.Struct("13P6q8iP")
+_CHUNK = struct.Struct("11P8if2i4xP")
 assert _ATTN.size == ctypes.sizeof(AttnParams) and _CHUNK.size == ctypes.sizeof(ChunkParams)
 assert _APPEND.size == ctypes.sizeof(AppendParams)
 
@@ -664,11 +666,13 @@ def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
                            prefix_len: torch.Tensor, q_out: Optional[torch.Tensor], k_cache: torch.Tensor,
                            v_cache: torch.Tensor, block_table: torch.Tensor, new_prefix_len: torch.Tensor,
                            rope: Optional[RopeConfig], status: Optional[torch.Tensor] = None,
-                           kv_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+                           kv_scale: Optional[torch.Tensor] = None, stream=None,
+                           appended: Optional[torch.Tensor] = None) -> None:
     """Append the new tokens k, v [T,Hkv,D] bf16 of all sequences (sequence b's are
     rows cu_len[b] .. cu_len[b+1]-1) to the paged cache from prefix_len on, q
     [T,Hq,D] and k rotated at their positions (q into the dense q_out), and write
-    new_prefix_len.  With ``kv_scale`` the cache is the 8-bit one.  q, k and v may
+    new_prefix_len and, in ``appended``, how many tokens of each sequence were
+    appended.  With ``kv_scale`` the cache is the 8-bit one.  q, k and v may
     be views of a fused projection; without ``rope`` (and q) k is stored as it is."""
     where = "tree_cache_append_rope"
     shape = T, Hkv, D = k.shape
@@ -695,6 +699,7 @@ def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
     if not (cache and pool == (nblk, Hkv, bs, D) and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
             and _is(prefix_len, _I32, (B,)) and _is(new_prefix_len, _I32, (B,))
             and (status is None or (_is(status, _I32, (B,)) and status.get_device() == dev))
+            and (appended is None or (_is(appended, _I32, (B,)) and appended.get_device() == dev))
             and v.get_device() == dev == k_cache.get_device() and v_cache.get_device() == dev == cu_len.get_device()
             and prefix_len.get_device() == dev == block_table.get_device() and new_prefix_len.get_device() == dev):
         _bad(where)
@@ -705,17 +710,18 @@ def tree_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
         k_cache.data_ptr(), v_cache.data_ptr(), 0 if kv_scale is None else kv_scale.data_ptr(), cu_len.data_ptr(),
         prefix_len.data_ptr(), block_table.data_ptr(), new_prefix_len.data_ptr(),
         0 if status is None else status.data_ptr(), turn[1], qt, qh, kt, kh, vt, vh,
-        B, T, Hq, Hkv, D, bs, nblk, maxb)
+        B, T, Hq, Hkv, D, bs, nblk, maxb, 0 if appended is None else appended.data_ptr())
     _check(lib().tree_cache_append_rope(block, handle), where)
 
 
 def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                  cu_len: torch.Tensor, kv_len: torch.Tensor, cu_len_host, kv_len_host, out: torch.Tensor,
                  lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, scale: float = 0.0,
-                 window: int = 0, sinks: int = 0) -> ChunkParams:
+                 window: int = 0, sinks: int = 0, appended: Optional[torch.Tensor] = None) -> ChunkParams:
     """Fill tree_chunk_attn_fwd's parameter block from tensors (shapes as in
     treespec.h), each of which is checked.  ``cu_len_host`` and ``kv_len_host`` are
-    the host's copies of ``cu_len`` and ``kv_len``.  The returned object keeps them all."""
+    the host's copies of ``cu_len`` and ``kv_len``; ``appended`` is what
+    tree_cache_append_rope wrote.  The returned object keeps them all."""
     where = "chunk_params"
     T, Hq, D = q.shape
     nblk, Hkv, bs, _ = k_cache.shape
@@ -726,17 +732,19 @@ def chunk_params(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if not (_is(q, _BF16, (T, Hq, D)) and _is(out, _BF16, (T, Hq, D)) and _is(k_cache, _BF16, pool)
             and _is(v_cache, _BF16, pool) and _is(block_table, _I32, (B, maxb)) and _is(cu_len, _I32, (B + 1,))
             and _is(kv_len, _I32, (B,)) and cu.shape == (B + 1,) and kv.shape == (B,)
-            and (lse is None or _is(lse, torch.float32, (T, Hq))) and (status is None or _is(status, _I32, (B,)))):
+            and (lse is None or _is(lse, torch.float32, (T, Hq))) and (status is None or _is(status, _I32, (B,)))
+            and (appended is None or _is(appended, _I32, (B,)))):
         _bad(where)
     dev = q.get_device()
-    for t in (out, k_cache, v_cache, block_table, cu_len, kv_len, lse, status):
+    for t in (out, k_cache, v_cache, block_table, cu_len, kv_len, lse, status, appended):
         if t is not None and t.get_device() != dev:
             _bad(where)
     p = ChunkParams.from_buffer_copy(_CHUNK.pack(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_len.data_ptr(),
         kv_len.data_ptr(), _address(cu), _address(kv), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        0 if status is None else status.data_ptr(), B, T, Hq, Hkv, D, bs, nblk, maxb, scale, window, sinks))
-    p._keep = (cu, kv, q, k_cache, v_cache, block_table, cu_len, kv_len, out, lse, status)
+        0 if status is None else status.data_ptr(), B, T, Hq, Hkv, D, bs, nblk, maxb, scale, window, sinks,
+        0 if appended is None else appended.data_ptr()))
+    p._keep = (cu, kv, q, k_cache, v_cache, block_table, cu_len, kv_len, out, lse, status, appended)
     p.device = dev
     return p
 

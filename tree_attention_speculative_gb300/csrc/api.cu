@@ -811,6 +811,7 @@ PagedArgs chunk_args(const ts_chunk_params* p) {
              p->D, p->block_size, p->num_blocks, p->max_blocks, p->scale, p->window, p->sinks);
   a.cu_len = p->cu_len;
   a.kv_len = p->kv_len;
+  a.appended = p->appended;
   return a;
 }
 
@@ -891,8 +892,10 @@ ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream stream) {
   const Span fresh = span(p->new_prefix_len, 4ull * p->B);
   const Span ints[3] = {span(p->prefix_len, 4ull * p->B), span(p->cu_len, 4ull * (p->B + 1ull)),
                         span(p->status, p->status ? 4ull * p->B : 0)};
+  const Span appended = span(p->appended, p->appended ? 4ull * p->B : 0);
   for (const Span& s : ints)
-    if (overlap(fresh, s) || overlap(q_out, s)) return TS_ERR_SHAPE;
+    if (overlap(fresh, s) || overlap(q_out, s) || overlap(appended, s)) return TS_ERR_SHAPE;
+  if (overlap(appended, fresh) || overlap(appended, q_out)) return TS_ERR_SHAPE;
   if (overlap(q_out, rows(p->q, qt, qh, Hq)) || overlap(q_out, rows(p->k, kt, kh, p->Hkv)) ||
       overlap(q_out, rows(p->v, vt, vh, p->Hkv)) || overlap(q_out, fresh))
     return TS_ERR_SHAPE;
@@ -908,6 +911,7 @@ ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream stream) {
   a.block_table = p->block_table;
   a.new_prefix_len = p->new_prefix_len;
   a.status = p->status;
+  a.appended = p->appended;
   a.B = p->B; a.T = p->T; a.Hq = Hq; a.Hkv = p->Hkv; a.D = p->D; a.bs = p->block_size;
   a.num_blocks = p->num_blocks; a.max_blocks = p->max_blocks;
   a.q_token = qt; a.q_head = qh; a.k_token = kt; a.k_head = kh; a.v_token = vt; a.v_head = vh;

@@ -11,9 +11,10 @@ namespace ts {
 constexpr int APPEND_MAX_LEN = 1 << 30;  // positions stay far inside 32 bits
 
 // A warp checks sequence b, all of it, and writes its new length: one with a bad
-// block keeps its old one, so what was written past it never counts.
+// block keeps its old one, so what was written past it never counts.  Returns how
+// many tokens it has become longer.
 template <class A>
-__device__ __forceinline__ void append_sequence(const A& a, int b, int lane) {
+__device__ __forceinline__ int append_sequence(const A& a, int b, int lane) {
   const int P = a.prefix_len[b], c0 = a.cu_len[b], c1 = a.cu_len[b + 1];
   const int st = a.status ? a.status[b] : TS_OK;
   // its rows are its own: no sequence before it ends, and none after it begins, among them
@@ -38,10 +39,12 @@ __device__ __forceinline__ void append_sequence(const A& a, int b, int lane) {
     }
   }
   ok = __all_sync(0xffffffffu, ok);
+  const int longer = ok && st == TS_OK ? c1 - c0 : 0;
   if (lane == 0) {
-    a.new_prefix_len[b] = ok && st == TS_OK ? P + (c1 - c0) : P;
+    a.new_prefix_len[b] = P + longer;
     if (!ok && st == TS_OK && a.status) a.status[b] = sized ? TS_ERR_BAD_BLOCK : TS_ERR_SHAPE;
   }
+  return longer;
 }
 
 // Whether cu_len rises throughout, which makes every sequence's rows its own: this

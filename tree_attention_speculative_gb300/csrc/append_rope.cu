@@ -38,7 +38,10 @@ k_append_rope(const __grid_constant__ AppendRopeArgs a, FastDiv heads) {
   pdl_trigger();
   if ((int)blockIdx.x < a.len_ctas) {
     const int b = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-    if (b < a.B) append_sequence(a, b, threadIdx.x & 31);
+    if (b < a.B) {
+      const int longer = append_sequence(a, b, threadIdx.x & 31);
+      if (a.appended && (threadIdx.x & 31) == 0) a.appended[b] = longer;
+    }
     return;
   }
   const int t0 = (blockIdx.x - a.len_ctas) * a.tok;

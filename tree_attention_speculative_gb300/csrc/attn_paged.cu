@@ -216,7 +216,7 @@ __device__ __forceinline__ int tile_key(const Item& I, int j) {
 // The lengths of sequence b as the device has them.
 struct Lens {
   int q0, len, kv;
-  bool ok;  // they are what the launch was planned for
+  bool ok;  // they are what the launch was planned for, and the rows are in the cache
 };
 __device__ __forceinline__ int ld_early(const int* p) {  // issued where it is written
   int v;
@@ -234,13 +234,18 @@ __device__ __forceinline__ Lens load_lens(int b, int planned, const PagedArgs& a
     l.ok = l.kv >= 0 && l.kv <= cap;
   } else {
     l.q0 = ld_early(a.cu_len + b);
-    const int q1 = ld_early(a.cu_len + b + 1);
+    const int q1 = ld_early(a.cu_len + b + 1), in_cache = a.appended ? ld_early(a.appended + b) : INT_MAX;
     l.ok = l.q0 >= 0 && q1 >= l.q0 && q1 <= a.T && q1 - l.q0 <= planned;
     l.len = l.ok ? q1 - l.q0 : 0;
-    l.ok = l.ok && l.kv >= l.len && l.kv <= cap;
+    l.ok = l.ok && l.kv >= l.len && l.kv <= cap && in_cache >= l.len;
   }
   if (!l.ok) l.len = 0;  // nothing of it is read or written
   return l;
+}
+
+// One thread: sequence b is refused, unless it has an error already.
+__device__ __forceinline__ void refuse(int32_t* status, int b) {
+  if (status && status[b] == TS_OK) status[b] = TS_ERR_SHAPE;
 }
 
 // The first n bits of a 64-bit word.
@@ -322,7 +327,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
   const bool grabber = warp == K_WARP && !single;
   Lens l0{0, 0, 0, false};
   if (single || grabber) l0 = load_lens<TREE>(b0, args.seq[pl0.e].rows, a);
-  if (single && !l0.ok && threadIdx.x == 0 && a.status) a.status[b0] = TS_ERR_SHAPE;
+  if (single && !l0.ok && threadIdx.x == 0) refuse(a.status, b0);
   const Item item0 = make_item<TREE>(pl0, b0, l0.q0, l0.len, l0.kv, args);
 
   // Entry k of the queue (every role but the K producer; with a CTA an item every
@@ -372,7 +377,7 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         I.n_tiles = 0;
         for (;;) {
           if (cand < 0) break;
-          if (!cl.ok && lane == 0 && a.status) a.status[args.seq[cpl.e].b] = TS_ERR_SHAPE;
+          if (!cl.ok && lane == 0) refuse(a.status, args.seq[cpl.e].b);
           I = make_item<TREE>(cpl, args.seq[cpl.e].b, cl.q0, cl.len, cl.kv, args);
           if (I.n_tiles) break;
           int nx = -1;

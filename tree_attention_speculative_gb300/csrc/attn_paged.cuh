@@ -26,6 +26,7 @@ struct PagedArgs {
   const int32_t* block_table;
   const int32_t* cu_len;  // chunk: rows cu_len[b] .. cu_len[b+1]-1 are sequence b's
   const int32_t* kv_len;  // chunk: tokens in the cache, the rows' own last; tree: the verified prefix
+  const int32_t* appended;  // chunk: how many rows are in the cache; null: all
   const __nv_bfloat16* k_tree;
   const __nv_bfloat16* v_tree;
   const uint64_t* anc_mask;

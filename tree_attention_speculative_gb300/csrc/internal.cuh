@@ -319,6 +319,7 @@ struct AppendRopeArgs {
   const int32_t* block_table;
   int32_t* new_prefix_len;
   int32_t* status;
+  int32_t* appended;  // null: not asked for
   int B, T, Hq, Hkv, D, bs, num_blocks, max_blocks;
   int R, interleaved;  // R = 0: nothing turns
   long long q_token, q_head, k_token, k_head, v_token, v_head;

@@ -229,7 +229,7 @@ class PromptStep:
     the paged cache with their rotary positions and attends; ``score`` gives the
     log probabilities of the tokens that followed.  ``window`` and ``sinks`` are those
     of a windowed layer (0: none).  ``status`` keeps a sequence's error: nothing more is
-    appended to it until the caller has set it back to 0."""
+    appended to it, and no rows of its are attended, until the caller has set it back to 0."""
 
     def __init__(self, B: int, max_tokens: int, Hq: int, Hkv: int, D: int, rope: RopeConfig, device="cuda",
                  scale: float = 0.0, window: int = 0, sinks: int = 0):
@@ -241,21 +241,25 @@ class PromptStep:
         self.lse = torch.zeros(max_tokens, Hq, dtype=torch.float32, device=dev)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
         self.status = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.appended = torch.full((B,), 1 << 30, dtype=torch.int32, device=dev)  # (before the first append: any rows)
         self.ws_attn = None
         self.outgrown = []
 
     def append(self, q, k, v, cu_len, prefix_len, k_cache, v_cache, block_table, kv_scale=None, stream=None):
         """The tokens into the cache (with ``kv_scale`` the 8-bit one); the rotated queries
-        and, in ``kv_len``, the sequences' new lengths."""
+        and, in ``kv_len`` and ``appended``, the sequences' new lengths and how much longer
+        they have become."""
         q_rot = None if q is None else self.q_rot[:q.shape[0]]
         tree_cache_append_rope(q, k, v, cu_len, prefix_len, q_rot, k_cache, v_cache, block_table, self.kv_len,
-                               self.rope, self.status, kv_scale, stream)
+                               self.rope, self.status, kv_scale, stream, self.appended)
         return q_rot
 
     def attention(self, q, k_cache, v_cache, block_table, cu_len, cu_len_host, kv_len_host, stream=None):
+        """The newest tokens' outputs, of as many as the last ``append`` put into the cache at
+        most: those of a sequence to which it appended nothing are left as they were."""
         T = q.shape[0]
         p = chunk_params(q, k_cache, v_cache, block_table, cu_len, self.kv_len, cu_len_host, kv_len_host, self.out[:T],
-                         self.lse[:T], self.status, self.scale, self.window, self.sinks)
+                         self.lse[:T], self.status, self.scale, self.window, self.sinks, self.appended)
         need = tree_chunk_attn_workspace_size(p)
         if need == 0:
             raise ValueError("tree_chunk_attn_fwd would reject these arguments")
