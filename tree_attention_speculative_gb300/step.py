@@ -149,8 +149,16 @@ class TreeVerifyStep:
         return attn_params(q, k_cache, v_cache, block_table, prefix_len, self.prefix_len_host, k_tree, v_tree,
                            self.anc, self.pos, self.out, self.lse, self.status, scale=self.scale)
 
-    def attn_workspace_bytes(self, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree) -> int:
-        return tree_attn_workspace_size(self._params(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree))
+    def _workspace_bytes(self, p, kv_scale) -> int:
+        if self.window and kv_scale is not None:
+            raise ValueError("a windowed layer's cache is bf16")
+        if self.window:
+            return tree_attn_window_workspace_size(p, self.window, self.sinks)
+        return tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
+
+    def attn_workspace_bytes(self, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, kv_scale=None) -> int:
+        """The bytes that ``attention`` needs for these arguments."""
+        return self._workspace_bytes(self._params(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree), kv_scale)
 
     def ancestry(self, parent, prefix_len, stream=None):
         build = tree_build_ancestry_forest if self.forest else tree_build_ancestry
@@ -166,12 +174,7 @@ class TreeVerifyStep:
 
     def attention(self, q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, stream=None, kv_scale=None):
         p = self._params(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree)
-        if self.window and kv_scale is not None:
-            raise ValueError("a windowed layer's cache is bf16")
-        if self.window:
-            need = tree_attn_window_workspace_size(p, self.window, self.sinks)
-        else:
-            need = tree_attn_workspace_size(p) if kv_scale is None else tree_attn_q8_workspace_size(p)
+        need = self._workspace_bytes(p, kv_scale)
         if need == 0:
             raise ValueError("tree_attn_fwd would reject these arguments")
         ws = _grown(self, "ws_attn" if kv_scale is None else "ws_attn_q8", need, stream)
