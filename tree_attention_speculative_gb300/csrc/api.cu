@@ -972,7 +972,7 @@ ts_status tree_token_logprobs(const ts_logprob_params* p, ts_stream stream) {
   const uintptr_t size = p->half ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(p->logits) % size) return TS_ERR_SHAPE;
   const float k = 1.4426950408889634f / p->temperature;
-  if (!positive(k)) return TS_ERR_SHAPE;  // (a temperature next to 0, or past 2^126)
+  if (!positive(k)) return TS_ERR_SHAPE;  // a temperature below log2(e) 2^-128: past fp32
   if (p->R == 0) return TS_OK;
   LogprobArgs a{};
   a.logits = p->logits;

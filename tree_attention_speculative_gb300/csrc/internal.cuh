@@ -345,7 +345,9 @@ struct LogprobArgs {
   int slice;  // vectors a CTA of the row's cluster
 };
 constexpr int LOGPROB_MAX_TOP = 32;
-constexpr int LOGPROB_MAX_V = 8 * (65536 - 8);  // a cluster of 8 CTAs, 16384 vectors of 4 each, wherever the row starts
+// The longest row: four CTAs' columns of fp32 (512 threads, 64 vectors of 4 values each), less
+// 64 values, so that it fits wherever the row starts.  (Clusters of 8, and bf16, would hold more.)
+constexpr int LOGPROB_MAX_V = 4 * 512 * 64 * 4 - 64;
 cudaError_t launch_logprobs(LogprobArgs a, cudaStream_t s);
 
 struct CommitQ8Args {
