@@ -18,7 +18,8 @@
  *                           the same for several roots per sequence
  *   tree_verify_stochastic  temperature verification by rejection sampling
  *   tree_commit_accepted    append the accepted path to the paged cache
- *   tree_attn_workspace_size, tree_attn_plan, tree_attn_plan_order, tree_verify_workspace_size
+ *   tree_attn_workspace_size, tree_attn_plan, tree_attn_plan_order, tree_verify_workspace_size,
+ *   tree_chunk_attn_plan, tree_attn_window_plan
  *                           host-only queries: workspace bytes, split plan
  *   tree_rope               rotary positions of the tree's queries and keys,
  *                           before the attention
@@ -763,6 +764,19 @@ typedef struct ts_chunk_params {
 TS_API size_t tree_chunk_attn_workspace_size(const ts_chunk_params* p);
 TS_API ts_status tree_chunk_attn_fwd(const ts_chunk_params* p, void* workspace, size_t workspace_bytes,
                                      ts_stream stream);
+
+/*
+ * tree_chunk_attn_plan, tree_attn_window_plan — how tree_chunk_attn_fwd and
+ * tree_attn_fwd_window (below) cut the work of these arguments' first 256 sequences
+ * with rows (host only, launches nothing).  *pairs: 1 where an item takes two
+ * tiles of 128 / (Hq / Hkv) tokens, which share each tile of keys, else 0.  The T tiles
+ * of 128 keys of an item's chain are cut into ceil(T / *chunk_tiles) splits;
+ * *max_splits is the most of any sequence.  Each output pointer may be NULL.
+ * Returns TS_ERR_NULL / TS_ERR_SHAPE / TS_ERR_UNSUPPORTED like the calls.
+ */
+TS_API ts_status tree_chunk_attn_plan(const ts_chunk_params* p, int32_t* chunk_tiles, int32_t* max_splits, int32_t* pairs);
+TS_API ts_status tree_attn_window_plan(const ts_attn_params* p, int window, int sinks, int32_t* chunk_tiles,
+                                       int32_t* max_splits, int32_t* pairs);
 
 /*
  * tree_chunk_attn_fwd_test — for testing only: tree_chunk_attn_fwd on at most

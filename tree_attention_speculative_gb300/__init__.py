@@ -149,7 +149,7 @@ EXPORTS = ("ts_status_str", "tree_build_ancestry", "tree_attn_workspace_size", "
            "tree_cache_append_q8", "tree_commit_accepted_q8", "tree_attn_q8_workspace_size", "tree_attn_fwd_q8",
            "tree_attn_fwd_q8_stall_test", "tree_cache_append_rope", "tree_chunk_attn_workspace_size",
            "tree_chunk_attn_fwd", "tree_chunk_attn_fwd_test", "tree_attn_window_workspace_size",
-           "tree_attn_fwd_window", "tree_token_logprobs")
+           "tree_attn_fwd_window", "tree_token_logprobs", "tree_chunk_attn_plan", "tree_attn_window_plan")
 
 # TS_VERIFY_NOALLOC_SCRATCH_BYTES of treespec.h
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -220,6 +220,10 @@ def lib() -> ctypes.CDLL:
         L.tree_chunk_attn_fwd.restype = i32
         L.tree_chunk_attn_fwd_test.argtypes = [ctypes.POINTER(ChunkParams), vp, sz, i32, i32, i32, ctypes.c_uint32, vp]
         L.tree_chunk_attn_fwd_test.restype = i32
+        L.tree_chunk_attn_plan.argtypes = [ctypes.POINTER(ChunkParams), vp, vp, vp]
+        L.tree_chunk_attn_plan.restype = i32
+        L.tree_attn_window_plan.argtypes = [ctypes.POINTER(AttnParams), i32, i32, vp, vp, vp]
+        L.tree_attn_window_plan.restype = i32
         L.tree_attn_window_workspace_size.argtypes = [ctypes.POINTER(AttnParams), i32, i32]
         L.tree_attn_window_workspace_size.restype = sz
         L.tree_attn_fwd_window.argtypes = [ctypes.POINTER(AttnParams), i32, i32, vp, sz, vp]
@@ -753,6 +757,17 @@ def tree_chunk_attn_workspace_size(params: ChunkParams) -> int:
     return int(lib().tree_chunk_attn_workspace_size(ctypes.byref(params)))
 
 
+def _paged_plan(where: str, call, *args) -> dict:
+    c, s, pairs = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
+    _check(call(*args, ctypes.byref(c), ctypes.byref(s), ctypes.byref(pairs)), where)
+    return {"chunk_tiles": c.value, "max_splits": s.value, "pairs": bool(pairs.value)}
+
+
+def tree_chunk_attn_plan(params: ChunkParams) -> dict:
+    """How tree_chunk_attn_fwd cuts these arguments' work (host only)."""
+    return _paged_plan("tree_chunk_attn_plan", lib().tree_chunk_attn_plan, ctypes.byref(params))
+
+
 def _chunk_stream(where: str, params: ChunkParams, workspace, stream) -> int:
     if not workspace.is_contiguous() or params.device != workspace.get_device():
         _bad(where)
@@ -781,6 +796,11 @@ def tree_chunk_attn_fwd_test(params: ChunkParams, workspace: torch.Tensor, max_c
 
 def tree_attn_window_workspace_size(params: AttnParams, window: int, sinks: int) -> int:
     return int(lib().tree_attn_window_workspace_size(ctypes.byref(params), window, sinks))
+
+
+def tree_attn_window_plan(params: AttnParams, window: int, sinks: int) -> dict:
+    """How tree_attn_fwd_window cuts these arguments' work (host only)."""
+    return _paged_plan("tree_attn_window_plan", lib().tree_attn_window_plan, ctypes.byref(params), window, sinks)
 
 
 def tree_attn_fwd_window(params: AttnParams, window: int, sinks: int, workspace: torch.Tensor, stream=None) -> None:

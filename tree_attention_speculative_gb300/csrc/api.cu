@@ -849,6 +849,18 @@ ts_status paged_impl(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_
                                                                                                         : TS_ERR_CUDA;
 }
 
+ts_status paged_plan(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, int32_t* chunk_tiles,
+                     int32_t* max_splits, int32_t* pairs) {
+  PagedPlan pl;
+  if (attn_paged_workspace(a, cu_len_host, kv_host, &pl) == 0) return TS_ERR_UNSUPPORTED;
+  int most = 1;
+  for (int k = 0; k < pl.n_seqs; ++k) most = std::max(most, pl.seq[k].splits);
+  if (chunk_tiles) *chunk_tiles = pl.chunk_tiles;
+  if (max_splits) *max_splits = most;
+  if (pairs) *pairs = pl.pair;
+  return TS_OK;
+}
+
 }  // namespace
 }  // namespace ts
 
@@ -943,6 +955,19 @@ ts_status tree_chunk_attn_fwd_test(const ts_chunk_params* p, void* workspace, si
   a.stall_tile = stall_seq >= 0 ? stall_tile : 0;
   a.wait_limit_ns = (unsigned long long)wait_limit_us * 1000ull;
   return paged_impl(a, p->cu_len_host, p->kv_len_host, workspace, workspace_bytes, stream);
+}
+
+ts_status tree_chunk_attn_plan(const ts_chunk_params* p, int32_t* chunk_tiles, int32_t* max_splits, int32_t* pairs) {
+  const ts_status st = check_chunk(p);
+  if (st != TS_OK) return st;
+  return paged_plan(chunk_args(p), p->cu_len_host, p->kv_len_host, chunk_tiles, max_splits, pairs);
+}
+
+ts_status tree_attn_window_plan(const ts_attn_params* p, int window, int sinks, int32_t* chunk_tiles, int32_t* max_splits,
+                                int32_t* pairs) {
+  const ts_status st = check_window(p, window, sinks);
+  if (st != TS_OK) return st;
+  return paged_plan(window_args(p, window, sinks), nullptr, p->prefix_len_host, chunk_tiles, max_splits, pairs);
 }
 
 size_t tree_attn_window_workspace_size(const ts_attn_params* p, int window, int sinks) {
