@@ -728,7 +728,8 @@ TS_API ts_status tree_cache_append_rope(const ts_append_params* p, ts_stream str
  *                kv_b may have changed by the time it is replayed, and n_b become
  *                smaller; a sequence with more rows than it was planned for, fewer
  *                tokens than rows, rows past T or tokens past its table's row gets
- *                TS_ERR_SHAPE and nothing written.
+ *                TS_ERR_SHAPE and nothing written.  (A batch planned without any
+ *                rows launches nothing.)
  *   appended     [B] int32 or NULL: how many rows a sequence has in its cache (as
  *                tree_cache_append_rope gives it).  One with more rows than that, for
  *                which the append failed, gets TS_ERR_SHAPE and nothing written.

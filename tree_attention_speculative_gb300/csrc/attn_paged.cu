@@ -148,6 +148,7 @@ struct KArgs {
   int box_rows, n_items, n_seqs, out32;
   FastDiv fd_hkv, fd_bs, fd_g;
   PagedSeq seq[PAGED_MAX_SEQS];
+  PagedGaps gaps;
 };
 
 // Entry of an item: the last with item0 <= it.
@@ -248,6 +249,21 @@ __device__ __forceinline__ void refuse(int32_t* status, int b) {
   if (status && status[b] == TS_OK) status[b] = TS_ERR_SHAPE;
 }
 
+// One thread: those of [c0, c1), planned without rows, that have some by now.
+__device__ __forceinline__ void refuse_gap(const PagedArgs& a, int c0, int c1) {
+  if (c0 >= c1 || a.cu_len[c0] == a.cu_len[c1]) return;
+  for (int c = c0; c < c1; ++c)
+    if (a.cu_len[c] != a.cu_len[c + 1]) refuse(a.status, c);
+}
+// At the first item of entry e: its neighbours.
+template <bool TREE>
+__device__ __forceinline__ void refuse_gaps(int e, const KArgs& t) {
+  if (TREE || !t.a.status) return;
+  const int b = t.seq[e].b;
+  refuse_gap(t.a, t.gaps.before[e], b);
+  if (b == t.gaps.last) refuse_gap(t.a, b + 1, t.gaps.end);
+}
+
 // The first n bits of a 64-bit word.
 __device__ __forceinline__ uint64_t first_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
@@ -327,7 +343,10 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
   const bool grabber = warp == K_WARP && !single;
   Lens l0{0, 0, 0, false};
   if (single || grabber) l0 = load_lens<TREE>(b0, args.seq[pl0.e].rows, a);
-  if (single && !l0.ok && threadIdx.x == 0) refuse(a.status, b0);
+  if (single && threadIdx.x == 0) {
+    if (!l0.ok) refuse(a.status, b0);
+    if ((int)blockIdx.x == args.seq[pl0.e].item0) refuse_gaps<TREE>(pl0.e, args);
+  }
   const Item item0 = make_item<TREE>(pl0, b0, l0.q0, l0.len, l0.kv, args);
 
   // Entry k of the queue (every role but the K producer; with a CTA an item every
@@ -377,7 +396,10 @@ k_attn_paged(const __grid_constant__ KArgs args, const __grid_constant__ CUtenso
         I.n_tiles = 0;
         for (;;) {
           if (cand < 0) break;
-          if (!cl.ok && lane == 0) refuse(a.status, args.seq[cpl.e].b);
+          if (lane == 0) {
+            if (!cl.ok) refuse(a.status, args.seq[cpl.e].b);
+            if (cand == args.seq[cpl.e].item0) refuse_gaps<TREE>(cpl.e, args);
+          }
           I = make_item<TREE>(cpl, args.seq[cpl.e].b, cl.q0, cl.len, cl.kv, args);
           if (I.n_tiles) break;
           int nx = -1;
@@ -1147,7 +1169,9 @@ static_assert(smem_bytes<128, false>() <= 227 * 1024 && smem_bytes<64, false>() 
               "");
 
 template <int D, bool TREE, bool PAIR>
-cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_items, bool cut, cudaStream_t s) {
+cudaError_t launch(const PagedArgs& a, const PagedPlan& pl, cudaStream_t s) {
+  const PagedSeq* seq = pl.seq;
+  const int n_seqs = pl.n_seqs, n_items = pl.n_items;
   KArgs t{};
   t.a = a;
   t.box_rows = KV_TILE;
@@ -1159,6 +1183,9 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
   t.fd_bs = FastDiv::make(a.bs);
   t.fd_g = FastDiv::make(a.G);
   std::copy(seq, seq + n_seqs, t.seq);
+  std::copy(pl.gaps.before, pl.gaps.before + n_seqs, t.gaps.before);
+  t.gaps.last = pl.gaps.last;
+  t.gaps.end = pl.gaps.end;
   CUtensorMap m_q, m_kc, m_vc, m_kt, m_vt;
   {  // q [T, Hq, D]: a box of 64 channels, G heads, ROW_TILE / G tokens is 64 channels of 128 rows
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.T};
@@ -1188,7 +1215,7 @@ cudaError_t launch(const PagedArgs& a, const PagedSeq* seq, int n_seqs, int n_it
   const dim3 grid(n_items < ctas ? n_items : ctas);
   cudaError_t e = launch_pdl(k_attn_paged<D, TREE, PAIR>, grid, dim3(NUM_THREADS), smem_bytes<D, PAIR>(), s, t, m_q, m_kc, m_vc,
                              m_kt, m_vt);
-  if (e != cudaSuccess || !cut) return e;
+  if (e != cudaSuccess || pl.part_rows == 0) return e;
   JoinArgs j{};
   j.a = a;
   j.fd_hq = FastDiv::make(a.Hq);
@@ -1345,12 +1372,15 @@ Chains chains_of(const PagedArgs& a, int tok, int len, int kv) {
 template <bool TREE>
 void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* kv_host, int b0, PagedPlan* pl) {
   Chains both[2][PAGED_MAX_SEQS];
-  int rows[PAGED_MAX_SEQS], bs[PAGED_MAX_SEQS], order[PAGED_MAX_SEQS];
-  int n = 0, b = b0;
+  int rows[PAGED_MAX_SEQS], bs[PAGED_MAX_SEQS], order[PAGED_MAX_SEQS], before[PAGED_MAX_SEQS];
+  int n = 0, b = b0, gap = b0;
   bool pairs = false;  // some sequence has a second row tile
-  for (; b < a.B && n < PAGED_MAX_SEQS; ++b) {
+  for (; b < a.B; ++b) {
     const int len = TREE ? a.N : cu_len_host[b + 1] - cu_len_host[b];
     if (len == 0) continue;
+    if (n == PAGED_MAX_SEQS) break;
+    before[n] = gap;
+    gap = b + 1;
     rows[n] = len;
     bs[n] = b;
     both[0][n] = chains_of<TREE>(a, a.tok_tile, len, kv_host[b]);
@@ -1366,6 +1396,8 @@ void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* 
   pl->pair = false;
   pl->ok = true;
   if (n == 0) return;
+  pl->gaps.last = bs[n - 1];
+  pl->gaps.end = b;
   const int tree_tiles = TREE ? ceil_div(a.N, KV_TILE) : 0;
   Cut cut = plan_cut(both[0], rows, n, a.Hkv, a.Hq, a.D, tree_tiles, tile_time(a.D, a.bs, false));
   if (a.D == 64 && pairs) {
@@ -1392,6 +1424,7 @@ void plan_launch(const PagedArgs& a, const int32_t* cu_len_host, const int32_t* 
     q.splits = paged_splits(c[x].most, pl->chunk_tiles, INT_MAX);
     q.rows = rows[x];
     q.part_row = (int)part;
+    pl->gaps.before[k] = before[x];
     items += (long long)q.row_tiles * q.splits * a.Hkv;
     if (q.splits > 1) part += (long long)q.splits * q.rows;
     if (items > (1ll << 30) || part * a.Hq >= (1ll << 31)) pl->ok = false;
@@ -1434,7 +1467,7 @@ cudaError_t run(PagedArgs a, const int32_t* cu_len_host, const int32_t* kv_host,
     a.part_lse = a.part_o + (size_t)pl.part_rows * a.Hq * a.D;
     a.tok = pl.pair ? 2 * a.tok_tile : a.tok_tile;
     const auto f = a.D == 128 ? launch<128, TREE, false> : pl.pair ? launch<64, TREE, true> : launch<64, TREE, false>;
-    const cudaError_t e = f(a, pl.seq, pl.n_seqs, pl.n_items, pl.part_rows > 0, s);
+    const cudaError_t e = f(a, pl, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

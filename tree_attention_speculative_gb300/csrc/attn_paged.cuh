@@ -19,6 +19,13 @@ struct PagedSeq {
   int part_row;  // splits > 1: its first row (a token's) among the partial results
 };
 
+// The sequences of a launch that had no rows when it was planned: [before[e], b) are those
+// ahead of entry e's sequence b, [last + 1, end) those behind the last.
+struct PagedGaps {
+  int before[PAGED_MAX_SEQS];
+  int last, end;
+};
+
 struct PagedArgs {
   const __nv_bfloat16* q;  // [T, Hq, D]
   const __nv_bfloat16* k_cache;
@@ -85,6 +92,7 @@ __host__ __device__ inline int paged_split_start(int n, int ps, int s) {
 // A launch: sequences [.., b_end) of the call, at most PAGED_MAX_SEQS with rows.
 struct PagedPlan {
   PagedSeq seq[PAGED_MAX_SEQS];
+  PagedGaps gaps;
   int n_seqs, n_items, chunk_tiles, b_end;
   long long part_rows;  // tokens' rows of partial results
   bool pair;            // an item takes two row tiles
