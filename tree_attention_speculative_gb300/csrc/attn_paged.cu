@@ -34,12 +34,14 @@
 // But for pairs, the groups are joined at an item's end, and each stores half of the channels.
 //
 // What bounds it.  Long chains of heads of 128: the tensor cores under the power cap
-// (4096 tokens over 16K, 32 heads: 607 us in bursts, 1.58 PFLOP/s, 0.84 of the
-// measured GEMM rate; 645 us back to back).  Heads of 64 have half the products for the
-// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 449 us,
-// 1.15 PFLOP/s; without pairs 472 with blocks of 64, and 559 with blocks of 16, where
-// it is the issue of 16 TMA boxes a tile).  Single tokens: memory (32 sequences of 0-8K:
-// 80 us, 6.3 TB/s, 0.92 of the measured copy).  An item costs 2 to 3 us beyond its
+// (4096 tokens over 16K, 32 heads: 613-625 us in bursts, 1.55 PFLOP/s, 0.83 of the
+// measured GEMM rate; 652-677 us back to back).  Heads of 64 have half the products for the
+// same softmax, which then sets the pace (64 heads, 4 x 1024 tokens over 8K: 475-510 us, by
+// the chip's heat, 1.0-1.08 PFLOP/s).  What it was before a tile's largest weight was looked for
+// (at SUM_LIMIT): 449, without pairs 472 with blocks of 64, and 559 with blocks of 16, where
+// it is the issue of 16 TMA boxes a tile.  The kernels of heads of 64 spill 28 to 88 bytes a
+// thread at their cap of 168 registers, the trees' of 128 twelve, the chunks' none.  Single
+// tokens: memory (32 sequences of 0-8K: 81 us, 6.2 TB/s, 0.91 of the measured copy).  An item costs 2 to 3 us beyond its
 // tiles: the start of its pipeline, the last PV, the stores.  What carried it (64 heads of
 // 128 and of 64 on 64 trees of 64 nodes over 8K, us):
 //   one softmax group, 128 columns a thread                       848  823
@@ -1241,7 +1243,9 @@ cudaError_t launch(const PagedArgs& a, const PagedPlan& pl, cudaStream_t s) {
 // the items' starts, do not keep busy).  Cut chains cost a second kernel and their partial
 // results' round trip.  On fourteen ragged batches the plans were within 0 to 12 % of the
 // best of a sweep (by averages alone, a prompt's 1024 tokens beside 64-tile chains of
-// single tokens were left uncut: 72 us, now 64).
+// single tokens were left uncut: 73 us, now 65).  More than FEW_SEQS sequences are judged by
+// the average all the same, since dealing out takes time with the square of their number: nine more
+// sequences with a token of 5 keys make that batch 73 us again.
 struct Chains {
   int count;     // items' rows
   int most;      // tiles of the longest chain
