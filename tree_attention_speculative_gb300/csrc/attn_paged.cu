@@ -41,8 +41,9 @@
 // (at SUM_LIMIT): 449, without pairs 472 with blocks of 64, and 559 with blocks of 16, where
 // it is the issue of 16 TMA boxes a tile.  The kernels of heads of 64 spill 28 to 88 bytes a
 // thread at their cap of 168 registers, the trees' of 128 twelve, the chunks' none.  Single
-// tokens: memory (32 sequences of 0-8K: 81 us, 6.2 TB/s, 0.91 of the measured copy).  An item costs 2 to 3 us beyond its
-// tiles: the start of its pipeline, the last PV, the stores.  What carried it (64 heads of
+// tokens: memory (32 sequences of 0-8K: 81 us, 6.2 TB/s, 0.91 of the measured copy).  An
+// item costs 2 to 3 us beyond its tiles: the start of its pipeline, the last PV, the
+// stores.  What carried it (64 heads of
 // 128 and of 64 on 64 trees of 64 nodes over 8K, us):
 //   one softmax group, 128 columns a thread                       848  823
 //   two groups                                                    958  700
